@@ -12,7 +12,8 @@ Names follow the C ABI: ``kmeans_assign``, ``kmeans_assign_ffma``,
 ``kmeans_workspace_bytes``, ``kmeans_device_status``, ``kmeans_status_string``,
 and the shard entry points (``kmeans_lloyd_iter_partial``,
 ``kmeans_reduce_partials``, ``kmeanspp_shard_*``) that ``sharded.py`` drives
-across processes.
+across processes.  ``kmeans_route*`` and ``kmeans_linear*`` are the expert
+routing and the experts' products that ``experts.py`` makes a layer of.
 """
 from __future__ import annotations
 
@@ -48,6 +49,19 @@ OP_KMEANSPP_SHARD = 9
 OP_LLOYD_PARTIAL = 10
 OP_UPDATE_PARTIAL = 11
 
+# kmeans_linear_workspace_bytes
+OP_LINEAR = 0
+OP_LINEAR_GRAD = 1
+
+F32 = 0
+F16 = 1
+BF16 = 2
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+ROUTE_MAX_EXPERTS = 4096
+ROUTE_MAX_TOPK = 32
+ROUTE_MAX_WIDTH = 16000000
+LINEAR_MAX_EXPERTS = 1024
+
 INIT_GIVEN = 0
 INIT_KMEANSPP = 1
 FIT_RELOCATE_EMPTY = 0x100
@@ -72,6 +86,8 @@ EXPORTS = (
     "kmeans_lloyd_iter_fused", "kmeans_relocate_empty", "kmeans_update_partial", "kmeans_lloyd_iter_partial",
     "kmeans_reduce_partials", "kmeanspp_shard_exchange_bytes", "kmeanspp_shard_first", "kmeanspp_shard_pick",
     "kmeanspp_shard_dist", "kmeanspp_shard_commit", "kmeanspp_rows_read",
+    "kmeans_route_workspace_bytes", "kmeans_route", "kmeans_route_gather", "kmeans_route_combine",
+    "kmeans_route_combine_grad", "kmeans_linear_workspace_bytes", "kmeans_linear", "kmeans_linear_grad",
 )
 
 _lock = threading.Lock()
@@ -153,6 +169,22 @@ def load(path: str | None = None):
         lib.kmeanspp_shard_dist.restype = INT
         lib.kmeanspp_shard_commit.argtypes = [I64, I64, INT, INT, P, INT, I64, P, P, P, P, SZ, P]
         lib.kmeanspp_shard_commit.restype = INT
+        lib.kmeans_route_workspace_bytes.argtypes = [I64, I64, I64]
+        lib.kmeans_route_workspace_bytes.restype = SZ
+        lib.kmeans_route.argtypes = [P, INT, I64, I64, I64, P, P, P, P, SZ, P]
+        lib.kmeans_route.restype = INT
+        lib.kmeans_route_gather.argtypes = [P, I64, INT, P, P, I64, I64, I64, I64, P, P]
+        lib.kmeans_route_gather.restype = INT
+        lib.kmeans_route_combine.argtypes = [P, INT, P, P, I64, P, P, I64, I64, I64, I64, P, P]
+        lib.kmeans_route_combine.restype = INT
+        lib.kmeans_route_combine_grad.argtypes = [P, I64, P, INT, P, P, P, I64, I64, I64, I64, P, P, P]
+        lib.kmeans_route_combine_grad.restype = INT
+        lib.kmeans_linear_workspace_bytes.argtypes = [INT, I64, I64, I64, I64]
+        lib.kmeans_linear_workspace_bytes.restype = SZ
+        lib.kmeans_linear.argtypes = [P, I64, P, P, P, I64, INT, INT, P, I64, I64, I64, I64, P, P, P, SZ, P]
+        lib.kmeans_linear.restype = INT
+        lib.kmeans_linear_grad.argtypes = [P, I64, P, I64, P, P, INT, INT, P, I64, I64, I64, I64, P, P, P, P, SZ, P]
+        lib.kmeans_linear_grad.restype = INT
         _lib = lib
         return lib
 
@@ -631,3 +663,275 @@ def kmeanspp_shard_commit(n: int, d: int, n_trials: int, first: bool, pots, worl
                                       _ptr(indices), _ptr(centers), _ptr(total), _ptr(ws), ws.numel(),
                                       _stream_handle(stream))
     _raise(st, "kmeanspp_shard_commit")
+
+
+# ----------------------------------------- expert routing and expert products
+def _dtype_code(t, name):
+    torch = _torch()
+    code = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _check_rows(t, name, dtype, shape, device):
+    """A matrix whose rows are contiguous, with any pitch -> its pitch."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be on {device}, it is on {t.device} (the library has no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    pitch = t.stride(0)
+    if rows <= 1:
+        pitch = max(cols, 1)
+    if (cols > 1 and t.stride(1) != 1) or pitch < cols:
+        raise ValueError(f"{name}: the rows must be contiguous and apart from each other")
+    return pitch
+
+
+def _cuda_matrix(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (the library has no CPU path)")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
+
+
+def route_workspace(n: int, topk: int, n_experts: int, device=None):
+    """A device workspace for ``kmeans_route`` (uint8 tensor)."""
+    nbytes = int(load().kmeans_route_workspace_bytes(n, topk, n_experts))
+    if nbytes == 0:
+        raise KMeansError(KMEANS_ERR_INVALID_ARG, "kmeans_route_workspace_bytes")
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device or "cuda")
+
+
+def linear_workspace(op: int, m: int, n: int, k: int, n_experts: int = 1, device=None):
+    """A device workspace for ``kmeans_linear`` (OP_LINEAR) or
+    ``kmeans_linear_grad`` (OP_LINEAR_GRAD) of m rows, n output and k input
+    features (uint8 tensor)."""
+    nbytes = int(load().kmeans_linear_workspace_bytes(op, m, n, k, n_experts))
+    if nbytes == 0:
+        raise KMeansError(KMEANS_ERR_INVALID_ARG, "kmeans_linear_workspace_bytes")
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device or "cuda")
+
+
+def kmeans_route(experts, n_experts: int, offsets=None, order=None, rows=None, ws=None, stream=None):
+    """Slots sorted by expert -> ``(offsets (n_experts + 1,), order (n * topk,),
+    rows (n, topk))``, all int32.  ``experts`` (n, topk) or (n,): int32 or int64
+    ids, negative where the choice was dropped (kmeans_assign's labels route
+    each sample to its cluster)."""
+    torch = _torch()
+    if not isinstance(experts, torch.Tensor):
+        raise TypeError("experts must be a torch.Tensor")
+    if experts.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"experts must be int32 or int64, got {experts.dtype}")
+    _check(experts, "experts", experts.dtype)
+    if experts.dim() not in (1, 2):
+        raise ValueError(f"experts must be (n, topk) or (n,), got {tuple(experts.shape)}")
+    n, topk = experts.shape if experts.dim() == 2 else (experts.shape[0], 1)
+    dev = experts.device
+    if offsets is None:
+        offsets = torch.empty(int(n_experts) + 1, dtype=torch.int32, device=dev)
+    else:
+        _check(offsets, "offsets", torch.int32, (int(n_experts) + 1,), dev)
+    if order is None:
+        order = torch.empty(n * topk, dtype=torch.int32, device=dev)
+    else:
+        _check(order, "order", torch.int32, (n * topk,), dev)
+    if rows is None:
+        rows = torch.empty((n, topk), dtype=torch.int32, device=dev)
+    else:
+        _check(rows, "rows", torch.int32, (n, topk), dev)
+    if ws is None:
+        ws = route_workspace(n, topk, int(n_experts), dev)
+    else:
+        _check(ws, "ws", torch.uint8, device=dev)
+    st = load().kmeans_route(_ptr(experts), experts.element_size(), n, topk, int(n_experts), _ptr(offsets),
+                             _ptr(order), _ptr(rows), _ptr(ws), ws.numel(), _stream_handle(stream))
+    _raise(st, "kmeans_route")
+    return offsets, order, rows
+
+
+def _plan(rows, offsets, device):
+    torch = _torch()
+    _check(rows, "rows", torch.int32, device=device)
+    if rows.dim() != 2:
+        raise ValueError(f"rows must be (n, topk), got {tuple(rows.shape)}")
+    _check(offsets, "offsets", torch.int32, device=device)
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"offsets must be (n_experts + 1,), got {tuple(offsets.shape)}")
+    return rows.shape[0], rows.shape[1], offsets.shape[0] - 1
+
+
+def kmeans_route_gather(x, rows, offsets, xs=None, stream=None):
+    """The tokens in expert order -> ``xs (n * topk, d)``, zeros in the rows of
+    dropped choices.  ``rows`` and ``offsets`` are kmeans_route's."""
+    _cuda_matrix(x, "x")
+    code = _dtype_code(x, "x")
+    n, topk, n_experts = _plan(rows, offsets, x.device)
+    d = x.shape[1]
+    ldx = _check_rows(x, "x", x.dtype, (n, d), x.device)
+    if xs is None:
+        xs = _torch().empty((n * topk, d), dtype=x.dtype, device=x.device)
+    else:
+        _check(xs, "xs", x.dtype, (n * topk, d), x.device)
+    st = load().kmeans_route_gather(_ptr(x), ldx, code, _ptr(rows), _ptr(offsets), n, topk, n_experts, d, _ptr(xs),
+                                    _stream_handle(stream))
+    _raise(st, "kmeans_route_gather")
+    return xs
+
+
+def kmeans_route_combine(ys, rows, offsets, weights=None, residual=None, y=None, stream=None):
+    """The experts' rows back per token -> ``y (n, d)``: residual + the sum of
+    ``weights`` (n, topk) times the choices' rows of ``ys`` (n * topk, d).
+    Without weights, also the gradient of kmeans_route_gather."""
+    torch = _torch()
+    _cuda_matrix(ys, "ys")
+    code = _dtype_code(ys, "ys")
+    dev = ys.device
+    n, topk, n_experts = _plan(rows, offsets, dev)
+    d = ys.shape[1]
+    _check(ys, "ys", ys.dtype, (n * topk, d))
+    if weights is not None:
+        _check(weights, "weights", torch.float32, (n, topk), dev)
+    ldr = _check_rows(residual, "residual", ys.dtype, (n, d), dev) if residual is not None else 0
+    if y is None:
+        y = torch.empty((n, d), dtype=ys.dtype, device=dev)
+    else:
+        _check(y, "y", ys.dtype, (n, d), dev)
+    st = load().kmeans_route_combine(_ptr(ys), code, _ptr(weights), _ptr(residual), ldr, _ptr(rows), _ptr(offsets), n,
+                                     topk, n_experts, d, _ptr(y), _stream_handle(stream))
+    _raise(st, "kmeans_route_combine")
+    return y
+
+
+def kmeans_route_combine_grad(dy, ys, rows, offsets, weights, dys=None, dweights=None, stream=None):
+    """Gradient of kmeans_route_combine -> ``(dys (n * topk, d), dweights
+    (n, topk) float32)``; the residual's gradient is ``dy``."""
+    torch = _torch()
+    _cuda_matrix(ys, "ys")
+    code = _dtype_code(ys, "ys")
+    dev = ys.device
+    n, topk, n_experts = _plan(rows, offsets, dev)
+    d = ys.shape[1]
+    _check(ys, "ys", ys.dtype, (n * topk, d))
+    lddy = _check_rows(dy, "dy", ys.dtype, (n, d), dev)
+    _check(weights, "weights", torch.float32, (n, topk), dev)
+    if dys is None:
+        dys = torch.empty((n * topk, d), dtype=ys.dtype, device=dev)
+    else:
+        _check(dys, "dys", ys.dtype, (n * topk, d), dev)
+    if dweights is None:
+        dweights = torch.empty((n, topk), dtype=torch.float32, device=dev)
+    else:
+        _check(dweights, "dweights", torch.float32, (n, topk), dev)
+    st = load().kmeans_route_combine_grad(_ptr(dy), lddy, _ptr(ys), code, _ptr(weights), _ptr(rows), _ptr(offsets), n,
+                                          topk, n_experts, d, _ptr(dys), _ptr(dweights), _stream_handle(stream))
+    _raise(st, "kmeans_route_combine_grad")
+    return dys, dweights
+
+
+def _linear_args(x, w, offsets, activation):
+    """Checked ``(code, m, n, k, n_experts, activation code, weight shape)``."""
+    torch = _torch()
+    _cuda_matrix(x, "x")
+    code = _dtype_code(x, "x")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r} (one of {', '.join(ACTIVATIONS)})")
+    _check(w, "w", x.dtype, device=x.device)
+    m, k = x.shape
+    if offsets is None:
+        if w.dim() != 2 and not (w.dim() == 3 and w.shape[0] == 1):
+            raise ValueError(f"w must be (n, k) without offsets, got {tuple(w.shape)}")
+        n_experts = 1
+    else:
+        if w.dim() != 3:
+            raise ValueError(f"w must be (n_experts, n, k) with offsets, got {tuple(w.shape)}")
+        n_experts = w.shape[0]
+        _check(offsets, "offsets", torch.int32, (n_experts + 1,), x.device)
+    if w.shape[-1] != k:
+        raise ValueError(f"w has {w.shape[-1]} input features, x has {k}")
+    return code, m, w.shape[-2], k, n_experts, ACTIVATIONS[activation]
+
+
+def kmeans_linear(x, w, bias=None, residual=None, offsets=None, activation="none", save_pre=False, y=None, pre=None,
+                  ws=None, stream=None):
+    """``act(x w^T + bias) + residual`` -> ``(y (m, n), pre (m, n) or None)``.
+
+    Dense: w (n, k), bias (n,).  Experts: w (n_experts, n, k), bias (n_experts,
+    n) and offsets (n_experts + 1,): rows offsets[e] .. offsets[e + 1] - 1 of x
+    are expert e's, rows past the last offset give zeros.  ``activation``:
+    none, relu, gelu, gelu_tanh or silu.  ``save_pre`` (or a ``pre`` to write
+    into) keeps the values before the activation for kmeans_linear_grad.
+    float16 or bfloat16."""
+    torch = _torch()
+    code, m, n, k, n_experts, act = _linear_args(x, w, offsets, activation)
+    dev, dt = x.device, x.dtype
+    ldx = _check_rows(x, "x", dt, (m, k), dev)
+    if bias is not None:
+        _check(bias, "bias", dt, tuple(w.shape[:-1]), dev)
+    ldr = _check_rows(residual, "residual", dt, (m, n), dev) if residual is not None else 0
+    if y is None:
+        y = torch.empty((m, n), dtype=dt, device=dev)
+    else:
+        _check(y, "y", dt, (m, n), dev)
+    if pre is not None:
+        _check(pre, "pre", dt, (m, n), dev)
+    elif save_pre:
+        pre = torch.empty((m, n), dtype=dt, device=dev)
+    if ws is None:
+        ws = linear_workspace(OP_LINEAR, m, n, k, n_experts, dev)
+    else:
+        _check(ws, "ws", torch.uint8, device=dev)
+    st = load().kmeans_linear(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(residual), ldr, code, act, _ptr(offsets), m, n,
+                              k, n_experts, _ptr(y), _ptr(pre), _ptr(ws), ws.numel(), _stream_handle(stream))
+    _raise(st, "kmeans_linear")
+    return y, pre
+
+
+def kmeans_linear_grad(dy, x, w, pre=None, offsets=None, activation="none", need_dx=True, need_dw=True, need_db=True,
+                       dx=None, dw=None, db=None, ws=None, stream=None):
+    """Gradient of kmeans_linear -> ``(dx, dw, db)`` (None where not needed);
+    ``pre`` is what kmeans_linear kept (not needed without an activation).  The
+    residual's gradient is ``dy``."""
+    torch = _torch()
+    code, m, n, k, n_experts, act = _linear_args(x, w, offsets, activation)
+    dev, dt = x.device, x.dtype
+    ldx = _check_rows(x, "x", dt, (m, k), dev)
+    lddy = _check_rows(dy, "dy", dt, (m, n), dev)
+    if act != ACTIVATIONS["none"]:
+        if pre is None:
+            raise ValueError(f"activation {activation!r} needs pre")
+        _check(pre, "pre", dt, (m, n), dev)
+    if need_dx:
+        if dx is None:
+            dx = torch.empty((m, k), dtype=dt, device=dev)
+        else:
+            _check(dx, "dx", dt, (m, k), dev)
+    if need_dw:
+        if dw is None:
+            dw = torch.empty_like(w)
+        else:
+            _check(dw, "dw", dt, tuple(w.shape), dev)
+    if need_db:
+        if db is None:
+            db = torch.empty(w.shape[:-1], dtype=dt, device=dev)
+        else:
+            _check(db, "db", dt, tuple(w.shape[:-1]), dev)
+    if ws is None:
+        ws = linear_workspace(OP_LINEAR_GRAD, m, n, k, n_experts, dev)
+    else:
+        _check(ws, "ws", torch.uint8, device=dev)
+    dx, dw, db = dx if need_dx else None, dw if need_dw else None, db if need_db else None
+    st = load().kmeans_linear_grad(_ptr(dy), lddy, _ptr(x), ldx, _ptr(w), _ptr(pre), code, act, _ptr(offsets), m, n, k,
+                                   n_experts, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws.numel(),
+                                   _stream_handle(stream))
+    _raise(st, "kmeans_linear_grad")
+    return dx, dw, db

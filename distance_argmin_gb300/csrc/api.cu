@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/kmeans_gb300.h"
+#include "api_checks.cuh"
 #include "assign_common.cuh"
 #include "common.cuh"
 #include "kmeanspp.cuh"
@@ -17,8 +18,6 @@ using namespace km;
 
 namespace {
 
-constexpr int64_t kMaxIndex = 0x7fffffffLL;  // labels and member lists use 32-bit indices
-
 bool sizes_ok(int64_t n, int64_t k, int64_t d) {
     return n >= 1 && k >= 1 && k <= n && d >= 1 && n <= kMaxIndex && k <= kMaxIndex && d <= kMaxIndex;
 }
@@ -27,17 +26,6 @@ bool sizes_ok(int64_t n, int64_t k, int64_t d) {
 bool shard_sizes_ok(int64_t n, int64_t k, int64_t d) {
     return n >= 1 && k >= 1 && d >= 1 && n <= kMaxIndex && k <= kMaxIndex && d <= kMaxIndex;
 }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-int check_ws(const void *ws, size_t ws_bytes, size_t need) {
-    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return KMEANS_ERR_WORKSPACE;
-    if (ws_bytes < need) return KMEANS_ERR_WORKSPACE;
-    return KMEANS_OK;
-}
-
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? KMEANS_OK : KMEANS_ERR_CUDA; }
 
 int tc_path_ok(const float *X, const float *C, int64_t d) {
     return (d % 4 == 0 && aligned16(X) && aligned16(C)) ? KMEANS_OK : KMEANS_ERR_UNSUPPORTED;

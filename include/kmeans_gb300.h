@@ -442,6 +442,114 @@ int kmeans_fit(const float *X, float *C, int64_t *labels, float *best_dist, int3
                int64_t n, int64_t k, int64_t d, int init, uint64_t seed, int max_iter, double tol,
                int *n_iter, double *inertia_history, void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Expert routing and the experts' matrix products: a layer whose rows are
+ * each handled by the experts they were sent to, by the nearest centroid
+ * (the labels of kmeans_assign are expert ids) or by any other choice of up
+ * to KMEANS_ROUTE_MAX_TOPK experts per token.
+ *
+ *   slot   s = t * topk + j: choice j of token t, for n tokens
+ *   row    a slot's place once the slots are sorted by expert
+ *
+ * kmeans_route sorts, kmeans_route_gather copies the tokens into rows,
+ * kmeans_linear multiplies every expert's rows by its matrix,
+ * kmeans_route_combine adds the weighted rows back per token.  The gradients
+ * are kmeans_route_combine_grad, kmeans_linear_grad, and for the gather
+ * kmeans_route_combine without weights.
+ *
+ * Conventions on top of those above: activations are matrices of one type
+ * (KMEANS_F32, KMEANS_F16 or KMEANS_BF16) whose rows are contiguous; a row
+ * pitch argument ld* counts elements and is at least the row's length.
+ * Matrices without a pitch argument, and every output, are contiguous.  All
+ * arithmetic is float32 with one rounding per output.  Values may be infinite
+ * or NaN: they spread as the formulas say and never reach another token's or
+ * another expert's results; what belongs to a dropped slot is never read into
+ * a result.  Zero tokens, rows or choices are allowed.
+ * --------------------------------------------------------------------------- */
+enum { KMEANS_F32 = 0, KMEANS_F16 = 1, KMEANS_BF16 = 2 };
+
+/* z, max(z, 0), z Phi(z), its tanh form, z / (1 + exp(-z)) */
+enum {
+    KMEANS_ACT_NONE = 0,
+    KMEANS_ACT_RELU = 1,
+    KMEANS_ACT_GELU = 2,
+    KMEANS_ACT_GELU_TANH = 3,
+    KMEANS_ACT_SILU = 4
+};
+
+#define KMEANS_ROUTE_MAX_EXPERTS 4096
+#define KMEANS_ROUTE_MAX_TOPK 32
+#define KMEANS_ROUTE_MAX_WIDTH 16000000
+#define KMEANS_LINEAR_MAX_EXPERTS 1024
+
+/* Workspace of kmeans_route (0 when the sizes are invalid). */
+size_t kmeans_route_workspace_bytes(int64_t n, int64_t topk, int64_t n_experts);
+
+/* Slots sorted by expert.  experts (n, topk): ids of id_bytes bytes (4: int32,
+ * 8: int64), each in [0, n_experts), or negative for a choice that was
+ * dropped.  The slots of expert e become rows offsets[e] .. offsets[e + 1] - 1
+ * in slot order, the dropped ones follow at rows offsets[n_experts] and up.
+ * offsets (n_experts + 1), order (n * topk: the slot of each row) and rows
+ * (n * topk: the row of each slot) are int32; order and rows are inverse
+ * permutations.  An id of n_experts or more counts as dropped and sets
+ * KMEANS_ERR_DEVICE_LABEL in the workspace's status word.
+ * n * topk < 2^31, topk <= KMEANS_ROUTE_MAX_TOPK, n_experts <=
+ * KMEANS_ROUTE_MAX_EXPERTS. */
+int kmeans_route(const void *experts, int id_bytes, int64_t n, int64_t topk, int64_t n_experts,
+                 int32_t *offsets, int32_t *order, int32_t *rows, void *ws, size_t ws_bytes, void *stream);
+
+/* xs[rows[t, j]] = x[t], and zeros in the dropped rows.  x (n, d) with pitch
+ * ldx, xs (n * topk, d), d <= KMEANS_ROUTE_MAX_WIDTH.  rows and offsets as kmeans_route wrote them (here and
+ * below; a row outside [0, n * topk) is left out). */
+int kmeans_route_gather(const void *x, int64_t ldx, int dtype, const int32_t *rows, const int32_t *offsets,
+                        int64_t n, int64_t topk, int64_t n_experts, int64_t d, void *xs, void *stream);
+
+/* y[t] = residual[t] + sum_j weights[t, j] * ys[rows[t, j]] over the kept
+ * choices, in the order of j.  ys (n * topk, d), weights (n, topk) float32 or
+ * NULL for ones, residual (n, d) with pitch ldr or NULL, y (n, d).  y may be
+ * residual itself when ldr == d.  Without weights this is also the gradient
+ * of kmeans_route_gather. */
+int kmeans_route_combine(const void *ys, int dtype, const float *weights, const void *residual, int64_t ldr,
+                         const int32_t *rows, const int32_t *offsets, int64_t n, int64_t topk,
+                         int64_t n_experts, int64_t d, void *y, void *stream);
+
+/* Gradient of kmeans_route_combine: dys[rows[t, j]] = weights[t, j] * dy[t]
+ * (zeros in the dropped rows), dweights[t, j] = <dy[t], ys[rows[t, j]]> (0
+ * where dropped).  dy (n, d) with pitch lddy; the residual's gradient is dy. */
+int kmeans_route_combine_grad(const void *dy, int64_t lddy, const void *ys, int dtype, const float *weights,
+                              const int32_t *rows, const int32_t *offsets, int64_t n, int64_t topk,
+                              int64_t n_experts, int64_t d, void *dys, float *dweights, void *stream);
+
+/* Workspace of kmeans_linear (grad = 0) and kmeans_linear_grad (grad = 1) for
+ * m rows, n output and k input features (0 when the sizes are invalid). */
+size_t kmeans_linear_workspace_bytes(int grad, int64_t m, int64_t n, int64_t k, int64_t n_experts);
+
+/* For the rows r of expert e:  z = x[r] w[e]^T + bias[e],
+ * y[r] = act(z) + residual[r].  x (m, k) with pitch ldx, w (n_experts, n, k),
+ * bias (n_experts, n) or NULL, residual (m, n) with pitch ldr or NULL, y
+ * (m, n), pre (m, n) or NULL: receives z for the gradient.  Rows at or past
+ * offsets[n_experts] belong to no expert: y and pre are zero there.  offsets
+ * (n_experts + 1, ascending from 0, at most m) may be NULL when n_experts is
+ * 1: an ordinary dense layer.  Offsets that run backwards or past m are cut
+ * to what fits.  KMEANS_F16 or KMEANS_BF16; n_experts <=
+ * KMEANS_LINEAR_MAX_EXPERTS; m, n, k < 2^31, n_experts * n < 2^31, n, k >= 1.
+ * y must not alias an input, except residual when ldr == n. */
+int kmeans_linear(const void *x, int64_t ldx, const void *w, const void *bias, const void *residual,
+                  int64_t ldr, int dtype, int activation, const int32_t *offsets, int64_t m, int64_t n,
+                  int64_t k, int64_t n_experts, void *y, void *pre, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient of kmeans_linear: with dz = dy * act'(pre),
+ * dx[r] = dz[r] w[e], dw[e] = sum_r dz[r] x[r]^T, db[e] = sum_r dz[r].
+ * dy (m, n) with pitch lddy; pre (m, n) as kmeans_linear wrote it (NULL
+ * allowed for KMEANS_ACT_NONE).  dx (m, k), dw (n_experts, n, k) and db
+ * (n_experts, n) may each be NULL; dx is zero in rows of no expert, dw and db
+ * in experts without rows.  The products take dz rounded to the matrices'
+ * type; db sums it before that rounding.  The residual's gradient is dy. */
+int kmeans_linear_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w,
+                       const void *pre, int dtype, int activation, const int32_t *offsets, int64_t m,
+                       int64_t n, int64_t k, int64_t n_experts, void *dx, void *dw, void *db,
+                       void *ws, size_t ws_bytes, void *stream);
+
 /* Synchronises `stream` and returns the device status word of the last call
  * that used `ws` (KMEANS_OK, KMEANS_ERR_DEVICE_TIMEOUT or
  * KMEANS_ERR_DEVICE_LABEL), or KMEANS_ERR_CUDA if the stream reports an error. */
