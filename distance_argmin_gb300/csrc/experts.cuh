@@ -44,8 +44,9 @@ struct LinearShape {
 };
 
 struct LinearLayout {
-    int64_t off_dz;    // (m, n) values after the activation's slope (gradient only; 0: none)
-    int64_t off_dbp;   // partial bias gradients (gradient only)
+    int64_t off_x;   // x with its rows on 16 bytes, where the caller's are not
+    int64_t off_w;   // w likewise (0: its rows are a multiple of 16 bytes)
+    int64_t off_dz;  // dy after the activation's slope, rows on 16 bytes (gradient)
     int64_t bytes;
 };
 

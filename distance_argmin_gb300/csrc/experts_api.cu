@@ -152,6 +152,7 @@ int kmeans_linear(const void *x, int64_t ldx, const void *w, const void *bias, c
     if (!elem_aligned(x, dtype) || !elem_aligned(residual, dtype) || !elem_aligned(y, dtype) ||
         !elem_aligned(pre, dtype))
         return KMEANS_ERR_INVALID_ARG;
+    if (!aligned16(w)) return KMEANS_ERR_UNSUPPORTED;
     const LinearLayout L = linear_layout(false, m, n, k, n_experts);
     const int wst = check_ws(ws, ws_bytes, (size_t)L.bytes);
     if (wst != KMEANS_OK) return wst;
@@ -170,6 +171,7 @@ int kmeans_linear_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx,
     const void *all[] = {dy, x, w, pre, dx, dw, db};
     for (const void *p : all)
         if (!elem_aligned(p, dtype)) return KMEANS_ERR_INVALID_ARG;
+    if (dx && !aligned16(w)) return KMEANS_ERR_UNSUPPORTED;
     const LinearLayout L = linear_layout(true, m, n, k, n_experts);
     const int wst = check_ws(ws, ws_bytes, (size_t)L.bytes);
     if (wst != KMEANS_OK) return wst;

@@ -1,55 +1,16 @@
-// The experts' matrix products with bias, activation and residual, and their
-// gradients.
-//
-//   forward  y[r, :]  = act(x[r, :] W_e^T + b_e) + residual[r, :]
-//   rows     dx[r, :] = dz[r, :] W_e              (r in expert e's rows)
-//   weights  dW_e     = dz_e^T x_e
-//
-// All three are out(q, p) = sum_c A(p, c) B(q, c), with p the contiguous
-// dimension of the output.
+// The experts' matrix products and their gradients: which kernels a call runs,
+// and what goes around the products (linear_tc.cu): rows brought to 16 bytes,
+// dz = dy act'(pre), and the bias gradient.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "experts.cuh"
+#include "linear_common.cuh"
 
 namespace km {
 
 namespace {
-
-enum class Product { kForward, kRows, kWeights };
-
-constexpr int kTile = 64;
-constexpr int kStep = 16;
-constexpr int kThreads = 256;
-
-struct ProductParams {
-    const void *a, *b, *bias, *residual;
-    void *out, *pre;
-    const int32_t *offsets;
-    int64_t m, n, k, lda, ldb, ldr;
-    int n_experts, activation;
-};
-
-__device__ __forceinline__ float wide(__half v) { return __half2float(v); }
-__device__ __forceinline__ float wide(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T>
-__device__ __forceinline__ T narrow(float v);
-template <>
-__device__ __forceinline__ __half narrow(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 narrow(float v) { return __float2bfloat16_rn(v); }
-
-__device__ __forceinline__ float activate_as(int act, float z) {
-    switch (act) {
-        case KMEANS_ACT_RELU: return activate<KMEANS_ACT_RELU>(z);
-        case KMEANS_ACT_GELU: return activate<KMEANS_ACT_GELU>(z);
-        case KMEANS_ACT_GELU_TANH: return activate<KMEANS_ACT_GELU_TANH>(z);
-        case KMEANS_ACT_SILU: return activate<KMEANS_ACT_SILU>(z);
-        default: return z;
-    }
-}
 
 __device__ __forceinline__ float slope_as(int act, float z) {
     switch (act) {
@@ -61,130 +22,34 @@ __device__ __forceinline__ float slope_as(int act, float z) {
     }
 }
 
-// First row of expert e, kept inside [0, m] and not before `from`.
-__device__ __forceinline__ int64_t first_row(const int32_t *offsets, int e, int64_t from, int64_t m) {
-    const int64_t v = offsets[e];
-    return v < from ? from : (v > m ? m : v);
-}
-
-// Rows of unit `u` of the row products: the tiles of expert 0, of expert 1, ...
-// and last those of the rows that belong to no expert (expert = n_experts).
-__device__ bool row_tile(const ProductParams &p, int64_t u, int &expert, int64_t &r0, int64_t &r1) {
-    if (!p.offsets) {
-        expert = 0;
-        r0 = u * kTile;
-        r1 = min(r0 + kTile, p.m);
-        return r0 < p.m;
-    }
-    int64_t at = first_row(p.offsets, 0, 0, p.m);
-    if (at > 0) at = 0;
-    for (int e = 0; e <= p.n_experts; ++e) {
-        const int64_t end = e < p.n_experts ? first_row(p.offsets, e + 1, at, p.m) : p.m;
-        const int64_t tiles = (end - at + kTile - 1) / kTile;
-        if (u < tiles) {
-            expert = e;
-            r0 = at + u * kTile;
-            r1 = min(r0 + kTile, end);
-            return true;
-        }
-        u -= tiles;
-        at = end;
-    }
-    return false;
-}
-
-template <typename T, Product MODE>
-__global__ void __launch_bounds__(kThreads) linear_tile_kernel(const ProductParams p) {
-    __shared__ float as[kStep][kTile + 1], bs[kStep][kTile + 1];
+// dst(r, c) = src(r, c) with the rows of dst on 16 bytes.
+template <typename T>
+__global__ void linear_align_kernel(const T *src, int64_t lds, int64_t rows, int64_t cols, T *dst, int64_t ldd,
+                                    uint32_t *clear) {
     griddep_wait();
-    const T *A = static_cast<const T *>(p.a), *B = static_cast<const T *>(p.b);
-    int expert;
-    int64_t q0, q1, c0, c1;  // output rows of this block, contraction range
-    const int64_t cols = MODE == Product::kForward ? p.n : p.k;
-    if (MODE == Product::kWeights) {
-        expert = blockIdx.z;
-        c0 = 0;
-        c1 = p.m;
-        if (p.offsets) {
-            c0 = 0;
-            c1 = 0;
-            for (int e = 0; e <= expert; ++e) {
-                c0 = c1;
-                c1 = first_row(p.offsets, e + 1, c0, p.m);
-            }
-        }
-        q0 = (int64_t)blockIdx.y * kTile;
-        q1 = min(q0 + kTile, p.n);
-    } else {
-        if (!row_tile(p, blockIdx.y, expert, q0, q1)) return;
-        c0 = 0;
-        c1 = expert == p.n_experts ? 0 : (MODE == Product::kForward ? p.k : p.n);
-    }
-    const int64_t p0 = (int64_t)blockIdx.x * kTile;
-    const int tp = threadIdx.x & 15, tq = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int64_t c = c0; c < c1; c += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-            const bool by_c = MODE == Product::kForward;  // A's contiguous dimension is the contraction
-            const int pi = by_c ? i / kStep : i % kTile, ci = by_c ? i % kStep : i / kTile;
-            float v = 0.f;
-            if (p0 + pi < cols && c + ci < c1) {
-                if (MODE == Product::kForward) v = wide(A[((int64_t)expert * p.n + p0 + pi) * p.k + c + ci]);
-                if (MODE == Product::kRows) v = wide(A[((int64_t)expert * p.n + c + ci) * p.k + p0 + pi]);
-                if (MODE == Product::kWeights) v = wide(A[(c + ci) * p.lda + p0 + pi]);
-            }
-            as[ci][pi] = v;
-            const bool rows_c = MODE != Product::kWeights;
-            const int qi = rows_c ? i / kStep : i % kTile, cj = rows_c ? i % kStep : i / kTile;
-            v = 0.f;
-            if (q0 + qi < q1 && c + cj < c1)
-                v = wide(rows_c ? B[(q0 + qi) * p.ldb + c + cj] : B[(c + cj) * p.ldb + q0 + qi]);
-            bs[cj][qi] = v;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int s = 0; s < kStep; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(bs[s][tq + 16 * i], as[s][tp + 16 * j], acc[i][j]);
-        __syncthreads();
-    }
-    const bool real = MODE != Product::kForward || expert < p.n_experts;
-    for (int i = 0; i < 4; ++i) {
-        const int64_t q = q0 + tq + 16 * i;
-        if (q >= q1) continue;
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = p0 + tp + 16 * j;
-            if (c >= cols) continue;
-            float v = acc[i][j];
-            const int64_t at = (MODE == Product::kWeights ? (int64_t)expert * p.n + q : q) * cols + c;
-            if (MODE == Product::kForward) {
-                if (real && p.bias) v += wide(static_cast<const T *>(p.bias)[(int64_t)expert * p.n + c]);
-                if (p.pre) static_cast<T *>(p.pre)[at] = narrow<T>(v);
-                v = real ? activate_as(p.activation, v) : 0.f;
-                if (real && p.residual) v += wide(static_cast<const T *>(p.residual)[q * p.ldr + c]);
-            }
-            static_cast<T *>(p.out)[at] = narrow<T>(v);
-        }
-    }
+    if (clear && blockIdx.x == 0 && threadIdx.x == 0) *clear = 0u;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int64_t c = threadIdx.x; c < cols; c += blockDim.x) dst[r * ldd + c] = src[r * lds + c];
 }
 
 // dz = dy act'(pre), rounded to the matrices' type.
 template <typename T>
-__global__ void linear_slope_kernel(const T *dy, int64_t lddy, const T *pre, int64_t m, int64_t n, int act, T *dz) {
+__global__ void linear_slope_kernel(const T *dy, int64_t lddy, const T *pre, int64_t m, int64_t n, int act, T *dz,
+                                    int64_t ldz, uint32_t *clear) {
     griddep_wait();
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < m * n; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = i / n, c = i - r * n;
-        const float g = wide(dy[r * lddy + c]);
-        dz[i] = narrow<T>(act == KMEANS_ACT_NONE ? g : g * slope_as(act, wide(pre[i])));
-    }
+    if (clear && blockIdx.x == 0 && threadIdx.x == 0) *clear = 0u;
+    for (int64_t r = blockIdx.x; r < m; r += gridDim.x)
+        for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
+            const float g = widen(dy[r * lddy + c]);
+            dz[r * ldz + c] = narrow<T>(act == KMEANS_ACT_NONE ? g : g * slope_as(act, widen(pre[r * n + c])));
+        }
 }
 
 template <typename T>
 __global__ void linear_bias_grad_kernel(const T *dy, int64_t lddy, const T *pre, const int32_t *offsets, int64_t m,
-                                        int64_t n, int act, T *db) {
+                                        int64_t n, int act, T *db, uint32_t *clear) {
     griddep_wait();
+    if (clear && (blockIdx.x | blockIdx.y | threadIdx.x) == 0u) *clear = 0u;
     const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (c >= n) return;
     const int expert = blockIdx.y;
@@ -198,8 +63,8 @@ __global__ void linear_bias_grad_kernel(const T *dy, int64_t lddy, const T *pre,
     }
     float sum = 0.f, lost = 0.f;  // compensated: one thread adds a whole column
     for (int64_t r = r0; r < r1; ++r) {
-        const float g = wide(dy[r * lddy + c]);
-        const float v = (act == KMEANS_ACT_NONE ? g : g * slope_as(act, wide(pre[r * n + c]))) - lost;
+        const float g = widen(dy[r * lddy + c]);
+        const float v = (act == KMEANS_ACT_NONE ? g : g * slope_as(act, widen(pre[r * n + c]))) - lost;
         const float t = sum + v;
         lost = (t - sum) - v;
         sum = t;
@@ -207,53 +72,88 @@ __global__ void linear_bias_grad_kernel(const T *dy, int64_t lddy, const T *pre,
     db[(int64_t)expert * n + c] = narrow<T>(sum);
 }
 
-ProductParams product_params(const LinearShape &sh) {
-    ProductParams p{};
-    p.offsets = sh.offsets;
-    p.m = sh.m;
-    p.n = sh.n;
-    p.k = sh.k;
-    p.n_experts = sh.n_experts;
-    return p;
-}
+// One call's kernels on the stream: the first of them clears the status word.
+template <typename T>
+struct Call {
+    const LinearShape &sh;
+    const LinearLayout &L;
+    uint8_t *ws;
+    cudaStream_t s;
+    uint32_t *clear;
 
-unsigned tiles(int64_t v) { return (unsigned)((v + kTile - 1) / kTile); }
+    Call(const LinearShape &sh_, const LinearLayout &L_, uint8_t *ws_, cudaStream_t s_)
+        : sh(sh_), L(L_), ws(ws_), s(s_), clear(&reinterpret_cast<WsHeader *>(ws_)->status) {}
+    uint32_t *first() {
+        uint32_t *c = clear;
+        clear = nullptr;
+        return c;
+    }
 
-template <typename T, Product MODE>
-cudaError_t launch_product(const LinearShape &sh, const ProductParams &p, cudaStream_t s) {
-    const unsigned cols = tiles(MODE == Product::kForward ? sh.n : sh.k);
-    const dim3 grid = MODE == Product::kWeights
-                          ? dim3(cols, tiles(sh.n), (unsigned)sh.n_experts)
-                          : dim3(cols, tiles(sh.m) + (sh.offsets ? (unsigned)sh.n_experts + 1 : 0));
-    return launch_kernel(true, linear_tile_kernel<T, MODE>, grid, dim3(kThreads), 0, s, p);
+    cudaError_t align(const void *&src, int64_t &pitch, int64_t rows, int64_t cols, int64_t off) {
+        if (rows16(src, pitch) || off == 0 || rows == 0) return cudaSuccess;
+        T *dst = reinterpret_cast<T *>(ws + off);
+        const int64_t ldd = align_up(cols, 8);
+        const cudaError_t e = launch_kernel(true, linear_align_kernel<T>, dim3((unsigned)(rows < 8192 ? rows : 8192)),
+                                            dim3(256), 0, s, static_cast<const T *>(src), pitch, rows, cols, dst, ldd,
+                                            first());
+        src = dst;
+        pitch = ldd;
+        return e;
+    }
+    cudaError_t align_w(Product16 &g) {
+        return align(g.a, g.pitch_w, (int64_t)sh.n_experts * sh.n, sh.k, L.off_w);
+    }
+    template <Product MODE>
+    cudaError_t product(const Product16 &g) {
+        return launch_linear_tc(MODE, sh, g, &reinterpret_cast<WsHeader *>(ws)->status, first() != nullptr, s);
+    }
+};
+
+template <typename T>
+cudaError_t forward_typed(const LinearShape &sh, Product16 g, const LinearLayout &L, uint8_t *ws, cudaStream_t s) {
+    Call<T> call(sh, L, ws, s);
+    cudaError_t e = call.align_w(g);
+    if (e == cudaSuccess) e = call.align(g.b, g.ldb, sh.m, sh.k, L.off_x);
+    if (e == cudaSuccess) e = call.template product<Product::kForward>(g);
+    return e;
 }
 
 template <typename T>
 cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w,
                        const void *pre, int activation, void *dx, void *dw, void *db, const LinearLayout &L,
                        uint8_t *ws, cudaStream_t s) {
-    T *dz = reinterpret_cast<T *>(ws + L.off_dz);
+    Call<T> call(sh, L, ws, s);
     cudaError_t e = cudaSuccess;
-    if (sh.m > 0)
-        e = launch_kernel(true, linear_slope_kernel<T>, dim3(152 * 8), dim3(256), 0, s, static_cast<const T *>(dy),
-                          lddy, static_cast<const T *>(pre), sh.m, sh.n, activation, dz);
+    Product16 g{};
+    g.b = dy;
+    g.ldb = lddy;
+    if ((activation != KMEANS_ACT_NONE || !rows16(dy, lddy)) && sh.m > 0 && (dx || dw)) {
+        T *dz = reinterpret_cast<T *>(ws + L.off_dz);
+        g.b = dz;
+        g.ldb = align_up(sh.n, 8);
+        e = launch_kernel(true, linear_slope_kernel<T>, dim3((unsigned)(sh.m < 8192 ? sh.m : 8192)), dim3(256), 0, s,
+                          static_cast<const T *>(dy), lddy, static_cast<const T *>(pre), sh.m, sh.n, activation, dz,
+                          g.ldb, call.first());
+    }
     if (e == cudaSuccess && db)
         e = launch_kernel(true, linear_bias_grad_kernel<T>, dim3((unsigned)((sh.n + 127) / 128), (unsigned)sh.n_experts),
                           dim3(128), 0, s, static_cast<const T *>(dy), lddy, static_cast<const T *>(pre), sh.offsets,
-                          sh.m, sh.n, activation, static_cast<T *>(db));
-    ProductParams p = product_params(sh);
-    p.b = dz;
-    p.ldb = sh.n;
+                          sh.m, sh.n, activation, static_cast<T *>(db), call.first());
     if (e == cudaSuccess && dx && sh.m > 0) {
-        p.a = w;
-        p.out = dx;
-        e = launch_product<T, Product::kRows>(sh, p, s);
+        g.a = w;
+        g.pitch_w = sh.k;
+        g.out = dx;
+        e = call.align_w(g);
+        if (e == cudaSuccess) e = call.template product<Product::kRows>(g);
     }
+    if (e == cudaSuccess && dw && sh.m == 0)
+        return cudaMemsetAsync(dw, 0, (size_t)sh.n_experts * (size_t)sh.n * (size_t)sh.k * sizeof(T), s);
     if (e == cudaSuccess && dw) {
-        p.a = x;
-        p.lda = ldx;
-        p.out = dw;
-        e = launch_product<T, Product::kWeights>(sh, p, s);
+        g.a = x;
+        g.lda = ldx;
+        g.out = dw;
+        e = call.align(g.a, g.lda, sh.m, sh.k, L.off_x);
+        if (e == cudaSuccess) e = call.template product<Product::kWeights>(g);
     }
     return e;
 }
@@ -261,13 +161,17 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
 }  // namespace
 
 LinearLayout linear_layout(bool grad, int64_t m, int64_t n, int64_t k, int64_t n_experts) {
-    (void)k;
-    (void)n_experts;
     LinearLayout L{};
     int64_t o = align_up((int64_t)sizeof(WsHeader), 1024);
+    L.off_x = o;
+    o = align_up(o + m * align_up(k, 8) * 2, 1024);
+    if (k % 8 != 0) {
+        L.off_w = o;
+        o = align_up(o + n_experts * n * align_up(k, 8) * 2, 1024);
+    }
     if (grad) {
         L.off_dz = o;
-        o = align_up(o + m * n * 2, 1024);
+        o = align_up(o + m * align_up(n, 8) * 2, 1024);
     }
     L.bytes = o;
     return L;
@@ -276,28 +180,28 @@ LinearLayout linear_layout(bool grad, int64_t m, int64_t n, int64_t k, int64_t n
 cudaError_t launch_linear(const LinearShape &sh, const void *x, int64_t ldx, const void *w, const void *bias,
                           const void *residual, int64_t ldr, int activation, void *y, void *pre,
                           const LinearLayout &L, uint8_t *ws, cudaStream_t s) {
-    (void)L;
-    cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(WsHeader), s);  // this call's status word
-    if (e != cudaSuccess || sh.m == 0) return e;
-    ProductParams p = product_params(sh);
-    p.a = w;
-    p.b = x;
-    p.ldb = ldx;
-    p.bias = bias;
-    p.residual = residual;
-    p.ldr = ldr;
-    p.activation = activation;
-    p.out = y;
-    p.pre = pre;
-    return sh.bf16 ? launch_product<__nv_bfloat16, Product::kForward>(sh, p, s)
-                   : launch_product<__half, Product::kForward>(sh, p, s);
+    if (sh.m == 0) return cudaMemsetAsync(ws, 0, sizeof(WsHeader), s);  // this call's status word
+    Product16 g{};
+    g.a = w;
+    g.pitch_w = sh.k;
+    g.b = x;
+    g.ldb = ldx;
+    g.bias = bias;
+    g.residual = residual;
+    g.ldr = ldr;
+    g.activation = activation;
+    g.out = y;
+    g.pre = pre;
+    return sh.bf16 ? forward_typed<__nv_bfloat16>(sh, g, L, ws, s) : forward_typed<__half>(sh, g, L, ws, s);
 }
 
 cudaError_t launch_linear_grad(const LinearShape &sh, const void *dy, int64_t lddy, const void *x, int64_t ldx,
                                const void *w, const void *pre, int activation, void *dx, void *dw, void *db,
                                const LinearLayout &L, uint8_t *ws, cudaStream_t s) {
-    const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(WsHeader), s);  // this call's status word
-    if (e != cudaSuccess) return e;
+    if (sh.m == 0) {
+        const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(WsHeader), s);  // this call's status word
+        if (e != cudaSuccess) return e;
+    }
     return sh.bf16 ? grad_typed<__nv_bfloat16>(sh, dy, lddy, x, ldx, w, pre, activation, dx, dw, db, L, ws, s)
                    : grad_typed<__half>(sh, dy, lddy, x, ldx, w, pre, activation, dx, dw, db, L, ws, s);
 }

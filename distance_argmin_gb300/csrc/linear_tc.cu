@@ -1,0 +1,578 @@
+// The experts' products on the sm_103a tensor cores.
+//
+// All three products are out(q, p) = sum_c A(p, c) B(q, c) with p contiguous in
+// the output (see linear_common.cuh).  The output's contiguous dimension is
+// always the MMA's M: 256 wide per CTA pair, and the rows are its N, 16 to 256
+// in steps of 32.  A group of few rows then costs an MMA of few columns, and
+// each tensor-memory lane holds one output feature, so that a warp's 32 lanes
+// are 32 neighbours in memory.
+//
+//              A (M = p)              B (N = q)            contraction
+//   forward    W_e, K-major           x,  K-major          input features
+//   rows       W_e, M contiguous      dz, K-major          output features
+//   weights    x,   M contiguous      dz, N contiguous     the expert's rows
+//
+// Everything is loaded by TMA with the 128-byte swizzle; an operand whose
+// contiguous dimension is not the contraction is fed to the MMA as it lies in
+// memory (the descriptor's other major mode), so nothing is transposed.
+// Ragged edges: the contraction's tail is the tensor maps' zero fill (W is a
+// 3-D map, so an expert's last features never run into the next expert's);
+// rows of the next expert that a tile of B covers are columns the epilogue does
+// not store; and where the rows are the contraction (weights) the relay warp
+// clears the rows past the expert's end in shared memory, in both operands
+// (a zero times another expert's infinity would be NaN).
+//
+// Structure: CTA pairs (cta_group::2), persistent over the units (256 features
+// x BN rows), a band of 8 feature tiles at a time so that the pairs running
+// together share rows and features in L2.
+//   warps 0-7   epilogue: tensor memory -> registers -> a padded shared-memory
+//               tile per warp -> rows of 32 neighbouring features: bias,
+//               activation, residual, one rounding, 16-byte stores
+//   warp 8      TMA producer (each CTA: its half of A and of B)
+//   warp 9      allocates tensor memory; in the even CTA issues the MMAs
+//   warp 10     relay: sees this CTA's stage land, clears rows if needed, and
+//               tells the even CTA
+// Two accumulators alternate, so a unit's epilogue overlaps the next one's
+// MMAs.  Every wait is bounded as in the assignment.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "assign_common.cuh"
+#include "linear_common.cuh"
+#include "ptx.cuh"
+#include "tensor_map.cuh"
+
+namespace km {
+
+namespace lt {
+constexpr int BP = 256;            // features per unit (UMMA M of the pair)
+constexpr int BP_CTA = BP / 2;
+constexpr int BK = 64;             // contraction per stage: 128 bytes of 16-bit values
+constexpr int EPI_WARPS = 8;
+constexpr int WARP_TMA = EPI_WARPS, WARP_MMA = WARP_TMA + 1, WARP_RELAY = WARP_TMA + 2;
+constexpr int THREADS = (WARP_RELAY + 1) * 32;
+constexpr int EPI_ROWS = 16;       // rows staged at a time per epilogue warp
+constexpr int EPI_PITCH = 36;      // floats: 8 rows x 32 bytes then hit distinct banks
+constexpr int STAGING = EPI_WARPS * EPI_ROWS * EPI_PITCH * 4;
+constexpr int BAND = 8;            // feature tiles per raster band
+constexpr int SMEM_LIMIT = 232448;
+constexpr int BAR_BYTES = 512;
+
+template <int BN>
+struct Cfg {
+    static constexpr int A_BYTES = BP_CTA * BK * 2;
+    static constexpr int B_BYTES = BN / 2 * BK * 2;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int STAGES = BN >= 256 ? 6 : BN >= 128 ? 8 : 9;
+    static constexpr int STAGING_BASE = STAGES * STAGE;
+    static constexpr int BAR_BASE = STAGING_BASE + STAGING;
+    static constexpr int TABLE_BASE = BAR_BASE + BAR_BYTES;
+    static constexpr int TMEM_COLS = 2 * BN;  // >= 64
+    static constexpr int FULL = 0, READY = STAGES, EMPTY = 2 * STAGES, T_FULL = 3 * STAGES, T_EMPTY = T_FULL + 2,
+                         DRAIN = T_EMPTY + 2, NUM_BARS = DRAIN + 1;
+    static constexpr int smem_bytes(int n_experts) { return TABLE_BASE + 2 * (n_experts + 2) * 4 + 1024; }
+    static_assert(NUM_BARS * 8 + 16 <= BAR_BYTES, "barriers fit");
+    static_assert(STAGE % 1024 == 0 && STAGING % 1024 == 0, "stages stay 1 KiB aligned");
+    static_assert(TABLE_BASE + 2 * (KMEANS_LINEAR_MAX_EXPERTS + 2) * 4 + 1024 <= SMEM_LIMIT, "fits");
+};
+}  // namespace lt
+
+struct LinearTcParams {
+    const int32_t *offsets;
+    int64_t m;
+    int n_experts;
+    int cols;         // size of the output's contiguous dimension
+    int num_p;        // feature tiles
+    int out_rows;     // weights: output features of an expert
+    int contraction;  // forward, rows
+    const void *bias, *residual;
+    int64_t ldr;
+    int activation;
+    void *out, *pre;
+    int wide_out, wide_res;  // 16-byte accesses allowed
+    uint32_t *status;
+    int clear;  // first kernel of the call: it clears the status word
+};
+
+// The units: expert by expert, bands of BAND feature tiles, in a band the
+// feature tiles of one row tile after the other.  `edges[e]` is expert e's
+// first row, `tiles[e]` the row tiles before it; for the row products entry
+// n_experts is the group of rows that belong to no expert.
+struct Unit {
+    int expert, p0, q0, qn;  // q0: first output row (row products: of the matrix, weights: of the expert)
+    int c0, c1;              // contraction range (rows of x for weights)
+};
+
+template <Product MODE, int BN>
+struct Units {
+    const LinearTcParams &p;
+    const int *edges, *tiles;
+    int64_t total;
+    int e = 0;
+
+    __device__ Units(const LinearTcParams &p_, const int *edges_, const int *tiles_)
+        : p(p_), edges(edges_), tiles(tiles_) {
+        total = MODE == Product::kWeights ? (int64_t)p.n_experts * p.num_p * row_tiles()
+                                          : (int64_t)tiles[p.n_experts + 1] * p.num_p;
+    }
+    __device__ int row_tiles() const { return (p.out_rows + BN - 1) / BN; }
+
+    // `u` never decreases from call to call.
+    __device__ Unit at(int64_t u) {
+        int per;
+        if (MODE == Product::kWeights) {
+            per = row_tiles();
+            e = (int)(u / ((int64_t)per * p.num_p));
+            u -= (int64_t)e * per * p.num_p;
+        } else {
+            while (u >= (int64_t)tiles[e + 1] * p.num_p) ++e;
+            u -= (int64_t)tiles[e] * p.num_p;
+            per = tiles[e + 1] - tiles[e];
+        }
+        const int64_t band_units = (int64_t)lt::BAND * per;
+        const int band = (int)(u / band_units);
+        const int r = (int)(u - band * band_units);
+        const int wide = min(lt::BAND, p.num_p - band * lt::BAND);
+        const int q = r / wide;
+        Unit t;
+        t.expert = e;
+        t.p0 = (band * lt::BAND + r - q * wide) * lt::BP;
+        if (MODE == Product::kWeights) {
+            t.q0 = q * BN;
+            t.qn = min(BN, p.out_rows - t.q0);
+            t.c0 = edges[e];
+            t.c1 = edges[e + 1];
+        } else {
+            t.q0 = edges[e] + q * BN;
+            t.qn = min(BN, edges[e + 1] - t.q0);
+            t.c0 = 0;
+            t.c1 = e < p.n_experts ? p.contraction : 0;
+        }
+        return t;
+    }
+};
+
+// One warp fills the tables: a running maximum of the offsets, cut to m, and
+// the row tiles before each group.
+template <Product MODE, int BN>
+__device__ void fill_tables(const LinearTcParams &p, int *edges, int *tiles, int lane) {
+    int last = 0, count = 0;
+    if (lane == 0) edges[0] = tiles[0] = 0;
+    for (int e0 = 0; e0 <= p.n_experts; e0 += 32) {
+        const int e = e0 + lane;  // group e ends at edge e + 1
+        int end = 0;
+        if (e < p.n_experts) end = p.offsets ? max(0, (int)min((int64_t)p.offsets[e + 1], p.m)) : (int)p.m;
+        if (e == p.n_experts) end = (int)p.m;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(0xffffffffu, end, o));
+        end = max(end, last);
+        int start = __shfl_up_sync(0xffffffffu, end, 1);
+        if (lane == 0) start = last;
+        int t = (end - start + BN - 1) / BN;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += v;
+        }
+        t += count;
+        if (e <= p.n_experts) {
+            edges[e + 1] = end;
+            tiles[e + 1] = t;
+        }
+        last = __shfl_sync(0xffffffffu, end, 31);
+        count = __shfl_sync(0xffffffffu, t, 31);
+    }
+}
+
+// Rows [q, q + 8 rows of the lane groups): one warp's staged values of 32
+// features leave for memory.  Lane group l / 4 takes a row, lane l % 4 eight
+// of its features.
+template <Product MODE, typename T, int ACT>
+__device__ __forceinline__ void store_rows(const LinearTcParams &p, const float *staged, int64_t out_row, int rows,
+                                           int f, bool zero, int lane) {
+#pragma unroll
+    for (int i = 0; i < lt::EPI_ROWS / 8; ++i) {
+        const int r = (lane >> 2) + 8 * i;
+        if (r >= rows || f >= p.cols) continue;
+        const float4 lo = *reinterpret_cast<const float4 *>(staged + r * lt::EPI_PITCH + (lane & 3) * 8);
+        const float4 hi = *reinterpret_cast<const float4 *>(staged + r * lt::EPI_PITCH + (lane & 3) * 8 + 4);
+        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        const int64_t row = out_row + r;
+        const int left = min(8, p.cols - f);
+        T *out = static_cast<T *>(p.out) + row * p.cols + f;
+        if constexpr (MODE == Product::kForward) {
+            if (p.pre) {
+                T *pre = static_cast<T *>(p.pre) + row * p.cols + f;
+                if (p.wide_out && left == 8) {
+                    *reinterpret_cast<uint4 *>(pre) = make_uint4(narrow2<T>(v[0], v[1]), narrow2<T>(v[2], v[3]),
+                                                                 narrow2<T>(v[4], v[5]), narrow2<T>(v[6], v[7]));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (c < left) pre[c] = narrow<T>(v[c]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = activate<ACT>(v[c]);
+            if (p.residual && !zero) {
+                const T *res = static_cast<const T *>(p.residual) + row * p.ldr + f;
+                if (p.wide_res && left == 8) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(res);
+                    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 a = widen2<T>(words[c]);
+                        v[2 * c] += a.x;
+                        v[2 * c + 1] += a.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (c < left) v[c] += widen(res[c]);
+                }
+            }
+        }
+        if (p.wide_out && left == 8) {
+            *reinterpret_cast<uint4 *>(out) = make_uint4(narrow2<T>(v[0], v[1]), narrow2<T>(v[2], v[3]),
+                                                         narrow2<T>(v[4], v[5]), narrow2<T>(v[6], v[7]));
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < left) out[c] = narrow<T>(v[c]);
+        }
+    }
+}
+
+template <Product MODE, int BN, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
+    linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const LinearTcParams p) {
+    using C = lt::Cfg<BN>;
+    constexpr bool A_MN = MODE != Product::kForward, B_MN = MODE == Product::kWeights;
+    static_assert(!B_MN || BN >= 128, "an N-contiguous operand comes in chunks of 64 per CTA");
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    const uint32_t sbase = smem_addr(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::BAR_BASE);
+    auto bar = [&](int i) { return smem_addr(bars + i); };
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + C::NUM_BARS);
+    int *edges = reinterpret_cast<int *>(smem + C::TABLE_BASE);
+    int *tiles = edges + p.n_experts + 2;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(bar(C::FULL + s), 1);
+            mbar_init(bar(C::READY + s), 2);  // the relay of each CTA (even CTA's copy)
+            mbar_init(bar(C::EMPTY + s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(C::T_FULL + b), 1);
+            mbar_init(bar(C::T_EMPTY + b), 2 * lt::EPI_WARPS);  // both CTAs' epilogue warps (even CTA's copy)
+        }
+        mbar_init(bar(C::DRAIN), 1);
+        fence_barrier_init();
+    }
+    if (warp == lt::WARP_MMA) {
+        tmem_alloc_pair(smem_addr(tmem_holder), C::TMEM_COLS);
+        tmem_relinquish_pair();
+        tc_fence_before();
+    }
+    griddep_wait();
+    // this call's status word: a wait of this launch runs out two seconds from
+    // now at the earliest, long after the first block has cleared it
+    if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
+    if (warp == 0) fill_tables<MODE, BN>(p, edges, tiles, lane);
+    cluster_sync();  // barriers, tensor memory and tables exist in both CTAs
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    Units<MODE, BN> units(p, edges, tiles);
+
+    if (warp < lt::EPI_WARPS) {
+        // ------------------------------------------------------------ epilogue
+        const int quarter = warp & 3, part = warp >> 2;
+        float *staged = reinterpret_cast<float *>(smem + C::STAGING_BASE) + warp * lt::EPI_ROWS * lt::EPI_PITCH;
+        int use = 0;
+        for (int64_t u = pair; u < units.total; u += num_pairs) {
+            const Unit t = units.at(u);
+            const bool zero = t.c1 <= t.c0;  // nothing to multiply: rows of no expert, experts without rows
+            const int buf = use & 1;
+            if (!zero) {
+                if (!mbar_wait_warp(bar(C::T_FULL + buf), (use >> 1) & 1, p.status)) break;
+                tc_fence_after();
+            }
+            const uint32_t acc = tmem_base + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
+            const int f = t.p0 + rank * lt::BP_CTA + quarter * 32;  // this warp's first feature
+            float bias = 0.f;
+            if (MODE == Product::kForward && p.bias && !zero && f + lane < p.cols)
+                bias = widen(static_cast<const T *>(p.bias)[(int64_t)t.expert * p.cols + f + lane]);
+            const int64_t out_row = MODE == Product::kWeights ? (int64_t)t.expert * p.out_rows + t.q0 : t.q0;
+#pragma unroll 1
+            for (int c0 = part * (BN / 2); c0 < min(t.qn, (part + 1) * (BN / 2)); c0 += lt::EPI_ROWS) {
+                float v[lt::EPI_ROWS];
+                if (zero) {
+#pragma unroll
+                    for (int i = 0; i < lt::EPI_ROWS; ++i) v[i] = 0.f;
+                } else {
+                    tmem_ld_32x32b_x16(acc + (uint32_t)c0, v);
+                }
+                __syncwarp();  // the previous rows have been read
+#pragma unroll
+                for (int i = 0; i < lt::EPI_ROWS; ++i) staged[i * lt::EPI_PITCH + lane] = v[i] + bias;
+                __syncwarp();
+                const int rows = t.qn - c0;
+                if constexpr (MODE == Product::kForward) {
+                    with_activation(p.activation, [&](auto a) {
+                        store_rows<MODE, T, decltype(a)::value>(p, staged, out_row + c0, rows, f + (lane & 3) * 8, zero,
+                                                                lane);
+                    });
+                } else {
+                    store_rows<MODE, T, KMEANS_ACT_NONE>(p, staged, out_row + c0, rows, f + (lane & 3) * 8, zero, lane);
+                }
+            }
+            if (!zero) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_cta(bar(C::T_EMPTY + buf), 0));
+                ++use;
+            }
+        }
+    } else if (warp == lt::WARP_TMA) {
+        // ------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            tma_prefetch_desc(&tmA);
+            tma_prefetch_desc(&tmB);
+            int it = 0;
+            bool ok = true;
+            for (int64_t u = pair; u < units.total && ok; u += num_pairs) {
+                const Unit t = units.at(u);
+                const int pa = t.p0 + rank * lt::BP_CTA;
+                // the MMA's N is cut to the rows that exist (a multiple of 32);
+                // each CTA holds half of it
+                const int qb = t.q0 + rank * (MODE == Product::kWeights ? BN / 2 : (min(BN, (t.qn + 31) & ~31) >> 1));
+                for (int c = t.c0; c < t.c1; c += lt::BK, ++it) {
+                    const int s = it % C::STAGES;
+                    if (!mbar_wait(bar(C::EMPTY + s), ((it / C::STAGES) & 1) ^ 1, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES, full = bar(C::FULL + s);
+                    mbar_arrive_expect_tx(full, C::STAGE);
+                    if constexpr (MODE == Product::kForward) {
+                        tma_load_3d(sa, &tmA, full, c, pa, t.expert);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < lt::BP_CTA / 64; ++h) {
+                            if constexpr (MODE == Product::kRows)
+                                tma_load_3d(sa + h * (64 * lt::BK * 2), &tmA, full, pa + h * 64, c, t.expert);
+                            else
+                                tma_load_2d(sa + h * (64 * lt::BK * 2), &tmA, full, pa + h * 64, c);
+                        }
+                    }
+                    if constexpr (B_MN) {
+#pragma unroll
+                        for (int h = 0; h < BN / 2 / 64; ++h)
+                            tma_load_2d(sb + h * (64 * lt::BK * 2), &tmB, full, qb + h * 64, c);
+                    } else {
+                        tma_load_2d(sb, &tmB, full, c, qb);
+                    }
+                }
+            }
+            if (!ok) {
+                // let copies already in flight land before the CTA exits
+                for (int j = max(0, it - C::STAGES); j < it; ++j)
+                    mbar_wait_drain(bar(C::FULL + (j % C::STAGES)), (j / C::STAGES) & 1);
+            }
+        }
+    } else if (warp == lt::WARP_RELAY) {
+        // -------------------------------------------------------------- relay
+        int it = 0;
+        bool ok = true;
+        for (int64_t u = pair; u < units.total && ok; u += num_pairs) {
+            const Unit t = units.at(u);
+            for (int c = t.c0; c < t.c1; c += lt::BK, ++it) {
+                const int s = it % C::STAGES;
+                if (!mbar_wait_warp(bar(C::FULL + s), (it / C::STAGES) & 1, p.status)) {
+                    ok = false;
+                    break;
+                }
+                if (MODE == Product::kWeights && t.c1 - c < lt::BK) {
+                    // rows past the expert's end: every 64-value chunk of both
+                    // operands holds them as whole 128-byte lines
+                    uint8_t *st = smem + s * C::STAGE;
+                    constexpr int CHUNKS = C::STAGE / (64 * lt::BK * 2);
+                    for (int i = (t.c1 - c) * 8 + lane; i < lt::BK * 8; i += 32)
+#pragma unroll
+                        for (int h = 0; h < CHUNKS; ++h)
+                            *reinterpret_cast<uint4 *>(st + h * (64 * lt::BK * 2) + i * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive_cluster(map_to_cta(bar(C::READY + s), 0));
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- MMA issue
+        if (lane == 0 && rank == 0) {
+            int it = 0, use = 0;
+            bool ok = true;
+            for (int64_t u = pair; u < units.total && ok; u += num_pairs) {
+                const Unit t = units.at(u);
+                if (t.c1 <= t.c0) continue;
+                const int n = MODE == Product::kWeights ? BN : min(BN, (t.qn + 31) & ~31);
+                const uint32_t idesc = umma_idesc_16_f32(sizeof(T) == 2 && !std::is_same<T, __half>::value, A_MN, B_MN,
+                                                         lt::BP, n);
+                const int buf = use & 1;
+                if (!mbar_wait_cluster(bar(C::T_EMPTY + buf), ((use >> 1) & 1) ^ 1, p.status)) break;
+                tc_fence_after();
+                const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
+                for (int c = t.c0; c < t.c1; c += lt::BK, ++it) {
+                    const int s = it % C::STAGES;
+                    const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES;
+                    // 16 values of the contraction: 32 bytes along a K-major
+                    // row, or 16 lines of 128 bytes
+                    uint64_t da[4], db[4];
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        da[kk] = A_MN ? umma_smem_desc_mn(sa + kk * 2048, 64 * lt::BK * 2, 1024)
+                                      : umma_smem_desc(sa + kk * 32, 1024, kLayoutSW128);
+                        db[kk] = B_MN ? umma_smem_desc_mn(sb + kk * 2048, 64 * lt::BK * 2, 1024)
+                                      : umma_smem_desc(sb + kk * 32, 1024, kLayoutSW128);
+                    }
+                    if (!mbar_wait_cluster(bar(C::READY + s), (it / C::STAGES) & 1, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_ss_pair(acc, da[kk], db[kk], idesc, (c != t.c0 || kk != 0) ? 1u : 0u);
+                    mma_commit_pair_multicast(bar(C::EMPTY + s), 0x3);
+                }
+                if (!ok) break;
+                mma_commit_pair_multicast(bar(C::T_FULL + buf), 0x3);
+                ++use;
+            }
+            // no MMA may still be writing tensor memory when it is released
+            mma_commit_pair(bar(C::DRAIN));
+            mbar_wait_drain(bar(C::DRAIN), 0);
+        }
+    }
+
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while its peer may still signal it
+    if (warp == lt::WARP_MMA) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+namespace {
+
+bool encode(CUtensorMap *map, bool bf16, const void *base, int rank, const uint64_t *dims, const uint64_t *pitch_elems,
+            const uint32_t *box) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t d[3], strides[2];
+    cuuint32_t b[3], one[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i) strides[i - 1] = pitch_elems[i - 1] * 2;
+    }
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+               const_cast<void *>(base), d, strides, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Product MODE, int BN, typename T>
+cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcParams &p, cudaStream_t s) {
+    using C = lt::Cfg<BN>;
+    static std::once_flag once[kMaxDevices];
+    static std::atomic<int> err[kMaxDevices];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const int slot = dev >= 0 && dev < kMaxDevices ? dev : 0;
+    once_per_device(once, [&] {
+        err[slot].store((int)cudaFuncSetAttribute(linear_tc_kernel<MODE, BN, T>,
+                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, lt::SMEM_LIMIT));
+    });
+    if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
+
+    CUtensorMap tmA, tmB;
+    bool ok;
+    if (MODE == Product::kWeights) {
+        const uint64_t da[2] = {(uint64_t)sh.k, (uint64_t)sh.m}, pa[1] = {(uint64_t)g.lda};
+        const uint64_t db[2] = {(uint64_t)sh.n, (uint64_t)sh.m}, pb[1] = {(uint64_t)g.ldb};
+        const uint32_t box[2] = {64, lt::BK};
+        ok = encode(&tmA, sh.bf16, g.a, 2, da, pa, box) && encode(&tmB, sh.bf16, g.b, 2, db, pb, box);
+    } else {
+        const uint64_t da[3] = {(uint64_t)sh.k, (uint64_t)sh.n, (uint64_t)sh.n_experts};
+        const uint64_t pa[2] = {(uint64_t)g.pitch_w, (uint64_t)(g.pitch_w * sh.n)};
+        const uint32_t ba[3] = {64, MODE == Product::kForward ? (uint32_t)lt::BP_CTA : (uint32_t)lt::BK, 1};
+        const uint64_t db[2] = {(uint64_t)p.contraction, (uint64_t)sh.m}, pb[1] = {(uint64_t)g.ldb};
+        const uint32_t bb[2] = {lt::BK, BN / 2};
+        ok = encode(&tmA, sh.bf16, g.a, 3, da, pa, ba) && encode(&tmB, sh.bf16, g.b, 2, db, pb, bb);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+
+    // at most one unit per row tile, expert and feature tile
+    const int64_t row_tiles = MODE == Product::kWeights ? (sh.n + BN - 1) / BN * sh.n_experts
+                                                        : (sh.m + BN - 1) / BN + (sh.offsets ? sh.n_experts : 0);
+    const int64_t most = device_sm_count() / 2, units = row_tiles * p.num_p;
+    const unsigned pairs = (unsigned)(units < most ? units : most);
+    return launch_kernel(true, linear_tc_kernel<MODE, BN, T>, dim3(2 * (pairs ? pairs : 1)), dim3(lt::THREADS),
+                         C::smem_bytes(sh.n_experts), s, tmA, tmB, p);
+}
+
+template <Product MODE, int BN>
+cudaError_t launch_typed(const LinearShape &sh, const Product16 &g, const LinearTcParams &p, cudaStream_t s) {
+    return sh.bf16 ? launch_tc<MODE, BN, __nv_bfloat16>(sh, g, p, s) : launch_tc<MODE, BN, __half>(sh, g, p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product16 &g, uint32_t *status, bool clear,
+                             cudaStream_t s) {
+    LinearTcParams p{};
+    p.offsets = sh.offsets;
+    p.m = sh.m;
+    p.n_experts = sh.n_experts;
+    p.cols = (int)(mode == Product::kForward ? sh.n : sh.k);
+    p.num_p = (p.cols + lt::BP - 1) / lt::BP;
+    p.out_rows = (int)sh.n;
+    p.contraction = (int)(mode == Product::kForward ? sh.k : sh.n);
+    p.bias = g.bias;
+    p.residual = g.residual;
+    p.ldr = g.ldr;
+    p.activation = g.activation;
+    p.out = g.out;
+    p.pre = g.pre;
+    p.wide_out = rows16(g.out, p.cols) && (!g.pre || rows16(g.pre, p.cols));
+    p.wide_res = g.residual && rows16(g.residual, g.ldr);
+    p.status = status;
+    p.clear = clear;
+    if (mode == Product::kWeights) return launch_typed<Product::kWeights, 256>(sh, g, p, s);
+    // rows per unit: about an expert's average rows, so that small groups do
+    // not load and multiply rows of their neighbours
+    const int64_t rows = sh.m / sh.n_experts;
+    if (mode == Product::kForward) {
+        if (rows > 128) return launch_typed<Product::kForward, 256>(sh, g, p, s);
+        if (rows > 64) return launch_typed<Product::kForward, 128>(sh, g, p, s);
+        return launch_typed<Product::kForward, 64>(sh, g, p, s);
+    }
+    if (rows > 128) return launch_typed<Product::kRows, 256>(sh, g, p, s);
+    if (rows > 64) return launch_typed<Product::kRows, 128>(sh, g, p, s);
+    return launch_typed<Product::kRows, 64>(sh, g, p, s);
+}
+
+}  // namespace km

@@ -532,7 +532,10 @@ size_t kmeans_linear_workspace_bytes(int grad, int64_t m, int64_t n, int64_t k, 
  * (n_experts + 1, ascending from 0, at most m) may be NULL when n_experts is
  * 1: an ordinary dense layer.  Offsets that run backwards or past m are cut
  * to what fits.  KMEANS_F16 or KMEANS_BF16; n_experts <=
- * KMEANS_LINEAR_MAX_EXPERTS; m, n, k < 2^31, n_experts * n < 2^31, n, k >= 1.
+ * KMEANS_LINEAR_MAX_EXPERTS; m, n, k < 2^31, n_experts * n < 2^31, n, k >= 1;
+ * w starts on 16 bytes (KMEANS_ERR_UNSUPPORTED otherwise).  Rows of x or w
+ * that do not all start on 16 bytes (k or ldx not a multiple of 8, or an odd
+ * start of x) are first copied into the workspace.
  * y must not alias an input, except residual when ldr == n. */
 int kmeans_linear(const void *x, int64_t ldx, const void *w, const void *bias, const void *residual,
                   int64_t ldr, int dtype, int activation, const int32_t *offsets, int64_t m, int64_t n,

@@ -66,13 +66,14 @@ def test_expert_entry_points_validate_on_the_host(km):
     assert lin(act=5) == BAD and lin(act=-1) == BAD and lin(dt=7) == BAD and lin(res=F, ldr=63) == BAD
     assert lin(E=2) == BAD  # experts without offsets
     assert lin(off=odd, E=2) == BAD and lin(x=odd) == BAD and lin(pre=odd) == BAD
-    assert lin(dt=0) == NO and lin(off=F, E=1025) == NO
+    assert lin(dt=0) == NO and lin(off=F, E=1025) == NO and lin(w=ctypes.c_void_p(0x10008)) == NO
     assert lin(wsb=need - 1) == km.KMEANS_ERR_WORKSPACE and lin(ws=None) == km.KMEANS_ERR_WORKSPACE
     grad = lambda dy=F, ld=64, x=F, ldx=32, w=F, pre=F, dt=1, act=4, off=None, m=100, n=64, k=32, E=1, dx=F, dw=F, \
         db=F, wsb=1 << 40: lib.kmeans_linear_grad(dy, ld, x, ldx, w, pre, dt, act, off, m, n, k, E, dx, dw, db, W, wsb,
                                                   None)
     assert grad(dy=None) == BAD and grad(ld=63) == BAD and grad(pre=None) == BAD and grad(x=None) == BAD
     assert grad(w=None) == BAD and grad(db=odd) == BAD and grad(dt=0) == NO
+    assert grad(w=ctypes.c_void_p(0x10008)) == NO
     assert grad(wsb=need_g - 1) == km.KMEANS_ERR_WORKSPACE
 
 

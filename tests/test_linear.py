@@ -317,7 +317,10 @@ def test_strided_and_unaligned_inputs(gpu_lib, m, dtype):
     off.copy_(w)
     x = normal((m, k), dtype, 1)
     ref, _ = gpu_lib.kmeans_linear(x, w)
-    assert torch.equal(gpu_lib.kmeans_linear(x, off)[0], ref)
+    for call in (lambda: gpu_lib.kmeans_linear(x, off), lambda: gpu_lib.kmeans_linear_grad(ref, x, off)):
+        with pytest.raises(gpu_lib.KMeansError) as err:  # w has to start on 16 bytes
+            call()
+        assert err.value.status == gpu_lib.KMEANS_ERR_UNSUPPORTED
     out = torch.empty(m * n + 1, dtype=dtype, device="cuda")[1:].view(m, n)
     assert torch.equal(gpu_lib.kmeans_linear(x, w, y=out)[0], ref)
 
