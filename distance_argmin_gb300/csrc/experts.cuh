@@ -47,6 +47,7 @@ struct LinearLayout {
     int64_t off_x;   // x with its rows on 16 bytes, where the caller's are not
     int64_t off_w;   // w likewise (0: its rows are a multiple of 16 bytes)
     int64_t off_dz;  // dy after the activation's slope, rows on 16 bytes (gradient)
+    int64_t off_partial;  // the bias gradient's sums per row tile (gradient)
     int64_t bytes;
 };
 
@@ -60,31 +61,61 @@ cudaError_t launch_linear_grad(const LinearShape &sh, const void *dy, int64_t ld
                                const LinearLayout &L, uint8_t *ws, cudaStream_t s);
 
 // --------------------------------------------------------- shared arithmetic
-// The activations and their slopes, in float32.  exp is the accurate expf:
-// the products' epilogues have time for it, and a value that is kept in 16
-// bits should carry that rounding alone.
+// The activations and their slopes in float32, on the hardware's exp2 and
+// reciprocal (a few 2^-23 each): the products' epilogue has some twenty
+// instructions per value before it, not the loads, sets the pace.
+//   z Phi(z)        Phi through erf(x) = 1 - (a1 t + .. + a5 t^5) exp(-x^2),
+//                   t = 1 / (1 + p x), x >= 0: Abramowitz and Stegun, formula
+//                   7.1.26, within 1.5e-7; the slope's density shares the exp
+//   its tanh form   (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
+// Each is within 2^-19 (|z| + 1) of its formula, below the last bit that 16
+// bits keep, except next to a zero of the result.
+__device__ __forceinline__ float logistic(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+// Phi(z), and exp(-z^2 / 2) beside it
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+    const float x = fabsf(z) * 0.70710678118654752f;
+    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+    e = __expf(-x * x);
+    float poly = fmaf(t, 1.061405429f, -1.453152027f);
+    poly = fmaf(t, poly, 1.421413741f);
+    poly = fmaf(t, poly, -0.284496736f);
+    poly = fmaf(t, poly, 0.254829592f);
+    const float tail = 0.5f * poly * t * e;  // (1 - erf x) / 2
+    return z < 0.f ? tail : 1.f - tail;
+}
+
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == KMEANS_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
-    if constexpr (ACT == KMEANS_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    if constexpr (ACT == KMEANS_ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, e);
+    }
     if constexpr (ACT == KMEANS_ACT_GELU_TANH)
-        return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-    if constexpr (ACT == KMEANS_ACT_SILU) return z / (1.f + expf(-z));
+        return z * logistic(z * fmaf(0.0713548162726f, z * z, 1.5957691216057308f));
+    if constexpr (ACT == KMEANS_ACT_SILU) return z * logistic(z);
     return z;
 }
 
 template <int ACT>
 __device__ __forceinline__ float slope(float z) {
     if constexpr (ACT == KMEANS_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-    if constexpr (ACT == KMEANS_ACT_GELU)
-        return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+    if constexpr (ACT == KMEANS_ACT_GELU) {
+        float e;
+        const float c = normal_cdf(z, e);
+        return fmaf(z * 0.39894228040143268f, e, c);
+    }
     if constexpr (ACT == KMEANS_ACT_GELU_TANH) {
-        const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-        return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.79788456080286536f * (1.f + 0.134145f * z * z);
+        // u' = 2 sqrt(2 / pi) (1 + 3 a z^2); far out s (1 - s) is 0 while z u'
+        // may be infinite, hence the cut
+        const float zz = fminf(z * z, 1e4f);
+        const float s = logistic(z * fmaf(0.0713548162726f, z * z, 1.5957691216057308f));
+        return fmaf(z * s * (1.f - s), fmaf(0.2140644488178f, zz, 1.5957691216057308f), s);
     }
     if constexpr (ACT == KMEANS_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-z));
-        return s * (1.f + z * (1.f - s));
+        const float s = logistic(z);
+        return fmaf(z * s, 1.f - s, s);
     }
     return 1.f;
 }

@@ -12,16 +12,6 @@ namespace km {
 
 namespace {
 
-__device__ __forceinline__ float slope_as(int act, float z) {
-    switch (act) {
-        case KMEANS_ACT_RELU: return slope<KMEANS_ACT_RELU>(z);
-        case KMEANS_ACT_GELU: return slope<KMEANS_ACT_GELU>(z);
-        case KMEANS_ACT_GELU_TANH: return slope<KMEANS_ACT_GELU_TANH>(z);
-        case KMEANS_ACT_SILU: return slope<KMEANS_ACT_SILU>(z);
-        default: return 1.f;
-    }
-}
-
 // dst(r, c) = src(r, c) with the rows of dst on 16 bytes.
 template <typename T>
 __global__ void linear_align_kernel(const T *src, int64_t lds, int64_t rows, int64_t cols, T *dst, int64_t ldd,
@@ -32,45 +22,174 @@ __global__ void linear_align_kernel(const T *src, int64_t lds, int64_t rows, int
         for (int64_t c = threadIdx.x; c < cols; c += blockDim.x) dst[r * ldd + c] = src[r * lds + c];
 }
 
-// dz = dy act'(pre), rounded to the matrices' type.
-template <typename T>
-__global__ void linear_slope_kernel(const T *dy, int64_t lddy, const T *pre, int64_t m, int64_t n, int act, T *dz,
-                                    int64_t ldz, uint32_t *clear) {
-    griddep_wait();
-    if (clear && blockIdx.x == 0 && threadIdx.x == 0) *clear = 0u;
-    for (int64_t r = blockIdx.x; r < m; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < n; c += blockDim.x) {
-            const float g = widen(dy[r * lddy + c]);
-            dz[r * ldz + c] = narrow<T>(act == KMEANS_ACT_NONE ? g : g * slope_as(act, widen(pre[r * n + c])));
+// dz = dy act'(pre), rounded to the matrices' type, and the bias gradient's
+// partial sums from the same read.  A block takes 64 rows of one expert by 256
+// columns: a lane 8 columns (16 bytes where the rows allow), a warp every
+// eighth row.  Its column sums of the unrounded values go to one row of
+// `partial` per row tile; linear_bias_join_kernel adds an expert's in order, so
+// the result does not depend on the schedule.
+constexpr int kSlopeRows = 64;
+constexpr int kSlopeCols = 256;
+constexpr int kSlopeThreads = 256;
+
+// Row tile `u` counted over the experts (whole warp): its expert, its rows, and
+// the tiles before the expert's first.
+struct RowTile {
+    int expert, before;
+    int64_t r0, r1;
+};
+
+__device__ bool find_row_tile(const int32_t *offsets, int n_experts, int64_t m, int u, RowTile &t) {
+    const int lane = threadIdx.x & 31;
+    int last = 0, count = 0;
+    for (int e0 = 0; e0 < n_experts; e0 += 32) {
+        const int e = e0 + lane;
+        int end = 0;
+        if (e < n_experts) end = offsets ? max(0, (int)min((int64_t)offsets[e + 1], m)) : (int)m;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(0xffffffffu, end, o));
+        end = max(end, last);
+        int start = __shfl_up_sync(0xffffffffu, end, 1);
+        if (lane == 0) start = last;
+        const int own = (end - start + kSlopeRows - 1) / kSlopeRows;
+        int upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
         }
+        upto += count;
+        const uint32_t past = __ballot_sync(0xffffffffu, u < upto);
+        if (past) {
+            const int who = __ffs(past) - 1;
+            t.expert = e0 + who;
+            t.before = __shfl_sync(0xffffffffu, upto - own, who);
+            t.r0 = __shfl_sync(0xffffffffu, start, who) + (int64_t)(u - t.before) * kSlopeRows;
+            t.r1 = min(t.r0 + kSlopeRows, (int64_t)__shfl_sync(0xffffffffu, end, who));
+            return true;
+        }
+        last = __shfl_sync(0xffffffffu, end, 31);
+        count = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
+
+template <bool WIDE, typename T>
+__device__ __forceinline__ void load8(const T *p, int left, float (&v)[8]) {
+    if constexpr (WIDE) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float2 a = widen2<T>(words[c]);
+            v[2 * c] = a.x;
+            v[2 * c + 1] = a.y;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = c < left ? widen(p[c]) : 0.f;
+    }
+}
+
+template <bool WIDE, typename T>
+__global__ void __launch_bounds__(kSlopeThreads) linear_slope_kernel(const T *dy, int64_t lddy, const T *pre,
+                                                                     const int32_t *offsets, int n_experts, int64_t m,
+                                                                     int64_t n, int act, T *dz, int64_t ldz,
+                                                                     float *partial, uint32_t *clear) {
+    __shared__ float sums[kSlopeThreads / 32][kSlopeCols];
+    griddep_wait();
+    if (clear && (blockIdx.x | blockIdx.y | threadIdx.x) == 0u) *clear = 0u;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    RowTile t;
+    if (!find_row_tile(offsets, n_experts, m, blockIdx.y, t)) return;
+    const int64_t c0 = (int64_t)blockIdx.x * kSlopeCols + lane * 8;
+    const int left = (int)min((int64_t)8, n - c0);
+    float sum[8] = {};
+    if (left > 0)
+        with_activation(act, [&](auto a) {
+            constexpr int ACT = decltype(a)::value;
+#pragma unroll 4
+            for (int64_t r = t.r0 + warp; r < t.r1; r += kSlopeThreads / 32) {
+                float g[8], z[8];
+                load8<WIDE>(dy + r * lddy + c0, left, g);
+                if constexpr (ACT != KMEANS_ACT_NONE) load8<WIDE>(pre + r * n + c0, left, z);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    if constexpr (ACT != KMEANS_ACT_NONE) g[c] *= slope<ACT>(z[c]);
+                    sum[c] += g[c];
+                }
+                if (dz) {
+                    T *out = dz + r * ldz + c0;  // dz's rows always start on 16 bytes
+                    if (left == 8) {
+                        *reinterpret_cast<uint4 *>(out) = make_uint4(narrow2<T>(g[0], g[1]), narrow2<T>(g[2], g[3]),
+                                                                     narrow2<T>(g[4], g[5]), narrow2<T>(g[6], g[7]));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            if (c < left) out[c] = narrow<T>(g[c]);
+                    }
+                }
+            }
+        });
+    if (!partial) return;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sums[warp][lane * 8 + c] = sum[c];
+    __syncthreads();
+    const int64_t col = (int64_t)blockIdx.x * kSlopeCols + threadIdx.x;
+    if (col >= n) return;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSlopeThreads / 32; ++w) s += sums[w][threadIdx.x];
+    partial[(int64_t)blockIdx.y * n + col] = s;
 }
 
 template <typename T>
-__global__ void linear_bias_grad_kernel(const T *dy, int64_t lddy, const T *pre, const int32_t *offsets, int64_t m,
-                                        int64_t n, int act, T *db, uint32_t *clear) {
+__global__ void __launch_bounds__(kSlopeThreads) linear_bias_join_kernel(const float *partial, const int32_t *offsets,
+                                                                         int64_t m, int64_t n, T *db) {
+    __shared__ int range[2];
     griddep_wait();
-    if (clear && (blockIdx.x | blockIdx.y | threadIdx.x) == 0u) *clear = 0u;
-    const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= n) return;
     const int expert = blockIdx.y;
-    int64_t r0 = 0, r1 = m;
-    if (offsets) {
-        r1 = 0;
-        for (int e = 0; e <= expert; ++e) {
-            r0 = r1;
-            r1 = first_row(offsets, e + 1, r0, m);
+    if (threadIdx.x < 32) {
+        // the tiles before this expert's first and its own
+        int first = 0, last = 0;
+        if (!offsets) {
+            last = (int)((m + kSlopeRows - 1) / kSlopeRows);
+        } else {
+            const int lane = threadIdx.x;
+            int top = 0, sum = 0;
+            for (int e0 = 0; e0 <= expert; e0 += 32) {
+                const int e = e0 + lane;
+                int end = e <= expert ? max(0, (int)min((int64_t)offsets[e + 1], m)) : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(0xffffffffu, end, o));
+                end = max(end, top);
+                int start = __shfl_up_sync(0xffffffffu, end, 1);
+                if (lane == 0) start = top;
+                const int own = (end - start + kSlopeRows - 1) / kSlopeRows;
+                const int before = e < expert ? own : 0;
+                sum += __reduce_add_sync(0xffffffffu, before);
+                if (expert - e0 < 32) last = __shfl_sync(0xffffffffu, own, expert - e0);
+                top = __shfl_sync(0xffffffffu, end, 31);
+            }
+            first = sum;
+            last += first;
+        }
+        if (threadIdx.x == 0) {
+            range[0] = first;
+            range[1] = last;
         }
     }
-    float sum = 0.f, lost = 0.f;  // compensated: one thread adds a whole column
-    for (int64_t r = r0; r < r1; ++r) {
-        const float g = widen(dy[r * lddy + c]);
-        const float v = (act == KMEANS_ACT_NONE ? g : g * slope_as(act, widen(pre[r * n + c]))) - lost;
-        const float t = sum + v;
-        lost = (t - sum) - v;
-        sum = t;
-    }
-    db[(int64_t)expert * n + c] = narrow<T>(sum);
+    __syncthreads();
+    const int64_t col = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (col >= n) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int u = range[0]; u < range[1]; ++u) s += partial[(int64_t)u * n + col];
+    db[(int64_t)expert * n + col] = narrow<T>(s);
 }
+
+// Most row tiles that m rows of so many experts make.
+int64_t slope_tiles(int64_t m, int64_t n_experts) { return (m + kSlopeRows - 1) / kSlopeRows + n_experts; }
 
 // One call's kernels on the stream: the first of them clears the status word.
 template <typename T>
@@ -127,18 +246,28 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
     Product16 g{};
     g.b = dy;
     g.ldb = lddy;
-    if ((activation != KMEANS_ACT_NONE || !rows16(dy, lddy)) && sh.m > 0 && (dx || dw)) {
-        T *dz = reinterpret_cast<T *>(ws + L.off_dz);
-        g.b = dz;
-        g.ldb = align_up(sh.n, 8);
-        e = launch_kernel(true, linear_slope_kernel<T>, dim3((unsigned)(sh.m < 8192 ? sh.m : 8192)), dim3(256), 0, s,
-                          static_cast<const T *>(dy), lddy, static_cast<const T *>(pre), sh.m, sh.n, activation, dz,
-                          g.ldb, call.first());
+    const bool keep = (activation != KMEANS_ACT_NONE || !rows16(dy, lddy)) && (dx || dw);
+    if (sh.m > 0 && (keep || db)) {
+        T *dz = keep ? reinterpret_cast<T *>(ws + L.off_dz) : nullptr;
+        const int64_t ldz = align_up(sh.n, 8);
+        if (keep) {
+            g.b = dz;
+            g.ldb = ldz;
+        }
+        const dim3 grid((unsigned)((sh.n + kSlopeCols - 1) / kSlopeCols), (unsigned)slope_tiles(sh.m, sh.offsets ? sh.n_experts : 0));
+        const bool wide = sh.n % 8 == 0 && rows16(dy, lddy) && (activation == KMEANS_ACT_NONE || rows16(pre, sh.n));
+        float *partial = db ? reinterpret_cast<float *>(ws + L.off_partial) : nullptr;
+        e = launch_kernel(true, wide ? linear_slope_kernel<true, T> : linear_slope_kernel<false, T>, grid,
+                          dim3(kSlopeThreads), 0, s, static_cast<const T *>(dy), lddy, static_cast<const T *>(pre),
+                          sh.offsets, sh.n_experts, sh.m, sh.n, activation, dz, ldz, partial, call.first());
+        if (e == cudaSuccess && db)
+            e = launch_kernel(true, linear_bias_join_kernel<T>,
+                              dim3((unsigned)((sh.n + kSlopeThreads - 1) / kSlopeThreads), (unsigned)sh.n_experts),
+                              dim3(kSlopeThreads), 0, s, static_cast<const float *>(partial), sh.offsets, sh.m, sh.n,
+                              static_cast<T *>(db));
     }
-    if (e == cudaSuccess && db)
-        e = launch_kernel(true, linear_bias_grad_kernel<T>, dim3((unsigned)((sh.n + 127) / 128), (unsigned)sh.n_experts),
-                          dim3(128), 0, s, static_cast<const T *>(dy), lddy, static_cast<const T *>(pre), sh.offsets,
-                          sh.m, sh.n, activation, static_cast<T *>(db), call.first());
+    if (e == cudaSuccess && db && sh.m == 0)
+        e = cudaMemsetAsync(db, 0, (size_t)sh.n_experts * (size_t)sh.n * sizeof(T), s);
     if (e == cudaSuccess && dx && sh.m > 0) {
         g.a = w;
         g.pitch_w = sh.k;
@@ -172,6 +301,8 @@ LinearLayout linear_layout(bool grad, int64_t m, int64_t n, int64_t k, int64_t n
     if (grad) {
         L.off_dz = o;
         o = align_up(o + m * align_up(n, 8) * 2, 1024);
+        L.off_partial = o;
+        o = align_up(o + slope_tiles(m, n_experts) * n * 4, 1024);
     }
     L.bytes = o;
     return L;

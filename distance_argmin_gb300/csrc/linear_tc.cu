@@ -185,41 +185,56 @@ __device__ void fill_tables(const LinearTcParams &p, int *edges, int *tiles, int
     }
 }
 
-// Rows [q, q + 8 rows of the lane groups): one warp's staged values of 32
-// features leave for memory.  Lane group l / 4 takes a row, lane l % 4 eight
-// of its features.
+// What a lane stores of 16 staged rows of 32 features: lane group l / 4 takes
+// rows l / 4 and 8 + l / 4, lane l % 4 eight of the features.
+constexpr int kLaneRows = lt::EPI_ROWS / 8;
+
+// The residual's values of those rows, where 16-byte loads fetch them: asked
+// for a chunk ahead (their latency is longer than a chunk's work).
+template <typename T>
+__device__ __forceinline__ void prefetch_residual(const LinearTcParams &p, int64_t row, int rows, int f, int lane,
+                                                  uint4 (&res)[kLaneRows]) {
+#pragma unroll
+    for (int i = 0; i < kLaneRows; ++i) {
+        const int r = (lane >> 2) + 8 * i;
+        if (r < rows && f + 8 <= p.cols)
+            res[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.residual) + (row + r) * p.ldr + f);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *out, const float (&v)[8], bool whole, int left) {
+    if (whole) {
+        *reinterpret_cast<uint4 *>(out) =
+            make_uint4(narrow2<T>(v[0], v[1]), narrow2<T>(v[2], v[3]), narrow2<T>(v[4], v[5]), narrow2<T>(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < left) out[c] = narrow<T>(v[c]);
+    }
+}
+
 template <Product MODE, typename T, int ACT>
 __device__ __forceinline__ void store_rows(const LinearTcParams &p, const float *staged, int64_t out_row, int rows,
-                                           int f, bool zero, int lane) {
+                                           int f, bool add, const uint4 (&ahead)[kLaneRows], int lane) {
+    const int left = p.cols - f;
+    if (left <= 0) return;
+    const bool whole = p.wide_out && left >= 8;
 #pragma unroll
-    for (int i = 0; i < lt::EPI_ROWS / 8; ++i) {
+    for (int i = 0; i < kLaneRows; ++i) {
         const int r = (lane >> 2) + 8 * i;
-        if (r >= rows || f >= p.cols) continue;
+        if (r >= rows) continue;
         const float4 lo = *reinterpret_cast<const float4 *>(staged + r * lt::EPI_PITCH + (lane & 3) * 8);
         const float4 hi = *reinterpret_cast<const float4 *>(staged + r * lt::EPI_PITCH + (lane & 3) * 8 + 4);
         float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const int64_t row = out_row + r;
-        const int left = min(8, p.cols - f);
-        T *out = static_cast<T *>(p.out) + row * p.cols + f;
+        const int64_t row = out_row + r, at = row * p.cols + f;
         if constexpr (MODE == Product::kForward) {
-            if (p.pre) {
-                T *pre = static_cast<T *>(p.pre) + row * p.cols + f;
-                if (p.wide_out && left == 8) {
-                    *reinterpret_cast<uint4 *>(pre) = make_uint4(narrow2<T>(v[0], v[1]), narrow2<T>(v[2], v[3]),
-                                                                 narrow2<T>(v[4], v[5]), narrow2<T>(v[6], v[7]));
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (c < left) pre[c] = narrow<T>(v[c]);
-                }
-            }
+            if (p.pre) store8(static_cast<T *>(p.pre) + at, v, whole, left);
 #pragma unroll
             for (int c = 0; c < 8; ++c) v[c] = activate<ACT>(v[c]);
-            if (p.residual && !zero) {
-                const T *res = static_cast<const T *>(p.residual) + row * p.ldr + f;
-                if (p.wide_res && left == 8) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(res);
-                    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+            if (add) {
+                if (p.wide_res && left >= 8) {
+                    const uint32_t words[4] = {ahead[i].x, ahead[i].y, ahead[i].z, ahead[i].w};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const float2 a = widen2<T>(words[c]);
@@ -227,20 +242,45 @@ __device__ __forceinline__ void store_rows(const LinearTcParams &p, const float 
                         v[2 * c + 1] += a.y;
                     }
                 } else {
+                    const T *res = static_cast<const T *>(p.residual) + row * p.ldr + f;
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         if (c < left) v[c] += widen(res[c]);
                 }
             }
         }
-        if (p.wide_out && left == 8) {
-            *reinterpret_cast<uint4 *>(out) = make_uint4(narrow2<T>(v[0], v[1]), narrow2<T>(v[2], v[3]),
-                                                         narrow2<T>(v[4], v[5]), narrow2<T>(v[6], v[7]));
-        } else {
+        store8(static_cast<T *>(p.out) + at, v, whole, left);
+    }
+}
+
+// One warp's columns [c, end) of a unit: accumulator -> staged rows -> memory.
+// While one chunk of 16 rows is finished, the next one's accumulator and
+// residual are on their way.
+template <Product MODE, typename T, int ACT>
+__device__ __forceinline__ void finish_unit(const LinearTcParams &p, float *staged, uint32_t acc, int64_t out_row,
+                                            int c, int end, int f, float bias, bool zero, int lane) {
+    const bool add = MODE == Product::kForward && p.residual && !zero;
+    const int fl = f + (lane & 3) * 8;
+    uint32_t r[16] = {};
+    uint4 res[kLaneRows] = {};
+    if (!zero) tmem_ld_16_issue(acc + (uint32_t)c, r);
+    if (add && p.wide_res) prefetch_residual<T>(p, out_row + c, end - c, fl, lane, res);
+#pragma unroll 1
+    for (; c < end; c += lt::EPI_ROWS) {
+        if (!zero) tmem_ld_16_wait(r);
+        __syncwarp();  // the previous rows have been read
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c < left) out[c] = narrow<T>(v[c]);
+        for (int i = 0; i < lt::EPI_ROWS; ++i) staged[i * lt::EPI_PITCH + lane] = __uint_as_float(r[i]) + bias;
+        __syncwarp();
+        uint4 now[kLaneRows];
+#pragma unroll
+        for (int i = 0; i < kLaneRows; ++i) now[i] = res[i];
+        if (c + lt::EPI_ROWS < end) {
+            if (!zero) tmem_ld_16_issue(acc + (uint32_t)(c + lt::EPI_ROWS), r);
+            if (add && p.wide_res)
+                prefetch_residual<T>(p, out_row + c + lt::EPI_ROWS, end - c - lt::EPI_ROWS, fl, lane, res);
         }
+        store_rows<MODE, T, ACT>(p, staged, out_row + c, end - c, fl, add, now, lane);
     }
 }
 
@@ -312,28 +352,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             if (MODE == Product::kForward && p.bias && !zero && f + lane < p.cols)
                 bias = widen(static_cast<const T *>(p.bias)[(int64_t)t.expert * p.cols + f + lane]);
             const int64_t out_row = MODE == Product::kWeights ? (int64_t)t.expert * p.out_rows + t.q0 : t.q0;
-#pragma unroll 1
-            for (int c0 = part * (BN / 2); c0 < min(t.qn, (part + 1) * (BN / 2)); c0 += lt::EPI_ROWS) {
-                float v[lt::EPI_ROWS];
-                if (zero) {
-#pragma unroll
-                    for (int i = 0; i < lt::EPI_ROWS; ++i) v[i] = 0.f;
-                } else {
-                    tmem_ld_32x32b_x16(acc + (uint32_t)c0, v);
-                }
-                __syncwarp();  // the previous rows have been read
-#pragma unroll
-                for (int i = 0; i < lt::EPI_ROWS; ++i) staged[i * lt::EPI_PITCH + lane] = v[i] + bias;
-                __syncwarp();
-                const int rows = t.qn - c0;
-                if constexpr (MODE == Product::kForward) {
+            const int c0 = part * (BN / 2), c1 = min(t.qn, (part + 1) * (BN / 2));
+            if (c0 < c1) {
+                if constexpr (MODE == Product::kForward)
                     with_activation(p.activation, [&](auto a) {
-                        store_rows<MODE, T, decltype(a)::value>(p, staged, out_row + c0, rows, f + (lane & 3) * 8, zero,
-                                                                lane);
+                        finish_unit<MODE, T, decltype(a)::value>(p, staged, acc, out_row, c0, c1, f, bias, zero, lane);
                     });
-                } else {
-                    store_rows<MODE, T, KMEANS_ACT_NONE>(p, staged, out_row + c0, rows, f + (lane & 3) * 8, zero, lane);
-                }
+                else
+                    finish_unit<MODE, T, KMEANS_ACT_NONE>(p, staged, acc, out_row, c0, c1, f, 0.f, zero, lane);
             }
             if (!zero) {
                 tc_fence_before();
