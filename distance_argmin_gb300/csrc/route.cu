@@ -22,7 +22,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "experts.cuh"
+#include "linear_common.cuh"
 #include "ptx.cuh"
 
 namespace km {
@@ -51,11 +51,21 @@ __device__ __forceinline__ int ld_cluster_i32(const int *p, uint32_t rank) {
     return v;
 }
 
+constexpr int kRouteBatch = 8;  // groups of 32 slots whose ids are in flight together
+
+// The keys of slots s + 32 b + lane below `end` (-1 past it).
 template <typename Id>
-__device__ __forceinline__ int route_key(const Id *experts, uint32_t s, int n_experts, bool &bad) {
-    const Id v = experts[s];
-    if (v >= (Id)n_experts) bad = true;
-    return (v < 0 || v >= (Id)n_experts) ? n_experts : (int)v;
+__device__ __forceinline__ void route_keys(const Id *experts, uint32_t s, uint32_t end, int n_experts, bool &bad,
+                                           int (&key)[kRouteBatch]) {
+    Id id[kRouteBatch];
+#pragma unroll
+    for (int b = 0; b < kRouteBatch; ++b) id[b] = s + 32u * b < end ? experts[s + 32u * b] : (Id)0;
+#pragma unroll
+    for (int b = 0; b < kRouteBatch; ++b) {
+        const bool live = s + 32u * b < end;
+        if (live && id[b] >= (Id)n_experts) bad = true;
+        key[b] = !live ? -1 : (id[b] < 0 || id[b] >= (Id)n_experts) ? n_experts : (int)id[b];
+    }
 }
 
 // Shared memory: hist[warps][keys], tot[keys], base[keys], 32 words of scan
@@ -89,12 +99,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     int *mine = hist + warp * keys;
 
     bool bad = false;
-    for (uint32_t s = s0; s < s1; s += 32) {
-        const bool live = s + lane < s1;
-        const int key = live ? route_key(experts, s + lane, p.n_experts, bad) : -1;
-        const uint32_t same = __match_any_sync(kFull, key);
-        if (live && (same & below) == 0u) mine[key] += __popc(same);
-        __syncwarp();
+    int key[kRouteBatch];
+    for (uint32_t s = s0; s < s1; s += 32 * kRouteBatch) {
+        route_keys(experts, s + lane, s1, p.n_experts, bad, key);
+#pragma unroll
+        for (int b = 0; b < kRouteBatch; ++b)
+            if (key[b] >= 0) atomicAdd(mine + key[b], 1);
     }
     __syncthreads();
     // per key: each warp's first place among this block's, and the block's total
@@ -143,74 +153,161 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
         run += chunk;
         __syncthreads();
     }
-    // hand out rows
-    for (uint32_t s = s0; s < s1; s += 32) {
-        const bool live = s + lane < s1;
-        const int key = live ? route_key(experts, s + lane, p.n_experts, bad) : -1;
-        const uint32_t same = __match_any_sync(kFull, key);
-        int row = 0;
-        if (live) row = base[key] + mine[key] + __popc(same & below);
-        __syncwarp();
-        if (live && (same & below) == 0u) mine[key] += __popc(same);
-        __syncwarp();
-        if (live) {
-            p.rows[s + lane] = row;
-            p.order[row] = (int)(s + lane);
+    // hand out rows (one batch's keys are still in registers)
+    for (uint32_t s = s0; s < s1; s += 32 * kRouteBatch) {
+        if (s1 - s0 > 32 * kRouteBatch) route_keys(experts, s + lane, s1, p.n_experts, bad, key);
+#pragma unroll
+        for (int b = 0; b < kRouteBatch; ++b) {
+            if (s + 32u * b >= s1) break;  // the same for the whole warp
+            const bool live = key[b] >= 0;
+            const uint32_t same = __match_any_sync(kFull, key[b]);
+            int row = 0;
+            if (live) row = base[key[b]] + mine[key[b]] + __popc(same & below);
+            __syncwarp();
+            if (live && (same & below) == 0u) mine[key[b]] += __popc(same);
+            __syncwarp();
+            if (live) {
+                const uint32_t slot = s + 32u * b + lane;
+                p.rows[slot] = row;
+                p.order[row] = (int)slot;
+            }
         }
     }
     cluster_sync();  // no block leaves while another may still read its totals
 }
 
 // -------------------------------------------------------------- row movement
+// Rows move in pieces of 16 bytes counted from the row's start; a lane's
+// neighbours hold the neighbouring pieces.  Where every row starts on 16 bytes
+// (WHOLE) a piece is one access.  Otherwise a piece is read as the two aligned
+// 16-byte words it lies in and shifted into place, and written as one aligned
+// word put together from the left neighbour's piece and its own; only the ends
+// of a run of lanes, and words that reach past the tensor, go value by value.
+// (d = 1031 in 16 bits, 4097 tokens of three choices: 31 us a value at a time.)
 template <typename T>
-__device__ __forceinline__ float to_float(T v);
-template <>
-__device__ __forceinline__ float to_float(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-template <typename T>
-__device__ __forceinline__ T from_float(float v);
-template <>
-__device__ __forceinline__ float from_float(float v) { return v; }
-template <>
-__device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
-
-// V consecutive elements moved as one access
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-    T v[V];
+struct Piece {
+    static constexpr int V = 16 / (int)sizeof(T);
+    uint4 w;
+    __device__ void to_floats(float (&f)[V]) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(u[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = widen2<T>(u[i]);
+                f[2 * i] = v.x;
+                f[2 * i + 1] = v.y;
+            }
+        }
+    }
+    __device__ static Piece from_floats(const float (&f)[V]) {
+        Piece p;
+        if constexpr (sizeof(T) == 4)
+            p.w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        else
+            p.w = make_uint4(narrow2<T>(f[0], f[1]), narrow2<T>(f[2], f[3]), narrow2<T>(f[4], f[5]),
+                             narrow2<T>(f[6], f[7]));
+        return p;
+    }
 };
 
-// A piece of V elements at p, the first `left` of which exist, as one access
-// (WHOLE: aligned, and every piece is complete) or element by element.
-template <bool WHOLE, typename T, int V>
-__device__ __forceinline__ Pack<T, V> load_piece(const T *p, int64_t left) {
-    if constexpr (WHOLE) return *reinterpret_cast<const Pack<T, V> *>(p);
-    Pack<T, V> v;
-#pragma unroll
-    for (int i = 0; i < V; ++i) v.v[i] = i < left ? p[i] : from_float<T>(0.f);
-    return v;
+// Bytes [s, s + 16) of a and b in a row; s is even and below 16.
+__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, uint32_t s) {
+    uint32_t w0 = a.x, w1 = a.y, w2 = a.z, w3 = a.w, w4 = b.x, w5 = b.y, w6 = b.z;
+    if (s & 8u) {
+        w0 = w2; w1 = w3; w2 = w4; w3 = w5; w4 = w6; w5 = b.w;
+    }
+    if (s & 4u) {
+        w0 = w1; w1 = w2; w2 = w3; w3 = w4; w4 = w5;
+    }
+    const uint32_t r = (s & 3u) * 8u;
+    return make_uint4(__funnelshift_r(w0, w1, r), __funnelshift_r(w1, w2, r), __funnelshift_r(w2, w3, r),
+                      __funnelshift_r(w3, w4, r));
 }
 
-template <bool WHOLE, typename T, int V>
-__device__ __forceinline__ void store_piece(T *p, const Pack<T, V> &v, int64_t left) {
-    if constexpr (WHOLE) {
-        *reinterpret_cast<Pack<T, V> *>(p) = v;
-    } else {
+__device__ __forceinline__ uint16_t half_of(const uint4 &v, int i) {
+    const uint32_t w = i < 4 ? (i < 2 ? v.x : v.y) : (i < 6 ? v.z : v.w);
+    return (uint16_t)(w >> ((i & 1) * 16));
+}
+
+// Where a tensor's bytes lie.
+struct Span {
+    const uint8_t *lo, *hi;
+};
+
+// `bytes` of the piece at p exist (1 .. 16).
+template <bool WHOLE>
+__device__ __forceinline__ uint4 load_piece(const uint8_t *p, int bytes, const Span &in) {
+    if constexpr (WHOLE) return *reinterpret_cast<const uint4 *>(p);
+    const uint32_t s = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
+    const uint8_t *a = p - s;
+    const bool two = s + bytes > 16;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (a >= in.lo && a + (two ? 32 : 16) <= in.hi) {
+        const uint4 first = *reinterpret_cast<const uint4 *>(a);
+        const uint4 second = two ? *reinterpret_cast<const uint4 *>(a + 16) : zero;
+        uint4 v = shifted(first, second, s);
+        if (bytes < 16) {  // nothing past the row
+            uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < left) p[i] = v.v[i];
+            for (int i = 0; i < 4; ++i) {
+                const int left = bytes - 4 * i;
+                u[i] = left >= 4 ? u[i] : (left >= 2 ? u[i] & 0xffffu : 0u);
+            }
+            v = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        return v;
     }
+    uint32_t u[4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (2 * i < bytes) u[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + 2 * i) << ((i & 1) * 16);
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// The piece v at p.  Not WHOLE: the whole warp calls it together; `prev` is the
+// left neighbour's piece when `joined` says that it belongs to the same row
+// just before, `next` whether the right neighbour's follows in the same call.
+template <bool WHOLE>
+__device__ __forceinline__ void store_piece(uint8_t *p, const uint4 &v, int bytes, const uint4 &prev, bool joined,
+                                            bool next) {
+    if constexpr (WHOLE) {
+        *reinterpret_cast<uint4 *>(p) = v;
+        return;
+    }
+    const int m = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+    if (m == 0 && bytes == 16) {
+        *reinterpret_cast<uint4 *>(p) = v;
+        return;
+    }
+    int from = 0;  // bytes of this piece already written with the left neighbour's
+    if (m != 0 && joined && bytes >= 16 - m) {
+        *reinterpret_cast<uint4 *>(p - m) = shifted(prev, v, (uint32_t)(16 - m));
+        from = 16 - m;
+    } else if (m != 0 && joined) {  // a short last piece: the neighbour's end has no word to share
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (2 * i >= 16 - m) *reinterpret_cast<uint16_t *>(p - 16 + 2 * i) = half_of(prev, i);
+    }
+    // with a right neighbour the last m bytes are its to write
+    const int to = next && m != 0 ? 16 - m : bytes;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (2 * i >= from && 2 * i < to) *reinterpret_cast<uint16_t *>(p + 2 * i) = half_of(v, i);
+}
+
+__device__ __forceinline__ uint4 left_neighbour(const uint4 &v) {
+    return make_uint4(__shfl_up_sync(kFull, v.x, 1), __shfl_up_sync(kFull, v.y, 1), __shfl_up_sync(kFull, v.z, 1),
+                      __shfl_up_sync(kFull, v.w, 1));
 }
 
 struct MoveParams {
     const int32_t *rows, *offsets;
-    int64_t n, slots, vecs;  // vecs: pieces (accesses) per row
+    int64_t n, slots;
+    int64_t row_bytes;
+    int pieces;  // per row
     int topk, n_experts;
     int tpr_log2;  // threads per row
 };
@@ -220,97 +317,123 @@ constexpr int kGatherUnroll = 4;
 
 // xs[row(t, j)] = x[t]; a thread holds up to kGatherUnroll pieces of its token
 // and writes them to every choice's row.
-template <typename W>
-__global__ void __launch_bounds__(kMoveThreads) route_gather_kernel(const MoveParams p, const W *__restrict__ x,
-                                                                    int64_t ldx, W *__restrict__ xs) {
+template <bool WHOLE>
+__global__ void __launch_bounds__(kMoveThreads) route_gather_kernel(const MoveParams p, const uint8_t *x,
+                                                                    int64_t pitch, Span in, uint8_t *xs) {
     griddep_wait();
     const int tpr = 1 << p.tpr_log2;
+    const int sub = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (kMoveThreads >> p.tpr_log2) + (threadIdx.x >> p.tpr_log2);
-    if (t >= p.n) return;
-    const int64_t v0 = (int64_t)blockIdx.y * (tpr * kGatherUnroll) + (threadIdx.x & (tpr - 1));
+    const bool live = t < p.n;
+    if (WHOLE && !live) return;
+    const int v0 = (int)blockIdx.y * (tpr * kGatherUnroll) + sub;
     const int kept = p.offsets[p.n_experts];
-    W val[kGatherUnroll];
+    uint4 val[kGatherUnroll], prev[kGatherUnroll];
 #pragma unroll
-    for (int u = 0; u < kGatherUnroll; ++u)
-        if (v0 + u * tpr < p.vecs) val[u] = x[t * ldx + v0 + u * tpr];
+    for (int u = 0; u < kGatherUnroll; ++u) {
+        const int v = v0 + u * tpr;
+        val[u] = make_uint4(0, 0, 0, 0);
+        if (live && v < p.pieces)
+            val[u] = load_piece<WHOLE>(x + t * pitch + (int64_t)v * 16, (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16),
+                                       in);
+        if (!WHOLE) prev[u] = left_neighbour(val[u]);
+    }
+    if (!live) return;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
     for (int j = 0; j < p.topk; ++j) {
         const int r = p.rows[t * p.topk + j];
         if (r < 0 || r >= p.slots) continue;
+        const bool on = r < kept;
 #pragma unroll
-        for (int u = 0; u < kGatherUnroll; ++u)
-            if (v0 + u * tpr < p.vecs) xs[(int64_t)r * p.vecs + v0 + u * tpr] = r < kept ? val[u] : W{};
+        for (int u = 0; u < kGatherUnroll; ++u) {
+            const int v = v0 + u * tpr;
+            if (v >= p.pieces) continue;
+            store_piece<WHOLE>(xs + (int64_t)r * p.row_bytes + (int64_t)v * 16, on ? val[u] : zero,
+                               (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16), on ? prev[u] : zero,
+                               sub > 0 && lane > 0, sub + 1 < tpr && lane < 31 && v + 1 < p.pieces);
+        }
     }
 }
 
 constexpr int kCombineUnroll = 4;  // choices whose rows are in flight together
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveParams p, const T *__restrict__ ys,
+template <bool WHOLE, typename T>
+__global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveParams p, const uint8_t *ys, Span in,
                                                                      const float *__restrict__ weights,
-                                                                     const T *residual, int64_t ldr, T *y) {
-    using P = Pack<T, V>;
+                                                                     const uint8_t *residual, int64_t pitch, Span res_in,
+                                                                     uint8_t *y) {
+    using P = Piece<T>;
     griddep_wait();
     const int tpr = 1 << p.tpr_log2;
+    const int sub = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (kMoveThreads >> p.tpr_log2) + (threadIdx.x >> p.tpr_log2);
-    const int64_t v = (int64_t)blockIdx.y * tpr + (threadIdx.x & (tpr - 1));
-    if (t >= p.n || v >= p.vecs) return;
+    const int v = (int)blockIdx.y * tpr + sub;
+    const bool live = t < p.n && v < p.pieces;
+    if (WHOLE && !live) return;
+    const int bytes = (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16);
     const int kept = p.topk > 0 ? p.offsets[p.n_experts] : 0;
     const int64_t limit = kept < p.slots ? kept : p.slots;
-    const int64_t d = p.vecs * V;
-    float acc[V];
+    float acc[P::V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (int j0 = 0; j0 < p.topk; j0 += kCombineUnroll) {
-        P part[kCombineUnroll];
-        float w[kCombineUnroll];
-        bool on[kCombineUnroll];
+    for (int i = 0; i < P::V; ++i) acc[i] = 0.f;
+    if (live) {
+        for (int j0 = 0; j0 < p.topk; j0 += kCombineUnroll) {
+            P part[kCombineUnroll];
+            float w[kCombineUnroll];
+            bool on[kCombineUnroll];
 #pragma unroll
-        for (int u = 0; u < kCombineUnroll; ++u) {
-            const int j = j0 + u;
-            const int r = j < p.topk ? p.rows[t * p.topk + j] : -1;
-            on[u] = r >= 0 && r < limit;
-            if (on[u]) {
-                w[u] = weights ? weights[t * p.topk + j] : 1.f;
-                part[u] = *reinterpret_cast<const P *>(ys + r * d + v * V);
+            for (int u = 0; u < kCombineUnroll; ++u) {
+                const int j = j0 + u;
+                const int r = j < p.topk ? p.rows[t * p.topk + j] : -1;
+                on[u] = r >= 0 && r < limit;
+                if (on[u]) {
+                    w[u] = weights ? weights[t * p.topk + j] : 1.f;
+                    part[u].w = load_piece<WHOLE>(ys + r * p.row_bytes + (int64_t)v * 16, bytes, in);
+                }
             }
+#pragma unroll
+            for (int u = 0; u < kCombineUnroll; ++u)
+                if (on[u]) {
+                    float f[P::V];
+                    part[u].to_floats(f);
+#pragma unroll
+                    for (int i = 0; i < P::V; ++i) acc[i] = fmaf(w[u], f[i], acc[i]);
+                }
         }
+        if (residual) {
+            P res;
+            res.w = load_piece<WHOLE>(residual + t * pitch + (int64_t)v * 16, bytes, res_in);
+            float f[P::V];
+            res.to_floats(f);
 #pragma unroll
-        for (int u = 0; u < kCombineUnroll; ++u)
-            if (on[u]) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(w[u], to_float(part[u].v[i]), acc[i]);
-            }
+            for (int i = 0; i < P::V; ++i) acc[i] += f[i];
+        }
     }
-    P out;
-    if (residual) {
-        const P res = *reinterpret_cast<const P *>(residual + t * ldr + v * V);
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += to_float(res.v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) out.v[i] = from_float<T>(acc[i]);
-    *reinterpret_cast<P *>(y + t * d + v * V) = out;
+    const P out = P::from_floats(acc);
+    uint4 prev = make_uint4(0, 0, 0, 0);
+    if (!WHOLE) prev = left_neighbour(out.w);
+    if (live)
+        store_piece<WHOLE>(y + t * p.row_bytes + (int64_t)v * 16, out.w, bytes, prev, sub > 0 && lane > 0,
+                           sub + 1 < tpr && lane < 31 && v + 1 < p.pieces);
 }
 
+constexpr int64_t kManyTokens = 152 * 16;
 constexpr int kGradChoices = 8;  // choices whose products a thread sums in one walk along the row
 
-// One group of tpr threads per token walks the row; a block whose groups are
-// wider than a warp joins the warps' sums in shared memory.  A thread takes
-// the same V elements at a time whatever the alignment, so the sums have one
-// order.
-template <bool WHOLE, typename T, int V>
-__global__ void __launch_bounds__(kMoveThreads) route_combine_grad_kernel(const MoveParams p, int64_t d,
-                                                                          const T *__restrict__ dy, int64_t lddy,
-                                                                          const T *__restrict__ ys,
-                                                                          const float *__restrict__ weights,
-                                                                          T *__restrict__ dys,
-                                                                          float *__restrict__ dweights) {
-    using P = Pack<T, V>;
+// A group of tpr threads per token walks the row; a block whose groups are
+// wider than a warp joins the warps' sums in shared memory.  The pieces are
+// the same whatever the alignment, so the sums have one order.
+template <bool WHOLE, typename T>
+__global__ void __launch_bounds__(kMoveThreads) route_combine_grad_kernel(const MoveParams p, const uint8_t *dy,
+                                                                          int64_t pitch, Span dy_in, const uint8_t *ys,
+                                                                          Span in, const float *__restrict__ weights,
+                                                                          uint8_t *dys, float *__restrict__ dweights) {
+    using P = Piece<T>;
     __shared__ float part[kGradChoices][kMoveThreads / 32];
     griddep_wait();
     const int tpr = 1 << p.tpr_log2;
     const int64_t t = (int64_t)blockIdx.x * (kMoveThreads >> p.tpr_log2) + (threadIdx.x >> p.tpr_log2);
-    const int sub = threadIdx.x & (tpr - 1), warp = threadIdx.x >> 5;
+    const int sub = threadIdx.x & (tpr - 1), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool live = t < p.n;
     const int kept = p.offsets[p.n_experts];
     const int64_t limit = kept < p.slots ? kept : p.slots;
@@ -322,37 +445,49 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_grad_kernel(const 
             const int j = j0 + u;
             sum[u] = 0.f;
             row[u] = live && j < p.topk ? p.rows[t * p.topk + j] : -1;
+            w[u] = row[u] >= 0 ? weights[t * p.topk + j] : 0.f;
             if (row[u] >= p.slots) row[u] = -1;
-            w[u] = row[u] >= 0 && row[u] < limit ? weights[t * p.topk + j] : 0.f;
         }
-        if (live)
-            for (int64_t v = sub; v < p.vecs; v += tpr) {
-                const int64_t left = d - v * V;
-                const P g = load_piece<WHOLE, T, V>(dy + t * lddy + v * V, left);
-                P in[kGradChoices];
+        // the warp stays together: the stores pass pieces between lanes
+        for (int v0 = sub & ~31; v0 < p.pieces; v0 += tpr) {
+            const int v = v0 + (sub & 31);
+            const bool here = live && v < p.pieces;
+            if (WHOLE && !here) continue;
+            const int bytes = (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16);
+            P g, got[kGradChoices];
+            g.w = make_uint4(0, 0, 0, 0);
+            if (here) g.w = load_piece<WHOLE>(dy + t * pitch + (int64_t)v * 16, bytes, dy_in);
 #pragma unroll
-                for (int u = 0; u < kGradChoices; ++u)
-                    if (row[u] >= 0 && row[u] < limit) in[u] = load_piece<WHOLE, T, V>(ys + row[u] * d + v * V, left);
+            for (int u = 0; u < kGradChoices; ++u)
+                if (here && row[u] >= 0 && row[u] < limit)
+                    got[u].w = load_piece<WHOLE>(ys + row[u] * p.row_bytes + (int64_t)v * 16, bytes, in);
+            float gf[P::V];
+            g.to_floats(gf);
 #pragma unroll
-                for (int u = 0; u < kGradChoices; ++u) {
-                    if (row[u] < 0) continue;
-                    const bool on = row[u] < limit;
-                    P out;
+            for (int u = 0; u < kGradChoices; ++u) {
+                const bool on = row[u] >= 0 && row[u] < limit;
+                float f[P::V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float gi = to_float(g.v[i]);
-                        out.v[i] = from_float<T>(on ? w[u] * gi : 0.f);
-                        if (on) sum[u] = fmaf(gi, to_float(in[u].v[i]), sum[u]);
-                    }
-                    store_piece<WHOLE, T, V>(dys + row[u] * d + v * V, out, left);
+                for (int i = 0; i < P::V; ++i) f[i] = on ? w[u] * gf[i] : 0.f;
+                const P out = P::from_floats(f);
+                if (here && on) {
+                    got[u].to_floats(f);
+#pragma unroll
+                    for (int i = 0; i < P::V; ++i) sum[u] = fmaf(gf[i], f[i], sum[u]);
                 }
+                uint4 prev = out.w;
+                if (!WHOLE) prev = left_neighbour(out.w);
+                if (here && row[u] >= 0)
+                    store_piece<WHOLE>(dys + row[u] * p.row_bytes + (int64_t)v * 16, out.w, bytes, prev,
+                                       sub > 0 && lane > 0, sub + 1 < tpr && lane < 31 && v + 1 < p.pieces);
             }
+        }
 #pragma unroll
         for (int u = 0; u < kGradChoices; ++u)
             for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) sum[u] += __shfl_xor_sync(kFull, sum[u], o);
         if (tpr > 32) {
             __syncthreads();  // the previous choices' sums have been read
-            if ((threadIdx.x & 31) == 0) {
+            if (lane == 0) {
 #pragma unroll
                 for (int u = 0; u < kGradChoices; ++u) part[u][warp] = sum[u];
             }
@@ -377,11 +512,16 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_grad_kernel(const 
 
 int elem_bytes(int dtype) { return dtype == KMEANS_F32 ? 4 : 2; }
 
-// Widest access (bytes, a power of two up to 16) that every row start allows.
-int row_access(int64_t row_bytes, int64_t pitch_bytes, std::initializer_list<const void *> ptrs) {
-    uint64_t bits = (uint64_t)row_bytes | (uint64_t)pitch_bytes | 16u;
+// Every row of every matrix starts on 16 bytes.
+bool whole_rows(int64_t row_bytes, int64_t pitch_bytes, std::initializer_list<const void *> ptrs) {
+    uint64_t bits = (uint64_t)row_bytes | (uint64_t)pitch_bytes;
     for (const void *q : ptrs) bits |= reinterpret_cast<uintptr_t>(q);
-    return (int)(bits & (~bits + 1));
+    return (bits & 15u) == 0;
+}
+
+Span span(const void *base, int64_t rows, int64_t pitch_bytes, int64_t row_bytes) {
+    const uint8_t *b = static_cast<const uint8_t *>(base);
+    return {b, base && rows > 0 ? b + (rows - 1) * pitch_bytes + row_bytes : b};
 }
 
 int log2_at_least(int64_t v, int most) {
@@ -390,76 +530,54 @@ int log2_at_least(int64_t v, int most) {
     return l;
 }
 
-MoveParams move_params(const RouteRows &r, int64_t vecs, int tpr_log2) {
+MoveParams move_params(const RouteRows &r, int dtype) {
     MoveParams p{};
     p.rows = r.rows;
     p.offsets = r.offsets;
     p.n = r.n;
     p.slots = r.n * r.topk;
-    p.vecs = vecs;
+    p.row_bytes = r.d * elem_bytes(dtype);
+    p.pieces = (int)((p.row_bytes + 15) / 16);
     p.topk = r.topk;
     p.n_experts = r.n_experts;
-    p.tpr_log2 = tpr_log2;
     return p;
 }
 
-template <typename W>
-cudaError_t gather_as(const RouteRows &r, int64_t row_bytes, int64_t pitch_bytes, const void *x, void *xs,
-                      cudaStream_t s) {
-    const int64_t vecs = row_bytes / (int64_t)sizeof(W);
-    const int l = log2_at_least((vecs + kGatherUnroll - 1) / kGatherUnroll, 8);
-    const MoveParams p = move_params(r, vecs, l);
-    const int64_t per_y = (int64_t)kGatherUnroll << l;
-    const dim3 grid((unsigned)((r.n + (kMoveThreads >> l) - 1) / (kMoveThreads >> l)),
-                    (unsigned)((vecs + per_y - 1) / per_y));
-    return launch_kernel(true, route_gather_kernel<W>, grid, dim3(kMoveThreads), 0, s, p, static_cast<const W *>(x),
-                         pitch_bytes / (int64_t)sizeof(W), static_cast<W *>(xs));
-}
-
-template <typename T, int V>
-cudaError_t combine_as(const RouteRows &r, const void *ys, const float *weights, const void *residual, int64_t ldr,
-                       void *y, cudaStream_t s) {
-    const int64_t vecs = r.d / V;
-    const int l = log2_at_least(vecs, 8);
-    const dim3 grid((unsigned)((r.n + (kMoveThreads >> l) - 1) / (kMoveThreads >> l)),
-                    (unsigned)((vecs + (1 << l) - 1) >> l));
-    return launch_kernel(true, route_combine_kernel<T, V>, grid, dim3(kMoveThreads), 0, s, move_params(r, vecs, l),
-                         static_cast<const T *>(ys), weights, static_cast<const T *>(residual), ldr,
-                         static_cast<T *>(y));
-}
-
-template <bool WHOLE, typename T, int V>
-cudaError_t combine_grad_as(const RouteRows &r, const void *dy, int64_t lddy, const void *ys, const float *weights,
-                            void *dys, float *dweights, cudaStream_t s) {
-    const int64_t vecs = (r.d + V - 1) / V;
-    const int l = log2_at_least(vecs, 8);
-    const dim3 grid((unsigned)((r.n + (kMoveThreads >> l) - 1) / (kMoveThreads >> l)));
-    return launch_kernel(true, route_combine_grad_kernel<WHOLE, T, V>, grid, dim3(kMoveThreads), 0, s, move_params(r, vecs, l), r.d,
-                         static_cast<const T *>(dy), lddy, static_cast<const T *>(ys), weights, static_cast<T *>(dys),
-                         dweights);
+unsigned row_blocks(const MoveParams &p) {
+    const int64_t per = kMoveThreads >> p.tpr_log2;
+    return (unsigned)((p.n + per - 1) / per);
 }
 
 template <typename T>
-cudaError_t combine_typed(const RouteRows &r, const void *ys, const float *weights, const void *residual, int64_t ldr,
+cudaError_t combine_typed(MoveParams p, const void *ys, const float *weights, const void *residual, int64_t ldr,
                           void *y, cudaStream_t s) {
-    const int64_t b = sizeof(T);
-    const int wide = row_access(r.d * b, residual ? ldr * b : 0, {ys, residual, y});
-    return wide == 16 ? combine_as<T, 16 / (int)sizeof(T)>(r, ys, weights, residual, ldr, y, s)
-                      : combine_as<T, 1>(r, ys, weights, residual, ldr, y, s);
+    const int64_t pitch = ldr * (int64_t)sizeof(T);
+    p.tpr_log2 = log2_at_least(p.pieces, 8);
+    const dim3 grid(row_blocks(p), (unsigned)((p.pieces + (1 << p.tpr_log2) - 1) >> p.tpr_log2));
+    const bool whole = whole_rows(p.row_bytes, residual ? pitch : 0, {ys, residual, y});
+    return launch_kernel(true, whole ? route_combine_kernel<true, T> : route_combine_kernel<false, T>, grid,
+                         dim3(kMoveThreads), 0, s, p, static_cast<const uint8_t *>(ys),
+                         span(ys, p.slots, p.row_bytes, p.row_bytes), weights, static_cast<const uint8_t *>(residual),
+                         pitch, span(residual, p.n, pitch, p.row_bytes), static_cast<uint8_t *>(y));
 }
 
 template <typename T>
-cudaError_t combine_grad_typed(const RouteRows &r, const void *dy, int64_t lddy, const void *ys, const float *weights,
+cudaError_t combine_grad_typed(MoveParams p, const void *dy, int64_t lddy, const void *ys, const float *weights,
                                void *dys, float *dweights, cudaStream_t s) {
-    const int64_t b = sizeof(T);
-    const int wide = row_access(r.d * b, lddy * b, {dy, ys, dys});
-    constexpr int V = 16 / (int)sizeof(T);
-    return wide == 16 ? combine_grad_as<true, T, V>(r, dy, lddy, ys, weights, dys, dweights, s)
-                      : combine_grad_as<false, T, V>(r, dy, lddy, ys, weights, dys, dweights, s);
+    const int64_t pitch = lddy * (int64_t)sizeof(T);
+    // a warp per token where there are enough of them: no block-wide join, and
+    // the rows of other tokens hide each other's latency (16384 tokens of 8
+    // choices, d = 2048: a block per token 344 us)
+    p.tpr_log2 = log2_at_least(p.pieces, p.n >= kManyTokens ? 5 : 8);
+    const bool whole = whole_rows(p.row_bytes, pitch, {dy, ys, dys});
+    return launch_kernel(true, whole ? route_combine_grad_kernel<true, T> : route_combine_grad_kernel<false, T>,
+                         dim3(row_blocks(p)), dim3(kMoveThreads), 0, s, p, static_cast<const uint8_t *>(dy), pitch,
+                         span(dy, p.n, pitch, p.row_bytes), static_cast<const uint8_t *>(ys),
+                         span(ys, p.slots, p.row_bytes, p.row_bytes), weights, static_cast<uint8_t *>(dys), dweights);
 }
 
 template <typename Id>
-cudaError_t route_as(const RouteParams &p, int blocks, size_t smem, cudaStream_t s) {
+cudaError_t route_as(const RouteParams &p, int blocks, int threads, size_t smem, cudaStream_t s) {
     static std::once_flag once[kMaxDevices];
     static std::atomic<int> err[kMaxDevices];
     int dev = 0;
@@ -472,7 +590,7 @@ cudaError_t route_as(const RouteParams &p, int blocks, size_t smem, cudaStream_t
     if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kRouteThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -500,38 +618,47 @@ cudaError_t launch_route(const void *experts, int id_bytes, int64_t slots, int n
     p.status = status;
     const int keys = n_experts + 1;
     const int room = (kRouteSmemMax - 2 * keys * 4 - 128) / (keys * 4);
-    p.warps = room < kRouteThreads / 32 ? room : kRouteThreads / 32;
     int blocks = 1;
     while (blocks < kRouteMaxCluster && (int64_t)blocks * kRouteSlotsPerBlock < slots) blocks *= 2;
+    // no more counting warps than groups of 32 slots: their counts are cleared
+    // and added up key by key
+    const int64_t groups = (slots + 31) / 32, per_block = (groups + blocks - 1) / blocks;
+    p.warps = room < kRouteThreads / 32 ? room : kRouteThreads / 32;
+    if (per_block < p.warps) p.warps = per_block > 0 ? (int)per_block : 1;
+    const int threads = p.warps > 8 || keys > 512 ? kRouteThreads : 256;
     const size_t smem = (size_t)((p.warps + 2) * keys + 32) * 4;
-    return id_bytes == 8 ? route_as<int64_t>(p, blocks, smem, s) : route_as<int32_t>(p, blocks, smem, s);
+    return id_bytes == 8 ? route_as<int64_t>(p, blocks, threads, smem, s) : route_as<int32_t>(p, blocks, threads, smem, s);
 }
 
 cudaError_t launch_route_gather(const RouteRows &r, int dtype, const void *x, int64_t ldx, void *xs, cudaStream_t s) {
-    const int64_t b = elem_bytes(dtype);
-    switch (row_access(r.d * b, ldx * b, {x, xs})) {
-        case 16: return gather_as<uint4>(r, r.d * b, ldx * b, x, xs, s);
-        case 8: return gather_as<uint2>(r, r.d * b, ldx * b, x, xs, s);
-        case 4: return gather_as<uint32_t>(r, r.d * b, ldx * b, x, xs, s);
-        default: return gather_as<uint16_t>(r, r.d * b, ldx * b, x, xs, s);
-    }
+    MoveParams p = move_params(r, dtype);
+    const int64_t pitch = ldx * elem_bytes(dtype);
+    p.tpr_log2 = log2_at_least((p.pieces + kGatherUnroll - 1) / kGatherUnroll, 8);
+    const int per_y = kGatherUnroll << p.tpr_log2;
+    const dim3 grid(row_blocks(p), (unsigned)((p.pieces + per_y - 1) / per_y));
+    const bool whole = whole_rows(p.row_bytes, pitch, {x, xs});
+    return launch_kernel(true, whole ? route_gather_kernel<true> : route_gather_kernel<false>, grid,
+                         dim3(kMoveThreads), 0, s, p, static_cast<const uint8_t *>(x), pitch,
+                         span(x, p.n, pitch, p.row_bytes), static_cast<uint8_t *>(xs));
 }
 
 cudaError_t launch_route_combine(const RouteRows &r, int dtype, const void *ys, const float *weights,
                                  const void *residual, int64_t ldr, void *y, cudaStream_t s) {
+    const MoveParams p = move_params(r, dtype);
     switch (dtype) {
-        case KMEANS_F32: return combine_typed<float>(r, ys, weights, residual, ldr, y, s);
-        case KMEANS_F16: return combine_typed<__half>(r, ys, weights, residual, ldr, y, s);
-        default: return combine_typed<__nv_bfloat16>(r, ys, weights, residual, ldr, y, s);
+        case KMEANS_F32: return combine_typed<float>(p, ys, weights, residual, ldr, y, s);
+        case KMEANS_F16: return combine_typed<__half>(p, ys, weights, residual, ldr, y, s);
+        default: return combine_typed<__nv_bfloat16>(p, ys, weights, residual, ldr, y, s);
     }
 }
 
 cudaError_t launch_route_combine_grad(const RouteRows &r, int dtype, const void *dy, int64_t lddy, const void *ys,
                                       const float *weights, void *dys, float *dweights, cudaStream_t s) {
+    const MoveParams p = move_params(r, dtype);
     switch (dtype) {
-        case KMEANS_F32: return combine_grad_typed<float>(r, dy, lddy, ys, weights, dys, dweights, s);
-        case KMEANS_F16: return combine_grad_typed<__half>(r, dy, lddy, ys, weights, dys, dweights, s);
-        default: return combine_grad_typed<__nv_bfloat16>(r, dy, lddy, ys, weights, dys, dweights, s);
+        case KMEANS_F32: return combine_grad_typed<float>(p, dy, lddy, ys, weights, dys, dweights, s);
+        case KMEANS_F16: return combine_grad_typed<__half>(p, dy, lddy, ys, weights, dys, dweights, s);
+        default: return combine_grad_typed<__nv_bfloat16>(p, dy, lddy, ys, weights, dys, dweights, s);
     }
 }
 
