@@ -207,9 +207,15 @@ def n_trials_for(k: int) -> int:
 
 
 # ----------------------------------------------------------------- helpers
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -666,12 +672,30 @@ def kmeanspp_shard_commit(n: int, d: int, n_trials: int, first: bool, pots, worl
 
 
 # ----------------------------------------- expert routing and expert products
+# A routed layer's calls on a few tokens last microseconds on the GPU, so what
+# happens before the launch counts: one look at the tensors decides whether all
+# is as it should be, and only if not are they looked at again for the reason.
+_codes = {}
+
+
 def _dtype_code(t, name):
-    torch = _torch()
-    code = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}.get(t.dtype)
+    if not _codes:
+        torch = _torch()
+        _codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    code = _codes.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     return code
+
+
+def _check_on(t, name, dtype, shape, device):
+    """_check for a tensor whose device and shape are known."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _check(t, name, dtype, shape, device)
 
 
 def _check_rows(t, name, dtype, shape, device):
@@ -679,16 +703,16 @@ def _check_rows(t, name, dtype, shape, device):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} must be on {device}, it is on {t.device} (the library has no CPU path)")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    rows, cols = t.shape
-    pitch = t.stride(0)
-    if rows <= 1:
-        pitch = max(cols, 1)
+    rows, cols = shape
+    if t.is_contiguous():
+        return max(cols, 1)
+    pitch = t.stride(0) if rows > 1 else max(cols, 1)
     if (cols > 1 and t.stride(1) != 1) or pitch < cols:
         raise ValueError(f"{name}: the rows must be contiguous and apart from each other")
     return pitch
@@ -702,6 +726,30 @@ def _cuda_matrix(t, name):
         raise ValueError(f"{name} must be on a CUDA device (the library has no CPU path)")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_on(stream, device, *made):
+    """The stream's handle; the current one of the tensors' device by default.
+    ``made``: tensors this call allocated (on the current stream), which may be
+    given back while the work on another stream still uses them."""
+    torch = _torch()
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+    for t in made:
+        if t is not None:
+            t.record_stream(on)
+    return on.cuda_stream
+
+
+def _workspace_on(ws, device):
+    torch = _torch()
+    if not (isinstance(ws, torch.Tensor) and ws.dtype is torch.uint8 and ws.device == device and ws.is_contiguous()):
+        _check(ws, "ws", torch.uint8, device=device)
 
 
 def route_workspace(n: int, topk: int, n_experts: int, device=None):
@@ -730,44 +778,50 @@ def kmeans_route(experts, n_experts: int, offsets=None, order=None, rows=None, w
     torch = _torch()
     if not isinstance(experts, torch.Tensor):
         raise TypeError("experts must be a torch.Tensor")
-    if experts.dtype not in (torch.int32, torch.int64):
+    if experts.dtype is not torch.int64 and experts.dtype is not torch.int32:
         raise TypeError(f"experts must be int32 or int64, got {experts.dtype}")
-    _check(experts, "experts", experts.dtype)
     if experts.dim() not in (1, 2):
         raise ValueError(f"experts must be (n, topk) or (n,), got {tuple(experts.shape)}")
+    dev, n_experts = experts.device, int(n_experts)
     n, topk = experts.shape if experts.dim() == 2 else (experts.shape[0], 1)
-    dev = experts.device
+    if dev.type != "cuda" or not experts.is_contiguous():
+        _check(experts, "experts", experts.dtype)
+    if n_experts < 1:
+        raise ValueError(f"n_experts must be at least 1, got {n_experts}")
+    made = [None] * 4
     if offsets is None:
-        offsets = torch.empty(int(n_experts) + 1, dtype=torch.int32, device=dev)
+        offsets = made[0] = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
     else:
-        _check(offsets, "offsets", torch.int32, (int(n_experts) + 1,), dev)
+        _check_on(offsets, "offsets", torch.int32, (n_experts + 1,), dev)
     if order is None:
-        order = torch.empty(n * topk, dtype=torch.int32, device=dev)
+        order = made[1] = torch.empty(n * topk, dtype=torch.int32, device=dev)
     else:
-        _check(order, "order", torch.int32, (n * topk,), dev)
+        _check_on(order, "order", torch.int32, (n * topk,), dev)
     if rows is None:
-        rows = torch.empty((n, topk), dtype=torch.int32, device=dev)
+        rows = made[2] = torch.empty((n, topk), dtype=torch.int32, device=dev)
     else:
-        _check(rows, "rows", torch.int32, (n, topk), dev)
+        _check_on(rows, "rows", torch.int32, (n, topk), dev)
     if ws is None:
-        ws = route_workspace(n, topk, int(n_experts), dev)
+        ws = made[3] = route_workspace(n, topk, n_experts, dev)
     else:
-        _check(ws, "ws", torch.uint8, device=dev)
-    st = load().kmeans_route(_ptr(experts), experts.element_size(), n, topk, int(n_experts), _ptr(offsets),
-                             _ptr(order), _ptr(rows), _ptr(ws), ws.numel(), _stream_handle(stream))
+        _workspace_on(ws, dev)
+    st = (_lib or load()).kmeans_route(_addr(experts), experts.element_size(), n, topk, n_experts, _addr(offsets),
+                                       _addr(order), _addr(rows), _addr(ws), ws.numel(),
+                                       _stream_on(stream, dev, *made))
     _raise(st, "kmeans_route")
     return offsets, order, rows
 
 
 def _plan(rows, offsets, device):
     torch = _torch()
-    _check(rows, "rows", torch.int32, device=device)
-    if rows.dim() != 2:
-        raise ValueError(f"rows must be (n, topk), got {tuple(rows.shape)}")
-    _check(offsets, "offsets", torch.int32, device=device)
-    if offsets.dim() != 1 or offsets.shape[0] < 2:
-        raise ValueError(f"offsets must be (n_experts + 1,), got {tuple(offsets.shape)}")
-    return rows.shape[0], rows.shape[1], offsets.shape[0] - 1
+    if not (isinstance(rows, torch.Tensor) and rows.dim() == 2):
+        raise ValueError("rows must be (n, topk), as kmeans_route wrote them")
+    if not (isinstance(offsets, torch.Tensor) and offsets.dim() == 1 and offsets.numel() >= 2):
+        raise ValueError("offsets must be (n_experts + 1,), as kmeans_route wrote them")
+    _check_on(rows, "rows", torch.int32, rows.shape, device)
+    _check_on(offsets, "offsets", torch.int32, offsets.shape, device)
+    n, topk = rows.shape
+    return n, topk, offsets.numel() - 1
 
 
 def kmeans_route_gather(x, rows, offsets, xs=None, stream=None):
@@ -775,15 +829,17 @@ def kmeans_route_gather(x, rows, offsets, xs=None, stream=None):
     dropped choices.  ``rows`` and ``offsets`` are kmeans_route's."""
     _cuda_matrix(x, "x")
     code = _dtype_code(x, "x")
-    n, topk, n_experts = _plan(rows, offsets, x.device)
+    dev, dt = x.device, x.dtype
+    n, topk, n_experts = _plan(rows, offsets, dev)
     d = x.shape[1]
-    ldx = _check_rows(x, "x", x.dtype, (n, d), x.device)
+    ldx = _check_rows(x, "x", dt, (n, d), dev)
+    made = None
     if xs is None:
-        xs = _torch().empty((n * topk, d), dtype=x.dtype, device=x.device)
+        xs = made = _torch().empty((n * topk, d), dtype=dt, device=dev)
     else:
-        _check(xs, "xs", x.dtype, (n * topk, d), x.device)
-    st = load().kmeans_route_gather(_ptr(x), ldx, code, _ptr(rows), _ptr(offsets), n, topk, n_experts, d, _ptr(xs),
-                                    _stream_handle(stream))
+        _check_on(xs, "xs", dt, (n * topk, d), dev)
+    st = (_lib or load()).kmeans_route_gather(_addr(x), ldx, code, _addr(rows), _addr(offsets), n, topk, n_experts, d, _addr(xs),
+                                    _stream_on(stream, dev, made))
     _raise(st, "kmeans_route_gather")
     return xs
 
@@ -798,16 +854,17 @@ def kmeans_route_combine(ys, rows, offsets, weights=None, residual=None, y=None,
     dev = ys.device
     n, topk, n_experts = _plan(rows, offsets, dev)
     d = ys.shape[1]
-    _check(ys, "ys", ys.dtype, (n * topk, d))
+    _check_on(ys, "ys", ys.dtype, (n * topk, d), dev)
+    made = None
     if weights is not None:
-        _check(weights, "weights", torch.float32, (n, topk), dev)
+        _check_on(weights, "weights", torch.float32, (n, topk), dev)
     ldr = _check_rows(residual, "residual", ys.dtype, (n, d), dev) if residual is not None else 0
     if y is None:
-        y = torch.empty((n, d), dtype=ys.dtype, device=dev)
+        y = made = torch.empty((n, d), dtype=ys.dtype, device=dev)
     else:
-        _check(y, "y", ys.dtype, (n, d), dev)
-    st = load().kmeans_route_combine(_ptr(ys), code, _ptr(weights), _ptr(residual), ldr, _ptr(rows), _ptr(offsets), n,
-                                     topk, n_experts, d, _ptr(y), _stream_handle(stream))
+        _check_on(y, "y", ys.dtype, (n, d), dev)
+    st = (_lib or load()).kmeans_route_combine(_addr(ys), code, _addr(weights), _addr(residual), ldr, _addr(rows), _addr(offsets), n,
+                                     topk, n_experts, d, _addr(y), _stream_on(stream, dev, made))
     _raise(st, "kmeans_route_combine")
     return y
 
@@ -821,19 +878,20 @@ def kmeans_route_combine_grad(dy, ys, rows, offsets, weights, dys=None, dweights
     dev = ys.device
     n, topk, n_experts = _plan(rows, offsets, dev)
     d = ys.shape[1]
-    _check(ys, "ys", ys.dtype, (n * topk, d))
+    _check_on(ys, "ys", ys.dtype, (n * topk, d), dev)
+    made = [None, None]
     lddy = _check_rows(dy, "dy", ys.dtype, (n, d), dev)
-    _check(weights, "weights", torch.float32, (n, topk), dev)
+    _check_on(weights, "weights", torch.float32, (n, topk), dev)
     if dys is None:
-        dys = torch.empty((n * topk, d), dtype=ys.dtype, device=dev)
+        dys = made[0] = torch.empty((n * topk, d), dtype=ys.dtype, device=dev)
     else:
-        _check(dys, "dys", ys.dtype, (n * topk, d), dev)
+        _check_on(dys, "dys", ys.dtype, (n * topk, d), dev)
     if dweights is None:
-        dweights = torch.empty((n, topk), dtype=torch.float32, device=dev)
+        dweights = made[1] = torch.empty((n, topk), dtype=torch.float32, device=dev)
     else:
-        _check(dweights, "dweights", torch.float32, (n, topk), dev)
-    st = load().kmeans_route_combine_grad(_ptr(dy), lddy, _ptr(ys), code, _ptr(weights), _ptr(rows), _ptr(offsets), n,
-                                          topk, n_experts, d, _ptr(dys), _ptr(dweights), _stream_handle(stream))
+        _check_on(dweights, "dweights", torch.float32, (n, topk), dev)
+    st = (_lib or load()).kmeans_route_combine_grad(_addr(dy), lddy, _addr(ys), code, _addr(weights), _addr(rows), _addr(offsets), n,
+                                          topk, n_experts, d, _addr(dys), _addr(dweights), _stream_on(stream, dev, *made))
     _raise(st, "kmeans_route_combine_grad")
     return dys, dweights
 
@@ -845,7 +903,9 @@ def _linear_args(x, w, offsets, activation):
     code = _dtype_code(x, "x")
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r} (one of {', '.join(ACTIVATIONS)})")
-    _check(w, "w", x.dtype, device=x.device)
+    if not isinstance(w, torch.Tensor):
+        raise TypeError("w must be a torch.Tensor")
+    _check_on(w, "w", x.dtype, w.shape, x.device)
     m, k = x.shape
     if offsets is None:
         if w.dim() != 2 and not (w.dim() == 3 and w.shape[0] == 1):
@@ -855,7 +915,7 @@ def _linear_args(x, w, offsets, activation):
         if w.dim() != 3:
             raise ValueError(f"w must be (n_experts, n, k) with offsets, got {tuple(w.shape)}")
         n_experts = w.shape[0]
-        _check(offsets, "offsets", torch.int32, (n_experts + 1,), x.device)
+        _check_on(offsets, "offsets", torch.int32, (n_experts + 1,), x.device)
     if w.shape[-1] != k:
         raise ValueError(f"w has {w.shape[-1]} input features, x has {k}")
     return code, m, w.shape[-2], k, n_experts, ACTIVATIONS[activation]
@@ -876,22 +936,23 @@ def kmeans_linear(x, w, bias=None, residual=None, offsets=None, activation="none
     dev, dt = x.device, x.dtype
     ldx = _check_rows(x, "x", dt, (m, k), dev)
     if bias is not None:
-        _check(bias, "bias", dt, tuple(w.shape[:-1]), dev)
+        _check_on(bias, "bias", dt, tuple(w.shape[:-1]), dev)
     ldr = _check_rows(residual, "residual", dt, (m, n), dev) if residual is not None else 0
+    made = [None] * 3
     if y is None:
-        y = torch.empty((m, n), dtype=dt, device=dev)
+        y = made[0] = torch.empty((m, n), dtype=dt, device=dev)
     else:
-        _check(y, "y", dt, (m, n), dev)
+        _check_on(y, "y", dt, (m, n), dev)
     if pre is not None:
-        _check(pre, "pre", dt, (m, n), dev)
+        _check_on(pre, "pre", dt, (m, n), dev)
     elif save_pre:
-        pre = torch.empty((m, n), dtype=dt, device=dev)
+        pre = made[1] = torch.empty((m, n), dtype=dt, device=dev)
     if ws is None:
-        ws = linear_workspace(OP_LINEAR, m, n, k, n_experts, dev)
+        ws = made[2] = linear_workspace(OP_LINEAR, m, n, k, n_experts, dev)
     else:
-        _check(ws, "ws", torch.uint8, device=dev)
-    st = load().kmeans_linear(_ptr(x), ldx, _ptr(w), _ptr(bias), _ptr(residual), ldr, code, act, _ptr(offsets), m, n,
-                              k, n_experts, _ptr(y), _ptr(pre), _ptr(ws), ws.numel(), _stream_handle(stream))
+        _workspace_on(ws, dev)
+    st = (_lib or load()).kmeans_linear(_addr(x), ldx, _addr(w), _addr(bias), _addr(residual), ldr, code, act, _addr(offsets), m, n,
+                              k, n_experts, _addr(y), _addr(pre), _addr(ws), ws.numel(), _stream_on(stream, dev, *made))
     _raise(st, "kmeans_linear")
     return y, pre
 
@@ -909,29 +970,30 @@ def kmeans_linear_grad(dy, x, w, pre=None, offsets=None, activation="none", need
     if act != ACTIVATIONS["none"]:
         if pre is None:
             raise ValueError(f"activation {activation!r} needs pre")
-        _check(pre, "pre", dt, (m, n), dev)
+        _check_on(pre, "pre", dt, (m, n), dev)
+    made = [None] * 4
     if need_dx:
         if dx is None:
-            dx = torch.empty((m, k), dtype=dt, device=dev)
+            dx = made[0] = torch.empty((m, k), dtype=dt, device=dev)
         else:
-            _check(dx, "dx", dt, (m, k), dev)
+            _check_on(dx, "dx", dt, (m, k), dev)
     if need_dw:
         if dw is None:
-            dw = torch.empty_like(w)
+            dw = made[1] = torch.empty_like(w)
         else:
-            _check(dw, "dw", dt, tuple(w.shape), dev)
+            _check_on(dw, "dw", dt, tuple(w.shape), dev)
     if need_db:
         if db is None:
-            db = torch.empty(w.shape[:-1], dtype=dt, device=dev)
+            db = made[2] = torch.empty(w.shape[:-1], dtype=dt, device=dev)
         else:
-            _check(db, "db", dt, tuple(w.shape[:-1]), dev)
+            _check_on(db, "db", dt, tuple(w.shape[:-1]), dev)
     if ws is None:
-        ws = linear_workspace(OP_LINEAR_GRAD, m, n, k, n_experts, dev)
+        ws = made[3] = linear_workspace(OP_LINEAR_GRAD, m, n, k, n_experts, dev)
     else:
         _check(ws, "ws", torch.uint8, device=dev)
     dx, dw, db = dx if need_dx else None, dw if need_dw else None, db if need_db else None
-    st = load().kmeans_linear_grad(_ptr(dy), lddy, _ptr(x), ldx, _ptr(w), _ptr(pre), code, act, _ptr(offsets), m, n, k,
-                                   n_experts, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws.numel(),
-                                   _stream_handle(stream))
+    st = (_lib or load()).kmeans_linear_grad(_addr(dy), lddy, _addr(x), ldx, _addr(w), _addr(pre), code, act, _addr(offsets), m, n, k,
+                                   n_experts, _addr(dx), _addr(dw), _addr(db), _addr(ws), ws.numel(),
+                                   _stream_on(stream, dev, *made))
     _raise(st, "kmeans_linear_grad")
     return dx, dw, db

@@ -230,6 +230,7 @@ struct Call {
 
 template <typename T>
 cudaError_t forward_typed(const LinearShape &sh, Product16 g, const LinearLayout &L, uint8_t *ws, cudaStream_t s) {
+    if (few_rows(sh)) return launch_linear_few(sh, g, &reinterpret_cast<WsHeader *>(ws)->status, s);
     Call<T> call(sh, L, ws, s);
     cudaError_t e = call.align_w(g);
     if (e == cudaSuccess) e = call.align(g.b, g.ldb, sh.m, sh.k, L.off_x);

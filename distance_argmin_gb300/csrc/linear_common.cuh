@@ -9,7 +9,7 @@
 
 #include <type_traits>
 
-#include "experts.cuh"
+#include "pieces.cuh"
 
 namespace km {
 
@@ -32,45 +32,6 @@ struct Product16 {
     void *out, *pre;
 };
 
-template <typename T>
-__device__ __forceinline__ float widen(T v);
-template <>
-__device__ __forceinline__ float widen(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-template <typename T>
-__device__ __forceinline__ T narrow(float v);
-template <>
-__device__ __forceinline__ __half narrow(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 narrow(float v) { return __float2bfloat16_rn(v); }
-
-// Two values in one word, the first in the low half.
-template <typename T>
-__device__ __forceinline__ uint32_t narrow2(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t narrow2<__half>(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t narrow2<__nv_bfloat16>(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-template <typename T>
-__device__ __forceinline__ float2 widen2(uint32_t v);
-template <>
-__device__ __forceinline__ float2 widen2<__half>(uint32_t v) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
-}
-template <>
-__device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t v) {
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-}
-
 // f applied with the activation as a compile-time constant: one branch around
 // a whole loop instead of one per value.
 template <typename F>
@@ -91,6 +52,40 @@ __device__ __forceinline__ int64_t first_row(const int32_t *offsets, int e, int6
     return v < from ? from : (v > m ? m : v);
 }
 
+// The row tiles (of ROWS rows) of a call, expert by expert: edges[e] is expert
+// e's first row (the offsets' running maximum, cut to m), tiles[e] the tiles
+// before it; group n_experts holds the rows of no expert.  Filled by one warp;
+// each table has n_experts + 2 entries.
+template <int ROWS>
+__device__ void fill_tables(const int32_t *offsets, int n_experts, int64_t m, int *edges, int *tiles, int lane) {
+    int last = 0, count = 0;
+    if (lane == 0) edges[0] = tiles[0] = 0;
+    for (int e0 = 0; e0 <= n_experts; e0 += 32) {
+        const int e = e0 + lane;  // group e ends at edge e + 1
+        int end = 0;
+        if (e < n_experts) end = offsets ? max(0, (int)min((int64_t)offsets[e + 1], m)) : (int)m;
+        if (e == n_experts) end = (int)m;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(0xffffffffu, end, o));
+        end = max(end, last);
+        int start = __shfl_up_sync(0xffffffffu, end, 1);
+        if (lane == 0) start = last;
+        int t = (int)(((int64_t)end - start + ROWS - 1) / ROWS);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) t += v;
+        }
+        t += count;
+        if (e <= n_experts) {
+            edges[e + 1] = end;
+            tiles[e + 1] = t;
+        }
+        last = __shfl_sync(0xffffffffu, end, 31);
+        count = __shfl_sync(0xffffffffu, t, 31);
+    }
+}
+
 // A matrix whose rows all start on 16 bytes.
 inline bool rows16(const void *base, int64_t pitch_elems) {
     return (reinterpret_cast<uintptr_t>(base) & 15u) == 0 && pitch_elems % 8 == 0;
@@ -100,5 +95,9 @@ inline bool rows16(const void *base, int64_t pitch_elems) {
 // kernel is the call's first and clears the status word.
 cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product16 &g, uint32_t *status, bool clear,
                              cudaStream_t s);
+
+// The forward product of few rows per expert; x and w as they lie.
+bool few_rows(const LinearShape &sh);
+cudaError_t launch_linear_few(const LinearShape &sh, const Product16 &g, uint32_t *status, cudaStream_t s);
 
 }  // namespace km

@@ -96,9 +96,8 @@ struct LinearTcParams {
 };
 
 // The units: expert by expert, bands of BAND feature tiles, in a band the
-// feature tiles of one row tile after the other.  `edges[e]` is expert e's
-// first row, `tiles[e]` the row tiles before it; for the row products entry
-// n_experts is the group of rows that belong to no expert.
+// feature tiles of one row tile after the other (edges and tiles: see
+// fill_tables).
 struct Unit {
     int expert, p0, q0, qn;  // q0: first output row (row products: of the matrix, weights: of the expert)
     int c0, c1;              // contraction range (rows of x for weights)
@@ -152,38 +151,6 @@ struct Units {
         return t;
     }
 };
-
-// One warp fills the tables: a running maximum of the offsets, cut to m, and
-// the row tiles before each group.
-template <Product MODE, int BN>
-__device__ void fill_tables(const LinearTcParams &p, int *edges, int *tiles, int lane) {
-    int last = 0, count = 0;
-    if (lane == 0) edges[0] = tiles[0] = 0;
-    for (int e0 = 0; e0 <= p.n_experts; e0 += 32) {
-        const int e = e0 + lane;  // group e ends at edge e + 1
-        int end = 0;
-        if (e < p.n_experts) end = p.offsets ? max(0, (int)min((int64_t)p.offsets[e + 1], p.m)) : (int)p.m;
-        if (e == p.n_experts) end = (int)p.m;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(0xffffffffu, end, o));
-        end = max(end, last);
-        int start = __shfl_up_sync(0xffffffffu, end, 1);
-        if (lane == 0) start = last;
-        int t = (end - start + BN - 1) / BN;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += v;
-        }
-        t += count;
-        if (e <= p.n_experts) {
-            edges[e + 1] = end;
-            tiles[e + 1] = t;
-        }
-        last = __shfl_sync(0xffffffffu, end, 31);
-        count = __shfl_sync(0xffffffffu, t, 31);
-    }
-}
 
 // What a lane stores of 16 staged rows of 32 features: lane group l / 4 takes
 // rows l / 4 and 8 + l / 4, lane l % 4 eight of the features.
@@ -327,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     // this call's status word: a wait of this launch runs out two seconds from
     // now at the earliest, long after the first block has cleared it
     if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
-    if (warp == 0) fill_tables<MODE, BN>(p, edges, tiles, lane);
+    if (warp == 0) fill_tables<BN>(p.offsets, p.n_experts, p.m, edges, tiles, lane);
     cluster_sync();  // barriers, tensor memory and tables exist in both CTAs
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;

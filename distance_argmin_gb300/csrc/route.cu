@@ -22,7 +22,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "linear_common.cuh"
+#include "pieces.cuh"
 #include "ptx.cuh"
 
 namespace km {
@@ -212,60 +212,6 @@ struct Piece {
         return p;
     }
 };
-
-// Bytes [s, s + 16) of a and b in a row; s is even and below 16.
-__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, uint32_t s) {
-    uint32_t w0 = a.x, w1 = a.y, w2 = a.z, w3 = a.w, w4 = b.x, w5 = b.y, w6 = b.z;
-    if (s & 8u) {
-        w0 = w2; w1 = w3; w2 = w4; w3 = w5; w4 = w6; w5 = b.w;
-    }
-    if (s & 4u) {
-        w0 = w1; w1 = w2; w2 = w3; w3 = w4; w4 = w5;
-    }
-    const uint32_t r = (s & 3u) * 8u;
-    return make_uint4(__funnelshift_r(w0, w1, r), __funnelshift_r(w1, w2, r), __funnelshift_r(w2, w3, r),
-                      __funnelshift_r(w3, w4, r));
-}
-
-__device__ __forceinline__ uint16_t half_of(const uint4 &v, int i) {
-    const uint32_t w = i < 4 ? (i < 2 ? v.x : v.y) : (i < 6 ? v.z : v.w);
-    return (uint16_t)(w >> ((i & 1) * 16));
-}
-
-// Where a tensor's bytes lie.
-struct Span {
-    const uint8_t *lo, *hi;
-};
-
-// `bytes` of the piece at p exist (1 .. 16).
-template <bool WHOLE>
-__device__ __forceinline__ uint4 load_piece(const uint8_t *p, int bytes, const Span &in) {
-    if constexpr (WHOLE) return *reinterpret_cast<const uint4 *>(p);
-    const uint32_t s = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
-    const uint8_t *a = p - s;
-    const bool two = s + bytes > 16;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    if (a >= in.lo && a + (two ? 32 : 16) <= in.hi) {
-        const uint4 first = *reinterpret_cast<const uint4 *>(a);
-        const uint4 second = two ? *reinterpret_cast<const uint4 *>(a + 16) : zero;
-        uint4 v = shifted(first, second, s);
-        if (bytes < 16) {  // nothing past the row
-            uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int left = bytes - 4 * i;
-                u[i] = left >= 4 ? u[i] : (left >= 2 ? u[i] & 0xffffu : 0u);
-            }
-            v = make_uint4(u[0], u[1], u[2], u[3]);
-        }
-        return v;
-    }
-    uint32_t u[4] = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (2 * i < bytes) u[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + 2 * i) << ((i & 1) * 16);
-    return make_uint4(u[0], u[1], u[2], u[3]);
-}
 
 // The piece v at p.  Not WHOLE: the whole warp calls it together; `prev` is the
 // left neighbour's piece when `joined` says that it belongs to the same row
