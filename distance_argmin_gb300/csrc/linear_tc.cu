@@ -30,13 +30,16 @@
 //               activation, residual, one rounding, 16-byte stores
 //   warp 8      TMA producer (each CTA: its half of A and of B)
 //   warp 9      allocates tensor memory; in the even CTA issues the MMAs
-//   warp 10     relay: sees this CTA's stage land, clears rows if needed, and
-//               tells the even CTA
+//   warp 10     (weights) relay: sees this CTA's stage land, clears rows if
+//               needed, and tells the even CTA; the row products' loads count
+//               on the even CTA's barrier by themselves
 // Two accumulators alternate, so a unit's epilogue overlaps the next one's
 // MMAs.  Every wait is bounded as in the assignment.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <cstdlib>
 
 #include "assign_common.cuh"
 #include "linear_common.cuh"
@@ -92,6 +95,7 @@ struct LinearTcParams {
     void *out, *pre;
     int wide_out, wide_res;  // 16-byte accesses allowed
     uint32_t *status;
+    int test_starve;  // test hook: the producer issues no loads, so the pipeline waits run out
     int clear;  // first kernel of the call: it clears the status word
 };
 
@@ -257,6 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                      const LinearTcParams p) {
     using C = lt::Cfg<BN>;
     constexpr bool A_MN = MODE != Product::kForward, B_MN = MODE == Product::kWeights;
+    constexpr bool RELAY = MODE == Product::kWeights;  // rows may have to be cleared before the MMA
     static_assert(!B_MN || BN >= 128, "an N-contiguous operand comes in chunks of 64 per CTA");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
@@ -341,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             tma_prefetch_desc(&tmA);
             tma_prefetch_desc(&tmB);
             int it = 0;
-            bool ok = true;
+            bool ok = !p.test_starve;
             for (int64_t u = pair; u < units.total && ok; u += num_pairs) {
                 const Unit t = units.at(u);
                 const int pa = t.p0 + rank * lt::BP_CTA;
@@ -355,29 +360,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                         break;
                     }
                     const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES, full = bar(C::FULL + s);
-                    mbar_arrive_expect_tx(full, C::STAGE);
-                    if constexpr (MODE == Product::kForward) {
-                        tma_load_3d(sa, &tmA, full, c, pa, t.expert);
-                    } else {
+                    if constexpr (RELAY) {
+                        mbar_arrive_expect_tx(full, C::STAGE);
 #pragma unroll
-                        for (int h = 0; h < lt::BP_CTA / 64; ++h) {
-                            if constexpr (MODE == Product::kRows)
-                                tma_load_3d(sa + h * (64 * lt::BK * 2), &tmA, full, pa + h * 64, c, t.expert);
-                            else
-                                tma_load_2d(sa + h * (64 * lt::BK * 2), &tmA, full, pa + h * 64, c);
-                        }
-                    }
-                    if constexpr (B_MN) {
+                        for (int h = 0; h < lt::BP_CTA / 64; ++h)
+                            tma_load_2d(sa + h * (64 * lt::BK * 2), &tmA, full, pa + h * 64, c);
 #pragma unroll
                         for (int h = 0; h < BN / 2 / 64; ++h)
                             tma_load_2d(sb + h * (64 * lt::BK * 2), &tmB, full, qb + h * 64, c);
                     } else {
-                        tma_load_2d(sb, &tmB, full, c, qb);
+                        // both CTAs' bytes count on the even CTA's barrier
+                        if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::STAGE);
+                        const uint32_t pair_full = map_to_cta(full, 0);
+                        if constexpr (MODE == Product::kForward) {
+                            tma_load_3d_pair(sa, &tmA, pair_full, c, pa, t.expert);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < lt::BP_CTA / 64; ++h)
+                                tma_load_3d_pair(sa + h * (64 * lt::BK * 2), &tmA, pair_full, pa + h * 64, c, t.expert);
+                        }
+                        tma_load_2d_pair(sb, &tmB, pair_full, c, qb);
                     }
                 }
             }
-            if (!ok) {
-                // let copies already in flight land before the CTA exits
+            if (!ok && (RELAY || rank == 0)) {
+                // let copies already in flight land before the CTAs exit (the
+                // odd CTA's are on the even one's barriers, and it leaves last)
                 for (int j = max(0, it - C::STAGES); j < it; ++j)
                     mbar_wait_drain(bar(C::FULL + (j % C::STAGES)), (j / C::STAGES) & 1);
             }
@@ -385,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     } else if (warp == lt::WARP_RELAY) {
         // -------------------------------------------------------------- relay
         int it = 0;
-        bool ok = true;
+        bool ok = RELAY;
         for (int64_t u = pair; u < units.total && ok; u += num_pairs) {
             const Unit t = units.at(u);
             for (int c = t.c0; c < t.c1; c += lt::BK, ++it) {
@@ -394,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                     ok = false;
                     break;
                 }
-                if (MODE == Product::kWeights && t.c1 - c < lt::BK) {
+                if (t.c1 - c < lt::BK) {
                     // rows past the expert's end: every 64-value chunk of both
                     // operands holds them as whole 128-byte lines
                     uint8_t *st = smem + s * C::STAGE;
@@ -437,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                         db[kk] = B_MN ? umma_smem_desc_mn(sb + kk * 2048, 64 * lt::BK * 2, 1024)
                                       : umma_smem_desc(sb + kk * 32, 1024, kLayoutSW128);
                     }
-                    if (!mbar_wait_cluster(bar(C::READY + s), (it / C::STAGES) & 1, p.status)) {
+                    if (!mbar_wait_cluster(bar((RELAY ? C::READY : C::FULL) + s), (it / C::STAGES) & 1, p.status)) {
                         ok = false;
                         break;
                     }
@@ -554,6 +562,10 @@ cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product1
     p.wide_res = g.residual && rows16(g.residual, g.ldr);
     p.status = status;
     p.clear = clear;
+    // test-only fault injection (no trap, no fault), as in the assignment: every
+    // consumer's bounded wait runs out and the status word reports the timeout
+    const char *starve = getenv("KMEANS_GB300_TEST_STARVE_PIPELINE");
+    p.test_starve = (starve != nullptr && starve[0] == '1') ? 1 : 0;
     if (mode == Product::kWeights) return launch_typed<Product::kWeights, 256>(sh, g, p, s);
     // rows per unit: about an expert's average rows, so that small groups do
     // not load and multiply rows of their neighbours

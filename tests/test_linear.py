@@ -393,3 +393,20 @@ def test_weights_of_more_than_two_to_the_31_values(gpu_lib, rows):
     within(dx, rdx.double(), rdx.double().abs(), 0, torch.bfloat16, 2.0 ** -8 * rdx.double().abs() + 1e-3)
     within(dw[-1], rdw.double(), rdw.double().abs(), 0, torch.bfloat16, 2.0 ** -8 * rdw.double().abs() + 1e-3)
     assert not dw[:-1].any()
+
+
+def test_a_starved_pipeline_reports_a_timeout_and_the_next_call_works(gpu_lib, monkeypatch):
+    x, w, dy = (normal(s, torch.bfloat16, i) for i, s in enumerate([(300, 128), (264, 128), (300, 264)]))
+    wf = gpu_lib.linear_workspace(gpu_lib.OP_LINEAR, 300, 264, 128)
+    wg = gpu_lib.linear_workspace(gpu_lib.OP_LINEAR_GRAD, 300, 264, 128)
+    ref = (gpu_lib.kmeans_linear(x, w)[0], *gpu_lib.kmeans_linear_grad(dy, x, w))
+    monkeypatch.setenv("KMEANS_GB300_TEST_STARVE_PIPELINE", "1")
+    gpu_lib.kmeans_linear(x, w, ws=wf)
+    assert gpu_lib.kmeans_device_status(wf) == gpu_lib.KMEANS_ERR_DEVICE_TIMEOUT
+    gpu_lib.kmeans_linear_grad(dy, x, w, ws=wg)
+    assert gpu_lib.kmeans_device_status(wg) == gpu_lib.KMEANS_ERR_DEVICE_TIMEOUT
+    monkeypatch.delenv("KMEANS_GB300_TEST_STARVE_PIPELINE")
+    got = (gpu_lib.kmeans_linear(x, w, ws=wf)[0], *gpu_lib.kmeans_linear_grad(dy, x, w, ws=wg))
+    assert gpu_lib.kmeans_device_status(wf) == gpu_lib.KMEANS_OK == gpu_lib.kmeans_device_status(wg)
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
