@@ -70,13 +70,29 @@ cudaError_t launch_linear_grad(const LinearShape &sh, const void *dy, int64_t ld
 //   its tanh form   (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
 // Each is within 2^-19 (|z| + 1) of its formula, below the last bit that 16
 // bits keep, except next to a zero of the result.
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float reciprocal_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+// 1 / (1 + 2^-x)
+__device__ __forceinline__ float logistic2(float x) { return reciprocal_approx(1.f + exp2_approx(-x)); }
+__device__ __forceinline__ float logistic(float z) { return logistic2(z * kLog2E); }
 
 // Phi(z), and exp(-z^2 / 2) beside it
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
     const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-    e = __expf(-x * x);
+    const float t = reciprocal_approx(fmaf(0.3275911f, x, 1.f));
+    e = exp2_approx(-kLog2E * x * x);
     float poly = fmaf(t, 1.061405429f, -1.453152027f);
     poly = fmaf(t, poly, 1.421413741f);
     poly = fmaf(t, poly, -0.284496736f);
@@ -93,7 +109,7 @@ __device__ __forceinline__ float activate(float z) {
         return z * normal_cdf(z, e);
     }
     if constexpr (ACT == KMEANS_ACT_GELU_TANH)
-        return z * logistic(z * fmaf(0.0713548162726f, z * z, 1.5957691216057308f));
+        return z * logistic2(z * fmaf(0.0713548162726f * kLog2E, z * z, 1.5957691216057308f * kLog2E));
     if constexpr (ACT == KMEANS_ACT_SILU) return z * logistic(z);
     return z;
 }
@@ -110,7 +126,7 @@ __device__ __forceinline__ float slope(float z) {
         // u' = 2 sqrt(2 / pi) (1 + 3 a z^2); far out s (1 - s) is 0 while z u'
         // may be infinite, hence the cut
         const float zz = fminf(z * z, 1e4f);
-        const float s = logistic(z * fmaf(0.0713548162726f, z * z, 1.5957691216057308f));
+        const float s = logistic2(z * fmaf(0.0713548162726f * kLog2E, z * z, 1.5957691216057308f * kLog2E));
         return fmaf(z * s * (1.f - s), fmaf(0.2140644488178f, zz, 1.5957691216057308f), s);
     }
     if constexpr (ACT == KMEANS_ACT_SILU) {

@@ -25,12 +25,12 @@
 // Structure: CTA pairs (cta_group::2), persistent over the units (256 features
 // x BN rows), a band of 8 feature tiles at a time so that the pairs running
 // together share rows and features in L2.
-//   warps 0-7   epilogue: tensor memory -> registers -> a padded shared-memory
+//   warps 0-15  epilogue: tensor memory -> registers -> a padded shared-memory
 //               tile per warp -> rows of 32 neighbouring features: bias,
 //               activation, residual, one rounding, 16-byte stores
-//   warp 8      TMA producer (each CTA: its half of A and of B)
-//   warp 9      allocates tensor memory; in the even CTA issues the MMAs
-//   warp 10     (weights) relay: sees this CTA's stage land, clears rows if
+//   warp 16     TMA producer (each CTA: its half of A and of B)
+//   warp 17     allocates tensor memory; in the even CTA issues the MMAs
+//   warp 18     (weights) relay: sees this CTA's stage land, clears rows if
 //               needed, and tells the even CTA; the row products' loads count
 //               on the even CTA's barrier by themselves
 // Two accumulators alternate, so a unit's epilogue overlaps the next one's
@@ -52,13 +52,15 @@ namespace lt {
 constexpr int BP = 256;            // features per unit (UMMA M of the pair)
 constexpr int BP_CTA = BP / 2;
 constexpr int BK = 64;             // contraction per stage: 128 bytes of 16-bit values
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 16;       // four per tensor-memory lane quarter, a quarter of the columns each
 constexpr int WARP_TMA = EPI_WARPS, WARP_MMA = WARP_TMA + 1, WARP_RELAY = WARP_TMA + 2;
 constexpr int THREADS = (WARP_RELAY + 1) * 32;
-constexpr int EPI_ROWS = 16;       // rows staged at a time per epilogue warp
+constexpr int EPI_ROWS = 8;        // rows staged at a time per epilogue warp
 constexpr int EPI_PITCH = 36;      // floats: 8 rows x 32 bytes then hit distinct banks
 constexpr int STAGING = EPI_WARPS * EPI_ROWS * EPI_PITCH * 4;
 constexpr int BAND = 8;            // feature tiles per raster band
+constexpr int LIST_UNITS = 32;     // units a warp works out at a time
+constexpr int LIST_BYTES = LIST_UNITS * 24;
 constexpr int SMEM_LIMIT = 232448;
 constexpr int BAR_BYTES = 512;
 
@@ -70,7 +72,8 @@ struct Cfg {
     static constexpr int STAGES = BN >= 256 ? 6 : BN >= 128 ? 8 : 9;
     static constexpr int STAGING_BASE = STAGES * STAGE;
     static constexpr int BAR_BASE = STAGING_BASE + STAGING;
-    static constexpr int TABLE_BASE = BAR_BASE + BAR_BYTES;
+    static constexpr int LIST_BASE = BAR_BASE + BAR_BYTES;
+    static constexpr int TABLE_BASE = LIST_BASE + 3 * LIST_BYTES;
     static constexpr int TMEM_COLS = 2 * BN;  // >= 64
     static constexpr int FULL = 0, READY = STAGES, EMPTY = 2 * STAGES, T_FULL = 3 * STAGES, T_EMPTY = T_FULL + 2,
                          DRAIN = T_EMPTY + 2, NUM_BARS = DRAIN + 1;
@@ -107,35 +110,34 @@ struct Unit {
     int c0, c1;              // contraction range (rows of x for weights)
 };
 
+// (There are fewer than 2^31 units: each is 64 rows x 256 features or more of
+// a matrix in memory.)
 template <Product MODE, int BN>
 struct Units {
     const LinearTcParams &p;
     const int *edges, *tiles;
-    int64_t total;
+    int total;
     int e = 0;
 
     __device__ Units(const LinearTcParams &p_, const int *edges_, const int *tiles_)
         : p(p_), edges(edges_), tiles(tiles_) {
-        total = MODE == Product::kWeights ? (int64_t)p.n_experts * p.num_p * row_tiles()
-                                          : (int64_t)tiles[p.n_experts + 1] * p.num_p;
+        total = (MODE == Product::kWeights ? p.n_experts * row_tiles() : tiles[p.n_experts + 1]) * p.num_p;
     }
     __device__ int row_tiles() const { return (p.out_rows + BN - 1) / BN; }
 
     // `u` never decreases from call to call.
-    __device__ Unit at(int64_t u) {
+    __device__ Unit at(int u) {
         int per;
         if (MODE == Product::kWeights) {
             per = row_tiles();
-            e = (int)(u / ((int64_t)per * p.num_p));
-            u -= (int64_t)e * per * p.num_p;
+            e = u / (per * p.num_p);
+            u -= e * per * p.num_p;
         } else {
-            while (u >= (int64_t)tiles[e + 1] * p.num_p) ++e;
-            u -= (int64_t)tiles[e] * p.num_p;
+            while (u >= tiles[e + 1] * p.num_p) ++e;
+            u -= tiles[e] * p.num_p;
             per = tiles[e + 1] - tiles[e];
         }
-        const int64_t band_units = (int64_t)lt::BAND * per;
-        const int band = (int)(u / band_units);
-        const int r = (int)(u - band * band_units);
+        const int band = u / (lt::BAND * per), r = u - band * (lt::BAND * per);
         const int wide = min(lt::BAND, p.num_p - band * lt::BAND);
         const int q = r / wide;
         Unit t;
@@ -156,23 +158,6 @@ struct Units {
     }
 };
 
-// What a lane stores of 16 staged rows of 32 features: lane group l / 4 takes
-// rows l / 4 and 8 + l / 4, lane l % 4 eight of the features.
-constexpr int kLaneRows = lt::EPI_ROWS / 8;
-
-// The residual's values of those rows, where 16-byte loads fetch them: asked
-// for a chunk ahead (their latency is longer than a chunk's work).
-template <typename T>
-__device__ __forceinline__ void prefetch_residual(const LinearTcParams &p, int64_t row, int rows, int f, int lane,
-                                                  uint4 (&res)[kLaneRows]) {
-#pragma unroll
-    for (int i = 0; i < kLaneRows; ++i) {
-        const int r = (lane >> 2) + 8 * i;
-        if (r < rows && f + 8 <= p.cols)
-            res[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.residual) + (row + r) * p.ldr + f);
-    }
-}
-
 template <typename T>
 __device__ __forceinline__ void store8(T *out, const float (&v)[8], bool whole, int left) {
     if (whole) {
@@ -185,75 +170,84 @@ __device__ __forceinline__ void store8(T *out, const float (&v)[8], bool whole, 
     }
 }
 
-template <Product MODE, typename T, int ACT>
-__device__ __forceinline__ void store_rows(const LinearTcParams &p, const float *staged, int64_t out_row, int rows,
-                                           int f, bool add, const uint4 (&ahead)[kLaneRows], int lane) {
-    const int left = p.cols - f;
-    if (left <= 0) return;
-    const bool whole = p.wide_out && left >= 8;
+// One warp's columns [c0, end) of a unit, 8 rows of 32 features at a time:
+// accumulator -> staged rows -> memory.  In memory's order lane group l / 4 has
+// a row, lane l % 4 eight of its features.  The residual of all the columns is
+// asked for before the accumulator is waited for, so its latency passes behind
+// the unit's MMAs, and the next chunk's accumulator is on its way while one is
+// finished.  (Tried and slower on a dense 8192 x 8192 x 2048, 164 us: 2-byte
+// stores from the accumulator's layout without staging 170 us, one bulk copy
+// per row of 128 features 174 us.)
+template <Product MODE, int BN, typename T>
+struct Finish {
+    static constexpr int COLS = BN / (lt::EPI_WARPS / 4), CHUNKS = COLS / lt::EPI_ROWS;
+    static constexpr bool FORWARD = MODE == Product::kForward;
+    const LinearTcParams &p;
+    float *staged;
+    int lane;
+    int c0, end, f;   // f: this lane's first feature in memory's order
+    int64_t out_row;  // of the unit's column 0
+    bool add;
+    uint4 res[FORWARD ? CHUNKS : 1];
+
+    __device__ bool wide_add() const { return add && p.wide_res && f + 8 <= p.cols; }
+
+    __device__ void prefetch() {
+        if constexpr (FORWARD) {
+            if (!wide_add()) return;
+            const T *at = static_cast<const T *>(p.residual) + (out_row + c0 + (lane >> 2)) * p.ldr + f;
+            const int64_t step = lt::EPI_ROWS * p.ldr;
 #pragma unroll
-    for (int i = 0; i < kLaneRows; ++i) {
-        const int r = (lane >> 2) + 8 * i;
-        if (r >= rows) continue;
-        const float4 lo = *reinterpret_cast<const float4 *>(staged + r * lt::EPI_PITCH + (lane & 3) * 8);
-        const float4 hi = *reinterpret_cast<const float4 *>(staged + r * lt::EPI_PITCH + (lane & 3) * 8 + 4);
-        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const int64_t row = out_row + r, at = row * p.cols + f;
-        if constexpr (MODE == Product::kForward) {
-            if (p.pre) store8(static_cast<T *>(p.pre) + at, v, whole, left);
+            for (int i = 0; i < CHUNKS; ++i, at += step)
+                if (c0 + i * lt::EPI_ROWS + (lane >> 2) < end) res[i] = *reinterpret_cast<const uint4 *>(at);
+        }
+    }
+
+    template <int ACT>
+    __device__ void run(uint32_t acc, float bias, bool zero) {
+        const int left = p.cols - f, row = c0 + (lane >> 2);
+        const bool whole = p.wide_out && left >= 8, wide = wide_add();
+        const int64_t step = (int64_t)lt::EPI_ROWS * p.cols;
+        int64_t at = (out_row + row) * p.cols + f;
+        const float *mine = staged + (lane >> 2) * lt::EPI_PITCH + (lane & 3) * 8;
+        uint32_t r[8] = {};
+        if (!zero) tmem_ld_8_issue(acc + (uint32_t)c0, r);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = activate<ACT>(v[c]);
-            if (add) {
-                if (p.wide_res && left >= 8) {
-                    const uint32_t words[4] = {ahead[i].x, ahead[i].y, ahead[i].z, ahead[i].w};
+        for (int i = 0; i < CHUNKS; ++i, at += step) {
+            if (c0 + i * lt::EPI_ROWS >= end) break;
+            if (i) __syncwarp();  // the previous rows have been read; the warp is together again
+            if (!zero) tmem_ld_8_wait(r);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float2 a = widen2<T>(words[c]);
-                        v[2 * c] += a.x;
-                        v[2 * c + 1] += a.y;
+            for (int j = 0; j < lt::EPI_ROWS; ++j) staged[j * lt::EPI_PITCH + lane] = __uint_as_float(r[j]) + bias;
+            __syncwarp();
+            if (!zero && i + 1 < CHUNKS && c0 + (i + 1) * lt::EPI_ROWS < end)
+                tmem_ld_8_issue(acc + (uint32_t)(c0 + (i + 1) * lt::EPI_ROWS), r);
+            if (row + i * lt::EPI_ROWS >= end || left <= 0) continue;
+            const float4 lo = *reinterpret_cast<const float4 *>(mine), hi = *reinterpret_cast<const float4 *>(mine + 4);
+            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            if constexpr (FORWARD) {
+                if (p.pre) store8(static_cast<T *>(p.pre) + at, v, whole, left);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = activate<ACT>(v[k]);
+                if (wide) {
+                    const uint32_t words[4] = {res[i].x, res[i].y, res[i].z, res[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 a = widen2<T>(words[k]);
+                        v[2 * k] += a.x;
+                        v[2 * k + 1] += a.y;
                     }
-                } else {
-                    const T *res = static_cast<const T *>(p.residual) + row * p.ldr + f;
+                } else if (add) {
+                    const T *src = static_cast<const T *>(p.residual) + (out_row + row + i * lt::EPI_ROWS) * p.ldr + f;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (c < left) v[c] += widen(res[c]);
+                    for (int k = 0; k < 8; ++k)
+                        if (k < left) v[k] += widen(src[k]);
                 }
             }
+            store8(static_cast<T *>(p.out) + at, v, whole, left);
         }
-        store8(static_cast<T *>(p.out) + at, v, whole, left);
     }
-}
-
-// One warp's columns [c, end) of a unit: accumulator -> staged rows -> memory.
-// While one chunk of 16 rows is finished, the next one's accumulator and
-// residual are on their way.
-template <Product MODE, typename T, int ACT>
-__device__ __forceinline__ void finish_unit(const LinearTcParams &p, float *staged, uint32_t acc, int64_t out_row,
-                                            int c, int end, int f, float bias, bool zero, int lane) {
-    const bool add = MODE == Product::kForward && p.residual && !zero;
-    const int fl = f + (lane & 3) * 8;
-    uint32_t r[16] = {};
-    uint4 res[kLaneRows] = {};
-    if (!zero) tmem_ld_16_issue(acc + (uint32_t)c, r);
-    if (add && p.wide_res) prefetch_residual<T>(p, out_row + c, end - c, fl, lane, res);
-#pragma unroll 1
-    for (; c < end; c += lt::EPI_ROWS) {
-        if (!zero) tmem_ld_16_wait(r);
-        __syncwarp();  // the previous rows have been read
-#pragma unroll
-        for (int i = 0; i < lt::EPI_ROWS; ++i) staged[i * lt::EPI_PITCH + lane] = __uint_as_float(r[i]) + bias;
-        __syncwarp();
-        uint4 now[kLaneRows];
-#pragma unroll
-        for (int i = 0; i < kLaneRows; ++i) now[i] = res[i];
-        if (c + lt::EPI_ROWS < end) {
-            if (!zero) tmem_ld_16_issue(acc + (uint32_t)(c + lt::EPI_ROWS), r);
-            if (add && p.wide_res)
-                prefetch_residual<T>(p, out_row + c + lt::EPI_ROWS, end - c - lt::EPI_ROWS, fl, lane, res);
-        }
-        store_rows<MODE, T, ACT>(p, staged, out_row + c, end - c, fl, add, now, lane);
-    }
-}
+};
 
 template <Product MODE, int BN, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
@@ -308,30 +302,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     if (warp < lt::EPI_WARPS) {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3, part = warp >> 2;
-        float *staged = reinterpret_cast<float *>(smem + C::STAGING_BASE) + warp * lt::EPI_ROWS * lt::EPI_PITCH;
+        using F = Finish<MODE, BN, T>;
+        F fin{p, reinterpret_cast<float *>(smem + C::STAGING_BASE) + warp * lt::EPI_ROWS * lt::EPI_PITCH, lane};
         int use = 0;
-        for (int64_t u = pair; u < units.total; u += num_pairs) {
+        for (int u = pair; u < units.total; u += num_pairs) {
             const Unit t = units.at(u);
             const bool zero = t.c1 <= t.c0;  // nothing to multiply: rows of no expert, experts without rows
             const int buf = use & 1;
+            const int f = t.p0 + rank * lt::BP_CTA + quarter * 32;  // this warp's first feature
+            float bias = 0.f;
+            if (MODE == Product::kForward && p.bias && !zero && f + lane < p.cols)
+                bias = widen(static_cast<const T *>(p.bias)[(int64_t)t.expert * p.cols + f + lane]);
+            fin.c0 = part * F::COLS;
+            fin.end = min(t.qn, fin.c0 + F::COLS);
+            fin.f = f + (lane & 3) * 8;
+            fin.out_row = MODE == Product::kWeights ? (int64_t)t.expert * p.out_rows + t.q0 : (int64_t)t.q0;
+            fin.add = MODE == Product::kForward && p.residual && !zero;
+            fin.prefetch();
             if (!zero) {
                 if (!mbar_wait_warp(bar(C::T_FULL + buf), (use >> 1) & 1, p.status)) break;
                 tc_fence_after();
             }
             const uint32_t acc = tmem_base + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
-            const int f = t.p0 + rank * lt::BP_CTA + quarter * 32;  // this warp's first feature
-            float bias = 0.f;
-            if (MODE == Product::kForward && p.bias && !zero && f + lane < p.cols)
-                bias = widen(static_cast<const T *>(p.bias)[(int64_t)t.expert * p.cols + f + lane]);
-            const int64_t out_row = MODE == Product::kWeights ? (int64_t)t.expert * p.out_rows + t.q0 : t.q0;
-            const int c0 = part * (BN / 2), c1 = min(t.qn, (part + 1) * (BN / 2));
-            if (c0 < c1) {
+            if (fin.c0 < fin.end) {
                 if constexpr (MODE == Product::kForward)
-                    with_activation(p.activation, [&](auto a) {
-                        finish_unit<MODE, T, decltype(a)::value>(p, staged, acc, out_row, c0, c1, f, bias, zero, lane);
-                    });
+                    with_activation(p.activation, [&](auto a) { fin.template run<decltype(a)::value>(acc, bias, zero); });
                 else
-                    finish_unit<MODE, T, KMEANS_ACT_NONE>(p, staged, acc, out_row, c0, c1, f, 0.f, zero, lane);
+                    fin.template run<KMEANS_ACT_NONE>(acc, bias, zero);
             }
             if (!zero) {
                 tc_fence_before();
@@ -340,125 +337,150 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                 ++use;
             }
         }
-    } else if (warp == lt::WARP_TMA) {
-        // ------------------------------------------------------- TMA producer
-        if (lane == 0) {
+    } else {
+        // One thread of each of these warps feeds the pipeline, and an MMA or
+        // a load that it issues late is lost time: working out a unit costs
+        // some thousand cycles of one thread (between two units that was 2200
+        // cycles without an MMA), so the warp does it for 32 units at once.
+        Unit *list = reinterpret_cast<Unit *>(smem + C::LIST_BASE + (warp - lt::WARP_TMA) * lt::LIST_BYTES);
+        const bool issuer = warp == lt::WARP_RELAY || lane == 0;  // the relay's lanes stay together
+        int s = 0, use = 0;
+        uint32_t phase = 0;
+        bool ok = !(warp == lt::WARP_TMA && p.test_starve) && !(warp == lt::WARP_RELAY && !RELAY) &&
+                  !(warp == lt::WARP_MMA && rank != 0);
+        int issued = 0;
+        auto advance = [&] {
+            if (++s == C::STAGES) {
+                s = 0;
+                phase ^= 1;
+            }
+        };
+        if (warp == lt::WARP_TMA && lane == 0) {
             tma_prefetch_desc(&tmA);
             tma_prefetch_desc(&tmB);
-            int it = 0;
-            bool ok = !p.test_starve;
-            for (int64_t u = pair; u < units.total && ok; u += num_pairs) {
-                const Unit t = units.at(u);
-                const int pa = t.p0 + rank * lt::BP_CTA;
-                // the MMA's N is cut to the rows that exist (a multiple of 32);
-                // each CTA holds half of it
-                const int qb = t.q0 + rank * (MODE == Product::kWeights ? BN / 2 : (min(BN, (t.qn + 31) & ~31) >> 1));
-                for (int c = t.c0; c < t.c1; c += lt::BK, ++it) {
-                    const int s = it % C::STAGES;
-                    if (!mbar_wait(bar(C::EMPTY + s), ((it / C::STAGES) & 1) ^ 1, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES, full = bar(C::FULL + s);
-                    if constexpr (RELAY) {
-                        mbar_arrive_expect_tx(full, C::STAGE);
-#pragma unroll
-                        for (int h = 0; h < lt::BP_CTA / 64; ++h)
-                            tma_load_2d(sa + h * (64 * lt::BK * 2), &tmA, full, pa + h * 64, c);
-#pragma unroll
-                        for (int h = 0; h < BN / 2 / 64; ++h)
-                            tma_load_2d(sb + h * (64 * lt::BK * 2), &tmB, full, qb + h * 64, c);
-                    } else {
-                        // both CTAs' bytes count on the even CTA's barrier
-                        if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::STAGE);
-                        const uint32_t pair_full = map_to_cta(full, 0);
-                        if constexpr (MODE == Product::kForward) {
-                            tma_load_3d_pair(sa, &tmA, pair_full, c, pa, t.expert);
-                        } else {
+        }
+        for (int u0 = pair; u0 < units.total; u0 += lt::LIST_UNITS * num_pairs) {
+            __syncwarp();
+            const int mine = u0 + lane * num_pairs;
+            if (mine < units.total) list[lane] = units.at(mine);
+            __syncwarp();
+            const int here = min(lt::LIST_UNITS, (units.total - u0 + num_pairs - 1) / num_pairs);
+            for (int i = 0; i < here && ok && issuer; ++i) {
+                const Unit t = list[i];
+                if (warp == lt::WARP_TMA) {
+                    // ------------------------------------------- TMA producer
+                    const int pa = t.p0 + rank * lt::BP_CTA;
+                    // the MMA's N is cut to the rows that exist (a multiple of
+                    // 32); each CTA holds half of it
+                    const int qb =
+                        t.q0 + rank * (MODE == Product::kWeights ? BN / 2 : (min(BN, (t.qn + 31) & ~31) >> 1));
+                    for (int c = t.c0; c < t.c1; c += lt::BK) {
+                        if (!mbar_wait(bar(C::EMPTY + s), phase ^ 1, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES, full = bar(C::FULL + s);
+                        if constexpr (RELAY) {
+                            mbar_arrive_expect_tx(full, C::STAGE);
 #pragma unroll
                             for (int h = 0; h < lt::BP_CTA / 64; ++h)
-                                tma_load_3d_pair(sa + h * (64 * lt::BK * 2), &tmA, pair_full, pa + h * 64, c, t.expert);
-                        }
-                        tma_load_2d_pair(sb, &tmB, pair_full, c, qb);
-                    }
-                }
-            }
-            if (!ok && (RELAY || rank == 0)) {
-                // let copies already in flight land before the CTAs exit (the
-                // odd CTA's are on the even one's barriers, and it leaves last)
-                for (int j = max(0, it - C::STAGES); j < it; ++j)
-                    mbar_wait_drain(bar(C::FULL + (j % C::STAGES)), (j / C::STAGES) & 1);
-            }
-        }
-    } else if (warp == lt::WARP_RELAY) {
-        // -------------------------------------------------------------- relay
-        int it = 0;
-        bool ok = RELAY;
-        for (int64_t u = pair; u < units.total && ok; u += num_pairs) {
-            const Unit t = units.at(u);
-            for (int c = t.c0; c < t.c1; c += lt::BK, ++it) {
-                const int s = it % C::STAGES;
-                if (!mbar_wait_warp(bar(C::FULL + s), (it / C::STAGES) & 1, p.status)) {
-                    ok = false;
-                    break;
-                }
-                if (t.c1 - c < lt::BK) {
-                    // rows past the expert's end: every 64-value chunk of both
-                    // operands holds them as whole 128-byte lines
-                    uint8_t *st = smem + s * C::STAGE;
-                    constexpr int CHUNKS = C::STAGE / (64 * lt::BK * 2);
-                    for (int i = (t.c1 - c) * 8 + lane; i < lt::BK * 8; i += 32)
+                                tma_load_2d(sa + h * (64 * lt::BK * 2), &tmA, full, pa + h * 64, c);
 #pragma unroll
-                        for (int h = 0; h < CHUNKS; ++h)
-                            *reinterpret_cast<uint4 *>(st + h * (64 * lt::BK * 2) + i * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive_cluster(map_to_cta(bar(C::READY + s), 0));
-            }
-        }
-    } else {
-        // ---------------------------------------------------------- MMA issue
-        if (lane == 0 && rank == 0) {
-            int it = 0, use = 0;
-            bool ok = true;
-            for (int64_t u = pair; u < units.total && ok; u += num_pairs) {
-                const Unit t = units.at(u);
-                if (t.c1 <= t.c0) continue;
-                const int n = MODE == Product::kWeights ? BN : min(BN, (t.qn + 31) & ~31);
-                const uint32_t idesc = umma_idesc_16_f32(sizeof(T) == 2 && !std::is_same<T, __half>::value, A_MN, B_MN,
-                                                         lt::BP, n);
-                const int buf = use & 1;
-                if (!mbar_wait_cluster(bar(C::T_EMPTY + buf), ((use >> 1) & 1) ^ 1, p.status)) break;
-                tc_fence_after();
-                const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
-                for (int c = t.c0; c < t.c1; c += lt::BK, ++it) {
-                    const int s = it % C::STAGES;
-                    const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES;
+                            for (int h = 0; h < BN / 2 / 64; ++h)
+                                tma_load_2d(sb + h * (64 * lt::BK * 2), &tmB, full, qb + h * 64, c);
+                        } else {
+                            // both CTAs' bytes count on the even CTA's barrier
+                            if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::STAGE);
+                            const uint32_t pair_full = map_to_cta(full, 0);
+                            if constexpr (MODE == Product::kForward) {
+                                tma_load_3d_pair(sa, &tmA, pair_full, c, pa, t.expert);
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < lt::BP_CTA / 64; ++h)
+                                    tma_load_3d_pair(sa + h * (64 * lt::BK * 2), &tmA, pair_full, pa + h * 64, c,
+                                                     t.expert);
+                            }
+                            tma_load_2d_pair(sb, &tmB, pair_full, c, qb);
+                        }
+                        ++issued;
+                        advance();
+                    }
+                } else if (warp == lt::WARP_RELAY) {
+                    // -------------------------------------------------- relay
+                    for (int c = t.c0; c < t.c1; c += lt::BK) {
+                        if (!mbar_wait_warp(bar(C::FULL + s), phase, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        if (t.c1 - c < lt::BK) {
+                            // rows past the expert's end: every 64-value chunk
+                            // of both operands holds them as whole 128-byte
+                            // lines
+                            uint8_t *st = smem + s * C::STAGE;
+                            constexpr int CHUNKS = C::STAGE / (64 * lt::BK * 2);
+                            for (int k = (t.c1 - c) * 8 + lane; k < lt::BK * 8; k += 32)
+#pragma unroll
+                                for (int h = 0; h < CHUNKS; ++h)
+                                    *reinterpret_cast<uint4 *>(st + h * (64 * lt::BK * 2) + k * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        if (lane == 0) mbar_arrive_cluster(map_to_cta(bar(C::READY + s), 0));
+                        advance();
+                    }
+                } else if (t.c1 > t.c0) {
+                    // ---------------------------------------------- MMA issue
+                    const int n = MODE == Product::kWeights ? BN : min(BN, (t.qn + 31) & ~31);
+                    const uint32_t idesc =
+                        umma_idesc_16_f32(std::is_same<T, __nv_bfloat16>::value, A_MN, B_MN, lt::BP, n);
                     // 16 values of the contraction: 32 bytes along a K-major
                     // row, or 16 lines of 128 bytes
-                    uint64_t da[4], db[4];
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        da[kk] = A_MN ? umma_smem_desc_mn(sa + kk * 2048, 64 * lt::BK * 2, 1024)
-                                      : umma_smem_desc(sa + kk * 32, 1024, kLayoutSW128);
-                        db[kk] = B_MN ? umma_smem_desc_mn(sb + kk * 2048, 64 * lt::BK * 2, 1024)
-                                      : umma_smem_desc(sb + kk * 32, 1024, kLayoutSW128);
-                    }
-                    if (!mbar_wait_cluster(bar((RELAY ? C::READY : C::FULL) + s), (it / C::STAGES) & 1, p.status)) {
+                    constexpr uint32_t A_STEP = (A_MN ? 2048 : 32) >> 4, B_STEP = (B_MN ? 2048 : 32) >> 4;
+                    const uint64_t a0 = A_MN ? umma_smem_desc_mn(sbase, 64 * lt::BK * 2, 1024)
+                                             : umma_smem_desc(sbase, 1024, kLayoutSW128);
+                    const uint64_t b0 = B_MN ? umma_smem_desc_mn(sbase + C::A_BYTES, 64 * lt::BK * 2, 1024)
+                                             : umma_smem_desc(sbase + C::A_BYTES, 1024, kLayoutSW128);
+                    const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32);
+                    const int buf = use & 1;
+                    const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
+                    if (!mbar_wait_cluster(bar(C::T_EMPTY + buf), ((use >> 1) & 1) ^ 1, p.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_ss_pair(acc, da[kk], db[kk], idesc, (c != t.c0 || kk != 0) ? 1u : 0u);
-                    mma_commit_pair_multicast(bar(C::EMPTY + s), 0x3);
+                    uint32_t more = 0;  // the first MMA of a unit clears the accumulator
+                    for (int left = (t.c1 - t.c0 + lt::BK - 1) / lt::BK; left > 0; --left) {
+                        const uint32_t off = (uint32_t)s * (C::STAGE >> 4);
+                        const uint32_t a_lo = (uint32_t)a0 + off, b_lo = (uint32_t)b0 + off;
+                        if (!mbar_wait_cluster(bar((RELAY ? C::READY : C::FULL) + s), phase, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        mma_16_ss_pair(acc, a_lo, a_hi, b_lo, b_hi, idesc, more);
+                        mma_16_ss_pair(acc, a_lo + A_STEP, a_hi, b_lo + B_STEP, b_hi, idesc, 1u);
+                        mma_16_ss_pair(acc, a_lo + 2 * A_STEP, a_hi, b_lo + 2 * B_STEP, b_hi, idesc, 1u);
+                        mma_16_ss_pair(acc, a_lo + 3 * A_STEP, a_hi, b_lo + 3 * B_STEP, b_hi, idesc, 1u);
+                        mma_commit_pair_multicast(bar(C::EMPTY + s), 0x3);
+                        more = 1u;
+                        advance();
+                    }
+                    if (!ok) break;
+                    mma_commit_pair_multicast(bar(C::T_FULL + buf), 0x3);
+                    ++use;
                 }
-                if (!ok) break;
-                mma_commit_pair_multicast(bar(C::T_FULL + buf), 0x3);
-                ++use;
             }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+        }
+        if (warp == lt::WARP_TMA && lane == 0 && !ok && (RELAY || rank == 0)) {
+            // let copies already in flight land before the CTAs exit (the odd
+            // CTA's are on the even one's barriers, and it leaves last)
+            for (int j = max(0, issued - C::STAGES); j < issued; ++j)
+                mbar_wait_drain(bar(C::FULL + (j % C::STAGES)), (j / C::STAGES) & 1);
+        }
+        if (warp == lt::WARP_MMA && lane == 0 && rank == 0) {
             // no MMA may still be writing tensor memory when it is released
             mma_commit_pair(bar(C::DRAIN));
             mbar_wait_drain(bar(C::DRAIN), 0);
