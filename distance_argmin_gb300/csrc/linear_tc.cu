@@ -249,6 +249,9 @@ struct Finish {
     }
 };
 
+// A value that all lanes of a converged warp hold, in a uniform register.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+
 template <Product MODE, int BN, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -338,77 +341,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             }
         }
     } else {
-        // One thread of each of these warps feeds the pipeline, and an MMA or
-        // a load that it issues late is lost time: working out a unit costs
-        // some thousand cycles of one thread (between two units that was 2200
-        // cycles without an MMA), so the warp does it for 32 units at once.
+        // These warps feed the pipeline, and an MMA or a load that they issue
+        // late is lost time, also because the epilogue's warps take turns with
+        // them.  So the whole warp walks the units (the addresses and
+        // descriptors are then uniform and need no moves between register
+        // files), one elected lane issues, and units are worked out 32 at a
+        // time, one per lane (one after the other they cost some thousand
+        // cycles each: 2200 cycles without an MMA between two units).
         Unit *list = reinterpret_cast<Unit *>(smem + C::LIST_BASE + (warp - lt::WARP_TMA) * lt::LIST_BYTES);
-        const bool issuer = warp == lt::WARP_RELAY || lane == 0;  // the relay's lanes stay together
-        int s = 0, use = 0;
+        const bool leader = elect_one();
+        int s = 0, use = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = !(warp == lt::WARP_TMA && p.test_starve) && !(warp == lt::WARP_RELAY && !RELAY) &&
                   !(warp == lt::WARP_MMA && rank != 0);
-        int issued = 0;
         auto advance = [&] {
             if (++s == C::STAGES) {
                 s = 0;
                 phase ^= 1;
             }
         };
-        if (warp == lt::WARP_TMA && lane == 0) {
+        if (warp == lt::WARP_TMA && leader) {
             tma_prefetch_desc(&tmA);
             tma_prefetch_desc(&tmB);
         }
-        for (int u0 = pair; u0 < units.total; u0 += lt::LIST_UNITS * num_pairs) {
+        for (int u0 = pair; u0 < units.total && ok; u0 += lt::LIST_UNITS * num_pairs) {
             __syncwarp();
             const int mine = u0 + lane * num_pairs;
             if (mine < units.total) list[lane] = units.at(mine);
             __syncwarp();
             const int here = min(lt::LIST_UNITS, (units.total - u0 + num_pairs - 1) / num_pairs);
-            for (int i = 0; i < here && ok && issuer; ++i) {
+            for (int i = 0; i < here && ok; ++i) {
                 const Unit t = list[i];
+                const int kblocks = uniform((t.c1 - t.c0 + lt::BK - 1) / lt::BK);
                 if (warp == lt::WARP_TMA) {
                     // ------------------------------------------- TMA producer
-                    const int pa = t.p0 + rank * lt::BP_CTA;
+                    const int pa = uniform(t.p0) + rank * lt::BP_CTA, e = uniform(t.expert);
                     // the MMA's N is cut to the rows that exist (a multiple of
                     // 32); each CTA holds half of it
-                    const int qb =
-                        t.q0 + rank * (MODE == Product::kWeights ? BN / 2 : (min(BN, (t.qn + 31) & ~31) >> 1));
-                    for (int c = t.c0; c < t.c1; c += lt::BK) {
-                        if (!mbar_wait(bar(C::EMPTY + s), phase ^ 1, p.status)) {
+                    const int qb = uniform(
+                        t.q0 + rank * (MODE == Product::kWeights ? BN / 2 : (min(BN, (t.qn + 31) & ~31) >> 1)));
+                    int c = uniform(t.c0);
+                    for (int left = kblocks; left > 0; --left, c += lt::BK) {
+                        if (!mbar_wait_converged(bar(C::EMPTY + s), phase ^ 1, p.status)) {
                             ok = false;
                             break;
                         }
                         const uint32_t sa = sbase + s * C::STAGE, sb = sa + C::A_BYTES, full = bar(C::FULL + s);
-                        if constexpr (RELAY) {
-                            mbar_arrive_expect_tx(full, C::STAGE);
-#pragma unroll
-                            for (int h = 0; h < lt::BP_CTA / 64; ++h)
-                                tma_load_2d(sa + h * (64 * lt::BK * 2), &tmA, full, pa + h * 64, c);
-#pragma unroll
-                            for (int h = 0; h < BN / 2 / 64; ++h)
-                                tma_load_2d(sb + h * (64 * lt::BK * 2), &tmB, full, qb + h * 64, c);
-                        } else {
-                            // both CTAs' bytes count on the even CTA's barrier
-                            if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::STAGE);
-                            const uint32_t pair_full = map_to_cta(full, 0);
-                            if constexpr (MODE == Product::kForward) {
-                                tma_load_3d_pair(sa, &tmA, pair_full, c, pa, t.expert);
-                            } else {
+                        if (leader) {
+                            if constexpr (RELAY) {
+                                mbar_arrive_expect_tx(full, C::STAGE);
 #pragma unroll
                                 for (int h = 0; h < lt::BP_CTA / 64; ++h)
-                                    tma_load_3d_pair(sa + h * (64 * lt::BK * 2), &tmA, pair_full, pa + h * 64, c,
-                                                     t.expert);
+                                    tma_load_2d(sa + h * (64 * lt::BK * 2), &tmA, full, pa + h * 64, c);
+#pragma unroll
+                                for (int h = 0; h < BN / 2 / 64; ++h)
+                                    tma_load_2d(sb + h * (64 * lt::BK * 2), &tmB, full, qb + h * 64, c);
+                            } else {
+                                // both CTAs' bytes count on the even CTA's barrier
+                                if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::STAGE);
+                                const uint32_t pair_full = map_to_cta(full, 0);
+                                if constexpr (MODE == Product::kForward) {
+                                    tma_load_3d_pair(sa, &tmA, pair_full, c, pa, e);
+                                } else {
+#pragma unroll
+                                    for (int h = 0; h < lt::BP_CTA / 64; ++h)
+                                        tma_load_3d_pair(sa + h * (64 * lt::BK * 2), &tmA, pair_full, pa + h * 64, c, e);
+                                }
+                                tma_load_2d_pair(sb, &tmB, pair_full, c, qb);
                             }
-                            tma_load_2d_pair(sb, &tmB, pair_full, c, qb);
                         }
+                        __syncwarp();
                         ++issued;
                         advance();
                     }
                 } else if (warp == lt::WARP_RELAY) {
                     // -------------------------------------------------- relay
                     for (int c = t.c0; c < t.c1; c += lt::BK) {
-                        if (!mbar_wait_warp(bar(C::FULL + s), phase, p.status)) {
+                        if (!mbar_wait_converged(bar(C::FULL + s), phase, p.status)) {
                             ok = false;
                             break;
                         }
@@ -426,12 +435,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                             fence_proxy_async_smem();
                             __syncwarp();
                         }
-                        if (lane == 0) mbar_arrive_cluster(map_to_cta(bar(C::READY + s), 0));
+                        if (leader) mbar_arrive_cluster(map_to_cta(bar(C::READY + s), 0));
+                        __syncwarp();
                         advance();
                     }
-                } else if (t.c1 > t.c0) {
+                } else if (kblocks > 0) {
                     // ---------------------------------------------- MMA issue
-                    const int n = MODE == Product::kWeights ? BN : min(BN, (t.qn + 31) & ~31);
+                    const int n = MODE == Product::kWeights ? BN : uniform(min(BN, (t.qn + 31) & ~31));
                     const uint32_t idesc =
                         umma_idesc_16_f32(std::is_same<T, __nv_bfloat16>::value, A_MN, B_MN, lt::BP, n);
                     // 16 values of the contraction: 32 bytes along a K-major
@@ -444,43 +454,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                     const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32);
                     const int buf = use & 1;
                     const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
-                    if (!mbar_wait_cluster(bar(C::T_EMPTY + buf), ((use >> 1) & 1) ^ 1, p.status)) {
+                    if (!mbar_wait_converged(bar(C::T_EMPTY + buf), ((use >> 1) & 1) ^ 1, p.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     uint32_t more = 0;  // the first MMA of a unit clears the accumulator
-                    for (int left = (t.c1 - t.c0 + lt::BK - 1) / lt::BK; left > 0; --left) {
+                    for (int left = kblocks; left > 0; --left) {
                         const uint32_t off = (uint32_t)s * (C::STAGE >> 4);
                         const uint32_t a_lo = (uint32_t)a0 + off, b_lo = (uint32_t)b0 + off;
-                        if (!mbar_wait_cluster(bar((RELAY ? C::READY : C::FULL) + s), phase, p.status)) {
+                        if (!mbar_wait_converged(bar((RELAY ? C::READY : C::FULL) + s), phase, p.status)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        mma_16_ss_pair(acc, a_lo, a_hi, b_lo, b_hi, idesc, more);
-                        mma_16_ss_pair(acc, a_lo + A_STEP, a_hi, b_lo + B_STEP, b_hi, idesc, 1u);
-                        mma_16_ss_pair(acc, a_lo + 2 * A_STEP, a_hi, b_lo + 2 * B_STEP, b_hi, idesc, 1u);
-                        mma_16_ss_pair(acc, a_lo + 3 * A_STEP, a_hi, b_lo + 3 * B_STEP, b_hi, idesc, 1u);
-                        mma_commit_pair_multicast(bar(C::EMPTY + s), 0x3);
+                        if (leader) {
+                            mma_16_ss_pair(acc, a_lo, a_hi, b_lo, b_hi, idesc, more);
+                            mma_16_ss_pair(acc, a_lo + A_STEP, a_hi, b_lo + B_STEP, b_hi, idesc, 1u);
+                            mma_16_ss_pair(acc, a_lo + 2 * A_STEP, a_hi, b_lo + 2 * B_STEP, b_hi, idesc, 1u);
+                            mma_16_ss_pair(acc, a_lo + 3 * A_STEP, a_hi, b_lo + 3 * B_STEP, b_hi, idesc, 1u);
+                            mma_commit_pair_multicast(bar(C::EMPTY + s), 0x3);
+                        }
+                        __syncwarp();
                         more = 1u;
                         advance();
                     }
                     if (!ok) break;
-                    mma_commit_pair_multicast(bar(C::T_FULL + buf), 0x3);
+                    if (leader) mma_commit_pair_multicast(bar(C::T_FULL + buf), 0x3);
+                    __syncwarp();
                     ++use;
                 }
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
         }
-        if (warp == lt::WARP_TMA && lane == 0 && !ok && (RELAY || rank == 0)) {
+        if (warp == lt::WARP_TMA && leader && !ok && (RELAY || rank == 0)) {
             // let copies already in flight land before the CTAs exit (the odd
             // CTA's are on the even one's barriers, and it leaves last)
             for (int j = max(0, issued - C::STAGES); j < issued; ++j)
                 mbar_wait_drain(bar(C::FULL + (j % C::STAGES)), (j / C::STAGES) & 1);
         }
-        if (warp == lt::WARP_MMA && lane == 0 && rank == 0) {
+        if (warp == lt::WARP_MMA && leader && rank == 0) {
             // no MMA may still be writing tensor memory when it is released
             mma_commit_pair(bar(C::DRAIN));
             mbar_wait_drain(bar(C::DRAIN), 0);

@@ -50,6 +50,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0u;
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t pred;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(pred));
+    return pred != 0u;
+}
+
 // Single-thread bounded wait for the phase with parity `parity` to complete.
 // Returns false (after raising kFlagTimeout) when the wall-clock limit passes,
 // or as soon as another thread anywhere has raised an error.
@@ -90,6 +101,12 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ui
             if (__shfl_sync(0xffffffffu, bail, 0)) return false;
         }
     }
+}
+
+// mbar_wait_warp with a short way through when the phase is already over.
+__device__ __forceinline__ bool mbar_wait_converged(uint32_t bar, uint32_t parity, uint32_t *status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return mbar_wait_warp(bar, parity, status);
 }
 
 // ---------------------------------------------------------------------------
