@@ -23,12 +23,12 @@ __global__ void linear_align_kernel(const T *src, int64_t lds, int64_t rows, int
 }
 
 // dz = dy act'(pre), rounded to the matrices' type, and the bias gradient's
-// partial sums from the same read.  A block takes 64 rows of one expert by 256
+// partial sums from the same read.  A block takes 128 rows of one expert by 256
 // columns: a lane 8 columns (16 bytes where the rows allow), a warp every
 // eighth row.  Its column sums of the unrounded values go to one row of
 // `partial` per row tile; linear_bias_join_kernel adds an expert's in order, so
 // the result does not depend on the schedule.
-constexpr int kSlopeRows = 64;
+constexpr int kSlopeRows = 128;
 constexpr int kSlopeCols = 256;
 constexpr int kSlopeThreads = 256;
 
@@ -75,31 +75,29 @@ __device__ bool find_row_tile(const int32_t *offsets, int n_experts, int64_t m, 
 }
 
 template <bool WIDE, typename T>
-__device__ __forceinline__ void load8(const T *p, int left, float (&v)[8]) {
-    if constexpr (WIDE) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ uint4 load8(const T *p, int left) {
+    if constexpr (WIDE) return *reinterpret_cast<const uint4 *>(p);
+    uint32_t w[4] = {};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float2 a = widen2<T>(words[c]);
-            v[2 * c] = a.x;
-            v[2 * c + 1] = a.y;
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = c < left ? widen(p[c]) : 0.f;
-    }
+    for (int c = 0; c < 8; ++c)
+        if (c < left) w[c / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[c] << ((c & 1) * 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+constexpr int kSlopeBatch = 4;  // rows whose loads are in flight together
+
 template <bool WIDE, typename T>
-__global__ void __launch_bounds__(kSlopeThreads) linear_slope_kernel(const T *dy, int64_t lddy, const T *pre,
-                                                                     const int32_t *offsets, int n_experts, int64_t m,
-                                                                     int64_t n, int act, T *dz, int64_t ldz,
-                                                                     float *partial, uint32_t *clear) {
+__global__ void __launch_bounds__(kSlopeThreads, 2) linear_slope_kernel(const T *__restrict__ dy, int64_t lddy,
+                                                                        const T *__restrict__ pre,
+                                                                        const int32_t *__restrict__ offsets,
+                                                                        int n_experts, int64_t m, int64_t n, int act,
+                                                                        T *__restrict__ dz, int64_t ldz,
+                                                                        float *__restrict__ partial, uint32_t *clear) {
     __shared__ float sums[kSlopeThreads / 32][kSlopeCols];
     griddep_wait();
     if (clear && (blockIdx.x | blockIdx.y | threadIdx.x) == 0u) *clear = 0u;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int WARPS = kSlopeThreads / 32;
     RowTile t;
     if (!find_row_tile(offsets, n_experts, m, blockIdx.y, t)) return;
     const int64_t c0 = (int64_t)blockIdx.x * kSlopeCols + lane * 8;
@@ -108,25 +106,43 @@ __global__ void __launch_bounds__(kSlopeThreads) linear_slope_kernel(const T *dy
     if (left > 0)
         with_activation(act, [&](auto a) {
             constexpr int ACT = decltype(a)::value;
-#pragma unroll 4
-            for (int64_t r = t.r0 + warp; r < t.r1; r += kSlopeThreads / 32) {
-                float g[8], z[8];
-                load8<WIDE>(dy + r * lddy + c0, left, g);
-                if constexpr (ACT != KMEANS_ACT_NONE) load8<WIDE>(pre + r * n + c0, left, z);
+            for (int64_t r = t.r0 + warp; r < t.r1; r += WARPS * kSlopeBatch) {
+                uint4 g[kSlopeBatch], z[kSlopeBatch];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    if constexpr (ACT != KMEANS_ACT_NONE) g[c] *= slope<ACT>(z[c]);
-                    sum[c] += g[c];
+                for (int b = 0; b < kSlopeBatch; ++b) {
+                    const int64_t row = r + b * WARPS;
+                    if (row >= t.r1) continue;
+                    g[b] = load8<WIDE>(dy + row * lddy + c0, left);
+                    if constexpr (ACT != KMEANS_ACT_NONE) z[b] = load8<WIDE>(pre + row * n + c0, left);
                 }
-                if (dz) {
-                    T *out = dz + r * ldz + c0;  // dz's rows always start on 16 bytes
-                    if (left == 8) {
-                        *reinterpret_cast<uint4 *>(out) = make_uint4(narrow2<T>(g[0], g[1]), narrow2<T>(g[2], g[3]),
-                                                                     narrow2<T>(g[4], g[5]), narrow2<T>(g[6], g[7]));
-                    } else {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            if (c < left) out[c] = narrow<T>(g[c]);
+                for (int b = 0; b < kSlopeBatch; ++b) {
+                    const int64_t row = r + b * WARPS;
+                    if (row >= t.r1) continue;
+                    const uint32_t gw[4] = {g[b].x, g[b].y, g[b].z, g[b].w}, zw[4] = {z[b].x, z[b].y, z[b].z, z[b].w};
+                    uint32_t ow[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float2 v = widen2<T>(gw[c]);
+                        if constexpr (ACT != KMEANS_ACT_NONE) {
+                            const float2 y = widen2<T>(zw[c]);
+                            v.x *= slope<ACT>(y.x);
+                            v.y *= slope<ACT>(y.y);
+                        }
+                        sum[2 * c] += v.x;
+                        sum[2 * c + 1] += v.y;
+                        ow[c] = narrow2<T>(v.x, v.y);
+                    }
+                    if (dz) {
+                        T *out = dz + row * ldz + c0;  // dz's rows always start on 16 bytes
+                        if (left == 8) {
+                            *reinterpret_cast<uint4 *>(out) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                if (c < left)
+                                    reinterpret_cast<uint16_t *>(out)[c] = (uint16_t)(ow[c / 2] >> ((c & 1) * 16));
+                        }
                     }
                 }
             }
@@ -139,7 +155,7 @@ __global__ void __launch_bounds__(kSlopeThreads) linear_slope_kernel(const T *dy
     if (col >= n) return;
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSlopeThreads / 32; ++w) s += sums[w][threadIdx.x];
+    for (int w = 0; w < WARPS; ++w) s += sums[w][threadIdx.x];
     partial[(int64_t)blockIdx.y * n + col] = s;
 }
 

@@ -64,14 +64,18 @@ constexpr int LIST_BYTES = LIST_UNITS * 24;
 constexpr int SMEM_LIMIT = 232448;
 constexpr int BAR_BYTES = 512;
 
-template <int BN>
+constexpr int PARTS = EPI_WARPS / 4;  // groups of four epilogue warps, one per lane quarter
+constexpr int STORE_ROWS = 16;        // rows of a bulk store (weights): two buffers of 16 x 256 bytes per part
+constexpr int STORE_BYTES = STORE_ROWS * BP_CTA * 2;
+
+template <int BN, bool STORES = false>
 struct Cfg {
     static constexpr int A_BYTES = BP_CTA * BK * 2;
     static constexpr int B_BYTES = BN / 2 * BK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = BN >= 256 ? 6 : BN >= 128 ? 8 : 9;
+    static constexpr int STAGES = STORES ? 5 : BN >= 256 ? 6 : BN >= 128 ? 8 : 9;
     static constexpr int STAGING_BASE = STAGES * STAGE;
-    static constexpr int BAR_BASE = STAGING_BASE + STAGING;
+    static constexpr int BAR_BASE = STAGING_BASE + (STORES ? PARTS * 2 * STORE_BYTES : STAGING);
     static constexpr int LIST_BASE = BAR_BASE + BAR_BYTES;
     static constexpr int TABLE_BASE = LIST_BASE + 3 * LIST_BYTES;
     static constexpr int TMEM_COLS = 2 * BN;  // >= 64
@@ -97,6 +101,7 @@ struct LinearTcParams {
     int activation;
     void *out, *pre;
     int wide_out, wide_res;  // 16-byte accesses allowed
+    int bulk;                // weights: the output leaves by bulk stores
     uint32_t *status;
     int test_starve;  // test hook: the producer issues no loads, so the pipeline waits run out
     int clear;  // first kernel of the call: it clears the status word
@@ -249,14 +254,55 @@ struct Finish {
     }
 };
 
+// The weights product's output has no ragged rows, so a part (four warps, one
+// per lane quarter) rounds 16 rows of its 128 features into shared memory, in
+// the 128-byte swizzle, and one lane sends them off as two bulk tensor stores
+// that end at the matrix's edges by themselves.  Half the shared-memory traffic
+// of staging in float32 (which the MMAs beside it feel, see Finish) and whole
+// lines to L2.
+template <typename T>
+__device__ __forceinline__ void store_part(const LinearTcParams &p, const CUtensorMap *tmOut, uint8_t *buffers, int &ring,
+                                           uint32_t acc, int part, int quarter, int lane, int f, int q, int end,
+                                           int expert, bool zero) {
+    const uint32_t column = (uint32_t)(quarter & 1) * 4 + (lane >> 3);  // 16-byte chunk of the 128-byte row
+    for (int c = 0; c < end; c += lt::STORE_ROWS) {
+        uint32_t r[2][8] = {};
+        if (!zero) {
+            tmem_ld_8_issue(acc + (uint32_t)c, r[0]);
+            tmem_ld_8_issue(acc + (uint32_t)(c + 8), r[1]);
+        }
+        uint8_t *buf = buffers + ring * lt::STORE_BYTES;
+        uint8_t *half = buf + (quarter >> 1) * (lt::STORE_ROWS * 128) + (lane & 7) * 2;
+        if (!zero) {
+            tmem_ld_8_wait(r[0]);
+            tmem_ld_8_wait(r[1]);
+        }
+#pragma unroll
+        for (int j = 0; j < lt::STORE_ROWS; ++j)
+            *reinterpret_cast<T *>(half + j * 128 + ((column ^ (uint32_t)(j & 7)) << 4)) =
+                narrow<T>(__uint_as_float(r[j >> 3][j & 7]));
+        // the stores out of the other buffer have read it: it may be written
+        // once everyone has passed this barrier
+        if (quarter == 0) bulk_wait_read();
+        fence_proxy_async_smem();
+        named_barrier(1 + part, 128);
+        if (quarter == 0 && lane == 0) {
+            tma_store_3d(tmOut, smem_addr(buf), f, q + c, expert);
+            if (f + 64 < p.cols) tma_store_3d(tmOut, smem_addr(buf) + lt::STORE_ROWS * 128, f + 64, q + c, expert);
+            bulk_commit();
+        }
+        ring ^= 1;
+    }
+}
+
 // A value that all lanes of a converged warp hold, in a uniform register.
 __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
 template <Product MODE, int BN, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const LinearTcParams p) {
-    using C = lt::Cfg<BN>;
+                     const __grid_constant__ CUtensorMap tmOut, const LinearTcParams p) {
+    using C = lt::Cfg<BN, MODE == Product::kWeights>;
     constexpr bool A_MN = MODE != Product::kForward, B_MN = MODE == Product::kWeights;
     constexpr bool RELAY = MODE == Product::kWeights;  // rows may have to be cleared before the MMA
     static_assert(!B_MN || BN >= 128, "an N-contiguous operand comes in chunks of 64 per CTA");
@@ -307,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
         const int quarter = warp & 3, part = warp >> 2;
         using F = Finish<MODE, BN, T>;
         F fin{p, reinterpret_cast<float *>(smem + C::STAGING_BASE) + warp * lt::EPI_ROWS * lt::EPI_PITCH, lane};
-        int use = 0;
+        int use = 0, ring = 0;
         for (int u = pair; u < units.total; u += num_pairs) {
             const Unit t = units.at(u);
             const bool zero = t.c1 <= t.c0;  // nothing to multiply: rows of no expert, experts without rows
@@ -323,11 +369,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             fin.add = MODE == Product::kForward && p.residual && !zero;
             fin.prefetch();
             if (!zero) {
-                if (!mbar_wait_warp(bar(C::T_FULL + buf), (use >> 1) & 1, p.status)) break;
+                bool ok = mbar_wait_warp(bar(C::T_FULL + buf), (use >> 1) & 1, p.status);
+                // a part that meets at barriers goes on together or not at all
+                if (MODE == Product::kWeights) ok = named_barrier_all(1 + part, 128, ok);
+                if (!ok) break;
                 tc_fence_after();
             }
             const uint32_t acc = tmem_base + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
-            if (fin.c0 < fin.end) {
+            if (MODE == Product::kWeights && p.bulk) {
+                const int fc = t.p0 + rank * lt::BP_CTA;
+                if (fin.c0 < fin.end && fc < p.cols)
+                    store_part<T>(p, &tmOut, smem + C::STAGING_BASE + part * 2 * lt::STORE_BYTES, ring,
+                                  acc + (uint32_t)fin.c0, part, quarter, lane, fc, t.q0 + fin.c0, fin.end - fin.c0,
+                                  t.expert, zero);
+            } else if (fin.c0 < fin.end) {
                 if constexpr (MODE == Product::kForward)
                     with_activation(p.activation, [&](auto a) { fin.template run<decltype(a)::value>(acc, bias, zero); });
                 else
@@ -340,6 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                 ++use;
             }
         }
+        if (MODE == Product::kWeights && quarter == 0) bulk_wait();  // this lane's stores out of shared memory
     } else {
         // These warps feed the pipeline, and an MMA or a load that they issue
         // late is lost time, also because the epilogue's warps take turns with
@@ -531,7 +587,7 @@ bool encode(CUtensorMap *map, bool bf16, const void *base, int rank, const uint6
 
 template <Product MODE, int BN, typename T>
 cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcParams &p, cudaStream_t s) {
-    using C = lt::Cfg<BN>;
+    using C = lt::Cfg<BN, MODE == Product::kWeights>;
     static std::once_flag once[kMaxDevices];
     static std::atomic<int> err[kMaxDevices];
     int dev = 0;
@@ -543,13 +599,19 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
     });
     if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
 
-    CUtensorMap tmA, tmB;
+    CUtensorMap tmA, tmB, tmOut{};
     bool ok;
     if (MODE == Product::kWeights) {
         const uint64_t da[2] = {(uint64_t)sh.k, (uint64_t)sh.m}, pa[1] = {(uint64_t)g.lda};
         const uint64_t db[2] = {(uint64_t)sh.n, (uint64_t)sh.m}, pb[1] = {(uint64_t)g.ldb};
         const uint32_t box[2] = {64, lt::BK};
         ok = encode(&tmA, sh.bf16, g.a, 2, da, pa, box) && encode(&tmB, sh.bf16, g.b, 2, db, pb, box);
+        if (p.bulk) {
+            const uint64_t dd[3] = {(uint64_t)sh.k, (uint64_t)sh.n, (uint64_t)sh.n_experts};
+            const uint64_t pd[2] = {(uint64_t)sh.k, (uint64_t)(sh.k * sh.n)};
+            const uint32_t bd[3] = {64, lt::STORE_ROWS, 1};
+            ok = ok && encode(&tmOut, sh.bf16, g.out, 3, dd, pd, bd);
+        }
     } else {
         const uint64_t da[3] = {(uint64_t)sh.k, (uint64_t)sh.n, (uint64_t)sh.n_experts};
         const uint64_t pa[2] = {(uint64_t)g.pitch_w, (uint64_t)(g.pitch_w * sh.n)};
@@ -566,7 +628,7 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
     const int64_t most = device_sm_count() / 2, units = row_tiles * p.num_p;
     const unsigned pairs = (unsigned)(units < most ? units : most);
     return launch_kernel(true, linear_tc_kernel<MODE, BN, T>, dim3(2 * (pairs ? pairs : 1)), dim3(lt::THREADS),
-                         C::smem_bytes(sh.n_experts), s, tmA, tmB, p);
+                         C::smem_bytes(sh.n_experts), s, tmA, tmB, tmOut, p);
 }
 
 template <Product MODE, int BN>
@@ -594,6 +656,7 @@ cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product1
     p.pre = g.pre;
     p.wide_out = rows16(g.out, p.cols) && (!g.pre || rows16(g.pre, p.cols));
     p.wide_res = g.residual && rows16(g.residual, g.ldr);
+    p.bulk = mode == Product::kWeights && rows16(g.out, p.cols);
     p.status = status;
     p.clear = clear;
     // test-only fault injection (no trap, no fault), as in the assignment: every
