@@ -23,12 +23,12 @@ __global__ void linear_align_kernel(const T *src, int64_t lds, int64_t rows, int
 }
 
 // dz = dy act'(pre), rounded to the matrices' type, and the bias gradient's
-// partial sums from the same read.  A block takes 128 rows of one expert by 256
-// columns: a lane 8 columns (16 bytes where the rows allow), a warp every
+// partial sums from the same read.  A block takes up to 128 rows of one expert
+// by 256 columns: a lane 8 columns (16 bytes where the rows allow), a warp every
 // eighth row.  Its column sums of the unrounded values go to one row of
 // `partial` per row tile; linear_bias_join_kernel adds an expert's in order, so
 // the result does not depend on the schedule.
-constexpr int kSlopeRows = 128;
+constexpr int kSlopeMaxRows = 128, kSlopeMinRows = 16;
 constexpr int kSlopeCols = 256;
 constexpr int kSlopeThreads = 256;
 
@@ -39,7 +39,7 @@ struct RowTile {
     int64_t r0, r1;
 };
 
-__device__ bool find_row_tile(const int32_t *offsets, int n_experts, int64_t m, int u, RowTile &t) {
+__device__ bool find_row_tile(const int32_t *offsets, int n_experts, int64_t m, int rows, int u, RowTile &t) {
     const int lane = threadIdx.x & 31;
     int last = 0, count = 0;
     for (int e0 = 0; e0 < n_experts; e0 += 32) {
@@ -51,7 +51,7 @@ __device__ bool find_row_tile(const int32_t *offsets, int n_experts, int64_t m, 
         end = max(end, last);
         int start = __shfl_up_sync(0xffffffffu, end, 1);
         if (lane == 0) start = last;
-        const int own = (end - start + kSlopeRows - 1) / kSlopeRows;
+        const int own = (int)(((int64_t)end - start + rows - 1) / rows);
         int upto = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -64,8 +64,8 @@ __device__ bool find_row_tile(const int32_t *offsets, int n_experts, int64_t m, 
             const int who = __ffs(past) - 1;
             t.expert = e0 + who;
             t.before = __shfl_sync(0xffffffffu, upto - own, who);
-            t.r0 = __shfl_sync(0xffffffffu, start, who) + (int64_t)(u - t.before) * kSlopeRows;
-            t.r1 = min(t.r0 + kSlopeRows, (int64_t)__shfl_sync(0xffffffffu, end, who));
+            t.r0 = __shfl_sync(0xffffffffu, start, who) + (int64_t)(u - t.before) * rows;
+            t.r1 = min(t.r0 + rows, (int64_t)__shfl_sync(0xffffffffu, end, who));
             return true;
         }
         last = __shfl_sync(0xffffffffu, end, 31);
@@ -90,8 +90,8 @@ template <bool WIDE, typename T>
 __global__ void __launch_bounds__(kSlopeThreads, 2) linear_slope_kernel(const T *__restrict__ dy, int64_t lddy,
                                                                         const T *__restrict__ pre,
                                                                         const int32_t *__restrict__ offsets,
-                                                                        int n_experts, int64_t m, int64_t n, int act,
-                                                                        T *__restrict__ dz, int64_t ldz,
+                                                                        int n_experts, int64_t m, int64_t n, int rows,
+                                                                        int act, T *__restrict__ dz, int64_t ldz,
                                                                         float *__restrict__ partial, uint32_t *clear) {
     __shared__ float sums[kSlopeThreads / 32][kSlopeCols];
     griddep_wait();
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kSlopeThreads, 2) linear_slope_kernel(const T 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int WARPS = kSlopeThreads / 32;
     RowTile t;
-    if (!find_row_tile(offsets, n_experts, m, blockIdx.y, t)) return;
+    if (!find_row_tile(offsets, n_experts, m, rows, blockIdx.y, t)) return;
     const int64_t c0 = (int64_t)blockIdx.x * kSlopeCols + lane * 8;
     const int left = (int)min((int64_t)8, n - c0);
     float sum[8] = {};
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kSlopeThreads, 2) linear_slope_kernel(const T 
 
 template <typename T>
 __global__ void __launch_bounds__(kSlopeThreads) linear_bias_join_kernel(const float *partial, const int32_t *offsets,
-                                                                         int64_t m, int64_t n, T *db) {
+                                                                         int64_t m, int64_t n, int rows, T *db) {
     __shared__ int range[2];
     griddep_wait();
     const int expert = blockIdx.y;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kSlopeThreads) linear_bias_join_kernel(const f
         // the tiles before this expert's first and its own
         int first = 0, last = 0;
         if (!offsets) {
-            last = (int)((m + kSlopeRows - 1) / kSlopeRows);
+            last = (int)((m + rows - 1) / rows);
         } else {
             const int lane = threadIdx.x;
             int top = 0, sum = 0;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kSlopeThreads) linear_bias_join_kernel(const f
                 end = max(end, top);
                 int start = __shfl_up_sync(0xffffffffu, end, 1);
                 if (lane == 0) start = top;
-                const int own = (end - start + kSlopeRows - 1) / kSlopeRows;
+                const int own = (int)(((int64_t)end - start + rows - 1) / rows);
                 const int before = e < expert ? own : 0;
                 sum += __reduce_add_sync(0xffffffffu, before);
                 if (expert - e0 < 32) last = __shfl_sync(0xffffffffu, own, expert - e0);
@@ -204,8 +204,19 @@ __global__ void __launch_bounds__(kSlopeThreads) linear_bias_join_kernel(const f
     db[(int64_t)expert * n + col] = narrow<T>(s);
 }
 
+// Rows of a block: fewer where that gives every SM a block or two (257 rows of
+// 1000 columns: 16 blocks of 128 rows, or 68 of 16).
+int slope_rows(int64_t m, int64_t n) {
+    int rows = kSlopeMaxRows;
+    while (rows > kSlopeMinRows && (m + rows - 1) / rows * ((n + kSlopeCols - 1) / kSlopeCols) < 2 * 152) rows /= 2;
+    return rows;
+}
+
 // Most row tiles that m rows of so many experts make.
-int64_t slope_tiles(int64_t m, int64_t n_experts) { return (m + kSlopeRows - 1) / kSlopeRows + n_experts; }
+int64_t slope_tiles(int64_t m, int64_t n, int64_t n_experts) {
+    const int rows = slope_rows(m, n);
+    return (m + rows - 1) / rows + n_experts;
+}
 
 // One call's kernels on the stream: the first of them clears the status word.
 template <typename T>
@@ -271,17 +282,18 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
             g.b = dz;
             g.ldb = ldz;
         }
-        const dim3 grid((unsigned)((sh.n + kSlopeCols - 1) / kSlopeCols), (unsigned)slope_tiles(sh.m, sh.offsets ? sh.n_experts : 0));
+        const dim3 grid((unsigned)((sh.n + kSlopeCols - 1) / kSlopeCols), (unsigned)slope_tiles(sh.m, sh.n, sh.offsets ? sh.n_experts : 0));
         const bool wide = sh.n % 8 == 0 && rows16(dy, lddy) && (activation == KMEANS_ACT_NONE || rows16(pre, sh.n));
         float *partial = db ? reinterpret_cast<float *>(ws + L.off_partial) : nullptr;
         e = launch_kernel(true, wide ? linear_slope_kernel<true, T> : linear_slope_kernel<false, T>, grid,
                           dim3(kSlopeThreads), 0, s, static_cast<const T *>(dy), lddy, static_cast<const T *>(pre),
-                          sh.offsets, sh.n_experts, sh.m, sh.n, activation, dz, ldz, partial, call.first());
+                          sh.offsets, sh.n_experts, sh.m, sh.n, slope_rows(sh.m, sh.n), activation, dz, ldz, partial,
+                          call.first());
         if (e == cudaSuccess && db)
             e = launch_kernel(true, linear_bias_join_kernel<T>,
                               dim3((unsigned)((sh.n + kSlopeThreads - 1) / kSlopeThreads), (unsigned)sh.n_experts),
                               dim3(kSlopeThreads), 0, s, static_cast<const float *>(partial), sh.offsets, sh.m, sh.n,
-                              static_cast<T *>(db));
+                              slope_rows(sh.m, sh.n), static_cast<T *>(db));
     }
     if (e == cudaSuccess && db && sh.m == 0)
         e = cudaMemsetAsync(db, 0, (size_t)sh.n_experts * (size_t)sh.n * sizeof(T), s);
@@ -319,7 +331,7 @@ LinearLayout linear_layout(bool grad, int64_t m, int64_t n, int64_t k, int64_t n
         L.off_dz = o;
         o = align_up(o + m * align_up(n, 8) * 2, 1024);
         L.off_partial = o;
-        o = align_up(o + slope_tiles(m, n_experts) * n * 4, 1024);
+        o = align_up(o + slope_tiles(m, n, n_experts) * n * 4, 1024);
     }
     L.bytes = o;
     return L;

@@ -73,7 +73,7 @@ struct Cfg {
     static constexpr int A_BYTES = BP_CTA * BK * 2;
     static constexpr int B_BYTES = BN / 2 * BK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = STORES ? 5 : BN >= 256 ? 6 : BN >= 128 ? 8 : 9;
+    static constexpr int STAGES = STORES ? (BN >= 256 ? 5 : 6) : BN >= 256 ? 6 : BN >= 128 ? 8 : 9;
     static constexpr int STAGING_BASE = STAGES * STAGE;
     static constexpr int BAR_BASE = STAGING_BASE + (STORES ? PARTS * 2 * STORE_BYTES : STAGING);
     static constexpr int LIST_BASE = BAR_BASE + BAR_BYTES;
@@ -663,18 +663,30 @@ cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product1
     // consumer's bounded wait runs out and the status word reports the timeout
     const char *starve = getenv("KMEANS_GB300_TEST_STARVE_PIPELINE");
     p.test_starve = (starve != nullptr && starve[0] == '1') ? 1 : 0;
-    if (mode == Product::kWeights) return launch_typed<Product::kWeights, 256>(sh, g, p, s);
-    // rows per unit: about an expert's average rows, so that small groups do
-    // not load and multiply rows of their neighbours
+    // Rows per unit.  As many as 256 for the fewest bytes per MMA (a stage of
+    // 256 x 256 x 64 just fills shared memory's bandwidth); about an expert's
+    // average rows where there are fewer, so that small groups do not load
+    // their neighbours' rows; and no more than needed to keep everything in one
+    // round of the CTA pairs: the smaller the unit then, the sooner it is done
+    // (gradient of 257 rows, 1000 x 520: XXX).
+    const int64_t pairs = device_sm_count() / 2;
+    auto one_round = [&](int64_t bn) {
+        const int64_t tiles = mode == Product::kWeights ? (sh.n + bn - 1) / bn * sh.n_experts
+                                                        : (sh.m + bn - 1) / bn + (sh.offsets ? sh.n_experts : 0);
+        return tiles * p.num_p <= pairs;
+    };
+    if (mode == Product::kWeights)
+        return one_round(128) ? launch_typed<Product::kWeights, 128>(sh, g, p, s)
+                              : launch_typed<Product::kWeights, 256>(sh, g, p, s);
     const int64_t rows = sh.m / sh.n_experts;
-    if (mode == Product::kForward) {
-        if (rows > 128) return launch_typed<Product::kForward, 256>(sh, g, p, s);
-        if (rows > 64) return launch_typed<Product::kForward, 128>(sh, g, p, s);
-        return launch_typed<Product::kForward, 64>(sh, g, p, s);
-    }
-    if (rows > 128) return launch_typed<Product::kRows, 256>(sh, g, p, s);
-    if (rows > 64) return launch_typed<Product::kRows, 128>(sh, g, p, s);
-    return launch_typed<Product::kRows, 64>(sh, g, p, s);
+    const int bn = rows <= 64 || one_round(64) ? 64 : rows <= 128 || one_round(128) ? 128 : 256;
+    if (mode == Product::kForward)
+        return bn == 256   ? launch_typed<Product::kForward, 256>(sh, g, p, s)
+               : bn == 128 ? launch_typed<Product::kForward, 128>(sh, g, p, s)
+                           : launch_typed<Product::kForward, 64>(sh, g, p, s);
+    return bn == 256   ? launch_typed<Product::kRows, 256>(sh, g, p, s)
+           : bn == 128 ? launch_typed<Product::kRows, 128>(sh, g, p, s)
+                       : launch_typed<Product::kRows, 64>(sh, g, p, s);
 }
 
 }  // namespace km

@@ -34,7 +34,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 // ------------------------------------------------------------------ the sort
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteSmemMax = 224 * 1024;
-constexpr int kRouteMaxCluster = 8;
+constexpr int kRouteMaxCluster = 16;
 constexpr int kRouteSlotsPerBlock = 4096;  // below this many slots another block does not pay its exchange
 
 struct RouteParams {
@@ -68,11 +68,25 @@ __device__ __forceinline__ void route_keys(const Id *experts, uint32_t s, uint32
     }
 }
 
+// Lanes of the warp whose key equals this lane's, by its bits: one vote per bit
+// is far cheaper than a match instruction, which takes the warp's distinct keys
+// one after the other (65536 slots over 1024 experts spent 19 of 38 thousand
+// cycles in eight of them per warp).
+__device__ __forceinline__ uint32_t same_key(int key, bool live, int bits) {
+    uint32_t same = __ballot_sync(kFull, live);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (key >> b) & 1;
+        const uint32_t ones = __ballot_sync(kFull, one);
+        same &= one ? ones : ~ones;
+    }
+    return same;
+}
+
 // Shared memory: hist[warps][keys], tot[keys], base[keys], 32 words of scan
 // scratch, with keys = n_experts + 1.
 template <typename Id>
 __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams p) {
-    extern __shared__ int route_smem[];
+    extern __shared__ __align__(16) int route_smem[];
     const int keys = p.n_experts + 1;
     int *hist = route_smem;
     int *tot = hist + p.warps * keys;
@@ -86,9 +100,6 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
 
     griddep_wait();
     if (rank == 0 && tid == 0) *p.status = 0u;
-    for (int i = tid; i < p.warps * keys; i += blockDim.x) hist[i] = 0;
-    __syncthreads();
-
     // this warp's run of consecutive slots, whole groups of 32
     const int total_warps = blocks * p.warps;
     const int groups = (int)(((uint32_t)p.slots + 31u) / 32u);
@@ -100,8 +111,17 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
 
     bool bad = false;
     int key[kRouteBatch];
+    if (s0 < s1) route_keys(experts, s0 + lane, s1, p.n_experts, bad, key);
+    for (int i = tid * 4; i < p.warps * keys; i += blockDim.x * 4) {
+        if (i + 4 <= p.warps * keys) {
+            *reinterpret_cast<int4 *>(hist + i) = make_int4(0, 0, 0, 0);
+        } else {
+            for (int k = i; k < p.warps * keys; ++k) hist[k] = 0;
+        }
+    }
+    __syncthreads();
     for (uint32_t s = s0; s < s1; s += 32 * kRouteBatch) {
-        route_keys(experts, s + lane, s1, p.n_experts, bad, key);
+        if (s != s0) route_keys(experts, s + lane, s1, p.n_experts, bad, key);
 #pragma unroll
         for (int b = 0; b < kRouteBatch; ++b)
             if (key[b] >= 0) atomicAdd(mine + key[b], 1);
@@ -110,28 +130,46 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
     // per key: each warp's first place among this block's, and the block's total
     for (int e = tid; e < keys; e += blockDim.x) {
         int sum = 0;
-        for (int w = 0; w < p.warps; ++w) {
-            const int c = hist[w * keys + e];
-            hist[w * keys + e] = sum;
-            sum += c;
+        for (int w0 = 0; w0 < p.warps; w0 += 8) {
+            int c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = w0 + i < p.warps ? hist[(w0 + i) * keys + e] : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (w0 + i < p.warps) hist[(w0 + i) * keys + e] = sum;
+                sum += c[i];
+            }
         }
         tot[e] = sum;
     }
     cluster_sync();  // every block's totals are readable; the status word is cleared
     if (__syncthreads_or(bad) && tid == 0) flag_error(p.status, kFlagBadLabel);
 
-    // base[e] = all slots of smaller keys + the lower blocks' slots of key e
-    int run = 0;  // keys are scanned blockDim.x at a time
-    for (int e0 = 0; e0 < keys; e0 += blockDim.x) {
-        const int e = e0 + tid;
-        int all = 0, lower = 0;
-        if (e < keys)
-            for (int r = 0; r < blocks; ++r) {
-                const int c = blocks == 1 ? tot[e] : ld_cluster_i32(tot + e, (uint32_t)r);
-                all += c;
-                if (r < (int)rank) lower += c;
+    // base[e] = all slots of smaller keys + the lower blocks' slots of key e;
+    // a thread has two neighbouring keys, so that 1024 experts and their
+    // dropped slots are one round
+    int run = 0;
+    for (int e0 = 0; e0 < keys; e0 += 2 * blockDim.x) {
+        const int e = e0 + 2 * tid;
+        int all[2] = {}, lower[2] = {};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (e + i >= keys) continue;
+            if (blocks == 1) {
+                all[i] = tot[e + i];
+                continue;
             }
-        int inc = all;
+            int c[kRouteMaxCluster];
+#pragma unroll
+            for (int r = 0; r < kRouteMaxCluster; ++r) c[r] = r < blocks ? ld_cluster_i32(tot + e + i, (uint32_t)r) : 0;
+#pragma unroll
+            for (int r = 0; r < kRouteMaxCluster; ++r) {
+                all[i] += c[r];
+                if (r < (int)rank) lower[i] += c[r];
+            }
+        }
+        const int own = all[0] + all[1];
+        int inc = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(kFull, inc, o);
@@ -139,28 +177,30 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
         }
         if (lane == 31) scan[warp] = inc;
         __syncthreads();
-        int before = 0, chunk = 0;
-        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-            const int v = scan[w];
-            if (w < warp) before += v;
-            chunk += v;
-        }
-        if (e < keys) {
-            const int first = run + before + inc - all;
-            base[e] = first + lower;
-            if (rank == 0) p.offsets[e] = first;  // offsets[n_experts]: the kept slots
-        }
+        // each warp adds up the others' sums by itself
+        const int warps = (int)(blockDim.x >> 5);
+        const int sums = lane < warps ? scan[lane] : 0;
+        const int before = __reduce_add_sync(kFull, lane < warp ? sums : 0), chunk = __reduce_add_sync(kFull, sums);
+        int first = run + before + inc - own;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (e + i < keys) {
+                base[e + i] = first + lower[i];
+                if (rank == 0) p.offsets[e + i] = first;  // offsets[n_experts]: the kept slots
+                first += all[i];
+            }
         run += chunk;
         __syncthreads();
     }
     // hand out rows (one batch's keys are still in registers)
+    const int bits = 32 - __clz(p.n_experts);
     for (uint32_t s = s0; s < s1; s += 32 * kRouteBatch) {
         if (s1 - s0 > 32 * kRouteBatch) route_keys(experts, s + lane, s1, p.n_experts, bad, key);
 #pragma unroll
         for (int b = 0; b < kRouteBatch; ++b) {
             if (s + 32u * b >= s1) break;  // the same for the whole warp
             const bool live = key[b] >= 0;
-            const uint32_t same = __match_any_sync(kFull, key[b]);
+            const uint32_t same = same_key(key[b], live, bits);
             int row = 0;
             if (live) row = base[key[b]] + mine[key[b]] + __popc(same & below);
             __syncwarp();
@@ -522,18 +562,39 @@ cudaError_t combine_grad_typed(MoveParams p, const void *dy, int64_t lddy, const
                          span(ys, p.slots, p.row_bytes, p.row_bytes), weights, static_cast<uint8_t *>(dys), dweights);
 }
 
+// Most blocks of one cluster: 16 where the device can hold such a cluster (it
+// needs that many free SMs next to each other), else the portable 8.
+template <typename Id>
+int route_max_cluster() {
+    static std::atomic<int> cached[kMaxDevices];
+    return cached_per_device(cached, [] {
+        if (cudaFuncSetAttribute(route_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmemMax) !=
+                cudaSuccess ||
+            cudaFuncSetAttribute(route_kernel<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+            cudaGetLastError();  // clear; the launch reports what is wrong
+            return 8;
+        }
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(kRouteMaxCluster);
+        cfg.blockDim = dim3(kRouteThreads);
+        cfg.dynamicSmemBytes = kRouteSmemMax;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = kRouteMaxCluster;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, route_kernel<Id>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            clusters = 0;
+        }
+        return clusters > 0 ? kRouteMaxCluster : 8;
+    });
+}
+
 template <typename Id>
 cudaError_t route_as(const RouteParams &p, int blocks, int threads, size_t smem, cudaStream_t s) {
-    static std::once_flag once[kMaxDevices];
-    static std::atomic<int> err[kMaxDevices];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const int slot = dev >= 0 && dev < kMaxDevices ? dev : 0;
-    once_per_device(once, [&] {
-        err[slot].store((int)cudaFuncSetAttribute(route_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  kRouteSmemMax));
-    });
-    if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3((unsigned)threads);
@@ -564,8 +625,9 @@ cudaError_t launch_route(const void *experts, int id_bytes, int64_t slots, int n
     p.status = status;
     const int keys = n_experts + 1;
     const int room = (kRouteSmemMax - 2 * keys * 4 - 128) / (keys * 4);
+    const int most = id_bytes == 8 ? route_max_cluster<int64_t>() : route_max_cluster<int32_t>();
     int blocks = 1;
-    while (blocks < kRouteMaxCluster && (int64_t)blocks * kRouteSlotsPerBlock < slots) blocks *= 2;
+    while (blocks < most && (int64_t)blocks * kRouteSlotsPerBlock < slots) blocks *= 2;
     // no more counting warps than groups of 32 slots: their counts are cleared
     // and added up key by key
     const int64_t groups = (slots + 31) / 32, per_block = (groups + blocks - 1) / blocks;
