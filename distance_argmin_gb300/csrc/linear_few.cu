@@ -1,24 +1,32 @@
 // The forward product for few rows per expert: y = act(x W_e^T + b_e) + res
 // where reading W is all that takes time.
 //
-// A block takes 16 features of one expert and up to 8 NT of its rows.  Its 8
+// A unit is 16 features of one expert and up to 8 of its rows.  A block's 8
 // warps share the contraction, 128 values (256 bytes of each feature) at a
-// time: a lane loads 16 bytes of two features and of each row, which are
-// operands of mma.m16n8k16 as they stand, because the order of the contraction
-// inside an instruction is free as long as both operands use the same (words 0
-// and 1 of the lane's four make one instruction, words 2 and 3 the next).  W
-// goes from memory to registers to the tensor cores, nothing is staged; a
-// block has 16 features of 128 x 8 values (32 KB) in flight at once.  The legacy MMA is enough here: one instruction per 32
-// bytes of W loaded, far below its rate.  The warps' sums meet in shared
-// memory, where bias, activation, residual and the rounding are applied.
+// time: a lane loads 16 bytes of two features and of one row, which are operands
+// of mma.m16n8k16 as they stand, because the order of the contraction inside an
+// instruction is free as long as both operands use the same (words 0 and 1 of
+// the lane's four make one instruction, words 2 and 3 the next).  The legacy
+// MMA is enough here: one instruction per 512 bytes of W, far below its rate.
 //
-// Rows that do not start on 16 bytes are read as shifted words (pieces.cuh), so
-// W is never copied first.
+// W goes from memory to registers to the tensor cores, nothing is staged; what
+// bounds it is how many bytes are on their way, 32 KB a block and four blocks
+// an SM.  (A ring of cp.async slots per lane, filled across the ends of units,
+// measured the same: 24 rows over 20 experts of 4096 x 2048 56 us against
+// 55, 6.1 TB/s.)  Where there are few units for the SMs, a cluster of blocks splits each
+// one's contraction, and the sums are joined through distributed shared memory
+// (2048 features of 8192: 14.0 us without, 8.7 with).
+//
+// Rows that do not start on 16 bytes are read as shifted words (pieces.cuh)
+// into registers, so W is never copied first.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "assign_common.cuh"
 #include "linear_common.cuh"
+#include "ptx.cuh"
 
 namespace km {
 
@@ -26,9 +34,11 @@ namespace {
 
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
-constexpr int kFewFeatures = 16;
+constexpr int kFewFeatures = 16, kFewRows = 8;  // of one instruction
 constexpr int kFewStep = 128;  // contraction of a warp's step
 constexpr int kFewPieces = kFewStep / 32;
+constexpr int kFewBlocks = 4;  // per SM
+static_assert(kFewRows * kFewFeatures == kFewThreads / 2, "half of the threads finish a unit");
 
 struct FewParams {
     const int32_t *offsets;
@@ -41,6 +51,7 @@ struct FewParams {
     int64_t ldr;
     int activation;
     void *y, *pre;
+    int split;  // blocks of a cluster that share a unit's contraction
     uint32_t *status;
 };
 
@@ -66,102 +77,166 @@ __device__ __forceinline__ void mma_16816<__nv_bfloat16>(float (&c)[4], uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <bool WHOLE, int NT, typename T>
-__global__ void __launch_bounds__(kFewThreads, WHOLE && NT == 1 ? 4 : 2) linear_few_kernel(const FewParams p) {
-    constexpr int ROWS = 8 * NT;
+__device__ __forceinline__ float ld_cluster_f32(const float *p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_cta(smem_addr(p), rank)) : "memory");
+    return v;
+}
+
+// The units in order: an expert's row tiles one after the other on the same
+// features.
+struct FewUnit {
+    int e, f0, r0, rows;
+};
+
+__device__ __forceinline__ FewUnit few_unit(const FewParams &p, const int *edges, const int *tiles, int u, int &e) {
+    while (u >= tiles[e + 1] * p.num_p) ++e;
+    const int local = u - tiles[e] * p.num_p, per = tiles[e + 1] - tiles[e];
+    const int feature = per == 1 ? local : local / per;
+    FewUnit t;
+    t.e = e;
+    t.f0 = feature * kFewFeatures;
+    t.r0 = edges[e] + (local - feature * per) * kFewRows;
+    t.rows = min(kFewRows, edges[e + 1] - t.r0);
+    return t;
+}
+
+template <bool WHOLE, typename T>
+__global__ void __launch_bounds__(kFewThreads, WHOLE ? kFewBlocks : 2) linear_few_kernel(const FewParams p) {
     extern __shared__ int few_smem[];
-    __shared__ float part[kFewWarps][kFewFeatures][ROWS + 1];
+    __shared__ float part[2][kFewWarps][kFewFeatures][kFewRows + 1];
+    __shared__ float sums[2][kFewRows * kFewFeatures];  // of this block, for the cluster's first
     int *edges = few_smem, *tiles = edges + p.n_experts + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int split = p.split, crank = split > 1 ? (int)cluster_ctarank() : 0;
     griddep_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
-    if (warp == 0) fill_tables<ROWS>(p.offsets, p.n_experts, p.m, edges, tiles, lane);
+    if (warp == 0) fill_tables<kFewRows>(p.offsets, p.n_experts, p.m, edges, tiles, lane);
     __syncthreads();
-    const int64_t total = (int64_t)tiles[p.n_experts + 1] * p.num_p;
-    int e = 0;
-    for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
-        while (u >= (int64_t)tiles[e + 1] * p.num_p) ++e;
-        // an expert's row tiles one after the other on the same features
-        const int64_t local = u - (int64_t)tiles[e] * p.num_p;
-        const int per = tiles[e + 1] - tiles[e];
-        const int f0 = (int)(local / per) * kFewFeatures;
-        const int64_t r0 = edges[e] + (local % per) * ROWS;
-        const int rows = (int)min((int64_t)ROWS, edges[e + 1] - r0);
-        const bool real = e < p.n_experts;
-        float acc[NT][4] = {};
+    const int total = tiles[p.n_experts + 1] * p.num_p;  // below 2^31: each is 16 rows of a matrix in memory
+    const int first = blockIdx.x / split, stride = gridDim.x / split;
+    const int kwarp = (crank * kFewWarps + warp) * kFewStep, kstride = split * kFewWarps * kFewStep;
+
+    int e = 0, parity = 0;
+    for (int u = first; u < total; u += stride, parity ^= 1) {
+        const FewUnit t = few_unit(p, edges, tiles, u, e);
+        const bool real = t.e < p.n_experts;
+        float acc[4] = {};
         if (real) {
-            const int64_t wrow = (int64_t)e * p.n + f0 + g;
-            const uint8_t *w0 = p.w + wrow * p.k * 2, *w1 = w0 + (int64_t)8 * p.k * 2;
-            const bool on0 = f0 + g < p.n, on1 = f0 + g + 8 < p.n;
+            const uint8_t *w0 = p.w + ((int64_t)t.e * p.n + t.f0 + g) * p.k * 2, *w1 = w0 + (int64_t)8 * p.k * 2;
+            const bool on0 = t.f0 + g < p.n, on1 = t.f0 + g + 8 < p.n;
             const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-            for (int k0 = warp * kFewStep; k0 < p.k; k0 += kFewWarps * kFewStep) {
-                uint4 a[kFewPieces][2], b[kFewPieces][NT];
+            for (int k0 = kwarp; k0 < p.k; k0 += kstride) {
+                uint4 a[kFewPieces][2], b[kFewPieces];
 #pragma unroll
                 for (int i = 0; i < kFewPieces; ++i) {
                     const int k = k0 + 32 * i + t4 * 8, bytes = min(16, (p.k - k) * 2);
                     a[i][0] = on0 && bytes > 0 ? load_piece<WHOLE>(w0 + (int64_t)k * 2, bytes, p.w_in) : zero;
                     a[i][1] = on1 && bytes > 0 ? load_piece<WHOLE>(w1 + (int64_t)k * 2, bytes, p.w_in) : zero;
-#pragma unroll
-                    for (int q = 0; q < NT; ++q)
-                        b[i][q] = 8 * q + g < rows && bytes > 0
-                                      ? load_piece<WHOLE>(p.x + ((r0 + 8 * q + g) * p.ldx + k) * 2, bytes, p.x_in)
-                                      : zero;
+                    b[i] = g < t.rows && bytes > 0
+                               ? load_piece<WHOLE>(p.x + (((int64_t)t.r0 + g) * p.ldx + k) * 2, bytes, p.x_in)
+                               : zero;
                 }
 #pragma unroll
-                for (int i = 0; i < kFewPieces; ++i)
-#pragma unroll
-                    for (int q = 0; q < NT; ++q) {
-                        mma_16816<T>(acc[q], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, b[i][q].x, b[i][q].y);
-                        mma_16816<T>(acc[q], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, b[i][q].z, b[i][q].w);
-                    }
+                for (int i = 0; i < kFewPieces; ++i) {
+                    mma_16816<T>(acc, a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, b[i].x, b[i].y);
+                    mma_16816<T>(acc, a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, b[i].z, b[i].w);
+                }
             }
         }
-        __syncthreads();  // the previous unit's sums have been read
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-            part[warp][g][8 * q + 2 * t4] = acc[q][0];
-            part[warp][g][8 * q + 2 * t4 + 1] = acc[q][1];
-            part[warp][g + 8][8 * q + 2 * t4] = acc[q][2];
-            part[warp][g + 8][8 * q + 2 * t4 + 1] = acc[q][3];
-        }
+        // The two copies of `part` alternate, and so do the half of the warps
+        // that finishes a unit and the half that goes on with the next.
+        part[parity][warp][g][2 * t4] = acc[0];
+        part[parity][warp][g][2 * t4 + 1] = acc[1];
+        part[parity][warp][g + 8][2 * t4] = acc[2];
+        part[parity][warp][g + 8][2 * t4 + 1] = acc[3];
         __syncthreads();
-        for (int i = threadIdx.x; i < kFewFeatures * rows; i += kFewThreads) {
-            const int f = i % kFewFeatures, r = i / kFewFeatures;
-            if (f0 + f >= p.n) continue;
-            float z = 0.f;
+        const int at_work = (int)threadIdx.x - parity * (kFewThreads / 2);
+        const bool finishing = at_work >= 0 && at_work < kFewThreads / 2;
+        if (split == 1 && !finishing) continue;
+        const int f = at_work % kFewFeatures, r = at_work / kFewFeatures;
+        const bool mine = finishing && r < t.rows && t.f0 + f < p.n;
+        float z = 0.f, bias = 0.f;
+        if (mine && crank == 0 && real && p.bias) bias = widen(static_cast<const T *>(p.bias)[(int64_t)t.e * p.n + t.f0 + f]);
+        if (finishing) {
 #pragma unroll
-            for (int w = 0; w < kFewWarps; ++w) z += part[w][f][r];
-            const int64_t at = (r0 + r) * p.n + f0 + f;
-            if (real && p.bias) z += widen(static_cast<const T *>(p.bias)[(int64_t)e * p.n + f0 + f]);
+            for (int w = 0; w < kFewWarps; ++w) z += part[parity][w][f][r];
+        }
+        if (split > 1) {
+            // the two halves of `sums` alternate: a unit's are read before the
+            // next unit's barrier, and written again after it
+            if (finishing) sums[parity][at_work] = z;
+            cluster_sync();
+            if (crank != 0 || !finishing) continue;
+            z = 0.f;
+            for (int c = 0; c < split; ++c) z += ld_cluster_f32(&sums[parity][at_work], (uint32_t)c);
+        }
+        if (mine) {
+            const int64_t row = (int64_t)t.r0 + r, at = row * p.n + t.f0 + f;
+            z += bias;
             if (p.pre) static_cast<T *>(p.pre)[at] = narrow<T>(z);
             float v = z;
             with_activation(p.activation, [&](auto a) { v = activate<decltype(a)::value>(z); });
-            if (real && p.residual) v += widen(static_cast<const T *>(p.residual)[(r0 + r) * p.ldr + f0 + f]);
+            if (real && p.residual) v += widen(static_cast<const T *>(p.residual)[row * p.ldr + t.f0 + f]);
             static_cast<T *>(p.y)[at] = narrow<T>(v);
         }
     }
+    if (split > 1) cluster_sync();  // no block leaves while its sums may still be read
 }
 
-template <int NT, typename T>
-cudaError_t launch_few(const LinearShape &sh, const FewParams &p, bool whole, cudaStream_t s) {
-    const int64_t tiles = (sh.m + 8 * NT - 1) / (8 * NT) + (sh.offsets ? sh.n_experts : 0);
-    const int64_t units = tiles * p.num_p, most = (int64_t)device_sm_count() * 4;
+template <bool WHOLE, typename T>
+cudaError_t launch_few(const LinearShape &sh, FewParams p, cudaStream_t s) {
     const size_t smem = 2 * (size_t)(sh.n_experts + 2) * 4;
-    return launch_kernel(true, whole ? linear_few_kernel<true, NT, T> : linear_few_kernel<false, NT, T>,
-                         dim3((unsigned)(units < most ? units : most)), dim3(kFewThreads), smem, s, p);
+    // blocks that run at once
+    const int64_t blocks = device_sm_count() * (int64_t)(WHOLE ? kFewBlocks : 2);
+    // row tiles: at most, and about as many as rows that choose freely make
+    const double n_e = (double)sh.n_experts, m = (double)sh.m;
+    const int64_t most = sh.offsets ? (sh.m < sh.n_experts ? sh.m : sh.n_experts) + sh.m / kFewRows + 1 : 1;
+    const double about = sh.offsets ? n_e * (1.0 - std::pow(1.0 - 1.0 / n_e, m)) + m / (2 * kFewRows * n_e) : 1.0;
+    const int64_t units = (int64_t)(about * p.num_p + 0.5);
+    // Split the contraction where that is sooner done: a block takes in some 11
+    // bytes of W a nanosecond, a unit costs it 0.3 us besides and, split, 1.7 us
+    // more for the cluster to meet.
+    p.split = 1;
+    double best = 0;
+    for (int c = 1; c <= 8; c *= 2) {
+        if (c > 1 && sh.k < (int64_t)c * kFewWarps * kFewStep) break;
+        const int64_t clusters = blocks / c;
+        const double each = (double)(kFewFeatures * 2 * sh.k) / c / 11.0 + (c > 1 ? 2000.0 : 300.0);
+        const double cost = (double)((units + clusters - 1) / clusters) * each;
+        if (c == 1 || cost < best) {
+            best = cost;
+            p.split = c;
+        }
+    }
+    const int64_t clusters = blocks / p.split;
+    const unsigned grid = (unsigned)((most * p.num_p < clusters ? most * p.num_p : clusters) * p.split);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2u : 1u;
+    return cudaLaunchKernelEx(&cfg, linear_few_kernel<WHOLE, T>, p);
 }
 
 }  // namespace
 
-// Where W is read once and little is done with it.  One expert: up to 16 rows,
-// two tiles of one instruction's 8 (n = 8192, k = 2048: 1 or 8 rows 8.1 us, 16
-// rows 11.2, where the tensor-core units take 15.3 us for any number up to 64).
-// Several experts: their rows are not known here, so few of them on average; an
-// expert with more reads its part of W again (from L2) every 8 rows (64
-// experts, n = 4096, k = 2048: 128 rows 159 us, 6.3 TB/s; 256 rows 207 us in
-// tiles of 16, and 1024 rows 167 us in the tensor-core units).
-bool few_rows(const LinearShape &sh) { return sh.offsets ? sh.m <= 2 * (int64_t)sh.n_experts : sh.m <= 16; }
+// Where W is read once and little is done with it.  One expert: up to 8 rows
+// (n = 8192, k = 2048: 8.1 us; the tensor-core units take 10.9 us for any
+// number up to 24, 16 rows in two tiles of this kernel 11.2).  Several experts:
+// their rows are not known here, so few of them on average; an expert with more
+// reads its part of W again (from L2) every 8 rows (64 experts, n = 4096, k =
+// 2048: 128 rows 159 us, 6.3 TB/s; 1024 rows 167 us in the tensor-core units).
+bool few_rows(const LinearShape &sh) { return sh.offsets ? sh.m <= 2 * (int64_t)sh.n_experts : sh.m <= kFewRows; }
 
 cudaError_t launch_linear_few(const LinearShape &sh, const Product16 &g, uint32_t *status, cudaStream_t s) {
     FewParams p{};
@@ -184,9 +259,8 @@ cudaError_t launch_linear_few(const LinearShape &sh, const Product16 &g, uint32_
     p.pre = g.pre;
     p.status = status;
     const bool whole = rows16(g.a, sh.k) && rows16(g.b, g.ldb);
-    const bool one = sh.offsets || sh.m <= 8;
-    if (sh.bf16) return one ? launch_few<1, __nv_bfloat16>(sh, p, whole, s) : launch_few<2, __nv_bfloat16>(sh, p, whole, s);
-    return one ? launch_few<1, __half>(sh, p, whole, s) : launch_few<2, __half>(sh, p, whole, s);
+    if (whole) return sh.bf16 ? launch_few<true, __nv_bfloat16>(sh, p, s) : launch_few<true, __half>(sh, p, s);
+    return sh.bf16 ? launch_few<false, __nv_bfloat16>(sh, p, s) : launch_few<false, __half>(sh, p, s);
 }
 
 }  // namespace km

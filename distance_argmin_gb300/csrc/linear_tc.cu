@@ -668,7 +668,9 @@ cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product1
     // average rows where there are fewer, so that small groups do not load
     // their neighbours' rows; and no more than needed to keep everything in one
     // round of the CTA pairs: the smaller the unit then, the sooner it is done
-    // (gradient of 257 rows, 1000 x 520: XXX).
+    // (24 rows through 8192 x 2048 10.9 us, 15.3 in units of 256; the gradient's
+    // two products of 257 rows, 1000 x 520, 12.9 and 10.0 us in units of 256, 9.5
+    // and 8.2 as chosen).
     const int64_t pairs = device_sm_count() / 2;
     auto one_round = [&](int64_t bn) {
         const int64_t tiles = mode == Product::kWeights ? (sh.n + bn - 1) / bn * sh.n_experts

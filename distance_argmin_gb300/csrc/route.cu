@@ -529,6 +529,18 @@ MoveParams move_params(const RouteRows &r, int dtype) {
     return p;
 }
 
+// Threads per row, 1 to 256 as a power of two, for rows of `units` of a
+// thread's work: the count that leaves the fewest threads without any (129
+// pieces take 160 threads by 32, 256 by 256).
+int threads_per_row_log2(int64_t units) {
+    int best = log2_at_least(units, 8);
+    for (int l = best - 1; l >= 5; --l) {
+        const auto used = [&](int k) { return ((units + (1 << k) - 1) >> k) << k; };
+        if (used(l) < used(best)) best = l;
+    }
+    return best;
+}
+
 unsigned row_blocks(const MoveParams &p) {
     const int64_t per = kMoveThreads >> p.tpr_log2;
     return (unsigned)((p.n + per - 1) / per);
@@ -538,7 +550,7 @@ template <typename T>
 cudaError_t combine_typed(MoveParams p, const void *ys, const float *weights, const void *residual, int64_t ldr,
                           void *y, cudaStream_t s) {
     const int64_t pitch = ldr * (int64_t)sizeof(T);
-    p.tpr_log2 = log2_at_least(p.pieces, 8);
+    p.tpr_log2 = threads_per_row_log2(p.pieces);
     const dim3 grid(row_blocks(p), (unsigned)((p.pieces + (1 << p.tpr_log2) - 1) >> p.tpr_log2));
     const bool whole = whole_rows(p.row_bytes, residual ? pitch : 0, {ys, residual, y});
     return launch_kernel(true, whole ? route_combine_kernel<true, T> : route_combine_kernel<false, T>, grid,
@@ -641,7 +653,7 @@ cudaError_t launch_route(const void *experts, int id_bytes, int64_t slots, int n
 cudaError_t launch_route_gather(const RouteRows &r, int dtype, const void *x, int64_t ldx, void *xs, cudaStream_t s) {
     MoveParams p = move_params(r, dtype);
     const int64_t pitch = ldx * elem_bytes(dtype);
-    p.tpr_log2 = log2_at_least((p.pieces + kGatherUnroll - 1) / kGatherUnroll, 8);
+    p.tpr_log2 = threads_per_row_log2((p.pieces + kGatherUnroll - 1) / kGatherUnroll);
     const int per_y = kGatherUnroll << p.tpr_log2;
     const dim3 grid(row_blocks(p), (unsigned)((p.pieces + per_y - 1) / per_y));
     const bool whole = whole_rows(p.row_bytes, pitch, {x, xs});
