@@ -84,10 +84,10 @@ __device__ __forceinline__ uint4 load8(const T *p, int left) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kSlopeBatch = 4;  // rows whose loads are in flight together
+constexpr int kSlopeBatch = 2;  // rows whose loads are in flight together
 
 template <bool WIDE, typename T>
-__global__ void __launch_bounds__(kSlopeThreads, 2) linear_slope_kernel(const T *__restrict__ dy, int64_t lddy,
+__global__ void __launch_bounds__(kSlopeThreads, 4) linear_slope_kernel(const T *__restrict__ dy, int64_t lddy,
                                                                         const T *__restrict__ pre,
                                                                         const int32_t *__restrict__ offsets,
                                                                         int n_experts, int64_t m, int64_t n, int rows,
@@ -125,9 +125,7 @@ __global__ void __launch_bounds__(kSlopeThreads, 2) linear_slope_kernel(const T 
                     for (int c = 0; c < 4; ++c) {
                         float2 v = widen2<T>(gw[c]);
                         if constexpr (ACT != KMEANS_ACT_NONE) {
-                            const float2 y = widen2<T>(zw[c]);
-                            v.x *= slope<ACT>(y.x);
-                            v.y *= slope<ACT>(y.y);
+                            v = __fmul2_rn(v, slope2<ACT>(widen2<T>(zw[c])));
                         }
                         sum[2 * c] += v.x;
                         sum[2 * c + 1] += v.y;

@@ -254,43 +254,52 @@ struct Finish {
     }
 };
 
-// The weights product's output has no ragged rows, so a part (four warps, one
-// per lane quarter) rounds 16 rows of its 128 features into shared memory, in
-// the 128-byte swizzle, and one lane sends them off as two bulk tensor stores
-// that end at the matrix's edges by themselves.  Half the shared-memory traffic
-// of staging in float32 (which the MMAs beside it feel, see Finish) and whole
-// lines to L2.
+// The weights product's output has no ragged rows and is the call's largest
+// traffic, so here a part (four warps, one per lane quarter) rounds 16 rows of
+// its 128 features into shared memory and one lane sends them off as two bulk
+// tensor stores, whole lines that end at the matrix's edges by themselves.  The
+// accumulator is read as MMA fragments, which stmatrix transposes into rows in
+// the 128-byte swizzle.  (64 experts of 4096 x 2048 over 4096 rows, 1.07 GB
+// written: 265 us with Finish, 236 with 2-byte stores into the same buffers,
+// 211 as it stands; the same way out for the row products, whose last rows
+// cannot leave by bulk stores, was no faster than Finish.)
 template <typename T>
 __device__ __forceinline__ void store_part(const LinearTcParams &p, const CUtensorMap *tmOut, uint8_t *buffers, int &ring,
                                            uint32_t acc, int part, int quarter, int lane, int f, int q, int end,
                                            int expert, bool zero) {
-    const uint32_t column = (uint32_t)(quarter & 1) * 4 + (lane >> 3);  // 16-byte chunk of the 128-byte row
+    // stmatrix: lane l addresses row l % 8 of matrix l / 8; the matrices of half
+    // h (16 of the warp's features) are rows 0-7 of features 0-7 and 8-15, then
+    // rows 8-15 of both
+    const int m = lane >> 3, row = (m >> 1) * 8 + (lane & 7);
+    const uint32_t at = (uint32_t)((quarter >> 1) * (lt::STORE_ROWS * 128) + row * 128);
+    const uint32_t chunk = (uint32_t)((quarter & 1) * 4 + (m & 1));
     for (int c = 0; c < end; c += lt::STORE_ROWS) {
         uint32_t r[2][8] = {};
         if (!zero) {
-            tmem_ld_8_issue(acc + (uint32_t)c, r[0]);
-            tmem_ld_8_issue(acc + (uint32_t)(c + 8), r[1]);
-        }
-        uint8_t *buf = buffers + ring * lt::STORE_BYTES;
-        uint8_t *half = buf + (quarter >> 1) * (lt::STORE_ROWS * 128) + (lane & 7) * 2;
-        if (!zero) {
+            tmem_ld_frag_issue(acc + (uint32_t)c, r[0]);
+            tmem_ld_frag_issue(acc + (uint32_t)c + (16u << 16), r[1]);
             tmem_ld_8_wait(r[0]);
             tmem_ld_8_wait(r[1]);
         }
+        const uint32_t buf = smem_addr(buffers + ring * lt::STORE_BYTES);
 #pragma unroll
-        for (int j = 0; j < lt::STORE_ROWS; ++j)
-            *reinterpret_cast<T *>(half + j * 128 + ((column ^ (uint32_t)(j & 7)) << 4)) =
-                narrow<T>(__uint_as_float(r[j >> 3][j & 7]));
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = narrow2<T>(__uint_as_float(r[h][2 * k]), __uint_as_float(r[h][2 * k + 1]));
+            stmatrix_trans(buf + at + (((chunk + 2 * h) ^ (uint32_t)(row & 7)) << 4), w[0], w[1], w[2], w[3]);
+        }
         // the stores out of the other buffer have read it: it may be written
         // once everyone has passed this barrier
-        if (quarter == 0) bulk_wait_read();
         fence_proxy_async_smem();
+        if (quarter == 0 && lane == 0) bulk_wait_read();
         named_barrier(1 + part, 128);
         if (quarter == 0 && lane == 0) {
-            tma_store_3d(tmOut, smem_addr(buf), f, q + c, expert);
-            if (f + 64 < p.cols) tma_store_3d(tmOut, smem_addr(buf) + lt::STORE_ROWS * 128, f + 64, q + c, expert);
+            tma_store_3d(tmOut, buf, f, q + c, expert);
+            if (f + 64 < p.cols) tma_store_3d(tmOut, buf + lt::STORE_ROWS * 128, f + 64, q + c, expert);
             bulk_commit();
         }
+        __syncwarp();
         ring ^= 1;
     }
 }
@@ -395,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                 ++use;
             }
         }
-        if (MODE == Product::kWeights && quarter == 0) bulk_wait();  // this lane's stores out of shared memory
+        if (MODE == Product::kWeights && quarter == 0 && lane == 0) bulk_wait();  // this thread's stores out of shared memory
     } else {
         // These warps feed the pipeline, and an MMA or a load that they issue
         // late is lost time, also because the epilogue's warps take turns with

@@ -385,6 +385,27 @@ __device__ __forceinline__ void tmem_ld_8_wait(uint32_t (&r)[8]) {
                  : "memory");
 }
 
+// 16 lanes x 16 consecutive columns in the layout of an MMA fragment: this
+// thread receives rows lane / 4 and 8 + lane / 4, columns 2 (lane % 4) and the
+// next (r[0..1], r[2..3]), and the same 8 columns on (r[4..7]).  Waited for with
+// tmem_ld_8_wait.
+__device__ __forceinline__ void tmem_ld_frag_issue(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values from fragments to shared memory,
+// transposed on the way: thread l's word of matrix i holds the values of
+// column lane / 4 in rows 2 (lane % 4) and the next; `row` is the address of
+// row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_trans(uint32_t row, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(row), "r"(w0), "r"(w1),
+                 "r"(w2), "r"(w3)
+                 : "memory");
+}
+
 template <int W>
 __device__ __forceinline__ void tmem_ld_one(uint32_t taddr, float (&v)[W]) {
     static_assert(W == 32, "32 columns");
