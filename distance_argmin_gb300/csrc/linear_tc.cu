@@ -310,7 +310,8 @@ __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xfffff
 template <Product MODE, int BN, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                     const __grid_constant__ CUtensorMap tmOut, const LinearTcParams p) {
+                     const __grid_constant__ CUtensorMap tmB32, const __grid_constant__ CUtensorMap tmOut,
+                     const LinearTcParams p) {
     using C = lt::Cfg<BN, MODE == Product::kWeights>;
     constexpr bool A_MN = MODE != Product::kForward, B_MN = MODE == Product::kWeights;
     constexpr bool RELAY = MODE == Product::kWeights;  // rows may have to be cleared before the MMA
@@ -442,9 +443,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                     // ------------------------------------------- TMA producer
                     const int pa = uniform(t.p0) + rank * lt::BP_CTA, e = uniform(t.expert);
                     // the MMA's N is cut to the rows that exist (a multiple of
-                    // 32); each CTA holds half of it
-                    const int qb = uniform(
-                        t.q0 + rank * (MODE == Product::kWeights ? BN / 2 : (min(BN, (t.qn + 31) & ~31) >> 1)));
+                    // 32); each CTA holds half of it, and loads no more than
+                    // that in boxes of 32 rows (all of it is one box)
+                    const int half = MODE == Product::kWeights ? BN / 2 : uniform(min(BN, (t.qn + 31) & ~31) >> 1);
+                    const int boxes = half == BN / 2 ? 0 : (half + 31) / 32;
+                    const int qb = uniform(t.q0) + rank * half;
+                    const uint32_t bytes = 2u * (boxes ? C::A_BYTES + boxes * (32 * lt::BK * 2) : C::STAGE);
                     int c = uniform(t.c0);
                     for (int left = kblocks; left > 0; --left, c += lt::BK) {
                         if (!mbar_wait_converged(bar(C::EMPTY + s), phase ^ 1, p.status)) {
@@ -463,7 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                                     tma_load_2d(sb + h * (64 * lt::BK * 2), &tmB, full, qb + h * 64, c);
                             } else {
                                 // both CTAs' bytes count on the even CTA's barrier
-                                if (rank == 0) mbar_arrive_expect_tx(full, 2 * C::STAGE);
+                                if (rank == 0) mbar_arrive_expect_tx(full, bytes);
                                 const uint32_t pair_full = map_to_cta(full, 0);
                                 if constexpr (MODE == Product::kForward) {
                                     tma_load_3d_pair(sa, &tmA, pair_full, c, pa, e);
@@ -472,7 +476,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                                     for (int h = 0; h < lt::BP_CTA / 64; ++h)
                                         tma_load_3d_pair(sa + h * (64 * lt::BK * 2), &tmA, pair_full, pa + h * 64, c, e);
                                 }
-                                tma_load_2d_pair(sb, &tmB, pair_full, c, qb);
+                                if (boxes == 0) tma_load_2d_pair(sb, &tmB, pair_full, c, qb);
+                                for (int h = 0; h < boxes; ++h)
+                                    tma_load_2d_pair(sb + h * (32 * lt::BK * 2), &tmB32, pair_full, c, qb + h * 32);
                             }
                         }
                         __syncwarp();
@@ -608,7 +614,7 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
     });
     if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
 
-    CUtensorMap tmA, tmB, tmOut{};
+    CUtensorMap tmA, tmB, tmB32{}, tmOut{};
     bool ok;
     if (MODE == Product::kWeights) {
         const uint64_t da[2] = {(uint64_t)sh.k, (uint64_t)sh.m}, pa[1] = {(uint64_t)g.lda};
@@ -626,8 +632,9 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
         const uint64_t pa[2] = {(uint64_t)g.pitch_w, (uint64_t)(g.pitch_w * sh.n)};
         const uint32_t ba[3] = {64, MODE == Product::kForward ? (uint32_t)lt::BP_CTA : (uint32_t)lt::BK, 1};
         const uint64_t db[2] = {(uint64_t)p.contraction, (uint64_t)sh.m}, pb[1] = {(uint64_t)g.ldb};
-        const uint32_t bb[2] = {lt::BK, BN / 2};
-        ok = encode(&tmA, sh.bf16, g.a, 3, da, pa, ba) && encode(&tmB, sh.bf16, g.b, 2, db, pb, bb);
+        const uint32_t bb[2] = {lt::BK, BN / 2}, b32[2] = {lt::BK, 32};
+        ok = encode(&tmA, sh.bf16, g.a, 3, da, pa, ba) && encode(&tmB, sh.bf16, g.b, 2, db, pb, bb) &&
+             encode(&tmB32, sh.bf16, g.b, 2, db, pb, b32);
     }
     if (!ok) return cudaErrorInvalidValue;
 
@@ -637,7 +644,7 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
     const int64_t most = device_sm_count() / 2, units = row_tiles * p.num_p;
     const unsigned pairs = (unsigned)(units < most ? units : most);
     return launch_kernel(true, linear_tc_kernel<MODE, BN, T>, dim3(2 * (pairs ? pairs : 1)), dim3(lt::THREADS),
-                         C::smem_bytes(sh.n_experts), s, tmA, tmB, tmOut, p);
+                         C::smem_bytes(sh.n_experts), s, tmA, tmB, tmB32, tmOut, p);
 }
 
 template <Product MODE, int BN>
