@@ -12,14 +12,30 @@ namespace km {
 
 namespace {
 
-// dst(r, c) = src(r, c) with the rows of dst on 16 bytes.
-template <typename T>
-__global__ void linear_align_kernel(const T *src, int64_t lds, int64_t rows, int64_t cols, T *dst, int64_t ldd,
-                                    uint32_t *clear) {
+// dst(r, c) = src(r, c) with the rows of dst on 16 bytes: a thread moves 16-byte
+// pieces, read as shifted words.  Of `groups` matrices of `rows` rows (the
+// experts' W) only those of experts that may have rows are copied.
+constexpr int kAlignThreads = 256;
+
+__global__ void __launch_bounds__(kAlignThreads) linear_align_kernel(const uint8_t *src, int64_t pitch, Span in,
+                                                                     int64_t rows, int row_bytes, uint8_t *dst,
+                                                                     int64_t pitch_out, const int32_t *offsets,
+                                                                     uint32_t *clear) {
     griddep_wait();
-    if (clear && blockIdx.x == 0 && threadIdx.x == 0) *clear = 0u;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < cols; c += blockDim.x) dst[r * ldd + c] = src[r * lds + c];
+    if (clear && (blockIdx.x | blockIdx.y | threadIdx.x) == 0u) *clear = 0u;
+    const int64_t group = blockIdx.y;
+    if (offsets && offsets[group + 1] <= offsets[group]) return;
+    const int pieces = (row_bytes + 15) / 16;
+    // a row's pieces go to neighbouring threads
+    for (int64_t i = (int64_t)blockIdx.x * kAlignThreads + threadIdx.x; i < rows * pieces;
+         i += (int64_t)gridDim.x * kAlignThreads) {
+        const int64_t r = i / pieces;
+        const int at = (int)(i - r * pieces) * 16;
+        const int64_t row = group * rows + r;
+        // (dst's rows are padded to whole pieces)
+        *reinterpret_cast<uint4 *>(dst + row * pitch_out + at) =
+            load_piece<false>(src + row * pitch + at, min(16, row_bytes - at), in);
+    }
 }
 
 // dz = dy act'(pre), rounded to the matrices' type, and the bias gradient's
@@ -74,21 +90,12 @@ __device__ bool find_row_tile(const int32_t *offsets, int n_experts, int64_t m, 
     return false;
 }
 
-template <bool WIDE, typename T>
-__device__ __forceinline__ uint4 load8(const T *p, int left) {
-    if constexpr (WIDE) return *reinterpret_cast<const uint4 *>(p);
-    uint32_t w[4] = {};
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-        if (c < left) w[c / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[c] << ((c & 1) * 16);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 constexpr int kSlopeBatch = 2;  // rows whose loads are in flight together
 
 template <bool WIDE, typename T>
 __global__ void __launch_bounds__(kSlopeThreads, 4) linear_slope_kernel(const T *__restrict__ dy, int64_t lddy,
-                                                                        const T *__restrict__ pre,
+                                                                        Span dy_in, const T *__restrict__ pre,
+                                                                        Span pre_in,
                                                                         const int32_t *__restrict__ offsets,
                                                                         int n_experts, int64_t m, int64_t n, int rows,
                                                                         int act, T *__restrict__ dz, int64_t ldz,
@@ -112,8 +119,9 @@ __global__ void __launch_bounds__(kSlopeThreads, 4) linear_slope_kernel(const T 
                 for (int b = 0; b < kSlopeBatch; ++b) {
                     const int64_t row = r + b * WARPS;
                     if (row >= t.r1) continue;
-                    g[b] = load8<WIDE>(dy + row * lddy + c0, left);
-                    if constexpr (ACT != KMEANS_ACT_NONE) z[b] = load8<WIDE>(pre + row * n + c0, left);
+                    g[b] = load_piece<WIDE>(reinterpret_cast<const uint8_t *>(dy + row * lddy + c0), 2 * left, dy_in);
+                    if constexpr (ACT != KMEANS_ACT_NONE)
+                        z[b] = load_piece<WIDE>(reinterpret_cast<const uint8_t *>(pre + row * n + c0), 2 * left, pre_in);
                 }
 #pragma unroll
                 for (int b = 0; b < kSlopeBatch; ++b) {
@@ -216,6 +224,12 @@ int64_t slope_tiles(int64_t m, int64_t n, int64_t n_experts) {
     return (m + rows - 1) / rows + n_experts;
 }
 
+// Bytes of `rows` rows of 16-bit values.
+Span span16(const void *base, int64_t rows, int64_t pitch, int64_t cols) {
+    const uint8_t *b = static_cast<const uint8_t *>(base);
+    return {b, base && rows > 0 ? b + ((rows - 1) * pitch + cols) * 2 : b};
+}
+
 // One call's kernels on the stream: the first of them clears the status word.
 template <typename T>
 struct Call {
@@ -233,19 +247,21 @@ struct Call {
         return c;
     }
 
-    cudaError_t align(const void *&src, int64_t &pitch, int64_t rows, int64_t cols, int64_t off) {
+    cudaError_t align(const void *&src, int64_t &pitch, int64_t groups, int64_t rows, int64_t cols, int64_t off,
+                      const int32_t *offsets) {
         if (rows16(src, pitch) || off == 0 || rows == 0) return cudaSuccess;
-        T *dst = reinterpret_cast<T *>(ws + off);
-        const int64_t ldd = align_up(cols, 8);
-        const cudaError_t e = launch_kernel(true, linear_align_kernel<T>, dim3((unsigned)(rows < 8192 ? rows : 8192)),
-                                            dim3(256), 0, s, static_cast<const T *>(src), pitch, rows, cols, dst, ldd,
-                                            first());
-        src = dst;
+        const int64_t ldd = align_up(cols, 8), blocks = (rows * (ldd / 8) + kAlignThreads - 1) / kAlignThreads;
+        const cudaError_t e = launch_kernel(
+            true, linear_align_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096), (unsigned)groups),
+            dim3(kAlignThreads), 0, s, static_cast<const uint8_t *>(src), pitch * 2, span16(src, groups * rows, pitch, cols),
+            rows, (int)(cols * 2), ws + off, ldd * 2, offsets, first());
+        src = ws + off;
         pitch = ldd;
         return e;
     }
+    cudaError_t align_x(const void *&x, int64_t &pitch) { return align(x, pitch, 1, sh.m, sh.k, L.off_x, nullptr); }
     cudaError_t align_w(Product16 &g) {
-        return align(g.a, g.pitch_w, (int64_t)sh.n_experts * sh.n, sh.k, L.off_w);
+        return align(g.a, g.pitch_w, sh.n_experts, sh.n, sh.k, L.off_w, sh.offsets);
     }
     template <Product MODE>
     cudaError_t product(const Product16 &g) {
@@ -258,7 +274,7 @@ cudaError_t forward_typed(const LinearShape &sh, Product16 g, const LinearLayout
     if (few_rows(sh)) return launch_linear_few(sh, g, &reinterpret_cast<WsHeader *>(ws)->status, s);
     Call<T> call(sh, L, ws, s);
     cudaError_t e = call.align_w(g);
-    if (e == cudaSuccess) e = call.align(g.b, g.ldb, sh.m, sh.k, L.off_x);
+    if (e == cudaSuccess) e = call.align_x(g.b, g.ldb);
     if (e == cudaSuccess) e = call.template product<Product::kForward>(g);
     return e;
 }
@@ -284,7 +300,8 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
         const bool wide = sh.n % 8 == 0 && rows16(dy, lddy) && (activation == KMEANS_ACT_NONE || rows16(pre, sh.n));
         float *partial = db ? reinterpret_cast<float *>(ws + L.off_partial) : nullptr;
         e = launch_kernel(true, wide ? linear_slope_kernel<true, T> : linear_slope_kernel<false, T>, grid,
-                          dim3(kSlopeThreads), 0, s, static_cast<const T *>(dy), lddy, static_cast<const T *>(pre),
+                          dim3(kSlopeThreads), 0, s, static_cast<const T *>(dy), lddy,
+                          span16(dy, sh.m, lddy, sh.n), static_cast<const T *>(pre), span16(pre, sh.m, sh.n, sh.n),
                           sh.offsets, sh.n_experts, sh.m, sh.n, slope_rows(sh.m, sh.n), activation, dz, ldz, partial,
                           call.first());
         if (e == cudaSuccess && db)
@@ -308,7 +325,7 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
         g.a = x;
         g.lda = ldx;
         g.out = dw;
-        e = call.align(g.a, g.lda, sh.m, sh.k, L.off_x);
+        e = call.align_x(g.a, g.lda);
         if (e == cudaSuccess) e = call.template product<Product::kWeights>(g);
     }
     return e;

@@ -100,8 +100,7 @@ struct LinearTcParams {
     int64_t ldr;
     int activation;
     void *out, *pre;
-    int wide_out, wide_res;  // 16-byte accesses allowed
-    int bulk;                // weights: the output leaves by bulk stores
+    int wide;  // the rows of the outputs and the residual start on 16 bytes
     uint32_t *status;
     int test_starve;  // test hook: the producer issues no loads, so the pipeline waits run out
     int clear;  // first kernel of the call: it clears the status word
@@ -163,26 +162,15 @@ struct Units {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ void store8(T *out, const float (&v)[8], bool whole, int left) {
-    if (whole) {
-        *reinterpret_cast<uint4 *>(out) =
-            make_uint4(narrow2<T>(v[0], v[1]), narrow2<T>(v[2], v[3]), narrow2<T>(v[4], v[5]), narrow2<T>(v[6], v[7]));
-    } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (c < left) out[c] = narrow<T>(v[c]);
-    }
-}
-
 // One warp's columns [c0, end) of a unit, 8 rows of 32 features at a time:
 // accumulator -> staged rows -> memory.  In memory's order lane group l / 4 has
 // a row, lane l % 4 eight of its features.  The residual of all the columns is
 // asked for before the accumulator is waited for, so its latency passes behind
 // the unit's MMAs, and the next chunk's accumulator is on its way while one is
-// finished.  (Tried and slower on a dense 8192 x 8192 x 2048, 164 us: 2-byte
-// stores from the accumulator's layout without staging 170 us, one bulk copy
-// per row of 128 features 174 us.)
+// finished.  Rows that do not start on 16 bytes go straight from the
+// accumulator's layout, 32 neighbouring features of a row at a time (run_direct;
+// also for aligned rows it was no faster: dense 8192 x 8192 x 2048 170 us
+// against 164, and one bulk copy per row of 128 features 174).
 template <Product MODE, int BN, typename T>
 struct Finish {
     static constexpr int COLS = BN / (lt::EPI_WARPS / 4), CHUNKS = COLS / lt::EPI_ROWS;
@@ -190,17 +178,17 @@ struct Finish {
     const LinearTcParams &p;
     float *staged;
     int lane;
-    int c0, end, f;   // f: this lane's first feature in memory's order
+    int c0, end, f;   // f: the warp's first feature
     int64_t out_row;  // of the unit's column 0
     bool add;
     uint4 res[FORWARD ? CHUNKS : 1];
 
-    __device__ bool wide_add() const { return add && p.wide_res && f + 8 <= p.cols; }
+    __device__ int f8() const { return f + (lane & 3) * 8; }
 
     __device__ void prefetch() {
         if constexpr (FORWARD) {
-            if (!wide_add()) return;
-            const T *at = static_cast<const T *>(p.residual) + (out_row + c0 + (lane >> 2)) * p.ldr + f;
+            if (!add || !p.wide || f8() >= p.cols) return;
+            const T *at = static_cast<const T *>(p.residual) + (out_row + c0 + (lane >> 2)) * p.ldr + f8();
             const int64_t step = lt::EPI_ROWS * p.ldr;
 #pragma unroll
             for (int i = 0; i < CHUNKS; ++i, at += step)
@@ -208,13 +196,18 @@ struct Finish {
         }
     }
 
+    __device__ __forceinline__ static void store8(void *out, int64_t at, const float (&v)[8]) {
+        *reinterpret_cast<uint4 *>(static_cast<T *>(out) + at) =
+            make_uint4(narrow2<T>(v[0], v[1]), narrow2<T>(v[2], v[3]), narrow2<T>(v[4], v[5]), narrow2<T>(v[6], v[7]));
+    }
+
     template <int ACT>
     __device__ void run(uint32_t acc, float bias, bool zero) {
-        const int left = p.cols - f, row = c0 + (lane >> 2);
-        const bool whole = p.wide_out && left >= 8, wide = wide_add();
+        const int row = c0 + (lane >> 2);
+        const bool mine = f8() < p.cols;  // all eight: cols is a multiple of 8 here
         const int64_t step = (int64_t)lt::EPI_ROWS * p.cols;
-        int64_t at = (out_row + row) * p.cols + f;
-        const float *mine = staged + (lane >> 2) * lt::EPI_PITCH + (lane & 3) * 8;
+        int64_t at = (out_row + row) * p.cols + f8();
+        const float *src = staged + (lane >> 2) * lt::EPI_PITCH + (lane & 3) * 8;
         uint32_t r[8] = {};
         if (!zero) tmem_ld_8_issue(acc + (uint32_t)c0, r);
 #pragma unroll
@@ -227,14 +220,14 @@ struct Finish {
             __syncwarp();
             if (!zero && i + 1 < CHUNKS && c0 + (i + 1) * lt::EPI_ROWS < end)
                 tmem_ld_8_issue(acc + (uint32_t)(c0 + (i + 1) * lt::EPI_ROWS), r);
-            if (row + i * lt::EPI_ROWS >= end || left <= 0) continue;
-            const float4 lo = *reinterpret_cast<const float4 *>(mine), hi = *reinterpret_cast<const float4 *>(mine + 4);
+            if (row + i * lt::EPI_ROWS >= end || !mine) continue;
+            const float4 lo = *reinterpret_cast<const float4 *>(src), hi = *reinterpret_cast<const float4 *>(src + 4);
             float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             if constexpr (FORWARD) {
-                if (p.pre) store8(static_cast<T *>(p.pre) + at, v, whole, left);
+                if (p.pre) store8(p.pre, at, v);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] = activate<ACT>(v[k]);
-                if (wide) {
+                if (add) {
                     const uint32_t words[4] = {res[i].x, res[i].y, res[i].z, res[i].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -242,14 +235,46 @@ struct Finish {
                         v[2 * k] += a.x;
                         v[2 * k + 1] += a.y;
                     }
-                } else if (add) {
-                    const T *src = static_cast<const T *>(p.residual) + (out_row + row + i * lt::EPI_ROWS) * p.ldr + f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (k < left) v[k] += widen(src[k]);
                 }
             }
-            store8(static_cast<T *>(p.out) + at, v, whole, left);
+            store8(p.out, at, v);
+        }
+    }
+
+    // A lane keeps its feature; any alignment.
+    template <int ACT>
+    __device__ __forceinline__ void run_direct(uint32_t acc, float bias, bool zero) {
+        const bool mine = f + lane < p.cols;
+        const int64_t at0 = (out_row + c0) * p.cols + f + lane;
+        T *out = static_cast<T *>(p.out) + at0, *pre = FORWARD && p.pre ? static_cast<T *>(p.pre) + at0 : nullptr;
+        const T *rest = FORWARD && add ? static_cast<const T *>(p.residual) + (out_row + c0) * p.ldr + f + lane : nullptr;
+#pragma unroll 1
+        for (int c = c0; c < end; c += lt::EPI_ROWS) {
+            uint32_t r[8] = {};
+            __syncwarp();
+            if (!zero) {
+                tmem_ld_8_issue(acc + (uint32_t)c, r);
+                tmem_ld_8_wait(r);
+            }
+            float v[8], a[8] = {};
+#pragma unroll
+            for (int j = 0; j < lt::EPI_ROWS; ++j) {
+                v[j] = __uint_as_float(r[j]) + bias;
+                if (FORWARD && rest) {
+                    if (mine && c + j < end) a[j] = widen(*rest);
+                    rest += p.ldr;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < lt::EPI_ROWS; ++j) {
+                const bool on = mine && c + j < end;
+                if (FORWARD && pre) {
+                    if (on) *pre = narrow<T>(v[j]);
+                    pre += p.cols;
+                }
+                if (on) *out = narrow<T>(activate<ACT>(v[j]) + a[j]);
+                out += p.cols;
+            }
         }
     }
 };
@@ -374,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                 bias = widen(static_cast<const T *>(p.bias)[(int64_t)t.expert * p.cols + f + lane]);
             fin.c0 = part * F::COLS;
             fin.end = min(t.qn, fin.c0 + F::COLS);
-            fin.f = f + (lane & 3) * 8;
+            fin.f = f;
             fin.out_row = MODE == Product::kWeights ? (int64_t)t.expert * p.out_rows + t.q0 : (int64_t)t.q0;
             fin.add = MODE == Product::kForward && p.residual && !zero;
             fin.prefetch();
@@ -386,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                 tc_fence_after();
             }
             const uint32_t acc = tmem_base + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
-            if (MODE == Product::kWeights && p.bulk) {
+            if (MODE == Product::kWeights && p.wide) {
                 const int fc = t.p0 + rank * lt::BP_CTA;
                 if (fin.c0 < fin.end && fc < p.cols)
                     store_part<T>(p, &tmOut, smem + C::STAGING_BASE + part * 2 * lt::STORE_BYTES, ring,
@@ -394,9 +419,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                                   t.expert, zero);
             } else if (fin.c0 < fin.end) {
                 if constexpr (MODE == Product::kForward)
-                    with_activation(p.activation, [&](auto a) { fin.template run<decltype(a)::value>(acc, bias, zero); });
-                else
+                    with_activation(p.activation, [&](auto a) {
+                        if (p.wide)
+                            fin.template run<decltype(a)::value>(acc, bias, zero);
+                        else
+                            fin.template run_direct<decltype(a)::value>(acc, bias, zero);
+                    });
+                else if (p.wide)
                     fin.template run<KMEANS_ACT_NONE>(acc, bias, zero);
+                else
+                    fin.template run_direct<KMEANS_ACT_NONE>(acc, bias, zero);
             }
             if (!zero) {
                 tc_fence_before();
@@ -621,7 +653,7 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
         const uint64_t db[2] = {(uint64_t)sh.n, (uint64_t)sh.m}, pb[1] = {(uint64_t)g.ldb};
         const uint32_t box[2] = {64, lt::BK};
         ok = encode(&tmA, sh.bf16, g.a, 2, da, pa, box) && encode(&tmB, sh.bf16, g.b, 2, db, pb, box);
-        if (p.bulk) {
+        if (p.wide) {
             const uint64_t dd[3] = {(uint64_t)sh.k, (uint64_t)sh.n, (uint64_t)sh.n_experts};
             const uint64_t pd[2] = {(uint64_t)sh.k, (uint64_t)(sh.k * sh.n)};
             const uint32_t bd[3] = {64, lt::STORE_ROWS, 1};
@@ -670,9 +702,7 @@ cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product1
     p.activation = g.activation;
     p.out = g.out;
     p.pre = g.pre;
-    p.wide_out = rows16(g.out, p.cols) && (!g.pre || rows16(g.pre, p.cols));
-    p.wide_res = g.residual && rows16(g.residual, g.ldr);
-    p.bulk = mode == Product::kWeights && rows16(g.out, p.cols);
+    p.wide = rows16(g.out, p.cols) && (!g.pre || rows16(g.pre, p.cols)) && (!g.residual || rows16(g.residual, g.ldr));
     p.status = status;
     p.clear = clear;
     // test-only fault injection (no trap, no fault), as in the assignment: every
