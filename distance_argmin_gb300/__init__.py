@@ -732,18 +732,18 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_on(stream, device, *made):
-    """The stream's handle; the current one of the tensors' device by default.
-    ``made``: tensors this call allocated (on the current stream), which may be
-    given back while the work on another stream still uses them."""
+def _current(device):
+    """Handle of the device's current stream."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
+def _on_stream(stream, fn, *args):
+    """``fn(*args)`` with ``stream`` as the current stream, so that what it
+    allocates belongs to that stream (a block that the current stream has given
+    back may still be in use there)."""
     torch = _torch()
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
-    for t in made:
-        if t is not None:
-            t.record_stream(on)
-    return on.cuda_stream
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+        return fn(*args)
 
 
 def _workspace_on(ws, device):
@@ -775,6 +775,8 @@ def kmeans_route(experts, n_experts: int, offsets=None, order=None, rows=None, w
     rows (n, topk))``, all int32.  ``experts`` (n, topk) or (n,): int32 or int64
     ids, negative where the choice was dropped (kmeans_assign's labels route
     each sample to its cluster)."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_route, experts, n_experts, offsets, order, rows, ws)
     torch = _torch()
     if not isinstance(experts, torch.Tensor):
         raise TypeError("experts must be a torch.Tensor")
@@ -788,26 +790,25 @@ def kmeans_route(experts, n_experts: int, offsets=None, order=None, rows=None, w
         _check(experts, "experts", experts.dtype)
     if n_experts < 1:
         raise ValueError(f"n_experts must be at least 1, got {n_experts}")
-    made = [None] * 4
     if offsets is None:
-        offsets = made[0] = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
+        offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
     else:
         _check_on(offsets, "offsets", torch.int32, (n_experts + 1,), dev)
     if order is None:
-        order = made[1] = torch.empty(n * topk, dtype=torch.int32, device=dev)
+        order = torch.empty(n * topk, dtype=torch.int32, device=dev)
     else:
         _check_on(order, "order", torch.int32, (n * topk,), dev)
     if rows is None:
-        rows = made[2] = torch.empty((n, topk), dtype=torch.int32, device=dev)
+        rows = torch.empty((n, topk), dtype=torch.int32, device=dev)
     else:
         _check_on(rows, "rows", torch.int32, (n, topk), dev)
     if ws is None:
-        ws = made[3] = route_workspace(n, topk, n_experts, dev)
+        ws = route_workspace(n, topk, n_experts, dev)
     else:
         _workspace_on(ws, dev)
     st = (_lib or load()).kmeans_route(_addr(experts), experts.element_size(), n, topk, n_experts, _addr(offsets),
                                        _addr(order), _addr(rows), _addr(ws), ws.numel(),
-                                       _stream_on(stream, dev, *made))
+                                       _current(dev))
     _raise(st, "kmeans_route")
     return offsets, order, rows
 
@@ -827,19 +828,20 @@ def _plan(rows, offsets, device):
 def kmeans_route_gather(x, rows, offsets, xs=None, stream=None):
     """The tokens in expert order -> ``xs (n * topk, d)``, zeros in the rows of
     dropped choices.  ``rows`` and ``offsets`` are kmeans_route's."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_route_gather, x, rows, offsets, xs)
     _cuda_matrix(x, "x")
     code = _dtype_code(x, "x")
     dev, dt = x.device, x.dtype
     n, topk, n_experts = _plan(rows, offsets, dev)
     d = x.shape[1]
     ldx = _check_rows(x, "x", dt, (n, d), dev)
-    made = None
     if xs is None:
-        xs = made = _torch().empty((n * topk, d), dtype=dt, device=dev)
+        xs = _torch().empty((n * topk, d), dtype=dt, device=dev)
     else:
         _check_on(xs, "xs", dt, (n * topk, d), dev)
-    st = (_lib or load()).kmeans_route_gather(_addr(x), ldx, code, _addr(rows), _addr(offsets), n, topk, n_experts, d, _addr(xs),
-                                    _stream_on(stream, dev, made))
+    st = (_lib or load()).kmeans_route_gather(_addr(x), ldx, code, _addr(rows), _addr(offsets), n, topk, n_experts, d,
+                                              _addr(xs), _current(dev))
     _raise(st, "kmeans_route_gather")
     return xs
 
@@ -848,6 +850,8 @@ def kmeans_route_combine(ys, rows, offsets, weights=None, residual=None, y=None,
     """The experts' rows back per token -> ``y (n, d)``: residual + the sum of
     ``weights`` (n, topk) times the choices' rows of ``ys`` (n * topk, d).
     Without weights, also the gradient of kmeans_route_gather."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_route_combine, ys, rows, offsets, weights, residual, y)
     torch = _torch()
     _cuda_matrix(ys, "ys")
     code = _dtype_code(ys, "ys")
@@ -855,16 +859,15 @@ def kmeans_route_combine(ys, rows, offsets, weights=None, residual=None, y=None,
     n, topk, n_experts = _plan(rows, offsets, dev)
     d = ys.shape[1]
     _check_on(ys, "ys", ys.dtype, (n * topk, d), dev)
-    made = None
     if weights is not None:
         _check_on(weights, "weights", torch.float32, (n, topk), dev)
     ldr = _check_rows(residual, "residual", ys.dtype, (n, d), dev) if residual is not None else 0
     if y is None:
-        y = made = torch.empty((n, d), dtype=ys.dtype, device=dev)
+        y = torch.empty((n, d), dtype=ys.dtype, device=dev)
     else:
         _check_on(y, "y", ys.dtype, (n, d), dev)
-    st = (_lib or load()).kmeans_route_combine(_addr(ys), code, _addr(weights), _addr(residual), ldr, _addr(rows), _addr(offsets), n,
-                                     topk, n_experts, d, _addr(y), _stream_on(stream, dev, made))
+    st = (_lib or load()).kmeans_route_combine(_addr(ys), code, _addr(weights), _addr(residual), ldr, _addr(rows),
+                                               _addr(offsets), n, topk, n_experts, d, _addr(y), _current(dev))
     _raise(st, "kmeans_route_combine")
     return y
 
@@ -872,6 +875,8 @@ def kmeans_route_combine(ys, rows, offsets, weights=None, residual=None, y=None,
 def kmeans_route_combine_grad(dy, ys, rows, offsets, weights, dys=None, dweights=None, stream=None):
     """Gradient of kmeans_route_combine -> ``(dys (n * topk, d), dweights
     (n, topk) float32)``; the residual's gradient is ``dy``."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_route_combine_grad, dy, ys, rows, offsets, weights, dys, dweights)
     torch = _torch()
     _cuda_matrix(ys, "ys")
     code = _dtype_code(ys, "ys")
@@ -879,19 +884,19 @@ def kmeans_route_combine_grad(dy, ys, rows, offsets, weights, dys=None, dweights
     n, topk, n_experts = _plan(rows, offsets, dev)
     d = ys.shape[1]
     _check_on(ys, "ys", ys.dtype, (n * topk, d), dev)
-    made = [None, None]
     lddy = _check_rows(dy, "dy", ys.dtype, (n, d), dev)
     _check_on(weights, "weights", torch.float32, (n, topk), dev)
     if dys is None:
-        dys = made[0] = torch.empty((n * topk, d), dtype=ys.dtype, device=dev)
+        dys = torch.empty((n * topk, d), dtype=ys.dtype, device=dev)
     else:
         _check_on(dys, "dys", ys.dtype, (n * topk, d), dev)
     if dweights is None:
-        dweights = made[1] = torch.empty((n, topk), dtype=torch.float32, device=dev)
+        dweights = torch.empty((n, topk), dtype=torch.float32, device=dev)
     else:
         _check_on(dweights, "dweights", torch.float32, (n, topk), dev)
-    st = (_lib or load()).kmeans_route_combine_grad(_addr(dy), lddy, _addr(ys), code, _addr(weights), _addr(rows), _addr(offsets), n,
-                                          topk, n_experts, d, _addr(dys), _addr(dweights), _stream_on(stream, dev, *made))
+    st = (_lib or load()).kmeans_route_combine_grad(_addr(dy), lddy, _addr(ys), code, _addr(weights), _addr(rows),
+                                                    _addr(offsets), n, topk, n_experts, d, _addr(dys), _addr(dweights),
+                                                    _current(dev))
     _raise(st, "kmeans_route_combine_grad")
     return dys, dweights
 
@@ -931,6 +936,8 @@ def kmeans_linear(x, w, bias=None, residual=None, offsets=None, activation="none
     none, relu, gelu, gelu_tanh or silu.  ``save_pre`` (or a ``pre`` to write
     into) keeps the values before the activation for kmeans_linear_grad.
     float16 or bfloat16."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_linear, x, w, bias, residual, offsets, activation, save_pre, y, pre, ws)
     torch = _torch()
     code, m, n, k, n_experts, act = _linear_args(x, w, offsets, activation)
     dev, dt = x.device, x.dtype
@@ -938,21 +945,21 @@ def kmeans_linear(x, w, bias=None, residual=None, offsets=None, activation="none
     if bias is not None:
         _check_on(bias, "bias", dt, tuple(w.shape[:-1]), dev)
     ldr = _check_rows(residual, "residual", dt, (m, n), dev) if residual is not None else 0
-    made = [None] * 3
     if y is None:
-        y = made[0] = torch.empty((m, n), dtype=dt, device=dev)
+        y = torch.empty((m, n), dtype=dt, device=dev)
     else:
         _check_on(y, "y", dt, (m, n), dev)
     if pre is not None:
         _check_on(pre, "pre", dt, (m, n), dev)
     elif save_pre:
-        pre = made[1] = torch.empty((m, n), dtype=dt, device=dev)
+        pre = torch.empty((m, n), dtype=dt, device=dev)
     if ws is None:
-        ws = made[2] = linear_workspace(OP_LINEAR, m, n, k, n_experts, dev)
+        ws = linear_workspace(OP_LINEAR, m, n, k, n_experts, dev)
     else:
         _workspace_on(ws, dev)
-    st = (_lib or load()).kmeans_linear(_addr(x), ldx, _addr(w), _addr(bias), _addr(residual), ldr, code, act, _addr(offsets), m, n,
-                              k, n_experts, _addr(y), _addr(pre), _addr(ws), ws.numel(), _stream_on(stream, dev, *made))
+    st = (_lib or load()).kmeans_linear(_addr(x), ldx, _addr(w), _addr(bias), _addr(residual), ldr, code, act,
+                                        _addr(offsets), m, n, k, n_experts, _addr(y), _addr(pre), _addr(ws),
+                                        ws.numel(), _current(dev))
     _raise(st, "kmeans_linear")
     return y, pre
 
@@ -962,6 +969,9 @@ def kmeans_linear_grad(dy, x, w, pre=None, offsets=None, activation="none", need
     """Gradient of kmeans_linear -> ``(dx, dw, db)`` (None where not needed);
     ``pre`` is what kmeans_linear kept (not needed without an activation).  The
     residual's gradient is ``dy``."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_linear_grad, dy, x, w, pre, offsets, activation, need_dx, need_dw, need_db,
+                          dx, dw, db, ws)
     torch = _torch()
     code, m, n, k, n_experts, act = _linear_args(x, w, offsets, activation)
     dev, dt = x.device, x.dtype
@@ -971,29 +981,28 @@ def kmeans_linear_grad(dy, x, w, pre=None, offsets=None, activation="none", need
         if pre is None:
             raise ValueError(f"activation {activation!r} needs pre")
         _check_on(pre, "pre", dt, (m, n), dev)
-    made = [None] * 4
     if need_dx:
         if dx is None:
-            dx = made[0] = torch.empty((m, k), dtype=dt, device=dev)
+            dx = torch.empty((m, k), dtype=dt, device=dev)
         else:
             _check_on(dx, "dx", dt, (m, k), dev)
     if need_dw:
         if dw is None:
-            dw = made[1] = torch.empty_like(w)
+            dw = torch.empty_like(w)
         else:
             _check_on(dw, "dw", dt, tuple(w.shape), dev)
     if need_db:
         if db is None:
-            db = made[2] = torch.empty(w.shape[:-1], dtype=dt, device=dev)
+            db = torch.empty(w.shape[:-1], dtype=dt, device=dev)
         else:
             _check_on(db, "db", dt, tuple(w.shape[:-1]), dev)
     if ws is None:
-        ws = made[3] = linear_workspace(OP_LINEAR_GRAD, m, n, k, n_experts, dev)
+        ws = linear_workspace(OP_LINEAR_GRAD, m, n, k, n_experts, dev)
     else:
         _check(ws, "ws", torch.uint8, device=dev)
     dx, dw, db = dx if need_dx else None, dw if need_dw else None, db if need_db else None
-    st = (_lib or load()).kmeans_linear_grad(_addr(dy), lddy, _addr(x), ldx, _addr(w), _addr(pre), code, act, _addr(offsets), m, n, k,
-                                   n_experts, _addr(dx), _addr(dw), _addr(db), _addr(ws), ws.numel(),
-                                   _stream_on(stream, dev, *made))
+    st = (_lib or load()).kmeans_linear_grad(_addr(dy), lddy, _addr(x), ldx, _addr(w), _addr(pre), code, act,
+                                             _addr(offsets), m, n, k, n_experts, _addr(dx), _addr(dw), _addr(db),
+                                             _addr(ws), ws.numel(), _current(dev))
     _raise(st, "kmeans_linear_grad")
     return dx, dw, db

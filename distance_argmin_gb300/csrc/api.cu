@@ -604,7 +604,7 @@ const char *kmeans_status_string(int status) {
         case KMEANS_ERR_WORKSPACE: return "workspace too small or not 256-byte aligned";
         case KMEANS_ERR_CUDA: return "CUDA runtime error";
         case KMEANS_ERR_DEVICE_TIMEOUT: return "a device pipeline wait ran out of time";
-        case KMEANS_ERR_DEVICE_LABEL: return "a label outside [0, k) reached the update";
+        case KMEANS_ERR_DEVICE_LABEL: return "a label outside [0, k) or an expert id past the last expert";
         case KMEANS_ERR_SCRATCH_LIMIT:
             return "problem too large for the built-in scratch of kmeans_assign_noalloc "
                    "(use kmeans_assign with a workspace)";
@@ -621,7 +621,9 @@ const char *kmeans_build_info(void) {
            "hi.hi and correction accumulators above; X/C ring 4, split ring 6); comparator = FFMA 128x128; "
            "update = counting-scatter member list (k <= 32768; LSD radix above) + compensated segmented mean; "
            "sharded update = per-rank sums reduced in rank order; k-means++ = Philox4x32-10 greedy D^2 with "
-           "triangle-inequality row pruning (single GPU; sharded steps without)";
+           "triangle-inequality row pruning (single GPU; sharded steps without); experts = one-cluster stable sort, "
+           "16-byte row movers, tcgen05 cta_group::2 products of 256 features x 64 to 256 rows (BK 64), "
+           "mma.sync product for few rows";
 }
 
 }  // extern "C"

@@ -89,7 +89,7 @@ inline int cached_per_device(std::atomic<int> (&cache)[kMaxDevices], Fn &&comput
 // ---------------------------------------------------------------------------
 enum : uint32_t {
     kFlagTimeout = 1u,   // a pipeline wait ran out of time
-    kFlagBadLabel = 2u,  // update saw a label outside [0, k)
+    kFlagBadLabel = 2u,  // update saw a label outside [0, k), the routing an id past the last expert
     kFlagExchange = 4u,  // sharded k-means++: no rank's exchange block owned a trial
 };
 

@@ -20,6 +20,22 @@ order and keeps what the gradient needs.
 from __future__ import annotations
 
 import contextlib
+import functools
+
+
+def _on_stream(fn):
+    """Run ``fn`` with its ``stream`` argument as the current CUDA stream: its
+    calls, and what they allocate, then belong to that stream."""
+    @functools.wraps(fn)
+    def wrapped(*args, stream=None, **kwargs):
+        ctx = contextlib.nullcontext()
+        if stream is not None:
+            import torch
+            ctx = torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(int(stream)))
+        with ctx:
+            return fn(*args, **kwargs)
+    return wrapped
 
 
 def _km():
@@ -27,26 +43,24 @@ def _km():
     return km
 
 
-def nearest_experts(x, centroids, ws=None, stream=None):
+@_on_stream
+def nearest_experts(x, centroids, ws=None):
     """Expert of each token: its nearest centroid -> int64 ids ``(n, 1)``.
     ``x`` (n, d) and ``centroids`` (n_experts, d) float32, n >= n_experts as
     kmeans_assign requires (fewer tokens: see ``few_nearest_experts``)."""
-    labels, _, _ = _km().kmeans_assign(x, centroids, ws=ws, stream=stream)
+    labels, _, _ = _km().kmeans_assign(x, centroids, ws=ws)
     return labels.view(-1, 1)
 
 
-def few_nearest_experts(x, centroids, stream=None):
+@_on_stream
+def few_nearest_experts(x, centroids):
     """nearest_experts for any number of tokens: fewer than the experts are
     repeated to as many rows as kmeans_assign wants."""
     n, k = x.shape[0], centroids.shape[0]
     if n >= k:
-        return nearest_experts(x, centroids, stream=stream)
-    import torch
-    on = contextlib.nullcontext() if stream is None else torch.cuda.stream(
-        stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
-    with on:
-        padded = x.repeat((k + n - 1) // max(n, 1), 1) if n else x.new_zeros(k, x.shape[1])
-        return nearest_experts(padded, centroids)[:n]
+        return nearest_experts(x, centroids)
+    padded = x.repeat((k + n - 1) // n, 1) if n else x.new_zeros(k, x.shape[1])
+    return nearest_experts(padded, centroids)[:n]
 
 
 class Saved:
@@ -56,8 +70,8 @@ class Saved:
         self.__dict__.update(kept)
 
 
-def experts_forward(x, ids, w1, w2, b1=None, b2=None, weights=None, residual=None, activation="gelu", keep=False,
-                    stream=None):
+@_on_stream
+def experts_forward(x, ids, w1, w2, b1=None, b2=None, weights=None, residual=None, activation="gelu", keep=False):
     """``(y, saved)``: y (n, d_out) of tokens x (n, d), float16 or bfloat16.
 
     ``ids`` (n, topk) experts of each token (negative: none); ``w1`` (n_experts,
@@ -67,17 +81,18 @@ def experts_forward(x, ids, w1, w2, b1=None, b2=None, weights=None, residual=Non
     ``saved``, else None."""
     km = _km()
     n_experts = w1.shape[0]
-    offsets, _, rows = km.kmeans_route(ids, n_experts, stream=stream)
-    xs = km.kmeans_route_gather(x, rows, offsets, stream=stream)
-    h, pre = km.kmeans_linear(xs, w1, bias=b1, offsets=offsets, activation=activation, save_pre=keep, stream=stream)
-    ys, _ = km.kmeans_linear(h, w2, bias=b2, offsets=offsets, stream=stream)
-    y = km.kmeans_route_combine(ys, rows, offsets, weights=weights, residual=residual, stream=stream)
+    offsets, _, rows = km.kmeans_route(ids, n_experts)
+    xs = km.kmeans_route_gather(x, rows, offsets)
+    h, pre = km.kmeans_linear(xs, w1, bias=b1, offsets=offsets, activation=activation, save_pre=keep)
+    ys, _ = km.kmeans_linear(h, w2, bias=b2, offsets=offsets)
+    y = km.kmeans_route_combine(ys, rows, offsets, weights=weights, residual=residual)
     saved = Saved(offsets=offsets, rows=rows, xs=xs, pre=pre, h=h, ys=ys, weights=weights, activation=activation,
                   has_b1=b1 is not None, has_b2=b2 is not None) if keep else None
     return y, saved
 
 
-def experts_backward(dy, saved, w1, w2, stream=None):
+@_on_stream
+def experts_backward(dy, saved, w1, w2):
     """Gradients of experts_forward -> dict with ``x``, ``w1``, ``b1``, ``w2``,
     ``b2`` and ``weights`` (None where the forward pass had none); the
     residual's gradient is ``dy``."""
@@ -87,12 +102,10 @@ def experts_backward(dy, saved, w1, w2, stream=None):
     if weights is None:
         import torch
         weights = torch.ones(s.rows.shape, dtype=torch.float32, device=dy.device)
-        if stream is not None:
-            torch.cuda.current_stream().synchronize()  # the ones are there before another stream reads them
-    dys, dweights = km.kmeans_route_combine_grad(dy, s.ys, s.rows, s.offsets, weights, stream=stream)
-    dh, dw2, db2 = km.kmeans_linear_grad(dys, s.h, w2, offsets=s.offsets, need_db=s.has_b2, stream=stream)
+    dys, dweights = km.kmeans_route_combine_grad(dy, s.ys, s.rows, s.offsets, weights)
+    dh, dw2, db2 = km.kmeans_linear_grad(dys, s.h, w2, offsets=s.offsets, need_db=s.has_b2)
     dxs, dw1, db1 = km.kmeans_linear_grad(dh, s.xs, w1, pre=s.pre, offsets=s.offsets, activation=s.activation,
-                                          need_db=s.has_b1, stream=stream)
-    dx = km.kmeans_route_combine(dxs, s.rows, s.offsets, stream=stream)
+                                          need_db=s.has_b1)
+    dx = km.kmeans_route_combine(dxs, s.rows, s.offsets)
     return {"x": dx, "w1": dw1, "b1": db1, "w2": dw2, "b2": db2,
             "weights": dweights if s.weights is not None else None}

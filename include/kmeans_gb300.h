@@ -2,7 +2,8 @@
  * kmeans_gb300.h -- C ABI of the GB300 (sm_103a) k-means library.
  *
  * The library computes one Lloyd iteration of k-means and greedy k-means++
- * seeding on one GPU.  Every entry point takes caller-owned DEVICE pointers,
+ * seeding on one GPU, and (further down) a layer of experts whose rows the
+ * clusters, or any other choice, route.  Every entry point takes caller-owned DEVICE pointers,
  * the sizes n (samples), k (centroids), d (features), a caller-owned device
  * workspace, a seed and a CUDA stream, enqueues its kernels on that stream and
  * returns without synchronising.  The library allocates no memory.
@@ -78,7 +79,8 @@ typedef enum {
     KMEANS_ERR_WORKSPACE = 3,       /* ws too small or misaligned                */
     KMEANS_ERR_CUDA = 4,            /* a CUDA runtime call failed                */
     KMEANS_ERR_DEVICE_TIMEOUT = 5,  /* a device pipeline wait ran out of time    */
-    KMEANS_ERR_DEVICE_LABEL = 6,    /* kmeans_update saw a label outside [0, k)  */
+    KMEANS_ERR_DEVICE_LABEL = 6,    /* kmeans_update saw a label outside [0, k),
+                                       kmeans_route an id of n_experts or more   */
     KMEANS_ERR_SCRATCH_LIMIT = 7,   /* kmeans_assign_noalloc: the problem needs more
                                        than KMEANS_NOALLOC_SCRATCH_BYTES of scratch */
     KMEANS_ERR_DEVICE_EXCHANGE = 8  /* kmeanspp_shard_dist: no rank's exchange block
