@@ -368,6 +368,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
         mbar_init(bar(C::DRAIN), 1);
         fence_barrier_init();
     }
+    if (warp == lt::WARP_TMA && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        if (MODE != Product::kWeights) tma_prefetch_desc(&tmB32);
+    }
     if (warp == lt::WARP_MMA) {
         tmem_alloc_pair(smem_addr(tmem_holder), C::TMEM_COLS);
         tmem_relinquish_pair();
@@ -458,10 +463,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                 phase ^= 1;
             }
         };
-        if (warp == lt::WARP_TMA && leader) {
-            tma_prefetch_desc(&tmA);
-            tma_prefetch_desc(&tmB);
-        }
         for (int u0 = pair; u0 < units.total && ok; u0 += lt::LIST_UNITS * num_pairs) {
             __syncwarp();
             const int mine = u0 + lane * num_pairs;
