@@ -102,12 +102,14 @@ __global__ void __launch_bounds__(kSlopeThreads, 4) linear_slope_kernel(const T 
                                                                         float *__restrict__ partial, uint32_t *clear) {
     __shared__ float sums[kSlopeThreads / 32][kSlopeCols];
     griddep_wait();
-    if (clear && (blockIdx.x | blockIdx.y | threadIdx.x) == 0u) *clear = 0u;
+    if (clear && (blockIdx.x | threadIdx.x) == 0u) *clear = 0u;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int WARPS = kSlopeThreads / 32;
+    const int strips = (int)((n + kSlopeCols - 1) / kSlopeCols);
+    const int tile = (int)(blockIdx.x / strips), strip = (int)(blockIdx.x % strips);
     RowTile t;
-    if (!find_row_tile(offsets, n_experts, m, rows, blockIdx.y, t)) return;
-    const int64_t c0 = (int64_t)blockIdx.x * kSlopeCols + lane * 8;
+    if (!find_row_tile(offsets, n_experts, m, rows, tile, t)) return;
+    const int64_t c0 = (int64_t)strip * kSlopeCols + lane * 8;
     const int left = (int)min((int64_t)8, n - c0);
     float sum[8] = {};
     if (left > 0)
@@ -157,12 +159,12 @@ __global__ void __launch_bounds__(kSlopeThreads, 4) linear_slope_kernel(const T 
 #pragma unroll
     for (int c = 0; c < 8; ++c) sums[warp][lane * 8 + c] = sum[c];
     __syncthreads();
-    const int64_t col = (int64_t)blockIdx.x * kSlopeCols + threadIdx.x;
+    const int64_t col = (int64_t)strip * kSlopeCols + threadIdx.x;
     if (col >= n) return;
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) s += sums[w][threadIdx.x];
-    partial[(int64_t)blockIdx.y * n + col] = s;
+    partial[(int64_t)tile * n + col] = s;
 }
 
 template <typename T>
@@ -208,6 +210,30 @@ __global__ void __launch_bounds__(kSlopeThreads) linear_bias_join_kernel(const f
 #pragma unroll 8
     for (int u = range[0]; u < range[1]; ++u) s += partial[(int64_t)u * n + col];
     db[(int64_t)expert * n + col] = narrow<T>(s);
+}
+
+// dw[e] = the sums of expert e's chunks of rows, in order, where it has several.
+template <typename T>
+__global__ void __launch_bounds__(kSlopeThreads) linear_weights_join_kernel(const float *__restrict__ partial,
+                                                                            const int32_t *offsets, int n_experts,
+                                                                            int64_t m, int chunk, int64_t size, T *dw) {
+    extern __shared__ int join_smem[];
+    int *edges = join_smem, *tiles = edges + n_experts + 2, *slots = tiles + n_experts + 2;
+    griddep_wait();
+    if (threadIdx.x < 32) fill_tables(offsets, n_experts, m, chunk, edges, tiles, slots, threadIdx.x);
+    __syncthreads();
+    for (int e = 0; e < n_experts; ++e) {
+        const int chunks = slots[e + 1] - slots[e];
+        if (chunks == 0) continue;
+        const float *from = partial + (int64_t)slots[e] * size;
+        for (int64_t i = (int64_t)blockIdx.x * kSlopeThreads + threadIdx.x; i < size;
+             i += (int64_t)gridDim.x * kSlopeThreads) {
+            float s = 0.f;
+#pragma unroll 8
+            for (int c = 0; c < chunks; ++c) s += from[(int64_t)c * size + i];
+            dw[(int64_t)e * size + i] = narrow<T>(s);
+        }
+    }
 }
 
 // Rows of a block: fewer where that gives every SM a block or two (257 rows of
@@ -296,7 +322,7 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
             g.b = dz;
             g.ldb = ldz;
         }
-        const dim3 grid((unsigned)((sh.n + kSlopeCols - 1) / kSlopeCols), (unsigned)slope_tiles(sh.m, sh.n, sh.offsets ? sh.n_experts : 0));
+        const dim3 grid((unsigned)((sh.n + kSlopeCols - 1) / kSlopeCols * slope_tiles(sh.m, sh.n, sh.offsets ? sh.n_experts : 0)));
         const bool wide = sh.n % 8 == 0 && rows16(dy, lddy) && (activation == KMEANS_ACT_NONE || rows16(pre, sh.n));
         float *partial = db ? reinterpret_cast<float *>(ws + L.off_partial) : nullptr;
         e = launch_kernel(true, wide ? linear_slope_kernel<true, T> : linear_slope_kernel<false, T>, grid,
@@ -325,8 +351,17 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
         g.a = x;
         g.lda = ldx;
         g.out = dw;
+        const WeightsSplit split = weights_split(sh.m, sh.n, sh.k, sh.n_experts);
+        g.partial = reinterpret_cast<float *>(ws + L.off_sums);
         e = call.align_x(g.a, g.lda);
         if (e == cudaSuccess) e = call.template product<Product::kWeights>(g);
+        if (e == cudaSuccess && split.slots > 0) {
+            const int64_t size = sh.n * sh.k, blocks = (size + kSlopeThreads - 1) / kSlopeThreads;
+            e = launch_kernel(true, linear_weights_join_kernel<T>, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)),
+                              dim3(kSlopeThreads), 3 * (size_t)(sh.n_experts + 2) * 4, s,
+                              static_cast<const float *>(g.partial), sh.offsets, sh.n_experts, sh.m, split.chunk, size,
+                              static_cast<T *>(dw));
+        }
     }
     return e;
 }
@@ -345,6 +380,8 @@ LinearLayout linear_layout(bool grad, int64_t m, int64_t n, int64_t k, int64_t n
     if (grad) {
         L.off_dz = o;
         o = align_up(o + m * align_up(n, 8) * 2, 1024);
+        L.off_sums = o;
+        o = align_up(o + weights_split(m, n, k, n_experts).slots * n * k * 4, 1024);
         L.off_partial = o;
         o = align_up(o + slope_tiles(m, n, n_experts) * n * 4, 1024);
     }

@@ -30,6 +30,7 @@ struct Product16 {
     int64_t ldr;
     int activation;
     void *out, *pre;
+    float *partial;           // weights: the chunks' sums (see WeightsSplit)
 };
 
 // f applied with the activation as a compile-time constant: one branch around
@@ -52,39 +53,64 @@ __device__ __forceinline__ int64_t first_row(const int32_t *offsets, int e, int6
     return v < from ? from : (v > m ? m : v);
 }
 
-// The row tiles (of ROWS rows) of a call, expert by expert: edges[e] is expert
+// The row tiles (of `rows` rows) of a call, expert by expert: edges[e] is expert
 // e's first row (the offsets' running maximum, cut to m), tiles[e] the tiles
 // before it; group n_experts holds the rows of no expert.  Filled by one warp;
-// each table has n_experts + 2 entries.
-template <int ROWS>
-__device__ void fill_tables(const int32_t *offsets, int n_experts, int64_t m, int *edges, int *tiles, int lane) {
-    int last = 0, count = 0;
-    if (lane == 0) edges[0] = tiles[0] = 0;
+// each table has n_experts + 2 entries.  With `slots` an expert has a tile also
+// without rows, and slots[e] counts the tiles before it of experts that have
+// more than one.
+__device__ inline void fill_tables(const int32_t *offsets, int n_experts, int64_t m, int rows, int *edges, int *tiles,
+                                   int *slots, int lane) {
+    constexpr uint32_t all = 0xffffffffu;
+    int last = 0, count = 0, taken = 0;
+    if (lane == 0) {
+        edges[0] = tiles[0] = 0;
+        if (slots) slots[0] = 0;
+    }
     for (int e0 = 0; e0 <= n_experts; e0 += 32) {
         const int e = e0 + lane;  // group e ends at edge e + 1
         int end = 0;
         if (e < n_experts) end = offsets ? max(0, (int)min((int64_t)offsets[e + 1], m)) : (int)m;
         if (e == n_experts) end = (int)m;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(0xffffffffu, end, o));
+        for (int o = 1; o < 32; o <<= 1) end = max(end, __shfl_up_sync(all, end, o));
         end = max(end, last);
-        int start = __shfl_up_sync(0xffffffffu, end, 1);
+        int start = __shfl_up_sync(all, end, 1);
         if (lane == 0) start = last;
-        int t = (int)(((int64_t)end - start + ROWS - 1) / ROWS);
+        int t = (int)(((int64_t)end - start + rows - 1) / rows);
+        if (slots) t = e < n_experts ? max(t, 1) : 0;
+        int several = slots && t > 1 ? t : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += v;
+            const int v = __shfl_up_sync(all, t, o), w = __shfl_up_sync(all, several, o);
+            if (lane >= o) {
+                t += v;
+                several += w;
+            }
         }
         t += count;
+        several += taken;
         if (e <= n_experts) {
             edges[e + 1] = end;
             tiles[e + 1] = t;
+            if (slots) slots[e + 1] = several;
         }
-        last = __shfl_sync(0xffffffffu, end, 31);
-        count = __shfl_sync(0xffffffffu, t, 31);
+        last = __shfl_sync(all, end, 31);
+        count = __shfl_sync(all, t, 31);
+        taken = __shfl_sync(all, several, 31);
     }
 }
+
+// The weights product's contraction runs over an expert's rows, `chunk` of them
+// at most in one accumulator: the tensor cores cut off what a sum's last bit
+// does not hold, some 6e-9 of it per row, and few output tiles over many rows
+// would leave most SMs idle.  The chunks' sums of an expert with several meet
+// in float32 in the workspace (`slots` matrices).
+struct WeightsSplit {
+    int chunk;
+    int64_t slots;  // most partial matrices there can be; 0: every expert is one chunk
+};
+WeightsSplit weights_split(int64_t m, int64_t n, int64_t k, int64_t n_experts);
 
 // A matrix whose rows all start on 16 bytes.
 inline bool rows16(const void *base, int64_t pitch_elems) {

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kFewThreads, WHOLE ? kFewBlocks : 2) linear_fe
     const int split = p.split, crank = split > 1 ? (int)cluster_ctarank() : 0;
     griddep_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
-    if (warp == 0) fill_tables<kFewRows>(p.offsets, p.n_experts, p.m, edges, tiles, lane);
+    if (warp == 0) fill_tables(p.offsets, p.n_experts, p.m, kFewRows, edges, tiles, nullptr, lane);
     __syncthreads();
     const int total = tiles[p.n_experts + 1] * p.num_p;  // below 2^31: each is 16 rows of a matrix in memory
     const int first = blockIdx.x / split, stride = gridDim.x / split;

@@ -60,7 +60,7 @@ constexpr int EPI_PITCH = 36;      // floats: 8 rows x 32 bytes then hit distinc
 constexpr int STAGING = EPI_WARPS * EPI_ROWS * EPI_PITCH * 4;
 constexpr int BAND = 8;            // feature tiles per raster band
 constexpr int LIST_UNITS = 32;     // units a warp works out at a time
-constexpr int LIST_BYTES = LIST_UNITS * 24;
+constexpr int LIST_BYTES = LIST_UNITS * 28;
 constexpr int SMEM_LIMIT = 232448;
 constexpr int BAR_BYTES = 512;
 
@@ -81,10 +81,11 @@ struct Cfg {
     static constexpr int TMEM_COLS = 2 * BN;  // >= 64
     static constexpr int FULL = 0, READY = STAGES, EMPTY = 2 * STAGES, T_FULL = 3 * STAGES, T_EMPTY = T_FULL + 2,
                          DRAIN = T_EMPTY + 2, NUM_BARS = DRAIN + 1;
-    static constexpr int smem_bytes(int n_experts) { return TABLE_BASE + 2 * (n_experts + 2) * 4 + 1024; }
+    static constexpr int smem_bytes_most() { return TABLE_BASE + 3 * (KMEANS_LINEAR_MAX_EXPERTS + 2) * 4 + 1024; }
+    static constexpr int smem_bytes(int n_experts) { return TABLE_BASE + (STORES ? 3 : 2) * (n_experts + 2) * 4 + 1024; }
     static_assert(NUM_BARS * 8 + 16 <= BAR_BYTES, "barriers fit");
     static_assert(STAGE % 1024 == 0 && STAGING % 1024 == 0, "stages stay 1 KiB aligned");
-    static_assert(TABLE_BASE + 2 * (KMEANS_LINEAR_MAX_EXPERTS + 2) * 4 + 1024 <= SMEM_LIMIT, "fits");
+    static_assert(smem_bytes_most() <= SMEM_LIMIT, "fits");
 };
 }  // namespace lt
 
@@ -95,6 +96,8 @@ struct LinearTcParams {
     int cols;         // size of the output's contiguous dimension
     int num_p;        // feature tiles
     int out_rows;     // weights: output features of an expert
+    int chunk;        // weights: rows of a unit's contraction at most
+    float *partial;
     int contraction;  // forward, rows
     const void *bias, *residual;
     int64_t ldr;
@@ -112,6 +115,7 @@ struct LinearTcParams {
 struct Unit {
     int expert, p0, q0, qn;  // q0: first output row (row products: of the matrix, weights: of the expert)
     int c0, c1;              // contraction range (rows of x for weights)
+    int slot;                // weights: the partial matrix this chunk of rows goes to (-1: the output)
 };
 
 // (There are fewer than 2^31 units: each is 64 rows x 256 features or more of
@@ -119,23 +123,25 @@ struct Unit {
 template <Product MODE, int BN>
 struct Units {
     const LinearTcParams &p;
-    const int *edges, *tiles;
+    const int *edges, *tiles, *slots;
     int total;
     int e = 0;
 
-    __device__ Units(const LinearTcParams &p_, const int *edges_, const int *tiles_)
-        : p(p_), edges(edges_), tiles(tiles_) {
-        total = (MODE == Product::kWeights ? p.n_experts * row_tiles() : tiles[p.n_experts + 1]) * p.num_p;
+    __device__ Units(const LinearTcParams &p_, const int *edges_, const int *tiles_, const int *slots_)
+        : p(p_), edges(edges_), tiles(tiles_), slots(slots_) {
+        total = tiles[p.n_experts + 1] * p.num_p * (MODE == Product::kWeights ? row_tiles() : 1);
     }
     __device__ int row_tiles() const { return (p.out_rows + BN - 1) / BN; }
 
     // `u` never decreases from call to call.
     __device__ Unit at(int u) {
-        int per;
+        int per, chunk = 0;
         if (MODE == Product::kWeights) {
             per = row_tiles();
-            e = u / (per * p.num_p);
-            u -= e * per * p.num_p;
+            const int g = u / (per * p.num_p);  // chunk of rows, over all experts
+            while (g >= tiles[e + 1]) ++e;
+            chunk = g - tiles[e];
+            u -= g * per * p.num_p;
         } else {
             while (u >= tiles[e + 1] * p.num_p) ++e;
             u -= tiles[e] * p.num_p;
@@ -150,8 +156,9 @@ struct Units {
         if (MODE == Product::kWeights) {
             t.q0 = q * BN;
             t.qn = min(BN, p.out_rows - t.q0);
-            t.c0 = edges[e];
-            t.c1 = edges[e + 1];
+            t.c0 = edges[e] + chunk * p.chunk;
+            t.c1 = min(edges[e + 1], t.c0 + p.chunk);
+            t.slot = tiles[e + 1] - tiles[e] > 1 ? slots[e] + chunk : -1;
         } else {
             t.q0 = edges[e] + q * BN;
             t.qn = min(BN, edges[e + 1] - t.q0);
@@ -329,6 +336,24 @@ __device__ __forceinline__ void store_part(const LinearTcParams &p, const CUtens
     }
 }
 
+// One chunk's sums of a unit, as they are: a warp's columns as rows of 32
+// neighbouring features.
+template <int BN>
+__device__ __forceinline__ void store_sums(float *out, int cols, uint32_t acc, int c0, int end, int f, int lane) {
+    const bool mine = f + lane < cols;
+    out += (int64_t)c0 * cols + f + lane;
+#pragma unroll 1
+    for (int c = c0; c < end; c += lt::EPI_ROWS) {
+        uint32_t r[8];
+        __syncwarp();
+        tmem_ld_8_issue(acc + (uint32_t)c, r);
+        tmem_ld_8_wait(r);
+#pragma unroll
+        for (int j = 0; j < lt::EPI_ROWS; ++j, out += cols)
+            if (mine && c + j < end) *out = __uint_as_float(r[j]);
+    }
+}
+
 // A value that all lanes of a converged warp hold, in a uniform register.
 __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
@@ -340,6 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     using C = lt::Cfg<BN, MODE == Product::kWeights>;
     constexpr bool A_MN = MODE != Product::kForward, B_MN = MODE == Product::kWeights;
     constexpr bool RELAY = MODE == Product::kWeights;  // rows may have to be cleared before the MMA
+    constexpr bool WEIGHTS = MODE == Product::kWeights;
     static_assert(!B_MN || BN >= 128, "an N-contiguous operand comes in chunks of 64 per CTA");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
@@ -349,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     auto bar = [&](int i) { return smem_addr(bars + i); };
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + C::NUM_BARS);
     int *edges = reinterpret_cast<int *>(smem + C::TABLE_BASE);
-    int *tiles = edges + p.n_experts + 2;
+    int *tiles = edges + p.n_experts + 2, *slots = tiles + p.n_experts + 2;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
@@ -382,11 +408,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     // this call's status word: a wait of this launch runs out two seconds from
     // now at the earliest, long after the first block has cleared it
     if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
-    if (warp == 0) fill_tables<BN>(p.offsets, p.n_experts, p.m, edges, tiles, lane);
+    if (warp == 0) fill_tables(p.offsets, p.n_experts, p.m, WEIGHTS ? p.chunk : BN, edges, tiles, WEIGHTS ? slots : nullptr, lane);
     cluster_sync();  // barriers, tensor memory and tables exist in both CTAs
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    Units<MODE, BN> units(p, edges, tiles);
+    Units<MODE, BN> units(p, edges, tiles, slots);
 
     if (warp < lt::EPI_WARPS) {
         // ------------------------------------------------------------ epilogue
@@ -416,7 +442,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                 tc_fence_after();
             }
             const uint32_t acc = tmem_base + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
-            if (MODE == Product::kWeights && p.wide) {
+            if (MODE == Product::kWeights && t.slot >= 0) {
+                if (fin.c0 < fin.end)
+                    store_sums<BN>(p.partial + ((int64_t)t.slot * p.out_rows + t.q0) * p.cols, p.cols, acc, fin.c0, fin.end,
+                                   f, lane);
+            } else if (MODE == Product::kWeights && p.wide) {
                 const int fc = t.p0 + rank * lt::BP_CTA;
                 if (fin.c0 < fin.end && fc < p.cols)
                     store_part<T>(p, &tmOut, smem + C::STAGING_BASE + part * 2 * lt::STORE_BYTES, ring,
@@ -672,7 +702,8 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
     if (!ok) return cudaErrorInvalidValue;
 
     // at most one unit per row tile, expert and feature tile
-    const int64_t row_tiles = MODE == Product::kWeights ? (sh.n + BN - 1) / BN * sh.n_experts
+    const int64_t row_tiles = MODE == Product::kWeights
+                                  ? (sh.n + BN - 1) / BN * (sh.n_experts + sh.m / p.chunk + 1)
                                                         : (sh.m + BN - 1) / BN + (sh.offsets ? sh.n_experts : 0);
     const int64_t most = device_sm_count() / 2, units = row_tiles * p.num_p;
     const unsigned pairs = (unsigned)(units < most ? units : most);
@@ -687,6 +718,21 @@ cudaError_t launch_typed(const LinearShape &sh, const Product16 &g, const Linear
 
 }  // namespace
 
+WeightsSplit weights_split(int64_t m, int64_t n, int64_t k, int64_t n_experts) {
+    constexpr int64_t longest = 32768, shortest = 512;
+    // output tiles of all experts, and how many chunks of an expert's average
+    // rows would give every pair of SMs a unit (152 of them on a GB300)
+    const int64_t tiles = (n + 127) / 128 * ((k + lt::BP - 1) / lt::BP) * n_experts, pairs = 76;
+    int64_t chunk = longest;
+    if (2 * tiles <= pairs) {
+        const int64_t parts = pairs / tiles, average = m / n_experts;
+        chunk = align_up((average + parts - 1) / parts, lt::BK);
+        chunk = chunk < shortest ? shortest : chunk > longest ? longest : chunk;
+    }
+    // an expert of several chunks has at most twice as many as its rows fill
+    return {(int)chunk, m > chunk ? (n_experts == 1 ? (m + chunk - 1) / chunk : 2 * m / chunk) : 0};
+}
+
 cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product16 &g, uint32_t *status, bool clear,
                              cudaStream_t s) {
     LinearTcParams p{};
@@ -696,6 +742,8 @@ cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product1
     p.cols = (int)(mode == Product::kForward ? sh.n : sh.k);
     p.num_p = (p.cols + lt::BP - 1) / lt::BP;
     p.out_rows = (int)sh.n;
+    p.chunk = weights_split(sh.m, sh.n, sh.k, sh.n_experts).chunk;
+    p.partial = g.partial;
     p.contraction = (int)(mode == Product::kForward ? sh.k : sh.n);
     p.bias = g.bias;
     p.residual = g.residual;
@@ -720,7 +768,7 @@ cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product1
     // and 8.2 as chosen).
     const int64_t pairs = device_sm_count() / 2;
     auto one_round = [&](int64_t bn) {
-        const int64_t tiles = mode == Product::kWeights ? (sh.n + bn - 1) / bn * sh.n_experts
+        const int64_t tiles = mode == Product::kWeights ? (sh.n + bn - 1) / bn * (sh.n_experts + sh.m / p.chunk)
                                                         : (sh.m + bn - 1) / bn + (sh.offsets ? sh.n_experts : 0);
         return tiles * p.num_p <= pairs;
     };

@@ -536,7 +536,7 @@ int threads_per_row_log2(int64_t units) {
     int best = log2_at_least(units, 8);
     for (int l = best - 1; l >= 5; --l) {
         const auto used = [&](int k) { return ((units + (1 << k) - 1) >> k) << k; };
-        if (used(l) < used(best)) best = l;
+        if (used(l) < used(best) && (used(l) >> l) <= 65535) best = l;  // blocks of a grid's second dimension
     }
     return best;
 }

@@ -410,3 +410,44 @@ def test_a_starved_pipeline_reports_a_timeout_and_the_next_call_works(gpu_lib, m
     assert gpu_lib.kmeans_device_status(wf) == gpu_lib.KMEANS_OK == gpu_lib.kmeans_device_status(wg)
     for a, b in zip(got, ref):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("m,n,k", [(9_000_000, 16, 8), (200_000, 72, 40), (20_000, 512, 520), (3000, 33, 17)])
+def test_the_weight_gradient_of_many_rows_keeps_its_bits(gpu_lib, m, n, k):
+    """Sums over many rows: the accumulator's cut-off (up to 2^-23 of the running
+    sum in each of its additions, 16 rows at a time) may not add up over all of
+    them.  At most 32768 rows share an accumulator, so 2048 additions lose up to
+    2^-12 of the largest running sum, which is the sum itself where it grows and
+    within six standard deviations of the walk, the root of the sum of the
+    products' squares, where it wanders; the result's rounding to 8 bits is up to
+    2^-8 of it.  The forward pass of as many rows is checked beside it."""
+    x, dy = normal((m, k), torch.bfloat16, 1), normal((m, n), torch.bfloat16, 2)
+    x[:, 0] = x[:, 0].abs()  # sums that grow with the rows, next to ones that wander
+    dy[:, 0] = dy[:, 0].abs()
+    w = normal((n, k), torch.bfloat16, 3)
+    ws = gpu_lib.linear_workspace(gpu_lib.OP_LINEAR_GRAD, m, n, k)
+    dx, dw, db = gpu_lib.kmeans_linear_grad(dy, x, w, ws=ws)
+    assert gpu_lib.kmeans_device_status(ws) == gpu_lib.KMEANS_OK
+    def sums(f):
+        return sum(f(dy[a:a + (1 << 20)].double(), x[a:a + (1 << 20)].double()) for a in range(0, m, 1 << 20))
+
+    for got, exact, squares in ((dw, sums(lambda g, v: g.t() @ v), sums(lambda g, v: (g * g).t() @ (v * v))),
+                                (db, sums(lambda g, v: g.sum(0)), sums(lambda g, v: (g * g).sum(0)))):
+        bound = 2.0 ** -8 * exact.abs() + 2.0 ** -12 * (exact.abs() + 6 * squares.sqrt())
+        assert bool(((got.double() - exact).abs() <= bound).all())
+    last = slice(m - 500, m)
+    within(dx[last], dy[last].double() @ w.double(), dy[last].double().abs() @ w.double().abs(), steps_for(n),
+           torch.bfloat16)
+    y, _ = gpu_lib.kmeans_linear(x, w)
+    within(y[last], x[last].double() @ w.double().t(), x[last].double().abs() @ w.double().abs().t(), steps_for(k),
+           torch.bfloat16)
+    again = gpu_lib.kmeans_linear_grad(dy, x, w, need_dx=False, ws=ws)
+    assert torch.equal(again[1], dw) and torch.equal(again[2], db)
+
+
+def test_experts_of_one_and_of_several_chunks_of_rows(gpu_lib):
+    # few output tiles: chunks are short here, so some experts take several
+    counts = np.array([5000, 0, 300, 700, 1, 2600])
+    m = int(counts.sum()) + 40
+    x, dy = normal((m, 24), torch.float16, 1), normal((m, 40), torch.float16, 2)
+    check_gradient(gpu_lib, dy, x, normal((6, 40, 24), torch.float16, 3), None, as_offsets(counts), "none")
