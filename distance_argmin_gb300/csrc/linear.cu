@@ -330,7 +330,17 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
                           span16(dy, sh.m, lddy, sh.n), static_cast<const T *>(pre), span16(pre, sh.m, sh.n, sh.n),
                           sh.offsets, sh.n_experts, sh.m, sh.n, slope_rows(sh.m, sh.n), activation, dz, ldz, partial,
                           call.first());
-        if (e == cudaSuccess && db)
+        // Few row tiles per expert are joined by the weight gradient's epilogue
+        // warps, which have nothing to do yet when it starts (ragged gradient:
+        // 6.5 us of a launch of its own); many by a kernel with a thread each.
+        const int rows = slope_rows(sh.m, sh.n);
+        const bool on_the_side = dw && db && sh.m / rows <= 16 * (int64_t)sh.n_experts;
+        if (on_the_side) {
+            g.db = db;
+            g.bias_sums = partial;
+            g.bias_rows = rows;
+        }
+        if (e == cudaSuccess && db && !on_the_side)
             e = launch_kernel(true, linear_bias_join_kernel<T>,
                               dim3((unsigned)((sh.n + kSlopeThreads - 1) / kSlopeThreads), (unsigned)sh.n_experts),
                               dim3(kSlopeThreads), 0, s, static_cast<const float *>(partial), sh.offsets, sh.m, sh.n,

@@ -31,6 +31,9 @@ struct Product16 {
     int activation;
     void *out, *pre;
     float *partial;           // weights: the chunks' sums (see WeightsSplit)
+    void *db;                 // weights: the bias gradient, joined on the side from
+    const float *bias_sums;   // the sums of `bias_rows` rows each (null: not here)
+    int bias_rows;
 };
 
 // f applied with the activation as a compile-time constant: one branch around

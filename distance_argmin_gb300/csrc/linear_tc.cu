@@ -81,11 +81,11 @@ struct Cfg {
     static constexpr int TMEM_COLS = 2 * BN;  // >= 64
     static constexpr int FULL = 0, READY = STAGES, EMPTY = 2 * STAGES, T_FULL = 3 * STAGES, T_EMPTY = T_FULL + 2,
                          DRAIN = T_EMPTY + 2, NUM_BARS = DRAIN + 1;
-    static constexpr int smem_bytes_most() { return TABLE_BASE + 3 * (KMEANS_LINEAR_MAX_EXPERTS + 2) * 4 + 1024; }
-    static constexpr int smem_bytes(int n_experts) { return TABLE_BASE + (STORES ? 3 : 2) * (n_experts + 2) * 4 + 1024; }
+    static constexpr int TABLES = STORES ? 5 : 2;  // of the experts, see the kernel
+    static constexpr int smem_bytes(int n_experts) { return TABLE_BASE + TABLES * (n_experts + 2) * 4 + 1024; }
     static_assert(NUM_BARS * 8 + 16 <= BAR_BYTES, "barriers fit");
     static_assert(STAGE % 1024 == 0 && STAGING % 1024 == 0, "stages stay 1 KiB aligned");
-    static_assert(smem_bytes_most() <= SMEM_LIMIT, "fits");
+    static_assert(TABLE_BASE + TABLES * (KMEANS_LINEAR_MAX_EXPERTS + 2) * 4 + 1024 <= SMEM_LIMIT, "fits");
 };
 }  // namespace lt
 
@@ -98,6 +98,9 @@ struct LinearTcParams {
     int out_rows;     // weights: output features of an expert
     int chunk;        // weights: rows of a unit's contraction at most
     float *partial;
+    void *db;         // weights: the bias gradient and the sums it is joined from
+    const float *bias_sums;
+    int bias_rows;
     int contraction;  // forward, rows
     const void *bias, *residual;
     int64_t ldr;
@@ -375,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     auto bar = [&](int i) { return smem_addr(bars + i); };
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + C::NUM_BARS);
     int *edges = reinterpret_cast<int *>(smem + C::TABLE_BASE);
-    int *tiles = edges + p.n_experts + 2, *slots = tiles + p.n_experts + 2;
+    int *tiles = edges + p.n_experts + 2, *slots = tiles + p.n_experts + 2, *bias_tiles = slots + p.n_experts + 2;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
@@ -409,6 +412,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     // now at the earliest, long after the first block has cleared it
     if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
     if (warp == 0) fill_tables(p.offsets, p.n_experts, p.m, WEIGHTS ? p.chunk : BN, edges, tiles, WEIGHTS ? slots : nullptr, lane);
+    if (WEIGHTS && p.db && warp == 1)  // (the second table is a copy of the edges)
+        fill_tables(p.offsets, p.n_experts, p.m, p.bias_rows, bias_tiles + p.n_experts + 2, bias_tiles, nullptr, lane);
     cluster_sync();  // barriers, tensor memory and tables exist in both CTAs
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
@@ -419,6 +424,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
         const int quarter = warp & 3, part = warp >> 2;
         using F = Finish<MODE, BN, T>;
         F fin{p, reinterpret_cast<float *>(smem + C::STAGING_BASE) + warp * lt::EPI_ROWS * lt::EPI_PITCH, lane};
+        if (WEIGHTS && p.db) {
+            // while the first units are on their way: the bias gradient, an
+            // expert's row tiles added in order
+            const int64_t count = (int64_t)p.n_experts * p.out_rows;
+            for (int64_t i = (int64_t)blockIdx.x * (lt::EPI_WARPS * 32) + threadIdx.x; i < count;
+                 i += (int64_t)gridDim.x * (lt::EPI_WARPS * 32)) {
+                const int e = (int)(i / p.out_rows), col = (int)(i - (int64_t)e * p.out_rows);
+                float s = 0.f;
+#pragma unroll 8
+                for (int tile = bias_tiles[e]; tile < bias_tiles[e + 1]; ++tile)
+                    s += p.bias_sums[(int64_t)tile * p.out_rows + col];
+                static_cast<T *>(p.db)[i] = narrow<T>(s);
+            }
+            __syncwarp();
+        }
         int use = 0, ring = 0;
         for (int u = pair; u < units.total; u += num_pairs) {
             const Unit t = units.at(u);
@@ -744,6 +764,9 @@ cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product1
     p.out_rows = (int)sh.n;
     p.chunk = weights_split(sh.m, sh.n, sh.k, sh.n_experts).chunk;
     p.partial = g.partial;
+    p.db = g.db;
+    p.bias_sums = g.bias_sums;
+    p.bias_rows = g.bias_rows;
     p.contraction = (int)(mode == Product::kForward ? sh.k : sh.n);
     p.bias = g.bias;
     p.residual = g.residual;
