@@ -341,81 +341,100 @@ __global__ void __launch_bounds__(kMoveThreads) route_gather_kernel(const MovePa
     }
 }
 
-constexpr int kCombineUnroll = 4;  // choices whose rows are in flight together
+constexpr int kInFlight = 4;  // rows' pieces that a thread of the combine has on their way
 
-template <bool WHOLE, typename T>
+// A thread has U pieces of its token and the rows of kInFlight / U choices in
+// flight: few choices leave room for several pieces (one at a time, 65536
+// tokens of one choice, d = 2048 float32, took 398 us, 4.0 TB/s).
+template <bool WHOLE, typename T, int U>
 __global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveParams p, const uint8_t *ys, Span in,
                                                                      const float *__restrict__ weights,
                                                                      const uint8_t *residual, int64_t pitch, Span res_in,
                                                                      uint8_t *y) {
     using P = Piece<T>;
+    constexpr int CH = kInFlight / U;
     griddep_wait();
     const int tpr = 1 << p.tpr_log2;
     const int sub = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (kMoveThreads >> p.tpr_log2) + (threadIdx.x >> p.tpr_log2);
-    const int v = (int)blockIdx.y * tpr + sub;
-    const bool live = t < p.n && v < p.pieces;
-    if (WHOLE && !live) return;
-    const int bytes = (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16);
+    const int v0 = (int)blockIdx.y * (tpr * U) + sub;
+    const bool live = t < p.n;
+    if (WHOLE && (!live || v0 >= p.pieces)) return;
     const int kept = p.topk > 0 ? p.offsets[p.n_experts] : 0;
     const int64_t limit = kept < p.slots ? kept : p.slots;
-    float acc[P::V];
+    bool here[U];
+    int bytes[U];
+    P res[U];
 #pragma unroll
-    for (int i = 0; i < P::V; ++i) acc[i] = 0.f;
-    if (live) {
-        for (int j0 = 0; j0 < p.topk; j0 += kCombineUnroll) {
-            P part[kCombineUnroll];
-            float w[kCombineUnroll];
-            bool on[kCombineUnroll];
-#pragma unroll
-            for (int u = 0; u < kCombineUnroll; ++u) {
-                const int j = j0 + u;
-                const int r = j < p.topk ? p.rows[t * p.topk + j] : -1;
-                on[u] = r >= 0 && r < limit;
-                if (on[u]) {
-                    w[u] = weights ? weights[t * p.topk + j] : 1.f;
-                    part[u].w = load_piece<WHOLE>(ys + r * p.row_bytes + (int64_t)v * 16, bytes, in);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kCombineUnroll; ++u)
-                if (on[u]) {
-                    float f[P::V];
-                    part[u].to_floats(f);
-#pragma unroll
-                    for (int i = 0; i < P::V; ++i) acc[i] = fmaf(w[u], f[i], acc[i]);
-                }
-        }
-        if (residual) {
-            P res;
-            res.w = load_piece<WHOLE>(residual + t * pitch + (int64_t)v * 16, bytes, res_in);
-            float f[P::V];
-            res.to_floats(f);
-#pragma unroll
-            for (int i = 0; i < P::V; ++i) acc[i] += f[i];
-        }
+    for (int u = 0; u < U; ++u) {
+        const int v = v0 + u * tpr;
+        here[u] = live && v < p.pieces;
+        bytes[u] = (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16);
+        if (residual && here[u]) res[u].w = load_piece<WHOLE>(residual + t * pitch + (int64_t)v * 16, bytes[u], res_in);
     }
-    const P out = P::from_floats(acc);
-    uint4 prev = make_uint4(0, 0, 0, 0);
-    if (!WHOLE) prev = left_neighbour(out.w);
-    if (live)
-        store_piece<WHOLE>(y + t * p.row_bytes + (int64_t)v * 16, out.w, bytes, prev, sub > 0 && lane > 0,
-                           sub + 1 < tpr && lane < 31 && v + 1 < p.pieces);
+    float acc[U][P::V];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < P::V; ++i) acc[u][i] = 0.f;
+    for (int j0 = 0; live && j0 < p.topk; j0 += CH) {
+        P part[CH][U];
+        float w[CH];
+        bool on[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int j = j0 + c;
+            const int r = j < p.topk ? p.rows[t * p.topk + j] : -1;
+            on[c] = r >= 0 && r < limit;
+            if (!on[c]) continue;
+            w[c] = weights ? weights[t * p.topk + j] : 1.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (here[u])
+                    part[c][u].w = load_piece<WHOLE>(ys + r * p.row_bytes + (int64_t)(v0 + u * tpr) * 16, bytes[u], in);
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (on[c])
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float f[P::V];
+                    part[c][u].to_floats(f);
+#pragma unroll
+                    for (int i = 0; i < P::V; ++i) acc[u][i] = fmaf(w[c], f[i], acc[u][i]);
+                }
+    }
+    if (!WHOLE) __syncwarp();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (residual) {
+            float f[P::V];
+            res[u].to_floats(f);
+#pragma unroll
+            for (int i = 0; i < P::V; ++i) acc[u][i] += f[i];
+        }
+        const P out = P::from_floats(acc[u]);
+        uint4 prev = make_uint4(0, 0, 0, 0);
+        if (!WHOLE) prev = left_neighbour(out.w);
+        if (here[u])
+            store_piece<WHOLE>(y + t * p.row_bytes + (int64_t)(v0 + u * tpr) * 16, out.w, bytes[u], prev,
+                               sub > 0 && lane > 0, sub + 1 < tpr && lane < 31 && v0 + u * tpr + 1 < p.pieces);
+    }
 }
 
 constexpr int64_t kManyTokens = 152 * 16;
-constexpr int kGradChoices = 8;  // choices whose products a thread sums in one walk along the row
 
-// A group of tpr threads per token walks the row; a block whose groups are
-// wider than a warp joins the warps' sums in shared memory.  The pieces are
-// the same whatever the alignment, so the sums have one order.
-template <bool WHOLE, typename T>
+// A group of tpr threads per token walks the row, CH choices at a time and U
+// pieces of each in flight; a block whose groups are wider than a warp joins
+// the warps' sums in shared memory.  The pieces and their order are the same
+// whatever the alignment, so the sums have one order.
+template <bool WHOLE, typename T, int CH, int U>
 __global__ void __launch_bounds__(kMoveThreads) route_combine_grad_kernel(const MoveParams p, const uint8_t *dy,
                                                                           int64_t pitch, Span dy_in, const uint8_t *ys,
                                                                           Span in, const float *__restrict__ weights,
                                                                           uint8_t *dys, float *__restrict__ dweights) {
     using P = Piece<T>;
-    __shared__ float part[kGradChoices][kMoveThreads / 32];
+    __shared__ float part[CH][kMoveThreads / 32];
     griddep_wait();
     const int tpr = 1 << p.tpr_log2;
     const int64_t t = (int64_t)blockIdx.x * (kMoveThreads >> p.tpr_log2) + (threadIdx.x >> p.tpr_log2);
@@ -423,75 +442,85 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_grad_kernel(const 
     const bool live = t < p.n;
     const int kept = p.offsets[p.n_experts];
     const int64_t limit = kept < p.slots ? kept : p.slots;
-    for (int j0 = 0; j0 < p.topk; j0 += kGradChoices) {
-        float sum[kGradChoices], w[kGradChoices];
-        int row[kGradChoices];
+    for (int j0 = 0; j0 < p.topk; j0 += CH) {
+        float sum[CH], w[CH];
+        int row[CH];
 #pragma unroll
-        for (int u = 0; u < kGradChoices; ++u) {
-            const int j = j0 + u;
-            sum[u] = 0.f;
-            row[u] = live && j < p.topk ? p.rows[t * p.topk + j] : -1;
-            w[u] = row[u] >= 0 ? weights[t * p.topk + j] : 0.f;
-            if (row[u] >= p.slots) row[u] = -1;
+        for (int c = 0; c < CH; ++c) {
+            const int j = j0 + c;
+            sum[c] = 0.f;
+            row[c] = live && j < p.topk ? p.rows[t * p.topk + j] : -1;
+            w[c] = row[c] >= 0 ? weights[t * p.topk + j] : 0.f;
+            if (row[c] >= p.slots) row[c] = -1;
         }
         // the warp stays together: the stores pass pieces between lanes
-        for (int v0 = sub & ~31; v0 < p.pieces; v0 += tpr) {
-            const int v = v0 + (sub & 31);
-            const bool here = live && v < p.pieces;
-            if (WHOLE && !here) continue;
-            const int bytes = (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16);
-            P g, got[kGradChoices];
-            g.w = make_uint4(0, 0, 0, 0);
-            if (here) g.w = load_piece<WHOLE>(dy + t * pitch + (int64_t)v * 16, bytes, dy_in);
+        for (int v0 = sub & ~31; v0 < p.pieces; v0 += tpr * U) {
+            P g[U], got[CH][U];
+            bool here[U];
+            int bytes[U];
 #pragma unroll
-            for (int u = 0; u < kGradChoices; ++u)
-                if (here && row[u] >= 0 && row[u] < limit)
-                    got[u].w = load_piece<WHOLE>(ys + row[u] * p.row_bytes + (int64_t)v * 16, bytes, in);
-            float gf[P::V];
-            g.to_floats(gf);
+            for (int u = 0; u < U; ++u) {
+                const int v = v0 + (sub & 31) + u * tpr;
+                here[u] = live && v < p.pieces;
+                bytes[u] = (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16);
+                g[u].w = make_uint4(0, 0, 0, 0);
+                if (here[u]) g[u].w = load_piece<WHOLE>(dy + t * pitch + (int64_t)v * 16, bytes[u], dy_in);
 #pragma unroll
-            for (int u = 0; u < kGradChoices; ++u) {
-                const bool on = row[u] >= 0 && row[u] < limit;
-                float f[P::V];
+                for (int c = 0; c < CH; ++c)
+                    if (here[u] && row[c] >= 0 && row[c] < limit)
+                        got[c][u].w = load_piece<WHOLE>(ys + row[c] * p.row_bytes + (int64_t)v * 16, bytes[u], in);
+            }
 #pragma unroll
-                for (int i = 0; i < P::V; ++i) f[i] = on ? w[u] * gf[i] : 0.f;
-                const P out = P::from_floats(f);
-                if (here && on) {
-                    got[u].to_floats(f);
+            for (int u = 0; u < U; ++u) {
+                const int v = v0 + (sub & 31) + u * tpr;
+                float gf[P::V];
+                g[u].to_floats(gf);
 #pragma unroll
-                    for (int i = 0; i < P::V; ++i) sum[u] = fmaf(gf[i], f[i], sum[u]);
+                for (int c = 0; c < CH; ++c) {
+                    const bool on = row[c] >= 0 && row[c] < limit;
+                    float f[P::V];
+#pragma unroll
+                    for (int i = 0; i < P::V; ++i) f[i] = on ? w[c] * gf[i] : 0.f;
+                    const P out = P::from_floats(f);
+                    if (here[u] && on) {
+                        got[c][u].to_floats(f);
+#pragma unroll
+                        for (int i = 0; i < P::V; ++i) sum[c] = fmaf(gf[i], f[i], sum[c]);
+                    }
+                    uint4 prev = out.w;
+                    if (!WHOLE) prev = left_neighbour(out.w);
+                    if (here[u] && row[c] >= 0)
+                        store_piece<WHOLE>(dys + row[c] * p.row_bytes + (int64_t)v * 16, out.w, bytes[u], prev,
+                                           sub > 0 && lane > 0, sub + 1 < tpr && lane < 31 && v + 1 < p.pieces);
+                    if (!WHOLE) __syncwarp();
                 }
-                uint4 prev = out.w;
-                if (!WHOLE) prev = left_neighbour(out.w);
-                if (here && row[u] >= 0)
-                    store_piece<WHOLE>(dys + row[u] * p.row_bytes + (int64_t)v * 16, out.w, bytes, prev,
-                                       sub > 0 && lane > 0, sub + 1 < tpr && lane < 31 && v + 1 < p.pieces);
             }
         }
+        __syncwarp();
 #pragma unroll
-        for (int u = 0; u < kGradChoices; ++u)
-            for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) sum[u] += __shfl_xor_sync(kFull, sum[u], o);
+        for (int c = 0; c < CH; ++c)
+            for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1) sum[c] += __shfl_xor_sync(kFull, sum[c], o);
         if (tpr > 32) {
             __syncthreads();  // the previous choices' sums have been read
             if (lane == 0) {
 #pragma unroll
-                for (int u = 0; u < kGradChoices; ++u) part[u][warp] = sum[u];
+                for (int c = 0; c < CH; ++c) part[c][warp] = sum[c];
             }
             __syncthreads();
             const int first = (threadIdx.x >> p.tpr_log2) * (tpr / 32);
             if (sub == 0) {
 #pragma unroll
-                for (int u = 0; u < kGradChoices; ++u) {
+                for (int c = 0; c < CH; ++c) {
                     float s = 0.f;
-                    for (int i = 0; i < tpr / 32; ++i) s += part[u][first + i];
-                    sum[u] = s;
+                    for (int i = 0; i < tpr / 32; ++i) s += part[c][first + i];
+                    sum[c] = s;
                 }
             }
         }
         if (live && sub == 0) {
 #pragma unroll
-            for (int u = 0; u < kGradChoices; ++u)
-                if (j0 + u < p.topk) dweights[t * p.topk + j0 + u] = sum[u];
+            for (int c = 0; c < CH; ++c)
+                if (j0 + c < p.topk) dweights[t * p.topk + j0 + c] = sum[c];
         }
     }
 }
@@ -546,17 +575,49 @@ unsigned row_blocks(const MoveParams &p) {
     return (unsigned)((p.n + per - 1) / per);
 }
 
+// Threads per row of a kernel whose threads take U pieces each; rows of unaligned
+// pieces keep their neighbours in neighbouring lanes.
+int mover_log2(const MoveParams &p, int u, bool whole) {
+    const int64_t units = (p.pieces + u - 1) / u;
+    return whole || units >= 32 ? threads_per_row_log2(units) : log2_at_least(p.pieces, 5);
+}
+
+template <bool WHOLE, typename T, int U>
+cudaError_t combine_as(MoveParams p, const void *ys, const float *weights, const void *residual, int64_t pitch, void *y,
+                       cudaStream_t s) {
+    p.tpr_log2 = mover_log2(p, U, WHOLE);
+    const int per = U << p.tpr_log2;
+    return launch_kernel(true, route_combine_kernel<WHOLE, T, U>,
+                         dim3(row_blocks(p), (unsigned)((p.pieces + per - 1) / per)), dim3(kMoveThreads), 0, s, p,
+                         static_cast<const uint8_t *>(ys), span(ys, p.slots, p.row_bytes, p.row_bytes), weights,
+                         static_cast<const uint8_t *>(residual), pitch, span(residual, p.n, pitch, p.row_bytes),
+                         static_cast<uint8_t *>(y));
+}
+
 template <typename T>
 cudaError_t combine_typed(MoveParams p, const void *ys, const float *weights, const void *residual, int64_t ldr,
                           void *y, cudaStream_t s) {
     const int64_t pitch = ldr * (int64_t)sizeof(T);
-    p.tpr_log2 = threads_per_row_log2(p.pieces);
-    const dim3 grid(row_blocks(p), (unsigned)((p.pieces + (1 << p.tpr_log2) - 1) >> p.tpr_log2));
     const bool whole = whole_rows(p.row_bytes, residual ? pitch : 0, {ys, residual, y});
-    return launch_kernel(true, whole ? route_combine_kernel<true, T> : route_combine_kernel<false, T>, grid,
-                         dim3(kMoveThreads), 0, s, p, static_cast<const uint8_t *>(ys),
-                         span(ys, p.slots, p.row_bytes, p.row_bytes), weights, static_cast<const uint8_t *>(residual),
-                         pitch, span(residual, p.n, pitch, p.row_bytes), static_cast<uint8_t *>(y));
+    // several pieces per thread only where the rows still fill the SMs
+    const bool many = p.n * p.pieces >= 152 * 2048 * 4;
+    if (p.topk > 3 || !many)
+        return whole ? combine_as<true, T, 1>(p, ys, weights, residual, pitch, y, s)
+                     : combine_as<false, T, 1>(p, ys, weights, residual, pitch, y, s);
+    if (p.topk > 1)
+        return whole ? combine_as<true, T, 2>(p, ys, weights, residual, pitch, y, s)
+                     : combine_as<false, T, 2>(p, ys, weights, residual, pitch, y, s);
+    return whole ? combine_as<true, T, 4>(p, ys, weights, residual, pitch, y, s)
+                 : combine_as<false, T, 4>(p, ys, weights, residual, pitch, y, s);
+}
+
+template <bool WHOLE, typename T, int CH, int U>
+cudaError_t combine_grad_as(const MoveParams &p, const void *dy, int64_t pitch, const void *ys, const float *weights,
+                            void *dys, float *dweights, cudaStream_t s) {
+    return launch_kernel(true, route_combine_grad_kernel<WHOLE, T, CH, U>, dim3(row_blocks(p)), dim3(kMoveThreads), 0, s,
+                         p, static_cast<const uint8_t *>(dy), pitch, span(dy, p.n, pitch, p.row_bytes),
+                         static_cast<const uint8_t *>(ys), span(ys, p.slots, p.row_bytes, p.row_bytes), weights,
+                         static_cast<uint8_t *>(dys), dweights);
 }
 
 template <typename T>
@@ -565,13 +626,17 @@ cudaError_t combine_grad_typed(MoveParams p, const void *dy, int64_t lddy, const
     const int64_t pitch = lddy * (int64_t)sizeof(T);
     // a warp per token where there are enough of them: no block-wide join, and
     // the rows of other tokens hide each other's latency (16384 tokens of 8
-    // choices, d = 2048: a block per token 344 us)
+    // choices, d = 2048: a block per token 344 us, 178 so)
     p.tpr_log2 = log2_at_least(p.pieces, p.n >= kManyTokens ? 5 : 8);
     const bool whole = whole_rows(p.row_bytes, pitch, {dy, ys, dys});
-    return launch_kernel(true, whole ? route_combine_grad_kernel<true, T> : route_combine_grad_kernel<false, T>,
-                         dim3(row_blocks(p)), dim3(kMoveThreads), 0, s, p, static_cast<const uint8_t *>(dy), pitch,
-                         span(dy, p.n, pitch, p.row_bytes), static_cast<const uint8_t *>(ys),
-                         span(ys, p.slots, p.row_bytes, p.row_bytes), weights, static_cast<uint8_t *>(dys), dweights);
+    if (p.topk > 4)
+        return whole ? combine_grad_as<true, T, 8, 1>(p, dy, pitch, ys, weights, dys, dweights, s)
+                     : combine_grad_as<false, T, 8, 1>(p, dy, pitch, ys, weights, dys, dweights, s);
+    if (p.topk > 2)
+        return whole ? combine_grad_as<true, T, 4, 2>(p, dy, pitch, ys, weights, dys, dweights, s)
+                     : combine_grad_as<false, T, 4, 2>(p, dy, pitch, ys, weights, dys, dweights, s);
+    return whole ? combine_grad_as<true, T, 2, 4>(p, dy, pitch, ys, weights, dys, dweights, s)
+                 : combine_grad_as<false, T, 2, 4>(p, dy, pitch, ys, weights, dys, dweights, s);
 }
 
 // Most blocks of one cluster: 16 where the device can hold such a cluster (it
@@ -653,10 +718,10 @@ cudaError_t launch_route(const void *experts, int id_bytes, int64_t slots, int n
 cudaError_t launch_route_gather(const RouteRows &r, int dtype, const void *x, int64_t ldx, void *xs, cudaStream_t s) {
     MoveParams p = move_params(r, dtype);
     const int64_t pitch = ldx * elem_bytes(dtype);
-    p.tpr_log2 = threads_per_row_log2((p.pieces + kGatherUnroll - 1) / kGatherUnroll);
+    const bool whole = whole_rows(p.row_bytes, pitch, {x, xs});
+    p.tpr_log2 = mover_log2(p, kGatherUnroll, whole);
     const int per_y = kGatherUnroll << p.tpr_log2;
     const dim3 grid(row_blocks(p), (unsigned)((p.pieces + per_y - 1) / per_y));
-    const bool whole = whole_rows(p.row_bytes, pitch, {x, xs});
     return launch_kernel(true, whole ? route_gather_kernel<true> : route_gather_kernel<false>, grid,
                          dim3(kMoveThreads), 0, s, p, static_cast<const uint8_t *>(x), pitch,
                          span(x, p.n, pitch, p.row_bytes), static_cast<uint8_t *>(xs));
