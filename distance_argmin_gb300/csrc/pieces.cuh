@@ -64,11 +64,6 @@ __device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, uint32_
                       __funnelshift_r(w3, w4, r));
 }
 
-__device__ __forceinline__ uint16_t half_of(const uint4 &v, int i) {
-    const uint32_t w = i < 4 ? (i < 2 ? v.x : v.y) : (i < 6 ? v.z : v.w);
-    return (uint16_t)(w >> ((i & 1) * 16));
-}
-
 // Where a tensor's bytes lie.
 struct Span {
     const uint8_t *lo, *hi;
@@ -102,6 +97,42 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t *p, int bytes, const S
     for (int i = 0; i < 8; ++i)
         if (2 * i < bytes) u[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + 2 * i) << ((i & 1) * 16);
     return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// The sixteen bytes at p, an even address that may lie before or past the
+// tensor: bytes outside it read as zero.
+__device__ __forceinline__ uint4 load_word(const uint8_t *p, const Span &in) {
+    const uint32_t s = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15u;
+    const uint8_t *a = p - s;
+    if (a >= in.lo && a + (s ? 32 : 16) <= in.hi) {
+        const uint4 first = *reinterpret_cast<const uint4 *>(a);
+        return s ? shifted(first, *reinterpret_cast<const uint4 *>(a + 16), s) : first;
+    }
+    uint32_t u[4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (p + 2 * i >= in.lo && p + 2 * i + 2 <= in.hi)
+            u[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + 2 * i) << ((i & 1) * 16);
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Bytes [lo, hi) of the aligned word at p, both even.
+__device__ __forceinline__ void store_word(uint8_t *p, const uint4 &v, int lo, int hi) {
+    if (lo <= 0 && hi >= 16) {
+        *reinterpret_cast<uint4 *>(p) = v;
+        return;
+    }
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool low = 4 * i >= lo && 4 * i + 2 <= hi, high = 4 * i + 2 >= lo && 4 * i + 4 <= hi;
+        if (low && high)
+            *reinterpret_cast<uint32_t *>(p + 4 * i) = u[i];
+        else if (low)
+            *reinterpret_cast<uint16_t *>(p + 4 * i) = (uint16_t)u[i];
+        else if (high)
+            *reinterpret_cast<uint16_t *>(p + 4 * i + 2) = (uint16_t)(u[i] >> 16);
+    }
 }
 
 }  // namespace km

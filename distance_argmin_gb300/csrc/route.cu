@@ -217,13 +217,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
 }
 
 // -------------------------------------------------------------- row movement
-// Rows move in pieces of 16 bytes counted from the row's start; a lane's
-// neighbours hold the neighbouring pieces.  Where every row starts on 16 bytes
-// (WHOLE) a piece is one access.  Otherwise a piece is read as the two aligned
-// 16-byte words it lies in and shifted into place, and written as one aligned
-// word put together from the left neighbour's piece and its own; only the ends
-// of a run of lanes, and words that reach past the tensor, go value by value.
-// (d = 1031 in 16 bits, 4097 tokens of three choices: 31 us a value at a time.)
+// Rows move in words of 16 bytes, neighbouring lanes at neighbouring words.
+// Where every row starts on 16 bytes (WHOLE) a word is one access.  Otherwise the
+// aligned words of the stored row are written, only its two ends in part, and
+// each is put together from the two aligned words of the source that hold it:
+// its shifts and checks then bound the kernels (16384 tokens of 8 choices,
+// d = 2047 bf16 against 2048: gather 144 us, 92; combine 222, 102; gradient 527,
+// 178).  Values one at a time took 31 us for the combine of 4097 tokens of three
+// choices, d = 1031 in 16 bits, words 13; 4-byte words took 20, and words shared
+// between neighbouring lanes by shuffles 19.
 template <typename T>
 struct Piece {
     static constexpr int V = 16 / (int)sizeof(T);
@@ -253,47 +255,11 @@ struct Piece {
     }
 };
 
-// The piece v at p.  Not WHOLE: the whole warp calls it together; `prev` is the
-// left neighbour's piece when `joined` says that it belongs to the same row
-// just before, `next` whether the right neighbour's follows in the same call.
-template <bool WHOLE>
-__device__ __forceinline__ void store_piece(uint8_t *p, const uint4 &v, int bytes, const uint4 &prev, bool joined,
-                                            bool next) {
-    if constexpr (WHOLE) {
-        *reinterpret_cast<uint4 *>(p) = v;
-        return;
-    }
-    const int m = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
-    if (m == 0 && bytes == 16) {
-        *reinterpret_cast<uint4 *>(p) = v;
-        return;
-    }
-    int from = 0;  // bytes of this piece already written with the left neighbour's
-    if (m != 0 && joined && bytes >= 16 - m) {
-        *reinterpret_cast<uint4 *>(p - m) = shifted(prev, v, (uint32_t)(16 - m));
-        from = 16 - m;
-    } else if (m != 0 && joined) {  // a short last piece: the neighbour's end has no word to share
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (2 * i >= 16 - m) *reinterpret_cast<uint16_t *>(p - 16 + 2 * i) = half_of(prev, i);
-    }
-    // with a right neighbour the last m bytes are its to write
-    const int to = next && m != 0 ? 16 - m : bytes;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (2 * i >= from && 2 * i < to) *reinterpret_cast<uint16_t *>(p + 2 * i) = half_of(v, i);
-}
-
-__device__ __forceinline__ uint4 left_neighbour(const uint4 &v) {
-    return make_uint4(__shfl_up_sync(kFull, v.x, 1), __shfl_up_sync(kFull, v.y, 1), __shfl_up_sync(kFull, v.z, 1),
-                      __shfl_up_sync(kFull, v.w, 1));
-}
-
 struct MoveParams {
     const int32_t *rows, *offsets;
     int64_t n, slots;
     int64_t row_bytes;
-    int pieces;  // per row
+    int words;  // 16-byte words that a row takes, at most
     int topk, n_experts;
     int tpr_log2;  // threads per row
 };
@@ -301,51 +267,76 @@ struct MoveParams {
 constexpr int kMoveThreads = 256;
 constexpr int kGatherUnroll = 4;
 
-// xs[row(t, j)] = x[t]; a thread holds up to kGatherUnroll pieces of its token
+// What an aligned word of a stored row takes of the row.
+struct RowWord {
+    int64_t at;  // the word's first byte within the row; negative in the first word
+    int lo, hi;  // the word's bytes that are in the row
+};
+
+template <bool WHOLE>
+__device__ __forceinline__ RowWord row_word(const uint8_t *row, int v, const MoveParams &p) {
+    if (WHOLE) return {(int64_t)v * 16, 0, v < p.words ? 16 : 0};
+    const int m = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
+    const int64_t at = (int64_t)v * 16 - m;
+    return {at, v == 0 ? m : 0, (int)min((int64_t)16, p.row_bytes - at)};
+}
+
+template <bool WHOLE>
+__device__ __forceinline__ uint4 load_16(const uint8_t *p, const Span &in) {
+    if constexpr (WHOLE) return *reinterpret_cast<const uint4 *>(p);
+    return load_word(p, in);
+}
+
+template <bool WHOLE>
+__device__ __forceinline__ void store_16(uint8_t *p, const uint4 &v, const RowWord &at) {
+    if constexpr (WHOLE)
+        *reinterpret_cast<uint4 *>(p) = v;
+    else
+        store_word(p, v, at.lo, at.hi);
+}
+
+// xs[row(t, j)] = x[t]; a thread holds up to kGatherUnroll words of its token
 // and writes them to every choice's row.
 template <bool WHOLE>
 __global__ void __launch_bounds__(kMoveThreads) route_gather_kernel(const MoveParams p, const uint8_t *x,
                                                                     int64_t pitch, Span in, uint8_t *xs) {
     griddep_wait();
     const int tpr = 1 << p.tpr_log2;
-    const int sub = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31;
+    const int sub = threadIdx.x & (tpr - 1);
     const int64_t t = (int64_t)blockIdx.x * (kMoveThreads >> p.tpr_log2) + (threadIdx.x >> p.tpr_log2);
-    const bool live = t < p.n;
-    if (WHOLE && !live) return;
     const int v0 = (int)blockIdx.y * (tpr * kGatherUnroll) + sub;
+    if (t >= p.n || v0 >= p.words) return;
     const int kept = p.offsets[p.n_experts];
-    uint4 val[kGatherUnroll], prev[kGatherUnroll];
-#pragma unroll
-    for (int u = 0; u < kGatherUnroll; ++u) {
-        const int v = v0 + u * tpr;
-        val[u] = make_uint4(0, 0, 0, 0);
-        if (live && v < p.pieces)
-            val[u] = load_piece<WHOLE>(x + t * pitch + (int64_t)v * 16, (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16),
-                                       in);
-        if (!WHOLE) prev[u] = left_neighbour(val[u]);
-    }
-    if (!live) return;
+    const uint8_t *src = x + t * pitch;
     const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 val[kGatherUnroll];
+    if (WHOLE) {  // the same words for every choice
+#pragma unroll
+        for (int u = 0; u < kGatherUnroll; ++u)
+            if (v0 + u * tpr < p.words) val[u] = load_16<true>(src + (int64_t)(v0 + u * tpr) * 16, in);
+    }
     for (int j = 0; j < p.topk; ++j) {
         const int r = p.rows[t * p.topk + j];
         if (r < 0 || r >= p.slots) continue;
         const bool on = r < kept;
+        uint8_t *dst = xs + (int64_t)r * p.row_bytes;
+        RowWord at[kGatherUnroll];
 #pragma unroll
         for (int u = 0; u < kGatherUnroll; ++u) {
-            const int v = v0 + u * tpr;
-            if (v >= p.pieces) continue;
-            store_piece<WHOLE>(xs + (int64_t)r * p.row_bytes + (int64_t)v * 16, on ? val[u] : zero,
-                               (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16), on ? prev[u] : zero,
-                               sub > 0 && lane > 0, sub + 1 < tpr && lane < 31 && v + 1 < p.pieces);
+            at[u] = row_word<WHOLE>(dst, v0 + u * tpr, p);
+            if (!WHOLE && at[u].hi > 0) val[u] = load_16<WHOLE>(src + at[u].at, in);
         }
+#pragma unroll
+        for (int u = 0; u < kGatherUnroll; ++u)
+            if (at[u].hi > 0) store_16<WHOLE>(dst + at[u].at, on ? val[u] : zero, at[u]);
     }
 }
 
-constexpr int kInFlight = 4;  // rows' pieces that a thread of the combine has on their way
+constexpr int kInFlight = 4;  // rows' words that a thread of the combine has on their way
 
-// A thread has U pieces of its token and the rows of kInFlight / U choices in
-// flight: few choices leave room for several pieces (one at a time, 65536
-// tokens of one choice, d = 2048 float32, took 398 us, 4.0 TB/s).
+// A thread has U words of its token and the rows of kInFlight / U choices in
+// flight: few choices leave room for several words (one at a time, 65536
+// tokens of one choice, d = 2048 float32, took 398 us, 4.0 TB/s; four, 239).
 template <bool WHOLE, typename T, int U>
 __global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveParams p, const uint8_t *ys, Span in,
                                                                      const float *__restrict__ weights,
@@ -355,29 +346,26 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveP
     constexpr int CH = kInFlight / U;
     griddep_wait();
     const int tpr = 1 << p.tpr_log2;
-    const int sub = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31;
+    const int sub = threadIdx.x & (tpr - 1);
     const int64_t t = (int64_t)blockIdx.x * (kMoveThreads >> p.tpr_log2) + (threadIdx.x >> p.tpr_log2);
     const int v0 = (int)blockIdx.y * (tpr * U) + sub;
-    const bool live = t < p.n;
-    if (WHOLE && (!live || v0 >= p.pieces)) return;
+    if (t >= p.n || v0 >= p.words) return;
     const int kept = p.topk > 0 ? p.offsets[p.n_experts] : 0;
     const int64_t limit = kept < p.slots ? kept : p.slots;
-    bool here[U];
-    int bytes[U];
+    uint8_t *dst = y + t * p.row_bytes;
+    RowWord at[U];
     P res[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int v = v0 + u * tpr;
-        here[u] = live && v < p.pieces;
-        bytes[u] = (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16);
-        if (residual && here[u]) res[u].w = load_piece<WHOLE>(residual + t * pitch + (int64_t)v * 16, bytes[u], res_in);
+        at[u] = row_word<WHOLE>(dst, v0 + u * tpr, p);
+        if (residual && at[u].hi > 0) res[u].w = load_16<WHOLE>(residual + t * pitch + at[u].at, res_in);
     }
     float acc[U][P::V];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < P::V; ++i) acc[u][i] = 0.f;
-    for (int j0 = 0; live && j0 < p.topk; j0 += CH) {
+    for (int j0 = 0; j0 < p.topk; j0 += CH) {
         P part[CH][U];
         float w[CH];
         bool on[CH];
@@ -390,8 +378,7 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveP
             w[c] = weights ? weights[t * p.topk + j] : 1.f;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (here[u])
-                    part[c][u].w = load_piece<WHOLE>(ys + r * p.row_bytes + (int64_t)(v0 + u * tpr) * 16, bytes[u], in);
+                if (at[u].hi > 0) part[c][u].w = load_16<WHOLE>(ys + r * p.row_bytes + at[u].at, in);
         }
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -404,21 +391,16 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveP
                     for (int i = 0; i < P::V; ++i) acc[u][i] = fmaf(w[c], f[i], acc[u][i]);
                 }
     }
-    if (!WHOLE) __syncwarp();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        if (at[u].hi <= 0) continue;
         if (residual) {
             float f[P::V];
             res[u].to_floats(f);
 #pragma unroll
             for (int i = 0; i < P::V; ++i) acc[u][i] += f[i];
         }
-        const P out = P::from_floats(acc[u]);
-        uint4 prev = make_uint4(0, 0, 0, 0);
-        if (!WHOLE) prev = left_neighbour(out.w);
-        if (here[u])
-            store_piece<WHOLE>(y + t * p.row_bytes + (int64_t)(v0 + u * tpr) * 16, out.w, bytes[u], prev,
-                               sub > 0 && lane > 0, sub + 1 < tpr && lane < 31 && v0 + u * tpr + 1 < p.pieces);
+        store_16<WHOLE>(dst + at[u].at, P::from_floats(acc[u]).w, at[u]);
     }
 }
 
@@ -426,10 +408,10 @@ constexpr int64_t kManyTokens = 152 * 16;
 
 // A group of tpr threads per token walks the row, CH choices at a time and U
 // pieces of each in flight; a block whose groups are wider than a warp joins
-// the warps' sums in shared memory.  The pieces and their order are the same
-// whatever the alignment, so the sums have one order.
+// the warps' sums in shared memory.  The sums run over dy's pieces whatever the
+// alignment, so that they have one order.
 template <bool WHOLE, typename T, int CH, int U>
-__global__ void __launch_bounds__(kMoveThreads) route_combine_grad_kernel(const MoveParams p, const uint8_t *dy,
+__global__ void __launch_bounds__(kMoveThreads, 2) route_combine_grad_kernel(const MoveParams p, const uint8_t *dy,
                                                                           int64_t pitch, Span dy_in, const uint8_t *ys,
                                                                           Span in, const float *__restrict__ weights,
                                                                           uint8_t *dys, float *__restrict__ dweights) {
@@ -453,46 +435,46 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_grad_kernel(const 
             w[c] = row[c] >= 0 ? weights[t * p.topk + j] : 0.f;
             if (row[c] >= p.slots) row[c] = -1;
         }
-        // the warp stays together: the stores pass pieces between lanes
-        for (int v0 = sub & ~31; v0 < p.pieces; v0 += tpr * U) {
+        for (int v0 = sub; live && v0 < p.words; v0 += tpr * U) {
             P g[U], got[CH][U];
             bool here[U];
-            int bytes[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int v = v0 + (sub & 31) + u * tpr;
-                here[u] = live && v < p.pieces;
-                bytes[u] = (int)min((int64_t)16, p.row_bytes - (int64_t)v * 16);
-                g[u].w = make_uint4(0, 0, 0, 0);
-                if (here[u]) g[u].w = load_piece<WHOLE>(dy + t * pitch + (int64_t)v * 16, bytes[u], dy_in);
+                const int64_t at = (int64_t)(v0 + u * tpr) * 16;
+                const int bytes = (int)min((int64_t)16, p.row_bytes - at);
+                here[u] = bytes > 0;
+                if (!here[u]) continue;
+                g[u].w = load_piece<WHOLE>(dy + t * pitch + at, bytes, dy_in);
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
-                    if (here[u] && row[c] >= 0 && row[c] < limit)
-                        got[c][u].w = load_piece<WHOLE>(ys + row[c] * p.row_bytes + (int64_t)v * 16, bytes[u], in);
+                    if (row[c] >= 0 && row[c] < limit)
+                        got[c][u].w = load_piece<WHOLE>(ys + row[c] * p.row_bytes + at, bytes, in);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int v = v0 + (sub & 31) + u * tpr;
-                float gf[P::V];
+                float gf[P::V], f[P::V];
                 g[u].to_floats(gf);
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     const bool on = row[c] >= 0 && row[c] < limit;
-                    float f[P::V];
-#pragma unroll
-                    for (int i = 0; i < P::V; ++i) f[i] = on ? w[c] * gf[i] : 0.f;
-                    const P out = P::from_floats(f);
                     if (here[u] && on) {
                         got[c][u].to_floats(f);
 #pragma unroll
                         for (int i = 0; i < P::V; ++i) sum[c] = fmaf(gf[i], f[i], sum[c]);
                     }
-                    uint4 prev = out.w;
-                    if (!WHOLE) prev = left_neighbour(out.w);
-                    if (here[u] && row[c] >= 0)
-                        store_piece<WHOLE>(dys + row[c] * p.row_bytes + (int64_t)v * 16, out.w, bytes[u], prev,
-                                           sub > 0 && lane > 0, sub + 1 < tpr && lane < 31 && v + 1 < p.pieces);
-                    if (!WHOLE) __syncwarp();
+                    if (row[c] < 0) continue;
+                    uint8_t *dst = dys + row[c] * p.row_bytes;
+                    const RowWord to = row_word<WHOLE>(dst, v0 + u * tpr, p);
+                    if (to.hi <= 0) continue;
+                    if (WHOLE) {
+#pragma unroll
+                        for (int i = 0; i < P::V; ++i) f[i] = gf[i];
+                    } else {
+                        P{load_16<WHOLE>(dy + t * pitch + to.at, dy_in)}.to_floats(f);
+                    }
+#pragma unroll
+                    for (int i = 0; i < P::V; ++i) f[i] = on ? w[c] * f[i] : 0.f;
+                    store_16<WHOLE>(dst + to.at, P::from_floats(f).w, to);
                 }
             }
         }
@@ -545,14 +527,14 @@ int log2_at_least(int64_t v, int most) {
     return l;
 }
 
-MoveParams move_params(const RouteRows &r, int dtype) {
+MoveParams move_params(const RouteRows &r, int bytes_per, bool whole) {
     MoveParams p{};
     p.rows = r.rows;
     p.offsets = r.offsets;
     p.n = r.n;
     p.slots = r.n * r.topk;
-    p.row_bytes = r.d * elem_bytes(dtype);
-    p.pieces = (int)((p.row_bytes + 15) / 16);
+    p.row_bytes = r.d * bytes_per;
+    p.words = (int)((p.row_bytes + (whole ? 15 : 29)) / 16);  // a row may start 14 bytes into a word
     p.topk = r.topk;
     p.n_experts = r.n_experts;
     return p;
@@ -575,68 +557,71 @@ unsigned row_blocks(const MoveParams &p) {
     return (unsigned)((p.n + per - 1) / per);
 }
 
-// Threads per row of a kernel whose threads take U pieces each; rows of unaligned
-// pieces keep their neighbours in neighbouring lanes.
-int mover_log2(const MoveParams &p, int u, bool whole) {
-    const int64_t units = (p.pieces + u - 1) / u;
-    return whole || units >= 32 ? threads_per_row_log2(units) : log2_at_least(p.pieces, 5);
+// A grid over rows of p.words words, `each` to a thread.
+dim3 word_grid(MoveParams &p, int each) {
+    p.tpr_log2 = threads_per_row_log2((p.words + each - 1) / each);
+    const int per = each << p.tpr_log2;
+    return dim3(row_blocks(p), (unsigned)((p.words + per - 1) / per));
 }
 
 template <bool WHOLE, typename T, int U>
 cudaError_t combine_as(MoveParams p, const void *ys, const float *weights, const void *residual, int64_t pitch, void *y,
                        cudaStream_t s) {
-    p.tpr_log2 = mover_log2(p, U, WHOLE);
-    const int per = U << p.tpr_log2;
-    return launch_kernel(true, route_combine_kernel<WHOLE, T, U>,
-                         dim3(row_blocks(p), (unsigned)((p.pieces + per - 1) / per)), dim3(kMoveThreads), 0, s, p,
+    const dim3 grid = word_grid(p, U);
+    return launch_kernel(true, route_combine_kernel<WHOLE, T, U>, grid, dim3(kMoveThreads), 0, s, p,
                          static_cast<const uint8_t *>(ys), span(ys, p.slots, p.row_bytes, p.row_bytes), weights,
                          static_cast<const uint8_t *>(residual), pitch, span(residual, p.n, pitch, p.row_bytes),
                          static_cast<uint8_t *>(y));
 }
 
 template <typename T>
-cudaError_t combine_typed(MoveParams p, const void *ys, const float *weights, const void *residual, int64_t ldr,
+cudaError_t combine_typed(const RouteRows &r, const void *ys, const float *weights, const void *residual, int64_t ldr,
                           void *y, cudaStream_t s) {
-    const int64_t pitch = ldr * (int64_t)sizeof(T);
-    const bool whole = whole_rows(p.row_bytes, residual ? pitch : 0, {ys, residual, y});
-    // several pieces per thread only where the rows still fill the SMs
-    const bool many = p.n * p.pieces >= 152 * 2048 * 4;
-    if (p.topk > 3 || !many)
-        return whole ? combine_as<true, T, 1>(p, ys, weights, residual, pitch, y, s)
-                     : combine_as<false, T, 1>(p, ys, weights, residual, pitch, y, s);
-    if (p.topk > 1)
-        return whole ? combine_as<true, T, 2>(p, ys, weights, residual, pitch, y, s)
-                     : combine_as<false, T, 2>(p, ys, weights, residual, pitch, y, s);
-    return whole ? combine_as<true, T, 4>(p, ys, weights, residual, pitch, y, s)
-                 : combine_as<false, T, 4>(p, ys, weights, residual, pitch, y, s);
+    const int64_t pitch = ldr * (int64_t)sizeof(T), row_bytes = r.d * (int64_t)sizeof(T);
+    const bool whole = whole_rows(row_bytes, residual ? pitch : 0, {ys, residual, y});
+    const MoveParams p = move_params(r, (int)sizeof(T), whole);
+    if (!whole) return combine_as<false, T, 1>(p, ys, weights, residual, pitch, y, s);
+    // several words per thread only where the rows still fill the SMs
+    const bool many = p.n * p.words >= 152 * 2048 * 4;
+    if (p.topk > 3 || !many) return combine_as<true, T, 1>(p, ys, weights, residual, pitch, y, s);
+    if (p.topk > 1) return combine_as<true, T, 2>(p, ys, weights, residual, pitch, y, s);
+    return combine_as<true, T, 4>(p, ys, weights, residual, pitch, y, s);
 }
 
 template <bool WHOLE, typename T, int CH, int U>
-cudaError_t combine_grad_as(const MoveParams &p, const void *dy, int64_t pitch, const void *ys, const float *weights,
+cudaError_t combine_grad_as(const RouteRows &r, const void *dy, int64_t pitch, const void *ys, const float *weights,
                             void *dys, float *dweights, cudaStream_t s) {
+    MoveParams p = move_params(r, (int)sizeof(T), WHOLE);
+    // a warp per token where there are enough of them: no block-wide join, and
+    // the rows of other tokens hide each other's latency (16384 tokens of 8
+    // choices, d = 2048: a block per token 344 us, 178 so)
+    p.tpr_log2 = log2_at_least((p.row_bytes + 15) / 16, p.n >= kManyTokens ? 5 : 8);
     return launch_kernel(true, route_combine_grad_kernel<WHOLE, T, CH, U>, dim3(row_blocks(p)), dim3(kMoveThreads), 0, s,
                          p, static_cast<const uint8_t *>(dy), pitch, span(dy, p.n, pitch, p.row_bytes),
                          static_cast<const uint8_t *>(ys), span(ys, p.slots, p.row_bytes, p.row_bytes), weights,
                          static_cast<uint8_t *>(dys), dweights);
 }
 
+template <bool WHOLE, typename T>
+cudaError_t combine_grad_sized(const RouteRows &r, const void *dy, int64_t pitch, const void *ys, const float *weights,
+                               void *dys, float *dweights, cudaStream_t s) {
+    // a shifted word takes the registers of two (two in flight for each choice:
+    // 16384 tokens of 4 choices, d = 513 float32, 159 us, one 146)
+    constexpr int each = WHOLE ? 2 : 1;
+    if constexpr (WHOLE) {
+        if (r.topk > 4) return combine_grad_as<WHOLE, T, 8, 1>(r, dy, pitch, ys, weights, dys, dweights, s);
+    }
+    if (r.topk > 2) return combine_grad_as<WHOLE, T, 4, each>(r, dy, pitch, ys, weights, dys, dweights, s);
+    return combine_grad_as<WHOLE, T, 2, 2 * each>(r, dy, pitch, ys, weights, dys, dweights, s);
+}
+
 template <typename T>
-cudaError_t combine_grad_typed(MoveParams p, const void *dy, int64_t lddy, const void *ys, const float *weights,
+cudaError_t combine_grad_typed(const RouteRows &r, const void *dy, int64_t lddy, const void *ys, const float *weights,
                                void *dys, float *dweights, cudaStream_t s) {
     const int64_t pitch = lddy * (int64_t)sizeof(T);
-    // a warp per token where there are enough of them: no block-wide join, and
-    // the rows of other tokens hide each other's latency (16384 tokens of 8
-    // choices, d = 2048: a block per token 344 us, 178 so)
-    p.tpr_log2 = log2_at_least(p.pieces, p.n >= kManyTokens ? 5 : 8);
-    const bool whole = whole_rows(p.row_bytes, pitch, {dy, ys, dys});
-    if (p.topk > 4)
-        return whole ? combine_grad_as<true, T, 8, 1>(p, dy, pitch, ys, weights, dys, dweights, s)
-                     : combine_grad_as<false, T, 8, 1>(p, dy, pitch, ys, weights, dys, dweights, s);
-    if (p.topk > 2)
-        return whole ? combine_grad_as<true, T, 4, 2>(p, dy, pitch, ys, weights, dys, dweights, s)
-                     : combine_grad_as<false, T, 4, 2>(p, dy, pitch, ys, weights, dys, dweights, s);
-    return whole ? combine_grad_as<true, T, 2, 4>(p, dy, pitch, ys, weights, dys, dweights, s)
-                 : combine_grad_as<false, T, 2, 4>(p, dy, pitch, ys, weights, dys, dweights, s);
+    return whole_rows(r.d * (int64_t)sizeof(T), pitch, {dy, ys, dys})
+               ? combine_grad_sized<true, T>(r, dy, pitch, ys, weights, dys, dweights, s)
+               : combine_grad_sized<false, T>(r, dy, pitch, ys, weights, dys, dweights, s);
 }
 
 // Most blocks of one cluster: 16 where the device can hold such a cluster (it
@@ -716,12 +701,10 @@ cudaError_t launch_route(const void *experts, int id_bytes, int64_t slots, int n
 }
 
 cudaError_t launch_route_gather(const RouteRows &r, int dtype, const void *x, int64_t ldx, void *xs, cudaStream_t s) {
-    MoveParams p = move_params(r, dtype);
     const int64_t pitch = ldx * elem_bytes(dtype);
-    const bool whole = whole_rows(p.row_bytes, pitch, {x, xs});
-    p.tpr_log2 = mover_log2(p, kGatherUnroll, whole);
-    const int per_y = kGatherUnroll << p.tpr_log2;
-    const dim3 grid(row_blocks(p), (unsigned)((p.pieces + per_y - 1) / per_y));
+    const bool whole = whole_rows(r.d * elem_bytes(dtype), pitch, {x, xs});
+    MoveParams p = move_params(r, elem_bytes(dtype), whole);
+    const dim3 grid = word_grid(p, kGatherUnroll);
     return launch_kernel(true, whole ? route_gather_kernel<true> : route_gather_kernel<false>, grid,
                          dim3(kMoveThreads), 0, s, p, static_cast<const uint8_t *>(x), pitch,
                          span(x, p.n, pitch, p.row_bytes), static_cast<uint8_t *>(xs));
@@ -729,21 +712,19 @@ cudaError_t launch_route_gather(const RouteRows &r, int dtype, const void *x, in
 
 cudaError_t launch_route_combine(const RouteRows &r, int dtype, const void *ys, const float *weights,
                                  const void *residual, int64_t ldr, void *y, cudaStream_t s) {
-    const MoveParams p = move_params(r, dtype);
     switch (dtype) {
-        case KMEANS_F32: return combine_typed<float>(p, ys, weights, residual, ldr, y, s);
-        case KMEANS_F16: return combine_typed<__half>(p, ys, weights, residual, ldr, y, s);
-        default: return combine_typed<__nv_bfloat16>(p, ys, weights, residual, ldr, y, s);
+        case KMEANS_F32: return combine_typed<float>(r, ys, weights, residual, ldr, y, s);
+        case KMEANS_F16: return combine_typed<__half>(r, ys, weights, residual, ldr, y, s);
+        default: return combine_typed<__nv_bfloat16>(r, ys, weights, residual, ldr, y, s);
     }
 }
 
 cudaError_t launch_route_combine_grad(const RouteRows &r, int dtype, const void *dy, int64_t lddy, const void *ys,
                                       const float *weights, void *dys, float *dweights, cudaStream_t s) {
-    const MoveParams p = move_params(r, dtype);
     switch (dtype) {
-        case KMEANS_F32: return combine_grad_typed<float>(p, dy, lddy, ys, weights, dys, dweights, s);
-        case KMEANS_F16: return combine_grad_typed<__half>(p, dy, lddy, ys, weights, dys, dweights, s);
-        default: return combine_grad_typed<__nv_bfloat16>(p, dy, lddy, ys, weights, dys, dweights, s);
+        case KMEANS_F32: return combine_grad_typed<float>(r, dy, lddy, ys, weights, dys, dweights, s);
+        case KMEANS_F16: return combine_grad_typed<__half>(r, dy, lddy, ys, weights, dys, dweights, s);
+        default: return combine_grad_typed<__nv_bfloat16>(r, dy, lddy, ys, weights, dys, dweights, s);
     }
 }
 
