@@ -217,41 +217,83 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
 }
 
 // -------------------------------------------------------------- row movement
-// Rows move in words of 16 bytes, neighbouring lanes at neighbouring words.
-// Where every row starts on 16 bytes (WHOLE) a word is one access.  Otherwise the
-// aligned words of the stored row are written, only its two ends in part, and
-// each is put together from the two aligned words of the source that hold it:
-// its shifts and checks then bound the kernels (16384 tokens of 8 choices,
-// d = 2047 bf16 against 2048: gather 144 us, 92; combine 222, 102; gradient 527,
-// 178).  Values one at a time took 31 us for the combine of 4097 tokens of three
-// choices, d = 1031 in 16 bits, words 13; 4-byte words took 20, and words shared
-// between neighbouring lanes by shuffles 19.
-template <typename T>
-struct Piece {
-    static constexpr int V = 16 / (int)sizeof(T);
-    uint4 w;
+// Rows move in words, neighbouring lanes at neighbouring words.  A word has as
+// many bytes as every stored row is aligned to, VEC = 16, 8 or 4, and is one
+// access (16384 tokens of 4 choices, d = 513 float32, 16-byte words put together
+// by shifts: gather 49 us, combine 66, gradient 146; 4-byte words 33, 49, 78).  Rows of
+// an odd number of 16-bit values (VEC = 2) have words of 16 bytes: the aligned
+// words of the stored row are written, only its two ends in part, and each is put
+// together from the two aligned words of the source that hold it; its shifts and
+// checks then bound the kernels (16384 tokens of 8 choices, d = 2047 bf16 against
+// 2048: gather 144 us, 92; combine 222, 102; gradient 527, 178).  For 4097 tokens
+// of three choices, d = 1031 in 16 bits, the combine takes 13 us so; values one
+// at a time took 31, 4-byte words 20, words shared between neighbouring lanes by
+// shuffles 19.
+template <int VEC>
+constexpr int kWordBytes = VEC == 2 ? 16 : VEC;
+
+template <typename T, int VEC>
+struct Word {
+    static constexpr int N = kWordBytes<VEC> / 4;          // 4-byte parts
+    static constexpr int V = kWordBytes<VEC> / (int)sizeof(T);  // values
+    uint32_t u[N];
     __device__ void to_floats(float (&f)[V]) const {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(u[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < N; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(u[i]);
+            } else {
                 const float2 v = widen2<T>(u[i]);
                 f[2 * i] = v.x;
                 f[2 * i + 1] = v.y;
             }
         }
     }
-    __device__ static Piece from_floats(const float (&f)[V]) {
-        Piece p;
-        if constexpr (sizeof(T) == 4)
-            p.w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-        else
-            p.w = make_uint4(narrow2<T>(f[0], f[1]), narrow2<T>(f[2], f[3]), narrow2<T>(f[4], f[5]),
-                             narrow2<T>(f[6], f[7]));
-        return p;
+    __device__ static Word from_floats(const float (&f)[V]) {
+        Word w;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (sizeof(T) == 4)
+                w.u[i] = __float_as_uint(f[i]);
+            else
+                w.u[i] = narrow2<T>(f[2 * i], f[2 * i + 1]);
+        }
+        return w;
+    }
+    __device__ static Word zero() {
+        Word w;
+#pragma unroll
+        for (int i = 0; i < N; ++i) w.u[i] = 0;
+        return w;
+    }
+    __device__ static Word of(const uint4 &v) {
+        static_assert(N == 4);
+        return {v.x, v.y, v.z, v.w};
+    }
+    // One access of all its bytes, or pieces of `align` bytes.
+    __device__ static Word load(const uint8_t *p, int align = kWordBytes<VEC>) {
+        Word w;
+        if (align >= 4 * N) {
+            if constexpr (N == 4) w = of(*reinterpret_cast<const uint4 *>(p));
+            if constexpr (N == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                w.u[0] = v.x;
+                w.u[1] = v.y;
+            }
+            if constexpr (N == 1) w.u[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else if (align >= 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w.u[i] = reinterpret_cast<const uint32_t *>(p)[i];
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+            for (int i = 0; i < N; ++i) w.u[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+        }
+        return w;
+    }
+    __device__ uint4 wide() const {
+        static_assert(N == 4);
+        return make_uint4(u[0], u[1], u[2], u[3]);
     }
 };
 
@@ -259,91 +301,101 @@ struct MoveParams {
     const int32_t *rows, *offsets;
     int64_t n, slots;
     int64_t row_bytes;
-    int words;  // 16-byte words that a row takes, at most
+    int words;  // words that a row takes, at most
+    int align;  // bytes, up to a word's, that the strided operand's rows are aligned to
     int topk, n_experts;
     int tpr_log2;  // threads per row
 };
 
 constexpr int kMoveThreads = 256;
-constexpr int kGatherUnroll = 4;
+template <int VEC>
+constexpr int kGatherUnroll = VEC == 2 || VEC == 16 ? 4 : 8;
 
-// What an aligned word of a stored row takes of the row.
+// What a word of a stored row takes of the row.
 struct RowWord {
-    int64_t at;  // the word's first byte within the row; negative in the first word
+    int64_t at;  // the word's first byte within the row; negative in a shifted row's first word
     int lo, hi;  // the word's bytes that are in the row
 };
 
-template <bool WHOLE>
+template <int VEC>
 __device__ __forceinline__ RowWord row_word(const uint8_t *row, int v, const MoveParams &p) {
-    if (WHOLE) return {(int64_t)v * 16, 0, v < p.words ? 16 : 0};
+    if (VEC > 2) return {(int64_t)v * VEC, 0, v < p.words ? VEC : 0};
     const int m = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
     const int64_t at = (int64_t)v * 16 - m;
     return {at, v == 0 ? m : 0, (int)min((int64_t)16, p.row_bytes - at)};
 }
 
-template <bool WHOLE>
-__device__ __forceinline__ uint4 load_16(const uint8_t *p, const Span &in) {
-    if constexpr (WHOLE) return *reinterpret_cast<const uint4 *>(p);
-    return load_word(p, in);
-}
-
-template <bool WHOLE>
-__device__ __forceinline__ void store_16(uint8_t *p, const uint4 &v, const RowWord &at) {
-    if constexpr (WHOLE)
-        *reinterpret_cast<uint4 *>(p) = v;
+template <typename T, int VEC>
+__device__ __forceinline__ Word<T, VEC> load_row(const uint8_t *p, const Span &in) {
+    if constexpr (VEC > 2)
+        return Word<T, VEC>::load(p);
     else
-        store_word(p, v, at.lo, at.hi);
+        return Word<T, VEC>::of(load_word(p, in));
 }
 
-// xs[row(t, j)] = x[t]; a thread holds up to kGatherUnroll words of its token
-// and writes them to every choice's row.
-template <bool WHOLE>
+template <typename T, int VEC>
+__device__ __forceinline__ Word<T, VEC> load_strided(const uint8_t *p, int align, const Span &in) {
+    if constexpr (VEC > 2)
+        return Word<T, VEC>::load(p, align);
+    else
+        return Word<T, VEC>::of(load_word(p, in));
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_row(uint8_t *p, const Word<T, VEC> &w, const RowWord &at) {
+    if constexpr (VEC == 16) *reinterpret_cast<uint4 *>(p) = w.wide();
+    if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(w.u[0], w.u[1]);
+    if constexpr (VEC == 4) *reinterpret_cast<uint32_t *>(p) = w.u[0];
+    if constexpr (VEC == 2) store_word(p, w.wide(), at.lo, at.hi);
+}
+
+// xs[row(t, j)] = x[t]; a thread holds up to U words of its token and writes
+// them to every choice's row.
+template <int VEC>
 __global__ void __launch_bounds__(kMoveThreads) route_gather_kernel(const MoveParams p, const uint8_t *x,
                                                                     int64_t pitch, Span in, uint8_t *xs) {
+    using W = Word<float, VEC>;
+    constexpr int U = kGatherUnroll<VEC>;
     griddep_wait();
     const int tpr = 1 << p.tpr_log2;
     const int sub = threadIdx.x & (tpr - 1);
     const int64_t t = (int64_t)blockIdx.x * (kMoveThreads >> p.tpr_log2) + (threadIdx.x >> p.tpr_log2);
-    const int v0 = (int)blockIdx.y * (tpr * kGatherUnroll) + sub;
+    const int v0 = (int)blockIdx.y * (tpr * U) + sub;
     if (t >= p.n || v0 >= p.words) return;
     const int kept = p.offsets[p.n_experts];
     const uint8_t *src = x + t * pitch;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 val[kGatherUnroll];
-    if (WHOLE) {  // the same words for every choice
+    W val[U];
+    if (VEC > 2) {  // the same words for every choice
 #pragma unroll
-        for (int u = 0; u < kGatherUnroll; ++u)
-            if (v0 + u * tpr < p.words) val[u] = load_16<true>(src + (int64_t)(v0 + u * tpr) * 16, in);
+        for (int u = 0; u < U; ++u)
+            if (v0 + u * tpr < p.words) val[u] = load_strided<float, VEC>(src + (int64_t)(v0 + u * tpr) * VEC, p.align, in);
     }
     for (int j = 0; j < p.topk; ++j) {
         const int r = p.rows[t * p.topk + j];
         if (r < 0 || r >= p.slots) continue;
         const bool on = r < kept;
         uint8_t *dst = xs + (int64_t)r * p.row_bytes;
-        RowWord at[kGatherUnroll];
+        RowWord at[U];
 #pragma unroll
-        for (int u = 0; u < kGatherUnroll; ++u) {
-            at[u] = row_word<WHOLE>(dst, v0 + u * tpr, p);
-            if (!WHOLE && at[u].hi > 0) val[u] = load_16<WHOLE>(src + at[u].at, in);
+        for (int u = 0; u < U; ++u) {
+            at[u] = row_word<VEC>(dst, v0 + u * tpr, p);
+            if (VEC == 2 && at[u].hi > 0) val[u] = load_row<float, VEC>(src + at[u].at, in);
         }
 #pragma unroll
-        for (int u = 0; u < kGatherUnroll; ++u)
-            if (at[u].hi > 0) store_16<WHOLE>(dst + at[u].at, on ? val[u] : zero, at[u]);
+        for (int u = 0; u < U; ++u)
+            if (at[u].hi > 0) store_row<float, VEC>(dst + at[u].at, on ? val[u] : W::zero(), at[u]);
     }
 }
 
-constexpr int kInFlight = 4;  // rows' words that a thread of the combine has on their way
-
-// A thread has U words of its token and the rows of kInFlight / U choices in
-// flight: few choices leave room for several words (one at a time, 65536
-// tokens of one choice, d = 2048 float32, took 398 us, 4.0 TB/s; four, 239).
-template <bool WHOLE, typename T, int U>
+// A thread has U words of its token and the rows of CH choices in flight: few
+// choices leave room for several words (one at a time, 65536 tokens of one
+// choice, d = 2048 float32, took 398 us, 4.0 TB/s; four, 239).
+template <int VEC, typename T, int CH, int U>
 __global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveParams p, const uint8_t *ys, Span in,
                                                                      const float *__restrict__ weights,
                                                                      const uint8_t *residual, int64_t pitch, Span res_in,
                                                                      uint8_t *y) {
-    using P = Piece<T>;
-    constexpr int CH = kInFlight / U;
+    using P = Word<T, VEC>;
     griddep_wait();
     const int tpr = 1 << p.tpr_log2;
     const int sub = threadIdx.x & (tpr - 1);
@@ -357,8 +409,8 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveP
     P res[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        at[u] = row_word<WHOLE>(dst, v0 + u * tpr, p);
-        if (residual && at[u].hi > 0) res[u].w = load_16<WHOLE>(residual + t * pitch + at[u].at, res_in);
+        at[u] = row_word<VEC>(dst, v0 + u * tpr, p);
+        if (residual && at[u].hi > 0) res[u] = load_strided<T, VEC>(residual + t * pitch + at[u].at, p.align, res_in);
     }
     float acc[U][P::V];
 #pragma unroll
@@ -378,7 +430,7 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveP
             w[c] = weights ? weights[t * p.topk + j] : 1.f;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (at[u].hi > 0) part[c][u].w = load_16<WHOLE>(ys + r * p.row_bytes + at[u].at, in);
+                if (at[u].hi > 0) part[c][u] = load_row<T, VEC>(ys + r * p.row_bytes + at[u].at, in);
         }
 #pragma unroll
         for (int c = 0; c < CH; ++c)
@@ -400,22 +452,22 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveP
 #pragma unroll
             for (int i = 0; i < P::V; ++i) acc[u][i] += f[i];
         }
-        store_16<WHOLE>(dst + at[u].at, P::from_floats(acc[u]).w, at[u]);
+        store_row<T, VEC>(dst + at[u].at, P::from_floats(acc[u]), at[u]);
     }
 }
 
 constexpr int64_t kManyTokens = 152 * 16;
 
 // A group of tpr threads per token walks the row, CH choices at a time and U
-// pieces of each in flight; a block whose groups are wider than a warp joins
-// the warps' sums in shared memory.  The sums run over dy's pieces whatever the
-// alignment, so that they have one order.
-template <bool WHOLE, typename T, int CH, int U>
+// words of each in flight; a block whose groups are wider than a warp joins
+// the warps' sums in shared memory.  Shifted rows' sums run over dy's words from
+// the row's start, wherever the row lies.
+template <int VEC, typename T, int CH, int U>
 __global__ void __launch_bounds__(kMoveThreads, 2) route_combine_grad_kernel(const MoveParams p, const uint8_t *dy,
                                                                           int64_t pitch, Span dy_in, const uint8_t *ys,
                                                                           Span in, const float *__restrict__ weights,
                                                                           uint8_t *dys, float *__restrict__ dweights) {
-    using P = Piece<T>;
+    using P = Word<T, VEC>;
     __shared__ float part[CH][kMoveThreads / 32];
     griddep_wait();
     const int tpr = 1 << p.tpr_log2;
@@ -440,15 +492,22 @@ __global__ void __launch_bounds__(kMoveThreads, 2) route_combine_grad_kernel(con
             bool here[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t at = (int64_t)(v0 + u * tpr) * 16;
-                const int bytes = (int)min((int64_t)16, p.row_bytes - at);
+                const int64_t at = (int64_t)(v0 + u * tpr) * kWordBytes<VEC>;
+                const int bytes = (int)min((int64_t)kWordBytes<VEC>, p.row_bytes - at);
                 here[u] = bytes > 0;
                 if (!here[u]) continue;
-                g[u].w = load_piece<WHOLE>(dy + t * pitch + at, bytes, dy_in);
+                if constexpr (VEC > 2)
+                    g[u] = load_strided<T, VEC>(dy + t * pitch + at, p.align, dy_in);
+                else
+                    g[u] = P::of(load_piece<false>(dy + t * pitch + at, bytes, dy_in));
 #pragma unroll
-                for (int c = 0; c < CH; ++c)
-                    if (row[c] >= 0 && row[c] < limit)
-                        got[c][u].w = load_piece<WHOLE>(ys + row[c] * p.row_bytes + at, bytes, in);
+                for (int c = 0; c < CH; ++c) {
+                    if (row[c] < 0 || row[c] >= limit) continue;
+                    if constexpr (VEC > 2)
+                        got[c][u] = load_row<T, VEC>(ys + row[c] * p.row_bytes + at, in);
+                    else
+                        got[c][u] = P::of(load_piece<false>(ys + row[c] * p.row_bytes + at, bytes, in));
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -464,17 +523,17 @@ __global__ void __launch_bounds__(kMoveThreads, 2) route_combine_grad_kernel(con
                     }
                     if (row[c] < 0) continue;
                     uint8_t *dst = dys + row[c] * p.row_bytes;
-                    const RowWord to = row_word<WHOLE>(dst, v0 + u * tpr, p);
+                    const RowWord to = row_word<VEC>(dst, v0 + u * tpr, p);
                     if (to.hi <= 0) continue;
-                    if (WHOLE) {
+                    if constexpr (VEC > 2) {
 #pragma unroll
                         for (int i = 0; i < P::V; ++i) f[i] = gf[i];
                     } else {
-                        P{load_16<WHOLE>(dy + t * pitch + to.at, dy_in)}.to_floats(f);
+                        load_row<T, VEC>(dy + t * pitch + to.at, dy_in).to_floats(f);
                     }
 #pragma unroll
                     for (int i = 0; i < P::V; ++i) f[i] = on ? w[c] * f[i] : 0.f;
-                    store_16<WHOLE>(dst + to.at, P::from_floats(f).w, to);
+                    store_row<T, VEC>(dst + to.at, P::from_floats(f), to);
                 }
             }
         }
@@ -509,11 +568,11 @@ __global__ void __launch_bounds__(kMoveThreads, 2) route_combine_grad_kernel(con
 
 int elem_bytes(int dtype) { return dtype == KMEANS_F32 ? 4 : 2; }
 
-// Every row of every matrix starts on 16 bytes.
-bool whole_rows(int64_t row_bytes, int64_t pitch_bytes, std::initializer_list<const void *> ptrs) {
-    uint64_t bits = (uint64_t)row_bytes | (uint64_t)pitch_bytes;
+// The most bytes, 16, 8, 4 or 2, that every row starts on a multiple of.
+int rows_align(int64_t pitch_bytes, std::initializer_list<const void *> ptrs) {
+    uint64_t bits = (uint64_t)pitch_bytes | 16u;
     for (const void *q : ptrs) bits |= reinterpret_cast<uintptr_t>(q);
-    return (bits & 15u) == 0;
+    return (int)(bits & (~bits + 1));
 }
 
 Span span(const void *base, int64_t rows, int64_t pitch_bytes, int64_t row_bytes) {
@@ -527,14 +586,17 @@ int log2_at_least(int64_t v, int most) {
     return l;
 }
 
-MoveParams move_params(const RouteRows &r, int bytes_per, bool whole) {
+// The stored rows have words of vec bytes (2: shifted ones); the strided
+// operand's rows are aligned to `align`.
+MoveParams move_params(const RouteRows &r, int bytes_per, int vec, int align) {
     MoveParams p{};
     p.rows = r.rows;
     p.offsets = r.offsets;
     p.n = r.n;
     p.slots = r.n * r.topk;
     p.row_bytes = r.d * bytes_per;
-    p.words = (int)((p.row_bytes + (whole ? 15 : 29)) / 16);  // a row may start 14 bytes into a word
+    p.words = (int)(vec > 2 ? p.row_bytes / vec : (p.row_bytes + 29) / 16);  // a row may start 14 bytes into a word
+    p.align = align;
     p.topk = r.topk;
     p.n_experts = r.n_experts;
     return p;
@@ -564,11 +626,11 @@ dim3 word_grid(MoveParams &p, int each) {
     return dim3(row_blocks(p), (unsigned)((p.words + per - 1) / per));
 }
 
-template <bool WHOLE, typename T, int U>
+template <int VEC, typename T, int CH, int U>
 cudaError_t combine_as(MoveParams p, const void *ys, const float *weights, const void *residual, int64_t pitch, void *y,
                        cudaStream_t s) {
     const dim3 grid = word_grid(p, U);
-    return launch_kernel(true, route_combine_kernel<WHOLE, T, U>, grid, dim3(kMoveThreads), 0, s, p,
+    return launch_kernel(true, route_combine_kernel<VEC, T, CH, U>, grid, dim3(kMoveThreads), 0, s, p,
                          static_cast<const uint8_t *>(ys), span(ys, p.slots, p.row_bytes, p.row_bytes), weights,
                          static_cast<const uint8_t *>(residual), pitch, span(residual, p.n, pitch, p.row_bytes),
                          static_cast<uint8_t *>(y));
@@ -577,51 +639,59 @@ cudaError_t combine_as(MoveParams p, const void *ys, const float *weights, const
 template <typename T>
 cudaError_t combine_typed(const RouteRows &r, const void *ys, const float *weights, const void *residual, int64_t ldr,
                           void *y, cudaStream_t s) {
-    const int64_t pitch = ldr * (int64_t)sizeof(T), row_bytes = r.d * (int64_t)sizeof(T);
-    const bool whole = whole_rows(row_bytes, residual ? pitch : 0, {ys, residual, y});
-    const MoveParams p = move_params(r, (int)sizeof(T), whole);
-    if (!whole) return combine_as<false, T, 1>(p, ys, weights, residual, pitch, y, s);
+    const int64_t pitch = ldr * (int64_t)sizeof(T);
+    const int vec = rows_align(r.d * (int64_t)sizeof(T), {ys, y});
+    const MoveParams p = move_params(r, (int)sizeof(T), vec, residual ? rows_align(pitch, {residual}) : 16);
+    if constexpr (sizeof(T) == 2) {
+        // 4097 tokens of 3 choices, d = 1031: four rows' words in flight 13.3 us,
+        // two of two rows 12.1; 16384 of 8, d = 2047: 224 and 263
+        if (vec == 2 && p.topk > 4) return combine_as<2, T, 4, 1>(p, ys, weights, residual, pitch, y, s);
+        if (vec == 2) return combine_as<2, T, 2, 2>(p, ys, weights, residual, pitch, y, s);
+    }
+    // short words: more of one row rather than more rows (16384 tokens of 8
+    // choices, d = 2046 bf16: one row's eight words 154 us, four rows' two 212,
+    // eight rows' two 247; d = 2044: two rows' four words 127 us, one row's eight 134, eight
+    // rows' one 291)
+    if (vec == 4) return combine_as<4, T, 1, 8>(p, ys, weights, residual, pitch, y, s);
+    if (vec == 8) return combine_as<8, T, 2, 4>(p, ys, weights, residual, pitch, y, s);
     // several words per thread only where the rows still fill the SMs
     const bool many = p.n * p.words >= 152 * 2048 * 4;
-    if (p.topk > 3 || !many) return combine_as<true, T, 1>(p, ys, weights, residual, pitch, y, s);
-    if (p.topk > 1) return combine_as<true, T, 2>(p, ys, weights, residual, pitch, y, s);
-    return combine_as<true, T, 4>(p, ys, weights, residual, pitch, y, s);
+    if (p.topk > 3 || !many) return combine_as<16, T, 4, 1>(p, ys, weights, residual, pitch, y, s);
+    if (p.topk > 1) return combine_as<16, T, 2, 2>(p, ys, weights, residual, pitch, y, s);
+    return combine_as<16, T, 1, 4>(p, ys, weights, residual, pitch, y, s);
 }
 
-template <bool WHOLE, typename T, int CH, int U>
-cudaError_t combine_grad_as(const RouteRows &r, const void *dy, int64_t pitch, const void *ys, const float *weights,
-                            void *dys, float *dweights, cudaStream_t s) {
-    MoveParams p = move_params(r, (int)sizeof(T), WHOLE);
+template <int VEC, typename T, int CH, int U>
+cudaError_t combine_grad_as(MoveParams p, const void *dy, int64_t pitch, const void *ys, const float *weights, void *dys,
+                            float *dweights, cudaStream_t s) {
     // a warp per token where there are enough of them: no block-wide join, and
     // the rows of other tokens hide each other's latency (16384 tokens of 8
     // choices, d = 2048: a block per token 344 us, 178 so)
-    p.tpr_log2 = log2_at_least((p.row_bytes + 15) / 16, p.n >= kManyTokens ? 5 : 8);
-    return launch_kernel(true, route_combine_grad_kernel<WHOLE, T, CH, U>, dim3(row_blocks(p)), dim3(kMoveThreads), 0, s,
+    p.tpr_log2 = log2_at_least((p.row_bytes + kWordBytes<VEC> - 1) / kWordBytes<VEC>, p.n >= kManyTokens ? 5 : 8);
+    return launch_kernel(true, route_combine_grad_kernel<VEC, T, CH, U>, dim3(row_blocks(p)), dim3(kMoveThreads), 0, s,
                          p, static_cast<const uint8_t *>(dy), pitch, span(dy, p.n, pitch, p.row_bytes),
                          static_cast<const uint8_t *>(ys), span(ys, p.slots, p.row_bytes, p.row_bytes), weights,
                          static_cast<uint8_t *>(dys), dweights);
-}
-
-template <bool WHOLE, typename T>
-cudaError_t combine_grad_sized(const RouteRows &r, const void *dy, int64_t pitch, const void *ys, const float *weights,
-                               void *dys, float *dweights, cudaStream_t s) {
-    // a shifted word takes the registers of two (two in flight for each choice:
-    // 16384 tokens of 4 choices, d = 513 float32, 159 us, one 146)
-    constexpr int each = WHOLE ? 2 : 1;
-    if constexpr (WHOLE) {
-        if (r.topk > 4) return combine_grad_as<WHOLE, T, 8, 1>(r, dy, pitch, ys, weights, dys, dweights, s);
-    }
-    if (r.topk > 2) return combine_grad_as<WHOLE, T, 4, each>(r, dy, pitch, ys, weights, dys, dweights, s);
-    return combine_grad_as<WHOLE, T, 2, 2 * each>(r, dy, pitch, ys, weights, dys, dweights, s);
 }
 
 template <typename T>
 cudaError_t combine_grad_typed(const RouteRows &r, const void *dy, int64_t lddy, const void *ys, const float *weights,
                                void *dys, float *dweights, cudaStream_t s) {
     const int64_t pitch = lddy * (int64_t)sizeof(T);
-    return whole_rows(r.d * (int64_t)sizeof(T), pitch, {dy, ys, dys})
-               ? combine_grad_sized<true, T>(r, dy, pitch, ys, weights, dys, dweights, s)
-               : combine_grad_sized<false, T>(r, dy, pitch, ys, weights, dys, dweights, s);
+    const int vec = rows_align(r.d * (int64_t)sizeof(T), {ys, dys});
+    const MoveParams p = move_params(r, (int)sizeof(T), vec, rows_align(pitch, {dy}));
+    if constexpr (sizeof(T) == 2) {
+        // a shifted word takes the registers of two
+        if (vec == 2)
+            return r.topk > 2 ? combine_grad_as<2, T, 4, 1>(p, dy, pitch, ys, weights, dys, dweights, s)
+                              : combine_grad_as<2, T, 2, 2>(p, dy, pitch, ys, weights, dys, dweights, s);
+    }
+    if (vec == 4 && p.topk > 4) return combine_grad_as<4, T, 8, 4>(p, dy, pitch, ys, weights, dys, dweights, s);
+    if (vec == 4) return combine_grad_as<4, T, 4, 4>(p, dy, pitch, ys, weights, dys, dweights, s);
+    if (vec == 8) return combine_grad_as<8, T, 2, 8>(p, dy, pitch, ys, weights, dys, dweights, s);
+    if (p.topk > 4) return combine_grad_as<16, T, 8, 1>(p, dy, pitch, ys, weights, dys, dweights, s);
+    if (p.topk > 2) return combine_grad_as<16, T, 4, 2>(p, dy, pitch, ys, weights, dys, dweights, s);
+    return combine_grad_as<16, T, 2, 4>(p, dy, pitch, ys, weights, dys, dweights, s);
 }
 
 // Most blocks of one cluster: 16 where the device can hold such a cluster (it
@@ -701,13 +771,19 @@ cudaError_t launch_route(const void *experts, int id_bytes, int64_t slots, int n
 }
 
 cudaError_t launch_route_gather(const RouteRows &r, int dtype, const void *x, int64_t ldx, void *xs, cudaStream_t s) {
-    const int64_t pitch = ldx * elem_bytes(dtype);
-    const bool whole = whole_rows(r.d * elem_bytes(dtype), pitch, {x, xs});
-    MoveParams p = move_params(r, elem_bytes(dtype), whole);
-    const dim3 grid = word_grid(p, kGatherUnroll);
-    return launch_kernel(true, whole ? route_gather_kernel<true> : route_gather_kernel<false>, grid,
-                         dim3(kMoveThreads), 0, s, p, static_cast<const uint8_t *>(x), pitch,
-                         span(x, p.n, pitch, p.row_bytes), static_cast<uint8_t *>(xs));
+    const int bytes = elem_bytes(dtype);
+    const int64_t pitch = ldx * bytes;
+    const int vec = rows_align(r.d * bytes, {xs});
+    MoveParams p = move_params(r, bytes, vec, rows_align(pitch, {x}));
+    const auto as = [&](auto kernel, int unroll) {
+        const dim3 grid = word_grid(p, unroll);
+        return launch_kernel(true, kernel, grid, dim3(kMoveThreads), 0, s, p, static_cast<const uint8_t *>(x), pitch,
+                             span(x, p.n, pitch, p.row_bytes), static_cast<uint8_t *>(xs));
+    };
+    if (vec == 16) return as(route_gather_kernel<16>, kGatherUnroll<16>);
+    if (vec == 8) return as(route_gather_kernel<8>, kGatherUnroll<8>);
+    if (vec == 4) return as(route_gather_kernel<4>, kGatherUnroll<4>);
+    return as(route_gather_kernel<2>, kGatherUnroll<2>);
 }
 
 cudaError_t launch_route_combine(const RouteRows &r, int dtype, const void *ys, const float *weights,
