@@ -330,11 +330,13 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
                           span16(dy, sh.m, lddy, sh.n), static_cast<const T *>(pre), span16(pre, sh.m, sh.n, sh.n),
                           sh.offsets, sh.n_experts, sh.m, sh.n, slope_rows(sh.m, sh.n), activation, dz, ldz, partial,
                           call.first());
-        // Few row tiles per expert are joined by the weight gradient's epilogue
-        // warps, which have nothing to do yet when it starts (ragged gradient:
-        // 6.5 us of a launch of its own); many by a kernel with a thread each.
+        // The row tiles' sums are joined by the weight gradient's epilogue warps,
+        // which have nothing to do yet when it starts (a launch of its own: 6.5 us
+        // of the ragged gradient, 12 of 32768 rows of 512 x 512); a kernel with a
+        // thread for each does it where there is no weight gradient, and where an
+        // expert has more tiles than those warps can add up on the way.
         const int rows = slope_rows(sh.m, sh.n);
-        const bool on_the_side = dw && db && sh.m / rows <= 16 * (int64_t)sh.n_experts;
+        const bool on_the_side = dw && db && sh.m / rows <= 512 * (int64_t)sh.n_experts;
         if (on_the_side) {
             g.db = db;
             g.bias_sums = partial;

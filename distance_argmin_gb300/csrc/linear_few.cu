@@ -236,7 +236,7 @@ cudaError_t launch_few(const LinearShape &sh, FewParams p, cudaStream_t s) {
 // their rows are not known here, so few of them on average; an expert with more
 // reads its part of W again (from L2) every 8 rows (64 experts, n = 4096, k =
 // 2048: 128 rows 159 us, 6.3 TB/s; 1024 rows 167 us in the tensor-core units).
-bool few_rows(const LinearShape &sh) { return sh.offsets ? sh.m <= 2 * (int64_t)sh.n_experts : sh.m <= kFewRows; }
+bool few_rows(const LinearShape &sh) { return sh.m <= kFewRows || (sh.offsets && sh.m <= 2 * (int64_t)sh.n_experts); }
 
 cudaError_t launch_linear_few(const LinearShape &sh, const Product16 &g, uint32_t *status, cudaStream_t s) {
     FewParams p{};

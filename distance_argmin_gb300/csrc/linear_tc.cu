@@ -425,17 +425,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
         using F = Finish<MODE, BN, T>;
         F fin{p, reinterpret_cast<float *>(smem + C::STAGING_BASE) + warp * lt::EPI_ROWS * lt::EPI_PITCH, lane};
         if (WEIGHTS && p.db) {
-            // while the first units are on their way: the bias gradient, an
-            // expert's row tiles added in order
-            const int64_t count = (int64_t)p.n_experts * p.out_rows;
-            for (int64_t i = (int64_t)blockIdx.x * (lt::EPI_WARPS * 32) + threadIdx.x; i < count;
-                 i += (int64_t)gridDim.x * (lt::EPI_WARPS * 32)) {
-                const int e = (int)(i / p.out_rows), col = (int)(i - (int64_t)e * p.out_rows);
+            // while the first units are on their way: the bias gradient, eight
+            // columns to a warp, an expert's row tiles dealt to four lanes each
+            // and their sums added in order
+            const int groups = (p.out_rows + 7) / 8, sub = lane >> 3;
+            for (int64_t i = (int64_t)blockIdx.x * lt::EPI_WARPS + warp; i < (int64_t)p.n_experts * groups;
+                 i += (int64_t)gridDim.x * lt::EPI_WARPS) {
+                const int e = (int)(i / groups), col = (int)(i - (int64_t)e * groups) * 8 + (lane & 7);
                 float s = 0.f;
+                if (col < p.out_rows) {
 #pragma unroll 8
-                for (int tile = bias_tiles[e]; tile < bias_tiles[e + 1]; ++tile)
-                    s += p.bias_sums[(int64_t)tile * p.out_rows + col];
-                static_cast<T *>(p.db)[i] = narrow<T>(s);
+                    for (int tile = bias_tiles[e] + sub; tile < bias_tiles[e + 1]; tile += 4)
+                        s += p.bias_sums[(int64_t)tile * p.out_rows + col];
+                }
+                s += __shfl_xor_sync(0xffffffffu, s, 8);
+                s += __shfl_xor_sync(0xffffffffu, s, 16);
+                if (sub == 0 && col < p.out_rows) static_cast<T *>(p.db)[(int64_t)e * p.out_rows + col] = narrow<T>(s);
             }
             __syncwarp();
         }
