@@ -137,25 +137,51 @@ __device__ __forceinline__ float slope(float z) {
     return 1.f;
 }
 
-// The slopes of two values.  The pass over dy has nothing else to compute, and
-// z Phi(z) costs it some thirty instructions a value one at a time: here the
-// multiplications and additions go two at a time.
+// Two values at a time: z Phi(z) takes some thirty instructions a value, and the
+// multiplications and additions among them go by pairs.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float2 normal_cdf2(float2 z, float2 &e) {
+    const float2 e2 = __fmul2_rn(__fmul2_rn(z, z), both(-0.5f * kLog2E));
+    e = make_float2(exp2_approx(e2.x), exp2_approx(e2.y));
+    constexpr float P = 0.3275911f * 0.70710678118654752f;
+    const float2 t = make_float2(reciprocal_approx(fmaf(P, fabsf(z.x), 1.f)), reciprocal_approx(fmaf(P, fabsf(z.y), 1.f)));
+    float2 poly = __ffma2_rn(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+    poly = __ffma2_rn(t, poly, both(0.5f * 1.421413741f));
+    poly = __ffma2_rn(t, poly, both(0.5f * -0.284496736f));
+    poly = __ffma2_rn(t, poly, both(0.5f * 0.254829592f));
+    const float2 tail = __fmul2_rn(__fmul2_rn(poly, t), e);  // 1 - Phi(|z|)
+    // Phi(z) = 1/2 + sign(z) (1/2 - tail)
+    const float2 half = __fadd2_rn(both(0.5f), make_float2(-tail.x, -tail.y));
+    return __fadd2_rn(both(0.5f), make_float2(copysignf(half.x, z.x), copysignf(half.y, z.y)));
+}
+
+// 1 / (1 + 2^x)
+__device__ __forceinline__ float2 inverse_power2(float2 x) {
+    const float2 d = __fadd2_rn(make_float2(exp2_approx(x.x), exp2_approx(x.y)), both(1.f));
+    return make_float2(reciprocal_approx(d.x), reciprocal_approx(d.y));
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 activate2(float2 z) {
+    if constexpr (ACT == KMEANS_ACT_GELU) {
+        float2 e;
+        return __fmul2_rn(z, normal_cdf2(z, e));
+    } else if constexpr (ACT == KMEANS_ACT_GELU_TANH) {
+        const float2 u = __ffma2_rn(both(-0.0713548162726f * kLog2E), __fmul2_rn(z, z), both(-1.5957691216057308f * kLog2E));
+        return __fmul2_rn(z, inverse_power2(__fmul2_rn(z, u)));
+    } else if constexpr (ACT == KMEANS_ACT_SILU) {
+        return __fmul2_rn(z, inverse_power2(__fmul2_rn(z, both(-kLog2E))));
+    } else {
+        return make_float2(activate<ACT>(z.x), activate<ACT>(z.y));
+    }
+}
+
 template <int ACT>
 __device__ __forceinline__ float2 slope2(float2 z) {
     if constexpr (ACT == KMEANS_ACT_GELU) {
-        const auto both = [](float v) { return make_float2(v, v); };
-        const float2 e2 = __fmul2_rn(__fmul2_rn(z, z), both(-0.5f * kLog2E));
-        const float2 e = make_float2(exp2_approx(e2.x), exp2_approx(e2.y));
-        constexpr float P = 0.3275911f * 0.70710678118654752f;
-        const float2 t = make_float2(reciprocal_approx(fmaf(P, fabsf(z.x), 1.f)), reciprocal_approx(fmaf(P, fabsf(z.y), 1.f)));
-        float2 poly = __ffma2_rn(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
-        poly = __ffma2_rn(t, poly, both(0.5f * 1.421413741f));
-        poly = __ffma2_rn(t, poly, both(0.5f * -0.284496736f));
-        poly = __ffma2_rn(t, poly, both(0.5f * 0.254829592f));
-        const float2 tail = __fmul2_rn(__fmul2_rn(poly, t), e);  // 1 - Phi(|z|)
-        // Phi(z) = 1/2 + sign(z) (1/2 - tail)
-        const float2 half = __fadd2_rn(both(0.5f), make_float2(-tail.x, -tail.y));
-        const float2 cdf = __fadd2_rn(both(0.5f), make_float2(copysignf(half.x, z.x), copysignf(half.y, z.y)));
+        float2 e;
+        const float2 cdf = normal_cdf2(z, e);
         return __ffma2_rn(__fmul2_rn(z, both(0.39894228040143268f)), e, cdf);
     } else {
         return make_float2(slope<ACT>(z.x), slope<ACT>(z.y));

@@ -119,6 +119,11 @@ struct Unit {
     int expert, p0, q0, qn;  // q0: first output row (row products: of the matrix, weights: of the expert)
     int c0, c1;              // contraction range (rows of x for weights)
     int slot;                // weights: the partial matrix this chunk of rows goes to (-1: the output)
+
+    __device__ __forceinline__ Unit of_lane(int l) const {
+        const auto from = [l](int v) { return __shfl_sync(0xffffffffu, v, l); };
+        return {from(expert), from(p0), from(q0), from(qn), from(c0), from(c1), from(slot)};
+    }
 };
 
 // (There are fewer than 2^31 units: each is 64 rows x 256 features or more of
@@ -181,6 +186,12 @@ struct Units {
 // accumulator's layout, 32 neighbouring features of a row at a time (run_direct;
 // also for aligned rows it was no faster: dense 8192 x 8192 x 2048 170 us
 // against 164, and one bulk copy per row of 128 features 174).
+// Up to some 600 products per output the epilogue sets the pace, not the tensor
+// pipe.  Each SM then finishes 128 x 256 values, of a long matrix with 64 products each, say, in 2.7
+// us without an activation and 3.7 with GELU: shared memory 64% and issue 40
+// to 70% busy.  (Without the path for parts whose rows all exist, and with
+// activations one value at a time, 3.0 and 4.8 us; 16 or 32 accumulator columns
+// per load 3.1 and 3.5.)
 template <Product MODE, int BN, typename T>
 struct Finish {
     static constexpr int COLS = BN / (lt::EPI_WARPS / 4), CHUNKS = COLS / lt::EPI_ROWS;
@@ -206,15 +217,25 @@ struct Finish {
         }
     }
 
-    __device__ __forceinline__ static void store8(void *out, int64_t at, const float (&v)[8]) {
+    __device__ __forceinline__ static void store8(void *out, int64_t at, const float2 (&v)[4]) {
         *reinterpret_cast<uint4 *>(static_cast<T *>(out) + at) =
-            make_uint4(narrow2<T>(v[0], v[1]), narrow2<T>(v[2], v[3]), narrow2<T>(v[4], v[5]), narrow2<T>(v[6], v[7]));
+            make_uint4(narrow2<T>(v[0].x, v[0].y), narrow2<T>(v[1].x, v[1].y), narrow2<T>(v[2].x, v[2].y),
+                       narrow2<T>(v[3].x, v[3].y));
     }
 
     template <int ACT>
-    __device__ void run(uint32_t acc, float bias, bool zero) {
+    __device__ __forceinline__ void run(uint32_t acc, float bias, bool zero) {
+        if (end - c0 == COLS && f + 32 <= p.cols && !zero)
+            run_rows<ACT, true>(acc, bias, false);
+        else
+            run_rows<ACT, false>(acc, bias, zero);
+    }
+
+    // FULL: every row and feature of the warp's part exists.
+    template <int ACT, bool FULL>
+    __device__ void run_rows(uint32_t acc, float bias, bool zero) {
         const int row = c0 + (lane >> 2);
-        const bool mine = f8() < p.cols;  // all eight: cols is a multiple of 8 here
+        const bool mine = FULL || f8() < p.cols;  // all eight: cols is a multiple of 8 here
         const int64_t step = (int64_t)lt::EPI_ROWS * p.cols;
         int64_t at = (out_row + row) * p.cols + f8();
         const float *src = staged + (lane >> 2) * lt::EPI_PITCH + (lane & 3) * 8;
@@ -222,29 +243,29 @@ struct Finish {
         if (!zero) tmem_ld_8_issue(acc + (uint32_t)c0, r);
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i, at += step) {
-            if (c0 + i * lt::EPI_ROWS >= end) break;
+            if (!FULL && c0 + i * lt::EPI_ROWS >= end) break;
             if (i) __syncwarp();  // the previous rows have been read; the warp is together again
             if (!zero) tmem_ld_8_wait(r);
 #pragma unroll
-            for (int j = 0; j < lt::EPI_ROWS; ++j) staged[j * lt::EPI_PITCH + lane] = __uint_as_float(r[j]) + bias;
+            for (int j = 0; j < lt::EPI_ROWS; j += 2) {
+                const float2 v = __fadd2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), both(bias));
+                staged[j * lt::EPI_PITCH + lane] = v.x;
+                staged[(j + 1) * lt::EPI_PITCH + lane] = v.y;
+            }
             __syncwarp();
-            if (!zero && i + 1 < CHUNKS && c0 + (i + 1) * lt::EPI_ROWS < end)
+            if (!zero && i + 1 < CHUNKS && (FULL || c0 + (i + 1) * lt::EPI_ROWS < end))
                 tmem_ld_8_issue(acc + (uint32_t)(c0 + (i + 1) * lt::EPI_ROWS), r);
-            if (row + i * lt::EPI_ROWS >= end || !mine) continue;
+            if (!FULL && (row + i * lt::EPI_ROWS >= end || !mine)) continue;
             const float4 lo = *reinterpret_cast<const float4 *>(src), hi = *reinterpret_cast<const float4 *>(src + 4);
-            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            float2 v[4] = {{lo.x, lo.y}, {lo.z, lo.w}, {hi.x, hi.y}, {hi.z, hi.w}};
             if constexpr (FORWARD) {
                 if (p.pre) store8(p.pre, at, v);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = activate<ACT>(v[k]);
+                for (int k = 0; k < 4; ++k) v[k] = activate2<ACT>(v[k]);
                 if (add) {
                     const uint32_t words[4] = {res[i].x, res[i].y, res[i].z, res[i].w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 a = widen2<T>(words[k]);
-                        v[2 * k] += a.x;
-                        v[2 * k + 1] += a.y;
-                    }
+                    for (int k = 0; k < 4; ++k) v[k] = __fadd2_rn(v[k], widen2<T>(words[k]));
                 }
             }
             store8(p.out, at, v);
@@ -445,8 +466,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             __syncwarp();
         }
         int use = 0, ring = 0;
-        for (int u = pair; u < units.total; u += num_pairs) {
-            const Unit t = units.at(u);
+        Unit mine{};  // 32 units ahead, one per lane
+        for (int u = pair, i = 0; u < units.total; u += num_pairs, i = (i + 1) & 31) {
+            if (i == 0) {
+                const int ahead = u + lane * num_pairs;
+                if (ahead < units.total) mine = units.at(ahead);
+                __syncwarp();
+            }
+            const Unit t = mine.of_lane(i);
             const bool zero = t.c1 <= t.c0;  // nothing to multiply: rows of no expert, experts without rows
             const int buf = use & 1;
             const int f = t.p0 + rank * lt::BP_CTA + quarter * 32;  // this warp's first feature
