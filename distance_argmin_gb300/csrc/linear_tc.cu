@@ -168,8 +168,14 @@ struct Units {
             t.c1 = min(edges[e + 1], t.c0 + p.chunk);
             t.slot = tiles[e + 1] - tiles[e] > 1 ? slots[e] + chunk : -1;
         } else {
-            t.q0 = edges[e] + q * BN;
-            t.qn = min(BN, edges[e + 1] - t.q0);
+            // an expert's rows in equal parts (multiples of 32) rather than full
+            // ones and a rest: a stage of few rows takes more than its share,
+            // and the pairs' turns come out more even (16384 ragged rows of 30
+            // experts, dx of 4096 x 2048: 186 us with full ones, 174 so)
+            const int rows = edges[e + 1] - edges[e];
+            const int step = min(BN, ((rows + per - 1) / per + 31) & ~31);
+            t.q0 = edges[e] + q * step;
+            t.qn = min(step, edges[e + 1] - t.q0);
             t.c0 = 0;
             t.c1 = e < p.n_experts ? p.contraction : 0;
         }
