@@ -2,7 +2,7 @@
 //
 // All three products are out(q, p) = sum_c A(p, c) B(q, c) with p contiguous in
 // the output (see linear_common.cuh).  The output's contiguous dimension is
-// always the MMA's M: 256 wide per CTA pair, and the rows are its N, 16 to 256
+// always the MMA's M: 256 wide per CTA pair, and the rows are its N, 32 to 256
 // in steps of 32.  A group of few rows then costs an MMA of few columns, and
 // each tensor-memory lane holds one output feature, so that a warp's 32 lanes
 // are 32 neighbours in memory.

@@ -549,7 +549,9 @@ int kmeans_linear(const void *x, int64_t ldx, const void *w, const void *bias, c
  * allowed for KMEANS_ACT_NONE).  dx (m, k), dw (n_experts, n, k) and db
  * (n_experts, n) may each be NULL; dx is zero in rows of no expert, dw and db
  * in experts without rows.  The products take dz rounded to the matrices'
- * type; db sums it before that rounding.  The residual's gradient is dy. */
+ * type; db sums it before that rounding.  Sums over an expert's rows are joined
+ * in float32 from chunks of at most 32768 rows.  The residual's gradient is
+ * dy. */
 int kmeans_linear_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w,
                        const void *pre, int dtype, int activation, const int32_t *offsets, int64_t m,
                        int64_t n, int64_t k, int64_t n_experts, void *dx, void *dw, void *db,
