@@ -173,7 +173,7 @@ struct Units {
             // and the pairs' turns come out more even (16384 ragged rows of 30
             // experts, dx of 4096 x 2048: 186 us with full ones, 174 so)
             const int rows = edges[e + 1] - edges[e];
-            const int step = min(BN, ((rows + per - 1) / per + 31) & ~31);
+            const int step = min(BN, ((rows - 1) / per + 32) & ~31);
             t.q0 = edges[e] + q * step;
             t.qn = min(step, edges[e + 1] - t.q0);
             t.c0 = 0;
@@ -189,9 +189,12 @@ struct Units {
 // asked for before the accumulator is waited for, so its latency passes behind
 // the unit's MMAs, and the next chunk's accumulator is on its way while one is
 // finished.  Rows that do not start on 16 bytes go straight from the
-// accumulator's layout, 32 neighbouring features of a row at a time (run_direct;
-// also for aligned rows it was no faster: dense 8192 x 8192 x 2048 170 us
-// against 164, and one bulk copy per row of 128 features 174).
+// accumulator's layout, 32 neighbouring features of a row at a time, with the
+// residual asked for in the same layout as early (run_direct: 19456 x 4095 of 64
+// products each 4.0 us a round of units, with a residual 13; it asked for late
+// 34, and by 4-byte words out of staged rows 11 and 30.  For aligned rows it is
+// slower: dense 8192 x 8192 x 2048 170 us against 164, and one bulk copy per row
+// of 128 features 174).
 // Up to some 600 products per output the epilogue sets the pace, not the tensor
 // pipe.  Each SM then finishes 128 x 256 values, of a long matrix with 64 products each, say, in 2.7
 // us without an activation and 3.7 with GELU: shared memory 64% and issue 40
@@ -214,7 +217,21 @@ struct Finish {
 
     __device__ void prefetch() {
         if constexpr (FORWARD) {
-            if (!add || !p.wide || f8() >= p.cols) return;
+            if (!add) return;
+            if (!p.wide) {  // a lane's feature of two rows to a word
+                if (f + lane >= p.cols) return;
+                const uint16_t *at = static_cast<const uint16_t *>(p.residual) + (out_row + c0) * p.ldr + f + lane;
+#pragma unroll
+                for (int i = 0; i < CHUNKS; ++i) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int j = 0; j < lt::EPI_ROWS; ++j, at += p.ldr)
+                        v[j] = c0 + i * lt::EPI_ROWS + j < end ? *at : 0;
+                    res[i] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+                }
+                return;
+            }
+            if (f8() >= p.cols) return;
             const T *at = static_cast<const T *>(p.residual) + (out_row + c0 + (lane >> 2)) * p.ldr + f8();
             const int64_t step = lt::EPI_ROWS * p.ldr;
 #pragma unroll
@@ -284,35 +301,41 @@ struct Finish {
         const bool mine = f + lane < p.cols;
         const int64_t at0 = (out_row + c0) * p.cols + f + lane;
         T *out = static_cast<T *>(p.out) + at0, *pre = FORWARD && p.pre ? static_cast<T *>(p.pre) + at0 : nullptr;
-        const T *rest = FORWARD && add ? static_cast<const T *>(p.residual) + (out_row + c0) * p.ldr + f + lane : nullptr;
-#pragma unroll 1
-        for (int c = c0; c < end; c += lt::EPI_ROWS) {
-            uint32_t r[8] = {};
+        uint32_t r[8] = {};
+        if (!zero) tmem_ld_8_issue(acc + (uint32_t)c0, r);
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int c = c0 + i * lt::EPI_ROWS;
+            if (c >= end) break;
             __syncwarp();
-            if (!zero) {
-                tmem_ld_8_issue(acc + (uint32_t)c, r);
-                tmem_ld_8_wait(r);
-            }
-            float v[8], a[8] = {};
+            if (!zero) tmem_ld_8_wait(r);
+            float2 v[4];
 #pragma unroll
-            for (int j = 0; j < lt::EPI_ROWS; ++j) {
-                v[j] = __uint_as_float(r[j]) + bias;
-                if (FORWARD && rest) {
-                    if (mine && c + j < end) a[j] = widen(*rest);
-                    rest += p.ldr;
+            for (int j = 0; j < 4; ++j)
+                v[j] = __fadd2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), both(bias));
+            if (!zero && i + 1 < CHUNKS && c + lt::EPI_ROWS < end) tmem_ld_8_issue(acc + (uint32_t)(c + lt::EPI_ROWS), r);
+            if (FORWARD && pre) {
+                store_rows(pre, v, c, mine);
+                pre += (int64_t)lt::EPI_ROWS * p.cols;
+            }
+            if constexpr (FORWARD) {
+                const uint32_t words[4] = {res[i].x, res[i].y, res[i].z, res[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] = activate2<ACT>(v[j]);
+                    if (add) v[j] = __fadd2_rn(v[j], widen2<T>(words[j]));
                 }
             }
-#pragma unroll
-            for (int j = 0; j < lt::EPI_ROWS; ++j) {
-                const bool on = mine && c + j < end;
-                if (FORWARD && pre) {
-                    if (on) *pre = narrow<T>(v[j]);
-                    pre += p.cols;
-                }
-                if (on) *out = narrow<T>(activate<ACT>(v[j]) + a[j]);
-                out += p.cols;
-            }
+            store_rows(out, v, c, mine);
+            out += (int64_t)lt::EPI_ROWS * p.cols;
         }
+    }
+
+    // A lane's feature of the rows c, c + 1, ..
+    __device__ __forceinline__ void store_rows(T *at, const float2 (&v)[4], int c, bool mine) const {
+#pragma unroll
+        for (int j = 0; j < lt::EPI_ROWS; ++j, at += p.cols)
+            if (mine && c + j < end) *at = narrow<T>(j & 1 ? v[j / 2].y : v[j / 2].x);
     }
 };
 
