@@ -220,15 +220,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteParams 
 // Rows move in words, neighbouring lanes at neighbouring words.  A word has as
 // many bytes as every stored row is aligned to, VEC = 16, 8 or 4, and is one
 // access (16384 tokens of 4 choices, d = 513 float32, 16-byte words put together
-// by shifts: gather 49 us, combine 66, gradient 146; 4-byte words 33, 49, 78).  Rows of
-// an odd number of 16-bit values (VEC = 2) have words of 16 bytes: the aligned
-// words of the stored row are written, only its two ends in part, and each is put
-// together from the two aligned words of the source that hold it; its shifts and
-// checks then bound the kernels (16384 tokens of 8 choices, d = 2047 bf16 against
-// 2048: gather 144 us, 92; combine 222, 102; gradient 527, 178).  For 4097 tokens
-// of three choices, d = 1031 in 16 bits, the combine takes 13 us so; values one
-// at a time took 31, 4-byte words 20, words shared between neighbouring lanes by
-// shuffles 19.
+// by shifts: gather 49 us, combine 66, gradient 146; 4-byte words 33, 49, 78).
+// Rows of an odd number of 16-bit values (VEC = 2) have words of 16 bytes: the
+// aligned words of the stored row are written, only its two ends in part, and
+// each is put together from the two aligned words of the source that hold it.
+// Their latency and some 200 instructions a word then bound the kernels (16384
+// tokens of 8 choices, d = 2047 bf16 against 2048: gather 141 us, 92; combine
+// 224, 102; gradient 529, 178).  For 4097 tokens of three choices, d = 1031 in 16
+// bits, the combine takes 12 us so; values one at a time took 31, 4-byte words
+// 20, words shared between neighbouring lanes by shuffles 19.
 template <int VEC>
 constexpr int kWordBytes = VEC == 2 ? 16 : VEC;
 
