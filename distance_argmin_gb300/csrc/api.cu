@@ -590,6 +590,14 @@ int kmeans_device_status(const void *ws, void *stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return KMEANS_ERR_CUDA;
     uint32_t st = 0;
     if (cudaMemcpy(&st, ws, sizeof(st), cudaMemcpyDeviceToHost) != cudaSuccess) return KMEANS_ERR_CUDA;
+    uint32_t words[kMaxPairWords];
+    const uint32_t pairs = st >> kPairCountShift;
+    if (pairs > 0 && pairs <= (uint32_t)kMaxPairWords) {
+        if (cudaMemcpy(words, static_cast<const uint8_t *>(ws) + kPairWordsOffset, pairs * sizeof(uint32_t),
+                       cudaMemcpyDeviceToHost) != cudaSuccess)
+            return KMEANS_ERR_CUDA;
+        for (uint32_t i = 0; i < pairs; ++i) st |= words[i];
+    }
     if (st & kFlagTimeout) return KMEANS_ERR_DEVICE_TIMEOUT;
     if (st & kFlagBadLabel) return KMEANS_ERR_DEVICE_LABEL;
     if (st & kFlagExchange) return KMEANS_ERR_DEVICE_EXCHANGE;

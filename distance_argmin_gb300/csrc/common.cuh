@@ -84,14 +84,22 @@ inline int cached_per_device(std::atomic<int> (&cache)[kMaxDevices], Fn &&comput
 
 // ---------------------------------------------------------------------------
 // Device status word.  Lives in the first bytes of the caller's workspace and
-// is cleared by every entry point before its first kernel.  Kernels OR flags
-// into it; the host maps them to kmeans_status codes.
+// is cleared by every entry point before the first kernel that may OR flags
+// into it or wait for another's; the host maps them to kmeans_status codes.
+//
+// A kernel whose CTA pairs wait only for themselves may be a call's first
+// kernel all the same: each pair then clears and uses a word of its own behind
+// the header, so that nothing has to be ordered between pairs, and block 0
+// leaves their number in the status word.
 // ---------------------------------------------------------------------------
 enum : uint32_t {
     kFlagTimeout = 1u,   // a pipeline wait ran out of time
     kFlagBadLabel = 2u,  // update saw a label outside [0, k), the routing an id past the last expert
     kFlagExchange = 4u,  // sharded k-means++: no rank's exchange block owned a trial
+    kFlagsMask = 0xffu,
 };
+constexpr int kPairCountShift = 8;  // status word: how many pair words hold flags too
+constexpr int kMaxPairWords = 128;
 
 struct WsHeader {
     uint32_t status;          // device status flags
@@ -109,6 +117,7 @@ static_assert(offsetof(WsHeader, fit_inertia) == 8 && offsetof(WsHeader, fit_nem
               "the fit's record is the header's first bytes");
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 static_assert(offsetof(WsHeader, kpp_rows) == 24, "8-byte aligned");
+constexpr size_t kPairWordsOffset = sizeof(WsHeader);  // from the workspace's start
 
 // Wall-clock limit of one pipeline wait.  A wait that legitimately takes this
 // long does not exist (the slowest stage waits for one k-block of a tile).
@@ -125,7 +134,7 @@ __device__ __forceinline__ void flag_error(uint32_t *status, uint32_t flag) {
 }
 
 __device__ __forceinline__ bool error_raised(const uint32_t *status) {
-    return *reinterpret_cast<const volatile uint32_t *>(status) != 0u;
+    return (*reinterpret_cast<const volatile uint32_t *>(status) & kFlagsMask) != 0u;
 }
 
 // ---------------------------------------------------------------------------

@@ -43,6 +43,7 @@ struct LinearShape {
     bool bf16;               // else fp16
 };
 
+// Starts with the header and the CTA pairs' status words.
 struct LinearLayout {
     int64_t off_x;   // x with its rows on 16 bytes, where the caller's are not
     int64_t off_w;   // w likewise (0: its rows are a multiple of 16 bytes)

@@ -402,7 +402,7 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
 
 LinearLayout linear_layout(bool grad, int64_t m, int64_t n, int64_t k, int64_t n_experts) {
     LinearLayout L{};
-    int64_t o = align_up((int64_t)sizeof(WsHeader), 1024);
+    int64_t o = align_up((int64_t)(kPairWordsOffset + kMaxPairWords * sizeof(uint32_t)), 1024);
     L.off_x = o;
     o = align_up(o + m * align_up(k, 8) * 2, 1024);
     if (k % 8 != 0) {

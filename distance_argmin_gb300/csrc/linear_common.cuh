@@ -121,7 +121,7 @@ inline bool rows16(const void *base, int64_t pitch_elems) {
 }
 
 // The product on the tensor cores; w, x and dz must be rows16.  `clear`: the
-// kernel is the call's first and clears the status word.
+// kernel is the call's first, so nothing has cleared the status word yet.
 cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product16 &g, uint32_t *status, bool clear,
                              cudaStream_t s);
 

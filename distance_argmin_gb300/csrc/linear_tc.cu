@@ -39,6 +39,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cstdlib>
 
 #include "assign_common.cuh"
@@ -109,7 +110,7 @@ struct LinearTcParams {
     int wide;  // the rows of the outputs and the residual start on 16 bytes
     uint32_t *status;
     int test_starve;  // test hook: the producer issues no loads, so the pipeline waits run out
-    int clear;  // first kernel of the call: it clears the status word
+    int clear;  // first kernel of the call: each pair has a status word of its own
 };
 
 // The units: expert by expert, bands of BAND feature tiles, in a band the
@@ -407,6 +408,20 @@ __device__ __forceinline__ void store_sums(float *out, int cols, uint32_t acc, i
     }
 }
 
+// The word that this pair's waits raise errors in and look at.  Worked out again
+// wherever a wait has to look (volatile): held in registers it costs the
+// epilogue's (19456 x 4096 of 64 products each 47.4 us, 45.5 so).
+struct PairStatus {
+    const LinearTcParams &p;
+    __device__ __forceinline__ uint32_t *word() const {
+        uint32_t block;
+        asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(block));
+        return p.clear ? p.status + kPairWordsOffset / 4 + (block >> 1) : p.status;
+    }
+    __device__ __forceinline__ bool raised() const { return error_raised(word()); }
+    __device__ __forceinline__ void flag(uint32_t f) const { flag_error(word(), f); }
+};
+
 // A value that all lanes of a converged warp hold, in a uniform register.
 __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
@@ -433,6 +448,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
     const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+    const PairStatus status{p};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -458,9 +474,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
         tc_fence_before();
     }
     griddep_wait();
-    // this call's status word: a wait of this launch runs out two seconds from
-    // now at the earliest, long after the first block has cleared it
-    if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
+    // cleared by the pair itself, ahead of the barrier below that its waits
+    // come after; the other pairs have theirs, whatever the workspace held
+    if (p.clear && rank == 0 && threadIdx.x == 0) {
+        *status.word() = 0u;
+        if (pair == 0) *p.status = (uint32_t)num_pairs << kPairCountShift;
+    }
     if (warp == 0) fill_tables(p.offsets, p.n_experts, p.m, WEIGHTS ? p.chunk : BN, edges, tiles, WEIGHTS ? slots : nullptr, lane);
     if (WEIGHTS && p.db && warp == 1)  // (the second table is a copy of the edges)
         fill_tables(p.offsets, p.n_experts, p.m, p.bias_rows, bias_tiles + p.n_experts + 2, bias_tiles, nullptr, lane);
@@ -516,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             fin.add = MODE == Product::kForward && p.residual && !zero;
             fin.prefetch();
             if (!zero) {
-                bool ok = mbar_wait_warp(bar(C::T_FULL + buf), (use >> 1) & 1, p.status);
+                bool ok = mbar_wait_warp(bar(C::T_FULL + buf), (use >> 1) & 1, status);
                 // a part that meets at barriers goes on together or not at all
                 if (MODE == Product::kWeights) ok = named_barrier_all(1 + part, 128, ok);
                 if (!ok) break;
@@ -595,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                     const uint32_t bytes = 2u * (boxes ? C::A_BYTES + boxes * (32 * lt::BK * 2) : C::STAGE);
                     int c = uniform(t.c0);
                     for (int left = kblocks; left > 0; --left, c += lt::BK) {
-                        if (!mbar_wait_converged(bar(C::EMPTY + s), phase ^ 1, p.status)) {
+                        if (!mbar_wait_converged(bar(C::EMPTY + s), phase ^ 1, status)) {
                             ok = false;
                             break;
                         }
@@ -632,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                 } else if (warp == lt::WARP_RELAY) {
                     // -------------------------------------------------- relay
                     for (int c = t.c0; c < t.c1; c += lt::BK) {
-                        if (!mbar_wait_converged(bar(C::FULL + s), phase, p.status)) {
+                        if (!mbar_wait_converged(bar(C::FULL + s), phase, status)) {
                             ok = false;
                             break;
                         }
@@ -669,7 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                     const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32);
                     const int buf = use & 1;
                     const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
-                    if (!mbar_wait_converged(bar(C::T_EMPTY + buf), ((use >> 1) & 1) ^ 1, p.status)) {
+                    if (!mbar_wait_converged(bar(C::T_EMPTY + buf), ((use >> 1) & 1) ^ 1, status)) {
                         ok = false;
                         break;
                     }
@@ -678,7 +697,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                     for (int left = kblocks; left > 0; --left) {
                         const uint32_t off = (uint32_t)s * (C::STAGE >> 4);
                         const uint32_t a_lo = (uint32_t)a0 + off, b_lo = (uint32_t)b0 + off;
-                        if (!mbar_wait_converged(bar((RELAY ? C::READY : C::FULL) + s), phase, p.status)) {
+                        if (!mbar_wait_converged(bar((RELAY ? C::READY : C::FULL) + s), phase, status)) {
                             ok = false;
                             break;
                         }
@@ -786,7 +805,7 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
     const int64_t row_tiles = MODE == Product::kWeights
                                   ? (sh.n + BN - 1) / BN * (sh.n_experts + sh.m / p.chunk + 1)
                                                         : (sh.m + BN - 1) / BN + (sh.offsets ? sh.n_experts : 0);
-    const int64_t most = device_sm_count() / 2, units = row_tiles * p.num_p;
+    const int64_t most = std::min(device_sm_count() / 2, kMaxPairWords), units = row_tiles * p.num_p;
     const unsigned pairs = (unsigned)(units < most ? units : most);
     return launch_kernel(true, linear_tc_kernel<MODE, BN, T>, dim3(2 * (pairs ? pairs : 1)), dim3(lt::THREADS),
                          C::smem_bytes(sh.n_experts), s, tmA, tmB, tmB32, tmOut, p);

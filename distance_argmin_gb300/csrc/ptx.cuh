@@ -79,9 +79,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_
     }
 }
 
+// Where a wait raises errors and looks for them.
+struct StatusWord {
+    uint32_t *word;
+    __device__ __forceinline__ bool raised() const { return error_raised(word); }
+    __device__ __forceinline__ void flag(uint32_t f) const { flag_error(word, f); }
+};
+
 // Whole-warp bounded wait: every lane observes the phase itself; the decision
 // to give up is taken once for the warp so the lanes never diverge.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t *status) {
+template <typename Status>
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const Status &status) {
     uint64_t t0 = 0;
     for (uint32_t spins = 0;; ++spins) {
         const bool done = mbar_try_wait(bar, parity);
@@ -91,10 +99,10 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ui
             if (lane_id() == 0) {
                 const uint64_t now = globaltimer_ns();
                 if (t0 == 0) t0 = now;
-                if (error_raised(status)) {
+                if (status.raised()) {
                     bail = 1;
                 } else if (now - t0 > kWaitLimitNs) {
-                    flag_error(status, kFlagTimeout);
+                    status.flag(kFlagTimeout);
                     bail = 1;
                 }
             }
@@ -103,8 +111,13 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ui
     }
 }
 
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t *status) {
+    return mbar_wait_warp(bar, parity, StatusWord{status});
+}
+
 // mbar_wait_warp with a short way through when the phase is already over.
-__device__ __forceinline__ bool mbar_wait_converged(uint32_t bar, uint32_t parity, uint32_t *status) {
+template <typename Status>
+__device__ __forceinline__ bool mbar_wait_converged(uint32_t bar, uint32_t parity, const Status &status) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return mbar_wait_warp(bar, parity, status);
 }
