@@ -442,7 +442,7 @@ cudaError_t launch_linear(const LinearShape &sh, const void *x, int64_t ldx, con
 cudaError_t launch_linear_grad(const LinearShape &sh, const void *dy, int64_t lddy, const void *x, int64_t ldx,
                                const void *w, const void *pre, int activation, void *dx, void *dw, void *db,
                                const LinearLayout &L, uint8_t *ws, cudaStream_t s) {
-    if (sh.m == 0) {
+    if (sh.m == 0 || !(dx || dw || db)) {  // no kernel that clears it
         const cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(WsHeader), s);  // this call's status word
         if (e != cudaSuccess) return e;
     }

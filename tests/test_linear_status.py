@@ -55,3 +55,13 @@ def test_a_timeout_is_reported_once_by_the_call_that_had_it(gpu_lib, monkeypatch
         ids[3, 1] = 6
         gpu_lib.kmeans_route(ids, 6, ws=ws)
         assert gpu_lib.kmeans_device_status(ws) == gpu_lib.KMEANS_ERR_DEVICE_LABEL
+
+
+@pytest.mark.parametrize("m", [0, 64])
+def test_a_gradient_of_nothing_leaves_a_clean_status(gpu_lib, m):
+    x, w, dy = (normal(s, torch.float16, i) for i, s in enumerate([(m, 16), (24, 16), (m, 24)]))
+    ws = gpu_lib.linear_workspace(gpu_lib.OP_LINEAR_GRAD, m, 24, 16)
+    ws.fill_(1)
+    out = gpu_lib.kmeans_linear_grad(dy, x, w, need_dx=False, need_dw=False, need_db=False, ws=ws)
+    assert out == (None, None, None)
+    assert gpu_lib.kmeans_device_status(ws) == gpu_lib.KMEANS_OK
