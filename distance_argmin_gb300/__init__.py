@@ -718,12 +718,15 @@ def _check_rows(t, name, dtype, shape, device):
     return pitch
 
 
-def _cuda_matrix(t, name):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+def _on_gpu(t, name):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (the library has no CPU path)")
+
+
+def _cuda_matrix(t, name):
+    _on_gpu(t, name)
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
 
@@ -737,12 +740,34 @@ def _current(device):
     return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
+def _launch(fn, device, *args):
+    """``fn(*args, stream)`` on ``device``'s current stream, with ``device`` as the
+    current one: the library's launches and their limits are the current
+    device's, and the stream's handle alone does not name one."""
+    if _torch()._C._cuda_getDevice() == device.index:
+        return fn(*args, _current(device))
+    with _torch().cuda.device(device):
+        return fn(*args, _current(device))
+
+
+def _stream_on(stream, tensor):
+    """``stream`` (a torch stream or a handle) as a torch stream of ``tensor``'s
+    device."""
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.ExternalStream(int(stream), device=tensor.device)
+    if stream.device != tensor.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {tensor.device}")
+    return stream
+
+
 def _on_stream(stream, fn, *args):
     """``fn(*args)`` with ``stream`` as the current stream, so that what it
     allocates belongs to that stream (a block that the current stream has given
-    back may still be in use there)."""
+    back may still be in use there).  The first argument is a tensor."""
     torch = _torch()
-    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+    _on_gpu(args[0], "the first argument")
+    with torch.cuda.stream(_stream_on(stream, args[0])):
         return fn(*args)
 
 
@@ -806,9 +831,8 @@ def kmeans_route(experts, n_experts: int, offsets=None, order=None, rows=None, w
         ws = route_workspace(n, topk, n_experts, dev)
     else:
         _workspace_on(ws, dev)
-    st = (_lib or load()).kmeans_route(_addr(experts), experts.element_size(), n, topk, n_experts, _addr(offsets),
-                                       _addr(order), _addr(rows), _addr(ws), ws.numel(),
-                                       _current(dev))
+    st = _launch((_lib or load()).kmeans_route, dev, _addr(experts), experts.element_size(), n, topk, n_experts,
+                 _addr(offsets), _addr(order), _addr(rows), _addr(ws), ws.numel())
     _raise(st, "kmeans_route")
     return offsets, order, rows
 
@@ -840,8 +864,8 @@ def kmeans_route_gather(x, rows, offsets, xs=None, stream=None):
         xs = _torch().empty((n * topk, d), dtype=dt, device=dev)
     else:
         _check_on(xs, "xs", dt, (n * topk, d), dev)
-    st = (_lib or load()).kmeans_route_gather(_addr(x), ldx, code, _addr(rows), _addr(offsets), n, topk, n_experts, d,
-                                              _addr(xs), _current(dev))
+    st = _launch((_lib or load()).kmeans_route_gather, dev, _addr(x), ldx, code, _addr(rows), _addr(offsets), n, topk,
+                 n_experts, d, _addr(xs))
     _raise(st, "kmeans_route_gather")
     return xs
 
@@ -866,8 +890,8 @@ def kmeans_route_combine(ys, rows, offsets, weights=None, residual=None, y=None,
         y = torch.empty((n, d), dtype=ys.dtype, device=dev)
     else:
         _check_on(y, "y", ys.dtype, (n, d), dev)
-    st = (_lib or load()).kmeans_route_combine(_addr(ys), code, _addr(weights), _addr(residual), ldr, _addr(rows),
-                                               _addr(offsets), n, topk, n_experts, d, _addr(y), _current(dev))
+    st = _launch((_lib or load()).kmeans_route_combine, dev, _addr(ys), code, _addr(weights), _addr(residual), ldr,
+                 _addr(rows), _addr(offsets), n, topk, n_experts, d, _addr(y))
     _raise(st, "kmeans_route_combine")
     return y
 
@@ -894,9 +918,8 @@ def kmeans_route_combine_grad(dy, ys, rows, offsets, weights, dys=None, dweights
         dweights = torch.empty((n, topk), dtype=torch.float32, device=dev)
     else:
         _check_on(dweights, "dweights", torch.float32, (n, topk), dev)
-    st = (_lib or load()).kmeans_route_combine_grad(_addr(dy), lddy, _addr(ys), code, _addr(weights), _addr(rows),
-                                                    _addr(offsets), n, topk, n_experts, d, _addr(dys), _addr(dweights),
-                                                    _current(dev))
+    st = _launch((_lib or load()).kmeans_route_combine_grad, dev, _addr(dy), lddy, _addr(ys), code, _addr(weights),
+                 _addr(rows), _addr(offsets), n, topk, n_experts, d, _addr(dys), _addr(dweights))
     _raise(st, "kmeans_route_combine_grad")
     return dys, dweights
 
@@ -957,9 +980,8 @@ def kmeans_linear(x, w, bias=None, residual=None, offsets=None, activation="none
         ws = linear_workspace(OP_LINEAR, m, n, k, n_experts, dev)
     else:
         _workspace_on(ws, dev)
-    st = (_lib or load()).kmeans_linear(_addr(x), ldx, _addr(w), _addr(bias), _addr(residual), ldr, code, act,
-                                        _addr(offsets), m, n, k, n_experts, _addr(y), _addr(pre), _addr(ws),
-                                        ws.numel(), _current(dev))
+    st = _launch((_lib or load()).kmeans_linear, dev, _addr(x), ldx, _addr(w), _addr(bias), _addr(residual), ldr, code,
+                 act, _addr(offsets), m, n, k, n_experts, _addr(y), _addr(pre), _addr(ws), ws.numel())
     _raise(st, "kmeans_linear")
     return y, pre
 
@@ -1001,8 +1023,7 @@ def kmeans_linear_grad(dy, x, w, pre=None, offsets=None, activation="none", need
     else:
         _check(ws, "ws", torch.uint8, device=dev)
     dx, dw, db = dx if need_dx else None, dw if need_dw else None, db if need_db else None
-    st = (_lib or load()).kmeans_linear_grad(_addr(dy), lddy, _addr(x), ldx, _addr(w), _addr(pre), code, act,
-                                             _addr(offsets), m, n, k, n_experts, _addr(dx), _addr(dw), _addr(db),
-                                             _addr(ws), ws.numel(), _current(dev))
+    st = _launch((_lib or load()).kmeans_linear_grad, dev, _addr(dy), lddy, _addr(x), ldx, _addr(w), _addr(pre), code,
+                 act, _addr(offsets), m, n, k, n_experts, _addr(dx), _addr(dw), _addr(db), _addr(ws), ws.numel())
     _raise(st, "kmeans_linear_grad")
     return dx, dw, db

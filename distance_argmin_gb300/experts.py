@@ -19,21 +19,20 @@ order and keeps what the gradient needs.
 """
 from __future__ import annotations
 
-import contextlib
 import functools
 
 
 def _on_stream(fn):
-    """Run ``fn`` with its ``stream`` argument as the current CUDA stream: its
-    calls, and what they allocate, then belong to that stream."""
+    """Run ``fn`` on its tensors' device, with its ``stream`` argument as the
+    current CUDA stream: its calls, and what they allocate, then belong to that
+    stream."""
     @functools.wraps(fn)
     def wrapped(*args, stream=None, **kwargs):
-        ctx = contextlib.nullcontext()
-        if stream is not None:
-            import torch
-            ctx = torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(int(stream)))
-        with ctx:
+        import torch
+        km = _km()
+        first = args[0] if args else kwargs.get("x", kwargs.get("dy"))
+        km._on_gpu(first, "the first argument")
+        with torch.cuda.device(first.device) if stream is None else torch.cuda.stream(km._stream_on(stream, first)):
             return fn(*args, **kwargs)
     return wrapped
 
