@@ -61,6 +61,7 @@ ROUTE_MAX_EXPERTS = 4096
 ROUTE_MAX_TOPK = 32
 ROUTE_MAX_WIDTH = 16000000
 LINEAR_MAX_EXPERTS = 1024
+LINEAR_MAX_SIZE = 2 ** 31 - 256
 
 INIT_GIVEN = 0
 INIT_KMEANSPP = 1

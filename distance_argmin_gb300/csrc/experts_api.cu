@@ -50,9 +50,12 @@ RouteRows route_rows(const int32_t *rows, const int32_t *offsets, int64_t n, int
     return r;
 }
 
+// (The matrices' sizes in bytes, and the workspace's, then fit 64 bits.)
 bool linear_sizes_ok(int64_t m, int64_t n, int64_t k, int64_t n_experts) {
-    return m >= 0 && m <= kMaxIndex && n >= 1 && n <= kMaxIndex && k >= 1 && k <= kMaxIndex && n_experts >= 1 &&
-           n_experts <= KMEANS_LINEAR_MAX_EXPERTS && n_experts * n <= kMaxIndex;
+    constexpr int64_t most = KMEANS_LINEAR_MAX_SIZE, values = (int64_t)1 << 42;
+    return m >= 0 && m <= most && n >= 1 && n <= most && k >= 1 && k <= most && n_experts >= 1 &&
+           n_experts <= KMEANS_LINEAR_MAX_EXPERTS && n_experts * n <= kMaxIndex && m * n < values && m * k < values &&
+           n_experts * n * k < values;
 }
 
 int check_linear(int dtype, int activation, const int32_t *offsets, int64_t m, int64_t n, int64_t k,

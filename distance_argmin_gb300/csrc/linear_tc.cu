@@ -113,6 +113,9 @@ struct LinearTcParams {
     int clear;  // first kernel of the call: each pair has a status word of its own
 };
 
+// Rows, features and their tiles are 32-bit: the sizes end KMEANS_LINEAR_MAX_SIZE,
+// a tile below 2^31, so that no tile's end or box of rows passes it.
+//
 // The units: expert by expert, bands of BAND feature tiles, in a band the
 // feature tiles of one row tile after the other (edges and tiles: see
 // fill_tables).
@@ -166,7 +169,7 @@ struct Units {
             t.q0 = q * BN;
             t.qn = min(BN, p.out_rows - t.q0);
             t.c0 = edges[e] + chunk * p.chunk;
-            t.c1 = min(edges[e + 1], t.c0 + p.chunk);
+            t.c1 = t.c0 + min(edges[e + 1] - t.c0, p.chunk);  // (c0 + chunk may pass 2^31)
             t.slot = tiles[e + 1] - tiles[e] > 1 ? slots[e] + chunk : -1;
         } else {
             // an expert's rows in equal parts (multiples of 32) rather than full

@@ -483,6 +483,7 @@ enum {
 #define KMEANS_ROUTE_MAX_TOPK 32
 #define KMEANS_ROUTE_MAX_WIDTH 16000000
 #define KMEANS_LINEAR_MAX_EXPERTS 1024
+#define KMEANS_LINEAR_MAX_SIZE 2147483392 /* of m, n and k: 2^31 - 256 */
 
 /* Workspace of kmeans_route (0 when the sizes are invalid). */
 size_t kmeans_route_workspace_bytes(int64_t n, int64_t topk, int64_t n_experts);
@@ -534,7 +535,8 @@ size_t kmeans_linear_workspace_bytes(int grad, int64_t m, int64_t n, int64_t k, 
  * (n_experts + 1, ascending from 0, at most m) may be NULL when n_experts is
  * 1: an ordinary dense layer.  Offsets that run backwards or past m are cut
  * to what fits.  KMEANS_F16 or KMEANS_BF16; n_experts <=
- * KMEANS_LINEAR_MAX_EXPERTS; m, n, k < 2^31, n_experts * n < 2^31, n, k >= 1;
+ * KMEANS_LINEAR_MAX_EXPERTS; m, n, k <= KMEANS_LINEAR_MAX_SIZE, n_experts * n <
+ * 2^31, n, k >= 1, and no matrix of 2^42 values or more;
  * w starts on 16 bytes (KMEANS_ERR_UNSUPPORTED otherwise).  Rows of x or w
  * that do not all start on 16 bytes (k or ldx not a multiple of 8, or an odd
  * start of x) are first copied into the workspace.
