@@ -741,14 +741,16 @@ def _current(device):
     return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
-def _launch(fn, device, *args):
-    """``fn(*args, stream)`` on ``device``'s current stream, with ``device`` as the
-    current one: the library's launches and their limits are the current
-    device's, and the stream's handle alone does not name one."""
-    if _torch()._C._cuda_getDevice() == device.index:
-        return fn(*args, _current(device))
+def _elsewhere(device):
+    """True where another device is current.  The library's launches and their
+    limits are the current device's, and a stream's handle does not name one."""
+    return _torch()._C._cuda_getDevice() != device.index
+
+
+def _on_device(device, fn, *args):
+    """``fn(*args)`` with ``device`` as the current one."""
     with _torch().cuda.device(device):
-        return fn(*args, _current(device))
+        return fn(*args)
 
 
 def _stream_on(stream, tensor):
@@ -814,6 +816,8 @@ def kmeans_route(experts, n_experts: int, offsets=None, order=None, rows=None, w
     n, topk = experts.shape if experts.dim() == 2 else (experts.shape[0], 1)
     if dev.type != "cuda" or not experts.is_contiguous():
         _check(experts, "experts", experts.dtype)
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_route, experts, n_experts, offsets, order, rows, ws)
     if n_experts < 1:
         raise ValueError(f"n_experts must be at least 1, got {n_experts}")
     if offsets is None:
@@ -832,8 +836,8 @@ def kmeans_route(experts, n_experts: int, offsets=None, order=None, rows=None, w
         ws = route_workspace(n, topk, n_experts, dev)
     else:
         _workspace_on(ws, dev)
-    st = _launch((_lib or load()).kmeans_route, dev, _addr(experts), experts.element_size(), n, topk, n_experts,
-                 _addr(offsets), _addr(order), _addr(rows), _addr(ws), ws.numel())
+    st = (_lib or load()).kmeans_route(_addr(experts), experts.element_size(), n, topk, n_experts, _addr(offsets),
+                                       _addr(order), _addr(rows), _addr(ws), ws.numel(), _current(dev))
     _raise(st, "kmeans_route")
     return offsets, order, rows
 
@@ -858,6 +862,8 @@ def kmeans_route_gather(x, rows, offsets, xs=None, stream=None):
     _cuda_matrix(x, "x")
     code = _dtype_code(x, "x")
     dev, dt = x.device, x.dtype
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_route_gather, x, rows, offsets, xs)
     n, topk, n_experts = _plan(rows, offsets, dev)
     d = x.shape[1]
     ldx = _check_rows(x, "x", dt, (n, d), dev)
@@ -865,8 +871,8 @@ def kmeans_route_gather(x, rows, offsets, xs=None, stream=None):
         xs = _torch().empty((n * topk, d), dtype=dt, device=dev)
     else:
         _check_on(xs, "xs", dt, (n * topk, d), dev)
-    st = _launch((_lib or load()).kmeans_route_gather, dev, _addr(x), ldx, code, _addr(rows), _addr(offsets), n, topk,
-                 n_experts, d, _addr(xs))
+    st = (_lib or load()).kmeans_route_gather(_addr(x), ldx, code, _addr(rows), _addr(offsets), n, topk, n_experts, d,
+                                              _addr(xs), _current(dev))
     _raise(st, "kmeans_route_gather")
     return xs
 
@@ -881,6 +887,8 @@ def kmeans_route_combine(ys, rows, offsets, weights=None, residual=None, y=None,
     _cuda_matrix(ys, "ys")
     code = _dtype_code(ys, "ys")
     dev = ys.device
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_route_combine, ys, rows, offsets, weights, residual, y)
     n, topk, n_experts = _plan(rows, offsets, dev)
     d = ys.shape[1]
     _check_on(ys, "ys", ys.dtype, (n * topk, d), dev)
@@ -891,8 +899,8 @@ def kmeans_route_combine(ys, rows, offsets, weights=None, residual=None, y=None,
         y = torch.empty((n, d), dtype=ys.dtype, device=dev)
     else:
         _check_on(y, "y", ys.dtype, (n, d), dev)
-    st = _launch((_lib or load()).kmeans_route_combine, dev, _addr(ys), code, _addr(weights), _addr(residual), ldr,
-                 _addr(rows), _addr(offsets), n, topk, n_experts, d, _addr(y))
+    st = (_lib or load()).kmeans_route_combine(_addr(ys), code, _addr(weights), _addr(residual), ldr, _addr(rows),
+                                               _addr(offsets), n, topk, n_experts, d, _addr(y), _current(dev))
     _raise(st, "kmeans_route_combine")
     return y
 
@@ -906,6 +914,8 @@ def kmeans_route_combine_grad(dy, ys, rows, offsets, weights, dys=None, dweights
     _cuda_matrix(ys, "ys")
     code = _dtype_code(ys, "ys")
     dev = ys.device
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_route_combine_grad, dy, ys, rows, offsets, weights, dys, dweights)
     n, topk, n_experts = _plan(rows, offsets, dev)
     d = ys.shape[1]
     _check_on(ys, "ys", ys.dtype, (n * topk, d), dev)
@@ -919,8 +929,9 @@ def kmeans_route_combine_grad(dy, ys, rows, offsets, weights, dys=None, dweights
         dweights = torch.empty((n, topk), dtype=torch.float32, device=dev)
     else:
         _check_on(dweights, "dweights", torch.float32, (n, topk), dev)
-    st = _launch((_lib or load()).kmeans_route_combine_grad, dev, _addr(dy), lddy, _addr(ys), code, _addr(weights),
-                 _addr(rows), _addr(offsets), n, topk, n_experts, d, _addr(dys), _addr(dweights))
+    st = (_lib or load()).kmeans_route_combine_grad(_addr(dy), lddy, _addr(ys), code, _addr(weights), _addr(rows),
+                                                    _addr(offsets), n, topk, n_experts, d, _addr(dys), _addr(dweights),
+                                                    _current(dev))
     _raise(st, "kmeans_route_combine_grad")
     return dys, dweights
 
@@ -965,6 +976,8 @@ def kmeans_linear(x, w, bias=None, residual=None, offsets=None, activation="none
     torch = _torch()
     code, m, n, k, n_experts, act = _linear_args(x, w, offsets, activation)
     dev, dt = x.device, x.dtype
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_linear, x, w, bias, residual, offsets, activation, save_pre, y, pre, ws)
     ldx = _check_rows(x, "x", dt, (m, k), dev)
     if bias is not None:
         _check_on(bias, "bias", dt, tuple(w.shape[:-1]), dev)
@@ -981,8 +994,9 @@ def kmeans_linear(x, w, bias=None, residual=None, offsets=None, activation="none
         ws = linear_workspace(OP_LINEAR, m, n, k, n_experts, dev)
     else:
         _workspace_on(ws, dev)
-    st = _launch((_lib or load()).kmeans_linear, dev, _addr(x), ldx, _addr(w), _addr(bias), _addr(residual), ldr, code,
-                 act, _addr(offsets), m, n, k, n_experts, _addr(y), _addr(pre), _addr(ws), ws.numel())
+    st = (_lib or load()).kmeans_linear(_addr(x), ldx, _addr(w), _addr(bias), _addr(residual), ldr, code, act,
+                                        _addr(offsets), m, n, k, n_experts, _addr(y), _addr(pre), _addr(ws), ws.numel(),
+                                        _current(dev))
     _raise(st, "kmeans_linear")
     return y, pre
 
@@ -998,6 +1012,9 @@ def kmeans_linear_grad(dy, x, w, pre=None, offsets=None, activation="none", need
     torch = _torch()
     code, m, n, k, n_experts, act = _linear_args(x, w, offsets, activation)
     dev, dt = x.device, x.dtype
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_linear_grad, dy, x, w, pre, offsets, activation, need_dx, need_dw, need_db, dx,
+                          dw, db, ws)
     ldx = _check_rows(x, "x", dt, (m, k), dev)
     lddy = _check_rows(dy, "dy", dt, (m, n), dev)
     if act != ACTIVATIONS["none"]:
@@ -1024,7 +1041,8 @@ def kmeans_linear_grad(dy, x, w, pre=None, offsets=None, activation="none", need
     else:
         _check(ws, "ws", torch.uint8, device=dev)
     dx, dw, db = dx if need_dx else None, dw if need_dw else None, db if need_db else None
-    st = _launch((_lib or load()).kmeans_linear_grad, dev, _addr(dy), lddy, _addr(x), ldx, _addr(w), _addr(pre), code,
-                 act, _addr(offsets), m, n, k, n_experts, _addr(dx), _addr(dw), _addr(db), _addr(ws), ws.numel())
+    st = (_lib or load()).kmeans_linear_grad(_addr(dy), lddy, _addr(x), ldx, _addr(w), _addr(pre), code, act,
+                                             _addr(offsets), m, n, k, n_experts, _addr(dx), _addr(dw), _addr(db),
+                                             _addr(ws), ws.numel(), _current(dev))
     _raise(st, "kmeans_linear_grad")
     return dx, dw, db
