@@ -48,7 +48,7 @@ struct LinearLayout {
     int64_t off_x;   // x with its rows on 16 bytes, where the caller's are not
     int64_t off_w;   // w likewise (0: its rows are a multiple of 16 bytes)
     int64_t off_dz;  // dy after the activation's slope, rows on 16 bytes (gradient)
-    int64_t off_sums;     // the weight gradient's sums of chunks of rows (gradient)
+    int64_t off_sums;     // sums of chunks of a contraction
     int64_t off_partial;  // the bias gradient's sums per row tile (gradient)
     int64_t bytes;
 };

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "linear_common.cuh"
 
 namespace km {
@@ -376,6 +378,7 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
         g.a = w;
         g.pitch_w = ldw;
         g.out = dx;
+        g.partial = reinterpret_cast<float *>(ws + L.off_sums);
         e = call.template product<Product::kRows>(g);
     }
     if (e == cudaSuccess && dw && sh.m == 0)
@@ -409,11 +412,13 @@ LinearLayout linear_layout(bool grad, int64_t m, int64_t n, int64_t k, int64_t n
         L.off_w = o;
         o = align_up(o + n_experts * n * align_up(k, 8) * 2, 1024);
     }
+    // (the gradient's two products take turns with it)
+    L.off_sums = o;
+    o = align_up(o + std::max(chunk_sums_bytes(grad ? n : k),
+                              grad ? weights_split(m, n, k, n_experts).slots * n * k * 4 : 0), 1024);
     if (grad) {
         L.off_dz = o;
         o = align_up(o + m * align_up(n, 8) * 2, 1024);
-        L.off_sums = o;
-        o = align_up(o + weights_split(m, n, k, n_experts).slots * n * k * 4, 1024);
         L.off_partial = o;
         o = align_up(o + slope_tiles(m, n, n_experts) * n * 4, 1024);
     }
@@ -436,6 +441,7 @@ cudaError_t launch_linear(const LinearShape &sh, const void *x, int64_t ldx, con
     g.activation = activation;
     g.out = y;
     g.pre = pre;
+    g.partial = reinterpret_cast<float *>(ws + L.off_sums);
     return sh.bf16 ? forward_typed<__nv_bfloat16>(sh, g, L, ws, s) : forward_typed<__half>(sh, g, L, ws, s);
 }
 

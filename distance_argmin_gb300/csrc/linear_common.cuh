@@ -30,7 +30,7 @@ struct Product16 {
     int64_t ldr;
     int activation;
     void *out, *pre;
-    float *partial;           // weights: the chunks' sums (see WeightsSplit)
+    float *partial;           // the chunks' sums (see kChunk and WeightsSplit)
     void *db;                 // weights: the bias gradient, joined on the side from
     const float *bias_sums;   // the sums of `bias_rows` rows each (null: not here)
     int bias_rows;
@@ -104,10 +104,22 @@ __device__ inline void fill_tables(const int32_t *offsets, int n_experts, int64_
     }
 }
 
+// Most terms of a contraction in one accumulator.  The tensor cores cut off what
+// a sum's last bit does not hold, some 6e-9 of it per term, so that 32768 terms
+// lose up to 2e-4, half of float16's last bit, and 262144 would lose 1.7e-3.
+// Longer contractions are sums of chunks that meet in float32.  In the forward
+// and the rows product a pair goes through its unit's chunks one after the other
+// and keeps their sum so far in the workspace, a tile per CTA.
+constexpr int kChunk = 32768;
+constexpr int kPairs = 76;  // CTA pairs that run at once on the 152 SMs of a GB300
+constexpr int64_t kChunkTile = 128 * 256;  // values that a CTA has of a unit, at most
+inline int64_t chunk_sums_bytes(int64_t contraction) {
+    return contraction > kChunk ? 2 * kPairs * kChunkTile * 4 : 0;
+}
+
 // The weights product's contraction runs over an expert's rows, `chunk` of them
-// at most in one accumulator: the tensor cores cut off what a sum's last bit
-// does not hold, some 6e-9 of it per row, and few output tiles over many rows
-// would leave most SMs idle.  The chunks' sums of an expert with several meet
+// (up to kChunk, fewer where few output tiles over many rows would leave most
+// SMs idle) in one accumulator.  The chunks' sums of an expert with several meet
 // in float32 in the workspace (`slots` matrices).
 struct WeightsSplit {
     int chunk;

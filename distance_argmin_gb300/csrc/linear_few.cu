@@ -38,6 +38,7 @@ constexpr int kFewFeatures = 16, kFewRows = 8;  // of one instruction
 constexpr int kFewStep = 128;  // contraction of a warp's step
 constexpr int kFewPieces = kFewStep / 32;
 constexpr int kFewBlocks = 4;  // per SM
+constexpr int kFewSplit = 8;   // most blocks of a cluster
 static_assert(kFewRows * kFewFeatures == kFewThreads / 2, "half of the threads finish a unit");
 
 struct FewParams {
@@ -197,15 +198,17 @@ cudaError_t launch_few(const LinearShape &sh, FewParams p, cudaStream_t s) {
     const int64_t units = (int64_t)(about * p.num_p + 0.5);
     // Split the contraction where that is sooner done: a block takes in some 11
     // bytes of W a nanosecond, a unit costs it 0.3 us besides and, split, 1.7 us
-    // more for the cluster to meet.
+    // more for the cluster to meet.  Where a warp's accumulator would take more
+    // than kChunk terms it is split in any case (few_rows ends at kFewSplit).
     p.split = 1;
-    double best = 0;
-    for (int c = 1; c <= 8; c *= 2) {
+    double best = INFINITY;
+    for (int c = 1; c <= kFewSplit; c *= 2) {
         if (c > 1 && sh.k < (int64_t)c * kFewWarps * kFewStep) break;
+        if (sh.k > (int64_t)c * kFewWarps * kChunk) continue;
         const int64_t clusters = blocks / c;
         const double each = (double)(kFewFeatures * 2 * sh.k) / c / 11.0 + (c > 1 ? 2000.0 : 300.0);
         const double cost = (double)((units + clusters - 1) / clusters) * each;
-        if (c == 1 || cost < best) {
+        if (cost < best) {
             best = cost;
             p.split = c;
         }
@@ -236,7 +239,10 @@ cudaError_t launch_few(const LinearShape &sh, FewParams p, cudaStream_t s) {
 // their rows are not known here, so few of them on average; an expert with more
 // reads its part of W again (from L2) every 8 rows (64 experts, n = 4096, k =
 // 2048: 128 rows 159 us, 6.3 TB/s; 1024 rows 167 us in the tensor-core units).
-bool few_rows(const LinearShape &sh) { return sh.m <= kFewRows || (sh.offsets && sh.m <= 2 * (int64_t)sh.n_experts); }
+bool few_rows(const LinearShape &sh) {
+    return sh.k <= (int64_t)kFewSplit * kFewWarps * kChunk &&
+           (sh.m <= kFewRows || (sh.offsets && sh.m <= 2 * (int64_t)sh.n_experts));
+}
 
 cudaError_t launch_linear_few(const LinearShape &sh, const Product16 &g, uint32_t *status, cudaStream_t s) {
     FewParams p{};

@@ -53,6 +53,7 @@ namespace lt {
 constexpr int BP = 256;            // features per unit (UMMA M of the pair)
 constexpr int BP_CTA = BP / 2;
 constexpr int BK = 64;             // contraction per stage: 128 bytes of 16-bit values
+constexpr int CHUNK_BLOCKS = kChunk / BK;
 constexpr int EPI_WARPS = 16;       // four per tensor-memory lane quarter, a quarter of the columns each
 constexpr int WARP_TMA = EPI_WARPS, WARP_MMA = WARP_TMA + 1, WARP_RELAY = WARP_TMA + 2;
 constexpr int THREADS = (WARP_RELAY + 1) * 32;
@@ -425,10 +426,52 @@ struct PairStatus {
     __device__ __forceinline__ void flag(uint32_t f) const { flag_error(word(), f); }
 };
 
+// All but the last chunk of a row product's long contraction, for columns [c0,
+// end) of a warp's 32 features: each accumulator (two alternate, BN columns from
+// `acc` on) is added to the sum so far, which stays with the CTA, a lane reading
+// what it wrote; the last chunk's accumulator takes the sum of the others and
+// goes on as the unit's.  `at`: column 0 of the lane's feature.  Returns the last
+// chunk's count of accumulator uses, or -1 where a wait gave up.
+template <int BN>
+__device__ int sum_chunks(float *at, int c0, int end, uint32_t acc, uint32_t full, uint32_t empty, int left, int use,
+                          const PairStatus &status) {
+    for (bool first = true;; first = false, ++use) {
+        const uint32_t buf = (uint32_t)use & 1u;
+        if (!mbar_wait_warp(full + 8 * buf, (use >> 1) & 1, status)) return -1;
+        tc_fence_after();
+        left -= kChunk;
+#pragma unroll 1
+        for (int c = c0; c < end; c += 8) {
+            float *sum = at + c * lt::BP_CTA;
+            uint32_t r[8];
+            __syncwarp();
+            tmem_ld_8_issue(acc + buf * BN + (uint32_t)c, r);
+            tmem_ld_8_wait(r);
+            if (!first) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + sum[j * lt::BP_CTA]);
+            }
+            if (left > 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j * lt::BP_CTA] = __uint_as_float(r[j]);
+            } else {
+                tmem_st_8(acc + buf * BN + (uint32_t)c, r);
+            }
+        }
+        __syncwarp();
+        if (left <= 0) return use;
+        tc_fence_before();
+        __syncwarp();
+        if (lane_id() == 0) mbar_arrive_cluster(empty + 8 * buf);
+    }
+}
+
 // A value that all lanes of a converged warp hold, in a uniform register.
 __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
-template <Product MODE, int BN, typename T>
+// LONG: the row products where the contraction is longer than kChunk (a variant of
+// its own: the others' epilogue loses 8% to its registers where it sets the pace).
+template <Product MODE, int BN, typename T, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmB32, const __grid_constant__ CUtensorMap tmOut,
@@ -526,7 +569,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             }
             const Unit t = mine.of_lane(i);
             const bool zero = t.c1 <= t.c0;  // nothing to multiply: rows of no expert, experts without rows
-            const int buf = use & 1;
             const int f = t.p0 + rank * lt::BP_CTA + quarter * 32;  // this warp's first feature
             float bias = 0.f;
             if (MODE == Product::kForward && p.bias && !zero && f + lane < p.cols)
@@ -536,8 +578,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             fin.f = f;
             fin.out_row = MODE == Product::kWeights ? (int64_t)t.expert * p.out_rows + t.q0 : (int64_t)t.q0;
             fin.add = MODE == Product::kForward && p.residual && !zero;
+            bool ready = zero;
+            if (LONG && t.c1 - t.c0 > kChunk) {
+                use = sum_chunks<BN>(p.partial + (int64_t)blockIdx.x * kChunkTile + quarter * 32 + lane, fin.c0, fin.end,
+                                     tmem_base + ((uint32_t)(quarter * 32) << 16), bar(C::T_FULL),
+                                     map_to_cta(bar(C::T_EMPTY), 0), t.c1 - t.c0, use, status);
+                if (use < 0) break;
+                ready = true;
+            }
+            const int buf = use & 1;
             fin.prefetch();
-            if (!zero) {
+            if (!ready) {
                 bool ok = mbar_wait_warp(bar(C::T_FULL + buf), (use >> 1) & 1, status);
                 // a part that meets at barriers goes on together or not at all
                 if (MODE == Product::kWeights) ok = named_barrier_all(1 + part, 128, ok);
@@ -689,37 +740,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                     const uint64_t b0 = B_MN ? umma_smem_desc_mn(sbase + C::A_BYTES, 64 * lt::BK * 2, 1024)
                                              : umma_smem_desc(sbase + C::A_BYTES, 1024, kLayoutSW128);
                     const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32);
-                    const int buf = use & 1;
-                    const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
-                    if (!mbar_wait_converged(bar(C::T_EMPTY + buf), ((use >> 1) & 1) ^ 1, status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    uint32_t more = 0;  // the first MMA of a unit clears the accumulator
-                    for (int left = kblocks; left > 0; --left) {
-                        const uint32_t off = (uint32_t)s * (C::STAGE >> 4);
-                        const uint32_t a_lo = (uint32_t)a0 + off, b_lo = (uint32_t)b0 + off;
-                        if (!mbar_wait_converged(bar((RELAY ? C::READY : C::FULL) + s), phase, status)) {
+                    // (a chunk of rows is a unit of its own in the weights product)
+                    for (int blocks = kblocks; blocks > 0 && ok; blocks -= LONG ? lt::CHUNK_BLOCKS : blocks) {
+                        const int buf = use & 1;
+                        const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
+                        if (!mbar_wait_converged(bar(C::T_EMPTY + buf), ((use >> 1) & 1) ^ 1, status)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        if (leader) {
-                            mma_16_ss_pair(acc, a_lo, a_hi, b_lo, b_hi, idesc, more);
-                            mma_16_ss_pair(acc, a_lo + A_STEP, a_hi, b_lo + B_STEP, b_hi, idesc, 1u);
-                            mma_16_ss_pair(acc, a_lo + 2 * A_STEP, a_hi, b_lo + 2 * B_STEP, b_hi, idesc, 1u);
-                            mma_16_ss_pair(acc, a_lo + 3 * A_STEP, a_hi, b_lo + 3 * B_STEP, b_hi, idesc, 1u);
-                            mma_commit_pair_multicast(bar(C::EMPTY + s), 0x3);
+                        uint32_t more = 0;  // the first MMA of a chunk clears the accumulator
+                        for (int left = LONG ? min(blocks, lt::CHUNK_BLOCKS) : blocks; left > 0; --left) {
+                            const uint32_t off = (uint32_t)s * (C::STAGE >> 4);
+                            const uint32_t a_lo = (uint32_t)a0 + off, b_lo = (uint32_t)b0 + off;
+                            if (!mbar_wait_converged(bar((RELAY ? C::READY : C::FULL) + s), phase, status)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            if (leader) {
+                                mma_16_ss_pair(acc, a_lo, a_hi, b_lo, b_hi, idesc, more);
+                                mma_16_ss_pair(acc, a_lo + A_STEP, a_hi, b_lo + B_STEP, b_hi, idesc, 1u);
+                                mma_16_ss_pair(acc, a_lo + 2 * A_STEP, a_hi, b_lo + 2 * B_STEP, b_hi, idesc, 1u);
+                                mma_16_ss_pair(acc, a_lo + 3 * A_STEP, a_hi, b_lo + 3 * B_STEP, b_hi, idesc, 1u);
+                                mma_commit_pair_multicast(bar(C::EMPTY + s), 0x3);
+                            }
+                            __syncwarp();
+                            more = 1u;
+                            advance();
                         }
+                        if (!ok) break;
+                        if (leader) mma_commit_pair_multicast(bar(C::T_FULL + buf), 0x3);
                         __syncwarp();
-                        more = 1u;
-                        advance();
+                        ++use;
                     }
-                    if (!ok) break;
-                    if (leader) mma_commit_pair_multicast(bar(C::T_FULL + buf), 0x3);
-                    __syncwarp();
-                    ++use;
                 }
             }
         }
@@ -766,7 +820,7 @@ bool encode(CUtensorMap *map, bool bf16, const void *base, int rank, const uint6
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <Product MODE, int BN, typename T>
+template <Product MODE, int BN, typename T, bool LONG>
 cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcParams &p, cudaStream_t s) {
     using C = lt::Cfg<BN, MODE == Product::kWeights>;
     static std::once_flag once[kMaxDevices];
@@ -775,7 +829,7 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
     cudaGetDevice(&dev);
     const int slot = dev >= 0 && dev < kMaxDevices ? dev : 0;
     once_per_device(once, [&] {
-        err[slot].store((int)cudaFuncSetAttribute(linear_tc_kernel<MODE, BN, T>,
+        err[slot].store((int)cudaFuncSetAttribute(linear_tc_kernel<MODE, BN, T, LONG>,
                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, lt::SMEM_LIMIT));
     });
     if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
@@ -808,27 +862,40 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
     const int64_t row_tiles = MODE == Product::kWeights
                                   ? (sh.n + BN - 1) / BN * (sh.n_experts + sh.m / p.chunk + 1)
                                                         : (sh.m + BN - 1) / BN + (sh.offsets ? sh.n_experts : 0);
-    const int64_t most = std::min(device_sm_count() / 2, kMaxPairWords), units = row_tiles * p.num_p;
+    static_assert(kPairs <= kMaxPairWords, "a status word each");
+    const int64_t most = std::min(device_sm_count() / 2, kPairs), units = row_tiles * p.num_p;
     const unsigned pairs = (unsigned)(units < most ? units : most);
-    return launch_kernel(true, linear_tc_kernel<MODE, BN, T>, dim3(2 * (pairs ? pairs : 1)), dim3(lt::THREADS),
+    return launch_kernel(true, linear_tc_kernel<MODE, BN, T, LONG>, dim3(2 * (pairs ? pairs : 1)), dim3(lt::THREADS),
                          C::smem_bytes(sh.n_experts), s, tmA, tmB, tmB32, tmOut, p);
 }
 
-template <Product MODE, int BN>
+template <Product MODE, int BN, bool LONG = false>
 cudaError_t launch_typed(const LinearShape &sh, const Product16 &g, const LinearTcParams &p, cudaStream_t s) {
-    return sh.bf16 ? launch_tc<MODE, BN, __nv_bfloat16>(sh, g, p, s) : launch_tc<MODE, BN, __half>(sh, g, p, s);
+    return sh.bf16 ? launch_tc<MODE, BN, __nv_bfloat16, LONG>(sh, g, p, s)
+                   : launch_tc<MODE, BN, __half, LONG>(sh, g, p, s);
+}
+
+// The row products in units of `bn` rows (long contractions: 64 or 256, which
+// takes fewer rows as well).
+template <Product MODE>
+cudaError_t launch_rows(int bn, const LinearShape &sh, const Product16 &g, const LinearTcParams &p, cudaStream_t s) {
+    if (p.contraction > kChunk)
+        return bn == 64 ? launch_typed<MODE, 64, true>(sh, g, p, s) : launch_typed<MODE, 256, true>(sh, g, p, s);
+    return bn == 256   ? launch_typed<MODE, 256>(sh, g, p, s)
+           : bn == 128 ? launch_typed<MODE, 128>(sh, g, p, s)
+                       : launch_typed<MODE, 64>(sh, g, p, s);
 }
 
 }  // namespace
 
 WeightsSplit weights_split(int64_t m, int64_t n, int64_t k, int64_t n_experts) {
-    constexpr int64_t longest = 32768, shortest = 512;
+    constexpr int64_t longest = kChunk, shortest = 512;
     // output tiles of all experts, and how many chunks of an expert's average
-    // rows would give every pair of SMs a unit (152 of them on a GB300)
-    const int64_t tiles = (n + 127) / 128 * ((k + lt::BP - 1) / lt::BP) * n_experts, pairs = 76;
+    // rows would give every pair of SMs a unit
+    const int64_t tiles = (n + 127) / 128 * ((k + lt::BP - 1) / lt::BP) * n_experts;
     int64_t chunk = longest;
-    if (2 * tiles <= pairs) {
-        const int64_t parts = pairs / tiles, average = m / n_experts;
+    if (2 * tiles <= kPairs) {
+        const int64_t parts = kPairs / tiles, average = m / n_experts;
         chunk = align_up((average + parts - 1) / parts, lt::BK);
         chunk = chunk < shortest ? shortest : chunk > longest ? longest : chunk;
     }
@@ -872,7 +939,7 @@ cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product1
     // (24 rows through 8192 x 2048 10.9 us, 15.3 in units of 256; the gradient's
     // two products of 257 rows, 1000 x 520, 12.9 and 10.0 us in units of 256, 9.5
     // and 8.2 as chosen).
-    const int64_t pairs = device_sm_count() / 2;
+    const int64_t pairs = std::min(device_sm_count() / 2, kPairs);
     auto one_round = [&](int64_t bn) {
         const int64_t tiles = mode == Product::kWeights ? (sh.n + bn - 1) / bn * (sh.n_experts + sh.m / p.chunk)
                                                         : (sh.m + bn - 1) / bn + (sh.offsets ? sh.n_experts : 0);
@@ -883,13 +950,8 @@ cudaError_t launch_linear_tc(Product mode, const LinearShape &sh, const Product1
                               : launch_typed<Product::kWeights, 256>(sh, g, p, s);
     const int64_t rows = sh.m / sh.n_experts;
     const int bn = rows <= 64 || one_round(64) ? 64 : rows <= 128 || one_round(128) ? 128 : 256;
-    if (mode == Product::kForward)
-        return bn == 256   ? launch_typed<Product::kForward, 256>(sh, g, p, s)
-               : bn == 128 ? launch_typed<Product::kForward, 128>(sh, g, p, s)
-                           : launch_typed<Product::kForward, 64>(sh, g, p, s);
-    return bn == 256   ? launch_typed<Product::kRows, 256>(sh, g, p, s)
-           : bn == 128 ? launch_typed<Product::kRows, 128>(sh, g, p, s)
-                       : launch_typed<Product::kRows, 64>(sh, g, p, s);
+    return mode == Product::kForward ? launch_rows<Product::kForward>(bn, sh, g, p, s)
+                                     : launch_rows<Product::kRows>(bn, sh, g, p, s);
 }
 
 }  // namespace km

@@ -398,6 +398,14 @@ __device__ __forceinline__ void tmem_ld_8_wait(uint32_t (&r)[8]) {
                  : "memory");
 }
 
+// The same columns back into tensor memory, done when it returns.
+__device__ __forceinline__ void tmem_st_8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // 16 lanes x 16 consecutive columns in the layout of an MMA fragment: this
 // thread receives rows lane / 4 and 8 + lane / 4, columns 2 (lane % 4) and the
 // next (r[0..1], r[2..3]), and the same 8 columns on (r[4..7]).  Waited for with

@@ -463,7 +463,9 @@ int kmeans_fit(const float *X, float *C, int64_t *labels, float *best_dist, int3
  * (KMEANS_F32, KMEANS_F16 or KMEANS_BF16) whose rows are contiguous; a row
  * pitch argument ld* counts elements and is at least the row's length.
  * Matrices without a pitch argument, and every output, are contiguous.  All
- * arithmetic is float32 with one rounding per output.  Values may be infinite
+ * arithmetic is float32 with one rounding per output; a product's sum is joined
+ * from chunks of at most 32768 terms, which bounds what the tensor cores cut off
+ * (2^-12 of it where all terms have one sign).  Values may be infinite
  * or NaN: they spread as the formulas say and never reach another token's or
  * another expert's results; what belongs to a dropped slot is never read into
  * a result.  Zero tokens, rows or choices are allowed.
@@ -551,9 +553,7 @@ int kmeans_linear(const void *x, int64_t ldx, const void *w, const void *bias, c
  * allowed for KMEANS_ACT_NONE).  dx (m, k), dw (n_experts, n, k) and db
  * (n_experts, n) may each be NULL; dx is zero in rows of no expert, dw and db
  * in experts without rows.  The products take dz rounded to the matrices'
- * type; db sums it before that rounding.  Sums over an expert's rows are joined
- * in float32 from chunks of at most 32768 rows.  The residual's gradient is
- * dy. */
+ * type; db sums it before that rounding.  The residual's gradient is dy. */
 int kmeans_linear_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *w,
                        const void *pre, int dtype, int activation, const int32_t *offsets, int64_t m,
                        int64_t n, int64_t k, int64_t n_experts, void *dx, void *dw, void *db,
