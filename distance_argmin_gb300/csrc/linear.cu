@@ -29,7 +29,7 @@ struct AlignJob {
 };
 
 __global__ void __launch_bounds__(kAlignThreads) linear_align_kernel(const AlignJob w, int groups, const AlignJob x,
-                                                                     int row_bytes, int64_t pitch_out,
+                                                                     int64_t row_bytes, int64_t pitch_out,
                                                                      const int32_t *offsets, uint32_t *clear) {
     griddep_wait();
     if (clear && (blockIdx.x | threadIdx.x) == 0u) *clear = 0u;
@@ -39,16 +39,16 @@ __global__ void __launch_bounds__(kAlignThreads) linear_align_kernel(const Align
     const int block = of_w ? (int)blockIdx.x % w.blocks : (int)blockIdx.x - w_blocks;
     const int group = of_w ? (int)blockIdx.x / w.blocks : 0;
     if (of_w && offsets && offsets[group + 1] <= offsets[group]) return;
-    const int pieces = (row_bytes + 15) / 16;
+    const int pieces = (int)((row_bytes + 15) / 16);
     // a row's pieces go to neighbouring threads
     for (int64_t i = (int64_t)block * kAlignThreads + threadIdx.x; i < job.rows * pieces;
          i += (int64_t)job.blocks * kAlignThreads) {
         const int64_t r = i / pieces;
-        const int at = (int)(i - r * pieces) * 16;
+        const int64_t at = (i - r * pieces) * 16;
         const int64_t row = group * job.rows + r;
         // (dst's rows are padded to whole pieces)
         *reinterpret_cast<uint4 *>(job.dst + row * pitch_out + at) =
-            load_piece<false>(job.src + row * job.pitch + at, min(16, row_bytes - at), job.in);
+            load_piece<false>(job.src + row * job.pitch + at, (int)min((int64_t)16, row_bytes - at), job.in);
     }
 }
 
@@ -300,7 +300,7 @@ struct Call {
         const AlignJob jx = do_x ? job(*x, *ldx, 1, sh.m, L.off_x) : AlignJob{};
         const int64_t ldd = align_up(sh.k, 8);
         const cudaError_t e = launch_kernel(true, linear_align_kernel, dim3((unsigned)(jw.blocks * sh.n_experts + jx.blocks)),
-                                            dim3(kAlignThreads), 0, s, jw, sh.n_experts, jx, (int)(sh.k * 2), ldd * 2,
+                                            dim3(kAlignThreads), 0, s, jw, sh.n_experts, jx, sh.k * 2, ldd * 2,
                                             sh.offsets, first());
         if (do_w) {
             *w = jw.dst;

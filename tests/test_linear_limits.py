@@ -70,3 +70,28 @@ def test_rows_up_to_the_limit(gpu_lib, split):
     assert torch.equal(y[:ends].double(), x[:ends].double() @ w[0].double().t())
     del y, wf, x, dy
     torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k", [2 ** 30 + 8, 2 ** 30 + 1])
+def test_a_row_of_more_than_two_to_the_31_bytes(gpu_lib, k):
+    """As it lies, and brought to 16 bytes first: terms at both ends and between,
+    zeros elsewhere."""
+    torch.cuda.empty_cache()
+    x, w = torch.zeros(1, k, dtype=torch.float16, device="cuda"), torch.zeros(1, k, dtype=torch.float16, device="cuda")
+    at = torch.tensor([0, 7, 12345, 2 ** 21 + 3, 2 ** 29 + 5, 2 ** 30 - 1, k - 1], device="cuda")
+    x[0, at] = torch.tensor([1, 2, 4, 8, 16, 32, 64], dtype=torch.float16, device="cuda")
+    w[0, at] = torch.tensor([3, -1, 5, 7, -2, 1, 3], dtype=torch.float16, device="cuda")
+    ws = gpu_lib.linear_workspace(gpu_lib.OP_LINEAR, 1, 1, k)
+    y, _ = gpu_lib.kmeans_linear(x, w, ws=ws)
+    assert gpu_lib.kmeans_device_status(ws) == gpu_lib.KMEANS_OK
+    assert y.item() == (x[0, at] * w[0, at]).double().sum().item()
+    del ws
+    dy = torch.full((1, 1), 3.0, dtype=torch.float16, device="cuda")
+    ws = gpu_lib.linear_workspace(gpu_lib.OP_LINEAR_GRAD, 1, 1, k)
+    dx, dw, db = gpu_lib.kmeans_linear_grad(dy, x, w, ws=ws)
+    assert gpu_lib.kmeans_device_status(ws) == gpu_lib.KMEANS_OK
+    assert torch.equal(dx[0, at], 3 * w[0, at]) and torch.equal(dw[0, at], 3 * x[0, at]) and db.item() == 3
+    assert int(dx.count_nonzero()) == int(dw.count_nonzero()) == at.numel()
+    del x, w, dx, dw, ws
+    torch.cuda.empty_cache()
