@@ -220,10 +220,10 @@ __global__ void __launch_bounds__(kSlopeThreads) linear_bias_join_kernel(const f
     __syncthreads();
     const int64_t col = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (col >= n) return;
-    float s = 0.f;
+    LongSum s;
 #pragma unroll 8
-    for (int u = range[0]; u < range[1]; ++u) s += partial[(int64_t)u * n + col];
-    db[(int64_t)expert * n + col] = narrow<T>(s);
+    for (int u = range[0]; u < range[1]; ++u) s.add(partial[(int64_t)u * n + col]);
+    db[(int64_t)expert * n + col] = narrow<T>(s.value());
 }
 
 // dw[e] = the sums of expert e's chunks of rows, in order, where it has several.
@@ -242,10 +242,10 @@ __global__ void __launch_bounds__(kSlopeThreads) linear_weights_join_kernel(cons
         const float *from = partial + (int64_t)slots[e] * size;
         for (int64_t i = (int64_t)blockIdx.x * kSlopeThreads + threadIdx.x; i < size;
              i += (int64_t)gridDim.x * kSlopeThreads) {
-            float s = 0.f;
+            LongSum s;
 #pragma unroll 8
-            for (int c = 0; c < chunks; ++c) s += from[(int64_t)c * size + i];
-            dw[(int64_t)e * size + i] = narrow<T>(s);
+            for (int c = 0; c < chunks; ++c) s.add(from[(int64_t)c * size + i]);
+            dw[(int64_t)e * size + i] = narrow<T>(s.value());
         }
     }
 }

@@ -547,12 +547,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             for (int64_t i = (int64_t)blockIdx.x * lt::EPI_WARPS + warp; i < (int64_t)p.n_experts * groups;
                  i += (int64_t)gridDim.x * lt::EPI_WARPS) {
                 const int e = (int)(i / groups), col = (int)(i - (int64_t)e * groups) * 8 + (lane & 7);
-                float s = 0.f;
+                LongSum part_sum;
                 if (col < p.out_rows) {
 #pragma unroll 8
                     for (int tile = bias_tiles[e] + sub; tile < bias_tiles[e + 1]; tile += 4)
-                        s += p.bias_sums[(int64_t)tile * p.out_rows + col];
+                        part_sum.add(p.bias_sums[(int64_t)tile * p.out_rows + col]);
                 }
+                float s = part_sum.value();
                 s += __shfl_xor_sync(0xffffffffu, s, 8);
                 s += __shfl_xor_sync(0xffffffffu, s, 16);
                 if (sub == 0 && col < p.out_rows) static_cast<T *>(p.db)[(int64_t)e * p.out_rows + col] = narrow<T>(s);

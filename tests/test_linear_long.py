@@ -104,3 +104,29 @@ def test_few_rows(gpu_lib, m, n, k):
     close(y[:, n - 20:], exact(x, w[n - 20:]), k, torch.float16)
     del w
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("m,experts,need_dw", [(1 << 27, 1, True), (1 << 27, 1, False), (1 << 25, 1024, True)])
+def test_bias_gradient_of_many_equal_rows(gpu_lib, m, experts, need_dw):
+    """Alone, and beside the weight gradient (all rows with one of 1024 experts).
+    A tile's sum is of 128 rows, each within 2^-24 per addition; the tiles' sums
+    meet with their errors, the last rounding is float16's 2^-11."""
+    torch.cuda.empty_cache()
+    dy = torch.full((m, 8), 0.0004, dtype=torch.float16, device="cuda")
+    x = torch.zeros(m, 8, dtype=torch.float16, device="cuda")
+    w = torch.zeros((experts, 8, 8) if experts > 1 else (8, 8), dtype=torch.float16, device="cuda")
+    offsets = None
+    if experts > 1:
+        offsets = torch.zeros(experts + 1, dtype=torch.int32, device="cuda")
+        offsets[8:] = m
+    _, dw, db = gpu_lib.kmeans_linear_grad(dy, x, w, offsets=offsets, need_dx=False, need_dw=need_dw)
+    want = m * dy[0, 0].double()
+    got = (db[7] if experts > 1 else db).double()
+    assert bool(((got - want).abs() <= (2.0 ** -11 + 130 * 2.0 ** -24) * want).all()), ((got - want) / want).tolist()
+    if experts > 1:
+        assert not db[:7].any() and not db[8:].any()
+    dy[m // 2, 3] = float("inf")  # an infinite sum stays one
+    _, _, db = gpu_lib.kmeans_linear_grad(dy, x, w, offsets=offsets, need_dx=False, need_dw=need_dw)
+    assert (db[7] if experts > 1 else db)[3].item() == float("inf") and int(torch.isfinite(db).logical_not().sum()) == 1
+    del x, dy
+    torch.cuda.empty_cache()
