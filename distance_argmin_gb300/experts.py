@@ -9,7 +9,7 @@ of tokens is all the training the choice needs.  A learned choice passes its
 own ids and weights.
 
     offsets, order, rows = kmeans_route(ids)            slots sorted by expert
-    xs = kmeans_route_gather(x, rows)                   tokens in that order
+    xs = kmeans_route_gather(x, rows, offsets)          tokens in that order
     h  = act(xs w1[e]^T + b1[e])                        kmeans_linear
     ys = h w2[e]^T + b2[e]                              kmeans_linear
     y[t] = residual[t] + sum_j weights[t, j] ys[rows[t, j]]   kmeans_route_combine
