@@ -130,3 +130,17 @@ def test_bias_gradient_of_many_equal_rows(gpu_lib, m, experts, need_dw):
     assert (db[7] if experts > 1 else db)[3].item() == float("inf") and int(torch.isfinite(db).logical_not().sum()) == 1
     del x, dy
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("m", [40, 700])
+def test_a_starved_long_contraction_reports_a_timeout(gpu_lib, monkeypatch, m):
+    k = 70000
+    x, w = positive((m, k), torch.bfloat16, 1), positive((264, k), torch.bfloat16, 2, 2.0 ** -8)
+    ws = gpu_lib.linear_workspace(gpu_lib.OP_LINEAR, m, 264, k)
+    ref = gpu_lib.kmeans_linear(x, w)[0]
+    monkeypatch.setenv("KMEANS_GB300_TEST_STARVE_PIPELINE", "1")
+    gpu_lib.kmeans_linear(x, w, ws=ws)
+    assert gpu_lib.kmeans_device_status(ws) == gpu_lib.KMEANS_ERR_DEVICE_TIMEOUT
+    monkeypatch.delenv("KMEANS_GB300_TEST_STARVE_PIPELINE")
+    assert torch.equal(gpu_lib.kmeans_linear(x, w, ws=ws)[0], ref)
+    assert gpu_lib.kmeans_device_status(ws) == gpu_lib.KMEANS_OK
