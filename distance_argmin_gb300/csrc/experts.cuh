@@ -9,6 +9,8 @@
 
 namespace km {
 
+constexpr int kSMs = 152;  // of a GB300, which the rules on sizes are made for
+
 // ------------------------------------------------------------------ routing
 // One thread-block cluster sorts all slots; nothing but the status word needs
 // device scratch.

@@ -53,7 +53,10 @@ __global__ void __launch_bounds__(kAlignThreads) linear_align_kernel(const Align
 }
 
 // dz = dy act'(pre), rounded to the matrices' type, and the bias gradient's
-// partial sums from the same read.  A block takes up to 128 rows of one expert
+// partial sums from the same read.  The rounding is the products' operand type:
+// float32 or a pair of 16-bit parts would double their tensor time and dz's
+// traffic, for outputs that are rounded as much themselves (bf16 dx and dW 2.3e-3
+// off, 1.7e-3 with dz in float32; 32 experts 4096 x 2048, 16384 rows).  A block takes up to 128 rows of one expert
 // by 256 columns: a lane 8 columns (16 bytes where the rows allow), a warp every
 // eighth row.  Its column sums of the unrounded values go to one row of
 // `partial` per row tile; linear_bias_join_kernel adds an expert's in order, so
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(kSlopeThreads) linear_weights_join_kernel(cons
 // 1000 columns: 16 blocks of 128 rows, or 68 of 16).
 int slope_rows(int64_t m, int64_t n) {
     int rows = kSlopeMaxRows;
-    while (rows > kSlopeMinRows && (m + rows - 1) / rows * ((n + kSlopeCols - 1) / kSlopeCols) < 2 * 152) rows /= 2;
+    while (rows > kSlopeMinRows && (m + rows - 1) / rows * ((n + kSlopeCols - 1) / kSlopeCols) < 2 * kSMs) rows /= 2;
     return rows;
 }
 
@@ -392,7 +395,7 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
         e = call.template product<Product::kWeights>(g);
         if (e == cudaSuccess && split.slots > 0) {
             const int64_t size = sh.n * sh.k, blocks = (size + kSlopeThreads - 1) / kSlopeThreads;
-            e = launch_kernel(true, linear_weights_join_kernel<T>, dim3((unsigned)(blocks < 152 * 8 ? blocks : 152 * 8)),
+            e = launch_kernel(true, linear_weights_join_kernel<T>, dim3((unsigned)std::min(blocks, (int64_t)kSMs * 8)),
                               dim3(kSlopeThreads), 3 * (size_t)(sh.n_experts + 2) * 4, s,
                               static_cast<const float *>(g.partial), sh.offsets, sh.n_experts, sh.m, split.chunk, size,
                               static_cast<T *>(dw));

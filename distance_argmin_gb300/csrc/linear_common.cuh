@@ -125,7 +125,7 @@ __device__ inline void fill_tables(const int32_t *offsets, int n_experts, int64_
 // and the rows product a pair goes through its unit's chunks one after the other
 // and keeps their sum so far in the workspace, a tile per CTA.
 constexpr int kChunk = 32768;
-constexpr int kPairs = 76;  // CTA pairs that run at once on the 152 SMs of a GB300
+constexpr int kPairs = kSMs / 2;  // CTA pairs that run at once
 constexpr int64_t kChunkTile = 128 * 256;  // values that a CTA has of a unit, at most
 inline int64_t chunk_sums_bytes(int64_t contraction) {
     return contraction > kChunk ? 2 * kPairs * kChunkTile * 4 : 0;

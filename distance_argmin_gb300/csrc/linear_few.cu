@@ -233,7 +233,8 @@ cudaError_t launch_few(const LinearShape &sh, FewParams p, cudaStream_t s) {
 
 }  // namespace
 
-// Where W is read once and little is done with it.  One expert: up to 8 rows
+// Where W is read once and little is done with it, up to 2^21 input features
+// (kFewSplit blocks of kFewWarps accumulators of kChunk terms).  One expert: up to 8 rows
 // (n = 8192, k = 2048: 8.1 us; the tensor-core units take 10.9 us for any
 // number up to 24, 16 rows in two tiles of this kernel 11.2).  Several experts:
 // their rows are not known here, so few of them on average; an expert with more

@@ -201,9 +201,9 @@ struct Units {
 // slower: dense 8192 x 8192 x 2048 170 us against 164, and one bulk copy per row
 // of 128 features 174).
 // Up to some 600 products per output the epilogue sets the pace, not the tensor
-// pipe.  Each SM then finishes 128 x 256 values, of a long matrix with 64 products each, say, in 2.7
-// us without an activation and 3.7 with GELU: shared memory 64% and issue 40
-// to 70% busy.  (Without the path for parts whose rows all exist, and with
+// pipe.  Each SM then finishes 128 x 256 values, of a long matrix with 64 products
+// each, say, in 2.8 us without an activation and 3.8 with GELU: shared memory 64%
+// and issue 40 to 70% busy.  (Without the path for parts whose rows all exist, and with
 // activations one value at a time, 3.0 and 4.8 us; 16 or 32 accumulator columns
 // per load 3.1 and 3.5.)
 template <Product MODE, int BN, typename T>

@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kMoveThreads) route_combine_kernel(const MoveP
     }
 }
 
-constexpr int64_t kManyTokens = 152 * 16;
+constexpr int64_t kManyTokens = kSMs * 16;
 
 // A group of tpr threads per token walks the row, CH choices at a time and U
 // words of each in flight; a block whose groups are wider than a warp joins
@@ -655,7 +655,7 @@ cudaError_t combine_typed(const RouteRows &r, const void *ys, const float *weigh
     if (vec == 4) return combine_as<4, T, 1, 8>(p, ys, weights, residual, pitch, y, s);
     if (vec == 8) return combine_as<8, T, 2, 4>(p, ys, weights, residual, pitch, y, s);
     // several words per thread only where the rows still fill the SMs
-    const bool many = p.n * p.words >= 152 * 2048 * 4;
+    const bool many = p.n * p.words >= kSMs * 2048 * 4;
     if (p.topk > 3 || !many) return combine_as<16, T, 4, 1>(p, ys, weights, residual, pitch, y, s);
     if (p.topk > 1) return combine_as<16, T, 2, 2>(p, ys, weights, residual, pitch, y, s);
     return combine_as<16, T, 1, 4>(p, ys, weights, residual, pitch, y, s);
