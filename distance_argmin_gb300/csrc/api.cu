@@ -591,8 +591,8 @@ int kmeans_device_status(const void *ws, void *stream) {
     uint32_t st = 0;
     if (cudaMemcpy(&st, ws, sizeof(st), cudaMemcpyDeviceToHost) != cudaSuccess) return KMEANS_ERR_CUDA;
     uint32_t words[kMaxPairWords];
-    const uint32_t pairs = st >> kPairCountShift;
-    if (pairs > 0 && pairs <= (uint32_t)kMaxPairWords) {
+    const uint32_t pairs = (st & ~kPairWordsMarkMask) >> kPairCountShift;
+    if ((st & kPairWordsMarkMask) == kPairWordsMark && pairs <= (uint32_t)kMaxPairWords) {
         if (cudaMemcpy(words, static_cast<const uint8_t *>(ws) + kPairWordsOffset, pairs * sizeof(uint32_t),
                        cudaMemcpyDeviceToHost) != cudaSuccess)
             return KMEANS_ERR_CUDA;

@@ -98,7 +98,10 @@ enum : uint32_t {
     kFlagExchange = 4u,  // sharded k-means++: no rank's exchange block owned a trial
     kFlagsMask = 0xffu,
 };
-constexpr int kPairCountShift = 8;  // status word: how many pair words hold flags too
+// The status word that says that so many pair words hold flags too (marked, so
+// that a workspace no call has used is not taken for one).
+constexpr uint32_t kPairWordsMark = 0xC3000000u, kPairWordsMarkMask = 0xff000000u;
+constexpr int kPairCountShift = 8;
 constexpr int kMaxPairWords = 128;
 
 struct WsHeader {

@@ -524,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     // come after; the other pairs have theirs, whatever the workspace held
     if (p.clear && rank == 0 && threadIdx.x == 0) {
         *status.word() = 0u;
-        if (pair == 0) *p.status = (uint32_t)num_pairs << kPairCountShift;
+        if (pair == 0) *p.status = kPairWordsMark | (uint32_t)num_pairs << kPairCountShift;
     }
     if (warp == 0) fill_tables(p.offsets, p.n_experts, p.m, WEIGHTS ? p.chunk : BN, edges, tiles, WEIGHTS ? slots : nullptr, lane);
     if (WEIGHTS && p.db && warp == 1)  // (the second table is a copy of the edges)
