@@ -13,7 +13,8 @@ Names follow the C ABI: ``kmeans_assign``, ``kmeans_assign_ffma``,
 and the shard entry points (``kmeans_lloyd_iter_partial``,
 ``kmeans_reduce_partials``, ``kmeanspp_shard_*``) that ``sharded.py`` drives
 across processes.  ``kmeans_route*`` and ``kmeans_linear*`` are the expert
-routing and the experts' products that ``experts.py`` makes a layer of.
+routing and the experts' products that ``experts.py`` makes a layer of;
+``kmeans_gate`` and ``kmeans_layernorm`` (with ``_grad``) stand around them.
 """
 from __future__ import annotations
 
@@ -62,6 +63,8 @@ ROUTE_MAX_TOPK = 32
 ROUTE_MAX_WIDTH = 16000000
 LINEAR_MAX_EXPERTS = 1024
 LINEAR_MAX_SIZE = 2 ** 31 - 256
+GATE_SCORES = {"softmax": 0, "sigmoid": 1}
+GATE_MAX_GROUPS = 32
 
 INIT_GIVEN = 0
 INIT_KMEANSPP = 1
@@ -89,6 +92,8 @@ EXPORTS = (
     "kmeanspp_shard_dist", "kmeanspp_shard_commit", "kmeanspp_rows_read",
     "kmeans_route_workspace_bytes", "kmeans_route", "kmeans_route_gather", "kmeans_route_combine",
     "kmeans_route_combine_grad", "kmeans_linear_workspace_bytes", "kmeans_linear", "kmeans_linear_grad",
+    "kmeans_gate", "kmeans_gate_grad", "kmeans_layernorm_workspace_bytes", "kmeans_layernorm",
+    "kmeans_layernorm_grad",
 )
 
 _lock = threading.Lock()
@@ -186,6 +191,17 @@ def load(path: str | None = None):
         lib.kmeans_linear.restype = INT
         lib.kmeans_linear_grad.argtypes = [P, I64, P, I64, P, P, INT, INT, P, I64, I64, I64, I64, P, P, P, P, SZ, P]
         lib.kmeans_linear_grad.restype = INT
+        F = ctypes.c_float
+        lib.kmeans_gate.argtypes = [P, I64, INT, INT, P, I64, I64, I64, I64, I64, INT, F, P, P, P]
+        lib.kmeans_gate.restype = INT
+        lib.kmeans_gate_grad.argtypes = [P, P, I64, INT, INT, P, I64, I64, I64, INT, F, P, P]
+        lib.kmeans_gate_grad.restype = INT
+        lib.kmeans_layernorm_workspace_bytes.argtypes = [I64, I64]
+        lib.kmeans_layernorm_workspace_bytes.restype = SZ
+        lib.kmeans_layernorm.argtypes = [P, I64, INT, P, P, F, I64, I64, P, P, P, P]
+        lib.kmeans_layernorm.restype = INT
+        lib.kmeans_layernorm_grad.argtypes = [P, I64, P, I64, INT, P, P, P, P, I64, I64, I64, P, P, P, P, SZ, P]
+        lib.kmeans_layernorm_grad.restype = INT
         _lib = lib
         return lib
 
@@ -1046,3 +1062,184 @@ def kmeans_linear_grad(dy, x, w, pre=None, offsets=None, activation="none", need
                                              _addr(ws), ws.numel(), _current(dev))
     _raise(st, "kmeans_linear_grad")
     return dx, dw, db
+
+
+# --------------------------------------------- around the experts: gate, norm
+def _gate_args(logits, scores, topk, scale):
+    """Checked ``(code, n, n_experts, score code)``."""
+    _cuda_matrix(logits, "logits")
+    code = _dtype_code(logits, "logits")
+    if scores not in GATE_SCORES:
+        raise ValueError(f"unknown scores {scores!r} (one of {', '.join(GATE_SCORES)})")
+    n, n_experts = logits.shape
+    if n_experts < 1 or not 0 <= topk <= n_experts:
+        raise ValueError(f"topk must be in [0, {n_experts}] for {n_experts} experts, got {topk}")
+    if not math.isfinite(scale):
+        raise ValueError(f"scale must be finite, got {scale}")
+    return code, n, n_experts, GATE_SCORES[scores]
+
+
+def kmeans_gate(logits, topk: int, scores="softmax", bias=None, groups: int = 1, topk_groups: int = None,
+                renormalize=True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """Each token's experts from the router's ``logits`` (n, n_experts) ->
+    ``(ids (n, topk) int32, weights (n, topk) float32)``, what kmeans_route and
+    kmeans_route_combine take.
+
+    The ``topk`` experts with the largest scores (``softmax`` or ``sigmoid`` of
+    the logits) plus ``bias`` (n_experts,) float32, in descending order, equal
+    ones by index; of ``groups`` groups of neighbouring experts only the
+    ``topk_groups`` (all by default) with the largest sums of their two best
+    take part.  The weights are the scores times ``scale``, with ``renormalize``
+    divided by their sum.  An expert whose logit or bias is -inf is closed; a
+    token with fewer open ones gets ids of -1 with weight 0."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_gate, logits, topk, scores, bias, groups, topk_groups, renormalize, scale, ids,
+                          weights)
+    torch = _torch()
+    topk, groups, scale = int(topk), int(groups), float(scale)
+    code, n, n_experts, kind = _gate_args(logits, scores, topk, scale)
+    topk_groups = groups if topk_groups is None else int(topk_groups)
+    if groups < 1 or n_experts % groups or not 1 <= topk_groups <= groups:
+        raise ValueError(f"groups must divide the {n_experts} experts and topk_groups be one of 1 .. groups, got"
+                         f" {groups} and {topk_groups}")
+    dev = logits.device
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_gate, logits, topk, scores, bias, groups, topk_groups, renormalize, scale, ids,
+                          weights)
+    ldl = _check_rows(logits, "logits", logits.dtype, (n, n_experts), dev)
+    if bias is not None:
+        _check_on(bias, "bias", torch.float32, (n_experts,), dev)
+    if ids is None:
+        ids = torch.empty((n, topk), dtype=torch.int32, device=dev)
+    else:
+        _check_on(ids, "ids", torch.int32, (n, topk), dev)
+    if weights is None:
+        weights = torch.empty((n, topk), dtype=torch.float32, device=dev)
+    else:
+        _check_on(weights, "weights", torch.float32, (n, topk), dev)
+    st = (_lib or load()).kmeans_gate(_addr(logits), ldl, code, kind, _addr(bias), n, n_experts, topk, groups,
+                                      topk_groups, bool(renormalize), scale, _addr(ids), _addr(weights), _current(dev))
+    _raise(st, "kmeans_gate")
+    return ids, weights
+
+
+def kmeans_gate_grad(dweights, logits, ids, scores="softmax", renormalize=True, scale: float = 1.0, dlogits=None,
+                     stream=None):
+    """Gradient of kmeans_gate's weights -> ``dlogits (n, n_experts)``, from
+    ``dweights`` (n, topk) float32 and the logits, ids and options of the
+    forward call."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_gate_grad, dweights, logits, ids, scores, renormalize, scale, dlogits)
+    torch = _torch()
+    scale = float(scale)
+    _cuda_matrix(ids, "ids")
+    topk = ids.shape[1]
+    code, n, n_experts, kind = _gate_args(logits, scores, topk, scale)
+    dev, dt = logits.device, logits.dtype
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_gate_grad, dweights, logits, ids, scores, renormalize, scale, dlogits)
+    ldl = _check_rows(logits, "logits", dt, (n, n_experts), dev)
+    _check_on(ids, "ids", torch.int32, (n, topk), dev)
+    _check_on(dweights, "dweights", torch.float32, (n, topk), dev)
+    if dlogits is None:
+        dlogits = torch.empty((n, n_experts), dtype=dt, device=dev)
+    else:
+        _check_on(dlogits, "dlogits", dt, (n, n_experts), dev)
+    st = (_lib or load()).kmeans_gate_grad(_addr(dweights), _addr(logits), ldl, code, kind, _addr(ids), n, n_experts,
+                                           topk, bool(renormalize), scale, _addr(dlogits), _current(dev))
+    _raise(st, "kmeans_gate_grad")
+    return dlogits
+
+
+def layernorm_workspace(n: int, d: int, device=None):
+    """A device workspace for ``kmeans_layernorm_grad`` (uint8 tensor)."""
+    nbytes = int(load().kmeans_layernorm_workspace_bytes(n, d))
+    if nbytes == 0:
+        raise KMeansError(KMEANS_ERR_INVALID_ARG, "kmeans_layernorm_workspace_bytes")
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device or "cuda")
+
+
+def kmeans_layernorm(x, weight=None, bias=None, eps: float = 1e-5, save_stats=False, y=None, mean=None, rstd=None,
+                     stream=None):
+    """``(x - mean) * rstd * weight + bias`` per row of x (n, d) -> ``(y (n, d),
+    mean (n,) or None, rstd (n,) or None)``, rstd = 1 / sqrt(variance + eps).
+    ``weight`` and ``bias`` (d,) of x's type, 1 and 0 by default.
+    ``save_stats`` (or a ``mean`` and ``rstd`` to write into) keeps the rows'
+    float32 statistics for kmeans_layernorm_grad."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_layernorm, x, weight, bias, eps, save_stats, y, mean, rstd)
+    torch = _torch()
+    _cuda_matrix(x, "x")
+    code = _dtype_code(x, "x")
+    eps = float(eps)
+    if not (eps >= 0 and math.isfinite(eps)):
+        raise ValueError(f"eps must be at least 0, got {eps}")
+    dev, dt = x.device, x.dtype
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_layernorm, x, weight, bias, eps, save_stats, y, mean, rstd)
+    n, d = x.shape
+    ldx = _check_rows(x, "x", dt, (n, d), dev)
+    if weight is not None:
+        _check_on(weight, "weight", dt, (d,), dev)
+    if bias is not None:
+        _check_on(bias, "bias", dt, (d,), dev)
+    if y is None:
+        y = torch.empty((n, d), dtype=dt, device=dev)
+    else:
+        _check_on(y, "y", dt, (n, d), dev)
+    if mean is not None:
+        _check_on(mean, "mean", torch.float32, (n,), dev)
+    elif save_stats:
+        mean = torch.empty(n, dtype=torch.float32, device=dev)
+    if rstd is not None:
+        _check_on(rstd, "rstd", torch.float32, (n,), dev)
+    elif save_stats:
+        rstd = torch.empty(n, dtype=torch.float32, device=dev)
+    st = (_lib or load()).kmeans_layernorm(_addr(x), ldx, code, _addr(weight), _addr(bias), eps, n, d, _addr(y),
+                                           _addr(mean), _addr(rstd), _current(dev))
+    _raise(st, "kmeans_layernorm")
+    return y, mean, rstd
+
+
+def kmeans_layernorm_grad(dy, x, mean, rstd, weight=None, residual=None, need_dx=True, need_dweight=True,
+                          need_dbias=True, dx=None, dweight=None, dbias=None, ws=None, stream=None):
+    """Gradient of kmeans_layernorm -> ``(dx (n, d), dweight (d,), dbias (d,))``
+    (None where not needed).  ``mean`` and ``rstd`` are what it kept;
+    ``residual`` (n, d), the gradient that reaches x past the norm, is added to
+    dx."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_layernorm_grad, dy, x, mean, rstd, weight, residual, need_dx, need_dweight,
+                          need_dbias, dx, dweight, dbias, ws)
+    torch = _torch()
+    _cuda_matrix(x, "x")
+    code = _dtype_code(x, "x")
+    dev, dt = x.device, x.dtype
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_layernorm_grad, dy, x, mean, rstd, weight, residual, need_dx, need_dweight,
+                          need_dbias, dx, dweight, dbias, ws)
+    n, d = x.shape
+    ldx = _check_rows(x, "x", dt, (n, d), dev)
+    lddy = _check_rows(dy, "dy", dt, (n, d), dev)
+    ldr = _check_rows(residual, "residual", dt, (n, d), dev) if residual is not None else 0
+    _check_on(mean, "mean", torch.float32, (n,), dev)
+    _check_on(rstd, "rstd", torch.float32, (n,), dev)
+    if weight is not None:
+        _check_on(weight, "weight", dt, (d,), dev)
+    outs = []
+    for name, t, need, shape in (("dx", dx, need_dx, (n, d)), ("dweight", dweight, need_dweight, (d,)),
+                                 ("dbias", dbias, need_dbias, (d,))):
+        if need and t is None:
+            t = torch.empty(shape, dtype=dt, device=dev)
+        elif need:
+            _check_on(t, name, dt, shape, dev)
+        outs.append(t if need else None)
+    if ws is None:
+        ws = layernorm_workspace(n, d, dev)
+    else:
+        _workspace_on(ws, dev)
+    dx, dweight, dbias = outs
+    st = (_lib or load()).kmeans_layernorm_grad(_addr(dy), lddy, _addr(x), ldx, code, _addr(mean), _addr(rstd),
+                                                _addr(weight), _addr(residual), ldr, n, d, _addr(dx), _addr(dweight),
+                                                _addr(dbias), _addr(ws), ws.numel(), _current(dev))
+    _raise(st, "kmeans_layernorm_grad")
+    return dx, dweight, dbias

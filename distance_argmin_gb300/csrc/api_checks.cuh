@@ -14,6 +14,11 @@ constexpr int64_t kMaxIndex = 0x7fffffffLL;  // labels and member lists use 32-b
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+inline bool known_dtype(int dtype) { return dtype == KMEANS_F32 || dtype == KMEANS_F16 || dtype == KMEANS_BF16; }
+inline bool elem_aligned(const void *p, int dtype) {
+    return (reinterpret_cast<uintptr_t>(p) & (dtype == KMEANS_F32 ? 3u : 1u)) == 0;
+}
+
 inline int check_ws(const void *ws, size_t ws_bytes, size_t need) {
     if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return KMEANS_ERR_WORKSPACE;
     if (ws_bytes < need) return KMEANS_ERR_WORKSPACE;

@@ -20,12 +20,6 @@ int route_limits(int64_t topk, int64_t n_experts) {
                                                                                      : KMEANS_ERR_UNSUPPORTED;
 }
 
-bool known_dtype(int dtype) { return dtype == KMEANS_F32 || dtype == KMEANS_F16 || dtype == KMEANS_BF16; }
-
-bool elem_aligned(const void *p, int dtype) {
-    return (reinterpret_cast<uintptr_t>(p) & (dtype == KMEANS_F32 ? 3u : 1u)) == 0;
-}
-
 // What the three row-moving calls share.  `rows` and `offsets` may be null
 // only when there is no slot to look up.
 int check_rows(const int32_t *rows, const int32_t *offsets, int dtype, int64_t n, int64_t topk, int64_t n_experts,

@@ -1,0 +1,48 @@
+// What stands around the experts in a model: the gate that chooses them, the
+// layer norm in front and the cross entropy at the end: layouts and launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace km {
+
+// --------------------------------------------------------------------- gate
+struct GateShape {
+    int64_t n;
+    int n_experts, topk;
+    int groups, topk_groups;
+    bool sigmoid;      // else softmax
+    bool renormalize;
+    float scale;
+};
+
+cudaError_t launch_gate(const GateShape &g, int dtype, const void *logits, int64_t ldl, const float *bias, int32_t *ids,
+                        float *weights, cudaStream_t s);
+cudaError_t launch_gate_grad(const GateShape &g, int dtype, const float *dweights, const void *logits, int64_t ldl,
+                             const int32_t *ids, void *dlogits, cudaStream_t s);
+
+// --------------------------------------------------------------- layer norm
+struct NormShape {
+    int64_t n, d;
+    int dtype;
+};
+
+// Sums of dy and dy * normalised over some rows each, joined at the end.
+struct NormLayout {
+    int64_t off_partial;
+    int64_t bytes;
+};
+
+NormLayout norm_layout(int64_t n, int64_t d);
+
+cudaError_t launch_norm(const NormShape &sh, const void *x, int64_t ldx, const void *weight, const void *bias, float eps,
+                        void *y, float *mean, float *rstd, cudaStream_t s);
+cudaError_t launch_norm_grad(const NormShape &sh, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                             const float *mean, const float *rstd, const void *weight, const void *residual,
+                             int64_t ldr, void *dx, void *dweight, void *dbias, const NormLayout &L, uint8_t *ws,
+                             cudaStream_t s);
+
+}  // namespace km

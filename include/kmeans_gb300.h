@@ -559,6 +559,64 @@ int kmeans_linear_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx,
                        int64_t n, int64_t k, int64_t n_experts, void *dx, void *dw, void *db,
                        void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the experts: the learned choice of them, and layer norm.  The
+ * conventions are the expert layer's.
+ * --------------------------------------------------------------------------- */
+enum { KMEANS_GATE_SOFTMAX = 0, KMEANS_GATE_SIGMOID = 1 };
+
+#define KMEANS_GATE_MAX_GROUPS 32
+
+/* A token's experts and their weights from the router's logits (n, n_experts)
+ * with pitch ldl: with the scores s = softmax(l) or 1 / (1 + exp(-l)),
+ * c = s + bias (bias (n_experts) float32 or NULL) and `groups` groups of
+ * n_experts / groups neighbours, the topk_groups groups stay whose two largest
+ * c have the largest sum, and of their experts the topk with the largest c are
+ * taken, in descending order; equal ones by index.  ids (n, topk) int32 are
+ * what kmeans_route takes; weights (n, topk) float32 what kmeans_route_combine
+ * takes: scale * s, with `renormalize` scale * s / (the sum of the chosen s).
+ * An expert whose logit or bias is minus infinity is closed; a token with
+ * fewer than topk open experts gets ids of -1 with weight 0 after them.  Only
+ * weights know of `renormalize` and `scale`, only the choice of the bias.
+ * The order is that of exact arithmetic (without a bias, the logits' own; with
+ * one, that of values in float64).  NaN counts as the largest value, and a
+ * token that holds one has it in its weights.
+ * topk <= n_experts <= KMEANS_ROUTE_MAX_EXPERTS, topk <= KMEANS_ROUTE_MAX_TOPK,
+ * groups <= KMEANS_GATE_MAX_GROUPS divides n_experts, topk_groups <= groups. */
+int kmeans_gate(const void *logits, int64_t ldl, int dtype, int scores, const float *bias, int64_t n,
+                int64_t n_experts, int64_t topk, int64_t groups, int64_t topk_groups, int renormalize,
+                float scale, int32_t *ids, float *weights, void *stream);
+
+/* Gradient of the weights of kmeans_gate: dlogits (n, n_experts) from dweights
+ * (n, topk) float32 (kmeans_route_combine_grad writes them), the logits and
+ * the ids.  The choice has no gradient.  Ids outside [0, n_experts) and closed
+ * experts take no part; one named twice gets the sum. */
+int kmeans_gate_grad(const float *dweights, const void *logits, int64_t ldl, int dtype, int scores,
+                     const int32_t *ids, int64_t n, int64_t n_experts, int64_t topk, int renormalize,
+                     float scale, void *dlogits, void *stream);
+
+/* y = (x - mean) * rstd * weight + bias per row, with the mean and the
+ * variance v about it of the row's d values and rstd = 1 / sqrt(v + eps).
+ * x (n, d) with pitch ldx, y (n, d); weight and bias (d) of x's type or NULL
+ * (1 and 0); mean and rstd (n) float32 or NULL: kept for the gradient.  y may
+ * be x itself when ldx == d.  d <= KMEANS_ROUTE_MAX_WIDTH, eps >= 0. */
+int kmeans_layernorm(const void *x, int64_t ldx, int dtype, const void *weight, const void *bias, float eps,
+                     int64_t n, int64_t d, void *y, float *mean, float *rstd, void *stream);
+
+/* Workspace of kmeans_layernorm_grad (0 when the sizes are invalid). */
+size_t kmeans_layernorm_workspace_bytes(int64_t n, int64_t d);
+
+/* Gradient of kmeans_layernorm: with g = dy * weight and h = (x - mean) * rstd,
+ * dx = rstd * (g - mean(g) - h * mean(g * h)) + residual, dweight = sum dy * h
+ * and dbias = sum dy over the rows, in a fixed order.  dy and x (n, d) with
+ * their pitches, residual (n, d) with pitch ldr or NULL (the gradient that
+ * reaches x past the norm).  dx (n, d), dweight (d) and dbias (d) may each be
+ * NULL; dx may be dy, or residual, itself when it is contiguous. */
+int kmeans_layernorm_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx, int dtype, const float *mean,
+                          const float *rstd, const void *weight, const void *residual, int64_t ldr, int64_t n,
+                          int64_t d, void *dx, void *dweight, void *dbias, void *ws, size_t ws_bytes,
+                          void *stream);
+
 /* Synchronises `stream` and returns the device status word of the last call
  * that used `ws` (KMEANS_OK, KMEANS_ERR_DEVICE_TIMEOUT or
  * KMEANS_ERR_DEVICE_LABEL), or KMEANS_ERR_CUDA if the stream reports an error. */
