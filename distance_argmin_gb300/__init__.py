@@ -14,7 +14,8 @@ and the shard entry points (``kmeans_lloyd_iter_partial``,
 ``kmeans_reduce_partials``, ``kmeanspp_shard_*``) that ``sharded.py`` drives
 across processes.  ``kmeans_route*`` and ``kmeans_linear*`` are the expert
 routing and the experts' products that ``experts.py`` makes a layer of;
-``kmeans_gate`` and ``kmeans_layernorm`` (with ``_grad``) stand around them.
+``kmeans_gate``, ``kmeans_layernorm`` and ``kmeans_cross_entropy`` (each with
+its ``_grad``) stand around them.
 """
 from __future__ import annotations
 
@@ -53,6 +54,9 @@ OP_UPDATE_PARTIAL = 11
 # kmeans_linear_workspace_bytes
 OP_LINEAR = 0
 OP_LINEAR_GRAD = 1
+# kmeans_cross_entropy_workspace_bytes
+OP_CROSS_ENTROPY = 0
+OP_CROSS_ENTROPY_GRAD = 1
 
 F32 = 0
 F16 = 1
@@ -65,6 +69,7 @@ LINEAR_MAX_EXPERTS = 1024
 LINEAR_MAX_SIZE = 2 ** 31 - 256
 GATE_SCORES = {"softmax": 0, "sigmoid": 1}
 GATE_MAX_GROUPS = 32
+CROSS_ENTROPY_MAX_WIDTH = 32768
 
 INIT_GIVEN = 0
 INIT_KMEANSPP = 1
@@ -93,7 +98,8 @@ EXPORTS = (
     "kmeans_route_workspace_bytes", "kmeans_route", "kmeans_route_gather", "kmeans_route_combine",
     "kmeans_route_combine_grad", "kmeans_linear_workspace_bytes", "kmeans_linear", "kmeans_linear_grad",
     "kmeans_gate", "kmeans_gate_grad", "kmeans_layernorm_workspace_bytes", "kmeans_layernorm",
-    "kmeans_layernorm_grad",
+    "kmeans_layernorm_grad", "kmeans_cross_entropy_workspace_bytes", "kmeans_cross_entropy",
+    "kmeans_cross_entropy_grad",
 )
 
 _lock = threading.Lock()
@@ -202,6 +208,12 @@ def load(path: str | None = None):
         lib.kmeans_layernorm.restype = INT
         lib.kmeans_layernorm_grad.argtypes = [P, I64, P, I64, INT, P, P, P, P, I64, I64, I64, P, P, P, P, SZ, P]
         lib.kmeans_layernorm_grad.restype = INT
+        lib.kmeans_cross_entropy_workspace_bytes.argtypes = [INT, I64, I64, I64]
+        lib.kmeans_cross_entropy_workspace_bytes.restype = SZ
+        lib.kmeans_cross_entropy.argtypes = [P, I64, P, INT, P, INT, F, I64, I64, I64, P, P, P, SZ, P]
+        lib.kmeans_cross_entropy.restype = INT
+        lib.kmeans_cross_entropy_grad.argtypes = [P, P, I64, P, INT, P, INT, P, F, I64, I64, I64, P, P, P, SZ, P]
+        lib.kmeans_cross_entropy_grad.restype = INT
         _lib = lib
         return lib
 
@@ -1064,7 +1076,7 @@ def kmeans_linear_grad(dy, x, w, pre=None, offsets=None, activation="none", need
     return dx, dw, db
 
 
-# --------------------------------------------- around the experts: gate, norm
+# --------------------------------- around the experts: gate, norm, cross entropy
 def _gate_args(logits, scores, topk, scale):
     """Checked ``(code, n, n_experts, score code)``."""
     _cuda_matrix(logits, "logits")
@@ -1243,3 +1255,109 @@ def kmeans_layernorm_grad(dy, x, mean, rstd, weight=None, residual=None, need_dx
                                                 _addr(dbias), _addr(ws), ws.numel(), _current(dev))
     _raise(st, "kmeans_layernorm_grad")
     return dx, dweight, dbias
+
+
+def cross_entropy_workspace(op: int, m: int, n: int, k: int, device=None):
+    """A device workspace for ``kmeans_cross_entropy`` (OP_CROSS_ENTROPY) or
+    ``kmeans_cross_entropy_grad`` (OP_CROSS_ENTROPY_GRAD, enough for both) of m
+    rows, n classes and k features (uint8 tensor)."""
+    nbytes = int(load().kmeans_cross_entropy_workspace_bytes(op, m, n, k))
+    if nbytes == 0:
+        raise KMeansError(KMEANS_ERR_INVALID_ARG, "kmeans_cross_entropy_workspace_bytes")
+    return _torch().empty(nbytes, dtype=_torch().uint8, device=device or "cuda")
+
+
+def _classes_args(x, w, labels, scale):
+    """Checked ``(code, m, n, k, ldx)``; all on x's device."""
+    torch = _torch()
+    code, dev = _dtype_code(x, "x"), x.device
+    m, k = x.shape
+    ldx = _check_rows(x, "x", x.dtype, (m, k), dev)
+    if not (isinstance(w, torch.Tensor) and w.dim() == 2):
+        raise ValueError("w must be (n, k), a row for every class")
+    _check_on(w, "w", x.dtype, w.shape, dev)
+    if w.shape[1] != k:
+        raise ValueError(f"w has {w.shape[1]} features, x has {k}")
+    if not isinstance(labels, torch.Tensor):
+        raise TypeError("labels must be a torch.Tensor")
+    if labels.dtype is not torch.int64 and labels.dtype is not torch.int32:
+        raise TypeError(f"labels must be int32 or int64, got {labels.dtype}")
+    _check_on(labels, "labels", labels.dtype, (m,), dev)
+    if not (scale > 0 and math.isfinite(scale)):
+        raise ValueError(f"scale must be positive, got {scale}")
+    return code, m, w.shape[0], k, ldx
+
+
+def kmeans_cross_entropy(x, w, labels, scale: float = 1.0, loss=None, lse=None, ws=None, stream=None):
+    """Softmax cross entropy of the rows x (m, k) against the classes w (n, k),
+    whose m x n logits ``scale * x w^T`` are never stored -> ``(loss (m,),
+    lse (m,))`` float32: the logarithm of the sum of a row's exponentials, and
+    that minus its label's logit.
+
+    ``labels`` (m,) int32 or int64; a negative one marks a row that does not
+    count: loss and lse 0, and whatever it holds reaches nothing else.
+    float16 or bfloat16."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_cross_entropy, x, w, labels, scale, loss, lse, ws)
+    torch = _torch()
+    _cuda_matrix(x, "x")
+    dev, scale = x.device, float(scale)
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_cross_entropy, x, w, labels, scale, loss, lse, ws)
+    code, m, n, k, ldx = _classes_args(x, w, labels, scale)
+    if loss is None:
+        loss = torch.empty(m, dtype=torch.float32, device=dev)
+    else:
+        _check_on(loss, "loss", torch.float32, (m,), dev)
+    if lse is None:
+        lse = torch.empty(m, dtype=torch.float32, device=dev)
+    else:
+        _check_on(lse, "lse", torch.float32, (m,), dev)
+    if ws is None:
+        ws = cross_entropy_workspace(OP_CROSS_ENTROPY, m, n, k, dev)
+    else:
+        _workspace_on(ws, dev)
+    st = (_lib or load()).kmeans_cross_entropy(_addr(x), ldx, _addr(w), code, _addr(labels), labels.element_size(),
+                                               scale, m, n, k, _addr(loss), _addr(lse), _addr(ws), ws.numel(),
+                                               _current(dev))
+    _raise(st, "kmeans_cross_entropy")
+    return loss, lse
+
+
+def kmeans_cross_entropy_grad(dloss, x, w, labels, lse, scale: float = 1.0, need_dx=True, need_dw=True, dx=None,
+                              dw=None, ws=None, stream=None):
+    """Gradient of kmeans_cross_entropy's losses times ``dloss`` (m,) float32 ->
+    ``(dx (m, k), dw (n, k))`` (None where not needed); ``lse`` is what it
+    returned for the same x, w and labels.  For the mean over the rows that
+    count, dloss is 1 / their number."""
+    if stream is not None:
+        return _on_stream(stream, kmeans_cross_entropy_grad, dloss, x, w, labels, lse, scale, need_dx, need_dw, dx, dw,
+                          ws)
+    torch = _torch()
+    _cuda_matrix(x, "x")
+    dev, dt, scale = x.device, x.dtype, float(scale)
+    if _elsewhere(dev):
+        return _on_device(dev, kmeans_cross_entropy_grad, dloss, x, w, labels, lse, scale, need_dx, need_dw, dx, dw, ws)
+    code, m, n, k, ldx = _classes_args(x, w, labels, scale)
+    _check_on(dloss, "dloss", torch.float32, (m,), dev)
+    _check_on(lse, "lse", torch.float32, (m,), dev)
+    if need_dx:
+        if dx is None:
+            dx = torch.empty((m, k), dtype=dt, device=dev)
+        else:
+            _check_on(dx, "dx", dt, (m, k), dev)
+    if need_dw:
+        if dw is None:
+            dw = torch.empty((n, k), dtype=dt, device=dev)
+        else:
+            _check_on(dw, "dw", dt, (n, k), dev)
+    if ws is None:
+        ws = cross_entropy_workspace(OP_CROSS_ENTROPY_GRAD, m, n, k, dev)
+    else:
+        _workspace_on(ws, dev)
+    dx, dw = dx if need_dx else None, dw if need_dw else None
+    st = (_lib or load()).kmeans_cross_entropy_grad(_addr(dloss), _addr(x), ldx, _addr(w), code, _addr(labels),
+                                                    labels.element_size(), _addr(lse), scale, m, n, k, _addr(dx),
+                                                    _addr(dw), _addr(ws), ws.numel(), _current(dev))
+    _raise(st, "kmeans_cross_entropy_grad")
+    return dx, dw

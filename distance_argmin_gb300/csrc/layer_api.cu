@@ -1,4 +1,4 @@
-// C ABI of the gate and the layer norm (declared in include/kmeans_gb300.h):
+// C ABI of the gate, the layer norm and the cross entropy (declared in include/kmeans_gb300.h):
 // argument validation and the launches.
 #include <cuda_runtime.h>
 #include <math.h>
@@ -31,6 +31,26 @@ GateShape gate_shape(int scores, int64_t n, int64_t n_experts, int64_t topk, int
 }
 
 bool norm_sizes_ok(int64_t n, int64_t d) { return n >= 0 && n <= kMaxIndex && d >= 1 && d <= kMaxIndex; }
+
+// (The matrices' and the workspace's sizes in bytes then fit 64 bits.)
+bool xent_sizes_ok(int64_t m, int64_t n, int64_t k) {
+    constexpr int64_t most = KMEANS_LINEAR_MAX_SIZE, values = (int64_t)1 << 42;
+    return m >= 0 && m <= most && n >= 1 && n <= most && k >= 1 && k <= most && m * n < values && m * k < values &&
+           n * k < values;
+}
+
+int check_xent(int dtype, const void *x, int64_t ldx, const void *w, const void *labels, int id_bytes, float scale,
+               int64_t m, int64_t n, int64_t k) {
+    if (!known_dtype(dtype) || (id_bytes != 4 && id_bytes != 8) || !xent_sizes_ok(m, n, k) || !(scale > 0.f) ||
+        !isfinite(scale))
+        return KMEANS_ERR_INVALID_ARG;
+    if (m > 0 && (!x || !w || !labels || ldx < k)) return KMEANS_ERR_INVALID_ARG;
+    if (!elem_aligned(x, dtype) || !elem_aligned(w, dtype) ||
+        (reinterpret_cast<uintptr_t>(labels) & (uintptr_t)(id_bytes - 1)))
+        return KMEANS_ERR_INVALID_ARG;
+    if (dtype == KMEANS_F32 || k > KMEANS_CROSS_ENTROPY_MAX_WIDTH || !aligned16(w)) return KMEANS_ERR_UNSUPPORTED;
+    return KMEANS_OK;
+}
 
 }  // namespace
 
@@ -95,6 +115,39 @@ int kmeans_layernorm_grad(const void *dy, int64_t lddy, const void *x, int64_t l
     if (wst != KMEANS_OK) return wst;
     return cuda_status(launch_norm_grad({n, d, dtype}, dy, lddy, x, ldx, mean, rstd, weight, residual, ldr, dx, dweight,
                                         dbias, L, static_cast<uint8_t *>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+size_t kmeans_cross_entropy_workspace_bytes(int grad, int64_t m, int64_t n, int64_t k) {
+    if ((grad != 0 && grad != 1) || !xent_sizes_ok(m, n, k) || k > KMEANS_CROSS_ENTROPY_MAX_WIDTH) return 0;
+    return (size_t)xent_layout(grad != 0, m, n, k).bytes;
+}
+
+int kmeans_cross_entropy(const void *x, int64_t ldx, const void *w, int dtype, const void *labels, int id_bytes,
+                         float scale, int64_t m, int64_t n, int64_t k, float *loss, float *lse, void *ws,
+                         size_t ws_bytes, void *stream) {
+    const int st = check_xent(dtype, x, ldx, w, labels, id_bytes, scale, m, n, k);
+    if (st != KMEANS_OK) return st;
+    if ((m > 0 && (!loss || !lse)) || !aligned4(loss) || !aligned4(lse)) return KMEANS_ERR_INVALID_ARG;
+    const XentLayout L = xent_layout(false, m, n, k);
+    const int wst = check_ws(ws, ws_bytes, (size_t)L.bytes);
+    if (wst != KMEANS_OK) return wst;
+    return cuda_status(launch_xent({m, n, k, labels, id_bytes, scale, dtype == KMEANS_BF16}, x, ldx, w, loss, lse, L,
+                                   static_cast<uint8_t *>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+int kmeans_cross_entropy_grad(const float *dloss, const void *x, int64_t ldx, const void *w, int dtype,
+                              const void *labels, int id_bytes, const float *lse, float scale, int64_t m, int64_t n,
+                              int64_t k, void *dx, void *dw, void *ws, size_t ws_bytes, void *stream) {
+    const int st = check_xent(dtype, x, ldx, w, labels, id_bytes, scale, m, n, k);
+    if (st != KMEANS_OK) return st;
+    if ((m > 0 && (!dloss || !lse)) || !aligned4(dloss) || !aligned4(lse) || !elem_aligned(dx, dtype) ||
+        !elem_aligned(dw, dtype))
+        return KMEANS_ERR_INVALID_ARG;
+    const XentLayout L = xent_layout(true, m, n, k);
+    const int wst = check_ws(ws, ws_bytes, (size_t)L.bytes);
+    if (wst != KMEANS_OK) return wst;
+    return cuda_status(launch_xent_grad({m, n, k, labels, id_bytes, scale, dtype == KMEANS_BF16}, dloss, x, ldx, w, lse,
+                                        dx, dw, L, static_cast<uint8_t *>(ws), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

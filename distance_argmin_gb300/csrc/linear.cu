@@ -406,6 +406,14 @@ cudaError_t grad_typed(const LinearShape &sh, const void *dy, int64_t lddy, cons
 
 }  // namespace
 
+cudaError_t launch_align(const void *src, int64_t pitch, int64_t rows, int64_t cols, void *dst, cudaStream_t s) {
+    const int64_t blocks = (rows * ((cols + 7) / 8) + kAlignThreads - 1) / kAlignThreads;
+    const AlignJob job{static_cast<const uint8_t *>(src), static_cast<uint8_t *>(dst), pitch * 2, rows,
+                       span16(src, rows, pitch, cols), (int)(blocks < 4096 ? blocks : 4096)};
+    return launch_kernel(true, linear_align_kernel, dim3((unsigned)job.blocks), dim3(kAlignThreads), 0, s, job, 1,
+                         AlignJob{}, cols * 2, align_up(cols, 8) * 2, (const int32_t *)nullptr, (uint32_t *)nullptr);
+}
+
 LinearLayout linear_layout(bool grad, int64_t m, int64_t n, int64_t k, int64_t n_experts) {
     LinearLayout L{};
     int64_t o = align_up((int64_t)(kPairWordsOffset + kMaxPairWords * sizeof(uint32_t)), 1024);

@@ -18,7 +18,41 @@ namespace km {
 // weights  dW = dz^T x
 // All three are out(q, p) = sum_c A(p, c) B(q, c), with p the contiguous
 // dimension of the output: output features, input features, input features.
-enum class Product { kForward, kRows, kWeights };
+//
+// The cross entropy (xent.cu) takes three of them with other ends, and the
+// weights product with a factor:
+// log sum  z = x W^T with a row of x on each tensor-memory lane (p the rows, q the
+//          classes): only each row's largest z and sum of exponentials leave
+// softmax  z once more as in the forward product, dz = g (exp(z - lse) - 1[label])
+// sum      dx over a piece of the classes, added up in float32
+// scaled   dW of such a dz, which is kept times a power of two
+enum class Product { kForward, kRows, kWeights, kLogSum, kSoftmax, kRowsSum, kWeightsScaled };
+
+__host__ __device__ constexpr bool is_weights(Product m) { return m == Product::kWeights || m == Product::kWeightsScaled; }
+// A's contiguous dimension is the contraction.
+__host__ __device__ constexpr bool is_forward(Product m) {
+    return m == Product::kForward || m == Product::kLogSum || m == Product::kSoftmax;
+}
+
+// A row that counts: factor * lse (factor as below), the factor of its gradient,
+// its label, and which row of the caller's it is.
+struct alignas(16) EntropyRow {
+    float lse2, gradient;
+    int32_t label, source;
+};
+
+struct EntropyArgs {
+    const EntropyRow *rows;
+    const int32_t *count;  // rows that count
+    float factor;          // of z: the logits' scale, times log2(e)
+    float2 *stats;         // log sum: (reference, sum of 2^(factor z - reference)) per class part and row
+    float *target;         // log sum: z at the label
+    int first;             // class of the piece's first
+    float *sums;           // sum: dx so far
+    bool begin, last;      // sum: the first, the last piece
+    const float *inverse;  // of dz's scale
+    int64_t pitch;         // of dz (softmax), of stats' rows (log sum)
+};
 
 struct Product16 {
     const void *a;            // w (forward, rows) or x (weights)
@@ -34,6 +68,7 @@ struct Product16 {
     void *db;                 // weights: the bias gradient, joined on the side from
     const float *bias_sums;   // the sums of `bias_rows` rows each (null: not here)
     int bias_rows;
+    EntropyArgs entropy;
 };
 
 // f applied with the activation as a compile-time constant: one branch around
@@ -145,6 +180,9 @@ WeightsSplit weights_split(int64_t m, int64_t n, int64_t k, int64_t n_experts);
 inline bool rows16(const void *base, int64_t pitch_elems) {
     return (reinterpret_cast<uintptr_t>(base) & 15u) == 0 && pitch_elems % 8 == 0;
 }
+
+// dst(r, c) = src(r, c) with the rows of dst on 16 bytes, pitch a multiple of 8.
+cudaError_t launch_align(const void *src, int64_t pitch, int64_t rows, int64_t cols, void *dst, cudaStream_t s);
 
 // The product on the tensor cores; w, x and dz must be rows16.  `clear`: the
 // kernel is the call's first, so nothing has cleared the status word yet.

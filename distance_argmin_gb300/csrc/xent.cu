@@ -1,0 +1,496 @@
+// Softmax cross entropy of rows against a matrix of classes, whose logits are
+// never kept: z = scale x W^T, lse = log sum exp z, loss = lse - z_label, and
+// the gradient dz = dloss scale (exp(z - lse) - 1[label]), dx = dz W, dW = dz^T x.
+//
+// The rows that count (label >= 0) are first brought together, on 16 bytes, so
+// that the products see only them: ignored rows cost nothing, and whatever they
+// hold reaches no result.
+// Forward: the product (log sum, see linear_tc.cuh) leaves each row's largest
+// logit and sum of exponentials per 64 classes, which xent_join_kernel brings
+// together.  Gradient: piece by piece of the classes dz is formed from the logits
+// once more, in 16 bits, and goes into both products while it is near; dx is
+// added up in float32 from piece to piece.  The products bound both: 2 and 6
+// operations per row, class and feature.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cstdlib>
+
+#include "layer.cuh"
+#include "linear_tc.cuh"
+
+namespace km {
+
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ---------------------------------------------------- the rows that count
+constexpr int kBringRows = 64;      // rows of a block
+constexpr int kBringThreads = 256;
+// Up to so many rows a block counts the ones before its own itself (16 labels to
+// a thread); more are counted per block's share by a kernel in front.
+constexpr int64_t kCountHere = 4096;
+
+// Of kBringRows rows: how many count, whether a label is past the classes, and
+// the largest gradient's magnitude.
+struct alignas(8) Tally {
+    uint16_t count, bad;
+    float top;
+};
+
+struct Bring {
+    const void *labels;
+    int id_bytes;
+    int64_t m, classes, k;
+    const uint8_t *x;
+    int64_t ldx;  // bytes
+    Span x_in;
+    uint8_t *xs;
+    int64_t ldxs;  // bytes
+    EntropyRow *rows;
+    const Tally *tally;  // null: counted here
+    int32_t *offsets;    // (2): 0 and the rows that count
+    uint32_t *header, *word;  // status, see common.cuh: the products' waits use the word
+    float scale;
+    // forward: the ignored rows' results
+    float *loss, *lse;
+    // gradient
+    const float *dloss, *lse_in;
+    float *factors;  // dz's scale, and what undoes it
+    bool narrow;     // float16
+    uint16_t *dx;    // ignored rows get zeros
+};
+
+__device__ __forceinline__ int64_t label_of(const Bring &b, int64_t r) {
+    return b.id_bytes == 8 ? static_cast<const int64_t *>(b.labels)[r] : (int64_t)static_cast<const int32_t *>(b.labels)[r];
+}
+
+__global__ void __launch_bounds__(kBringThreads) xent_tally_kernel(const Bring b, Tally *tally, int64_t shares) {
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t share = (int64_t)blockIdx.x * (kBringThreads / 32) + (threadIdx.x >> 5);
+    if (share >= shares) return;
+    Tally t{0, 0, 0.f};
+#pragma unroll
+    for (int i = 0; i < kBringRows / 32; ++i) {
+        const int64_t r = share * kBringRows + i * 32 + lane;
+        const int64_t l = r < b.m ? label_of(b, r) : -1;
+        const bool real = l >= 0 && l < b.classes;
+        t.count += (uint16_t)__popc(__ballot_sync(kAll, real));
+        t.bad |= (uint16_t)__any_sync(kAll, l >= b.classes);
+        if (b.dloss && real) t.top = fmaxf(t.top, fabsf(b.dloss[r]));
+    }
+    t.top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(t.top)));  // (not negative, and never NaN)
+    if (lane == 0) tally[share] = t;
+}
+
+// Sums and maxima over the block, in every thread.
+struct Totals {
+    int before, all, bad;
+    float top;
+};
+
+__device__ __forceinline__ Totals block_totals(Totals t) {
+    __shared__ Totals part[kBringThreads / 32];
+    t.before = __reduce_add_sync(kAll, t.before);
+    t.all = __reduce_add_sync(kAll, t.all);
+    t.bad = __reduce_or_sync(kAll, t.bad);
+    t.top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(t.top)));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = t;
+    __syncthreads();
+    t = part[0];
+#pragma unroll
+    for (int w = 1; w < kBringThreads / 32; ++w) {
+        t.before += part[w].before;
+        t.all += part[w].all;
+        t.bad |= part[w].bad;
+        t.top = fmaxf(t.top, part[w].top);
+    }
+    return t;
+}
+
+// The power of two that takes gradients of at most `top` to [2^14, 2^15): dz has
+// their magnitude at most, and float16 then keeps probabilities down to 2^-29 of
+// it in full.  (bfloat16 has float32's range.)
+__device__ __forceinline__ int scale_exponent(float top) {
+    if (!(top > 0.f) || isinf(top)) return 0;
+    return max(-126, min(126, 14 - ilogbf(top)));
+}
+
+template <bool WHOLE>
+__global__ void __launch_bounds__(kBringThreads) xent_bring_kernel(const Bring b) {
+    __shared__ int places[kBringRows];
+    griddep_wait();
+    const int64_t r0 = (int64_t)blockIdx.x * kBringRows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Totals t{0, 0, 0, 0.f};
+    if (b.tally) {
+        const int64_t shares = (b.m + kBringRows - 1) / kBringRows;
+        for (int64_t i = threadIdx.x; i < shares; i += kBringThreads) {
+            const Tally s = b.tally[i];
+            t.all += s.count;
+            if (i < blockIdx.x) t.before += s.count;
+            t.bad |= s.bad;
+            t.top = fmaxf(t.top, s.top);
+        }
+    } else {
+        for (int64_t r = threadIdx.x; r < b.m; r += kBringThreads) {
+            const int64_t l = label_of(b, r);
+            const bool real = l >= 0 && l < b.classes;
+            t.all += real;
+            if (r < r0) t.before += real;
+            t.bad |= l >= b.classes;
+            if (b.dloss && real) t.top = fmaxf(t.top, fabsf(b.dloss[r]));
+        }
+    }
+    t = block_totals(t);
+    const int exponent = b.narrow ? scale_exponent(t.top * b.scale) : 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        b.offsets[0] = 0;
+        b.offsets[1] = t.all;
+        *b.word = 0u;
+        *b.header = kPairWordsMark | 1u << kPairCountShift | (t.bad ? kFlagBadLabel : 0u);
+        if (b.factors) {
+            b.factors[0] = ldexpf(1.f, exponent);
+            b.factors[1] = ldexpf(1.f, -exponent);
+        }
+    }
+    if (warp == 0) {
+        int at = t.before;
+#pragma unroll
+        for (int i = 0; i < kBringRows / 32; ++i) {
+            const int64_t r = r0 + i * 32 + lane;
+            const int64_t l = r < b.m ? label_of(b, r) : -1;
+            const bool real = l >= 0 && l < b.classes;
+            const uint32_t which = __ballot_sync(kAll, real);
+            const int place = at + __popc(which & ((1u << lane) - 1u));
+            places[i * 32 + lane] = real ? place : -1;
+            at += __popc(which);
+            if (real) {
+                EntropyRow row{0.f, 0.f, (int32_t)l, (int32_t)r};
+                if (b.dloss) {
+                    row.lse2 = b.lse_in[r] * kLog2E;
+                    row.gradient = ldexpf(b.dloss[r] * b.scale, exponent);
+                }
+                b.rows[place] = row;
+            } else if (r < b.m && b.loss) {
+                b.loss[r] = 0.f;
+                b.lse[r] = 0.f;
+            }
+        }
+    }
+    __syncthreads();
+    const int64_t row_bytes = b.k * 2;
+    const int pieces = (int)((row_bytes + 15) / 16), here = (int)min((int64_t)kBringRows, b.m - r0);
+    for (int i = warp; i < here; i += kBringThreads / 32) {
+        const int place = places[i];
+        if (place >= 0) {
+            const uint8_t *from = b.x + (r0 + i) * b.ldx;
+            uint8_t *to = b.xs + place * b.ldxs;
+#pragma unroll 4
+            for (int c = lane; c < pieces; c += 32)  // (xs's rows are padded to whole pieces)
+                *reinterpret_cast<uint4 *>(to + (int64_t)c * 16) =
+                    load_piece<WHOLE>(from + (int64_t)c * 16, (int)min((int64_t)16, row_bytes - (int64_t)c * 16), b.x_in);
+        } else if (b.dx) {
+            uint16_t *to = b.dx + (r0 + i) * b.k;
+            for (int64_t c = lane; c < b.k; c += 32) to[c] = 0;
+        }
+    }
+}
+
+// ------------------------------------------------------------------- forward
+constexpr int kJoinWarps = 32;
+
+__global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const EntropyRow *__restrict__ rows,
+                                                                    const int32_t *count, const float2 *__restrict__ stats,
+                                                                    int64_t pitch, int parts,
+                                                                    const float *__restrict__ target, float factor,
+                                                                    float *__restrict__ loss, float *__restrict__ lse) {
+    __shared__ float2 sums[kJoinWarps][32];
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t r = (int64_t)blockIdx.x * 32 + lane;
+    const bool mine = r < *count;
+    const auto join = [](float2 a, float2 b) {
+        const float top = fmaxf(a.x, b.x);
+        // (nothing stands for itself as (-inf, 0); an infinite sum stays one)
+        const float u = isinf(a.y) || a.x == top ? a.y : a.y * exp2f(a.x - top);
+        const float v = isinf(b.y) || b.x == top ? b.y : b.y * exp2f(b.x - top);
+        return make_float2(top, u + v);
+    };
+    float2 s = {-INFINITY, 0.f};
+    if (mine) {
+#pragma unroll 4
+        for (int i = warp; i < parts; i += kJoinWarps) s = join(s, stats[i * pitch + r]);
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp || !mine) return;
+    for (int w = 1; w < kJoinWarps; ++w) s = join(s, sums[w][lane]);
+    const float log = log2f(s.y);
+    const int64_t at = rows[r].source;
+    // The label's distance from the reference with one rounding, as in the sum's
+    // exponentials: where the label is all there is the two cancel, however large
+    // the logits.
+    const float l = kLn2 * (log - fmaf(target[r], factor, -s.x));
+    loss[at] = l < 0.f ? 0.f : l;
+    lse[at] = kLn2 * (s.x + log);
+}
+
+// ------------------------------------------------------------------ gradient
+// dW of one piece = the chunks' sums, where its rows made several.
+template <typename T>
+__global__ void __launch_bounds__(256) xent_weights_join_kernel(const float *__restrict__ partial, const int32_t *offsets,
+                                                                int chunk, int64_t size, const float *inverse, T *dw) {
+    griddep_wait();
+    const int chunks = (int)(((int64_t)offsets[1] + chunk - 1) / chunk);
+    if (chunks <= 1) return;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * 256) {
+        LongSum s;
+#pragma unroll 8
+        for (int c = 0; c < chunks; ++c) s.add(partial[(int64_t)c * size + i]);
+        dw[i] = narrow<T>(s.value() * *inverse);
+    }
+}
+
+int64_t pairs_here() { return std::min(device_sm_count() / 2, kPairs); }
+
+int test_starve() {
+    // test-only fault injection (no trap, no fault), as in the assignment
+    const char *starve = getenv("KMEANS_GB300_TEST_STARVE_PIPELINE");
+    return (starve != nullptr && starve[0] == '1') ? 1 : 0;
+}
+
+LinearTcParams params(const LinearShape &sh, int64_t cols, int64_t contraction, uint32_t *word, const EntropyArgs &e) {
+    LinearTcParams p{};
+    p.offsets = sh.offsets;
+    p.m = sh.m;
+    p.n_experts = 1;
+    p.cols = (int)cols;
+    p.num_p = (p.cols + lt::BP - 1) / lt::BP;
+    p.out_rows = (int)sh.n;
+    p.chunk = kChunk;
+    p.contraction = (int)contraction;
+    p.status = word;
+    p.test_starve = test_starve();
+    p.entropy = e;
+    return p;
+}
+
+// Rows per unit: few where all units then fit one round of the pairs (as for the
+// experts' products).
+template <Product MODE>
+cudaError_t product(const LinearShape &sh, const Product16 &g, const LinearTcParams &p, int64_t rows, cudaStream_t s) {
+    const auto fits = [&](int64_t bn) { return (rows + bn - 1) / bn * p.num_p <= pairs_here(); };
+    return fits(128) ? launch_typed<MODE, 128>(sh, g, p, s) : launch_typed<MODE, 256>(sh, g, p, s);
+}
+
+}  // namespace
+
+// Classes of a piece: about 2^28 values of dz (half a gigabyte), at least 2048 so
+// that dx's sums are read and written rarely, at most one accumulator's terms; all
+// pieces about equal.
+int64_t xent_piece(int64_t m, int64_t n) {
+    int64_t most = ((int64_t)1 << 28) / std::max(m, (int64_t)1);
+    most = std::min((int64_t)kChunk, std::max((int64_t)2048, most / 256 * 256));
+    const int64_t pieces = (n + most - 1) / most;
+    return std::min(align_up((n + pieces - 1) / pieces, 256), align_up(n, 8));
+}
+
+XentLayout xent_layout(bool grad, int64_t m, int64_t n, int64_t k) {
+    XentLayout L{};
+    int64_t o = align_up((int64_t)(kPairWordsOffset + kMaxPairWords * sizeof(uint32_t)), 1024);
+    const auto take = [&](int64_t bytes) {
+        const int64_t at = o;
+        o = align_up(o + bytes, 1024);
+        return at;
+    };
+    L.off_info = take(64);
+    L.off_rows = take(m * (int64_t)sizeof(EntropyRow));
+    L.off_tally = take((m + kBringRows - 1) / kBringRows * (int64_t)sizeof(Tally));
+    L.off_x = take(m * align_up(k, 8) * 2);
+    if (k % 8 != 0) L.off_w = take(n * align_up(k, 8) * 2);
+    if (!grad) {
+        L.off_target = take(m * 4);
+        L.off_stats = take(align_up(m, 32) * ((n + 31) / 32 + 2 * lt::PARTS) * 8);
+    } else {
+        const int64_t piece = xent_piece(m, n);
+        L.off_dz = take(m * piece * 2);
+        if (piece < n) L.off_sums = take(m * k * 4);
+        L.off_partial = take((m > kChunk ? (m + kChunk - 1) / kChunk : 0) * piece * k * 4);
+    }
+    L.bytes = grad ? std::max(o, xent_layout(false, m, n, k).bytes) : o;  // (the gradient's serves both)
+    return L;
+}
+
+namespace {
+
+// What both directions begin with.
+struct Start {
+    const void *w;
+    int64_t ldw;
+    const void *xs;
+    int64_t ldxs;
+    EntropyArgs entropy;
+    int32_t *offsets;
+    uint32_t *word;
+    float *factors;
+};
+
+cudaError_t start(const XentShape &sh, const void *x, int64_t ldx, const void *w, Bring b, const XentLayout &L,
+                  uint8_t *ws, Start &out, cudaStream_t s) {
+    const int64_t ldxs = align_up(sh.k, 8);
+    uint8_t *info = ws + L.off_info;
+    b.labels = sh.labels;
+    b.id_bytes = sh.id_bytes;
+    b.m = sh.m;
+    b.classes = sh.n;
+    b.k = sh.k;
+    b.x = static_cast<const uint8_t *>(x);
+    b.ldx = ldx * 2;
+    b.x_in = {b.x, b.x + ((sh.m - 1) * ldx + sh.k) * 2};
+    b.xs = ws + L.off_x;
+    b.ldxs = ldxs * 2;
+    b.rows = reinterpret_cast<EntropyRow *>(ws + L.off_rows);
+    b.offsets = reinterpret_cast<int32_t *>(info);
+    b.header = &reinterpret_cast<WsHeader *>(ws)->status;
+    b.word = reinterpret_cast<uint32_t *>(ws + kPairWordsOffset);
+    b.scale = sh.scale;
+    b.narrow = !sh.bf16;
+    out.factors = b.factors = b.dloss ? reinterpret_cast<float *>(info + 16) : nullptr;
+    const int64_t shares = (sh.m + kBringRows - 1) / kBringRows;
+    cudaError_t e = cudaSuccess;
+    if (sh.m > kCountHere) {
+        Tally *tally = reinterpret_cast<Tally *>(ws + L.off_tally);
+        constexpr int per = kBringThreads / 32;
+        e = launch_kernel(true, xent_tally_kernel, dim3((unsigned)((shares + per - 1) / per)), dim3(kBringThreads), 0, s, b,
+                          tally, shares);
+        b.tally = tally;
+    }
+    const bool whole = rows16(x, ldx) && sh.k % 8 == 0;
+    if (e == cudaSuccess)
+        e = launch_kernel(true, whole ? xent_bring_kernel<true> : xent_bring_kernel<false>, dim3((unsigned)shares),
+                          dim3(kBringThreads), 0, s, b);
+    out.w = w;
+    out.ldw = sh.k;
+    if (e == cudaSuccess && sh.k % 8 != 0) {
+        out.w = ws + L.off_w;
+        out.ldw = ldxs;
+        e = launch_align(w, sh.k, sh.n, sh.k, ws + L.off_w, s);
+    }
+    out.xs = b.xs;
+    out.ldxs = ldxs;
+    out.offsets = b.offsets;
+    out.word = b.word;
+    out.entropy = EntropyArgs{};
+    out.entropy.rows = b.rows;
+    out.entropy.count = b.offsets + 1;
+    out.entropy.factor = sh.scale * kLog2E;
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_xent(const XentShape &sh, const void *x, int64_t ldx, const void *w, float *loss, float *lse,
+                        const XentLayout &L, uint8_t *ws, cudaStream_t s) {
+    if (sh.m == 0) return cudaMemsetAsync(ws, 0, sizeof(WsHeader), s);  // this call's status word
+    Bring b{};
+    b.loss = loss;
+    b.lse = lse;
+    Start st;
+    cudaError_t e = start(sh, x, ldx, w, b, L, ws, st, s);
+    if (e != cudaSuccess) return e;
+    // the classes are the product's rows, the rows its features
+    const LinearShape ps{sh.n, sh.m, sh.k, 1, nullptr, sh.bf16};
+    Product16 g{};
+    g.a = st.xs;
+    g.pitch_w = st.ldxs;
+    g.b = st.w;
+    g.ldb = st.ldw;
+    EntropyArgs en = st.entropy;
+    en.stats = reinterpret_cast<float2 *>(ws + L.off_stats);
+    en.target = reinterpret_cast<float *>(ws + L.off_target);
+    en.pitch = align_up(sh.m, 32);
+    const LinearTcParams p = params(ps, sh.m, sh.k, st.word, en);
+    const int64_t tiles128 = (sh.n + 127) / 128;
+    const bool small = tiles128 * p.num_p <= pairs_here();
+    e = small ? launch_typed<Product::kLogSum, 128>(ps, g, p, s) : launch_typed<Product::kLogSum, 256>(ps, g, p, s);
+    if (e != cudaSuccess) return e;
+    const int parts = (int)((small ? tiles128 : (sh.n + 255) / 256) * lt::PARTS);
+    return launch_kernel(true, xent_join_kernel, dim3((unsigned)((sh.m + 31) / 32)), dim3(32 * kJoinWarps), 0, s,
+                         (const EntropyRow *)en.rows, en.count, (const float2 *)en.stats, en.pitch, parts,
+                         (const float *)en.target, en.factor, loss, lse);
+}
+
+cudaError_t launch_xent_grad(const XentShape &sh, const float *dloss, const void *x, int64_t ldx, const void *w,
+                             const float *lse, void *dx, void *dw, const XentLayout &L, uint8_t *ws, cudaStream_t s) {
+    if (sh.m == 0 || !(dx || dw)) {  // no kernel that clears it
+        cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(WsHeader), s);  // this call's status word
+        if (e == cudaSuccess && dw) e = cudaMemsetAsync(dw, 0, (size_t)sh.n * (size_t)sh.k * 2, s);
+        return e;
+    }
+    Bring b{};
+    b.dloss = dloss;
+    b.lse_in = lse;
+    b.dx = static_cast<uint16_t *>(dx);
+    Start st;
+    cudaError_t e = start(sh, x, ldx, w, b, L, ws, st, s);
+    const int64_t piece = xent_piece(sh.m, sh.n);
+    EntropyArgs en = st.entropy;
+    en.pitch = piece;
+    en.inverse = st.factors + 1;
+    en.sums = reinterpret_cast<float *>(ws + L.off_sums);
+    void *dz = ws + L.off_dz;
+    for (int64_t c = 0; c < sh.n && e == cudaSuccess; c += piece) {
+        const int64_t here = std::min(piece, sh.n - c);
+        const LinearShape ps{sh.m, here, sh.k, 1, st.offsets, sh.bf16};
+        en.first = (int)c;
+        en.begin = c == 0;
+        en.last = c + here == sh.n;
+        Product16 g{};
+        g.a = static_cast<const uint16_t *>(st.w) + c * st.ldw;
+        g.pitch_w = st.ldw;
+        g.b = st.xs;
+        g.ldb = st.ldxs;
+        LinearTcParams p = params(ps, here, sh.k, st.word, en);
+        p.out = dz;
+        e = product<Product::kSoftmax>(ps, g, p, sh.m, s);
+        g.b = dz;
+        g.ldb = piece;
+        if (e == cudaSuccess && dx) {
+            p = params(ps, sh.k, here, st.word, en);
+            p.out = dx;
+            e = product<Product::kRowsSum>(ps, g, p, sh.m, s);
+        }
+        if (e == cudaSuccess && dw) {
+            uint16_t *out = static_cast<uint16_t *>(dw) + c * sh.k;
+            g.a = st.xs;
+            g.lda = st.ldxs;
+            g.out = out;
+            p = params(ps, sh.k, here, st.word, en);
+            p.out = out;
+            p.wide = rows16(out, sh.k);
+            p.partial = reinterpret_cast<float *>(ws + L.off_partial);
+            e = product<Product::kWeightsScaled>(ps, g, p, here, s);
+            if (e == cudaSuccess && sh.m > kChunk) {
+                const int64_t size = here * sh.k, blocks = (size + 255) / 256;
+                const dim3 grid((unsigned)std::min(blocks, (int64_t)kSMs * 8));
+                const float *partial = p.partial;
+                const int32_t *offsets = st.offsets;
+                e = sh.bf16 ? launch_kernel(true, xent_weights_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, partial,
+                                            offsets, kChunk, size, en.inverse, reinterpret_cast<__nv_bfloat16 *>(out))
+                            : launch_kernel(true, xent_weights_join_kernel<__half>, grid, dim3(256), 0, s, partial, offsets,
+                                            kChunk, size, en.inverse, reinterpret_cast<__half *>(out));
+            }
+        }
+    }
+    return e;
+}
+
+}  // namespace km

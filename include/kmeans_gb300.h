@@ -560,8 +560,8 @@ int kmeans_linear_grad(const void *dy, int64_t lddy, const void *x, int64_t ldx,
                        void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
- * Around the experts: the learned choice of them, and layer norm.  The
- * conventions are the expert layer's.
+ * Around the experts: the learned choice of them, layer norm, and the loss of
+ * rows scored against classes.  The conventions are the expert layer's.
  * --------------------------------------------------------------------------- */
 enum { KMEANS_GATE_SOFTMAX = 0, KMEANS_GATE_SIGMOID = 1 };
 
@@ -616,6 +616,41 @@ int kmeans_layernorm_grad(const void *dy, int64_t lddy, const void *x, int64_t l
                           const float *rstd, const void *weight, const void *residual, int64_t ldr, int64_t n,
                           int64_t d, void *dx, void *dweight, void *dbias, void *ws, size_t ws_bytes,
                           void *stream);
+
+#define KMEANS_CROSS_ENTROPY_MAX_WIDTH 32768
+
+/* Workspace of kmeans_cross_entropy (grad = 0) and kmeans_cross_entropy_grad
+ * (grad = 1, enough for both) for m rows, n classes and k features (0 when the
+ * sizes are invalid).  It holds no m * n logits: the forward call keeps 8 bytes
+ * per 64 classes of a row, the gradient a piece of the classes at a time, of
+ * about 2^28 values. */
+size_t kmeans_cross_entropy_workspace_bytes(int grad, int64_t m, int64_t n, int64_t k);
+
+/* Softmax cross entropy against classes: z = scale * x[r] w^T over the n
+ * classes, lse[r] = log sum_c exp(z_c), loss[r] = lse[r] - z_label.
+ * x (m, k) with pitch ldx and w (n, k), KMEANS_F16 or KMEANS_BF16; w starts on
+ * 16 bytes (KMEANS_ERR_UNSUPPORTED otherwise); labels (m) of id_bytes bytes (4:
+ * int32, 8: int64), each in [0, n), or negative for a row that does not count:
+ * its loss and lse are 0 and what it holds reaches no other result.  A label of
+ * n or more counts as negative and sets KMEANS_ERR_DEVICE_LABEL in the
+ * workspace's status word.  loss and lse (m) float32; scale > 0.
+ * m, n <= KMEANS_LINEAR_MAX_SIZE, n >= 1, 1 <= k <=
+ * KMEANS_CROSS_ENTROPY_MAX_WIDTH, and no matrix, nor m * n, of 2^42 values or
+ * more.  Where k is not a multiple of 8, w is first copied into the workspace. */
+int kmeans_cross_entropy(const void *x, int64_t ldx, const void *w, int dtype, const void *labels, int id_bytes,
+                         float scale, int64_t m, int64_t n, int64_t k, float *loss, float *lse, void *ws,
+                         size_t ws_bytes, void *stream);
+
+/* Gradient of the losses, each times dloss (m) float32: with
+ * dz = dloss * scale * (exp(z - lse) - 1[label]), dx = dz w and dw = dz^T x.
+ * lse as kmeans_cross_entropy wrote it for the same x, w and labels.  dx (m, k)
+ * and dw (n, k) may each be NULL; dx is zero in rows that do not count.  The
+ * products take dz in the matrices' type (float16: times a power of two that
+ * brings the largest dloss * scale to 2^14, so that terms down to 2^-29 of it
+ * keep their digits).  dx and dw must not alias an input. */
+int kmeans_cross_entropy_grad(const float *dloss, const void *x, int64_t ldx, const void *w, int dtype,
+                              const void *labels, int id_bytes, const float *lse, float scale, int64_t m,
+                              int64_t n, int64_t k, void *dx, void *dw, void *ws, size_t ws_bytes, void *stream);
 
 /* Synchronises `stream` and returns the device status word of the last call
  * that used `ws` (KMEANS_OK, KMEANS_ERR_DEVICE_TIMEOUT or
