@@ -7,16 +7,20 @@
 // largest c have the largest sum stay; then the topk largest c are taken one
 // after the other, equal ones by index.  A logit or a bias of minus infinity
 // closes the expert: it is not chosen, and a token with too few open experts
-// gets -1 with weight 0.  NaN counts as the largest value, so that a token that
-// holds one shows it in its weights.
+// gets -1 with weight 0.  NaN counts as infinity, so that a token that holds one
+// shows it in its weights.
 //
 // The choice is that of exact arithmetic.  Without a bias the order is the
 // logits' own.  Sums (c, and the groups' scores) are formed in float32; where two
 // neighbours in the order, the last chosen and the first left out among them, are
-// nearer than their errors (gap_of) and not equal in both logit and bias, the row
-// is done again in float64.
+// nearer than their errors (gap_of) and not equal in both logit and bias, what is
+// near is formed again in float64.
 //
-// A warp has a token, a lane every 32nd expert.
+// A warp has a token, a lane PER neighbouring experts in registers.  What is left
+// out early costs least: no lane can hold one of the topk + 1 largest unless its
+// own largest is among the lanes' topk + 1 largest, so the smallest of those
+// bounds the values that are looked at further, a few more than topk.  They are
+// brought together, one to a lane, and each counts the ones before it.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -48,16 +52,16 @@ __device__ __forceinline__ void store_logit(T *p, float v) {
         *p = narrow<T>(v);
 }
 
-// Order-preserving keys: 0 for what cannot be chosen, NaN the largest, the two
+// Order-preserving keys: 0 for what cannot be chosen, NaN as infinity, the two
 // zeros equal.
 __device__ __forceinline__ uint32_t choice_key(float v) {
     if (v == -INFINITY) return 0u;
-    if (v != v) return 0xffffffffu;
+    if (v != v) v = INFINITY;
     return float_to_ord(v + 0.f);
 }
 __device__ __forceinline__ uint64_t choice_key(double v) {
     if (v == -(double)INFINITY) return 0ull;
-    if (v != v) return ~0ull;
+    if (v != v) v = INFINITY;
     const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
     return (u >> 63) ? ~u : (u | (1ull << 63));
 }
@@ -86,29 +90,6 @@ __device__ __forceinline__ float warp_fmax(float v) {
     return v;
 }
 
-// The largest key of the warp and the lowest expert that has it, which is taken
-// out; -1 where nothing is left.
-template <int PER>
-__device__ __forceinline__ int take_best(uint32_t (&key)[PER], int lane, uint32_t &best) {
-    uint32_t mine = key[0];
-    int at = 0;
-#pragma unroll
-    for (int i = 1; i < PER; ++i)
-        if (key[i] > mine) {
-            mine = key[i];
-            at = i;
-        }
-    best = warp_max(mine);
-    if (best == 0) return -1;
-    const int e = (int)__reduce_min_sync(kAll, mine == best ? (uint32_t)(at * 32 + lane) : 0x7fffffffu);
-    if ((e & 31) == lane) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (i == (e >> 5)) key[i] = 0;
-    }
-    return e;
-}
-
 // How near two values of the order may be in float32 without being looked at in
 // float64: twice what they may be off by.  A score is off by less than 2^-18 (an
 // exponential by |x| e^x 2^-23 + 2^-22 e^x, x <= 0; the sum of up to 4096 of
@@ -122,6 +103,8 @@ struct GateArgs {
     bool sigmoid, renormalize;
     float scale;
     const float *bias;
+    bool whole, bias_whole;  // rows of the logits, the bias, start on 16 bytes
+    int lanes_per_group;     // where a group is a power of two of whole lanes, else 0
 };
 
 // The row's score parameters: softmax takes exp(l - top) / sum.
@@ -148,99 +131,219 @@ __device__ __forceinline__ V exp_of(V v) {
         return exp(v);
 }
 
+// A lane's PER neighbouring values of a row, absent ones minus infinity.
+template <int PER, typename T>
+__device__ __forceinline__ void load_run(const T *row, int e0, int n_experts, bool whole, float (&f)[PER]) {
+    constexpr int BYTES = PER * (int)sizeof(T), WORD = BYTES >= 16 ? 16 : BYTES, N = WORD / (int)sizeof(T);
+    if (whole && e0 + PER <= n_experts) {
+#pragma unroll
+        for (int i = 0; i < PER; i += N) {
+            T v[N];
+            if constexpr (WORD == 16)
+                *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(row + e0 + i);
+            else if constexpr (WORD == 8)
+                *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(row + e0 + i);
+            else if constexpr (WORD == 4)
+                *reinterpret_cast<uint32_t *>(v) = *reinterpret_cast<const uint32_t *>(row + e0 + i);
+            else
+                v[0] = row[e0 + i];
+#pragma unroll
+            for (int j = 0; j < N; ++j) f[i + j] = load_logit(v + j);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) f[i] = e0 + i < n_experts ? load_logit(row + e0 + i) : -INFINITY;
+    }
+}
+
+// Values brought together: what the choice goes by, and the expert.
+constexpr int kNear = 64;
+struct alignas(8) Candidate {
+    uint32_t key;
+    int expert;
+};
+struct Candidates {
+    Candidate found[kNear], sorted[33];
+    double value[kNear];
+};
+
+// The largest of the lanes' values, each lane's taken out in turn (one lane a
+// turn): the count-th largest, or 0 where there are fewer.
+__device__ __forceinline__ uint32_t nth_largest(uint32_t key, int count, int lane) {
+    uint32_t best = 0;
+    for (int j = 0; j < count; ++j) {
+        best = warp_max(key);
+        if (best == 0) break;
+        const uint32_t who = __ballot_sync(kAll, key == best);
+        if (lane == __ffs(who) - 1) key = 0;
+    }
+    return best;
+}
+
+// The groups that stay, as bits: lane g has the score of group g.  `near`: the
+// first one left out is nearer to the last one kept than float32 can tell.
+__device__ __forceinline__ uint32_t best_groups(uint32_t total, int count, int lane, bool &near) {
+    uint32_t kept = 0, last = 0;
+    near = false;
+    for (int j = 0; j <= count; ++j) {
+        const uint32_t best = warp_max(total);
+        if (best == 0) break;
+        if (j == count) {  // (equal sums are rarely sums of equal parts, so they are looked at too)
+            const float a = key_value(last), b = key_value(best);
+            near = !(a - b > 2.f * gap_of(a, b));
+            break;
+        }
+        const int g = __ffs(__ballot_sync(kAll, total == best)) - 1;
+        kept |= 1u << g;
+        last = best;
+        if (lane == g) total = 0;
+    }
+    return kept;
+}
+
+__device__ __forceinline__ float group_total(float one, float two) { return two == -INFINITY ? one : one + two; }
+
+// The two largest of two pairs.
+__device__ __forceinline__ void merge_two(float &one, float &two, float other_one, float other_two) {
+    two = fmaxf(fminf(one, other_one), fmaxf(two, other_two));
+    one = fmaxf(one, other_one);
+}
+
+// The `wanted` largest in order, one after the other: where so many values are
+// equal that they do not fit the list.  Returns how many there were.
+template <int PER>
+__device__ __forceinline__ int take_in_turn(float (&f)[PER], int wanted, int lane, Candidates &list) {
+    int count = 0;
+    for (; count < wanted; ++count) {
+        float mine = f[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < PER; ++i)
+            if (f[i] > mine) {
+                mine = f[i];
+                at = i;
+            }
+        const uint32_t key = choice_key(mine), best = warp_max(key);
+        if (best == 0) break;
+        // the lowest lane has the lowest experts
+        if (lane == __ffs(__ballot_sync(kAll, key == best)) - 1) {
+            list.sorted[count] = {best, lane * PER + at};
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i == at) f[i] = -INFINITY;
+        }
+    }
+    return count;
+}
+
 // Chooses a row's experts: lane j receives the j-th (-1: none).  False: float32
 // does not decide.
 template <int PER, typename T>
-__device__ __forceinline__ bool choose(const GateArgs &p, const T *row, int lane, const Scores<float> &sc, int &chosen) {
-    using V = float;
-    using K = uint32_t;
-    K key[PER];
+__device__ __forceinline__ bool choose(const GateArgs &p, const T *row, int lane, const Scores<float> &sc,
+                                       float (&f)[PER], Candidates &list, int &chosen) {
+    const int e0 = lane * PER;
     const bool sums = p.bias || p.groups > 1;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 + lane;
-        key[i] = 0;
-        if (e < p.n_experts) {
-            const float l = load_logit(row + e);
-            if (l != -INFINITY) {
-                V c = l;
-                if (sums) c = score_of(sc, l);
-                if (p.bias) c += (V)p.bias[e];
-                key[i] = choice_key(c);
-            }
-        }
-    }
-    if (p.groups > 1) {
-        K total[1] = {0};  // lane g: group g's score
-        for (int g = 0; g < p.groups; ++g) {
-            const int lo = g * p.group_size, hi = lo + p.group_size;
-            K one = 0, two = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = i * 32 + lane;
-                const K k = e >= lo && e < hi ? key[i] : 0;
-                two = k > one ? one : (k > two ? k : two);
-                one = k > one ? k : one;
-            }
-            const K first = warp_max(one);
-            const uint32_t who = __ballot_sync(kAll, one == first);
-            const K second = warp_max(lane == __ffs(who) - 1 ? two : one);
-            if (lane == g && first) {
-                V sum = key_value(first);
-                if (second) sum += key_value(second);
-                total[0] = choice_key(sum);
-            }
-        }
-        uint32_t kept = 0;
-        K last = 0, next;
-        for (int j = 0; j < p.topk_groups; ++j) {
-            const int g = take_best<1>(total, lane, next);
-            if (g < 0) break;
-            kept |= 1u << g;
-            last = next;
-        }
-        // (equal sums are rarely sums of equal parts, so they are looked at too)
-        if (take_best<1>(total, lane, next) >= 0 && last &&
-            !(key_value(last) - key_value(next) > 2.f * gap_of(key_value(last), key_value(next))))
-            return false;
+    if (sums) {
+        float b[PER];
+        if (p.bias) load_run<PER>(p.bias, e0, p.n_experts, p.bias_whole, b);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = i * 32 + lane;
-            const bool in = e < p.n_experts && (kept >> (e / p.group_size) & 1u) && key[i];
-            // without a bias the rest of the choice goes by the logits
-            if (!in)
-                key[i] = 0;
-            else if (!p.bias)
-                key[i] = choice_key((V)load_logit(row + e));
+            const float c = p.bias ? score_of(sc, f[i]) + b[i] : score_of(sc, f[i]);
+            f[i] = f[i] == -INFINITY ? f[i] : c;
         }
     }
-    chosen = -1;
-    K value = 0, best;
-    for (int j = 0; j < p.topk; ++j) {
-        const int e = take_best(key, lane, best);
-        if (e < 0) break;
-        if (lane == j) {
-            chosen = e;
-            value = best;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) f[i] = f[i] != f[i] ? INFINITY : f[i];
+    if (p.groups > 1) {
+        uint32_t total = 0;  // lane g: group g's score
+        bool mine[PER];
+        if (p.lanes_per_group > 0) {  // whole lanes, a power of two of them
+            float one = -INFINITY, two = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) merge_two(one, two, f[i], -INFINITY);
+            for (int o = 1; o < p.lanes_per_group; o <<= 1)
+                merge_two(one, two, __shfl_xor_sync(kAll, one, o), __shfl_xor_sync(kAll, two, o));
+            const int from = lane * p.lanes_per_group;
+            const uint32_t sum = __shfl_sync(kAll, choice_key(group_total(one, two)), from & 31);
+            if (lane < p.groups) total = sum;
+        } else {
+            for (int g = 0; g < p.groups; ++g) {
+                const int lo = g * p.group_size - e0, hi = lo + p.group_size;
+                float one = -INFINITY, two = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) merge_two(one, two, i >= lo && i < hi ? f[i] : -INFINITY, -INFINITY);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1)
+                    merge_two(one, two, __shfl_xor_sync(kAll, one, o), __shfl_xor_sync(kAll, two, o));
+                if (lane == g) total = choice_key(group_total(one, two));
+            }
+        }
+        bool near;
+        const uint32_t kept = best_groups(total, p.topk_groups, lane, near);
+        if (near) return false;
+        if (p.lanes_per_group > 0) {
+            const bool in = kept >> (lane / p.lanes_per_group) & 1u;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) mine[i] = in && f[i] != -INFINITY;
+        } else {
+            int g = e0 / p.group_size, left = (g + 1) * p.group_size - e0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                mine[i] = g < 32 && (kept >> g & 1u) && f[i] != -INFINITY;
+                if (--left == 0) {
+                    ++g;
+                    left = p.group_size;
+                }
+            }
+        }
+        if (!p.bias) {  // the rest of the choice goes by the logits
+            load_run<PER>(row, e0, p.n_experts, p.whole, f);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) f[i] = f[i] != f[i] ? INFINITY : f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) f[i] = mine[i] ? f[i] : -INFINITY;
+    }
+    float high = f[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) high = fmaxf(high, f[i]);
+    const int wanted = min(p.topk + 1, 32);  // (32 lanes have no 33rd: then all are looked at)
+    const uint32_t bound = p.topk < 32 ? nth_largest(choice_key(high), wanted, lane) : 0u;
+    const float least = bound ? key_value(bound) : -INFINITY;
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool in = f[i] >= least && f[i] != -INFINITY;
+        const uint32_t who = __ballot_sync(kAll, in);
+        if (who == 0) continue;
+        const int at = count + __popc(who & ((1u << lane) - 1u));
+        if (in && at < kNear) list.found[at] = {choice_key(f[i]), e0 + i};
+        count += __popc(who);
+    }
+    __syncwarp();
+    if (count > kNear) {
+        count = take_in_turn(f, p.topk + 1, lane, list);
+    } else {
+        for (int i = lane; i < count; i += 32) {
+            const Candidate own = list.found[i];
+            int rank = 0;
+            for (int j = 0; j < count; ++j) {
+                const Candidate other = list.found[j];
+                rank += other.key > own.key || (other.key == own.key && other.expert < own.expert);
+            }
+            if (rank < 33) list.sorted[rank] = own;
         }
     }
-    if (p.bias) {
-        const int rest = take_best(key, lane, best);
-        int after = __shfl_down_sync(kAll, chosen, 1);
-        K after_value = __shfl_down_sync(kAll, value, 1);
-        if (lane == p.topk - 1) {
-            after = rest;
-            after_value = best;
-        }
-        bool near = false;
-        if (lane < p.topk && chosen >= 0 && after >= 0) {
-            const V a = key_value(value), b = key_value(after_value);
-            const bool same = load_logit(row + chosen) == load_logit(row + after) && p.bias[chosen] == p.bias[after];
-            near = !(a - b > gap_of(a, b)) && !same;
-        }
-        if (__any_sync(kAll, near)) return false;
+    __syncwarp();
+    chosen = lane < p.topk && lane < count ? list.sorted[lane].expert : -1;
+    bool near = false;
+    if (p.bias && chosen >= 0 && lane + 1 < count) {
+        const int after = list.sorted[lane + 1].expert;
+        const float a = key_value(list.sorted[lane].key), c = key_value(list.sorted[lane + 1].key);
+        near = !(a - c > gap_of(a, c)) &&
+               !(load_logit(row + chosen) == load_logit(row + after) && p.bias[chosen] == p.bias[after]);
     }
-    return true;
+    return !__any_sync(kAll, near);
 }
 
 template <typename T, typename V>
@@ -263,7 +366,7 @@ __device__ __forceinline__ Scores<V> row_scores(const GateArgs &p, const T *row,
     return sc;
 }
 
-// The same in float64, for the few rows that need it: as short as it can be, a
+// The whole row in float64, where too much is near: as short as it can be, a
 // lane's keys in local memory.
 constexpr int kExactPer = KMEANS_ROUTE_MAX_EXPERTS / 32;
 
@@ -293,7 +396,9 @@ __device__ __noinline__ int choose_exact(const GateArgs &p, const T *row, int la
         const int e = i * 32 + lane;
         const float l = e < p.n_experts ? load_logit(row + e) : -INFINITY;
         key[i] = 0;
-        if (l != -INFINITY) key[i] = choice_key(score_of(sc, l) + (p.bias ? (double)p.bias[e] : 0.0));
+        if (l != -INFINITY)
+            key[i] = p.bias || p.groups > 1 ? choice_key(score_of(sc, l) + (p.bias ? (double)p.bias[e] : 0.0))
+                                            : choice_key((double)l);
     }
     uint64_t best;
     if (p.groups > 1) {
@@ -340,6 +445,112 @@ __device__ __noinline__ int choose_exact(const GateArgs &p, const T *row, int la
     return chosen;
 }
 
+// The same where float32 does not decide: the values near the borders in float64,
+// up to kNear of them (choose_exact has all of them).  For the groups' scores that
+// is whatever may be among a group's two largest, for the order whatever may be
+// among the topk largest.
+template <typename T>
+__device__ __noinline__ int choose_near(const GateArgs &p, const T *row, int lane, Candidates &list) {
+    const Scores<float> sc = row_scores<T, float>(p, row, lane);
+    Scores<double> scd{p.sigmoid, 0, 0};
+    if (!p.sigmoid) scd = row_scores<T, double>(p, row, lane);
+    const int per = (p.n_experts + 31) / 32;
+    const auto value = [&](int e) {  // in float32
+        if (e >= p.n_experts) return -INFINITY;
+        const float l = load_logit(row + e);
+        const float c = p.bias ? score_of(sc, l) + p.bias[e] : score_of(sc, l);
+        return l == -INFINITY ? l : (c != c ? INFINITY : c);
+    };
+    const auto exact = [&](int e) {
+        const double c = score_of(scd, load_logit(row + e)) + (p.bias ? (double)p.bias[e] : 0.0);
+        return c != c ? (double)INFINITY : c;
+    };
+    int count = 0;
+    const auto add = [&](bool in, int e) {
+        const uint32_t who = __ballot_sync(kAll, in);
+        const int at = count + __popc(who & ((1u << lane) - 1u));
+        if (in && at < kNear) list.found[at].expert = e;
+        count += __popc(who);
+    };
+    uint32_t kept = ~0u;
+    __syncwarp();
+    if (p.groups > 1) {
+#pragma unroll 1
+        for (int g = 0; g < p.groups; ++g) {
+            const int lo = g * p.group_size, hi = lo + p.group_size;
+            float one = -INFINITY, two = -INFINITY;
+#pragma unroll 1
+            for (int e = lo + lane; e < hi; e += 32) merge_two(one, two, value(e), -INFINITY);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+                merge_two(one, two, __shfl_xor_sync(kAll, one, o), __shfl_xor_sync(kAll, two, o));
+#pragma unroll 1
+            for (int e = lo; e < hi; e += 32) {
+                const float c = e + lane < hi ? value(e + lane) : -INFINITY;
+                add(c != -INFINITY && !(two - c > gap_of(c, two)), e + lane);
+            }
+        }
+        if (count > kNear) return choose_exact(p, row, lane);
+        __syncwarp();
+        for (int i = lane; i < count; i += 32) list.value[i] = exact(list.found[i].expert);
+        __syncwarp();
+        double one = -INFINITY, two = -INFINITY;
+        for (int i = 0; i < count; ++i) {
+            if (list.found[i].expert / p.group_size != lane) continue;
+            const double c = list.value[i];
+            two = c > one ? one : (c > two ? c : two);
+            one = c > one ? c : one;
+        }
+        const uint64_t total = choice_key(two == -INFINITY ? one : one + two);
+        int rank = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const uint64_t other = (uint64_t)__shfl_sync(kAll, (unsigned long long)total, g);
+            rank += other > total || (other == total && g < lane);
+        }
+        kept = __ballot_sync(kAll, lane < p.groups && total != 0 && rank < p.topk_groups);
+        count = 0;
+        __syncwarp();
+    }
+    // without a bias the rest of the choice goes by the logits, which are exact
+    const auto order = [&](int e) {
+        if (e >= p.n_experts || (p.groups > 1 && !(kept >> (e / p.group_size) & 1u))) return -INFINITY;
+        const float c = value(e);
+        if (p.bias || c == -INFINITY) return c;
+        const float l = load_logit(row + e);
+        return l != l ? INFINITY : l;
+    };
+    float high = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) high = fmaxf(high, order(i * 32 + lane));
+    const uint32_t bound = nth_largest(choice_key(high), p.topk, lane);
+    const float least = bound ? key_value(bound) : -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < per; ++i) {
+        const int e = i * 32 + lane;
+        const float c = order(e);
+        add(c != -INFINITY && !(p.bias ? least - c > gap_of(c, least) : least > c), e);
+    }
+    if (count > kNear) return choose_exact(p, row, lane);
+    __syncwarp();
+    for (int i = lane; i < count; i += 32) {
+        const int e = list.found[i].expert;
+        list.value[i] = p.bias ? exact(e) : (double)order(e);
+    }
+    __syncwarp();
+    for (int i = lane; i < count; i += 32) {
+        const int e = list.found[i].expert;
+        const uint64_t own = choice_key(list.value[i]);
+        int rank = 0;
+        for (int j = 0; j < count; ++j) {
+            const uint64_t other = choice_key(list.value[j]);
+            rank += other > own || (other == own && list.found[j].expert < e);
+        }
+        if (rank < 33) list.sorted[rank].expert = e;
+    }
+    __syncwarp();
+    return lane < p.topk && lane < count ? list.sorted[lane].expert : -1;
+}
+
 // The chosen experts' shares of their sum; lane j has expert j's logit.  Scaled
 // by the largest of them where all are small, so that the quotient is defined.
 __device__ __forceinline__ float share_of(bool sigmoid, float l, bool real) {
@@ -359,14 +570,35 @@ __device__ __forceinline__ float share_of(bool sigmoid, float l, bool real) {
 template <int PER, typename T>
 __global__ void __launch_bounds__(kGateThreads) gate_kernel(const T *__restrict__ logits, const GateArgs p,
                                                             int32_t *__restrict__ ids, float *__restrict__ weights) {
+    __shared__ Candidates lists[kGateThreads / 32];
     griddep_wait();
     const int lane = threadIdx.x & 31;
+    Candidates &list = lists[threadIdx.x >> 5];
+    // (renormalised softmax weights that are chosen by the logits need no sum of all)
+    const bool need_sum = !p.sigmoid && (p.bias || p.groups > 1 || !p.renormalize);
     const int64_t step = (int64_t)gridDim.x * (kGateThreads / 32);
     for (int64_t r = (int64_t)blockIdx.x * (kGateThreads / 32) + (threadIdx.x >> 5); r < p.n; r += step) {
         const T *row = logits + r * p.ldl;
-        const Scores<float> sc = row_scores<T, float>(p, row, lane);
+        float f[PER];
+        load_run<PER>(row, lane * PER, p.n_experts, p.whole, f);
+        Scores<float> sc{p.sigmoid, 0.f, 0.f};
+        if (need_sum) {
+            float top = f[0];
+#pragma unroll
+            for (int i = 1; i < PER; ++i) top = fmaxf(top, f[i]);
+            top = warp_fmax(top);
+            sc.top = top == -INFINITY ? 0.f : top;  // no open expert: scores of 0
+            constexpr int SUMS = PER < 4 ? PER : 4;  // (see gap_of)
+            float sum[SUMS] = {};
+#pragma unroll
+            for (int i = 0; i < PER; ++i) sum[i % SUMS] += __expf(f[i] - sc.top);
+#pragma unroll
+            for (int i = 1; i < SUMS; ++i) sum[0] += sum[i];
+            const float all = warp_sum(sum[0]);
+            sc.inverse = all == 0.f ? 0.f : 1.f / all;
+        }
         int e;
-        if (!choose<PER, T>(p, row, lane, sc, e)) e = choose_exact<T>(p, row, lane);
+        if (!choose<PER>(p, row, lane, sc, f, list, e)) e = choose_near(p, row, lane, list);
         const bool real = lane < p.topk && e >= 0;
         const float l = real ? load_logit(row + e) : 0.f;
         float w = p.renormalize ? share_of(p.sigmoid, l, real) : score_of(sc, l);
@@ -445,15 +677,27 @@ unsigned gate_blocks(int64_t n) {
     return (unsigned)(blocks < most ? blocks : most);
 }
 
-GateArgs gate_args(const GateShape &g, int64_t ldl, const float *bias) {
-    return {g.n,          ldl, g.n_experts, g.topk, g.groups, g.topk_groups, g.n_experts / g.groups, g.sigmoid,
-            g.renormalize, g.scale, bias};
+// Values of a lane: a power of two of them up to 128.
+int gate_per(int n_experts) {
+    int per = 1;
+    while (per * 32 < n_experts) per *= 2;
+    return per;
+}
+
+bool on16(const void *p, int64_t pitch_bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && pitch_bytes % 16 == 0;
+}
+
+GateArgs gate_args(const GateShape &g, const void *logits, int64_t ldl, int bytes, const float *bias) {
+    const int size = g.n_experts / g.groups, per = gate_per(g.n_experts), lanes = size % per == 0 ? size / per : 0;
+    return {g.n, ldl, g.n_experts, g.topk, g.groups, g.topk_groups, size, g.sigmoid, g.renormalize, g.scale, bias,
+            on16(logits, ldl * bytes), on16(bias, 0), (lanes & (lanes - 1)) == 0 ? lanes : 0};
 }
 
 template <typename T>
 cudaError_t gate_typed(const GateShape &g, const void *logits, int64_t ldl, const float *bias, int32_t *ids,
                        float *weights, cudaStream_t s) {
-    const int per = (g.n_experts + 31) / 32;
+    const int per = gate_per(g.n_experts);
     void (*kernel)(const T *, GateArgs, int32_t *, float *) =
         per <= 1    ? gate_kernel<1, T>
         : per <= 2  ? gate_kernel<2, T>
@@ -461,9 +705,10 @@ cudaError_t gate_typed(const GateShape &g, const void *logits, int64_t ldl, cons
         : per <= 8  ? gate_kernel<8, T>
         : per <= 16 ? gate_kernel<16, T>
         : per <= 32 ? gate_kernel<32, T>
+        : per <= 64 ? gate_kernel<64, T>
                     : gate_kernel<128, T>;
     return launch_kernel(true, kernel, dim3(gate_blocks(g.n)), dim3(kGateThreads), 0, s, static_cast<const T *>(logits),
-                         gate_args(g, ldl, bias), ids, weights);
+                         gate_args(g, logits, ldl, (int)sizeof(T), bias), ids, weights);
 }
 
 template <typename T>
@@ -481,7 +726,7 @@ cudaError_t gate_grad_typed(const GateShape &g, const float *dweights, const voi
     if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
     return launch_kernel(true, gate_grad_kernel<T>, dim3(gate_blocks(g.n)), dim3(kGateThreads),
                          (size_t)g.n_experts * (kGateThreads / 32) * 4, s, dweights, static_cast<const T *>(logits),
-                         gate_args(g, ldl, nullptr), ids, static_cast<T *>(dlogits));
+                         gate_args(g, logits, ldl, (int)sizeof(T), nullptr), ids, static_cast<T *>(dlogits));
 }
 
 }  // namespace

@@ -275,3 +275,25 @@ def test_a_closed_expert_has_no_gradient(gpu_lib, kind):
                                        renormalize=renormalize)
         assert bool(torch.isfinite(got[0]).all()) and got[0, 3].item() == 0
         assert bool((got[1] == 0).all())
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,groups", [(256, 1), (256, 8), (1000, 5), (4096, 16)])
+def test_rows_of_many_equal_logits(gpu_lib, kind, biased, E, groups):
+    """Padding that a router sees: rows of zeros, of few different values, and of one large one."""
+    z = torch.zeros(4, E)
+    z[1] = (torch.arange(E) % 3).float()
+    z[2, E // 2] = 5.0
+    z[3, E - 40:] = 1.0
+    bias = np.zeros(E, np.float32)
+    bias[::7] = 0.125
+    ids, _ = gpu_lib.kmeans_gate(z.cuda(), 12, scores=kind, bias=torch.from_numpy(bias).cuda() if biased else None,
+                                 groups=groups, topk_groups=max(1, groups // 2))
+    want, _ = plain_gate(z.double().numpy(), 12, kind, bias.astype(np.float64) if biased else None, groups,
+                         max(1, groups // 2))
+    if groups > 1:  # equal groups' sums may differ by a rounding of float64 in the plain form: compare the values
+        got = np.take_along_axis(z.numpy(), ids.cpu().numpy().astype(np.int64), 1)
+        assert np.array_equal(np.sort(got, 1), np.sort(np.take_along_axis(z.numpy(), want, 1), 1))
+    else:
+        assert np.array_equal(ids.cpu().numpy(), want)
