@@ -13,7 +13,7 @@
 // The choice is that of exact arithmetic.  Without a bias the order is the
 // logits' own.  Sums (c, and the groups' scores) are formed in float32; where two
 // neighbours in the order, the last chosen and the first left out among them, are
-// nearer than their errors (gap_of) and not equal in both logit and bias, what is
+// nearer than their errors (GateArgs::gap_of) and not equal in both logit and bias, what is
 // near is formed again in float64.
 //
 // A warp has a token, a lane PER neighbouring experts in registers.  What is left
@@ -24,6 +24,9 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
+
+#include <type_traits>
 
 #include "assign_common.cuh"
 #include "layer.cuh"
@@ -36,13 +39,18 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kGateThreads = 128;
 
-template <typename T>
-__device__ __forceinline__ float load_logit(const T *p) {
-    if constexpr (sizeof(T) == 4)
-        return *p;
-    else
-        return widen<T>(*p);
-}
+// A token's logits.  Their type is looked at where they are loaded: the choice has
+// hundreds of instructions to those few, and a kernel of its own for every type
+// would be as much code again.
+struct Logits {
+    const uint8_t *p;
+    int dtype;
+    __device__ __forceinline__ float operator[](int e) const {
+        if (dtype == KMEANS_F32) return reinterpret_cast<const float *>(p)[e];
+        if (dtype == KMEANS_F16) return widen(reinterpret_cast<const __half *>(p)[e]);
+        return widen(reinterpret_cast<const __nv_bfloat16 *>(p)[e]);
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ void store_logit(T *p, float v) {
@@ -90,21 +98,20 @@ __device__ __forceinline__ float warp_fmax(float v) {
     return v;
 }
 
-// How near two values of the order may be in float32 without being looked at in
-// float64: twice what they may be off by.  A score is off by less than 2^-18 (an
-// exponential by |x| e^x 2^-23 + 2^-22 e^x, x <= 0; the sum of up to 4096 of
-// them, 32 to an accumulator, by 39 2^-24 of itself; the quotient by 2^-22), the
-// sum with the bias by half its last bit more, a group's two by twice that.
-__device__ __forceinline__ float gap_of(float a, float b) { return 0x1p-17f + 0x1p-21f * (fabsf(a) + fabsf(b)); }
-
 struct GateArgs {
-    int64_t n, ldl;
+    int64_t n, pitch;  // bytes
+    int dtype;
     int n_experts, topk, groups, topk_groups, group_size;
     bool sigmoid, renormalize;
     float scale;
     const float *bias;
     bool whole, bias_whole;  // rows of the logits, the bias, start on 16 bytes
     int lanes_per_group;     // where a group is a power of two of whole lanes, else 0
+    float gap;
+    // How near two values of the order may be in float32 without being looked at
+    // in float64: twice what they may be off by.  gap: a score's error, twice (see
+    // gate_args); then half a last bit of each sum with the bias.
+    __device__ __forceinline__ float gap_of(float a, float b) const { return gap + 0x1p-23f * (fabsf(a) + fabsf(b)); }
 };
 
 // The row's score parameters: softmax takes exp(l - top) / sum.
@@ -131,28 +138,39 @@ __device__ __forceinline__ V exp_of(V v) {
         return exp(v);
 }
 
-// A lane's PER neighbouring values of a row, absent ones minus infinity.
+// PER values from p on, whose first is on 16 bytes or their own size.
 template <int PER, typename T>
-__device__ __forceinline__ void load_run(const T *row, int e0, int n_experts, bool whole, float (&f)[PER]) {
+__device__ __forceinline__ void load_whole(const T *p, float (&f)[PER]) {
     constexpr int BYTES = PER * (int)sizeof(T), WORD = BYTES >= 16 ? 16 : BYTES, N = WORD / (int)sizeof(T);
-    if (whole && e0 + PER <= n_experts) {
+    using W = std::conditional_t<WORD == 16, uint4, std::conditional_t<WORD == 8, uint2, std::conditional_t<WORD == 4, uint32_t, uint16_t>>>;
 #pragma unroll
-        for (int i = 0; i < PER; i += N) {
-            T v[N];
-            if constexpr (WORD == 16)
-                *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(row + e0 + i);
-            else if constexpr (WORD == 8)
-                *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(row + e0 + i);
-            else if constexpr (WORD == 4)
-                *reinterpret_cast<uint32_t *>(v) = *reinterpret_cast<const uint32_t *>(row + e0 + i);
+    for (int i = 0; i < PER; i += N) {
+        const W w = reinterpret_cast<const W *>(p)[i / N];
+        T v[N];
+        memcpy(v, &w, sizeof w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if constexpr (sizeof(T) == 4)
+                f[i + j] = v[j];
             else
-                v[0] = row[e0 + i];
-#pragma unroll
-            for (int j = 0; j < N; ++j) f[i + j] = load_logit(v + j);
+                f[i + j] = widen<T>(v[j]);
         }
+    }
+}
+
+// A lane's PER neighbouring values of a row, absent ones minus infinity.
+template <int PER>
+__device__ __forceinline__ void load_run(const Logits &row, int e0, int n_experts, bool whole, float (&f)[PER]) {
+    if (whole && e0 + PER <= n_experts) {
+        if (row.dtype == KMEANS_F32)
+            load_whole<PER>(reinterpret_cast<const float *>(row.p) + e0, f);
+        else if (row.dtype == KMEANS_F16)
+            load_whole<PER>(reinterpret_cast<const __half *>(row.p) + e0, f);
+        else
+            load_whole<PER>(reinterpret_cast<const __nv_bfloat16 *>(row.p) + e0, f);
     } else {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) f[i] = e0 + i < n_experts ? load_logit(row + e0 + i) : -INFINITY;
+        for (int i = 0; i < PER; ++i) f[i] = e0 + i < n_experts ? row[e0 + i] : -INFINITY;
     }
 }
 
@@ -180,178 +198,12 @@ __device__ __forceinline__ uint32_t nth_largest(uint32_t key, int count, int lan
     return best;
 }
 
-// The groups that stay, as bits: lane g has the score of group g.  `near`: the
-// first one left out is nearer to the last one kept than float32 can tell.
-__device__ __forceinline__ uint32_t best_groups(uint32_t total, int count, int lane, bool &near) {
-    uint32_t kept = 0, last = 0;
-    near = false;
-    for (int j = 0; j <= count; ++j) {
-        const uint32_t best = warp_max(total);
-        if (best == 0) break;
-        if (j == count) {  // (equal sums are rarely sums of equal parts, so they are looked at too)
-            const float a = key_value(last), b = key_value(best);
-            near = !(a - b > 2.f * gap_of(a, b));
-            break;
-        }
-        const int g = __ffs(__ballot_sync(kAll, total == best)) - 1;
-        kept |= 1u << g;
-        last = best;
-        if (lane == g) total = 0;
-    }
-    return kept;
-}
-
-__device__ __forceinline__ float group_total(float one, float two) { return two == -INFINITY ? one : one + two; }
-
-// The two largest of two pairs.
-__device__ __forceinline__ void merge_two(float &one, float &two, float other_one, float other_two) {
-    two = fmaxf(fminf(one, other_one), fmaxf(two, other_two));
-    one = fmaxf(one, other_one);
-}
-
-// The `wanted` largest in order, one after the other: where so many values are
-// equal that they do not fit the list.  Returns how many there were.
-template <int PER>
-__device__ __forceinline__ int take_in_turn(float (&f)[PER], int wanted, int lane, Candidates &list) {
-    int count = 0;
-    for (; count < wanted; ++count) {
-        float mine = f[0];
-        int at = 0;
-#pragma unroll
-        for (int i = 1; i < PER; ++i)
-            if (f[i] > mine) {
-                mine = f[i];
-                at = i;
-            }
-        const uint32_t key = choice_key(mine), best = warp_max(key);
-        if (best == 0) break;
-        // the lowest lane has the lowest experts
-        if (lane == __ffs(__ballot_sync(kAll, key == best)) - 1) {
-            list.sorted[count] = {best, lane * PER + at};
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (i == at) f[i] = -INFINITY;
-        }
-    }
-    return count;
-}
-
-// Chooses a row's experts: lane j receives the j-th (-1: none).  False: float32
-// does not decide.
-template <int PER, typename T>
-__device__ __forceinline__ bool choose(const GateArgs &p, const T *row, int lane, const Scores<float> &sc,
-                                       float (&f)[PER], Candidates &list, int &chosen) {
-    const int e0 = lane * PER;
-    const bool sums = p.bias || p.groups > 1;
-    if (sums) {
-        float b[PER];
-        if (p.bias) load_run<PER>(p.bias, e0, p.n_experts, p.bias_whole, b);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const float c = p.bias ? score_of(sc, f[i]) + b[i] : score_of(sc, f[i]);
-            f[i] = f[i] == -INFINITY ? f[i] : c;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) f[i] = f[i] != f[i] ? INFINITY : f[i];
-    if (p.groups > 1) {
-        uint32_t total = 0;  // lane g: group g's score
-        bool mine[PER];
-        if (p.lanes_per_group > 0) {  // whole lanes, a power of two of them
-            float one = -INFINITY, two = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) merge_two(one, two, f[i], -INFINITY);
-            for (int o = 1; o < p.lanes_per_group; o <<= 1)
-                merge_two(one, two, __shfl_xor_sync(kAll, one, o), __shfl_xor_sync(kAll, two, o));
-            const int from = lane * p.lanes_per_group;
-            const uint32_t sum = __shfl_sync(kAll, choice_key(group_total(one, two)), from & 31);
-            if (lane < p.groups) total = sum;
-        } else {
-            for (int g = 0; g < p.groups; ++g) {
-                const int lo = g * p.group_size - e0, hi = lo + p.group_size;
-                float one = -INFINITY, two = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) merge_two(one, two, i >= lo && i < hi ? f[i] : -INFINITY, -INFINITY);
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1)
-                    merge_two(one, two, __shfl_xor_sync(kAll, one, o), __shfl_xor_sync(kAll, two, o));
-                if (lane == g) total = choice_key(group_total(one, two));
-            }
-        }
-        bool near;
-        const uint32_t kept = best_groups(total, p.topk_groups, lane, near);
-        if (near) return false;
-        if (p.lanes_per_group > 0) {
-            const bool in = kept >> (lane / p.lanes_per_group) & 1u;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) mine[i] = in && f[i] != -INFINITY;
-        } else {
-            int g = e0 / p.group_size, left = (g + 1) * p.group_size - e0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                mine[i] = g < 32 && (kept >> g & 1u) && f[i] != -INFINITY;
-                if (--left == 0) {
-                    ++g;
-                    left = p.group_size;
-                }
-            }
-        }
-        if (!p.bias) {  // the rest of the choice goes by the logits
-            load_run<PER>(row, e0, p.n_experts, p.whole, f);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) f[i] = f[i] != f[i] ? INFINITY : f[i];
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) f[i] = mine[i] ? f[i] : -INFINITY;
-    }
-    float high = f[0];
-#pragma unroll
-    for (int i = 1; i < PER; ++i) high = fmaxf(high, f[i]);
-    const int wanted = min(p.topk + 1, 32);  // (32 lanes have no 33rd: then all are looked at)
-    const uint32_t bound = p.topk < 32 ? nth_largest(choice_key(high), wanted, lane) : 0u;
-    const float least = bound ? key_value(bound) : -INFINITY;
-    int count = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const bool in = f[i] >= least && f[i] != -INFINITY;
-        const uint32_t who = __ballot_sync(kAll, in);
-        if (who == 0) continue;
-        const int at = count + __popc(who & ((1u << lane) - 1u));
-        if (in && at < kNear) list.found[at] = {choice_key(f[i]), e0 + i};
-        count += __popc(who);
-    }
-    __syncwarp();
-    if (count > kNear) {
-        count = take_in_turn(f, p.topk + 1, lane, list);
-    } else {
-        for (int i = lane; i < count; i += 32) {
-            const Candidate own = list.found[i];
-            int rank = 0;
-            for (int j = 0; j < count; ++j) {
-                const Candidate other = list.found[j];
-                rank += other.key > own.key || (other.key == own.key && other.expert < own.expert);
-            }
-            if (rank < 33) list.sorted[rank] = own;
-        }
-    }
-    __syncwarp();
-    chosen = lane < p.topk && lane < count ? list.sorted[lane].expert : -1;
-    bool near = false;
-    if (p.bias && chosen >= 0 && lane + 1 < count) {
-        const int after = list.sorted[lane + 1].expert;
-        const float a = key_value(list.sorted[lane].key), c = key_value(list.sorted[lane + 1].key);
-        near = !(a - c > gap_of(a, c)) &&
-               !(load_logit(row + chosen) == load_logit(row + after) && p.bias[chosen] == p.bias[after]);
-    }
-    return !__any_sync(kAll, near);
-}
-
-template <typename T, typename V>
-__device__ __forceinline__ Scores<V> row_scores(const GateArgs &p, const T *row, int lane) {
+template <typename V>
+__device__ __forceinline__ Scores<V> row_scores(const GateArgs &p, const Logits &row, int lane) {
     Scores<V> sc{p.sigmoid, 0, 0};
     if (p.sigmoid) return sc;
     float top = -INFINITY;
-    for (int e = lane; e < p.n_experts; e += 32) top = fmaxf(top, load_logit(row + e));
+    for (int e = lane; e < p.n_experts; e += 32) top = fmaxf(top, row[e]);
     top = warp_fmax(top);
     sc.top = top == -INFINITY ? 0.f : top;  // no open expert: scores of 0
     V sum[4] = {};  // (a lane's 128 terms one after the other would lose up to 2^-17)
@@ -359,7 +211,7 @@ __device__ __forceinline__ Scores<V> row_scores(const GateArgs &p, const T *row,
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = e0 + i * 32;
-            if (e < p.n_experts) sum[i] += exp_of((V)load_logit(row + e) - sc.top);
+            if (e < p.n_experts) sum[i] += exp_of((V)row[e] - sc.top);
         }
     const V all = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
     sc.inverse = all == (V)0 ? (V)0 : (V)1 / all;
@@ -386,15 +238,14 @@ __device__ int take_best_exact(uint64_t *key, int per, int lane, uint64_t &best)
     return e;
 }
 
-template <typename T>
-__device__ __noinline__ int choose_exact(const GateArgs &p, const T *row, int lane) {
+__device__ __noinline__ int choose_exact(const GateArgs &p, const Logits &row, int lane) {
     uint64_t key[kExactPer];
-    const Scores<double> sc = row_scores<T, double>(p, row, lane);
+    const Scores<double> sc = row_scores<double>(p, row, lane);
     const int per = (p.n_experts + 31) / 32;
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
         const int e = i * 32 + lane;
-        const float l = e < p.n_experts ? load_logit(row + e) : -INFINITY;
+        const float l = e < p.n_experts ? row[e] : -INFINITY;
         key[i] = 0;
         if (l != -INFINITY)
             key[i] = p.bias || p.groups > 1 ? choice_key(score_of(sc, l) + (p.bias ? (double)p.bias[e] : 0.0))
@@ -432,7 +283,7 @@ __device__ __noinline__ int choose_exact(const GateArgs &p, const T *row, int la
             if (key[i] && !(kept >> (e / p.group_size) & 1u))
                 key[i] = 0;
             else if (key[i] && !p.bias)
-                key[i] = choice_key((double)load_logit(row + e));
+                key[i] = choice_key((double)row[e]);
         }
     }
     int chosen = -1;
@@ -445,98 +296,41 @@ __device__ __noinline__ int choose_exact(const GateArgs &p, const T *row, int la
     return chosen;
 }
 
-// The same where float32 does not decide: the values near the borders in float64,
-// up to kNear of them (choose_exact has all of them).  For the groups' scores that
-// is whatever may be among a group's two largest, for the order whatever may be
-// among the topk largest.
-template <typename T>
-__device__ __noinline__ int choose_near(const GateArgs &p, const T *row, int lane, Candidates &list) {
-    const Scores<float> sc = row_scores<T, float>(p, row, lane);
-    Scores<double> scd{p.sigmoid, 0, 0};
-    if (!p.sigmoid) scd = row_scores<T, double>(p, row, lane);
-    const int per = (p.n_experts + 31) / 32;
-    const auto value = [&](int e) {  // in float32
-        if (e >= p.n_experts) return -INFINITY;
-        const float l = load_logit(row + e);
-        const float c = p.bias ? score_of(sc, l) + p.bias[e] : score_of(sc, l);
-        return l == -INFINITY ? l : (c != c ? INFINITY : c);
-    };
-    const auto exact = [&](int e) {
-        const double c = score_of(scd, load_logit(row + e)) + (p.bias ? (double)p.bias[e] : 0.0);
-        return c != c ? (double)INFINITY : c;
-    };
-    int count = 0;
-    const auto add = [&](bool in, int e) {
-        const uint32_t who = __ballot_sync(kAll, in);
-        const int at = count + __popc(who & ((1u << lane) - 1u));
-        if (in && at < kNear) list.found[at].expert = e;
-        count += __popc(who);
-    };
-    uint32_t kept = ~0u;
-    __syncwarp();
-    if (p.groups > 1) {
-#pragma unroll 1
-        for (int g = 0; g < p.groups; ++g) {
-            const int lo = g * p.group_size, hi = lo + p.group_size;
-            float one = -INFINITY, two = -INFINITY;
-#pragma unroll 1
-            for (int e = lo + lane; e < hi; e += 32) merge_two(one, two, value(e), -INFINITY);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1)
-                merge_two(one, two, __shfl_xor_sync(kAll, one, o), __shfl_xor_sync(kAll, two, o));
-#pragma unroll 1
-            for (int e = lo; e < hi; e += 32) {
-                const float c = e + lane < hi ? value(e + lane) : -INFINITY;
-                add(c != -INFINITY && !(two - c > gap_of(c, two)), e + lane);
-            }
-        }
-        if (count > kNear) return choose_exact(p, row, lane);
-        __syncwarp();
-        for (int i = lane; i < count; i += 32) list.value[i] = exact(list.found[i].expert);
-        __syncwarp();
-        double one = -INFINITY, two = -INFINITY;
-        for (int i = 0; i < count; ++i) {
-            if (list.found[i].expert / p.group_size != lane) continue;
-            const double c = list.value[i];
-            two = c > one ? one : (c > two ? c : two);
-            one = c > one ? c : one;
-        }
-        const uint64_t total = choice_key(two == -INFINITY ? one : one + two);
-        int rank = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const uint64_t other = (uint64_t)__shfl_sync(kAll, (unsigned long long)total, g);
-            rank += other > total || (other == total && g < lane);
-        }
-        kept = __ballot_sync(kAll, lane < p.groups && total != 0 && rank < p.topk_groups);
-        count = 0;
-        __syncwarp();
-    }
-    // without a bias the rest of the choice goes by the logits, which are exact
-    const auto order = [&](int e) {
-        if (e >= p.n_experts || (p.groups > 1 && !(kept >> (e / p.group_size) & 1u))) return -INFINITY;
-        const float c = value(e);
-        if (p.bias || c == -INFINITY) return c;
-        const float l = load_logit(row + e);
-        return l != l ? INFINITY : l;
-    };
-    float high = -INFINITY;
-#pragma unroll 1
-    for (int i = 0; i < per; ++i) high = fmaxf(high, order(i * 32 + lane));
-    const uint32_t bound = nth_largest(choice_key(high), p.topk, lane);
-    const float least = bound ? key_value(bound) : -INFINITY;
-#pragma unroll 1
-    for (int i = 0; i < per; ++i) {
-        const int e = i * 32 + lane;
-        const float c = order(e);
-        add(c != -INFINITY && !(p.bias ? least - c > gap_of(c, least) : least > c), e);
-    }
-    if (count > kNear) return choose_exact(p, row, lane);
-    __syncwarp();
+// What the candidates' order goes by, in float64.
+__device__ __noinline__ void exact_values(const GateArgs &p, const Logits &row, int lane, Candidates &list, int count) {
+    Scores<double> sc{p.sigmoid, 0, 0};
+    if (!p.sigmoid) sc = row_scores<double>(p, row, lane);
     for (int i = lane; i < count; i += 32) {
         const int e = list.found[i].expert;
-        list.value[i] = p.bias ? exact(e) : (double)order(e);
+        const double c = score_of(sc, row[e]) + (p.bias ? (double)p.bias[e] : 0.0);
+        list.value[i] = c != c ? (double)INFINITY : c;
     }
     __syncwarp();
+}
+
+// The groups that stay, of those (lane g: group g) with a bit in `near`, whose two
+// largest values are among the candidates.
+__device__ __noinline__ uint32_t refine_groups(const GateArgs &p, int lane, const Candidates &list, int count,
+                                               uint32_t near, int wanted) {
+    double one = -INFINITY, two = -INFINITY;
+    for (int i = 0; i < count; ++i) {
+        if (list.found[i].expert / p.group_size != lane) continue;
+        const double c = list.value[i];
+        two = c > one ? one : (c > two ? c : two);
+        one = c > one ? c : one;
+    }
+    const uint64_t total = choice_key(two == -INFINITY ? one : one + two);
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const uint64_t other = (uint64_t)__shfl_sync(kAll, (unsigned long long)total, g);
+        rank += (near >> g & 1u) && (other > total || (other == total && g < lane));
+    }
+    __syncwarp();
+    return __ballot_sync(kAll, (near >> lane & 1u) && rank < wanted);
+}
+
+// The candidates' experts in order: lane j has the j-th (-1: none).
+__device__ __noinline__ int refine_order(int topk, int lane, Candidates &list, int count) {
     for (int i = lane; i < count; i += 32) {
         const int e = list.found[i].expert;
         const uint64_t own = choice_key(list.value[i]);
@@ -548,7 +342,195 @@ __device__ __noinline__ int choose_near(const GateArgs &p, const T *row, int lan
         if (rank < 33) list.sorted[rank].expert = e;
     }
     __syncwarp();
-    return lane < p.topk && lane < count ? list.sorted[lane].expert : -1;
+    return lane < topk && lane < count ? list.sorted[lane].expert : -1;
+}
+
+__device__ __forceinline__ float group_total(float one, float two) { return two == -INFINITY ? one : one + two; }
+
+// The two largest of two pairs.
+__device__ __forceinline__ void merge_two(float &one, float &two, float other_one, float other_two) {
+    two = fmaxf(fminf(one, other_one), fmaxf(two, other_two));
+    one = fmaxf(one, other_one);
+}
+
+// The `wanted` largest in order, one after the other: where so many values are
+// equal that they do not fit the list.  Returns how many there were.
+template <int PER>
+__device__ __forceinline__ int take_in_turn(float (&f)[PER], int wanted, int lane, Candidates &list) {
+    int count = 0;
+    for (; count < wanted; ++count) {
+        float mine = f[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < PER; ++i)
+            if (f[i] > mine) {
+                mine = f[i];
+                at = i;
+            }
+        const uint32_t key = choice_key(mine), best = warp_max(key);
+        if (best == 0) break;
+        // the lowest lane has the lowest experts
+        if (lane == __ffs(__ballot_sync(kAll, key == best)) - 1) {
+            list.sorted[count] = {best, lane * PER + at};
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i == at) f[i] = -INFINITY;
+        }
+    }
+    return count;
+}
+
+// Chooses a row's experts: returns the j-th in lane j (-1: none).
+template <int PER>
+__device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int lane, const Scores<float> &sc, float (&f)[PER],
+                                      Candidates &list) {
+    const int e0 = lane * PER;
+    const bool sums = p.bias || p.groups > 1;
+    if (sums) {
+        float b[PER];
+        if (p.bias) load_run<PER>(Logits{reinterpret_cast<const uint8_t *>(p.bias), KMEANS_F32}, e0, p.n_experts,
+                                   p.bias_whole, b);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const float c = p.bias ? score_of(sc, f[i]) + b[i] : score_of(sc, f[i]);
+            f[i] = f[i] == -INFINITY ? f[i] : c;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) f[i] = f[i] != f[i] ? INFINITY : f[i];
+    if (p.groups > 1) {
+        float total = -INFINITY, second = -INFINITY;  // lane g: group g's score, its second largest value
+        bool mine[PER];
+        if (p.lanes_per_group > 0) {  // whole lanes, a power of two of them
+            float one = -INFINITY, two = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) merge_two(one, two, f[i], -INFINITY);
+            for (int o = 1; o < p.lanes_per_group; o <<= 1)
+                merge_two(one, two, __shfl_xor_sync(kAll, one, o), __shfl_xor_sync(kAll, two, o));
+            const int from = (lane * p.lanes_per_group) & 31;
+            total = __shfl_sync(kAll, group_total(one, two), from);
+            second = __shfl_sync(kAll, two, from);
+        } else {
+            for (int g = 0; g < p.groups; ++g) {
+                const int lo = g * p.group_size - e0, hi = lo + p.group_size;
+                float one = -INFINITY, two = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) merge_two(one, two, i >= lo && i < hi ? f[i] : -INFINITY, -INFINITY);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1)
+                    merge_two(one, two, __shfl_xor_sync(kAll, one, o), __shfl_xor_sync(kAll, two, o));
+                if (lane == g) {
+                    total = group_total(one, two);
+                    second = two;
+                }
+            }
+        }
+        if (lane >= p.groups) total = -INFINITY;
+        // the groups in order, and the first that is left out
+        uint32_t kept = 0, key = choice_key(total), last = 0, next = 0;
+        for (int j = 0; j <= p.topk_groups; ++j) {
+            next = warp_max(key);
+            if (next == 0 || j == p.topk_groups) break;
+            const int g = __ffs(__ballot_sync(kAll, key == next)) - 1;
+            kept |= 1u << g;
+            last = next;
+            if (lane == g) key = 0;
+        }
+        if (next != 0 && last != 0) {
+            const float in = key_value(last), out = key_value(next), gap = 2.f * p.gap_of(in, out);
+            if (!(in - out > gap)) {
+                // Near (equal sums are rarely sums of equal parts, so they are looked
+                // at too): what is further above the first left out than float32 may
+                // err stays, what is further below the last kept goes, and the rest
+                // is compared in float64.
+                const uint32_t sure = __ballot_sync(kAll, total > out + gap);
+                const uint32_t near = __ballot_sync(kAll, total >= in - gap && !(total > out + gap));
+                int count = 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int g = (e0 + i) / p.group_size;
+                    const float two = __shfl_sync(kAll, second, g & 31);
+                    const bool take = f[i] != -INFINITY && (near >> (g & 31) & 1u) && !(two - f[i] > p.gap_of(two, f[i]));
+                    const uint32_t who = __ballot_sync(kAll, take);
+                    const int at = count + __popc(who & ((1u << lane) - 1u));
+                    if (take && at < kNear) list.found[at].expert = e0 + i;
+                    count += __popc(who);
+                }
+                // (infinite sums have no order in float32)
+                if (count > kNear || !isfinite(in) || !isfinite(out)) return choose_exact(p, row, lane);
+                __syncwarp();
+                exact_values(p, row, lane, list, count);
+                kept = sure | refine_groups(p, lane, list, count, near, p.topk_groups - __popc(sure));
+            }
+        }
+        if (p.lanes_per_group > 0) {
+            const bool in = kept >> (lane / p.lanes_per_group) & 1u;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) mine[i] = in && f[i] != -INFINITY;
+        } else {
+            int g = e0 / p.group_size, left = (g + 1) * p.group_size - e0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                mine[i] = g < 32 && (kept >> g & 1u) && f[i] != -INFINITY;
+                if (--left == 0) {
+                    ++g;
+                    left = p.group_size;
+                }
+            }
+        }
+        if (!p.bias) {  // the rest of the choice goes by the logits
+            load_run<PER>(row, e0, p.n_experts, p.whole, f);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) f[i] = f[i] != f[i] ? INFINITY : f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) f[i] = mine[i] ? f[i] : -INFINITY;
+    }
+    float high = f[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) high = fmaxf(high, f[i]);
+    const int wanted = min(p.topk + 1, 32);  // (32 lanes have no 33rd: then all are looked at)
+    const uint32_t bound = p.topk < 32 ? nth_largest(choice_key(high), wanted, lane) : 0u;
+    float least = bound ? key_value(bound) : -INFINITY;
+    if (p.bias && isfinite(least)) least -= p.gap_of(least, least);  // and what may be as large
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool in = f[i] >= least && f[i] != -INFINITY;
+        const uint32_t who = __ballot_sync(kAll, in);
+        if (who == 0) continue;
+        const int at = count + __popc(who & ((1u << lane) - 1u));
+        if (in && at < kNear) list.found[at] = {choice_key(f[i]), e0 + i};
+        count += __popc(who);
+    }
+    __syncwarp();
+    const bool listed = count <= kNear;
+    if (!listed) {
+        count = take_in_turn(f, p.topk + 1, lane, list);
+    } else {
+        for (int i = lane; i < count; i += 32) {
+            const Candidate own = list.found[i];
+            int rank = 0;
+            for (int j = 0; j < count; ++j) {
+                const Candidate other = list.found[j];
+                rank += other.key > own.key || (other.key == own.key && other.expert < own.expert);
+            }
+            if (rank < 33) list.sorted[rank] = own;
+        }
+    }
+    __syncwarp();
+    const int chosen = lane < p.topk && lane < count ? list.sorted[lane].expert : -1;
+    bool near = false;
+    if (p.bias && chosen >= 0 && lane + 1 < count) {
+        const int after = list.sorted[lane + 1].expert;
+        const float a = key_value(list.sorted[lane].key), c = key_value(list.sorted[lane + 1].key);
+        near = !(a - c > p.gap_of(a, c)) &&
+               !(row[chosen] == row[after] && p.bias[chosen] == p.bias[after]);
+    }
+    if (!__any_sync(kAll, near)) return chosen;
+    if (!listed) return choose_exact(p, row, lane);
+    exact_values(p, row, lane, list, count);
+    return refine_order(p.topk, lane, list, count);
 }
 
 // The chosen experts' shares of their sum; lane j has expert j's logit.  Scaled
@@ -567,8 +549,8 @@ __device__ __forceinline__ float share_of(bool sigmoid, float l, bool real) {
     return real ? u / sum : 0.f;
 }
 
-template <int PER, typename T>
-__global__ void __launch_bounds__(kGateThreads) gate_kernel(const T *__restrict__ logits, const GateArgs p,
+template <int PER>
+__global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 16 ? 6 : PER <= 32 ? 4 : 2) gate_kernel(const uint8_t *__restrict__ logits, const GateArgs p,
                                                             int32_t *__restrict__ ids, float *__restrict__ weights) {
     __shared__ Candidates lists[kGateThreads / 32];
     griddep_wait();
@@ -578,7 +560,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(const T *__restrict_
     const bool need_sum = !p.sigmoid && (p.bias || p.groups > 1 || !p.renormalize);
     const int64_t step = (int64_t)gridDim.x * (kGateThreads / 32);
     for (int64_t r = (int64_t)blockIdx.x * (kGateThreads / 32) + (threadIdx.x >> 5); r < p.n; r += step) {
-        const T *row = logits + r * p.ldl;
+        const Logits row{logits + r * p.pitch, p.dtype};
         float f[PER];
         load_run<PER>(row, lane * PER, p.n_experts, p.whole, f);
         Scores<float> sc{p.sigmoid, 0.f, 0.f};
@@ -588,7 +570,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(const T *__restrict_
             for (int i = 1; i < PER; ++i) top = fmaxf(top, f[i]);
             top = warp_fmax(top);
             sc.top = top == -INFINITY ? 0.f : top;  // no open expert: scores of 0
-            constexpr int SUMS = PER < 4 ? PER : 4;  // (see gap_of)
+            constexpr int SUMS = PER < 4 ? PER : 4;  // (see gate_args)
             float sum[SUMS] = {};
 #pragma unroll
             for (int i = 0; i < PER; ++i) sum[i % SUMS] += __expf(f[i] - sc.top);
@@ -597,10 +579,9 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(const T *__restrict_
             const float all = warp_sum(sum[0]);
             sc.inverse = all == 0.f ? 0.f : 1.f / all;
         }
-        int e;
-        if (!choose<PER>(p, row, lane, sc, f, list, e)) e = choose_near(p, row, lane, list);
+        const int e = choose<PER>(p, row, lane, sc, f, list);
         const bool real = lane < p.topk && e >= 0;
-        const float l = real ? load_logit(row + e) : 0.f;
+        const float l = real ? row[e] : 0.f;
         float w = p.renormalize ? share_of(p.sigmoid, l, real) : score_of(sc, l);
         if (lane < p.topk) {
             ids[r * p.topk + lane] = real ? e : -1;
@@ -619,7 +600,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(const T *__restrict_
 // expert that is named twice gets the sum, in the choices' order.
 template <typename T>
 __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const float *__restrict__ dweights,
-                                                                 const T *__restrict__ logits, const GateArgs p,
+                                                                 const uint8_t *__restrict__ logits, const GateArgs p,
                                                                  const int32_t *__restrict__ ids,
                                                                  T *__restrict__ dlogits) {
     extern __shared__ float gate_smem[];
@@ -630,13 +611,13 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const float *__
     const bool dense = !p.sigmoid && !p.renormalize;
     const int64_t step = (int64_t)gridDim.x * (kGateThreads / 32);
     for (int64_t r = (int64_t)blockIdx.x * (kGateThreads / 32) + warp; r < p.n; r += step) {
-        const T *row = logits + r * p.ldl;
+        const Logits row{logits + r * p.pitch, p.dtype};
         T *out = dlogits + r * p.n_experts;
         Scores<float> sc{p.sigmoid, 0.f, 0.f};
-        if (dense) sc = row_scores<T, float>(p, row, lane);
+        if (dense) sc = row_scores<float>(p, row, lane);
         int e = lane < p.topk ? ids[r * p.topk + lane] : -1;
         if (e >= p.n_experts) e = -1;
-        const float l = e >= 0 ? load_logit(row + e) : -INFINITY;
+        const float l = e >= 0 ? row[e] : -INFINITY;
         const bool real = l != -INFINITY;  // an expert that is closed to the token has no weight
         const float g = real ? p.scale * dweights[r * p.topk + lane] : 0.f;
         float back = g, all = 0.f;
@@ -664,7 +645,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const float *__
         __syncwarp();
         for (int i = lane; i < p.n_experts; i += 32) {
             float v = own[i];
-            if (dense) v = score_of(sc, load_logit(row + i)) * (v - all);
+            if (dense) v = score_of(sc, row[i]) * (v - all);
             store_logit(out + i, v);
         }
         __syncwarp();
@@ -677,10 +658,10 @@ unsigned gate_blocks(int64_t n) {
     return (unsigned)(blocks < most ? blocks : most);
 }
 
-// Values of a lane: a power of two of them up to 128.
+// Values of a lane: a power of two of them, or 128 for more than 1024 experts.
 int gate_per(int n_experts) {
     int per = 1;
-    while (per * 32 < n_experts) per *= 2;
+    while (per * 32 < n_experts) per *= per < 32 ? 2 : 4;
     return per;
 }
 
@@ -688,31 +669,20 @@ bool on16(const void *p, int64_t pitch_bytes) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && pitch_bytes % 16 == 0;
 }
 
-GateArgs gate_args(const GateShape &g, const void *logits, int64_t ldl, int bytes, const float *bias) {
+GateArgs gate_args(const GateShape &g, int dtype, const void *logits, int64_t ldl, const float *bias) {
     const int size = g.n_experts / g.groups, per = gate_per(g.n_experts), lanes = size % per == 0 ? size / per : 0;
-    return {g.n, ldl, g.n_experts, g.topk, g.groups, g.topk_groups, size, g.sigmoid, g.renormalize, g.scale, bias,
-            on16(logits, ldl * bytes), on16(bias, 0), (lanes & (lanes - 1)) == 0 ? lanes : 0};
+    // Twice a score's error in float32, in 2^-24: an exponential of x is off by (2
+    // |x| + 4) of itself.  The logistic function damps that by s (1 - s), its sum
+    // and quotient add 5: 7.  In softmax |x| e^x is at most 0.37, the sum of n
+    // terms, four accumulators to a lane, adds n / 128 + 8, the rest 6.
+    const float gap = (g.sigmoid ? 16.f : (float)g.n_experts / 64.f + 30.f) * 0x1p-24f;
+    const int64_t pitch = ldl * (dtype == KMEANS_F32 ? 4 : 2);
+    return {g.n, pitch, dtype, g.n_experts, g.topk, g.groups, g.topk_groups, size, g.sigmoid, g.renormalize, g.scale, bias,
+            on16(logits, pitch), on16(bias, 0), (lanes & (lanes - 1)) == 0 ? lanes : 0, gap};
 }
 
 template <typename T>
-cudaError_t gate_typed(const GateShape &g, const void *logits, int64_t ldl, const float *bias, int32_t *ids,
-                       float *weights, cudaStream_t s) {
-    const int per = gate_per(g.n_experts);
-    void (*kernel)(const T *, GateArgs, int32_t *, float *) =
-        per <= 1    ? gate_kernel<1, T>
-        : per <= 2  ? gate_kernel<2, T>
-        : per <= 4  ? gate_kernel<4, T>
-        : per <= 8  ? gate_kernel<8, T>
-        : per <= 16 ? gate_kernel<16, T>
-        : per <= 32 ? gate_kernel<32, T>
-        : per <= 64 ? gate_kernel<64, T>
-                    : gate_kernel<128, T>;
-    return launch_kernel(true, kernel, dim3(gate_blocks(g.n)), dim3(kGateThreads), 0, s, static_cast<const T *>(logits),
-                         gate_args(g, logits, ldl, (int)sizeof(T), bias), ids, weights);
-}
-
-template <typename T>
-cudaError_t gate_grad_typed(const GateShape &g, const float *dweights, const void *logits, int64_t ldl,
+cudaError_t gate_grad_typed(const GateShape &g, int dtype, const float *dweights, const void *logits, int64_t ldl,
                             const int32_t *ids, void *dlogits, cudaStream_t s) {
     constexpr int most = KMEANS_ROUTE_MAX_EXPERTS * (kGateThreads / 32) * 4;
     static std::once_flag once[kMaxDevices];
@@ -725,24 +695,31 @@ cudaError_t gate_grad_typed(const GateShape &g, const float *dweights, const voi
     });
     if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
     return launch_kernel(true, gate_grad_kernel<T>, dim3(gate_blocks(g.n)), dim3(kGateThreads),
-                         (size_t)g.n_experts * (kGateThreads / 32) * 4, s, dweights, static_cast<const T *>(logits),
-                         gate_args(g, logits, ldl, (int)sizeof(T), nullptr), ids, static_cast<T *>(dlogits));
+                         (size_t)g.n_experts * (kGateThreads / 32) * 4, s, dweights, static_cast<const uint8_t *>(logits),
+                         gate_args(g, dtype, logits, ldl, nullptr), ids, static_cast<T *>(dlogits));
 }
 
 }  // namespace
 
 cudaError_t launch_gate(const GateShape &g, int dtype, const void *logits, int64_t ldl, const float *bias, int32_t *ids,
                         float *weights, cudaStream_t s) {
-    if (dtype == KMEANS_F32) return gate_typed<float>(g, logits, ldl, bias, ids, weights, s);
-    return dtype == KMEANS_F16 ? gate_typed<__half>(g, logits, ldl, bias, ids, weights, s)
-                               : gate_typed<__nv_bfloat16>(g, logits, ldl, bias, ids, weights, s);
+    const int per = gate_per(g.n_experts);
+    void (*kernel)(const uint8_t *, GateArgs, int32_t *, float *) = per <= 1    ? gate_kernel<1>
+                                                                    : per <= 2  ? gate_kernel<2>
+                                                                    : per <= 4  ? gate_kernel<4>
+                                                                    : per <= 8  ? gate_kernel<8>
+                                                                    : per <= 16 ? gate_kernel<16>
+                                                                    : per <= 32 ? gate_kernel<32>
+                                                                                : gate_kernel<128>;
+    return launch_kernel(true, kernel, dim3(gate_blocks(g.n)), dim3(kGateThreads), 0, s,
+                         static_cast<const uint8_t *>(logits), gate_args(g, dtype, logits, ldl, bias), ids, weights);
 }
 
 cudaError_t launch_gate_grad(const GateShape &g, int dtype, const float *dweights, const void *logits, int64_t ldl,
                              const int32_t *ids, void *dlogits, cudaStream_t s) {
-    if (dtype == KMEANS_F32) return gate_grad_typed<float>(g, dweights, logits, ldl, ids, dlogits, s);
-    return dtype == KMEANS_F16 ? gate_grad_typed<__half>(g, dweights, logits, ldl, ids, dlogits, s)
-                               : gate_grad_typed<__nv_bfloat16>(g, dweights, logits, ldl, ids, dlogits, s);
+    if (dtype == KMEANS_F32) return gate_grad_typed<float>(g, dtype, dweights, logits, ldl, ids, dlogits, s);
+    return dtype == KMEANS_F16 ? gate_grad_typed<__half>(g, dtype, dweights, logits, ldl, ids, dlogits, s)
+                               : gate_grad_typed<__nv_bfloat16>(g, dtype, dweights, logits, ldl, ids, dlogits, s);
 }
 
 }  // namespace km
