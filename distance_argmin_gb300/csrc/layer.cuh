@@ -63,8 +63,10 @@ struct XentLayout {
     int64_t off_w;       // w likewise (0: its rows are a multiple of 16 bytes)
     int64_t off_target;  // forward: the labels' logits
     int64_t off_stats;   // forward: largest logit and sum of exponentials per class part and row
+    int64_t off_share;   // gradient: each row's share of its gradient (xent.cu)
+    int64_t off_xw;      // gradient: the rows times their share
     int64_t off_dz;      // gradient: a piece's
-    int64_t off_sums;    // gradient: dx so far, where there are several pieces
+    int64_t off_sums;    // gradient: dx so far, where there are several pieces or parts
     int64_t off_partial; // gradient: sums of chunks of the rows
     int64_t bytes;
 };

@@ -23,19 +23,20 @@ namespace km {
 // weights product with a factor:
 // log sum  z = x W^T with a row of x on each tensor-memory lane (p the rows, q the
 //          classes): only each row's largest z and sum of exponentials leave
+// few      the same of few rows, a class on each lane
 // softmax  z once more as in the forward product, dz = g (exp(z - lse) - 1[label])
 // sum      dx over a piece of the classes, added up in float32
 // scaled   dW of such a dz, which is kept times a power of two
-enum class Product { kForward, kRows, kWeights, kLogSum, kSoftmax, kRowsSum, kWeightsScaled };
+enum class Product { kForward, kRows, kWeights, kLogSum, kLogSumFew, kSoftmax, kRowsSum, kWeightsScaled };
 
 __host__ __device__ constexpr bool is_weights(Product m) { return m == Product::kWeights || m == Product::kWeightsScaled; }
 // A's contiguous dimension is the contraction.
 __host__ __device__ constexpr bool is_forward(Product m) {
-    return m == Product::kForward || m == Product::kLogSum || m == Product::kSoftmax;
+    return m == Product::kForward || m == Product::kLogSum || m == Product::kLogSumFew || m == Product::kSoftmax;
 }
 
-// A row that counts: factor * lse (factor as below), the factor of its gradient,
-// its label, and which row of the caller's it is.
+// A row that counts: its lse times log2(e), the factor of its gradient, its label,
+// and which row of the caller's it is.
 struct alignas(16) EntropyRow {
     float lse2, gradient;
     int32_t label, source;
@@ -45,12 +46,16 @@ struct EntropyArgs {
     const EntropyRow *rows;
     const int32_t *count;  // rows that count
     float factor;          // of z: the logits' scale, times log2(e)
+    int tile;              // rows of a unit, a multiple of 32
     float2 *stats;         // log sum: (reference, sum of 2^(factor z - reference)) per class part and row
     float *target;         // log sum: z at the label
     int first;             // class of the piece's first
+    int splits;            // sum: parts of the contraction, each with sums of its own
     float *sums;           // sum: dx so far
+    int64_t split_stride;  // values from one part's sums to the next's
     bool begin, last;      // sum: the first, the last piece
     const float *inverse;  // of dz's scale
+    const float *share;    // sum: per row, what dx is to be multiplied with
     int64_t pitch;         // of dz (softmax), of stats' rows (log sum)
 };
 

@@ -128,7 +128,7 @@ struct Unit {
     int expert, p0, q0, qn;  // q0: first output row (row products: of the matrix, weights: of the expert)
     int c0, c1;              // contraction range (rows of x for weights)
     int slot;                // weights: the partial matrix this chunk of rows goes to (-1: the output);
-                             // log sum: the row tile
+                             // log sum: the row tile; sum: the contraction's part
 
     __device__ __forceinline__ Unit of_lane(int l) const {
         const auto from = [l](int v) { return __shfl_sync(0xffffffffu, v, l); };
@@ -152,6 +152,7 @@ struct Units {
         // (rows of no expert get zeros, but for the cross entropy, which has none of them)
         const bool rest = MODE == Product::kForward || MODE == Product::kRows || is_weights(MODE);
         total = tiles[p.n_experts + (rest ? 1 : 0)] * num_p() * (is_weights(MODE) ? row_tiles() : 1);
+        if (MODE == Product::kRowsSum) total *= p.entropy.splits;
     }
     __device__ __forceinline__ int num_p() const {
         if constexpr (MODE == Product::kLogSum)
@@ -171,6 +172,10 @@ struct Units {
             chunk = g - tiles[e];
             u -= g * per * num_p();
         } else {
+            if (MODE == Product::kRowsSum) {  // part after part of the contraction
+                chunk = u / (tiles[1] * num_p());
+                u -= chunk * (tiles[1] * num_p());
+            }
             while (u >= tiles[e + 1] * num_p()) ++e;
             u -= tiles[e] * num_p();
             per = tiles[e + 1] - tiles[e];
@@ -199,6 +204,12 @@ struct Units {
             if (MODE == Product::kLogSum) t.slot = q;
             t.c0 = 0;
             t.c1 = e < p.n_experts ? p.contraction : 0;
+            if (MODE == Product::kRowsSum) {
+                const int part = ((p.contraction - 1) / p.entropy.splits / lt::BK + 1) * lt::BK;
+                t.slot = chunk;
+                t.c0 = chunk * part;
+                t.c1 = min(t.c0 + part, p.contraction);
+            }
         }
         return t;
     }
@@ -467,6 +478,38 @@ __device__ __forceinline__ void log_sum(const LinearTcParams &p, uint32_t acc, i
     if (mine) g.stats[part * g.pitch + row] = make_float2(c0 < end && isinf(top) ? 0.f : top, sum);
 }
 
+// The same of few rows: a lane has a class, a column is a row, and the warp's 32
+// classes meet by shuffles; columns [c0, end) of the unit whose first row is q0.
+__device__ __forceinline__ void log_sum_few(const LinearTcParams &p, uint32_t acc, int c0, int end, int f, int lane,
+                                            int q0) {
+    const EntropyArgs &g = p.entropy;
+    const bool real = f + lane < p.cols;
+#pragma unroll 1
+    for (int c = c0; c < end; c += 8) {
+        uint32_t r[8];
+        __syncwarp();
+        tmem_ld_8_issue(acc + (uint32_t)c, r);
+        const int label = lane < 8 && c + lane < end ? g.rows[q0 + c + lane].label : -1;
+        tmem_ld_8_wait(r);
+        float2 mine = {-INFINITY, 0.f};  // lane j: column c + j
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float z = __uint_as_float(r[j]);
+            const int at = __shfl_sync(0xffffffffu, label, j);
+            if (at == f + lane && at >= 0) g.target[q0 + c + j] = z;
+            // (NaN is left out of the largest, and shows in the sum)
+            const float x = real ? z * g.factor : -INFINITY;
+            const float top = ord_to_float(__reduce_max_sync(0xffffffffu, x == x ? float_to_ord(x) : 0x007fffffu));
+            const float ref = isinf(top) ? 0.f : top;
+            float sum = real ? exp2_approx(fmaf(z, g.factor, -ref)) : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == j) mine = make_float2(ref, sum);
+        }
+        if (lane < 8 && c + lane < end) g.stats[(int64_t)(f >> 5) * g.pitch + q0 + c + lane] = mine;
+    }
+}
+
 // Softmax: as Finish, a lane with eight classes of a row, whose record is asked for
 // before the accumulator is waited for.  The matrix is rounded to the products'
 // type, as dz is everywhere; times a power of two (in the records' gradient), so
@@ -539,29 +582,30 @@ struct FinishSoftmax {
 
 // Sum: a warp's columns as rows of 32 neighbouring features, added to what the
 // pieces before have left in float32; the last piece rounds once and goes to the
-// rows' own places.
+// rows' own places, unless the contraction is split: then the parts' sums meet
+// after the last piece.  `none`: no term in this piece's part.
 template <typename T>
 __device__ __forceinline__ void add_sums(const LinearTcParams &p, uint32_t acc, int c0, int end, int f, int64_t row0,
-                                         int lane, float factor) {
+                                         int lane, float factor, int part, bool none) {
     const EntropyArgs &g = p.entropy;
-    const bool mine = f + lane < p.cols;
-    float *sums = g.sums + (row0 + c0) * p.cols + f + lane;
+    const bool mine = f + lane < p.cols, last = g.last && g.splits == 1;
+    float *sums = g.sums + part * g.split_stride + (row0 + c0) * p.cols + f + lane;
     T *out = static_cast<T *>(p.out) + f + lane;
 #pragma unroll 1
     for (int c = c0; c < end; c += lt::EPI_ROWS, sums += (int64_t)lt::EPI_ROWS * p.cols) {
-        uint32_t r[8];
+        uint32_t r[8] = {};
         float v[8];
         __syncwarp();
-        tmem_ld_8_issue(acc + (uint32_t)c, r);
+        if (!none) tmem_ld_8_issue(acc + (uint32_t)c, r);
 #pragma unroll
         for (int j = 0; j < lt::EPI_ROWS; ++j) v[j] = !g.begin && mine && c + j < end ? sums[(int64_t)j * p.cols] : 0.f;
-        tmem_ld_8_wait(r);
+        if (!none) tmem_ld_8_wait(r);
 #pragma unroll
         for (int j = 0; j < lt::EPI_ROWS; ++j) {
             if (!mine || c + j >= end) continue;
             v[j] += __uint_as_float(r[j]);
-            if (g.last)
-                out[(int64_t)g.rows[row0 + c + j].source * p.cols] = narrow<T>(v[j] * factor);
+            if (last)
+                out[(int64_t)g.rows[row0 + c + j].source * p.cols] = narrow<T>(v[j] * (factor * g.share[row0 + c + j]));
             else
                 sums[(int64_t)j * p.cols] = v[j];
         }
@@ -700,7 +744,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
         *status.word() = 0u;
         if (pair == 0) *p.status = kPairWordsMark | (uint32_t)num_pairs << kPairCountShift;
     }
-    if (warp == 0) fill_tables(p.offsets, p.n_experts, p.m, WEIGHTS ? p.chunk : BN, edges, tiles, WEIGHTS ? slots : nullptr, lane);
+    constexpr bool OWN_TILE = MODE == Product::kLogSum || MODE == Product::kSoftmax || MODE == Product::kRowsSum;
+    if (warp == 0)
+        fill_tables(p.offsets, p.n_experts, p.m, WEIGHTS ? p.chunk : OWN_TILE ? p.entropy.tile : BN, edges, tiles,
+                    WEIGHTS ? slots : nullptr, lane);
     if (WEIGHTS && p.db && warp == 1)  // (the second table is a copy of the edges)
         fill_tables(p.offsets, p.n_experts, p.m, p.bias_rows, bias_tiles + p.n_experts + 2, bias_tiles, nullptr, lane);
     cluster_sync();  // barriers, tensor memory and tables exist in both CTAs
@@ -777,10 +824,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             if constexpr (MODE == Product::kLogSum) {
                 log_sum<BN>(p, acc, fin.c0, fin.end, f + lane, f + lane < *p.entropy.count, label - t.q0,
                             t.slot * lt::PARTS + part);
+            } else if constexpr (MODE == Product::kLogSumFew) {
+                if (fin.c0 < fin.end && f < p.cols) log_sum_few(p, acc, fin.c0, fin.end, f, lane, t.q0);
             } else if constexpr (MODE == Product::kSoftmax) {
                 if (fin.c0 < fin.end) fin.run(acc);
             } else if constexpr (MODE == Product::kRowsSum) {
-                if (fin.c0 < fin.end) add_sums<T>(p, acc, fin.c0, fin.end, f, fin.out_row, lane, fin.factor);
+                if (fin.c0 < fin.end) add_sums<T>(p, acc, fin.c0, fin.end, f, fin.out_row, lane, fin.factor, t.slot, zero);
             } else if (WEIGHTS && t.slot >= 0) {
                 if (fin.c0 < fin.end)
                     store_sums<BN>(p.partial + ((int64_t)t.slot * p.out_rows + t.q0) * p.cols, p.cols, acc, fin.c0, fin.end,
@@ -1042,7 +1091,10 @@ cudaError_t launch_tc(const LinearShape &sh, const Product16 &g, const LinearTcP
     if (!ok) return cudaErrorInvalidValue;
 
     // at most one unit per row tile, expert and feature tile
-    const int64_t row_tiles = is_weights(MODE)
+    constexpr bool OWN_TILE = MODE == Product::kLogSum || MODE == Product::kSoftmax || MODE == Product::kRowsSum;
+    const int64_t row_tiles = OWN_TILE           ? (sh.m + p.entropy.tile - 1) / p.entropy.tile *
+                                             (MODE == Product::kRowsSum ? p.entropy.splits : 1)
+                              : is_weights(MODE)
                                   ? (sh.n + BN - 1) / BN * (sh.n_experts + sh.m / p.chunk + 1)
                                                         : (sh.m + BN - 1) / BN + (sh.offsets ? sh.n_experts : 0);
     static_assert(kPairs <= kMaxPairWords, "a status word each");

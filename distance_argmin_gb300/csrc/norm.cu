@@ -117,6 +117,22 @@ struct Cut {
     __device__ __forceinline__ bool has(int j) const { return j >= lo && j < hi; }
 };
 
+// What is not the row's of a word, as zero.
+template <typename T, Rows16 ROWS>
+__device__ __forceinline__ uint4 masked(const uint4 &w, const Cut<T, ROWS> &cut) {
+    const int lo = cut.lo * (int)sizeof(T), hi = cut.hi * (int)sizeof(T);
+    uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (4 * i < lo || 4 * i + 2 > hi) u[i] &= 0xffff0000u;
+        if (4 * i + 2 < lo || 4 * i + 4 > hi) u[i] &= 0xffffu;
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// (a row's end shares its aligned word with its neighbour, or with nothing)
+__device__ __forceinline__ bool in_tensor(const uint8_t *p, const Span &in) { return p >= in.lo && p + 16 <= in.hi; }
+
 // A word of row r; what is not the row's reads as zero.
 template <typename T, Rows16 ROWS>
 __device__ __forceinline__ uint4 load_row(const Rows &m, int64_t r, int c, int off, const Cut<T, ROWS> &cut) {
@@ -124,15 +140,7 @@ __device__ __forceinline__ uint4 load_row(const Rows &m, int64_t r, int c, int o
     const uint8_t *p = m.base + r * m.pitch + ((int64_t)c * N - off) * (int)sizeof(T);
     if constexpr (ROWS == Rows16::kAny) return load_piece<false>(p, cut.hi * (int)sizeof(T), m.in);
     if (cut.whole()) return *reinterpret_cast<const uint4 *>(p);
-    const uint4 w = load_word(p, m.in);
-    uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    const int lo = cut.lo * (int)sizeof(T), hi = cut.hi * (int)sizeof(T);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (4 * i < lo || 4 * i + 2 > hi) u[i] &= 0xffff0000u;
-        if (4 * i + 2 < lo || 4 * i + 4 > hi) u[i] &= 0xffffu;
-    }
-    return make_uint4(u[0], u[1], u[2], u[3]);
+    return masked<T, ROWS>(in_tensor(p, m.in) ? *reinterpret_cast<const uint4 *>(p) : load_word(p, m.in), cut);
 }
 
 // The same columns of a vector, 0 where there are none.
@@ -546,7 +554,7 @@ __global__ void __launch_bounds__(LANES ? kSharedBlock : 512, LANES ? 4 : 1)
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
             if (!mine.has(i)) continue;
-            if (mine.whole(i))
+            if (mine.whole(i) || (ROWS == Rows16::kAlike && in_tensor(p + i * mine.stride(), m.in)))
                 copy16(to + i * (int)blockDim.x, p + i * mine.stride());
             else
                 to[i * (int)blockDim.x] =
@@ -582,7 +590,13 @@ __global__ void __launch_bounds__(LANES ? kSharedBlock : 512, LANES ? 4 : 1)
             for (int i = 0; i < PIECES; ++i) {
                 if (!mine.has(i)) continue;
                 float2 g[PAIRS], h[PAIRS];  // (values that do not exist have dy = 0)
-                terms_of<T>(here[tensor + i * (int)blockDim.x], here[i * (int)blockDim.x], mu, rs, g, h);
+                uint4 uy = here[tensor + i * (int)blockDim.x], ux = here[i * (int)blockDim.x];
+                if (ROWS == Rows16::kAlike && !mine.whole(i)) {
+                    const Cut<T, ROWS> cut(i * width + t, at.off, d);
+                    uy = masked<T, ROWS>(uy, cut);
+                    ux = masked<T, ROWS>(ux, cut);
+                }
+                terms_of<T>(uy, ux, mu, rs, g, h);
                 if (SUMS) add_columns<PAIRS>(g, h, dw[SUMS ? i : 0], db[SUMS ? i : 0]);
                 weight_word<T>(in.w.base, kw[i], g);
                 add_terms<T>(g, h, sum, second);

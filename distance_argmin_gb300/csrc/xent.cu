@@ -31,17 +31,19 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------- the rows that count
-constexpr int kBringRows = 64;      // rows of a block
-constexpr int kBringThreads = 256;
+constexpr int kShareRows = 64;      // rows counted together
+constexpr int kBringRows = 8;       // rows of a block, a warp each
+constexpr int kBringThreads = 32 * kBringRows;
 // Up to so many rows a block counts the ones before its own itself (16 labels to
-// a thread); more are counted per block's share by a kernel in front.
+// a thread); more are counted by two kernels in front.
 constexpr int64_t kCountHere = 4096;
 
-// Of kBringRows rows: how many count, whether a label is past the classes, and
-// the largest gradient's magnitude.
-struct alignas(8) Tally {
-    uint16_t count, bad;
+// Of kShareRows rows: how many count (and then: before them), whether a label is
+// past the classes, and the largest gradient's magnitude.
+struct alignas(16) Tally {
+    int32_t count, bad;
     float top;
+    int32_t pad;
 };
 
 struct Bring {
@@ -54,7 +56,7 @@ struct Bring {
     uint8_t *xs;
     int64_t ldxs;  // bytes
     EntropyRow *rows;
-    const Tally *tally;  // null: counted here
+    const Tally *tally;  // of all shares, then of everything (null: counted here)
     int32_t *offsets;    // (2): 0 and the rows that count
     uint32_t *header, *word;  // status, see common.cuh: the products' waits use the word
     float scale;
@@ -62,13 +64,21 @@ struct Bring {
     float *loss, *lse;
     // gradient
     const float *dloss, *lse_in;
-    float *factors;  // dz's scale, and what undoes it
-    bool narrow;     // float16
-    uint16_t *dx;    // ignored rows get zeros
+    const uint8_t *w;  // (classes, k)
+    Span w_in;
+    float *factors;    // dz's scale, and what undoes it
+    float *share;      // per row, see below
+    uint8_t *xw;       // share * x, where dW is wanted
+    bool narrow;       // float16
+    uint16_t *dx;      // ignored rows get zeros
 };
 
 __device__ __forceinline__ int64_t label_of(const Bring &b, int64_t r) {
     return b.id_bytes == 8 ? static_cast<const int64_t *>(b.labels)[r] : (int64_t)static_cast<const int32_t *>(b.labels)[r];
+}
+
+__device__ __forceinline__ float warp_max(float v) {  // of what is not negative, and never NaN
+    return __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(v)));
 }
 
 __global__ void __launch_bounds__(kBringThreads) xent_tally_kernel(const Bring b, Tally *tally, int64_t shares) {
@@ -76,18 +86,66 @@ __global__ void __launch_bounds__(kBringThreads) xent_tally_kernel(const Bring b
     const int lane = threadIdx.x & 31;
     const int64_t share = (int64_t)blockIdx.x * (kBringThreads / 32) + (threadIdx.x >> 5);
     if (share >= shares) return;
-    Tally t{0, 0, 0.f};
+    Tally t{0, 0, 0.f, 0};
 #pragma unroll
-    for (int i = 0; i < kBringRows / 32; ++i) {
-        const int64_t r = share * kBringRows + i * 32 + lane;
+    for (int i = 0; i < kShareRows / 32; ++i) {
+        const int64_t r = share * kShareRows + i * 32 + lane;
         const int64_t l = r < b.m ? label_of(b, r) : -1;
         const bool real = l >= 0 && l < b.classes;
-        t.count += (uint16_t)__popc(__ballot_sync(kAll, real));
-        t.bad |= (uint16_t)__any_sync(kAll, l >= b.classes);
+        t.count += __popc(__ballot_sync(kAll, real));
+        t.bad |= __any_sync(kAll, l >= b.classes);
         if (b.dloss && real) t.top = fmaxf(t.top, fabsf(b.dloss[r]));
     }
-    t.top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(t.top)));  // (not negative, and never NaN)
+    t.top = warp_max(t.top);
     if (lane == 0) tally[share] = t;
+}
+
+// Each share's count becomes that of the rows before it; behind the shares, all.
+constexpr int kScanThreads = 1024;
+
+__global__ void __launch_bounds__(kScanThreads) xent_scan_kernel(Tally *tally, int64_t shares) {
+    __shared__ int sums[kScanThreads / 32];
+    __shared__ int any[kScanThreads / 32];
+    __shared__ float tops[kScanThreads / 32];
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int before = 0, bad = 0;
+    float top = 0.f;
+    for (int64_t i0 = 0; i0 < shares; i0 += kScanThreads) {
+        const int64_t i = i0 + threadIdx.x;
+        const Tally t = i < shares ? tally[i] : Tally{0, 0, 0.f, 0};
+        bad |= t.bad;
+        top = fmaxf(top, t.top);
+        int upto = t.count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kAll, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        int own = 0, all = 0;
+        for (int w = 0; w < kScanThreads / 32; ++w) {
+            if (w < warp) own += sums[w];
+            all += sums[w];
+        }
+        if (i < shares) tally[i].count = before + own + upto - t.count;
+        before += all;
+        __syncthreads();
+    }
+    bad = __any_sync(kAll, bad);
+    top = warp_max(top);
+    if (lane == 0) {
+        any[warp] = bad;
+        tops[warp] = top;
+    }
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int w = 1; w < kScanThreads / 32; ++w) {
+        bad |= any[w];
+        top = fmaxf(top, tops[w]);
+    }
+    tally[shares] = {before, bad, top, 0};
 }
 
 // Sums and maxima over the block, in every thread.
@@ -101,7 +159,7 @@ __device__ __forceinline__ Totals block_totals(Totals t) {
     t.before = __reduce_add_sync(kAll, t.before);
     t.all = __reduce_add_sync(kAll, t.all);
     t.bad = __reduce_or_sync(kAll, t.bad);
-    t.top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(t.top)));
+    t.top = warp_max(t.top);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = t;
     __syncthreads();
     t = part[0];
@@ -115,41 +173,47 @@ __device__ __forceinline__ Totals block_totals(Totals t) {
     return t;
 }
 
-// The power of two that takes gradients of at most `top` to [2^14, 2^15): dz has
-// their magnitude at most, and float16 then keeps probabilities down to 2^-29 of
-// it in full.  (bfloat16 has float32's range.)
+// The power of two that takes gradients of at most `top` to [2^13, 2^14): dz has
+// twice their magnitude at most, and float16 then keeps probabilities down to
+// 2^-28 of it in full.  (bfloat16 has float32's range.)
 __device__ __forceinline__ int scale_exponent(float top) {
     if (!(top > 0.f) || isinf(top)) return 0;
-    return max(-126, min(126, 14 - ilogbf(top)));
+    return max(-126, min(126, 13 - ilogbf(top)));
 }
 
-template <bool WHOLE>
+// dz is rounded to 16 bits, and where a row's dz has one large term, the label's
+// -(1 - p), its rounding would be that of all of dx (up to 2^-8 where rows are
+// few).  So a row's gradient is split into a share in [1/2, 1) and the rest, such
+// that the label's term is a power of two: dz is formed with the rest, dx is
+// multiplied with the share in float32, and dW takes share * x, whose roundings
+// are each value's own.  The label's probability need not be exact for that.
+__device__ __forceinline__ float share_of(float gradient, float z, float lse) {
+    const float rest = fminf(fmaxf(-expm1f(z - lse), 0x1p-20f), 1.f);
+    int e;
+    const float share = fabsf(frexpf(gradient * rest, &e));
+    return share >= 0.5f && share < 1.f ? share : 1.f;  // (0, infinite, NaN)
+}
+
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kBringThreads) xent_bring_kernel(const Bring b) {
-    __shared__ int places[kBringRows];
     griddep_wait();
-    const int64_t r0 = (int64_t)blockIdx.x * kBringRows;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t r0 = (int64_t)blockIdx.x * kBringRows, share0 = r0 / kShareRows * kShareRows;
     Totals t{0, 0, 0, 0.f};
     if (b.tally) {
-        const int64_t shares = (b.m + kBringRows - 1) / kBringRows;
-        for (int64_t i = threadIdx.x; i < shares; i += kBringThreads) {
-            const Tally s = b.tally[i];
-            t.all += s.count;
-            if (i < blockIdx.x) t.before += s.count;
-            t.bad |= s.bad;
-            t.top = fmaxf(t.top, s.top);
-        }
+        const Tally before = b.tally[r0 / kShareRows], all = b.tally[(b.m + kShareRows - 1) / kShareRows];
+        t = {before.count, all.count, all.bad, all.top};
     } else {
         for (int64_t r = threadIdx.x; r < b.m; r += kBringThreads) {
             const int64_t l = label_of(b, r);
             const bool real = l >= 0 && l < b.classes;
             t.all += real;
-            if (r < r0) t.before += real;
+            if (r < share0) t.before += real;
             t.bad |= l >= b.classes;
             if (b.dloss && real) t.top = fmaxf(t.top, fabsf(b.dloss[r]));
         }
+        t = block_totals(t);
     }
-    t = block_totals(t);
     const int exponent = b.narrow ? scale_exponent(t.top * b.scale) : 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         b.offsets[0] = 0;
@@ -161,47 +225,77 @@ __global__ void __launch_bounds__(kBringThreads) xent_bring_kernel(const Bring b
             b.factors[1] = ldexpf(1.f, -exponent);
         }
     }
-    if (warp == 0) {
-        int at = t.before;
+    const int64_t r = r0 + warp;
+    if (r >= b.m) return;
+    // this row among the ones of its share that count
+    int place = t.before;
+    int64_t label = -1;
 #pragma unroll
-        for (int i = 0; i < kBringRows / 32; ++i) {
-            const int64_t r = r0 + i * 32 + lane;
-            const int64_t l = r < b.m ? label_of(b, r) : -1;
-            const bool real = l >= 0 && l < b.classes;
-            const uint32_t which = __ballot_sync(kAll, real);
-            const int place = at + __popc(which & ((1u << lane) - 1u));
-            places[i * 32 + lane] = real ? place : -1;
-            at += __popc(which);
-            if (real) {
-                EntropyRow row{0.f, 0.f, (int32_t)l, (int32_t)r};
-                if (b.dloss) {
-                    row.lse2 = b.lse_in[r] * kLog2E;
-                    row.gradient = ldexpf(b.dloss[r] * b.scale, exponent);
+    for (int i = 0; i < kShareRows / 32; ++i) {
+        const int64_t s = share0 + i * 32 + lane;
+        const int64_t l = s <= r ? label_of(b, s) : -1;
+        const uint32_t which = __ballot_sync(kAll, s < r && l >= 0 && l < b.classes);
+        place += __popc(which);
+        const uint32_t own = __ballot_sync(kAll, s == r);
+        if (own) label = __shfl_sync(kAll, l, __ffs(own) - 1);
+    }
+    const int64_t row_bytes = b.k * 2;
+    const int pieces = (int)((row_bytes + 15) / 16);
+    if (label < 0 || label >= b.classes) {
+        if (lane == 0 && b.loss) {
+            b.loss[r] = 0.f;
+            b.lse[r] = 0.f;
+        }
+        if (b.dx)
+            for (int64_t c = lane; c < b.k; c += 32) b.dx[r * b.k + c] = 0;
+        return;
+    }
+    const uint8_t *from = b.x + r * b.ldx;
+    uint8_t *to = b.xs + place * b.ldxs;
+    const auto piece = [&](const uint8_t *p, int c, const Span &in) {
+        return load_piece<WHOLE>(p + (int64_t)c * 16, (int)min((int64_t)16, row_bytes - (int64_t)c * 16), in);
+    };
+    EntropyRow row{0.f, 0.f, (int32_t)label, (int32_t)r};
+    if (!b.dloss) {
+#pragma unroll 4
+        for (int c = lane; c < pieces; c += 32)  // (xs's rows are padded to whole pieces)
+            *reinterpret_cast<uint4 *>(to + (int64_t)c * 16) = piece(from, c, b.x_in);
+    } else {
+        const uint8_t *wl = b.w + label * row_bytes;
+        float2 z = {0.f, 0.f};
+#pragma unroll 4
+        for (int c = lane; c < pieces; c += 32) {
+            const uint4 ux = piece(from, c, b.x_in), uw = piece(wl, c, b.w_in);
+            *reinterpret_cast<uint4 *>(to + (int64_t)c * 16) = ux;
+            z = __ffma2_rn(widen2<T>(ux.x), widen2<T>(uw.x), z);
+            z = __ffma2_rn(widen2<T>(ux.y), widen2<T>(uw.y), z);
+            z = __ffma2_rn(widen2<T>(ux.z), widen2<T>(uw.z), z);
+            z = __ffma2_rn(widen2<T>(ux.w), widen2<T>(uw.w), z);
+        }
+        float sum = z.x + z.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        const float lse = b.lse_in[r], gradient = b.dloss[r] * b.scale;
+        const float share = share_of(gradient, sum * b.scale, lse);
+        row.lse2 = lse * kLog2E;
+        row.gradient = ldexpf(gradient / share, exponent);
+        if (lane == 0) b.share[place] = share;
+        if (b.xw) {
+            uint8_t *out = b.xw + place * b.ldxs;
+#pragma unroll 4
+            for (int c = lane; c < pieces; c += 32) {
+                const uint4 u = piece(from, c, b.x_in);
+                uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = __fmul2_rn(widen2<T>(v[i]), both(share));
+                    v[i] = narrow2<T>(f.x, f.y);
                 }
-                b.rows[place] = row;
-            } else if (r < b.m && b.loss) {
-                b.loss[r] = 0.f;
-                b.lse[r] = 0.f;
+                *reinterpret_cast<uint4 *>(out + (int64_t)c * 16) = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
     }
-    __syncthreads();
-    const int64_t row_bytes = b.k * 2;
-    const int pieces = (int)((row_bytes + 15) / 16), here = (int)min((int64_t)kBringRows, b.m - r0);
-    for (int i = warp; i < here; i += kBringThreads / 32) {
-        const int place = places[i];
-        if (place >= 0) {
-            const uint8_t *from = b.x + (r0 + i) * b.ldx;
-            uint8_t *to = b.xs + place * b.ldxs;
-#pragma unroll 4
-            for (int c = lane; c < pieces; c += 32)  // (xs's rows are padded to whole pieces)
-                *reinterpret_cast<uint4 *>(to + (int64_t)c * 16) =
-                    load_piece<WHOLE>(from + (int64_t)c * 16, (int)min((int64_t)16, row_bytes - (int64_t)c * 16), b.x_in);
-        } else if (b.dx) {
-            uint16_t *to = b.dx + (r0 + i) * b.k;
-            for (int64_t c = lane; c < b.k; c += 32) to[c] = 0;
-        }
-    }
+    if (lane == 0) b.rows[place] = row;
 }
 
 // ------------------------------------------------------------------- forward
@@ -212,7 +306,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const Entrop
                                                                     int64_t pitch, int parts,
                                                                     const float *__restrict__ target, float factor,
                                                                     float *__restrict__ loss, float *__restrict__ lse) {
-    __shared__ float2 sums[kJoinWarps][32];
+    __shared__ float2 sums[kJoinWarps][33];
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t r = (int64_t)blockIdx.x * 32 + lane;
@@ -226,19 +320,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const Entrop
     };
     float2 s = {-INFINITY, 0.f};
     if (mine) {
-#pragma unroll 4
+#pragma unroll 8
         for (int i = warp; i < parts; i += kJoinWarps) s = join(s, stats[i * pitch + r]);
     }
     sums[warp][lane] = s;
     __syncthreads();
-    if (warp || !mine) return;
-    for (int w = 1; w < kJoinWarps; ++w) s = join(s, sums[w][lane]);
+    // warp w: row w, whose parts its lanes bring together
+    s = sums[lane][warp];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s = join(s, make_float2(__shfl_xor_sync(kAll, s.x, o), __shfl_xor_sync(kAll, s.y, o)));
+    const int64_t row = (int64_t)blockIdx.x * 32 + warp;
+    if (lane || row >= *count) return;
     const float log = log2f(s.y);
-    const int64_t at = rows[r].source;
+    const int64_t at = rows[row].source;
     // The label's distance from the reference with one rounding, as in the sum's
     // exponentials: where the label is all there is the two cancel, however large
     // the logits.
-    const float l = kLn2 * (log - fmaf(target[r], factor, -s.x));
+    const float l = kLn2 * (log - fmaf(target[row], factor, -s.x));
     loss[at] = l < 0.f ? 0.f : l;
     lse[at] = kLn2 * (s.x + log);
 }
@@ -256,6 +355,23 @@ __global__ void __launch_bounds__(256) xent_weights_join_kernel(const float *__r
 #pragma unroll 8
         for (int c = 0; c < chunks; ++c) s.add(partial[(int64_t)c * size + i]);
         dw[i] = narrow<T>(s.value() * *inverse);
+    }
+}
+
+// dx = the sums of the parts of a split contraction, in order.
+template <typename T>
+__global__ void __launch_bounds__(256) xent_rows_join_kernel(const float *__restrict__ sums, int splits, int64_t stride,
+                                                             const EntropyRow *__restrict__ rows,
+                                                             const float *__restrict__ share, const int32_t *count,
+                                                             int64_t k, const float *inverse, T *dx) {
+    griddep_wait();
+    const int64_t size = *count * k;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < size; i += (int64_t)gridDim.x * 256) {
+        float s = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < splits; ++c) s += sums[c * stride + i];
+        const int64_t r = i / k;
+        dx[rows[r].source * k + (i - r * k)] = narrow<T>(s * (*inverse * share[r]));
     }
 }
 
@@ -283,12 +399,51 @@ LinearTcParams params(const LinearShape &sh, int64_t cols, int64_t contraction, 
     return p;
 }
 
-// Rows per unit: few where all units then fit one round of the pairs (as for the
-// experts' products).
+// Rows of a unit of a product with `rows` rows and num_p feature tiles.  A stage of
+// t rows takes the tensor pipe 2 t cycles and shared memory 256 + t (an operand of
+// 256 features goes in and out beside the rows), so large units are best; but all
+// pairs wait for the last round of units.  (1031 rows of 10007 classes, 928 that
+// count: three rounds of 256 or of 192.)
+int rows_per_unit(int64_t rows, int64_t num_p) {
+    int best = 256;
+    int64_t least = INT64_MAX;
+    for (int t = 256; t >= 64; t -= 32) {
+        const int64_t units = (rows + t - 1) / t * num_p, rounds = (units + kPairs - 1) / kPairs;
+        if (rounds * (256 + t) < least) {
+            least = rounds * (256 + t);
+            best = t;
+        }
+    }
+    return best;
+}
+
 template <Product MODE>
-cudaError_t product(const LinearShape &sh, const Product16 &g, const LinearTcParams &p, int64_t rows, cudaStream_t s) {
-    const auto fits = [&](int64_t bn) { return (rows + bn - 1) / bn * p.num_p <= pairs_here(); };
-    return fits(128) ? launch_typed<MODE, 128>(sh, g, p, s) : launch_typed<MODE, 256>(sh, g, p, s);
+cudaError_t product(const LinearShape &sh, const Product16 &g, LinearTcParams &p, int64_t rows, cudaStream_t s) {
+    p.entropy.tile = rows_per_unit(rows, p.num_p);
+    return p.entropy.tile <= 128 ? launch_typed<MODE, 128>(sh, g, p, s) : launch_typed<MODE, 256>(sh, g, p, s);
+}
+
+cudaError_t weights_product(const LinearShape &sh, const Product16 &g, const LinearTcParams &p, cudaStream_t s) {
+    constexpr Product MODE = Product::kWeightsScaled;
+    return (sh.n + 127) / 128 * p.num_p <= pairs_here() ? launch_typed<MODE, 128>(sh, g, p, s)
+                                                        : launch_typed<MODE, 256>(sh, g, p, s);
+}
+
+// Parts of dx's contraction (the classes of a piece), where dx has few tiles.
+int rows_splits(int64_t m, int64_t piece, int64_t k) {
+    const int64_t units = (m + 255) / 256 * ((k + lt::BP - 1) / lt::BP);
+    if (2 * units > kPairs) return 1;
+    return (int)std::max((int64_t)1, std::min(kPairs / units, piece / 512));
+}
+
+// Few rows: the classes go on the tensor-memory lanes.
+constexpr int64_t kFewRows = 64;
+
+// Class parts that the forward product leaves sums of.
+int64_t class_parts(int64_t m, int64_t n) {
+    if (m <= kFewRows) return (n + 31) / 32;
+    const int tile = rows_per_unit(n, (m + lt::BP - 1) / lt::BP);
+    return (n + tile - 1) / tile * lt::PARTS;
 }
 
 }  // namespace
@@ -313,16 +468,19 @@ XentLayout xent_layout(bool grad, int64_t m, int64_t n, int64_t k) {
     };
     L.off_info = take(64);
     L.off_rows = take(m * (int64_t)sizeof(EntropyRow));
-    L.off_tally = take((m + kBringRows - 1) / kBringRows * (int64_t)sizeof(Tally));
+    L.off_tally = take(((m + kShareRows - 1) / kShareRows + 1) * (int64_t)sizeof(Tally));
     L.off_x = take(m * align_up(k, 8) * 2);
     if (k % 8 != 0) L.off_w = take(n * align_up(k, 8) * 2);
     if (!grad) {
         L.off_target = take(m * 4);
-        L.off_stats = take(align_up(m, 32) * ((n + 31) / 32 + 2 * lt::PARTS) * 8);
+        L.off_stats = take(align_up(m, 32) * class_parts(m, n) * 8);
     } else {
         const int64_t piece = xent_piece(m, n);
+        const int splits = rows_splits(m, piece, k);
+        L.off_share = take(m * 4);
+        L.off_xw = take(m * align_up(k, 8) * 2);
         L.off_dz = take(m * piece * 2);
-        if (piece < n) L.off_sums = take(m * k * 4);
+        if (piece < n || splits > 1) L.off_sums = take(splits * m * k * 4);
         L.off_partial = take((m > kChunk ? (m + kChunk - 1) / kChunk : 0) * piece * k * 4);
     }
     L.bytes = grad ? std::max(o, xent_layout(false, m, n, k).bytes) : o;  // (the gradient's serves both)
@@ -364,19 +522,23 @@ cudaError_t start(const XentShape &sh, const void *x, int64_t ldx, const void *w
     b.scale = sh.scale;
     b.narrow = !sh.bf16;
     out.factors = b.factors = b.dloss ? reinterpret_cast<float *>(info + 16) : nullptr;
-    const int64_t shares = (sh.m + kBringRows - 1) / kBringRows;
+    b.w = static_cast<const uint8_t *>(w);
+    b.w_in = {b.w, b.w + sh.n * sh.k * 2};
     cudaError_t e = cudaSuccess;
     if (sh.m > kCountHere) {
         Tally *tally = reinterpret_cast<Tally *>(ws + L.off_tally);
+        const int64_t shares = (sh.m + kShareRows - 1) / kShareRows;
         constexpr int per = kBringThreads / 32;
         e = launch_kernel(true, xent_tally_kernel, dim3((unsigned)((shares + per - 1) / per)), dim3(kBringThreads), 0, s, b,
                           tally, shares);
+        if (e == cudaSuccess) e = launch_kernel(true, xent_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, tally, shares);
         b.tally = tally;
     }
     const bool whole = rows16(x, ldx) && sh.k % 8 == 0;
+    const auto bring = sh.bf16 ? (whole ? xent_bring_kernel<__nv_bfloat16, true> : xent_bring_kernel<__nv_bfloat16, false>)
+                               : (whole ? xent_bring_kernel<__half, true> : xent_bring_kernel<__half, false>);
     if (e == cudaSuccess)
-        e = launch_kernel(true, whole ? xent_bring_kernel<true> : xent_bring_kernel<false>, dim3((unsigned)shares),
-                          dim3(kBringThreads), 0, s, b);
+        e = launch_kernel(true, bring, dim3((unsigned)((sh.m + kBringRows - 1) / kBringRows)), dim3(kBringThreads), 0, s, b);
     out.w = w;
     out.ldw = sh.k;
     if (e == cudaSuccess && sh.k % 8 != 0) {
@@ -392,6 +554,7 @@ cudaError_t start(const XentShape &sh, const void *x, int64_t ldx, const void *w
     out.entropy.rows = b.rows;
     out.entropy.count = b.offsets + 1;
     out.entropy.factor = sh.scale * kLog2E;
+    out.entropy.splits = 1;
     return e;
 }
 
@@ -406,23 +569,31 @@ cudaError_t launch_xent(const XentShape &sh, const void *x, int64_t ldx, const v
     Start st;
     cudaError_t e = start(sh, x, ldx, w, b, L, ws, st, s);
     if (e != cudaSuccess) return e;
-    // the classes are the product's rows, the rows its features
-    const LinearShape ps{sh.n, sh.m, sh.k, 1, nullptr, sh.bf16};
-    Product16 g{};
-    g.a = st.xs;
-    g.pitch_w = st.ldxs;
-    g.b = st.w;
-    g.ldb = st.ldw;
     EntropyArgs en = st.entropy;
     en.stats = reinterpret_cast<float2 *>(ws + L.off_stats);
     en.target = reinterpret_cast<float *>(ws + L.off_target);
     en.pitch = align_up(sh.m, 32);
-    const LinearTcParams p = params(ps, sh.m, sh.k, st.word, en);
-    const int64_t tiles128 = (sh.n + 127) / 128;
-    const bool small = tiles128 * p.num_p <= pairs_here();
-    e = small ? launch_typed<Product::kLogSum, 128>(ps, g, p, s) : launch_typed<Product::kLogSum, 256>(ps, g, p, s);
+    Product16 g{};
+    if (sh.m <= kFewRows) {
+        const LinearShape ps{sh.m, sh.n, sh.k, 1, st.offsets, sh.bf16};
+        g.a = st.w;
+        g.pitch_w = st.ldw;
+        g.b = st.xs;
+        g.ldb = st.ldxs;
+        const LinearTcParams p = params(ps, sh.n, sh.k, st.word, en);
+        e = launch_typed<Product::kLogSumFew, 64>(ps, g, p, s);
+    } else {
+        // the classes are the product's rows, the rows its features
+        const LinearShape ps{sh.n, sh.m, sh.k, 1, nullptr, sh.bf16};
+        g.a = st.xs;
+        g.pitch_w = st.ldxs;
+        g.b = st.w;
+        g.ldb = st.ldw;
+        LinearTcParams p = params(ps, sh.m, sh.k, st.word, en);
+        e = product<Product::kLogSum>(ps, g, p, sh.n, s);
+    }
     if (e != cudaSuccess) return e;
-    const int parts = (int)((small ? tiles128 : (sh.n + 255) / 256) * lt::PARTS);
+    const int parts = (int)class_parts(sh.m, sh.n);
     return launch_kernel(true, xent_join_kernel, dim3((unsigned)((sh.m + 31) / 32)), dim3(32 * kJoinWarps), 0, s,
                          (const EntropyRow *)en.rows, en.count, (const float2 *)en.stats, en.pitch, parts,
                          (const float *)en.target, en.factor, loss, lse);
@@ -439,6 +610,8 @@ cudaError_t launch_xent_grad(const XentShape &sh, const float *dloss, const void
     b.dloss = dloss;
     b.lse_in = lse;
     b.dx = static_cast<uint16_t *>(dx);
+    b.share = reinterpret_cast<float *>(ws + L.off_share);
+    b.xw = dw ? ws + L.off_xw : nullptr;
     Start st;
     cudaError_t e = start(sh, x, ldx, w, b, L, ws, st, s);
     const int64_t piece = xent_piece(sh.m, sh.n);
@@ -446,6 +619,9 @@ cudaError_t launch_xent_grad(const XentShape &sh, const float *dloss, const void
     en.pitch = piece;
     en.inverse = st.factors + 1;
     en.sums = reinterpret_cast<float *>(ws + L.off_sums);
+    en.splits = rows_splits(sh.m, piece, sh.k);
+    en.split_stride = sh.m * sh.k;
+    en.share = b.share;
     void *dz = ws + L.off_dz;
     for (int64_t c = 0; c < sh.n && e == cudaSuccess; c += piece) {
         const int64_t here = std::min(piece, sh.n - c);
@@ -470,14 +646,14 @@ cudaError_t launch_xent_grad(const XentShape &sh, const float *dloss, const void
         }
         if (e == cudaSuccess && dw) {
             uint16_t *out = static_cast<uint16_t *>(dw) + c * sh.k;
-            g.a = st.xs;
+            g.a = b.xw;
             g.lda = st.ldxs;
             g.out = out;
             p = params(ps, sh.k, here, st.word, en);
             p.out = out;
             p.wide = rows16(out, sh.k);
             p.partial = reinterpret_cast<float *>(ws + L.off_partial);
-            e = product<Product::kWeightsScaled>(ps, g, p, here, s);
+            e = weights_product(ps, g, p, s);
             if (e == cudaSuccess && sh.m > kChunk) {
                 const int64_t size = here * sh.k, blocks = (size + 255) / 256;
                 const dim3 grid((unsigned)std::min(blocks, (int64_t)kSMs * 8));
@@ -489,6 +665,17 @@ cudaError_t launch_xent_grad(const XentShape &sh, const float *dloss, const void
                                             kChunk, size, en.inverse, reinterpret_cast<__half *>(out));
             }
         }
+    }
+    if (e == cudaSuccess && dx && en.splits > 1) {
+        const int64_t blocks = (sh.m * sh.k + 255) / 256;
+        const dim3 grid((unsigned)std::min(blocks, (int64_t)kSMs * 8));
+        const float *sums = en.sums;
+        const auto join = [&](auto kernel, auto *out) {
+            return launch_kernel(true, kernel, grid, dim3(256), 0, s, sums, en.splits, en.split_stride, en.rows, en.share,
+                                 en.count, sh.k, en.inverse, out);
+        };
+        e = sh.bf16 ? join(xent_rows_join_kernel<__nv_bfloat16>, static_cast<__nv_bfloat16 *>(dx))
+                    : join(xent_rows_join_kernel<__half>, static_cast<__half *>(dx));
     }
     return e;
 }

@@ -5,8 +5,10 @@ cores, within 6e-9 k + 2^-22 of the sum of its terms' magnitudes (cut off, not
 rounded); ``dz`` below is the largest of a row.  The logarithm of the sum is
 within dz + (2^-21 + |z| 2^-22) of its value, the loss within twice that.  In the
 gradient a probability is within (that + 2^-21) of itself, dz is rounded to 16
-bits (a relative 2^-b; float16 also 2^-39 of the largest dloss * scale, half its
-smallest step after the power of two), the products cut off as the logits do, and
+bits (a relative 2^-b; float16 also 2^-38 of the largest dloss * scale, half its
+smallest step 2^-24 after the power of two that takes that to 2^13), dW takes x
+times a factor in [1/2, 1), rounded to 16 bits once more (2^-b of each term, and
+2^-25, half float16's smallest step), the products cut off as the logits do, and
 the result is rounded once.  The hardware's exp2 gives 0 for what is below 2^-126,
 the smallest normal number: so much a probability may also be off by.
 """
@@ -70,7 +72,7 @@ def check_grad(km, dloss, x, w, labels, scale=1.0, **kw):
     rel = 2 * cut + 2.0 ** -20 + z.abs().amax(1) * 2.0 ** -21
     dz_off = g.abs()[:, None] * (p * rel[:, None] + 2.0 ** -126) + 2.0 ** -BITS[dt] * dz.abs() * (1 + rel[:, None])
     if dt is torch.float16 and g.numel():
-        dz_off = dz_off + 2.0 ** -39 * g.abs().max()
+        dz_off = dz_off + 2.0 ** -38 * g.abs().max()
     xd, wd = x[live].double(), w.double()
     want, off = torch.zeros(x.shape, dtype=torch.float64, device="cuda"), torch.zeros((), device="cuda")
     off = torch.zeros_like(want)
@@ -80,6 +82,8 @@ def check_grad(km, dloss, x, w, labels, scale=1.0, **kw):
     assert bool(((dx.double() - want).abs() <= bound).all())
     want_w = dz.t() @ xd
     off_w = dz_off.t() @ xd.abs() + (CUT * x.shape[0] + 2.0 ** -20) * (dz.abs().t() @ xd.abs())
+    # share * x: dz is then held as dz / share, which is at most twice as large
+    off_w = off_w + 2.0 ** -BITS[dt] * ((dz.abs() + dz_off).t() @ xd.abs()) + 2 * TINY[dt] * dz.abs().sum(0)[:, None]
     bound = off_w + 1.01 * 2.0 ** -BITS[dt] * (want_w.abs() + off_w) + TINY[dt]
     assert bool(((dw.double() - want_w).abs() <= bound).all())
     return lse, dx, dw
