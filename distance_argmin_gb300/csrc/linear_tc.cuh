@@ -57,6 +57,7 @@ constexpr int BP = 256;            // features per unit (UMMA M of the pair)
 constexpr int BP_CTA = BP / 2;
 constexpr int BK = 64;             // contraction per stage: 128 bytes of 16-bit values
 constexpr int CHUNK_BLOCKS = kChunk / BK;
+constexpr int LOG_BLOCKS = 512 / BK;  // of an accumulator of the log sums
 constexpr int EPI_WARPS = 16;       // four per tensor-memory lane quarter, a quarter of the columns each
 constexpr int WARP_TMA = EPI_WARPS, WARP_MMA = WARP_TMA + 1, WARP_RELAY = WARP_TMA + 2;
 constexpr int THREADS = (WARP_RELAY + 1) * 32;
@@ -429,85 +430,99 @@ __device__ __forceinline__ void store_part(const LinearTcParams &p, const CUtens
     }
 }
 
-// Log sum: a lane has a row and goes through the classes [c0, end) of its unit, 32
-// at a time: the largest factor * z so far and the sum of the exponentials about
-// it, in powers of two.  A row whose largest is infinite keeps the reference 0, so
-// that the sum says what it is (0, infinite or NaN); no classes leave (-inf, 0).
-template <int BN>
-__device__ __forceinline__ void log_sum(const LinearTcParams &p, uint32_t acc, int c0, int end, int64_t row, bool mine,
-                                        int label, int part) {
-    const EntropyArgs &g = p.entropy;
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll 1
-    for (int c = c0; c < end; c += 32) {
-        float v[32];
+// The logits of the log sums are results in float32, whose last bits an
+// accumulator of thousands of terms would cut off (see kChunk: 2048 terms left
+// losses 1.5e-6 off, a float32 product 6e-7).  So their contraction goes through
+// the two accumulators in chunks of 512 terms, which an epilogue warp adds up in
+// registers: COLS columns from `acc` on.  The accumulators are free again before
+// the exponentials begin.  Returns the count of accumulator uses, or -1 where a
+// wait gave up.
+template <int BN, int COLS, typename Status>
+__device__ __forceinline__ int sum_logits(float (&v)[COLS], uint32_t acc, uint32_t full, uint32_t empty, int blocks, int use,
+                                          const Status &status) {
+    const auto chunk = [&](auto first) {
+        const uint32_t buf = (uint32_t)use & 1u;
+        if (!mbar_wait_warp(full + 8 * buf, (use >> 1) & 1, status)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < COLS; c += 8) {
+            uint32_t r[8];
+            tmem_ld_8_issue(acc + buf * BN + (uint32_t)c, r);
+            tmem_ld_8_wait(r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[c + j] = decltype(first)::value ? __uint_as_float(r[j]) : v[c + j] + __uint_as_float(r[j]);
+        }
+        tc_fence_before();
         __syncwarp();
-        tmem_ld_32x32b_x32(acc + (uint32_t)c, v);
-        const int left = end - c;
-        float high = -INFINITY;
-        if (left >= 32) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) high = fmaxf(high, v[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                if (j >= left) v[j] = -INFINITY;
-                high = fmaxf(high, v[j]);
-            }
-        }
-        const int at = label - c;
-        if (__any_sync(0xffffffffu, (unsigned)at < 32u)) {
-            float z = 0.f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (at == j) z = v[j];
-            if (mine && (unsigned)at < 32u && at < left) g.target[row] = z;
-        }
-        const float next = fmaxf(top, high * g.factor);
-        const float ref = isinf(next) ? 0.f : next;
-        if (top != -INFINITY) sum *= exp2_approx(isinf(top) ? -ref : top - ref);
-        float2 more = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            const float2 x = __ffma2_rn(make_float2(v[j], v[j + 1]), both(g.factor), both(-ref));
-            more = __fadd2_rn(more, make_float2(exp2_approx(x.x), exp2_approx(x.y)));
-        }
-        sum += more.x + more.y;
-        top = next;
-    }
-    if (mine) g.stats[part * g.pitch + row] = make_float2(c0 < end && isinf(top) ? 0.f : top, sum);
+        if (lane_id() == 0) mbar_arrive_cluster(empty + 8 * buf);
+        ++use;
+        blocks -= lt::LOG_BLOCKS;
+        return true;
+    };
+    if (!chunk(std::true_type{})) return -1;
+#pragma unroll 1
+    while (blocks > 0)
+        if (!chunk(std::false_type{})) return -1;
+    return use;
 }
 
-// The same of few rows: a lane has a class, a column is a row, and the warp's 32
-// classes meet by shuffles; columns [c0, end) of the unit whose first row is q0.
-__device__ __forceinline__ void log_sum_few(const LinearTcParams &p, uint32_t acc, int c0, int end, int f, int lane,
-                                            int q0) {
+// Log sum: a lane has a row and `count` classes of it: the largest factor * z and
+// the sum of the exponentials about it, in powers of two.  A row whose largest is
+// infinite keeps the reference 0, so that the sum says what it is (0, infinite or
+// NaN); no classes leave (-inf, 0).  `label`: the row's, from the first class on.
+template <int COLS>
+__device__ __forceinline__ void log_sum(const EntropyArgs &g, float (&v)[COLS], int count, int64_t row, bool mine,
+                                        int label, int part) {
+    float high = -INFINITY;
+    if (count < COLS) {
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+            if (j >= count) v[j] = -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) high = fmaxf(high, v[j]);
+    if (__any_sync(0xffffffffu, (unsigned)label < (unsigned)COLS)) {
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+            if (label == j) z = v[j];
+        if (mine && (unsigned)label < (unsigned)COLS && label < count) g.target[row] = z;
+    }
+    const float top = high * g.factor, ref = isinf(top) ? 0.f : top;
+    float2 sum = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < COLS; j += 2) {
+        const float2 x = __ffma2_rn(make_float2(v[j], v[j + 1]), both(g.factor), both(-ref));
+        sum = __fadd2_rn(sum, make_float2(exp2_approx(x.x), exp2_approx(x.y)));
+    }
+    if (mine) g.stats[part * g.pitch + row] = make_float2(count > 0 ? ref : -INFINITY, sum.x + sum.y);
+}
+
+// The same of few rows: a lane has a class, v[j] is row q0 + j (of `count`), and the
+// warp's 32 classes from f on meet by shuffles.
+template <int COLS>
+__device__ __forceinline__ void log_sum_few(const LinearTcParams &p, const float (&v)[COLS], int count, int f, int lane,
+                                            int64_t q0) {
     const EntropyArgs &g = p.entropy;
     const bool real = f + lane < p.cols;
-#pragma unroll 1
-    for (int c = c0; c < end; c += 8) {
-        uint32_t r[8];
-        __syncwarp();
-        tmem_ld_8_issue(acc + (uint32_t)c, r);
-        const int label = lane < 8 && c + lane < end ? g.rows[q0 + c + lane].label : -1;
-        tmem_ld_8_wait(r);
-        float2 mine = {-INFINITY, 0.f};  // lane j: column c + j
+    const int label = lane < count ? g.rows[q0 + lane].label : -1;
+    float2 mine = {-INFINITY, 0.f};  // lane j: row q0 + j
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float z = __uint_as_float(r[j]);
-            const int at = __shfl_sync(0xffffffffu, label, j);
-            if (at == f + lane && at >= 0) g.target[q0 + c + j] = z;
-            // (NaN is left out of the largest, and shows in the sum)
-            const float x = real ? z * g.factor : -INFINITY;
-            const float top = ord_to_float(__reduce_max_sync(0xffffffffu, x == x ? float_to_ord(x) : 0x007fffffu));
-            const float ref = isinf(top) ? 0.f : top;
-            float sum = real ? exp2_approx(fmaf(z, g.factor, -ref)) : 0.f;
+    for (int j = 0; j < COLS; ++j) {
+        const float z = v[j];
+        const int at = __shfl_sync(0xffffffffu, label, j);
+        if (at == f + lane) g.target[q0 + j] = z;
+        // (NaN is left out of the largest, and shows in the sum)
+        const float x = real ? z * g.factor : -INFINITY;
+        const float top = ord_to_float(__reduce_max_sync(0xffffffffu, x == x ? float_to_ord(x) : 0x007fffffu));
+        const float ref = isinf(top) ? 0.f : top;
+        float sum = real ? exp2_approx(fmaf(z, g.factor, -ref)) : 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == j) mine = make_float2(ref, sum);
-        }
-        if (lane < 8 && c + lane < end) g.stats[(int64_t)(f >> 5) * g.pitch + q0 + c + lane] = mine;
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == j) mine = make_float2(ref, sum);
     }
+    if (lane < count) g.stats[(int64_t)(f >> 5) * g.pitch + q0 + lane] = mine;
 }
 
 // Softmax: as Finish, a lane with eight classes of a row, whose record is asked for
@@ -698,6 +713,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
     constexpr bool A_MN = !is_forward(MODE), B_MN = is_weights(MODE);
     constexpr bool RELAY = is_weights(MODE);  // rows may have to be cleared before the MMA
     constexpr bool WEIGHTS = is_weights(MODE);
+    constexpr bool LOG_SUM = MODE == Product::kLogSum || MODE == Product::kLogSumFew;
+    constexpr int CHUNK = LONG ? lt::CHUNK_BLOCKS : LOG_SUM ? lt::LOG_BLOCKS : 0;  // k-blocks of an accumulator (0: all)
     static_assert(!B_MN || BN >= 128, "an N-contiguous operand comes in chunks of 64 per CTA");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
@@ -801,6 +818,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             fin.f = f;
             fin.out_row = WEIGHTS ? (int64_t)t.expert * p.out_rows + t.q0 : (int64_t)t.q0;
             if constexpr (MODE == Product::kForward) fin.add = p.residual && !zero;
+            if constexpr (LOG_SUM) {
+                float v[F::COLS];
+                const int count = max(0, fin.end - fin.c0);
+                use = sum_logits<BN>(v, tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)fin.c0, bar(C::T_FULL),
+                                     map_to_cta(bar(C::T_EMPTY), 0), (t.c1 - t.c0 + lt::BK - 1) / lt::BK, use, status);
+                if (use < 0) break;
+                if constexpr (MODE == Product::kLogSumFew) {
+                    if (count > 0 && f < p.cols) log_sum_few(p, v, count, f, lane, (int64_t)t.q0 + fin.c0);
+                } else {
+                    const bool mine = f + lane < *p.entropy.count;
+                    const int label = mine ? p.entropy.rows[f + lane].label - t.q0 - fin.c0 : -1;
+                    log_sum(p.entropy, v, count, f + lane, mine, label, t.slot * lt::PARTS + part);
+                }
+                continue;
+            }
             bool ready = zero;
             if (LONG && t.c1 - t.c0 > kChunk) {
                 use = sum_chunks<BN>(p.partial + (int64_t)blockIdx.x * kChunkTile + quarter * 32 + lane, fin.c0, fin.end,
@@ -811,8 +843,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
             }
             const int buf = use & 1;
             fin.prefetch();
-            int label = -1;
-            if (MODE == Product::kLogSum && f + lane < *p.entropy.count) label = p.entropy.rows[f + lane].label;
             if (!ready) {
                 bool ok = mbar_wait_warp(bar(C::T_FULL + buf), (use >> 1) & 1, status);
                 // a part that meets at barriers goes on together or not at all
@@ -821,12 +851,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                 tc_fence_after();
             }
             const uint32_t acc = tmem_base + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
-            if constexpr (MODE == Product::kLogSum) {
-                log_sum<BN>(p, acc, fin.c0, fin.end, f + lane, f + lane < *p.entropy.count, label - t.q0,
-                            t.slot * lt::PARTS + part);
-            } else if constexpr (MODE == Product::kLogSumFew) {
-                if (fin.c0 < fin.end && f < p.cols) log_sum_few(p, acc, fin.c0, fin.end, f, lane, t.q0);
-            } else if constexpr (MODE == Product::kSoftmax) {
+            if constexpr (MODE == Product::kSoftmax) {
                 if (fin.c0 < fin.end) fin.run(acc);
             } else if constexpr (MODE == Product::kRowsSum) {
                 if (fin.c0 < fin.end) add_sums<T>(p, acc, fin.c0, fin.end, f, fin.out_row, lane, fin.factor, t.slot, zero);
@@ -975,7 +1000,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                                              : umma_smem_desc(sbase + C::A_BYTES, 1024, kLayoutSW128);
                     const uint32_t a_hi = (uint32_t)(a0 >> 32), b_hi = (uint32_t)(b0 >> 32);
                     // (a chunk of rows is a unit of its own in the weights product)
-                    for (int blocks = kblocks; blocks > 0 && ok; blocks -= LONG ? lt::CHUNK_BLOCKS : blocks) {
+                    for (int blocks = kblocks; blocks > 0 && ok; blocks -= CHUNK ? CHUNK : blocks) {
                         const int buf = use & 1;
                         const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
                         if (!mbar_wait_converged(bar(C::T_EMPTY + buf), ((use >> 1) & 1) ^ 1, status)) {
@@ -984,7 +1009,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::THREADS, 1)
                         }
                         tc_fence_after();
                         uint32_t more = 0;  // the first MMA of a chunk clears the accumulator
-                        for (int left = LONG ? min(blocks, lt::CHUNK_BLOCKS) : blocks; left > 0; --left) {
+                        for (int left = CHUNK ? min(blocks, CHUNK) : blocks; left > 0; --left) {
                             const uint32_t off = (uint32_t)s * (C::STAGE >> 4);
                             const uint32_t a_lo = (uint32_t)a0 + off, b_lo = (uint32_t)b0 + off;
                             if (!mbar_wait_converged(bar((RELAY ? C::READY : C::FULL) + s), phase, status)) {
