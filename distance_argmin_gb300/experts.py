@@ -5,8 +5,9 @@ Which expert a token goes to is a choice of up to ``ROUTE_MAX_TOPK`` ids per
 token.  With centroids it is the nearest one (``kmeans_assign``, the page "Three
 shapes that fit an eager Gram assignment", section "Gram assignment"): the
 clusters of the tokens are the experts, and a fit of the centroids on a sample
-of tokens is all the training the choice needs.  A learned choice passes its
-own ids and weights.
+of tokens is all the training the choice needs.  A learned choice is a router's
+(``kmeans_gate``), and ``block_forward`` is a whole block of a model around it:
+layer norm, gate, experts and the residual stream.
 
     offsets, order, rows = kmeans_route(ids)            slots sorted by expert
     xs = kmeans_route_gather(x, rows, offsets)          tokens in that order
@@ -108,3 +109,51 @@ def experts_backward(dy, saved, w1, w2):
     dx = km.kmeans_route_combine(dxs, s.rows, s.offsets)
     return {"x": dx, "w1": dw1, "b1": db1, "w2": dw2, "b2": db2,
             "weights": dweights if s.weights is not None else None}
+
+
+@_on_stream
+def block_forward(x, gate_w, w1, w2, topk, norm_weight=None, norm_bias=None, b1=None, b2=None, gate_bias=None,
+                  scores="softmax", groups=1, topk_groups=None, renormalize=True, scale=1.0, eps=1e-5,
+                  activation="gelu", keep=False):
+    """``(y, saved)``: y (n, d) = x + the gated experts of the normalised tokens.
+
+        h = kmeans_layernorm(x, norm_weight, norm_bias)
+        ids, weights = kmeans_gate(h gate_w^T, topk, ..)     gate_w (n_experts, d)
+        y = experts_forward(h, ids, w1, w2, .., weights, residual=x)
+
+    x (n, d) float16 or bfloat16, the experts' matrices as for experts_forward
+    with d_out = d; ``gate_bias`` (n_experts,) float32 and the options from
+    ``scores`` to ``scale`` are kmeans_gate's.  ``keep``: hold what the gradient
+    needs in ``saved``, else None."""
+    km = _km()
+    h, mean, rstd = km.kmeans_layernorm(x, norm_weight, norm_bias, eps=eps, save_stats=keep)
+    logits, _ = km.kmeans_linear(h, gate_w)
+    ids, weights = km.kmeans_gate(logits, topk, scores=scores, bias=gate_bias, groups=groups, topk_groups=topk_groups,
+                                  renormalize=renormalize, scale=scale)
+    y, saved = experts_forward(h, ids, w1, w2, b1, b2, weights=weights, residual=x, activation=activation, keep=keep)
+    if keep:
+        saved.__dict__.update(x=x, normed=h, mean=mean, rstd=rstd, logits=logits, ids=ids, how=dict(
+            scores=scores, renormalize=renormalize, scale=scale))
+    return y, saved
+
+
+@_on_stream
+def block_backward(dy, saved, gate_w, w1, w2, norm_weight=None):
+    """Gradients of block_forward -> dict with ``x``, ``gate_w``, ``w1``, ``b1``,
+    ``w2``, ``b2``, ``norm_weight`` and ``norm_bias`` (None where the forward
+    pass had none; the norm's by ``norm_weight``)."""
+    km = _km()
+    s = saved
+    dys, dweights = km.kmeans_route_combine_grad(dy, s.ys, s.rows, s.offsets, s.weights)
+    dlogits = km.kmeans_gate_grad(dweights, s.logits, s.ids, **s.how)
+    dh, dgate_w, _ = km.kmeans_linear_grad(dlogits, s.normed, gate_w, need_db=False)
+    dhid, dw2, db2 = km.kmeans_linear_grad(dys, s.h, w2, offsets=s.offsets, need_db=s.has_b2)
+    dxs, dw1, db1 = km.kmeans_linear_grad(dhid, s.xs, w1, pre=s.pre, offsets=s.offsets, activation=s.activation,
+                                          need_db=s.has_b1)
+    # the experts' way back to the tokens takes the gate's along
+    dh = km.kmeans_route_combine(dxs, s.rows, s.offsets, residual=dh)
+    affine = norm_weight is not None
+    dx, dnorm_weight, dnorm_bias = km.kmeans_layernorm_grad(dh, s.x, s.mean, s.rstd, weight=norm_weight, residual=dy,
+                                                            need_dweight=affine, need_dbias=affine)
+    return {"x": dx, "gate_w": dgate_w, "w1": dw1, "b1": db1, "w2": dw2, "b2": db2, "norm_weight": dnorm_weight,
+            "norm_bias": dnorm_bias}
