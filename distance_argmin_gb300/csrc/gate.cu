@@ -387,13 +387,18 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
     const int e0 = lane * PER;
     const bool sums = p.bias || p.groups > 1;
     if (sums) {
-        float b[PER];
-        if (p.bias) load_run<PER>(Logits{reinterpret_cast<const uint8_t *>(p.bias), KMEANS_F32}, e0, p.n_experts,
-                                   p.bias_whole, b);
+        constexpr int RUN = PER < 4 ? PER : 4;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const float c = p.bias ? score_of(sc, f[i]) + b[i] : score_of(sc, f[i]);
-            f[i] = f[i] == -INFINITY ? f[i] : c;
+        for (int i = 0; i < PER; i += RUN) {
+            float b[RUN] = {};
+            if (p.bias)
+                load_run<RUN>(Logits{reinterpret_cast<const uint8_t *>(p.bias), KMEANS_F32}, e0 + i, p.n_experts,
+                              p.bias_whole, b);
+#pragma unroll
+            for (int j = 0; j < RUN; ++j) {
+                const float c = score_of(sc, f[i + j]) + b[j];
+                f[i + j] = f[i + j] == -INFINITY ? f[i + j] : c;
+            }
         }
     }
 #pragma unroll
@@ -550,7 +555,7 @@ __device__ __forceinline__ float share_of(bool sigmoid, float l, bool real) {
 }
 
 template <int PER>
-__global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 16 ? 6 : PER <= 32 ? 4 : 2) gate_kernel(const uint8_t *__restrict__ logits, const GateArgs p,
+__global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 32 ? 6 : 2) gate_kernel(const uint8_t *__restrict__ logits, const GateArgs p,
                                                             int32_t *__restrict__ ids, float *__restrict__ weights) {
     __shared__ Candidates lists[kGateThreads / 32];
     griddep_wait();
@@ -654,7 +659,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const float *__
 }
 
 unsigned gate_blocks(int64_t n) {
-    const int64_t rows = kGateThreads / 32, blocks = (n + rows - 1) / rows, most = (int64_t)device_sm_count() * 16;
+    const int64_t rows = kGateThreads / 32, blocks = (n + rows - 1) / rows, most = (int64_t)device_sm_count() * 64;
     return (unsigned)(blocks < most ? blocks : most);
 }
 

@@ -522,14 +522,14 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
-constexpr int stages_of(int pieces) { return pieces == 4 ? 2 : 4; }
+constexpr int stages_of(int pieces) { return pieces >= 2 ? 2 : 4; }
 
 template <typename T, int LANES, int PIECES, Rows16 ROWS, bool SUMS>
-__global__ void __launch_bounds__(LANES ? kSharedBlock : 512, LANES ? 4 : 1)
+__global__ void __launch_bounds__(LANES ? kSharedBlock : PIECES == 2 ? 256 : 512, LANES ? 4 : PIECES == 2 ? 2 : 1)
     norm_grad_kernel(const GradRows in, int64_t n, int d, int period, T *dx, float *__restrict__ partial) {
     extern __shared__ uint4 ring[];
     constexpr int N = Word<T>::N, GROUPS = LANES ? kSharedBlock / LANES : 1, PAIRS = Word<T>::PAIRS;
-    constexpr int STAGES = PIECES == 4 ? 2 : 4;
+    constexpr int STAGES = PIECES >= 2 ? 2 : 4;
     in.start();
     const int width = LANES ? LANES : (int)blockDim.x;
     const int t = LANES ? (int)threadIdx.x % LANES : (int)threadIdx.x, group = LANES ? (int)threadIdx.x / LANES : 0;
@@ -538,13 +538,27 @@ __global__ void __launch_bounds__(LANES ? kSharedBlock : 512, LANES ? 4 : 1)
     const float scale = 1.f / (float)d;
     const bool add = in.residual.base && dx;
     float2 dw[SUMS ? PIECES : 1][PAIRS] = {}, db[SUMS ? PIECES : 1][PAIRS] = {};
+    // Up to two words a thread keeps its weights and its terms of the row opened:
+    // of the instructions per value a third went into opening them again.
+    constexpr bool HOLD = PIECES <= 2;
     uint4 kw[PIECES];
+    float2 fw[HOLD ? PIECES : 1][PAIRS];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
         const Cut<T, ROWS> cut(i * width + t, at.off, d);
         kw[i] = make_uint4(0, 0, 0, 0);
         if (in.w.base && !cut.none()) kw[i] = load_columns<T, ROWS>(in.w, i * width + t, at.off, cut);
+        if (HOLD) Word<T>::open(kw[i], fw[HOLD ? i : 0]);
     }
+    const auto weigh = [&](int i, float2 (&g)[PAIRS]) {
+        if (!in.w.base) return;
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) g[j] = __fmul2_rn(g[j], fw[HOLD ? i : 0][j]);
+        } else {
+            weight_word<T>(true, kw[i], g);
+        }
+    };
     // this thread's places in a stage: x's words, dy's, the residual's
     const int tensor = PIECES * (int)blockDim.x, stage_words = (add ? 3 : 2) * tensor;
     uint4 *own = ring + threadIdx.x;
@@ -584,21 +598,21 @@ __global__ void __launch_bounds__(LANES ? kSharedBlock : 512, LANES ? 4 : 1)
         next_mu = r + step < n ? in.mean[r + step] : 0.f;
         next_rs = r + step < n ? in.rstd[r + step] : 0.f;
         const uint4 *here = own + stage * stage_words;
-        float2 sum = {0.f, 0.f}, second = {0.f, 0.f};
+        float2 sum = {0.f, 0.f}, second = {0.f, 0.f}, terms[HOLD ? PIECES : 1][2][PAIRS];
         if (GROUPS == 1 || r < n) {
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
                 if (!mine.has(i)) continue;
-                float2 g[PAIRS], h[PAIRS];  // (values that do not exist have dy = 0)
+                float2(&g)[PAIRS] = terms[HOLD ? i : 0][0], (&h)[PAIRS] = terms[HOLD ? i : 0][1];
                 uint4 uy = here[tensor + i * (int)blockDim.x], ux = here[i * (int)blockDim.x];
-                if (ROWS == Rows16::kAlike && !mine.whole(i)) {
+                if (ROWS == Rows16::kAlike && !mine.whole(i)) {  // (values that do not exist have dy = 0)
                     const Cut<T, ROWS> cut(i * width + t, at.off, d);
                     uy = masked<T, ROWS>(uy, cut);
                     ux = masked<T, ROWS>(ux, cut);
                 }
                 terms_of<T>(uy, ux, mu, rs, g, h);
                 if (SUMS) add_columns<PAIRS>(g, h, dw[SUMS ? i : 0], db[SUMS ? i : 0]);
-                weight_word<T>(in.w.base, kw[i], g);
+                weigh(i, g);
                 add_terms<T>(g, h, sum, second);
             }
         }
@@ -610,9 +624,11 @@ __global__ void __launch_bounds__(LANES ? kSharedBlock : 512, LANES ? 4 : 1)
 #pragma unroll
                 for (int i = 0; i < PIECES; ++i) {
                     if (!mine.has(i)) continue;
-                    float2 g[PAIRS], h[PAIRS];
-                    terms_of<T>(here[tensor + i * (int)blockDim.x], here[i * (int)blockDim.x], mu, rs, g, h);
-                    weight_word<T>(in.w.base, kw[i], g);
+                    float2(&g)[PAIRS] = terms[HOLD ? i : 0][0], (&h)[PAIRS] = terms[HOLD ? i : 0][1];
+                    if (!HOLD) {
+                        terms_of<T>(here[tensor + i * (int)blockDim.x], here[i * (int)blockDim.x], mu, rs, g, h);
+                        weigh(i, g);
+                    }
                     finish_word<T>(g, h, rs, mg, mgh, add, add ? here[2 * tensor + i * (int)blockDim.x] : uint4{});
                     if (mine.whole(i))
                         *reinterpret_cast<uint4 *>(out + i * mine.stride()) = Word<T>::close(g);
@@ -632,10 +648,23 @@ __global__ void __launch_bounds__(LANES ? kSharedBlock : 512, LANES ? 4 : 1)
             if (group != k) continue;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
+                const int c0 = (i * width + t) * N - at.off;
+                if (whole_rows(ROWS)) {  // d and c0 are multiples of 4
+                    if (!mine.has(i)) continue;
+#pragma unroll
+                    for (int j = 0; j < PAIRS; j += 2) {
+                        float4 *to = reinterpret_cast<float4 *>(out + c0 + 2 * j);
+                        float4 *too = reinterpret_cast<float4 *>(out + d + c0 + 2 * j);
+                        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f), a = k ? *to : none, b = k ? *too : none;
+                        *to = make_float4(a.x + dw[i][j].x, a.y + dw[i][j].y, a.z + dw[i][j + 1].x, a.w + dw[i][j + 1].y);
+                        *too = make_float4(b.x + db[i][j].x, b.y + db[i][j].y, b.z + db[i][j + 1].x, b.w + db[i][j + 1].y);
+                    }
+                    continue;
+                }
                 const Cut<T, ROWS> cut(i * width + t, at.off, d);
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const int c = (i * width + t) * N + j - at.off;
+                    const int c = c0 + j;
                     if (!cut.has(j)) continue;
                     const float2 w2 = dw[i][j / 2], b2 = db[i][j / 2];
                     out[c] = (k ? out[c] : 0.f) + (j & 1 ? w2.y : w2.x);
@@ -862,8 +891,11 @@ cudaError_t norm_grad_typed(const NormShape &sh, const GradRows &in, int period,
             return run(words == 8 ? launch_grad<T, 8, 1, FULL, SUMS> : launch_grad<T, 8, 1, ROWS, SUMS>, kSharedBlock);
         if (words <= 32)
             return run(words == 32 ? launch_grad<T, 32, 1, FULL, SUMS> : launch_grad<T, 32, 1, ROWS, SUMS>, kSharedBlock);
-        if (words <= 128)
-            return run(words == 128 ? launch_grad<T, 32, 4, FULL, SUMS> : launch_grad<T, 32, 4, ROWS, SUMS>, kSharedBlock);
+        if (words <= 64)
+            return run(words == 64 ? launch_grad<T, 32, 2, FULL, SUMS> : launch_grad<T, 32, 2, ROWS, SUMS>, kSharedBlock);
+        if (words <= 512)
+            return run(words % 64 == 0 ? launch_grad<T, 0, 2, FULL, SUMS> : launch_grad<T, 0, 2, ROWS, SUMS>,
+                       threads_of(words, 2));
         return run(words % 128 == 0 ? launch_grad<T, 0, 4, FULL, SUMS> : launch_grad<T, 0, 4, ROWS, SUMS>,
                    threads_of(words, 4));
     };
