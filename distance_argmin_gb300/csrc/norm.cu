@@ -291,103 +291,161 @@ __device__ __forceinline__ void normalise(float2 (&v)[Word<T>::PAIRS], float off
 // Rows of LANES lanes share blocks of 128 threads; longer rows have a block.
 constexpr int kSharedBlock = 128;
 
-// PIECES words per thread: four where a row has them, since what goes with a row
-// (addresses, the sums' way through the block) is paid per thread; BATCH rows of a
-// group at a time, so that short rows too have enough on its way.
-template <typename T, int LANES, int PIECES, int BATCH, Rows16 ROWS>
-__global__ void __launch_bounds__(LANES ? kSharedBlock : 512, !whole_rows(ROWS) ? (LANES ? 4 : 1) : LANES ? 6 : 2)
+// Copies into shared memory that the thread does not wait for.
+__device__ __forceinline__ void copy16(uint4 *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// Rows on their way or worked on at a time.  (Four words a thread fill shared memory
+// with two.)
+__host__ __device__ constexpr int stages_of(int pieces) { return pieces == 4 ? 2 : 4; }
+
+// What a thread has of a row: PIECES words of up to three tensors in shared memory,
+// in places of its own, so that nobody waits for anybody else's copies.
+template <typename T, int PIECES, Rows16 ROWS>
+struct Fetch {
+    const Mine<T, PIECES, ROWS> &mine;
+    int off, d;
+    int64_t start;  // of the thread's first word from the row's first value on, in bytes
+    __device__ __forceinline__ void operator()(const Rows &m, int64_t r, uint4 *to) const {
+        const uint8_t *p = m.base + r * m.pitch + start;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            if (!mine.has(i)) continue;
+            uint4 *at = to + i * (int)blockDim.x;
+            if (mine.whole(i) || (ROWS == Rows16::kAlike && in_tensor(p + i * mine.stride(), m.in)))
+                copy16(at, p + i * mine.stride());
+            else
+                *at = load_row<T, ROWS>(m, r, mine.c0 + i * mine.width, off, Cut<T, ROWS>(mine.c0 + i * mine.width, off, d));
+        }
+    }
+    __device__ __forceinline__ uint4 read(const uint4 *from, int i) const {
+        const uint4 u = from[i * (int)blockDim.x];
+        if (ROWS != Rows16::kAlike || mine.whole(i)) return u;
+        return masked<T, ROWS>(u, Cut<T, ROWS>(mine.c0 + i * mine.width, off, d));
+    }
+};
+
+// A vector's columns of a thread: opened for good up to sixteen values a thread,
+// which takes a third off the instructions per value, and as they are above.
+template <typename T, int PIECES, Rows16 ROWS>
+struct Columns {
+    static constexpr bool HOLD = PIECES * Word<T>::N <= 16;
+    static constexpr int PAIRS = Word<T>::PAIRS;
+    uint4 raw[HOLD ? 1 : PIECES];
+    float2 open[HOLD ? PIECES : 1][PAIRS];
+    bool there;
+    __device__ __forceinline__ Columns(const Rows &v, const Mine<T, PIECES, ROWS> &mine, int off, int d) : there(v.base) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int c = mine.c0 + i * mine.width;
+            const Cut<T, ROWS> cut(c, off, d);
+            const uint4 u = there && !cut.none() ? load_columns<T, ROWS>(v, c, off, cut) : make_uint4(0, 0, 0, 0);
+            if constexpr (HOLD)
+                Word<T>::open(u, open[i]);
+            else
+                raw[i] = u;
+        }
+    }
+    __device__ __forceinline__ void get(int i, float2 (&f)[PAIRS]) const {
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) f[j] = open[i][j];
+        } else {
+            Word<T>::open(raw[i], f);
+        }
+    }
+    __device__ __forceinline__ void multiply(int i, float2 (&v)[PAIRS]) const {
+        if (!there) return;
+        float2 f[PAIRS];
+        get(i, f);
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) v[j] = __fmul2_rn(v[j], f[j]);
+    }
+    __device__ __forceinline__ void add(int i, float2 (&v)[PAIRS]) const {
+        if (!there) return;
+        float2 f[PAIRS];
+        get(i, f);
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) v[j] = __fadd2_rn(v[j], f[j]);
+    }
+};
+
+template <typename T, int LANES, int PIECES, Rows16 ROWS>
+__global__ void __launch_bounds__(LANES ? kSharedBlock : PIECES == 2 ? 256 : 512, LANES ? 5 : PIECES == 2 ? 2 : 1)
     norm_kernel(const Rows x, const Rows w, const Rows b, float eps, int64_t n, int d, int period, T *y, float *mean,
                 float *rstd) {
+    extern __shared__ uint4 ring[];
     constexpr int GROUPS = LANES ? kSharedBlock / LANES : 1, PAIRS = Word<T>::PAIRS, N = Word<T>::N;
-    constexpr bool ALONE = GROUPS * BATCH == 1;  // the loop's row is the only one
+    constexpr int STAGES = stages_of(PIECES);
     griddep_wait();
     const int width = LANES ? LANES : (int)blockDim.x;
     const int t = LANES ? (int)threadIdx.x % LANES : (int)threadIdx.x, group = LANES ? (int)threadIdx.x / LANES : 0;
     const Place at = place_of<T, ROWS>(x, period);
     const Mine<T, PIECES, ROWS> mine(t, width, at.off, d);
     const float scale = 1.f / (float)d;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    // vectors off 16 bytes cost eight loads a word: once
-    constexpr bool KEEP = !whole_rows(ROWS);
-    uint4 kw[KEEP ? PIECES : 1], kb[KEEP ? PIECES : 1];
-    if constexpr (KEEP) {
+    const Fetch<T, PIECES, ROWS> fetch{mine, at.off, d, ((int64_t)t * N - at.off) * (int)sizeof(T)};
+    const int stage_words = PIECES * (int)blockDim.x;
+    uint4 *own = ring + threadIdx.x;
+    const int64_t step = at.step * GROUPS, first = at.first + at.step * group;
+    const auto issue = [&](int64_t r, int stage) {
+        if (r < n) fetch(x, r, own + stage * stage_words);
+        copy_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k) issue(first + k * step, k);
+    const Columns<T, PIECES, ROWS> weight(w, mine, at.off, d), bias(b, mine, at.off, d);
+    int turn = 0, stage = 0;
+    for (int64_t q = at.first; q < n; q += step) {
+        const int64_t r = q + at.step * group;
+        const bool here = GROUPS == 1 || r < n;
+        // (into the stage that the last row has left)
+        issue(r + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+        copy_wait<STAGES - 1>();
+        const uint4 *from = own + stage * stage_words;
+        float2 v[PIECES][PAIRS], sum = {0.f, 0.f}, second = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const Cut<T, ROWS> cut(i * width + t, at.off, d);
-            kw[i] = w.base && !cut.none() ? load_columns<T, ROWS>(w, i * width + t, at.off, cut) : zero;
-            kb[i] = b.base && !cut.none() ? load_columns<T, ROWS>(b, i * width + t, at.off, cut) : zero;
-        }
-    }
-    const int64_t start = ((int64_t)t * N - at.off) * (int)sizeof(T);
-    int turn = 0;
-    for (int64_t q = at.first; q < n; q += at.step * (GROUPS * BATCH)) {
-        float2 v[BATCH][PIECES][PAIRS];
-        float mu[BATCH], off[BATCH], rs[BATCH];
+            const uint4 u = here && mine.has(i) ? fetch.read(from, i) : make_uint4(0, 0, 0, 0);
+            Word<T>::open(u, v[i]);
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const int64_t r = q + at.step * (group + GROUPS * k);
-            const uint8_t *p = x.base + r * x.pitch + start;
-            uint4 raw[PIECES];
+            for (int j = 0; j < PAIRS; ++j) sum = __fadd2_rn(sum, v[i][j]);
+        }
+        const float mu = group_sum<LANES>(make_float2(sum.x + sum.y, 0.f), turn).x * scale;
+        sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+            if (mine.has(i)) spread<T, ROWS>(v[i], mine.whole(i), i * width + t, at.off, d, mu, sum, second);
+        sum = group_sum<LANES>(make_float2(sum.x + sum.y, second.x + second.y), turn);
+        const float off = sum.x * scale, rs = rsqrtf(variance_of(sum.y * scale, off) + eps);
+        if (here) {
+            uint8_t *out = reinterpret_cast<uint8_t *>(y + r * d) + fetch.start;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
-                raw[i] = zero;
-                if ((ALONE || r < n) && mine.has(i)) {
-                    if (mine.whole(i))
-                        raw[i] = *reinterpret_cast<const uint4 *>(p + i * mine.stride());
-                    else
-                        raw[i] = load_row<T, ROWS>(x, r, i * width + t, at.off, Cut<T, ROWS>(i * width + t, at.off, d));
-                }
-            }
+                if (!mine.has(i)) continue;
 #pragma unroll
-            for (int i = 0; i < PIECES; ++i) Word<T>::open(raw[i], v[k][i]);
-        }
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            float2 sum = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < PIECES; ++i)
-#pragma unroll
-                for (int j = 0; j < PAIRS; ++j) sum = __fadd2_rn(sum, v[k][i][j]);
-            mu[k] = group_sum<LANES>(make_float2(sum.x + sum.y, 0.f), turn).x * scale;
-        }
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            float2 sum = {0.f, 0.f}, second = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < PIECES; ++i)
-                if (mine.has(i))
-                    spread<T, ROWS>(v[k][i], mine.whole(i), i * width + t, at.off, d, mu[k], sum, second);
-            sum = group_sum<LANES>(make_float2(sum.x + sum.y, second.x + second.y), turn);
-            off[k] = sum.x * scale;
-            rs[k] = rsqrtf(variance_of(sum.y * scale, off[k]) + eps);
-        }
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            if (!mine.has(i)) continue;
-            const int c = i * width + t;
-            const uint4 uw = KEEP ? kw[KEEP ? i : 0] : w.base ? reinterpret_cast<const uint4 *>(w.base)[c] : zero;
-            const uint4 ub = KEEP ? kb[KEEP ? i : 0] : b.base ? reinterpret_cast<const uint4 *>(b.base)[c] : zero;
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int64_t r = q + at.step * (group + GROUPS * k);
-                if (!ALONE && r >= n) continue;
-                normalise<T>(v[k][i], off[k], rs[k], w.base, uw, b.base, ub);
+                for (int j = 0; j < PAIRS; ++j) v[i][j] = __fmul2_rn(__fadd2_rn(v[i][j], both(-off)), both(rs));
+                weight.multiply(i, v[i]);
+                bias.add(i, v[i]);
                 if (mine.whole(i))
-                    *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(y + r * d) + start + i * mine.stride()) =
-                        Word<T>::close(v[k][i]);
+                    *reinterpret_cast<uint4 *>(out + i * mine.stride()) = Word<T>::close(v[i]);
                 else
-                    store_row<T, ROWS>(y + r * d, v[k][i], c, at.off, Cut<T, ROWS>(c, at.off, d));
+                    store_row<T, ROWS>(y + r * d, v[i], i * width + t, at.off, Cut<T, ROWS>(i * width + t, at.off, d));
+            }
+            if (t == 0) {
+                if (mean) mean[r] = mu + off;
+                if (rstd) rstd[r] = rs;
             }
         }
-#pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            const int64_t r = q + at.step * (group + GROUPS * k);
-            if (t == 0 && (ALONE || r < n)) {
-                if (mean) mean[r] = mu[k] + off[k];
-                if (rstd) rstd[r] = rs[k];
-            }
-        }
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
     }
+    copy_wait<0>();
 }
 
 // One row after the other, read again for every pass.
@@ -512,24 +570,12 @@ __device__ __forceinline__ void finish_word(float2 (&g)[Word<T>::PAIRS], const f
 // that nobody waits for anybody else's: in registers there is room for one row
 // ahead, which kept 55% of the copy rate (16384 x 4096 bfloat16 with the residual's
 // gradient: 126 us).
-__device__ __forceinline__ void copy16(uint4 *to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
-
-constexpr int stages_of(int pieces) { return pieces >= 2 ? 2 : 4; }
-
 template <typename T, int LANES, int PIECES, Rows16 ROWS, bool SUMS>
 __global__ void __launch_bounds__(LANES ? kSharedBlock : PIECES == 2 ? 256 : 512, LANES ? 4 : PIECES == 2 ? 2 : 1)
     norm_grad_kernel(const GradRows in, int64_t n, int d, int period, T *dx, float *__restrict__ partial) {
     extern __shared__ uint4 ring[];
     constexpr int N = Word<T>::N, GROUPS = LANES ? kSharedBlock / LANES : 1, PAIRS = Word<T>::PAIRS;
-    constexpr int STAGES = PIECES >= 2 ? 2 : 4;
+    constexpr int STAGES = stages_of(PIECES);
     in.start();
     const int width = LANES ? LANES : (int)blockDim.x;
     const int t = LANES ? (int)threadIdx.x % LANES : (int)threadIdx.x, group = LANES ? (int)threadIdx.x / LANES : 0;
@@ -538,43 +584,13 @@ __global__ void __launch_bounds__(LANES ? kSharedBlock : PIECES == 2 ? 256 : 512
     const float scale = 1.f / (float)d;
     const bool add = in.residual.base && dx;
     float2 dw[SUMS ? PIECES : 1][PAIRS] = {}, db[SUMS ? PIECES : 1][PAIRS] = {};
-    // Up to two words a thread keeps its weights and its terms of the row opened:
-    // of the instructions per value a third went into opening them again.
-    constexpr bool HOLD = PIECES <= 2;
-    uint4 kw[PIECES];
-    float2 fw[HOLD ? PIECES : 1][PAIRS];
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-        const Cut<T, ROWS> cut(i * width + t, at.off, d);
-        kw[i] = make_uint4(0, 0, 0, 0);
-        if (in.w.base && !cut.none()) kw[i] = load_columns<T, ROWS>(in.w, i * width + t, at.off, cut);
-        if (HOLD) Word<T>::open(kw[i], fw[HOLD ? i : 0]);
-    }
-    const auto weigh = [&](int i, float2 (&g)[PAIRS]) {
-        if (!in.w.base) return;
-        if constexpr (HOLD) {
-#pragma unroll
-            for (int j = 0; j < PAIRS; ++j) g[j] = __fmul2_rn(g[j], fw[HOLD ? i : 0][j]);
-        } else {
-            weight_word<T>(true, kw[i], g);
-        }
-    };
+    // (up to sixteen values a thread keeps its terms of the row, too)
+    constexpr bool HOLD = Columns<T, PIECES, ROWS>::HOLD;
+    const Columns<T, PIECES, ROWS> weight(in.w, mine, at.off, d);
     // this thread's places in a stage: x's words, dy's, the residual's
     const int tensor = PIECES * (int)blockDim.x, stage_words = (add ? 3 : 2) * tensor;
     uint4 *own = ring + threadIdx.x;
-    const int64_t start = ((int64_t)t * N - at.off) * (int)sizeof(T);
-    const auto fetch = [&](const Rows &m, int64_t r, uint4 *to) {
-        const uint8_t *p = m.base + r * m.pitch + start;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            if (!mine.has(i)) continue;
-            if (mine.whole(i) || (ROWS == Rows16::kAlike && in_tensor(p + i * mine.stride(), m.in)))
-                copy16(to + i * (int)blockDim.x, p + i * mine.stride());
-            else
-                to[i * (int)blockDim.x] =
-                    load_row<T, ROWS>(m, r, i * width + t, at.off, Cut<T, ROWS>(i * width + t, at.off, d));
-        }
-    };
+    const Fetch<T, PIECES, ROWS> fetch{mine, at.off, d, ((int64_t)t * N - at.off) * (int)sizeof(T)};
     const auto issue = [&](int64_t r, int stage) {
         if (r < n) {
             uint4 *to = own + stage * stage_words;
@@ -604,22 +620,17 @@ __global__ void __launch_bounds__(LANES ? kSharedBlock : PIECES == 2 ? 256 : 512
             for (int i = 0; i < PIECES; ++i) {
                 if (!mine.has(i)) continue;
                 float2(&g)[PAIRS] = terms[HOLD ? i : 0][0], (&h)[PAIRS] = terms[HOLD ? i : 0][1];
-                uint4 uy = here[tensor + i * (int)blockDim.x], ux = here[i * (int)blockDim.x];
-                if (ROWS == Rows16::kAlike && !mine.whole(i)) {  // (values that do not exist have dy = 0)
-                    const Cut<T, ROWS> cut(i * width + t, at.off, d);
-                    uy = masked<T, ROWS>(uy, cut);
-                    ux = masked<T, ROWS>(ux, cut);
-                }
+                const uint4 uy = fetch.read(here + tensor, i), ux = fetch.read(here, i);  // (what is not there: dy = 0)
                 terms_of<T>(uy, ux, mu, rs, g, h);
                 if (SUMS) add_columns<PAIRS>(g, h, dw[SUMS ? i : 0], db[SUMS ? i : 0]);
-                weigh(i, g);
+                weight.multiply(i, g);
                 add_terms<T>(g, h, sum, second);
             }
         }
         if (dx) {
             sum = group_sum<LANES>(make_float2(sum.x + sum.y, second.x + second.y), turn);
             const float mg = sum.x * scale, mgh = sum.y * scale;
-            uint8_t *out = reinterpret_cast<uint8_t *>(dx + r * d) + start;
+            uint8_t *out = reinterpret_cast<uint8_t *>(dx + r * d) + fetch.start;
             if (GROUPS == 1 || r < n) {
 #pragma unroll
                 for (int i = 0; i < PIECES; ++i) {
@@ -627,7 +638,7 @@ __global__ void __launch_bounds__(LANES ? kSharedBlock : PIECES == 2 ? 256 : 512
                     float2(&g)[PAIRS] = terms[HOLD ? i : 0][0], (&h)[PAIRS] = terms[HOLD ? i : 0][1];
                     if (!HOLD) {
                         terms_of<T>(here[tensor + i * (int)blockDim.x], here[i * (int)blockDim.x], mu, rs, g, h);
-                        weigh(i, g);
+                        weight.multiply(i, g);
                     }
                     finish_word<T>(g, h, rs, mg, mgh, add, add ? here[2 * tensor + i * (int)blockDim.x] : uint4{});
                     if (mine.whole(i))
@@ -819,50 +830,61 @@ unsigned blocks_of(int64_t wanted, int64_t most, int period) {
 // A thread block for rows of so many words.
 int threads_of(int64_t words, int pieces) { return (int)align_up((words + pieces - 1) / pieces, 32); }
 
-template <typename T, Rows16 ROWS>
-cudaError_t norm_typed(const NormShape &sh, const Rows &x, const Rows &w, const Rows &b, float eps, int period, T *y,
-                       float *mean, float *rstd, cudaStream_t s) {
-    constexpr int N = Word<T>::N;
-    const int64_t words = (sh.d + N - 1) / N + (ROWS == Rows16::kAlike ? 1 : 0);
-    const int d = (int)sh.d;
-    // as many blocks as run at once
-    const auto run = [&](auto kernel, int threads, int64_t rows) {
-        const int64_t most = kSMs * std::max(1, 1024 / threads);
-        return launch_kernel(true, kernel, dim3(blocks_of((sh.n + rows - 1) / rows, most, period)), dim3((unsigned)threads),
-                             0, s, x, w, b, eps, sh.n, d, period, y, mean, rstd);
-    };
-    constexpr Rows16 FULL = ROWS == Rows16::kWhole ? Rows16::kExact : ROWS;
-    if (words <= 8)
-        return run(words == 8 ? norm_kernel<T, 8, 1, 4, FULL> : norm_kernel<T, 8, 1, 4, ROWS>, kSharedBlock, kSharedBlock / 8);
-    if (words <= 32)
-        return run(words == 32 ? norm_kernel<T, 32, 1, 4, FULL> : norm_kernel<T, 32, 1, 4, ROWS>, kSharedBlock,
-                   kSharedBlock / 32);
-    if (words <= 64)
-        return run(words == 64 ? norm_kernel<T, 32, 2, 2, FULL> : norm_kernel<T, 32, 2, 2, ROWS>, kSharedBlock,
-                   kSharedBlock / 32);
-    if (words <= 128)
-        return run(words == 128 ? norm_kernel<T, 32, 4, 1, FULL> : norm_kernel<T, 32, 4, 1, ROWS>, kSharedBlock,
-                   kSharedBlock / 32);
-    if (words <= 2048)
-        return run(words % 128 == 0 ? norm_kernel<T, 0, 4, 1, FULL> : norm_kernel<T, 0, 4, 1, ROWS>, threads_of(words, 4), 1);
-    return run(norm_wide_kernel<T, ROWS>, kWideThreads, 1);
-}
+constexpr int kMostShared = 220 * 1024;
 
-// The gradient's rows in registers' reach; `count`: its blocks.
-template <typename T, int LANES, int PIECES, Rows16 ROWS, bool SUMS>
-cudaError_t launch_grad(const GradRows &in, int64_t n, int d, int period, T *dx, float *partial, int threads,
-                        int64_t &count, cudaStream_t s) {
-    constexpr int kMostShared = 220 * 1024;
-    const auto kernel = norm_grad_kernel<T, LANES, PIECES, ROWS, SUMS>;
+// Shared memory of so much may be asked for; once per kernel and device.
+template <auto KERNEL>
+cudaError_t allow_shared() {
     static std::once_flag once[kMaxDevices];
     static std::atomic<int> err[kMaxDevices];
     int dev = 0;
     cudaGetDevice(&dev);
     const int slot = dev >= 0 && dev < kMaxDevices ? dev : 0;
     once_per_device(once, [&] {
-        err[slot].store((int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared));
+        err[slot].store((int)cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared));
     });
-    if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
+    return (cudaError_t)err[slot].load();
+}
+
+template <typename T, int LANES, int PIECES, Rows16 ROWS>
+cudaError_t launch_norm(const Rows &x, const Rows &w, const Rows &b, float eps, int64_t n, int d, int period, T *y,
+                        float *mean, float *rstd, int threads, cudaStream_t s) {
+    constexpr auto kernel = norm_kernel<T, LANES, PIECES, ROWS>;
+    const cudaError_t e = allow_shared<kernel>();
+    if (e != cudaSuccess) return e;
+    const int64_t rows = LANES ? kSharedBlock / LANES : 1;
+    const int shared = stages_of(PIECES) * PIECES * threads * 16;
+    // as many blocks as run at once: by registers (see the launch bounds) and shared memory
+    const int resident = std::min(std::max(1, (LANES ? 640 : 512) / threads), kMostShared / shared);
+    return launch_kernel(true, kernel, dim3(blocks_of((n + rows - 1) / rows, align_up(kSMs * resident, 8), period)),
+                         dim3((unsigned)threads), (size_t)shared, s, x, w, b, eps, n, d, period, y, mean, rstd);
+}
+
+template <typename T, Rows16 ROWS>
+cudaError_t norm_typed(const NormShape &sh, const Rows &x, const Rows &w, const Rows &b, float eps, int period, T *y,
+                       float *mean, float *rstd, cudaStream_t s) {
+    constexpr int N = Word<T>::N;
+    const int64_t words = (sh.d + N - 1) / N + (ROWS == Rows16::kAlike ? 1 : 0);
+    const int d = (int)sh.d;
+    constexpr Rows16 FULL = ROWS == Rows16::kWhole ? Rows16::kExact : ROWS;
+    const auto run = [&](auto launch, int threads) { return launch(x, w, b, eps, sh.n, d, period, y, mean, rstd, threads, s); };
+    if (words <= 8) return run(words == 8 ? launch_norm<T, 8, 1, FULL> : launch_norm<T, 8, 1, ROWS>, kSharedBlock);
+    if (words <= 32) return run(words == 32 ? launch_norm<T, 32, 1, FULL> : launch_norm<T, 32, 1, ROWS>, kSharedBlock);
+    if (words <= 64) return run(words == 64 ? launch_norm<T, 32, 2, FULL> : launch_norm<T, 32, 2, ROWS>, kSharedBlock);
+    if (words <= 128) return run(words == 128 ? launch_norm<T, 32, 4, FULL> : launch_norm<T, 32, 4, ROWS>, kSharedBlock);
+    if (words <= 2048)
+        return run(words % 128 == 0 ? launch_norm<T, 0, 4, FULL> : launch_norm<T, 0, 4, ROWS>, threads_of(words, 4));
+    return launch_kernel(true, norm_wide_kernel<T, ROWS>, dim3(blocks_of(sh.n, kSMs * 2, period)), dim3(kWideThreads), 0, s, x,
+                         w, b, eps, sh.n, d, period, y, mean, rstd);
+}
+
+// The gradient's rows in registers' reach; `count`: its blocks.
+template <typename T, int LANES, int PIECES, Rows16 ROWS, bool SUMS>
+cudaError_t launch_grad(const GradRows &in, int64_t n, int d, int period, T *dx, float *partial, int threads,
+                        int64_t &count, cudaStream_t s) {
+    constexpr auto kernel = norm_grad_kernel<T, LANES, PIECES, ROWS, SUMS>;
+    const cudaError_t e = allow_shared<kernel>();
+    if (e != cudaSuccess) return e;
     const int64_t rows = LANES ? kSharedBlock / LANES : 1;
     const int shared = stages_of(PIECES) * (in.residual.base && dx ? 3 : 2) * PIECES * threads * 16;
     // as many blocks as run at once: by registers (see its launch bounds) and shared memory
@@ -891,11 +913,15 @@ cudaError_t norm_grad_typed(const NormShape &sh, const GradRows &in, int period,
             return run(words == 8 ? launch_grad<T, 8, 1, FULL, SUMS> : launch_grad<T, 8, 1, ROWS, SUMS>, kSharedBlock);
         if (words <= 32)
             return run(words == 32 ? launch_grad<T, 32, 1, FULL, SUMS> : launch_grad<T, 32, 1, ROWS, SUMS>, kSharedBlock);
-        if (words <= 64)
-            return run(words == 64 ? launch_grad<T, 32, 2, FULL, SUMS> : launch_grad<T, 32, 2, ROWS, SUMS>, kSharedBlock);
-        if (words <= 512)
-            return run(words % 64 == 0 ? launch_grad<T, 0, 2, FULL, SUMS> : launch_grad<T, 0, 2, ROWS, SUMS>,
-                       threads_of(words, 2));
+        // sixteen values a thread (16-bit types: 16384 x 4096 73 us so, 91 with 32;
+        // float32 x 2048: 130 so, 167 with eight)
+        constexpr int FEW = 16 / N;
+        if (words <= 32 * FEW)
+            return run(words == 32 * FEW ? launch_grad<T, 32, FEW, FULL, SUMS> : launch_grad<T, 32, FEW, ROWS, SUMS>,
+                       kSharedBlock);
+        if (words <= 256 * FEW)
+            return run(words % (32 * FEW) == 0 ? launch_grad<T, 0, FEW, FULL, SUMS> : launch_grad<T, 0, FEW, ROWS, SUMS>,
+                       threads_of(words, FEW));
         return run(words % 128 == 0 ? launch_grad<T, 0, 4, FULL, SUMS> : launch_grad<T, 0, 4, ROWS, SUMS>,
                    threads_of(words, 4));
     };

@@ -419,7 +419,7 @@ int rows_per_unit(int64_t rows, int64_t num_p) {
 
 template <Product MODE>
 cudaError_t product(const LinearShape &sh, const Product16 &g, LinearTcParams &p, int64_t rows, cudaStream_t s) {
-    p.entropy.tile = rows_per_unit(rows, p.num_p);
+    p.entropy.tile = rows_per_unit(rows, p.num_p * (MODE == Product::kRowsSum ? p.entropy.splits : 1));
     return p.entropy.tile <= 128 ? launch_typed<MODE, 128>(sh, g, p, s) : launch_typed<MODE, 256>(sh, g, p, s);
 }
 
