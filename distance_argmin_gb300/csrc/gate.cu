@@ -52,14 +52,6 @@ struct Logits {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ void store_logit(T *p, float v) {
-    if constexpr (sizeof(T) == 4)
-        *p = v;
-    else
-        *p = narrow<T>(v);
-}
-
 // Order-preserving keys: 0 for what cannot be chosen, NaN as infinity, the two
 // zeros equal.
 __device__ __forceinline__ uint32_t choice_key(float v) {
@@ -171,6 +163,42 @@ __device__ __forceinline__ void load_run(const Logits &row, int e0, int n_expert
     } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) f[i] = e0 + i < n_experts ? row[e0 + i] : -INFINITY;
+    }
+}
+
+template <int PER, typename T>
+__device__ __forceinline__ void store_whole(T *p, const float (&f)[PER]) {
+    constexpr int BYTES = PER * (int)sizeof(T), WORD = BYTES >= 16 ? 16 : BYTES, N = WORD / (int)sizeof(T);
+    using W = std::conditional_t<WORD == 16, uint4, std::conditional_t<WORD == 8, uint2, std::conditional_t<WORD == 4, uint32_t, uint16_t>>>;
+#pragma unroll
+    for (int i = 0; i < PER; i += N) {
+        T v[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if constexpr (sizeof(T) == 4)
+                v[j] = f[i + j];
+            else
+                v[j] = narrow<T>(f[i + j]);
+        }
+        W w;
+        memcpy(&w, v, sizeof w);
+        reinterpret_cast<W *>(p)[i / N] = w;
+    }
+}
+
+template <int PER, typename T>
+__device__ __forceinline__ void store_run(T *row, int e0, int n_experts, bool whole, const float (&f)[PER]) {
+    if (whole && e0 + PER <= n_experts) {
+        store_whole<PER>(row + e0, f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (e0 + i < n_experts) {
+                if constexpr (sizeof(T) == 4)
+                    row[e0 + i] = f[i];
+                else
+                    row[e0 + i] = narrow<T>(f[i]);
+            }
     }
 }
 
@@ -554,6 +582,24 @@ __device__ __forceinline__ float share_of(bool sigmoid, float l, bool real) {
     return real ? u / sum : 0.f;
 }
 
+// A softmax's parameters from the lanes' logits.
+template <int PER>
+__device__ __forceinline__ void softmax_scores(const float (&f)[PER], Scores<float> &sc) {
+    float top = f[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) top = fmaxf(top, f[i]);
+    top = warp_fmax(top);
+    sc.top = top == -INFINITY ? 0.f : top;  // no open expert: scores of 0
+    constexpr int SUMS = PER < 4 ? PER : 4;  // (see gate_args)
+    float sum[SUMS] = {};
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum[i % SUMS] += __expf(f[i] - sc.top);
+#pragma unroll
+    for (int i = 1; i < SUMS; ++i) sum[0] += sum[i];
+    const float all = warp_sum(sum[0]);
+    sc.inverse = all == 0.f ? 0.f : 1.f / all;
+}
+
 template <int PER>
 __global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 32 ? 6 : 2) gate_kernel(const uint8_t *__restrict__ logits, const GateArgs p,
                                                             int32_t *__restrict__ ids, float *__restrict__ weights) {
@@ -569,21 +615,7 @@ __global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 32 ? 6 : 2
         float f[PER];
         load_run<PER>(row, lane * PER, p.n_experts, p.whole, f);
         Scores<float> sc{p.sigmoid, 0.f, 0.f};
-        if (need_sum) {
-            float top = f[0];
-#pragma unroll
-            for (int i = 1; i < PER; ++i) top = fmaxf(top, f[i]);
-            top = warp_fmax(top);
-            sc.top = top == -INFINITY ? 0.f : top;  // no open expert: scores of 0
-            constexpr int SUMS = PER < 4 ? PER : 4;  // (see gate_args)
-            float sum[SUMS] = {};
-#pragma unroll
-            for (int i = 0; i < PER; ++i) sum[i % SUMS] += __expf(f[i] - sc.top);
-#pragma unroll
-            for (int i = 1; i < SUMS; ++i) sum[0] += sum[i];
-            const float all = warp_sum(sum[0]);
-            sc.inverse = all == 0.f ? 0.f : 1.f / all;
-        }
+        if (need_sum) softmax_scores(f, sc);
         const int e = choose<PER>(p, row, lane, sc, f, list);
         const bool real = lane < p.topk && e >= 0;
         const float l = real ? row[e] : 0.f;
@@ -601,30 +633,36 @@ __global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 32 ? 6 : 2
 //   softmax, renorm.  v_j (g_j - sum_m g_m v_m)
 //   sigmoid           g_j s_j (1 - s_j)
 //   sigmoid, renorm.  v_j (1 - s_j) (g_j - sum_m g_m v_m)
-// It goes to a row in shared memory, and the whole row leaves from there.  An
-// expert that is named twice gets the sum, in the choices' order.
-template <typename T>
+// It goes to a row in shared memory, experts apart, from which the lanes take their
+// PER neighbouring ones with them (as in the choice; 16384 x 128 bfloat16: 14 us
+// with an expert at a time, read three times, MEASURED so).  An expert that is
+// named twice gets the sum, in the choices' order.
+template <int PER, typename T>
 __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const float *__restrict__ dweights,
                                                                  const uint8_t *__restrict__ logits, const GateArgs p,
-                                                                 const int32_t *__restrict__ ids,
+                                                                 const int32_t *__restrict__ ids, bool out_whole,
                                                                  T *__restrict__ dlogits) {
-    extern __shared__ float gate_smem[];
+    extern __shared__ float4 gate_smem[];
     griddep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float *own = gate_smem + warp * p.n_experts;
-    for (int e = lane; e < p.n_experts; e += 32) own[e] = 0.f;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * PER;
+    float *own = reinterpret_cast<float *>(gate_smem) + warp * (32 * PER);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) own[e0 + i] = 0.f;
     const bool dense = !p.sigmoid && !p.renormalize;
     const int64_t step = (int64_t)gridDim.x * (kGateThreads / 32);
     for (int64_t r = (int64_t)blockIdx.x * (kGateThreads / 32) + warp; r < p.n; r += step) {
         const Logits row{logits + r * p.pitch, p.dtype};
-        T *out = dlogits + r * p.n_experts;
-        Scores<float> sc{p.sigmoid, 0.f, 0.f};
-        if (dense) sc = row_scores<float>(p, row, lane);
         int e = lane < p.topk ? ids[r * p.topk + lane] : -1;
         if (e >= p.n_experts) e = -1;
         const float l = e >= 0 ? row[e] : -INFINITY;
         const bool real = l != -INFINITY;  // an expert that is closed to the token has no weight
         const float g = real ? p.scale * dweights[r * p.topk + lane] : 0.f;
+        Scores<float> sc{p.sigmoid, 0.f, 0.f};
+        float f[PER];
+        if (dense) {
+            load_run<PER>(row, e0, p.n_experts, p.whole, f);
+            softmax_scores(f, sc);
+        }
         float back = g, all = 0.f;
         if (p.renormalize) {
             const float v = share_of(p.sigmoid, l, real);
@@ -648,11 +686,13 @@ __global__ void __launch_bounds__(kGateThreads) gate_grad_kernel(const float *__
         __syncwarp();
         if (first) own[e] = back;
         __syncwarp();
-        for (int i = lane; i < p.n_experts; i += 32) {
-            float v = own[i];
-            if (dense) v = score_of(sc, row[i]) * (v - all);
-            store_logit(out + i, v);
+        float v[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            v[i] = own[e0 + i];
+            if (dense) v[i] = score_of(sc, f[i]) * (v[i] - all);
         }
+        store_run<PER>(dlogits + r * p.n_experts, e0, p.n_experts, out_whole, v);
         __syncwarp();
         if (first) own[e] = 0.f;
     }
@@ -686,22 +726,39 @@ GateArgs gate_args(const GateShape &g, int dtype, const void *logits, int64_t ld
             on16(logits, pitch), on16(bias, 0), (lanes & (lanes - 1)) == 0 ? lanes : 0, gap};
 }
 
+template <int PER, typename T>
+cudaError_t launch_grad(const GateShape &g, int dtype, const float *dweights, const void *logits, int64_t ldl,
+                        const int32_t *ids, void *dlogits, cudaStream_t s) {
+    constexpr int shared = kGateThreads * PER * 4;  // a row per warp
+    if (shared > 48 * 1024) {
+        static std::once_flag once[kMaxDevices];
+        static std::atomic<int> err[kMaxDevices];
+        int dev = 0;
+        cudaGetDevice(&dev);
+        const int slot = dev >= 0 && dev < kMaxDevices ? dev : 0;
+        once_per_device(once, [&] {
+            err[slot].store((int)cudaFuncSetAttribute(gate_grad_kernel<PER, T>,
+                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, shared));
+        });
+        if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
+    }
+    return launch_kernel(true, gate_grad_kernel<PER, T>, dim3(gate_blocks(g.n)), dim3(kGateThreads), (size_t)shared, s,
+                         dweights, static_cast<const uint8_t *>(logits), gate_args(g, dtype, logits, ldl, nullptr), ids,
+                         on16(dlogits, (int64_t)g.n_experts * (int64_t)sizeof(T)), static_cast<T *>(dlogits));
+}
+
 template <typename T>
 cudaError_t gate_grad_typed(const GateShape &g, int dtype, const float *dweights, const void *logits, int64_t ldl,
                             const int32_t *ids, void *dlogits, cudaStream_t s) {
-    constexpr int most = KMEANS_ROUTE_MAX_EXPERTS * (kGateThreads / 32) * 4;
-    static std::once_flag once[kMaxDevices];
-    static std::atomic<int> err[kMaxDevices];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const int slot = dev >= 0 && dev < kMaxDevices ? dev : 0;
-    once_per_device(once, [&] {
-        err[slot].store((int)cudaFuncSetAttribute(gate_grad_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
-    });
-    if (err[slot].load() != cudaSuccess) return (cudaError_t)err[slot].load();
-    return launch_kernel(true, gate_grad_kernel<T>, dim3(gate_blocks(g.n)), dim3(kGateThreads),
-                         (size_t)g.n_experts * (kGateThreads / 32) * 4, s, dweights, static_cast<const uint8_t *>(logits),
-                         gate_args(g, dtype, logits, ldl, nullptr), ids, static_cast<T *>(dlogits));
+    const int per = gate_per(g.n_experts);
+    const auto run = [&](auto launch) { return launch(g, dtype, dweights, logits, ldl, ids, dlogits, s); };
+    return per <= 1    ? run(launch_grad<1, T>)
+           : per <= 2  ? run(launch_grad<2, T>)
+           : per <= 4  ? run(launch_grad<4, T>)
+           : per <= 8  ? run(launch_grad<8, T>)
+           : per <= 16 ? run(launch_grad<16, T>)
+           : per <= 32 ? run(launch_grad<32, T>)
+                       : run(launch_grad<128, T>);
 }
 
 }  // namespace
