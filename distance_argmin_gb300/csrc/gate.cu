@@ -266,7 +266,7 @@ __device__ int take_best_exact(uint64_t *key, int per, int lane, uint64_t &best)
     return e;
 }
 
-__device__ __noinline__ int choose_exact(const GateArgs &p, const Logits &row, int lane) {
+__device__ __noinline__ int choose_exact(const GateArgs &p, Logits row, int lane) {
     uint64_t key[kExactPer];
     const Scores<double> sc = row_scores<double>(p, row, lane);
     const int per = (p.n_experts + 31) / 32;
@@ -325,7 +325,7 @@ __device__ __noinline__ int choose_exact(const GateArgs &p, const Logits &row, i
 }
 
 // What the candidates' order goes by, in float64.
-__device__ __noinline__ void exact_values(const GateArgs &p, const Logits &row, int lane, Candidates &list, int count) {
+__device__ __noinline__ void exact_values(const GateArgs &p, Logits row, int lane, Candidates &list, int count) {
     Scores<double> sc{p.sigmoid, 0, 0};
     if (!p.sigmoid) sc = row_scores<double>(p, row, lane);
     for (int i = lane; i < count; i += 32) {
@@ -526,39 +526,59 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
     const uint32_t bound = p.topk < 32 ? nth_largest(choice_key(high), wanted, lane) : 0u;
     float least = bound ? key_value(bound) : -INFINITY;
     if (p.bias && isfinite(least)) least -= p.gap_of(least, least);  // and what may be as large
-    int count = 0;
+    // a lane's candidates go behind those of the lanes before it: by expert
+    using Mask = std::conditional_t<(PER > 32), unsigned long long, uint32_t>;
+    constexpr int WORDS = (PER + 63) / 64, BITS = PER / WORDS;
+    Mask in[WORDS] = {};
+    int own_count = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const bool in = f[i] >= least && f[i] != -INFINITY;
-        const uint32_t who = __ballot_sync(kAll, in);
-        if (who == 0) continue;
-        const int at = count + __popc(who & ((1u << lane) - 1u));
-        if (in && at < kNear) list.found[at] = {choice_key(f[i]), e0 + i};
-        count += __popc(who);
+    for (int w = 0; w < WORDS; ++w) {
+#pragma unroll
+        for (int i = 0; i < BITS; ++i)
+            if (f[w * BITS + i] >= least && f[w * BITS + i] != -INFINITY) in[w] |= (Mask)1 << i;
+        own_count += sizeof(Mask) == 8 ? __popcll(in[w]) : __popc((uint32_t)in[w]);
     }
-    __syncwarp();
+    int upto = own_count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, upto, o);
+        if (lane >= o) upto += v;
+    }
+    int count = __shfl_sync(kAll, upto, 31);
     const bool listed = count <= kNear;
-    if (!listed) {
-        count = take_in_turn(f, p.topk + 1, lane, list);
-    } else {
+    if (listed) {
+        int at = upto - own_count;
+        if (own_count) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (in[i / BITS] >> (i % BITS) & 1) list.found[at++] = {choice_key(f[i]), e0 + i};
+        }
+        __syncwarp();
         for (int i = lane; i < count; i += 32) {
             const Candidate own = list.found[i];
             int rank = 0;
             for (int j = 0; j < count; ++j) {
-                const Candidate other = list.found[j];
-                rank += other.key > own.key || (other.key == own.key && other.expert < own.expert);
+                const uint32_t other = list.found[j].key;
+                rank += other > own.key || (other == own.key && j < i);
             }
             if (rank < 33) list.sorted[rank] = own;
         }
+    } else {
+        __syncwarp();
+        count = take_in_turn(f, p.topk + 1, lane, list);
     }
     __syncwarp();
     const int chosen = lane < p.topk && lane < count ? list.sorted[lane].expert : -1;
+    if (!p.bias) return chosen;
     bool near = false;
-    if (p.bias && chosen >= 0 && lane + 1 < count) {
-        const int after = list.sorted[lane + 1].expert;
+    if (chosen >= 0 && lane + 1 < count) {
         const float a = key_value(list.sorted[lane].key), c = key_value(list.sorted[lane + 1].key);
-        near = !(a - c > p.gap_of(a, c)) &&
-               !(row[chosen] == row[after] && p.bias[chosen] == p.bias[after]);
+        near = !(a - c > p.gap_of(a, c));
+    }
+    if (!__any_sync(kAll, near)) return chosen;
+    if (near) {  // equal in logit and bias: their order is the experts'
+        const int after = list.sorted[lane + 1].expert;
+        near = !(row[chosen] == row[after] && p.bias[chosen] == p.bias[after]);
     }
     if (!__any_sync(kAll, near)) return chosen;
     if (!listed) return choose_exact(p, row, lane);
@@ -579,7 +599,7 @@ __device__ __forceinline__ float share_of(bool sigmoid, float l, bool real) {
     }
     u = real ? u : 0.f;
     const float sum = warp_sum(u);
-    return real ? u / sum : 0.f;
+    return real ? __fdividef(u, sum) : 0.f;
 }
 
 // A softmax's parameters from the lanes' logits.
@@ -601,7 +621,8 @@ __device__ __forceinline__ void softmax_scores(const float (&f)[PER], Scores<flo
 }
 
 template <int PER>
-__global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 32 ? 6 : 2) gate_kernel(const uint8_t *__restrict__ logits, const GateArgs p,
+__global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 32 ? 6 : 2) gate_kernel(const uint8_t *__restrict__ logits,
+                                                            const __grid_constant__ GateArgs p,
                                                             int32_t *__restrict__ ids, float *__restrict__ weights) {
     __shared__ Candidates lists[kGateThreads / 32];
     griddep_wait();
