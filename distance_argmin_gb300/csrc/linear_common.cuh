@@ -56,7 +56,7 @@ struct EntropyArgs {
     bool begin, last;      // sum: the first, the last piece
     const float *inverse;  // of dz's scale
     const float *share;    // sum: per row, what dx is to be multiplied with
-    int64_t pitch;         // of dz (softmax), of stats' rows (log sum)
+    int64_t pitch;         // of dz (softmax), of stats' class parts (log sum) or rows (few)
 };
 
 struct Product16 {

@@ -500,7 +500,7 @@ __device__ __forceinline__ void log_sum(const EntropyArgs &g, float (&v)[COLS], 
 }
 
 // The same of few rows: a lane has a class, v[j] is row q0 + j (of `count`), and the
-// warp's 32 classes from f on meet by shuffles.
+// warp's 32 classes from f on meet by shuffles; a row's parts are neighbours.
 template <int COLS>
 __device__ __forceinline__ void log_sum_few(const LinearTcParams &p, const float (&v)[COLS], int count, int f, int lane,
                                             int64_t q0) {
@@ -522,7 +522,7 @@ __device__ __forceinline__ void log_sum_few(const LinearTcParams &p, const float
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == j) mine = make_float2(ref, sum);
     }
-    if (lane < count) g.stats[(int64_t)(f >> 5) * g.pitch + q0 + lane] = mine;
+    if (lane < count) g.stats[(q0 + lane) * g.pitch + (f >> 5)] = mine;
 }
 
 // Softmax: as Finish, a lane with eight classes of a row, whose record is asked for

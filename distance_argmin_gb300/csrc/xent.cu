@@ -301,6 +301,35 @@ __global__ void __launch_bounds__(kBringThreads) xent_bring_kernel(const Bring b
 // ------------------------------------------------------------------- forward
 constexpr int kJoinWarps = 32;
 
+// Two parts' (reference, sum); nothing stands for itself as (-inf, 0), and an
+// infinite sum stays one.
+__device__ __forceinline__ float2 join_parts(float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x);
+    const float u = isinf(a.y) || a.x == top ? a.y : a.y * exp2f(a.x - top);
+    const float v = isinf(b.y) || b.x == top ? b.y : b.y * exp2f(b.x - top);
+    return make_float2(top, u + v);
+}
+
+__device__ __forceinline__ float2 join_lanes(float2 s) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s = join_parts(s, make_float2(__shfl_xor_sync(kAll, s.x, o), __shfl_xor_sync(kAll, s.y, o)));
+    return s;
+}
+
+__device__ __forceinline__ void write_loss(float2 s, const EntropyRow *rows, int64_t row, const float *target, float factor,
+                                           float *loss, float *lse) {
+    const float log = log2f(s.y);
+    const int64_t at = rows[row].source;
+    // The label's distance from the reference with one rounding, as in the sum's
+    // exponentials: where the label is all there is the two cancel, however large
+    // the logits.
+    const float l = kLn2 * (log - fmaf(target[row], factor, -s.x));
+    loss[at] = l < 0.f ? 0.f : l;
+    lse[at] = kLn2 * (s.x + log);
+}
+
+// 32 rows to a block; its warps take a share of the class parts each.
 __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const EntropyRow *__restrict__ rows,
                                                                     const int32_t *count, const float2 *__restrict__ stats,
                                                                     int64_t pitch, int parts,
@@ -310,36 +339,42 @@ __global__ void __launch_bounds__(32 * kJoinWarps) xent_join_kernel(const Entrop
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t r = (int64_t)blockIdx.x * 32 + lane;
-    const bool mine = r < *count;
-    const auto join = [](float2 a, float2 b) {
-        const float top = fmaxf(a.x, b.x);
-        // (nothing stands for itself as (-inf, 0); an infinite sum stays one)
-        const float u = isinf(a.y) || a.x == top ? a.y : a.y * exp2f(a.x - top);
-        const float v = isinf(b.y) || b.x == top ? b.y : b.y * exp2f(b.x - top);
-        return make_float2(top, u + v);
-    };
     float2 s = {-INFINITY, 0.f};
-    if (mine) {
+    if (r < *count) {
 #pragma unroll 8
-        for (int i = warp; i < parts; i += kJoinWarps) s = join(s, stats[i * pitch + r]);
+        for (int i = warp; i < parts; i += kJoinWarps) s = join_parts(s, stats[i * pitch + r]);
     }
     sums[warp][lane] = s;
     __syncthreads();
-    // warp w: row w, whose parts its lanes bring together
-    s = sums[lane][warp];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        s = join(s, make_float2(__shfl_xor_sync(kAll, s.x, o), __shfl_xor_sync(kAll, s.y, o)));
+    // warp w: row w, whose shares its lanes bring together
+    s = join_lanes(sums[lane][warp]);
     const int64_t row = (int64_t)blockIdx.x * 32 + warp;
-    if (lane || row >= *count) return;
-    const float log = log2f(s.y);
-    const int64_t at = rows[row].source;
-    // The label's distance from the reference with one rounding, as in the sum's
-    // exponentials: where the label is all there is the two cancel, however large
-    // the logits.
-    const float l = kLn2 * (log - fmaf(target[row], factor, -s.x));
-    loss[at] = l < 0.f ? 0.f : l;
-    lse[at] = kLn2 * (s.x + log);
+    if (lane == 0 && row < *count) write_loss(s, rows, row, target, factor, loss, lse);
+}
+
+// Few rows: a block has one, whose parts are neighbours (24 rows of 1024 parts in
+// the layout above: 5 us in one block).
+constexpr int kJoinFewThreads = 256;
+
+__global__ void __launch_bounds__(kJoinFewThreads) xent_join_few_kernel(const EntropyRow *__restrict__ rows,
+                                                                        const int32_t *count,
+                                                                        const float2 *__restrict__ stats, int64_t pitch,
+                                                                        int parts, const float *__restrict__ target,
+                                                                        float factor, float *__restrict__ loss,
+                                                                        float *__restrict__ lse) {
+    __shared__ float2 sums[kJoinFewThreads / 32];
+    griddep_wait();
+    const int64_t row = blockIdx.x;
+    if (row >= *count) return;
+    float2 s = {-INFINITY, 0.f};
+#pragma unroll 4
+    for (int i = threadIdx.x; i < parts; i += kJoinFewThreads) s = join_parts(s, stats[row * pitch + i]);
+    s = join_lanes(s);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int w = 1; w < kJoinFewThreads / 32; ++w) s = join_parts(s, sums[w]);
+    write_loss(s, rows, row, target, factor, loss, lse);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -572,7 +607,8 @@ cudaError_t launch_xent(const XentShape &sh, const void *x, int64_t ldx, const v
     EntropyArgs en = st.entropy;
     en.stats = reinterpret_cast<float2 *>(ws + L.off_stats);
     en.target = reinterpret_cast<float *>(ws + L.off_target);
-    en.pitch = align_up(sh.m, 32);
+    const int64_t parts = class_parts(sh.m, sh.n);
+    en.pitch = sh.m <= kFewRows ? parts : align_up(sh.m, 32);
     Product16 g{};
     if (sh.m <= kFewRows) {
         const LinearShape ps{sh.m, sh.n, sh.k, 1, st.offsets, sh.bf16};
@@ -593,10 +629,12 @@ cudaError_t launch_xent(const XentShape &sh, const void *x, int64_t ldx, const v
         e = product<Product::kLogSum>(ps, g, p, sh.n, s);
     }
     if (e != cudaSuccess) return e;
-    const int parts = (int)class_parts(sh.m, sh.n);
-    return launch_kernel(true, xent_join_kernel, dim3((unsigned)((sh.m + 31) / 32)), dim3(32 * kJoinWarps), 0, s,
-                         (const EntropyRow *)en.rows, en.count, (const float2 *)en.stats, en.pitch, parts,
-                         (const float *)en.target, en.factor, loss, lse);
+    const auto join = [&](auto kernel, int64_t blocks, int threads) {
+        return launch_kernel(true, kernel, dim3((unsigned)blocks), dim3((unsigned)threads), 0, s, en.rows, en.count,
+                             (const float2 *)en.stats, en.pitch, (int)parts, (const float *)en.target, en.factor, loss, lse);
+    };
+    return sh.m <= kFewRows ? join(xent_join_few_kernel, sh.m, kJoinFewThreads)
+                            : join(xent_join_kernel, (sh.m + 31) / 32, 32 * kJoinWarps);
 }
 
 cudaError_t launch_xent_grad(const XentShape &sh, const float *dloss, const void *x, int64_t ldx, const void *w,
