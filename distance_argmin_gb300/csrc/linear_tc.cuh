@@ -43,7 +43,6 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <cstdlib>
 
 #include "assign_common.cuh"
 #include "linear_common.cuh"

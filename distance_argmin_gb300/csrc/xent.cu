@@ -6,11 +6,17 @@
 // that the products see only them: ignored rows cost nothing, and whatever they
 // hold reaches no result.
 // Forward: the product (log sum, see linear_tc.cuh) leaves each row's largest
-// logit and sum of exponentials per 64 classes, which xent_join_kernel brings
-// together.  Gradient: piece by piece of the classes dz is formed from the logits
-// once more, in 16 bits, and goes into both products while it is near; dx is
-// added up in float32 from piece to piece.  The products bound both: 2 and 6
-// operations per row, class and feature.
+// logit and sum of exponentials per 64 classes (few rows: 32), which the join
+// kernels bring together.  Gradient: piece by piece of the classes dz is formed from
+// the logits once more, in 16 bits, and goes into both products while it is near;
+// dx is added up in float32 from piece to piece.
+//
+// The tensor pipe bounds both, 2 and 6 operations per row, class and feature: 8192
+// rows of 32768 classes, k = 2048, bfloat16, forward 568 to 577 us (1905 to 1935
+// TFLOP/s; a library product that writes the logits 552 to 581 over the same runs),
+// gradient 1710 to 1789 us (1844 to 1929 TFLOP/s).  Few rows are bound by the
+// classes' matrix: 24 rows of 131072 classes, k = 4096, 173 us, 6.2 TB/s (the
+// library's product 169).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
