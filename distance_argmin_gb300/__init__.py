@@ -1283,8 +1283,8 @@ def _classes_args(x, w, labels, scale):
     if labels.dtype is not torch.int64 and labels.dtype is not torch.int32:
         raise TypeError(f"labels must be int32 or int64, got {labels.dtype}")
     _check_on(labels, "labels", labels.dtype, (m,), dev)
-    if not (scale > 0 and math.isfinite(scale)):
-        raise ValueError(f"scale must be positive, got {scale}")
+    if not 0 < scale <= 2.0 ** 127:
+        raise ValueError(f"scale must be positive and at most 2^127, got {scale}")
     return code, m, w.shape[0], k, ldx
 
 
@@ -1295,8 +1295,8 @@ def kmeans_cross_entropy(x, w, labels, scale: float = 1.0, loss=None, lse=None, 
     that minus its label's logit.
 
     ``labels`` (m,) int32 or int64; a negative one marks a row that does not
-    count: loss and lse 0, and whatever it holds reaches nothing else.
-    float16 or bfloat16."""
+    count: loss and lse 0, and whatever it holds reaches nothing else.  One of n
+    or more does not count either, and ``kmeans_device_status(ws)`` reports it.  float16 or bfloat16."""
     if stream is not None:
         return _on_stream(stream, kmeans_cross_entropy, x, w, labels, scale, loss, lse, ws)
     torch = _torch()

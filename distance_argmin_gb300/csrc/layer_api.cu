@@ -41,8 +41,9 @@ bool xent_sizes_ok(int64_t m, int64_t n, int64_t k) {
 
 int check_xent(int dtype, const void *x, int64_t ldx, const void *w, const void *labels, int id_bytes, float scale,
                int64_t m, int64_t n, int64_t k) {
+    // (scale / ln 2, which the logits are multiplied with, has to be finite)
     if (!known_dtype(dtype) || (id_bytes != 4 && id_bytes != 8) || !xent_sizes_ok(m, n, k) || !(scale > 0.f) ||
-        !isfinite(scale))
+        scale > 0x1p127f)
         return KMEANS_ERR_INVALID_ARG;
     if (m > 0 && (!x || !w || !labels || ldx < k)) return KMEANS_ERR_INVALID_ARG;
     if (!elem_aligned(x, dtype) || !elem_aligned(w, dtype) ||

@@ -633,7 +633,8 @@ size_t kmeans_cross_entropy_workspace_bytes(int grad, int64_t m, int64_t n, int6
  * int32, 8: int64), each in [0, n), or negative for a row that does not count:
  * its loss and lse are 0 and what it holds reaches no other result.  A label of
  * n or more counts as negative and sets KMEANS_ERR_DEVICE_LABEL in the
- * workspace's status word.  loss and lse (m) float32; scale > 0.
+ * workspace's status word.  loss and lse (m) float32; 0 < scale <=
+ * 2^127.
  * m, n <= KMEANS_LINEAR_MAX_SIZE, n >= 1, 1 <= k <=
  * KMEANS_CROSS_ENTROPY_MAX_WIDTH, and no matrix, nor m * n, of 2^42 values or
  * more.  Where k is not a multiple of 8, w is first copied into the workspace. */

@@ -113,6 +113,15 @@ def test_the_cross_entropy_validates_on_the_host(km):
     assert grad(dt=0) == NO and grad(w=EIGHT) == NO and grad(wsb=need_g - 1) == WS
 
 
+@pytest.mark.parametrize("scale", [1.75 * 2.0 ** 127, 3e38])
+def test_a_scale_whose_product_with_the_logits_unit_overflows_is_refused(km, scale):
+    lib, BAD = km.load(), km.KMEANS_ERR_INVALID_ARG
+    # finite, but times 1 / ln 2 it is not: a row of zeros would lose log(n) to NaN
+    a = [F, 64, F, 2, F, 8]
+    assert lib.kmeans_cross_entropy(*a, scale, 100, 1000, 64, F, F, W, 1 << 50, None) == BAD
+    assert lib.kmeans_cross_entropy_grad(F, *a, F, scale, 100, 1000, 64, F, F, W, 1 << 50, None) == BAD
+
+
 def test_the_binding_refuses_what_is_not_on_the_gpu(km):
     import torch
     x, i = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
