@@ -13,8 +13,8 @@
 // The choice is that of exact arithmetic.  Without a bias the order is the
 // logits' own.  Sums (c, and the groups' scores) are formed in float32; where two
 // neighbours in the order, the last chosen and the first left out among them, are
-// nearer than their errors (GateArgs::gap_of) and not equal in both logit and bias, what is
-// near is formed again in float64.
+// nearer than their errors (Gap) and not equal in both logit and bias, what is near
+// is formed again in pairs of floats, and what is near even so in float64.
 //
 // A warp has a token, a lane PER neighbouring experts in registers.  What is left
 // out early costs least: no lane can hold one of the topk + 1 largest unless its
@@ -22,10 +22,11 @@
 // bounds the values that are looked at further, a few more than topk.  They are
 // brought together, one to a lane, and each counts the ones before it.
 //
-// Instructions bound it, 1183 of a warp per token: 16384 tokens, 8 of 256 float32
-// experts in 4 of 8 groups, sigmoid and bias take 24 to 26 us a call, where reading
-// the logits takes 2.6; 20.6 without the groups, 23.1 without the bias, 14.4
-// without both.  An argmax over all lanes and values for each choice took 68.
+// Instructions bound it: 16384 tokens, 8 of 256 float32 experts in 4 of 8 groups,
+// sigmoid and bias take 22 to 23 us a call, where reading the logits takes 2.6; 18.5
+// without the groups, 24 without the bias (the logits are loaded once more, for their
+// order), 12.4 without both.  An argmax over all lanes and values for each choice
+// took 68.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -104,11 +105,7 @@ struct GateArgs {
     const float *bias;
     bool whole, bias_whole;  // rows of the logits, the bias, start on 16 bytes
     int lanes_per_group;     // where a group is a power of two of whole lanes, else 0
-    float gap;
-    // How near two values of the order may be in float32 without being looked at
-    // in float64: twice what they may be off by.  gap: a score's error, twice (see
-    // gate_args); then half a last bit of each sum with the bias.
-    __device__ __forceinline__ float gap_of(float a, float b) const { return gap + 0x1p-23f * (fabsf(a) + fabsf(b)); }
+    float gap;               // a score's error in float32, twice, over the largest score (see gate_args)
 };
 
 // The row's score parameters: softmax takes exp(l - top) / sum.
@@ -116,6 +113,18 @@ template <typename V>
 struct Scores {
     bool sigmoid;
     V top, inverse;
+};
+
+// How near two values of the order may be in float32 without being looked at
+// further: twice what they may be off by, which is a score's error, no more than
+// the largest score's, and half a last bit of each sum with the bias.
+struct Gap {
+    float score;
+    __device__ __forceinline__ Gap(const GateArgs &p, const Scores<float> &sc)
+        : score(p.sigmoid ? p.gap : fminf(p.gap * sc.inverse, p.gap)) {}
+    __device__ __forceinline__ float operator()(float a, float b) const {
+        return score + 0x1p-23f * (fabsf(a) + fabsf(b));
+    }
 };
 
 __device__ __forceinline__ float score_of(const Scores<float> &s, float l) {
@@ -329,6 +338,133 @@ __device__ __noinline__ int choose_exact(const GateArgs &p, Logits row, int lane
     return chosen;
 }
 
+// A number as the sum of two floats, the second below half a last bit of the
+// first, and the sums and products of Dekker (1971) and Knuth.
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair short_sum(float a, float b) {  // |a| >= |b|
+    const float s = __fadd_rn(a, b);
+    return {s, __fadd_rn(b, -__fadd_rn(s, -a))};
+}
+__device__ __forceinline__ Pair sum_of(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fadd_rn(s, -a);
+    return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t))};
+}
+__device__ __forceinline__ Pair product_of(float a, float b) {
+    const float p = __fmul_rn(a, b);
+    return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Pair add(const Pair &a, const Pair &b) {
+    const Pair s = sum_of(a.hi, b.hi);
+    return short_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Pair multiply(const Pair &a, const Pair &b) {
+    const Pair p = product_of(a.hi, b.hi);
+    return short_sum(p.hi, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, p.lo)));
+}
+__device__ __forceinline__ Pair inverse_of(const Pair &a) {
+    const float q = __fdividef(1.f, a.hi);  // (what it is off by, twice 2^-24, goes out squared)
+    return short_sum(q, __fmul_rn(q, __fmaf_rn(-q, a.lo, __fmaf_rn(-q, a.hi, 1.f))));
+}
+
+// 2^(j / 32).
+__device__ const float2 kRoots[32] = {
+    {0x1p+0f, 0.f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f}, {0x1.11301ep+0f, -0x1.fdb496p-25f},
+    {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f}, {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.29e9ep+0f, -0x1.5c0424p-25f},
+    {0x1.306fep+0f, 0x1.4636e2p-25f}, {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.44e086p+0f, 0x1.8624b4p-30f},
+    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.5342b6p+0f, -0x1.2c561p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f}, {0x1.6247ecp+0f, -0x1.f8b55p-25f},
+    {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f}, {0x1.7a1148p+0f, -0x1.829fdp-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f},
+    {0x1.8ace54p+0f, 0x1.15506ep-27f}, {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f},
+    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b7f77p+0f, -0x1.a09438p-25f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f}, {0x1.cb720ep+0f, -0x1.8837ccp-27f},
+    {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.dfc974p+0f, -0x1.908c94p-25f}, {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.f50766p+0f, -0x1.246ebp-26f}};
+
+// exp of x in [-80, 80], 2^-43 of it for |x| <= 8, 2^-39 to the ends (below 2^-100
+// its second float loses bits), by Tang's method (1989): x = n ln(2) / 32 + r, and
+// exp(r) = 1 + r + r^2 / 2 + .. with |r| < 2^-6.5, whose terms from the cube on
+// need one float.
+__device__ __forceinline__ Pair exp_of(const Pair &x) {
+    constexpr float STEP = 0x1.62e43p-6f, STEP_REST = -0x1.05c61p-34f;  // ln(2) / 32
+    const float n = rintf(__fmul_rn(x.hi, 0x1.715476p+5f));
+    const Pair p = product_of(n, STEP);
+    const Pair r = sum_of(__fadd_rn(x.hi, -p.hi), __fmaf_rn(-n, STEP_REST, __fadd_rn(x.lo, -p.lo)));
+    Pair q = product_of(r.hi, r.hi);
+    q.lo = __fmaf_rn(2.f * r.hi, r.lo, q.lo);
+    const float cube = __fmul_rn(__fmul_rn(r.hi, q.hi),
+                                 __fmaf_rn(r.hi, __fmaf_rn(r.hi, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f));
+    Pair u = sum_of(r.hi, 0.5f * q.hi);
+    u.lo = __fadd_rn(u.lo, __fmaf_rn(0.5f, q.lo, __fadd_rn(r.lo, cube)));
+    const int i = (int)n;
+    const float2 root = kRoots[i & 31];
+    Pair t = product_of(root.x, u.hi);
+    t.lo = __fadd_rn(root.y, __fmaf_rn(root.x, u.lo, __fmaf_rn(root.y, u.hi, t.lo)));
+    const Pair s = sum_of(root.x, t.hi);
+    const Pair e = short_sum(s.hi, __fadd_rn(s.lo, t.lo));
+    const float power = __int_as_float(((i >> 5) + 127) << 23);
+    return {__fmul_rn(e.hi, power), __fmul_rn(e.lo, power)};
+}
+
+// exp(l - top), nothing where that is below e^-80.
+__device__ __forceinline__ Pair exp_below(float l, float top) {
+    const Pair x = sum_of(l, -top);
+    if (!(x.hi > -80.f)) return {0.f, 0.f};
+    return exp_of(x);
+}
+
+// What a row's scores as pairs need: nothing for the logistic function.
+struct PairScores {
+    float top;
+    Pair inverse;
+};
+
+// False where the row holds what has no finite scores.
+__device__ __forceinline__ bool pair_scores(const GateArgs &p, const Logits &row, int lane, PairScores &sc) {
+    sc = {0.f, {1.f, 0.f}};
+    if (p.sigmoid) return true;
+    float top = -INFINITY;
+    bool nan = false;
+    for (int e = lane; e < p.n_experts; e += 32) {
+        const float l = row[e];
+        top = fmaxf(top, l);
+        nan = nan || l != l;
+    }
+    top = warp_fmax(top);
+    if (__any_sync(kAll, nan) || !isfinite(top)) return false;
+    Pair sum = {0.f, 0.f};
+#pragma unroll 4
+    for (int e = lane; e < p.n_experts; e += 32) sum = add(sum, exp_below(row[e], top));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum = add(sum, Pair{__shfl_xor_sync(kAll, sum.hi, o), __shfl_xor_sync(kAll, sum.lo, o)});
+    sc = {top, inverse_of(sum)};
+    return true;
+}
+
+// What the choice goes by, the score within 2^-40.
+__device__ __forceinline__ double pair_value(const GateArgs &p, const Logits &row, int e, const PairScores &sc) {
+    const float l = row[e];
+    const float b = p.bias ? p.bias[e] : 0.f;
+    Pair s;
+    if (p.sigmoid)  // (past the ends it is 0 or 1 to 2^-57)
+        s = inverse_of(add({1.f, 0.f}, exp_of({fminf(fmaxf(-l, -40.f), 80.f), 0.f})));
+    else
+        s = multiply(exp_below(l, sc.top), sc.inverse);
+    const double c = (double)s.hi + ((double)s.lo + (double)b);
+    return l != l || c != c ? (double)INFINITY : c;
+}
+
+// The candidates' values so.
+__device__ __noinline__ bool near_values(const GateArgs &p, Logits row, int lane, Candidates &list, int count) {
+    PairScores sc;
+    if (!pair_scores(p, row, lane, sc)) return false;
+    for (int i = lane; i < count; i += 32) list.value[i] = pair_value(p, row, list.found[i].expert, sc);
+    __syncwarp();
+    return true;
+}
+
+// Whether such values' order may be another one than that of the exact ones.
+__device__ __forceinline__ bool nearer(double a, double b) { return !(fabs(a - b) > 0x1p-38 + 0x1p-50 * fabs(a)); }
+
 // What the candidates' order goes by, in float64.
 __device__ __noinline__ void exact_values(const GateArgs &p, Logits row, int lane, Candidates &list, int count) {
     Scores<double> sc{p.sigmoid, 0, 0};
@@ -341,29 +477,60 @@ __device__ __noinline__ void exact_values(const GateArgs &p, Logits row, int lan
     __syncwarp();
 }
 
+// The order where neighbours in it (lane j's expert and lane j + 1's) are near, each
+// pair by itself: lane j's expert then, or -2 in every lane where that does not
+// settle it.  A row that is looked at again keeps its SM waiting at the end, so this
+// is short: without it, all candidates in float64 and ranked again, 16384 x 256 in 8
+// groups took 26 us with sigmoid and 31 with softmax for a row in a thousand.
+__device__ __noinline__ int settle_pairs(const GateArgs &p, Logits row, int lane, int expert, bool near) {
+    PairScores sc;
+    if (!pair_scores(p, row, lane, sc)) return -2;
+    const double own = expert >= 0 ? pair_value(p, row, expert, sc) : 0.0, after = __shfl_down_sync(kAll, own, 1);
+    if (__any_sync(kAll, near && nearer(own, after))) return -2;
+    const uint32_t swap = __ballot_sync(kAll, near && after > own);
+    const int down = __shfl_down_sync(kAll, expert, 1), up = __shfl_up_sync(kAll, expert, 1);
+    return swap >> lane & 1u ? down : (swap << 1) >> lane & 1u ? up : expert;
+}
+
 // The groups that stay, of those (lane g: group g) with a bit in `near`, whose two
-// largest values are among the candidates.
+// largest values are among the candidates (their keys: the groups).  EXACT: in float64; else kAll where one
+// that stays is near one that does not (which all 32 cannot: they are left out of).
+template <bool EXACT>
 __device__ __noinline__ uint32_t refine_groups(const GateArgs &p, int lane, const Candidates &list, int count,
                                                uint32_t near, int wanted) {
     double one = -INFINITY, two = -INFINITY;
     for (int i = 0; i < count; ++i) {
-        if (list.found[i].expert / p.group_size != lane) continue;
+        if ((int)list.found[i].key != lane) continue;
         const double c = list.value[i];
         two = c > one ? one : (c > two ? c : two);
         one = c > one ? c : one;
     }
-    const uint64_t total = choice_key(two == -INFINITY ? one : one + two);
+    const double score = two == -INFINITY ? one : one + two;
+    const uint64_t total = choice_key(score);
     int rank = 0;
     for (int g = 0; g < p.groups; ++g) {
         const uint64_t other = (uint64_t)__shfl_sync(kAll, (unsigned long long)total, g);
         rank += (near >> g & 1u) && (other > total || (other == total && g < lane));
     }
     __syncwarp();
-    return __ballot_sync(kAll, (near >> lane & 1u) && rank < wanted);
+    const uint32_t kept = __ballot_sync(kAll, (near >> lane & 1u) && rank < wanted);
+    if constexpr (!EXACT) {
+        // the last that stays and the first that does not
+        const uint32_t last = __ballot_sync(kAll, (near >> lane & 1u) && rank == wanted - 1);
+        const uint32_t next = __ballot_sync(kAll, (near >> lane & 1u) && rank == wanted);
+        if (last && next) {
+            const double a = __shfl_sync(kAll, score, __ffs(last) - 1), b = __shfl_sync(kAll, score, __ffs(next) - 1);
+            if (nearer(a, b)) return kAll;
+        }
+    }
+    return kept;
 }
 
-// The candidates' experts in order: lane j has the j-th (-1: none).
-__device__ __noinline__ int refine_order(int topk, int lane, Candidates &list, int count) {
+// The candidates' experts in order: lane j has the j-th (-1: none).  EXACT: in
+// float64; else -2 in every lane where neighbours are near and not equal in both
+// logit and bias.
+template <bool EXACT>
+__device__ __noinline__ int refine_order(const GateArgs &p, const Logits row, int lane, Candidates &list, int count) {
     for (int i = lane; i < count; i += 32) {
         const int e = list.found[i].expert;
         const uint64_t own = choice_key(list.value[i]);
@@ -372,10 +539,20 @@ __device__ __noinline__ int refine_order(int topk, int lane, Candidates &list, i
             const uint64_t other = choice_key(list.value[j]);
             rank += other > own || (other == own && list.found[j].expert < e);
         }
-        if (rank < 33) list.sorted[rank].expert = e;
+        if (rank < 33) list.sorted[rank] = {(uint32_t)i, e};
     }
     __syncwarp();
-    return lane < topk && lane < count ? list.sorted[lane].expert : -1;
+    const int chosen = lane < p.topk && lane < count ? list.sorted[lane].expert : -1;
+    if constexpr (!EXACT) {
+        bool near = false;
+        if (chosen >= 0 && lane + 1 < count) {
+            const Candidate after = list.sorted[lane + 1];
+            near = nearer(list.value[list.sorted[lane].key], list.value[after.key]) &&
+                   !(row[chosen] == row[after.expert] && p.bias[chosen] == p.bias[after.expert]);
+        }
+        if (__any_sync(kAll, near)) return -2;
+    }
+    return chosen;
 }
 
 __device__ __forceinline__ float group_total(float one, float two) { return two == -INFINITY ? one : one + two; }
@@ -413,13 +590,14 @@ __device__ __forceinline__ int take_in_turn(float (&f)[PER], int wanted, int lan
     return count;
 }
 
-// Chooses a row's experts: returns the j-th in lane j (-1: none).
-template <int PER>
+// Chooses a row's experts: returns the j-th in lane j (-1: none).  SUMS: by sums with
+// a bias or within groups; else by the logits alone.
+template <int PER, bool SUMS>
 __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int lane, const Scores<float> &sc, float (&f)[PER],
                                       Candidates &list) {
     const int e0 = lane * PER;
-    const bool sums = p.bias || p.groups > 1;
-    if (sums) {
+    const Gap gap_of(p, sc);
+    if constexpr (SUMS) {
         constexpr int RUN = PER < 4 ? PER : 4;
 #pragma unroll
         for (int i = 0; i < PER; i += RUN) {
@@ -436,7 +614,7 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) f[i] = f[i] != f[i] ? INFINITY : f[i];
-    if (p.groups > 1) {
+    if (SUMS && p.groups > 1) {
         float total = -INFINITY, second = -INFINITY;  // lane g: group g's score, its second largest value
         bool mine[PER];
         if (p.lanes_per_group > 0) {  // whole lanes, a power of two of them
@@ -475,7 +653,7 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
             if (lane == g) key = 0;
         }
         if (next != 0 && last != 0) {
-            const float in = key_value(last), out = key_value(next), gap = 2.f * p.gap_of(in, out);
+            const float in = key_value(last), out = key_value(next), gap = 2.f * gap_of(in, out);
             if (!(in - out > gap)) {
                 // Near (equal sums are rarely sums of equal parts, so they are looked
                 // at too): what is further above the first left out than float32 may
@@ -483,22 +661,32 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
                 // is compared in float64.
                 const uint32_t sure = __ballot_sync(kAll, total > out + gap);
                 const uint32_t near = __ballot_sync(kAll, total >= in - gap && !(total > out + gap));
-                int count = 0;
+                int count = 0, g = e0 / p.group_size, left = (g + 1) * p.group_size - e0;
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int g = (e0 + i) / p.group_size;
                     const float two = __shfl_sync(kAll, second, g & 31);
-                    const bool take = f[i] != -INFINITY && (near >> (g & 31) & 1u) && !(two - f[i] > p.gap_of(two, f[i]));
+                    const bool take = f[i] != -INFINITY && (near >> (g & 31) & 1u) && !(two - f[i] > gap_of(two, f[i]));
                     const uint32_t who = __ballot_sync(kAll, take);
                     const int at = count + __popc(who & ((1u << lane) - 1u));
-                    if (take && at < kNear) list.found[at].expert = e0 + i;
+                    if (take && at < kNear) list.found[at] = {(uint32_t)g, e0 + i};
                     count += __popc(who);
+                    if (--left == 0) {
+                        ++g;
+                        left = p.group_size;
+                    }
                 }
                 // (infinite sums have no order in float32)
                 if (count > kNear || !isfinite(in) || !isfinite(out)) return choose_exact(p, row, lane);
                 __syncwarp();
-                exact_values(p, row, lane, list, count);
-                kept = sure | refine_groups(p, lane, list, count, near, p.topk_groups - __popc(sure));
+                const int wanted = p.topk_groups - __popc(sure);
+                uint32_t some = kAll;
+                if (near_values(p, row, lane, list, count))
+                    some = refine_groups<false>(p, lane, list, count, near, wanted);
+                if (some == kAll) {
+                    exact_values(p, row, lane, list, count);
+                    some = refine_groups<true>(p, lane, list, count, near, wanted);
+                }
+                kept = sure | some;
             }
         }
         if (p.lanes_per_group > 0) {
@@ -530,7 +718,7 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
     const int wanted = min(p.topk + 1, 32);  // (32 lanes have no 33rd: then all are looked at)
     const uint32_t bound = p.topk < 32 ? nth_largest(choice_key(high), wanted, lane) : 0u;
     float least = bound ? key_value(bound) : -INFINITY;
-    if (p.bias && isfinite(least)) least -= p.gap_of(least, least);  // and what may be as large
+    if (SUMS && p.bias && isfinite(least)) least -= gap_of(least, least);  // and what may be as large
     // a lane's candidates go behind those of the lanes before it: by expert
     using Mask = std::conditional_t<(PER > 32), unsigned long long, uint32_t>;
     constexpr int WORDS = (PER + 63) / 64, BITS = PER / WORDS;
@@ -573,22 +761,34 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
         count = take_in_turn(f, p.topk + 1, lane, list);
     }
     __syncwarp();
-    const int chosen = lane < p.topk && lane < count ? list.sorted[lane].expert : -1;
-    if (!p.bias) return chosen;
+    // (the first that is left out with them, to see what is near it)
+    const int expert = lane <= p.topk && lane < count ? list.sorted[lane].expert : -1;
+    const int chosen = lane < p.topk ? expert : -1;
+    if (!SUMS || !p.bias) return chosen;
     bool near = false;
-    if (chosen >= 0 && lane + 1 < count) {
+    if (expert >= 0 && lane + 1 < count) {
         const float a = key_value(list.sorted[lane].key), c = key_value(list.sorted[lane + 1].key);
-        near = !(a - c > p.gap_of(a, c));
+        near = !(a - c > gap_of(a, c));
     }
-    if (!__any_sync(kAll, near)) return chosen;
+    const uint32_t all = __ballot_sync(kAll, near);
+    if (all == 0) return chosen;
+    near = near && chosen >= 0;
     if (near) {  // equal in logit and bias: their order is the experts'
         const int after = list.sorted[lane + 1].expert;
         near = !(row[chosen] == row[after] && p.bias[chosen] == p.bias[after]);
     }
-    if (!__any_sync(kAll, near)) return chosen;
+    const uint32_t some = __ballot_sync(kAll, near);
+    if (some == 0) return chosen;
     if (!listed) return choose_exact(p, row, lane);
-    exact_values(p, row, lane, list, count);
-    return refine_order(p.topk, lane, list, count);
+    int order = -2;
+    if (!(some & (all << 1 | all >> 1)) && p.topk < 32) order = settle_pairs(p, row, lane, expert, near);
+    if (order != -2) return lane < p.topk ? order : -1;
+    if (near_values(p, row, lane, list, count)) order = refine_order<false>(p, row, lane, list, count);
+    if (order == -2) {
+        exact_values(p, row, lane, list, count);
+        order = refine_order<true>(p, row, lane, list, count);
+    }
+    return order;
 }
 
 // The chosen experts' shares of their sum; lane j has expert j's logit.  Scaled
@@ -625,16 +825,18 @@ __device__ __forceinline__ void softmax_scores(const float (&f)[PER], Scores<flo
     sc.inverse = all == 0.f ? 0.f : 1.f / all;
 }
 
-template <int PER>
-__global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 32 ? 6 : 2) gate_kernel(const uint8_t *__restrict__ logits,
-                                                            const __grid_constant__ GateArgs p,
-                                                            int32_t *__restrict__ ids, float *__restrict__ weights) {
+// (A kernel of its own for the logits alone: what sums need would make 16384 x 256, 8
+// choices, 15.0 us instead of 12.4, and 8192 x 1024 14.8 instead of 12.6.)
+template <int PER, bool SUMS>
+__global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 32 ? 6 : 2)
+    gate_kernel(const uint8_t *__restrict__ logits, const __grid_constant__ GateArgs p, int32_t *__restrict__ ids,
+                float *__restrict__ weights) {
     __shared__ Candidates lists[kGateThreads / 32];
     griddep_wait();
     const int lane = threadIdx.x & 31;
     Candidates &list = lists[threadIdx.x >> 5];
     // (renormalised softmax weights that are chosen by the logits need no sum of all)
-    const bool need_sum = !p.sigmoid && (p.bias || p.groups > 1 || !p.renormalize);
+    const bool need_sum = !p.sigmoid && (SUMS || !p.renormalize);
     const int64_t step = (int64_t)gridDim.x * (kGateThreads / 32);
     for (int64_t r = (int64_t)blockIdx.x * (kGateThreads / 32) + (threadIdx.x >> 5); r < p.n; r += step) {
         const Logits row{logits + r * p.pitch, p.dtype};
@@ -642,7 +844,7 @@ __global__ void __launch_bounds__(kGateThreads, PER <= 8 ? 8 : PER <= 32 ? 6 : 2
         load_run<PER>(row, lane * PER, p.n_experts, p.whole, f);
         Scores<float> sc{p.sigmoid, 0.f, 0.f};
         if (need_sum) softmax_scores(f, sc);
-        const int e = choose<PER>(p, row, lane, sc, f, list);
+        const int e = choose<PER, SUMS>(p, row, lane, sc, f, list);
         const bool real = lane < p.topk && e >= 0;
         const float l = real ? row[e] : 0.f;
         float w = p.renormalize ? share_of(p.sigmoid, l, real) : score_of(sc, l);
@@ -745,7 +947,8 @@ GateArgs gate_args(const GateShape &g, int dtype, const void *logits, int64_t ld
     // Twice a score's error in float32, in 2^-24: an exponential of x is off by (2
     // |x| + 4) of itself.  The logistic function damps that by s (1 - s), its sum
     // and quotient add 5: 7.  In softmax |x| e^x is at most 0.37, the sum of n
-    // terms, four accumulators to a lane, adds n / 128 + 8, the rest 6.
+    // terms, four accumulators to a lane, adds n / 128 + 8, the rest 6, all of it
+    // times the largest score, exp(0) over the sum.
     const float gap = (g.sigmoid ? 16.f : (float)g.n_experts / 64.f + 30.f) * 0x1p-24f;
     const int64_t pitch = ldl * (dtype == KMEANS_F32 ? 4 : 2);
     return {g.n, pitch, dtype, g.n_experts, g.topk, g.groups, g.topk_groups, size, g.sigmoid, g.renormalize, g.scale, bias,
@@ -787,18 +990,25 @@ cudaError_t gate_grad_typed(const GateShape &g, int dtype, const float *dweights
                        : run(launch_grad<128, T>);
 }
 
+using GateKernel = void (*)(const uint8_t *, GateArgs, int32_t *, float *);
+
+template <bool SUMS>
+GateKernel gate_kernel_of(int n_experts) {
+    const int per = gate_per(n_experts);
+    return per <= 1    ? gate_kernel<1, SUMS>
+           : per <= 2  ? gate_kernel<2, SUMS>
+           : per <= 4  ? gate_kernel<4, SUMS>
+           : per <= 8  ? gate_kernel<8, SUMS>
+           : per <= 16 ? gate_kernel<16, SUMS>
+           : per <= 32 ? gate_kernel<32, SUMS>
+                       : gate_kernel<128, SUMS>;
+}
+
 }  // namespace
 
 cudaError_t launch_gate(const GateShape &g, int dtype, const void *logits, int64_t ldl, const float *bias, int32_t *ids,
                         float *weights, cudaStream_t s) {
-    const int per = gate_per(g.n_experts);
-    void (*kernel)(const uint8_t *, GateArgs, int32_t *, float *) = per <= 1    ? gate_kernel<1>
-                                                                    : per <= 2  ? gate_kernel<2>
-                                                                    : per <= 4  ? gate_kernel<4>
-                                                                    : per <= 8  ? gate_kernel<8>
-                                                                    : per <= 16 ? gate_kernel<16>
-                                                                    : per <= 32 ? gate_kernel<32>
-                                                                                : gate_kernel<128>;
+    const auto kernel = bias || g.groups > 1 ? gate_kernel_of<true>(g.n_experts) : gate_kernel_of<false>(g.n_experts);
     return launch_kernel(true, kernel, dim3(gate_blocks(g.n)), dim3(kGateThreads), 0, s,
                          static_cast<const uint8_t *>(logits), gate_args(g, dtype, logits, ldl, bias), ids, weights);
 }

@@ -112,6 +112,40 @@ def test_sums_that_float32_cannot_tell_apart(gpu_lib, kind, groups, topk_groups)
     assert np.array_equal(ids.cpu().numpy(), want)
 
 
+def near_case(kind, groups, topk_groups, n=1500, E=48, topk=9):
+    """Scores and a bias that cancel to about 2^-25, differently for every token: some neighbours in the order are
+    2^-32 apart, some less than 2^-38.  Returns also the smallest distance that decides anything."""
+    r = np.random.RandomState(7)
+    base = r.randn(E).astype(np.float32)
+    bias = (0.5 - scores_of(base[None].astype(np.float64), kind)[0]).astype(np.float32)
+    z = base * (1 + r.randint(-1, 2, (n, E)) * np.float32(2.0 ** -23))
+    z = z.astype(np.float32)
+    c = scores_of(z.astype(np.float64), kind) + bias
+    least = []
+    if groups > 1:
+        size = E // groups
+        total = np.sort(c.reshape(n, groups, size), 2)[:, :, -2:].sum(2)
+        order = -np.sort(-total, 1)
+        least.append(order[:, topk_groups - 1] - order[:, topk_groups])
+        kept = total >= order[:, topk_groups - 1:topk_groups]
+        c = np.where(np.repeat(kept, size, 1), c, -np.inf)
+    order = -np.sort(-c, 1)[:, :topk + 1]
+    least.append((order[:, :-1] - order[:, 1:]).ravel())
+    return z, bias, np.concatenate(least)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,topk_groups", [(1, 1), (8, 3)])
+def test_the_order_of_sums_that_are_nearer_and_nearer(gpu_lib, kind, groups, topk_groups):
+    z, bias, gaps = near_case(kind, groups, topk_groups)
+    # both ways of telling them apart are needed, and float64 itself (2^-52 of 1) is enough
+    assert (gaps < 2.0 ** -38).sum() >= 5 and (gaps > 2.0 ** -38).sum() > 1000 and gaps.min() > 2.0 ** -50
+    ids, _ = gpu_lib.kmeans_gate(torch.from_numpy(z).cuda(), 9, scores=kind, bias=torch.from_numpy(bias).cuda(),
+                                 groups=groups, topk_groups=topk_groups)
+    want, _ = plain_gate(z.astype(np.float64), 9, kind, bias.astype(np.float64), groups, topk_groups)
+    assert np.array_equal(ids.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
 def test_equal_experts_are_taken_by_index(gpu_lib, kind, biased):
