@@ -46,6 +46,13 @@ constexpr int kBringThreads = 32 * kBringRows;
 // 117; 4096 of 4096 25 and 27.)
 constexpr int64_t kCountHere = 4096;
 
+// A class matrix of up to so many values that has to be brought to 16 bytes is so by
+// the rows' kernel, which saves a launch; larger ones by launch_align, whose warps
+// keep more in flight.  (1031 rows of 10007 classes, k = 515: forward 28.8 and
+// gradient 75 us, 32.3 and 80 apart; 2000 of 32768, k = 1023 the same; 24 of 32768,
+// k = 2047 forward 86 and 83; 100 of 100000, k = 2047 248 and 230.)
+constexpr int64_t kAlignHere = (int64_t)1 << 25;
+
 // Of kShareRows rows: how many count (and then: before them), whether a label is
 // past the classes, and the largest gradient's magnitude.
 struct alignas(16) Tally {
@@ -74,6 +81,8 @@ struct Bring {
     const float *dloss, *lse_in;
     const uint8_t *w;  // (classes, k)
     Span w_in;
+    uint8_t *wt;          // w's rows on 16 bytes, pitch ldxs, where they are not
+    unsigned row_blocks;  // blocks of rows; the ones behind them bring w's
     float *factors;    // dz's scale, and what undoes it
     float *share;      // per row, see below
     uint8_t *xw;       // share * x, where dW is wanted
@@ -206,6 +215,16 @@ template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kBringThreads) xent_bring_kernel(const Bring b) {
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (!WHOLE && blockIdx.x >= b.row_blocks) {
+        const int64_t r = (int64_t)(blockIdx.x - b.row_blocks) * kBringRows + warp, row_bytes = b.k * 2;
+        if (r >= b.classes) return;
+        const uint8_t *from = b.w + r * row_bytes;
+        uint8_t *to = b.wt + r * b.ldxs;
+#pragma unroll 4
+        for (int64_t c = lane * 16; c < row_bytes; c += 32 * 16)
+            *reinterpret_cast<uint4 *>(to + c) = load_piece<false>(from + c, (int)min((int64_t)16, row_bytes - c), b.w_in);
+        return;
+    }
     const int64_t r0 = (int64_t)blockIdx.x * kBringRows, share0 = r0 / kShareRows * kShareRows;
     Totals t{0, 0, 0, 0.f};
     if (b.tally) {
@@ -588,15 +607,19 @@ cudaError_t start(const XentShape &sh, const void *x, int64_t ldx, const void *w
     const bool whole = rows16(x, ldx) && sh.k % 8 == 0;
     const auto bring = sh.bf16 ? (whole ? xent_bring_kernel<__nv_bfloat16, true> : xent_bring_kernel<__nv_bfloat16, false>)
                                : (whole ? xent_bring_kernel<__half, true> : xent_bring_kernel<__half, false>);
-    if (e == cudaSuccess)
-        e = launch_kernel(true, bring, dim3((unsigned)((sh.m + kBringRows - 1) / kBringRows)), dim3(kBringThreads), 0, s, b);
     out.w = w;
     out.ldw = sh.k;
-    if (e == cudaSuccess && sh.k % 8 != 0) {
-        out.w = ws + L.off_w;
+    b.row_blocks = (unsigned)((sh.m + kBringRows - 1) / kBringRows);
+    unsigned blocks = b.row_blocks;
+    if (sh.k % 8 != 0) {
+        out.w = b.wt = ws + L.off_w;
         out.ldw = ldxs;
-        e = launch_align(w, sh.k, sh.n, sh.k, ws + L.off_w, s);
+        if (sh.n * sh.k <= kAlignHere)
+            blocks += (unsigned)((sh.n + kBringRows - 1) / kBringRows);
+        else if (e == cudaSuccess)
+            e = launch_align(w, sh.k, sh.n, sh.k, ws + L.off_w, s);
     }
+    if (e == cudaSuccess) e = launch_kernel(true, bring, dim3(blocks), dim3(kBringThreads), 0, s, b);
     out.xs = b.xs;
     out.ldxs = ldxs;
     out.offsets = b.offsets;

@@ -117,6 +117,14 @@ def test_several_pieces_of_the_classes(gpu_lib, dtype):
     check_grad(gpu_lib, dloss, x, w, labels)
 
 
+@pytest.mark.parametrize("m", [24, 70])
+def test_a_large_class_matrix_off_16_bytes(gpu_lib, m):
+    """34000 x 1001 values are brought to 16 bytes by a kernel of their own."""
+    x, w, labels, dloss = draw(m, 34000, 1001, torch.bfloat16, 8, 0.1)
+    check_forward(gpu_lib, x, w, labels)
+    check_grad(gpu_lib, dloss, x, w, labels)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_more_rows_than_an_accumulator_takes(gpu_lib, dtype):
     x, w, labels, dloss = draw(70000, 40, 24, dtype, 6, 0.3)
