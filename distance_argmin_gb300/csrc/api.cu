@@ -631,7 +631,7 @@ const char *kmeans_build_info(void) {
            "sharded update = per-rank sums reduced in rank order; k-means++ = Philox4x32-10 greedy D^2 with "
            "triangle-inequality row pruning (single GPU; sharded steps without); experts = one-cluster stable sort, "
            "16-byte row movers, tcgen05 cta_group::2 products of 256 features x 64 to 256 rows (BK 64), "
-           "mma.sync product for few rows; gate = a warp per token, near sums in float64; layer norm = rows of 16-byte "
+           "mma.sync product for few rows; gate = a warp per token, near sums in pairs of floats, then float64; layer norm = rows of 16-byte "
            "words, ahead in shared memory; cross entropy = the same products with log-sum and softmax epilogues";
 }
 
