@@ -498,7 +498,7 @@ cudaError_t weights_product(const LinearShape &sh, const Product16 &g, const Lin
 // take 73 us, in one 66; 1024 of 32768, k = 2048 256 and 257.)
 int rows_splits(int64_t m, int64_t piece, int64_t k) {
     const int64_t units = (m + 255) / 256 * ((k + lt::BP - 1) / lt::BP);
-    if (3 * units > kPairs) return 1;
+    if (units == 0 || 3 * units > kPairs) return 1;  // (no rows: nothing to split)
     return (int)std::max((int64_t)1, std::min(kPairs / units, piece / 512));
 }
 

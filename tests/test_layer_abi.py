@@ -136,3 +136,14 @@ def test_the_binding_refuses_what_is_not_on_the_gpu(km):
                  lambda: km.cross_entropy_workspace(km.OP_CROSS_ENTROPY, 4, 0, 8, device="cpu")):
         with pytest.raises(km.KMeansError):
             call()
+
+
+@pytest.mark.parametrize("n,k", [(1, 1), (1000, 64), (131072, 515)])
+def test_a_batch_of_no_rows_has_workspaces_and_a_gradient(km, n, k):
+    lib = km.load()
+    need, need_g = (lib.kmeans_cross_entropy_workspace_bytes(g, 0, n, k) for g in (0, 1))
+    assert 0 < need <= need_g
+    # the sizes are worked out before the workspace is refused, and nothing is enqueued
+    a = [None, k, None, 2, None, 8]
+    for wsb in (0, need_g - 1):
+        assert lib.kmeans_cross_entropy_grad(None, *a, None, 1.0, 0, n, k, F, F, W, wsb, None) == km.KMEANS_ERR_WORKSPACE
