@@ -117,7 +117,10 @@ struct Scores {
 
 // How near two values of the order may be in float32 without being looked at
 // further: twice what they may be off by, which is a score's error, no more than
-// the largest score's, and half a last bit of each sum with the bias.
+// the largest score's, and half a last bit of each sum with the bias.  A group's
+// score is the sum of two such values, which may be far larger than it where their
+// biases cancel: `parts`, the sum of both magnitudes (the largest of any group's),
+// is what its roundings go by, half a last bit of each part and of the sum.
 struct Gap {
     float score;
     __device__ __forceinline__ Gap(const GateArgs &p, const Scores<float> &sc)
@@ -125,6 +128,7 @@ struct Gap {
     __device__ __forceinline__ float operator()(float a, float b) const {
         return score + 0x1p-23f * (fabsf(a) + fabsf(b));
     }
+    __device__ __forceinline__ float of_groups(float parts) const { return 2.f * score + 0x1p-22f * parts; }
 };
 
 __device__ __forceinline__ float score_of(const Scores<float> &s, float l) {
@@ -462,8 +466,12 @@ __device__ __noinline__ bool near_values(const GateArgs &p, Logits row, int lane
     return true;
 }
 
-// Whether such values' order may be another one than that of the exact ones.
-__device__ __forceinline__ bool nearer(double a, double b) { return !(fabs(a - b) > 0x1p-38 + 0x1p-50 * fabs(a)); }
+// Whether the order of such values, or of sums of two of them, may be another one
+// than that of the exact ones; `size`: the magnitude that their roundings go by.
+__device__ __forceinline__ bool nearer(double a, double b, double size) {
+    return !(fabs(a - b) > 0x1p-38 + 0x1p-50 * size);
+}
+__device__ __forceinline__ bool nearer(double a, double b) { return nearer(a, b, fabs(a)); }
 
 // What the candidates' order goes by, in float64.
 __device__ __noinline__ void exact_values(const GateArgs &p, Logits row, int lane, Candidates &list, int count) {
@@ -494,10 +502,11 @@ __device__ __noinline__ int settle_pairs(const GateArgs &p, Logits row, int lane
 
 // The groups that stay, of those (lane g: group g) with a bit in `near`, whose two
 // largest values are among the candidates (their keys: the groups).  EXACT: in float64; else kAll where one
-// that stays is near one that does not (which all 32 cannot: they are left out of).
+// that stays is near one that does not (which all 32 cannot: they are left out of);
+// `parts`: see Gap.
 template <bool EXACT>
 __device__ __noinline__ uint32_t refine_groups(const GateArgs &p, int lane, const Candidates &list, int count,
-                                               uint32_t near, int wanted) {
+                                               uint32_t near, int wanted, float parts) {
     double one = -INFINITY, two = -INFINITY;
     for (int i = 0; i < count; ++i) {
         if ((int)list.found[i].key != lane) continue;
@@ -520,7 +529,7 @@ __device__ __noinline__ uint32_t refine_groups(const GateArgs &p, int lane, cons
         const uint32_t next = __ballot_sync(kAll, (near >> lane & 1u) && rank == wanted);
         if (last && next) {
             const double a = __shfl_sync(kAll, score, __ffs(last) - 1), b = __shfl_sync(kAll, score, __ffs(next) - 1);
-            if (nearer(a, b)) return kAll;
+            if (nearer(a, b, parts)) return kAll;
         }
     }
     return kept;
@@ -556,6 +565,11 @@ __device__ __noinline__ int refine_order(const GateArgs &p, const Logits row, in
 }
 
 __device__ __forceinline__ float group_total(float one, float two) { return two == -INFINITY ? one : one + two; }
+
+// Both parts' magnitudes; an infinite sum's order needs no such care.
+__device__ __forceinline__ float group_parts(float one, float two) {
+    return isfinite(group_total(one, two)) ? fabsf(one) + (two == -INFINITY ? 0.f : fabsf(two)) : 0.f;
+}
 
 // The two largest of two pairs.
 __device__ __forceinline__ void merge_two(float &one, float &two, float other_one, float other_two) {
@@ -616,6 +630,7 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
     for (int i = 0; i < PER; ++i) f[i] = f[i] != f[i] ? INFINITY : f[i];
     if (SUMS && p.groups > 1) {
         float total = -INFINITY, second = -INFINITY;  // lane g: group g's score, its second largest value
+        float parts = 0.f;                            // of a group that the lane has seen
         bool mine[PER];
         if (p.lanes_per_group > 0) {  // whole lanes, a power of two of them
             float one = -INFINITY, two = -INFINITY;
@@ -623,6 +638,7 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
             for (int i = 0; i < PER; ++i) merge_two(one, two, f[i], -INFINITY);
             for (int o = 1; o < p.lanes_per_group; o <<= 1)
                 merge_two(one, two, __shfl_xor_sync(kAll, one, o), __shfl_xor_sync(kAll, two, o));
+            parts = group_parts(one, two);
             const int from = (lane * p.lanes_per_group) & 31;
             total = __shfl_sync(kAll, group_total(one, two), from);
             second = __shfl_sync(kAll, two, from);
@@ -638,6 +654,7 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
                 if (lane == g) {
                     total = group_total(one, two);
                     second = two;
+                    parts = group_parts(one, two);
                 }
             }
         }
@@ -653,7 +670,10 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
             if (lane == g) key = 0;
         }
         if (next != 0 && last != 0) {
-            const float in = key_value(last), out = key_value(next), gap = 2.f * gap_of(in, out);
+            const float in = key_value(last), out = key_value(next);
+            // (not negative, so the bits' order is the values')
+            parts = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(parts)));
+            const float gap = gap_of.of_groups(parts);
             if (!(in - out > gap)) {
                 // Near (equal sums are rarely sums of equal parts, so they are looked
                 // at too): what is further above the first left out than float32 may
@@ -675,16 +695,16 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
                         left = p.group_size;
                     }
                 }
-                // (infinite sums have no order in float32)
-                if (count > kNear || !isfinite(in) || !isfinite(out)) return choose_exact(p, row, lane);
+                // (infinite sums have no order in float32, nor have sums whose parts are past it)
+                if (count > kNear || !isfinite(in) || !isfinite(out) || !isfinite(gap)) return choose_exact(p, row, lane);
                 __syncwarp();
                 const int wanted = p.topk_groups - __popc(sure);
                 uint32_t some = kAll;
                 if (near_values(p, row, lane, list, count))
-                    some = refine_groups<false>(p, lane, list, count, near, wanted);
+                    some = refine_groups<false>(p, lane, list, count, near, wanted, parts);
                 if (some == kAll) {
                     exact_values(p, row, lane, list, count);
-                    some = refine_groups<true>(p, lane, list, count, near, wanted);
+                    some = refine_groups<true>(p, lane, list, count, near, wanted, parts);
                 }
                 kept = sure | some;
             }
