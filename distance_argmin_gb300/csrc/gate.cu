@@ -291,11 +291,10 @@ __device__ __noinline__ int choose_exact(const GateArgs &p, Logits row, int lane
 #pragma unroll 1
     for (int i = 0; i < per; ++i) {
         const int e = i * 32 + lane;
-        const float l = e < p.n_experts ? row[e] : -INFINITY;
+        const float l = e < p.n_experts ? row[e] : -INFINITY, b = p.bias && e < p.n_experts ? p.bias[e] : 0.f;
         key[i] = 0;
-        if (l != -INFINITY)
-            key[i] = p.bias || p.groups > 1 ? choice_key(score_of(sc, l) + (p.bias ? (double)p.bias[e] : 0.0))
-                                            : choice_key((double)l);
+        if (l != -INFINITY && b != -INFINITY)
+            key[i] = p.bias || p.groups > 1 ? choice_key(score_of(sc, l) + (double)b) : choice_key((double)l);
     }
     uint64_t best;
     if (p.groups > 1) {
@@ -622,7 +621,8 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
 #pragma unroll
             for (int j = 0; j < RUN; ++j) {
                 const float c = score_of(sc, f[i + j]) + b[j];
-                f[i + j] = f[i + j] == -INFINITY ? f[i + j] : c;
+                // (closed by the bias, too, where the score is NaN)
+                f[i + j] = f[i + j] == -INFINITY || b[j] == -INFINITY ? -INFINITY : c;
             }
         }
     }

@@ -580,7 +580,7 @@ enum { KMEANS_GATE_SOFTMAX = 0, KMEANS_GATE_SIGMOID = 1 };
  * weights know of `renormalize` and `scale`, only the choice of the bias.
  * The order is that of exact arithmetic (without a bias, the logits' own; with
  * one, that of values in float64).  NaN counts as infinity, and a token that
- * holds one has it in its weights.
+ * holds one has it in its weights; an expert that its bias closes stays closed.
  * topk <= n_experts <= KMEANS_ROUTE_MAX_EXPERTS, topk <= KMEANS_ROUTE_MAX_TOPK,
  * groups <= KMEANS_GATE_MAX_GROUPS divides n_experts, topk_groups <= groups. */
 int kmeans_gate(const void *logits, int64_t ldl, int dtype, int scores, const float *bias, int64_t n,

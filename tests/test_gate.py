@@ -331,3 +331,23 @@ def test_rows_of_many_equal_logits(gpu_lib, kind, biased, E, groups):
         assert np.array_equal(np.sort(got, 1), np.sort(np.take_along_axis(z.numpy(), want, 1), 1))
     else:
         assert np.array_equal(ids.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(50, 1), (50, 5), (200, 1), (200, 8), (1000, 4)])
+def test_an_expert_that_its_bias_closes_stays_closed_beside_a_nan(gpu_lib, kind, E, groups):
+    """A softmax with a NaN (or an infinity) in it is NaN throughout: the open experts count as infinite then, the
+    closed ones as closed."""
+    z = draw(6, E, torch.float32, 3)
+    bias = torch.linspace(-0.1, 0.1, E)
+    closed = torch.arange(E) % 5 == 1
+    bias[closed] = -math.inf
+    z[2, 7], z[3, 6], z[4, 12] = math.nan, math.nan, math.inf  # (expert 6 is one of the closed)
+    z[5, 11] = math.inf  # (and so is 11)
+    ids, w = gpu_lib.kmeans_gate(z.cuda(), 6, scores=kind, bias=bias.cuda(), groups=groups, topk_groups=max(1, groups // 2))
+    assert bool((ids >= 0).all()) and not bool(closed[ids.cpu().long()].any())
+    for row in ids.tolist():
+        assert len(set(row)) == 6
+    clean, _ = gpu_lib.kmeans_gate(z[:2].cuda(), 6, scores=kind, bias=bias.cuda(), groups=groups,
+                                   topk_groups=max(1, groups // 2))
+    assert torch.equal(ids[:2], clean)
