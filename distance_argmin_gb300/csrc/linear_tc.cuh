@@ -467,9 +467,11 @@ __device__ __forceinline__ int sum_logits(float (&v)[COLS], uint32_t acc, uint32
 }
 
 // Log sum: a lane has a row and `count` classes of it: the largest factor * z and
-// the sum of the exponentials about it, in powers of two.  A row whose largest is
-// infinite keeps the reference 0, so that the sum says what it is (0, infinite or
-// NaN); no classes leave (-inf, 0).  `label`: the row's, from the first class on.
+// the sum of the exponentials about it, in powers of two.  Where the largest is
+// infinite they are taken about 0, so that the sum says what it is (0, infinite or
+// NaN), and where it is minus infinity (closed classes, or none) that is the
+// reference that leaves: (-inf, 0) counts for nothing beside other parts, however
+// small their logits.  `label`: the row's, from the first class on.
 template <int COLS>
 __device__ __forceinline__ void log_sum(const EntropyArgs &g, float (&v)[COLS], int count, int64_t row, bool mine,
                                         int label, int part) {
@@ -495,7 +497,7 @@ __device__ __forceinline__ void log_sum(const EntropyArgs &g, float (&v)[COLS], 
         const float2 x = __ffma2_rn(make_float2(v[j], v[j + 1]), both(g.factor), both(-ref));
         sum = __fadd2_rn(sum, make_float2(exp2_approx(x.x), exp2_approx(x.y)));
     }
-    if (mine) g.stats[part * g.pitch + row] = make_float2(count > 0 ? ref : -INFINITY, sum.x + sum.y);
+    if (mine) g.stats[part * g.pitch + row] = make_float2(top == -INFINITY ? top : ref, sum.x + sum.y);
 }
 
 // The same of few rows: a lane has a class, v[j] is row q0 + j (of `count`), and the
@@ -519,7 +521,7 @@ __device__ __forceinline__ void log_sum_few(const LinearTcParams &p, const float
         float sum = real ? exp2_approx(fmaf(z, g.factor, -ref)) : 0.f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == j) mine = make_float2(ref, sum);
+        if (lane == j) mine = make_float2(top == -INFINITY ? top : ref, sum);
     }
     if (lane < count) g.stats[(q0 + lane) * g.pitch + (f >> 5)] = mine;
 }

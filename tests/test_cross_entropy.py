@@ -268,3 +268,41 @@ def test_a_starved_pipeline_is_reported_and_the_next_call_works(gpu_lib, monkeyp
     got = gpu_lib.kmeans_cross_entropy(x, w, labels, ws=ws)
     assert gpu_lib.kmeans_device_status(ws) == gpu_lib.KMEANS_OK
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m", [5, 64, 300])
+@pytest.mark.parametrize("first", [0, 128, 576])
+def test_closed_classes_and_open_ones_far_below_zero(gpu_lib, m, first, dtype):
+    """256 neighbouring classes closed by a weight of -inf (more than any part of the classes whose sums are formed
+    together), the others' logits near -200: the reference of the closed parts must not count."""
+    n, k = 1000, 48
+    x, w, labels, _ = draw(m, n, k, dtype, 21)
+    x[:, 0], x[:, 1] = 1.0, 1.0
+    w[:, 0], w[:, 1] = 0.0, -200.0
+    open_ = torch.ones(n, dtype=torch.bool, device="cuda")
+    open_[first:first + 256] = False
+    w[~open_, 0] = -math.inf
+    labels = open_.nonzero()[:, 0][labels % int(open_.sum())]
+    loss, lse = gpu_lib.kmeans_cross_entropy(x, w, labels)
+    z, _, _, cut = plain(x, w[open_], labels % int(open_.sum()), 1.0)  # (the label's own logit is taken below)
+    want_lse = torch.logsumexp(z, 1)
+    want = want_lse - (x.double() * w[labels].double()).sum(1)
+    off = cut + 2.0 ** -21 + z.abs().amax(1) * 2.0 ** -22
+    assert bool(((lse.double() - want_lse).abs() <= off).all())
+    assert bool(((loss.double() - want).abs() <= 2 * off).all())
+
+
+@pytest.mark.parametrize("m", [5, 300])
+def test_a_closed_label_and_no_open_class(gpu_lib, m):
+    x, w, labels, _ = draw(m, 700, 16, torch.bfloat16, 22)
+    x[:, 0] = 1.0
+    w[:, 0] = 0.0
+    w[labels[0], 0] = -math.inf
+    loss, lse = gpu_lib.kmeans_cross_entropy(x, w, labels)
+    gone = labels == labels[0]
+    assert bool(torch.isinf(loss[gone]).all()) and bool((loss[gone] > 0).all())
+    assert bool(torch.isfinite(lse).all()) and bool(torch.isfinite(loss[~gone]).all())
+    w[:, 0] = -math.inf
+    loss, lse = gpu_lib.kmeans_cross_entropy(x, w, labels)
+    assert bool((lse == -math.inf).all()) and bool(loss.isnan().all())
