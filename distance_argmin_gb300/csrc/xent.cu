@@ -54,7 +54,7 @@ constexpr int64_t kCountHere = 4096;
 constexpr int64_t kAlignHere = (int64_t)1 << 25;
 
 // Of kShareRows rows: how many count (and then: before them), whether a label is
-// past the classes, and the largest gradient's magnitude.
+// past the classes, and the largest finite gradient's magnitude, dloss * scale.
 struct alignas(16) Tally {
     int32_t count, bad;
     float top;
@@ -94,6 +94,12 @@ __device__ __forceinline__ int64_t label_of(const Bring &b, int64_t r) {
     return b.id_bytes == 8 ? static_cast<const int64_t *>(b.labels)[r] : (int64_t)static_cast<const int32_t *>(b.labels)[r];
 }
 
+// (A row whose gradient is not finite has no say in what float16 keeps of the others.)
+__device__ __forceinline__ float larger_gradient(const Bring &b, float top, int64_t r) {
+    const float g = fabsf(b.dloss[r] * b.scale);
+    return isfinite(g) ? fmaxf(top, g) : top;
+}
+
 __device__ __forceinline__ float warp_max(float v) {  // of what is not negative, and never NaN
     return __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(v)));
 }
@@ -111,7 +117,7 @@ __global__ void __launch_bounds__(kBringThreads) xent_tally_kernel(const Bring b
         const bool real = l >= 0 && l < b.classes;
         t.count += __popc(__ballot_sync(kAll, real));
         t.bad |= __any_sync(kAll, l >= b.classes);
-        if (b.dloss && real) t.top = fmaxf(t.top, fabsf(b.dloss[r]));
+        if (b.dloss && real) t.top = larger_gradient(b, t.top, r);
     }
     t.top = warp_max(t.top);
     if (lane == 0) tally[share] = t;
@@ -194,7 +200,7 @@ __device__ __forceinline__ Totals block_totals(Totals t) {
 // twice their magnitude at most, and float16 then keeps probabilities down to
 // 2^-28 of it in full.  (bfloat16 has float32's range.)
 __device__ __forceinline__ int scale_exponent(float top) {
-    if (!(top > 0.f) || isinf(top)) return 0;
+    if (!(top > 0.f)) return 0;
     return max(-126, min(126, 13 - ilogbf(top)));
 }
 
@@ -237,11 +243,11 @@ __global__ void __launch_bounds__(kBringThreads) xent_bring_kernel(const Bring b
             t.all += real;
             if (r < share0) t.before += real;
             t.bad |= l >= b.classes;
-            if (b.dloss && real) t.top = fmaxf(t.top, fabsf(b.dloss[r]));
+            if (b.dloss && real) t.top = larger_gradient(b, t.top, r);
         }
         t = block_totals(t);
     }
-    const int exponent = b.narrow ? scale_exponent(t.top * b.scale) : 0;
+    const int exponent = b.narrow ? scale_exponent(t.top) : 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         b.offsets[0] = 0;
         b.offsets[1] = t.all;

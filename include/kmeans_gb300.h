@@ -647,8 +647,8 @@ int kmeans_cross_entropy(const void *x, int64_t ldx, const void *w, int dtype, c
  * lse as kmeans_cross_entropy wrote it for the same x, w and labels.  dx (m, k)
  * and dw (n, k) may each be NULL; dx is zero in rows that do not count.  The
  * products take dz in the matrices' type (float16: times a power of two that
- * brings the largest dloss * scale to 2^13, so that terms down to 2^-28 of it
- * keep their digits) and, for dw, each row of x times a factor in [1/2, 1),
+ * brings the largest finite dloss * scale to 2^13, so that terms down to 2^-28 of
+ * it keep their digits) and, for dw, each row of x times a factor in [1/2, 1),
  * rounded to that type, which leaves the label's term of dz a power of two.
  * dx and dw must not alias an input. */
 int kmeans_cross_entropy_grad(const float *dloss, const void *x, int64_t ldx, const void *w, int dtype,

@@ -306,3 +306,19 @@ def test_a_closed_label_and_no_open_class(gpu_lib, m):
     w[:, 0] = -math.inf
     loss, lse = gpu_lib.kmeans_cross_entropy(x, w, labels)
     assert bool((lse == -math.inf).all()) and bool(loss.isnan().all())
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("m", [60, 5000])
+def test_a_gradient_that_is_not_finite_keeps_to_its_row_of_dx(gpu_lib, m, bad):
+    """float16's power of two goes by the largest finite gradient: the other rows' dx stays what it was, to the bit."""
+    x, w, labels, dloss = draw(m, 2000, 64, torch.float16, 13)
+    _, lse = gpu_lib.kmeans_cross_entropy(x, w, labels)
+    top = int(dloss.argmax())
+    row = (top + m // 2) % m
+    clean, _ = gpu_lib.kmeans_cross_entropy_grad(dloss, x, w, labels, lse)
+    dloss[row] = bad
+    dx, _ = gpu_lib.kmeans_cross_entropy_grad(dloss, x, w, labels, lse)
+    keep = torch.ones(m, dtype=torch.bool, device="cuda")
+    keep[row] = False
+    assert torch.equal(dx[keep], clean[keep]) and not bool(torch.isfinite(dx[row]).any())
