@@ -133,7 +133,8 @@ def block_forward(x, gate_w, w1, w2, topk, norm_weight=None, norm_bias=None, b1=
     y, saved = experts_forward(h, ids, w1, w2, b1, b2, weights=weights, residual=x, activation=activation, keep=keep)
     if keep:
         saved.__dict__.update(x=x, normed=h, mean=mean, rstd=rstd, logits=logits, ids=ids, how=dict(
-            scores=scores, renormalize=renormalize, scale=scale))
+            scores=scores, renormalize=renormalize, scale=scale), has_norm_weight=norm_weight is not None,
+            has_norm_bias=norm_bias is not None)
     return y, saved
 
 
@@ -141,9 +142,11 @@ def block_forward(x, gate_w, w1, w2, topk, norm_weight=None, norm_bias=None, b1=
 def block_backward(dy, saved, gate_w, w1, w2, norm_weight=None):
     """Gradients of block_forward -> dict with ``x``, ``gate_w``, ``w1``, ``b1``,
     ``w2``, ``b2``, ``norm_weight`` and ``norm_bias`` (None where the forward
-    pass had none; the norm's by ``norm_weight``)."""
+    pass had none).  ``norm_weight``: the forward pass's, if it had one."""
     km = _km()
     s = saved
+    if (norm_weight is not None) != s.has_norm_weight:
+        raise ValueError("norm_weight must be given where block_forward had one, and only there")
     dys, dweights = km.kmeans_route_combine_grad(dy, s.ys, s.rows, s.offsets, s.weights)
     dlogits = km.kmeans_gate_grad(dweights, s.logits, s.ids, **s.how)
     dh, dgate_w, _ = km.kmeans_linear_grad(dlogits, s.normed, gate_w, need_db=False)
@@ -152,8 +155,7 @@ def block_backward(dy, saved, gate_w, w1, w2, norm_weight=None):
                                           need_db=s.has_b1)
     # the experts' way back to the tokens takes the gate's along
     dh = km.kmeans_route_combine(dxs, s.rows, s.offsets, residual=dh)
-    affine = norm_weight is not None
     dx, dnorm_weight, dnorm_bias = km.kmeans_layernorm_grad(dh, s.x, s.mean, s.rstd, weight=norm_weight, residual=dy,
-                                                            need_dweight=affine, need_dbias=affine)
+                                                            need_dweight=s.has_norm_weight, need_dbias=s.has_norm_bias)
     return {"x": dx, "gate_w": dgate_w, "w1": dw1, "b1": db1, "w2": dw2, "b2": db2, "norm_weight": dnorm_weight,
             "norm_bias": dnorm_bias}

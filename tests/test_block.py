@@ -113,3 +113,36 @@ def test_the_example_runs(gpu_lib):
     import gated_block
     losses, served = gated_block.main(steps=6, n=512, d=64, hidden=96, classes=300)
     assert len(losses) == 6 and all(v == v and v >= 0 for v in losses) and served == served
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_norm_with_a_bias_alone_or_a_weight_alone(gpu_lib, dtype):
+    """The same as with the other one given as ones, or zeros."""
+    from distance_argmin_gb300 import experts
+    x, gw = normal((60, 64), dtype, 1), normal((4, 64), dtype, 2, 0.125)
+    w1, w2 = normal((4, 96, 64), dtype, 3, 0.125), normal((4, 64, 96), dtype, 4, 0.1)
+    weight, bias, dy = normal((64,), dtype, 5, 0.1, 1.0), normal((64,), dtype, 6, 0.1), normal((60, 64), dtype, 7)
+    ones, zeros = torch.ones_like(weight), torch.zeros_like(bias)
+
+    def both(norm_weight, norm_bias):
+        y, saved = experts.block_forward(x, gw, w1, w2, 2, norm_weight, norm_bias, keep=True)
+        return y, experts.block_backward(dy, saved, gw, w1, w2, norm_weight)
+
+    for given, full, name in (((None, bias), (ones, bias), "norm_bias"), ((weight, None), (weight, zeros), "norm_weight")):
+        (y, got), (want_y, want) = both(*given), both(*full)
+        other = {"norm_bias": "norm_weight", "norm_weight": "norm_bias"}[name]
+        assert torch.equal(y, want_y) and got[other] is None and got[name] is not None
+        for key in ("x", "gate_w", "w1", "w2", name):
+            assert torch.equal(got[key], want[key]), key
+
+
+def test_a_norm_weight_that_the_forward_pass_did_not_have_is_refused(gpu_lib):
+    from distance_argmin_gb300 import experts
+    x, gw = normal((8, 64), torch.bfloat16, 1), normal((4, 64), torch.bfloat16, 2, 0.125)
+    w1, w2 = normal((4, 32, 64), torch.bfloat16, 3, 0.125), normal((4, 64, 32), torch.bfloat16, 4, 0.1)
+    weight = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    _, without = experts.block_forward(x, gw, w1, w2, 2, keep=True)
+    _, having = experts.block_forward(x, gw, w1, w2, 2, weight, keep=True)
+    for saved, norm_weight in ((without, weight), (having, None)):
+        with pytest.raises(ValueError, match="norm_weight"):
+            experts.block_backward(x, saved, gw, w1, w2, norm_weight)
