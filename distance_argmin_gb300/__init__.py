@@ -1260,7 +1260,8 @@ def kmeans_layernorm_grad(dy, x, mean, rstd, weight=None, residual=None, need_dx
 def cross_entropy_workspace(op: int, m: int, n: int, k: int, device=None):
     """A device workspace for ``kmeans_cross_entropy`` (OP_CROSS_ENTROPY) or
     ``kmeans_cross_entropy_grad`` (OP_CROSS_ENTROPY_GRAD, enough for both) of m
-    rows, n classes and k features (uint8 tensor)."""
+    rows, n classes and k features (uint8 tensor).  Fewer rows may need a larger
+    one."""
     nbytes = int(load().kmeans_cross_entropy_workspace_bytes(op, m, n, k))
     if nbytes == 0:
         raise KMeansError(KMEANS_ERR_INVALID_ARG, "kmeans_cross_entropy_workspace_bytes")

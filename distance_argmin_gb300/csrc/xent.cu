@@ -6,8 +6,8 @@
 // that the products see only them: ignored rows cost nothing, and whatever they
 // hold reaches no result.
 // Forward: the product (log sum, see linear_tc.cuh) leaves each row's largest
-// logit and sum of exponentials per 64 classes (few rows: 32), which the join
-// kernels bring together.  Gradient: piece by piece of the classes dz is formed from
+// logit and sum of exponentials per 16 to 64 classes (a quarter of a unit's; few
+// rows: 32), which the join kernels bring together.  Gradient: piece by piece of the classes dz is formed from
 // the logits once more, in 16 bits, and goes into both products while it is near;
 // dx is added up in float32 from piece to piece.
 //
@@ -522,9 +522,9 @@ int64_t class_parts(int64_t m, int64_t n) {
 
 }  // namespace
 
-// Classes of a piece: about 2^28 values of dz (half a gigabyte), at least 2048 so
-// that dx's sums are read and written rarely, at most one accumulator's terms; all
-// pieces about equal.  (Gradient of 8192 rows of 32768 classes, k = 2048: 1.78 to
+// Classes of a piece: about 2^28 values of dz (half a gigabyte), at least 2048
+// (more than 2^28 values from 2^17 rows on) so that dx's sums are read and written
+// rarely, at most one accumulator's terms; all pieces about equal.  (Gradient of 8192 rows of 32768 classes, k = 2048: 1.78 to
 // 1.86 ms in one piece, 2.00 in four, 2.11 in eight; 24 of 131072, k = 4096: 629 us
 // in four, 896 in sixteen.)
 int64_t xent_piece(int64_t m, int64_t n) {

@@ -622,8 +622,10 @@ int kmeans_layernorm_grad(const void *dy, int64_t lddy, const void *x, int64_t l
 /* Workspace of kmeans_cross_entropy (grad = 0) and kmeans_cross_entropy_grad
  * (grad = 1, enough for both) for m rows, n classes and k features (0 when the
  * sizes are invalid).  It holds no m * n logits: the forward call keeps 8 bytes
- * per 64 classes of a row, the gradient a piece of the classes at a time, of
- * about 2^28 values. */
+ * per 16 to 64 classes of a row, the gradient a piece of the classes at a time,
+ * of about 2^28 values or of 2048 classes where those are more, and dx's sums in
+ * float32.  Fewer rows may need more (their products are split further): a
+ * workspace for batches of several sizes has the largest of their sizes. */
 size_t kmeans_cross_entropy_workspace_bytes(int grad, int64_t m, int64_t n, int64_t k);
 
 /* Softmax cross entropy against classes: z = scale * x[r] w^T over the n

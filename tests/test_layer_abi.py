@@ -147,3 +147,22 @@ def test_a_batch_of_no_rows_has_workspaces_and_a_gradient(km, n, k):
     a = [None, k, None, 2, None, 8]
     for wsb in (0, need_g - 1):
         assert lib.kmeans_cross_entropy_grad(None, *a, None, 1.0, 0, n, k, F, F, W, wsb, None) == km.KMEANS_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("m", [1, 64, 65, 128, 1000, 8192, 2 ** 17, 2 ** 20])
+@pytest.mark.parametrize("n", [1, 257, 4096, 10007, 131072])
+@pytest.mark.parametrize("k", [64, 513, 4096])
+def test_the_cross_entropy_workspace_keeps_to_what_the_header_says(km, m, n, k):
+    lib = km.load()
+    forward, both = (lib.kmeans_cross_entropy_workspace_bytes(g, m, n, k) for g in (0, 1))
+    rows, wide = (m + 31) // 32 * 32, (k + 7) // 8 * 8
+    # 16 bytes a row and 4 for its label's logit, x once (and w, where it has to be brought to 16 bytes), 8 bytes per 16
+    # classes (a last unit of 64 has four parts, however few its classes); 16 KiB of status words and of space between
+    kept = 24 * m + 2 * m * wide + (2 * n * wide if k % 8 else 0) + (1 << 14)
+    assert 0 < forward <= kept + rows * (n / 16 + 4) * 8
+    # a piece is at most 8 classes more than n, 2^28 values or 2048 classes; dx's sums: a split product has at most 76
+    # units of 256 x 256, or 76 parts of one unit; dw's: one of m / 32768 chunks of a piece
+    piece = min(n + 8, 32768, max(2048, 2 ** 28 // m + 256))
+    sums = 4 * max(m, 256 * 76) * max(k, 256)
+    chunks = 4 * ((m + 32767) // 32768 if m > 32768 else 0) * piece * k
+    assert forward <= both <= max(kept + rows * (n / 16 + 4) * 8, kept + 2 * m * wide + 2 * m * piece + sums + chunks)
