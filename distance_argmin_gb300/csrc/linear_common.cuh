@@ -73,7 +73,6 @@ struct Product16 {
     void *db;                 // weights: the bias gradient, joined on the side from
     const float *bias_sums;   // the sums of `bias_rows` rows each (null: not here)
     int bias_rows;
-    EntropyArgs entropy;
 };
 
 // f applied with the activation as a compile-time constant: one branch around
