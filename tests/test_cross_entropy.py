@@ -322,3 +322,37 @@ def test_a_gradient_that_is_not_finite_keeps_to_its_row_of_dx(gpu_lib, m, bad):
     keep = torch.ones(m, dtype=torch.bool, device="cuda")
     keep[row] = False
     assert torch.equal(dx[keep], clean[keep]) and not bool(torch.isfinite(dx[row]).any())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(1, 500, 64), (24, 3000, 128), (70, 700, 72), (300, 2000, 64)])
+def test_the_label_term_of_dx_is_rounded_once(gpu_lib, m, n, k, dtype):
+    """A row's dz has one large term, its label's, whose rounding to 16 bits would be that of all of dx: it is a power
+    of two there, and dx is rounded once.  2^-b is allowed on the other terms alone; the label's is within what its
+    probability is (p rel / (1 - p)) and some float32 roundings.  A dz rounded as it stands is outside that."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m)
+    w = 0.05 * torch.randn(n, k, generator=g, device="cuda")
+    labels = torch.randperm(n, generator=g, device="cuda")[:m]
+    w[labels] *= 20.0
+    w = w.to(dtype)
+    x = (0.1 * torch.randn(m, k, generator=g, device="cuda")).to(dtype)
+    dloss = 1.0 + torch.rand(m, generator=g, device="cuda")
+    _, lse = gpu_lib.kmeans_cross_entropy(x, w, labels)
+    dx, _ = gpu_lib.kmeans_cross_entropy_grad(dloss, x, w, labels, lse, need_dw=False)
+    z, want_lse, _, cut = plain(x, w, labels, 1.0)
+    gd, wd = dloss.double()[:, None], w.double()
+    p = torch.exp(z - want_lse[:, None])
+    hot = torch.nn.functional.one_hot(labels, n).double()
+    dz = gd * (p - hot)
+    rel = (2 * cut + 2.0 ** -20 + z.abs().amax(1) * 2.0 ** -21)[:, None]
+    b = 2.0 ** -BITS[dtype]
+    others = gd * p * (1 - hot) * (rel + b * (1 + rel)) + (2.0 ** -38 * dloss.max().item() if dtype is torch.float16 else 0)
+    label = gd * hot * (p * rel + 2.0 ** -20 * (1 - p))
+    off = (others + label) @ wd.abs() + (CUT * n + 2.0 ** -20) * (dz.abs() @ wd.abs())
+    want = dz @ wd
+    bound = off + 1.01 * b * (want.abs() + off) + TINY[dtype]
+    assert bool(((dx.double() - want).abs() <= bound).all())
+    rounded = (dz.to(dtype).double() @ wd).to(dtype).double()
+    if m > 1:  # (one row's rounding may happen to be small)
+        assert bool(((rounded - want).abs() > bound).any())

@@ -351,3 +351,29 @@ def test_an_expert_that_its_bias_closes_stays_closed_beside_a_nan(gpu_lib, kind,
     clean, _ = gpu_lib.kmeans_gate(z[:2].cuda(), 6, scores=kind, bias=bias.cuda(), groups=groups,
                                    topk_groups=max(1, groups // 2))
     assert torch.equal(ids[:2], clean)
+
+
+@pytest.mark.parametrize("kind,reach", [("sigmoid", 12.0), ("sigmoid", 30.0), ("softmax", 6.0), ("softmax", 20.0)])
+@pytest.mark.parametrize("groups,topk_groups", [(1, 1), (6, 2)])
+def test_near_sums_of_logits_over_the_whole_range(gpu_lib, kind, reach, groups, topk_groups):
+    """As above with logits from one end of the exponential's range to the other: the pairs' exponential decides what
+    is 2^-38 apart or more."""
+    r = np.random.RandomState(int(reach))
+    n, E, topk = 1500, 48, 9
+    base = (reach * (2 * r.rand(E) - 1)).astype(np.float32)
+    bias = (0.5 - scores_of(base[None].astype(np.float64), kind)[0]).astype(np.float32)
+    z = (base * (1 + r.randint(-1, 2, (n, E)) * np.float32(2.0 ** -23))).astype(np.float32)
+    c = scores_of(z.astype(np.float64), kind) + bias
+    order = -np.sort(-c, 1)[:, :topk + 1]
+    clear = ((order[:, :-1] - order[:, 1:]) > 2.0 ** -48).all(1)
+    if groups > 1:
+        total = -np.sort(-np.sort(c.reshape(n, groups, -1), 2)[:, :, -2:].sum(2), 1)
+        clear &= total[:, topk_groups - 1] - total[:, topk_groups] > 2.0 ** -48
+        kept = np.sort(c.reshape(n, groups, -1), 2)[:, :, -2:].sum(2) >= total[:, topk_groups - 1:topk_groups]
+        order = -np.sort(-np.where(np.repeat(kept, E // groups, 1), c, -np.inf), 1)[:, :topk + 1]
+        clear &= ((order[:, :-1] - order[:, 1:]) > 2.0 ** -48).all(1)
+    assert clear.sum() > n // 2
+    ids, _ = gpu_lib.kmeans_gate(torch.from_numpy(z).cuda(), topk, scores=kind, bias=torch.from_numpy(bias).cuda(),
+                                 groups=groups, topk_groups=topk_groups)
+    want, _ = plain_gate(z.astype(np.float64), topk, kind, bias.astype(np.float64), groups, topk_groups)
+    assert np.array_equal(ids.cpu().numpy()[clear], want[clear])

@@ -196,3 +196,27 @@ def test_in_place(gpu_lib, d):
         a = {"dy": dy.clone(), "residual": res.clone()}
         got = gpu_lib.kmeans_layernorm_grad(a["dy"], x, mean, rstd, residual=a["residual"], dx=a[at])
         assert all(torch.equal(p, q) for p, q in zip(got, grads))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d", [(1, 2), (5, 33), (17, 64), (9, 1031), (40, 4096), (3, 8200), (2, 40000)])
+def test_no_eps_at_all(gpu_lib, n, d, dtype, monkeypatch):
+    import sys
+    monkeypatch.setattr(sys.modules[__name__], "EPS", 0.0)
+    x = normal((n, d), dtype, d)
+    check_forward(gpu_lib, x, normal((d,), dtype, 1, 0.3, 1.0), normal((d,), dtype, 2))
+    check_grad(gpu_lib, normal((n, d), dtype, d + 1), x, normal((d,), dtype, 1, 0.3, 1.0), None)
+
+
+@pytest.mark.parametrize("d", [8, 1024, 32768])
+def test_equal_values_without_eps_are_not_finite_in_their_row_alone(gpu_lib, d):
+    """0 / 0 by definition.  (Twos and a power of two of them: the mean is exact, and so is the variance.)"""
+    x = normal((7, d), torch.float32, 1)
+    clean = gpu_lib.kmeans_layernorm(x, eps=0.0, save_stats=True)
+    x[3] = 2.0
+    y, mean, rstd = gpu_lib.kmeans_layernorm(x, eps=0.0, save_stats=True)
+    keep = [r for r in range(7) if r != 3]
+    assert all(torch.equal(a[keep], b[keep]) for a, b in zip((y, mean, rstd), clean))
+    assert mean[3].item() == 2.0 and rstd[3].item() == float("inf") and bool(y[3].isnan().all())
+    dx, _, _ = gpu_lib.kmeans_layernorm_grad(x, x, mean, rstd, need_dweight=False, need_dbias=False)
+    assert bool(torch.isfinite(dx[keep]).all()) and not bool(torch.isfinite(dx[3]).any())
