@@ -122,8 +122,10 @@ def block_forward(x, gate_w, w1, w2, topk, norm_weight=None, norm_bias=None, b1=
         y = experts_forward(h, ids, w1, w2, .., weights, residual=x)
 
     x (n, d) float16 or bfloat16, the experts' matrices as for experts_forward
-    with d_out = d; ``gate_bias`` (n_experts,) float32 and the options from
-    ``scores`` to ``scale`` are kmeans_gate's.  ``keep``: hold what the gradient
+    with d_out = d (up to ``LINEAR_MAX_EXPERTS`` of them, fewer than the gate
+    alone takes); ``gate_bias`` (n_experts,) float32 and the options from
+    ``scores`` to ``scale`` are kmeans_gate's.  The router's logits are a
+    kmeans_linear's, in x's 16-bit type: the gate orders the rounded ones.  ``keep``: hold what the gradient
     needs in ``saved``, else None."""
     km = _km()
     h, mean, rstd = km.kmeans_layernorm(x, norm_weight, norm_bias, eps=eps, save_stats=keep)
