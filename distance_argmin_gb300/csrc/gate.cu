@@ -28,6 +28,7 @@
 // loaded once more, for their order), 12.4 without both.  An argmax over all lanes
 // and values for each choice took 68.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -119,8 +120,9 @@ struct Scores {
 // further: twice what they may be off by, which is a score's error, no more than
 // the largest score's, and half a last bit of each sum with the bias.  A group's
 // score is the sum of two such values, which may be far larger than it where their
-// biases cancel: `parts`, the sum of both magnitudes (the largest of any group's),
-// is what its roundings go by, half a last bit of each part and of the sum.
+// biases cancel: `of_group` is what it may be off by itself, half a last bit of each
+// part and of the sum, and 2^-16 of them for what this is off by.  (Infinite ones are
+// not off.)
 struct Gap {
     float score;
     __device__ __forceinline__ Gap(const GateArgs &p, const Scores<float> &sc)
@@ -128,7 +130,11 @@ struct Gap {
     __device__ __forceinline__ float operator()(float a, float b) const {
         return score + 0x1p-23f * (fabsf(a) + fabsf(b));
     }
-    __device__ __forceinline__ float of_groups(float parts) const { return 2.f * score + 0x1p-22f * parts; }
+    __device__ __forceinline__ float of_group(float one, float two) const {
+        constexpr float bit = 0x1.0001p-23f;
+        const float parts = bit * fabsf(one) + (two == -INFINITY ? 0.f : bit * fabsf(two));
+        return isfinite(parts) ? score + parts : 0.f;
+    }
 };
 
 __device__ __forceinline__ float score_of(const Scores<float> &s, float l) {
@@ -501,11 +507,10 @@ __device__ __noinline__ int settle_pairs(const GateArgs &p, Logits row, int lane
 
 // The groups that stay, of those (lane g: group g) with a bit in `near`, whose two
 // largest values are among the candidates (their keys: the groups).  EXACT: in float64; else kAll where one
-// that stays is near one that does not (which all 32 cannot: they are left out of);
-// `parts`: see Gap.
+// that stays is near one that does not (which all 32 cannot: they are left out of).
 template <bool EXACT>
 __device__ __noinline__ uint32_t refine_groups(const GateArgs &p, int lane, const Candidates &list, int count,
-                                               uint32_t near, int wanted, float parts) {
+                                               uint32_t near, int wanted) {
     double one = -INFINITY, two = -INFINITY;
     for (int i = 0; i < count; ++i) {
         if ((int)list.found[i].key != lane) continue;
@@ -528,7 +533,10 @@ __device__ __noinline__ uint32_t refine_groups(const GateArgs &p, int lane, cons
         const uint32_t next = __ballot_sync(kAll, (near >> lane & 1u) && rank == wanted);
         if (last && next) {
             const double a = __shfl_sync(kAll, score, __ffs(last) - 1), b = __shfl_sync(kAll, score, __ffs(next) - 1);
-            if (nearer(a, b, parts)) return kAll;
+            // (the parts' magnitudes, not negative: their bits' order is the values')
+            const float parts = (float)(fabs(one) + (two == -INFINITY ? 0.0 : fabs(two)));
+            const float most = __uint_as_float(__reduce_max_sync(kAll, near >> lane & 1u ? __float_as_uint(parts) : 0u));
+            if (nearer(a, b, most)) return kAll;
         }
     }
     return kept;
@@ -563,11 +571,9 @@ __device__ __noinline__ int refine_order(const GateArgs &p, const Logits row, in
     return chosen;
 }
 
-__device__ __forceinline__ float group_total(float one, float two) { return two == -INFINITY ? one : one + two; }
-
-// Both parts' magnitudes; an infinite sum's order needs no such care.
-__device__ __forceinline__ float group_parts(float one, float two) {
-    return isfinite(group_total(one, two)) ? fabsf(one) + (two == -INFINITY ? 0.f : fabsf(two)) : 0.f;
+// (A sum past float32's range is not infinite; below it, it may still be wanted.)
+__device__ __forceinline__ float group_total(float one, float two) {
+    return two == -INFINITY || one == INFINITY ? one : fminf(fmaxf(one + two, -FLT_MAX), FLT_MAX);
 }
 
 // The two largest of two pairs.
@@ -630,7 +636,7 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
     for (int i = 0; i < PER; ++i) f[i] = f[i] != f[i] ? INFINITY : f[i];
     if (SUMS && p.groups > 1) {
         float total = -INFINITY, second = -INFINITY;  // lane g: group g's score, its second largest value
-        float parts = 0.f;                            // of a group that the lane has seen
+        float off = 0.f;                              // what a group's score may be off by: here the lane's own
         bool mine[PER];
         if (p.lanes_per_group > 0) {  // whole lanes, a power of two of them
             float one = -INFINITY, two = -INFINITY;
@@ -638,7 +644,7 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
             for (int i = 0; i < PER; ++i) merge_two(one, two, f[i], -INFINITY);
             for (int o = 1; o < p.lanes_per_group; o <<= 1)
                 merge_two(one, two, __shfl_xor_sync(kAll, one, o), __shfl_xor_sync(kAll, two, o));
-            parts = group_parts(one, two);
+            off = gap_of.of_group(one, two);
             const int from = (lane * p.lanes_per_group) & 31;
             total = __shfl_sync(kAll, group_total(one, two), from);
             second = __shfl_sync(kAll, two, from);
@@ -654,7 +660,7 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
                 if (lane == g) {
                     total = group_total(one, two);
                     second = two;
-                    parts = group_parts(one, two);
+                    off = gap_of.of_group(one, two);
                 }
             }
         }
@@ -669,44 +675,52 @@ __device__ __forceinline__ int choose(const GateArgs &p, const Logits &row, int 
             last = next;
             if (lane == g) key = 0;
         }
-        if (next != 0 && last != 0) {
-            const float in = key_value(last), out = key_value(next);
+        if (next != 0) {  // (some group is left out)
             // (not negative, so the bits' order is the values')
-            parts = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(parts)));
-            const float gap = gap_of.of_groups(parts);
-            if (!(in - out > gap)) {
-                // Near (equal sums are rarely sums of equal parts, so they are looked
-                // at too): what is further above the first left out than float32 may
-                // err stays, what is further below the last kept goes, and the rest
-                // is compared in float64.
-                const uint32_t sure = __ballot_sync(kAll, total > out + gap);
-                const uint32_t near = __ballot_sync(kAll, total >= in - gap && !(total > out + gap));
-                int count = 0, g = e0 / p.group_size, left = (g + 1) * p.group_size - e0;
+            const float worst = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(off)));
+            if (!(key_value(last) - key_value(next) > 2.f * worst)) {
+                // What the groups that stay are no less than, what the others are no more than.
+                if (p.lanes_per_group > 0) off = __shfl_sync(kAll, off, (lane * p.lanes_per_group) & 31);
+                const bool in = kept >> lane & 1u;
+                off += isfinite(total) ? 0x1p-23f * fabsf(total) : 0.f;  // (these sums round, too)
+                const float low = total > -FLT_MAX ? total - off : -INFINITY, high = total < FLT_MAX ? total + off : INFINITY;
+                const float least = ord_to_float(__reduce_min_sync(kAll, float_to_ord(in ? low : INFINITY)));
+                const float most = ord_to_float(__reduce_max_sync(kAll, float_to_ord(in ? -INFINITY : high)));
+                if (!(least > most)) {
+                    // Near (equal sums are rarely sums of equal parts, so they are looked
+                    // at too): what is surely above all that are left out stays, what is
+                    // surely below all that are kept goes, and the rest is compared in
+                    // float64.
+                    const uint32_t sure = __ballot_sync(kAll, in && low > most);
+                    const uint32_t near = __ballot_sync(kAll, total != -INFINITY && (in ? !(low > most) : high >= least));
+                    int count = 0, g = e0 / p.group_size, left = (g + 1) * p.group_size - e0;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const float two = __shfl_sync(kAll, second, g & 31);
-                    const bool take = f[i] != -INFINITY && (near >> (g & 31) & 1u) && !(two - f[i] > gap_of(two, f[i]));
-                    const uint32_t who = __ballot_sync(kAll, take);
-                    const int at = count + __popc(who & ((1u << lane) - 1u));
-                    if (take && at < kNear) list.found[at] = {(uint32_t)g, e0 + i};
-                    count += __popc(who);
-                    if (--left == 0) {
-                        ++g;
-                        left = p.group_size;
+                    for (int i = 0; i < PER; ++i) {
+                        const float two = __shfl_sync(kAll, second, g & 31);
+                        const bool take = f[i] != -INFINITY && (near >> (g & 31) & 1u) && !(two - f[i] > gap_of(two, f[i]));
+                        const uint32_t who = __ballot_sync(kAll, take);
+                        const int at = count + __popc(who & ((1u << lane) - 1u));
+                        if (take && at < kNear) list.found[at] = {(uint32_t)g, e0 + i};
+                        count += __popc(who);
+                        if (--left == 0) {
+                            ++g;
+                            left = p.group_size;
+                        }
                     }
+                    // (infinite sums have no order in float32)
+                    if (count > kNear || __any_sync(kAll, (near >> lane & 1u) && !isfinite(total)))
+                        return choose_exact(p, row, lane);
+                    __syncwarp();
+                    const int wanted = p.topk_groups - __popc(sure);
+                    uint32_t some = kAll;
+                    if (near_values(p, row, lane, list, count))
+                        some = refine_groups<false>(p, lane, list, count, near, wanted);
+                    if (some == kAll) {
+                        exact_values(p, row, lane, list, count);
+                        some = refine_groups<true>(p, lane, list, count, near, wanted);
+                    }
+                    kept = sure | some;
                 }
-                // (infinite sums have no order in float32, nor have sums whose parts are past it)
-                if (count > kNear || !isfinite(in) || !isfinite(out) || !isfinite(gap)) return choose_exact(p, row, lane);
-                __syncwarp();
-                const int wanted = p.topk_groups - __popc(sure);
-                uint32_t some = kAll;
-                if (near_values(p, row, lane, list, count))
-                    some = refine_groups<false>(p, lane, list, count, near, wanted, parts);
-                if (some == kAll) {
-                    exact_values(p, row, lane, list, count);
-                    some = refine_groups<true>(p, lane, list, count, near, wanted, parts);
-                }
-                kept = sure | some;
             }
         }
         if (p.lanes_per_group > 0) {

@@ -84,3 +84,54 @@ def test_a_group_that_is_pinned_without_end_beside_ordinary_ones(gpu_lib, kind):
                                  topk_groups=3)
     want = np.argsort(-np.where(np.repeat(kept, 4, 1), c, -np.inf), 1, kind="stable")[:, :5]
     assert np.array_equal(ids.cpu().numpy()[clear], want[clear])
+
+
+def by_definition(z, bias, kind, topk, groups, topk_groups):
+    """Token by token in float64; a logit or a bias of -inf closes."""
+    s = scores_of(z, kind)
+    n, E = z.shape
+    size = E // groups
+    ids = np.full((n, topk), -1, np.int64)
+    for t in range(n):
+        c = s[t] + bias.astype(np.float64)
+        total = []
+        for g in range(groups):
+            best = sorted(c[g * size:(g + 1) * size], reverse=True)[:2]
+            total.append(best[0] if len(best) < 2 or best[1] == -np.inf else best[0] + best[1])
+        for g in sorted(range(groups), key=lambda g: (-total[g], g))[topk_groups:]:
+            c[g * size:(g + 1) * size] = -np.inf
+        order = sorted((e for e in range(E) if c[e] != -np.inf), key=lambda e: (-c[e], e))[:topk]
+        ids[t, :len(order)] = order
+    return ids
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("mask", [float(np.finfo(np.float32).min), -3e38, -1.5e38, -1e30, -1e4])
+@pytest.mark.parametrize("E,groups", [(32, 8), (30, 5), (256, 8), (96, 32)])
+def test_masks_of_the_lowest_value(gpu_lib, kind, E, groups, mask):
+    """A large negative bias holds an expert back, it does not close it: whole groups of such ones stay where the
+    number of groups asks for them, though their sums pass float32."""
+    n, size = 40, E // groups
+    r = np.random.RandomState(E)
+    z, bias = r.randn(n, E).astype(np.float32), (0.1 * r.randn(E)).astype(np.float32)
+    for g in (1, 3, groups - 1):
+        bias[g * size:(g + 1) * size] = mask
+    bias[2 * size + 1:3 * size] = mask  # one left
+    for topk_groups in sorted({1, groups // 2, groups - 3, groups - 2, groups - 1, groups}):
+        for topk in (2, min(32, topk_groups * size)):
+            ids, _ = gpu_lib.kmeans_gate(torch.from_numpy(z).cuda(), topk, scores=kind, bias=torch.from_numpy(bias).cuda(),
+                                         groups=groups, topk_groups=topk_groups)
+            want = by_definition(z, bias, kind, topk, groups, topk_groups)
+            assert np.array_equal(ids.cpu().numpy(), want), (topk_groups, topk)
+
+
+@pytest.mark.parametrize("large", [1e4, 1e30, 3e38])
+def test_a_group_with_large_biases_does_not_disturb_the_others(gpu_lib, large):
+    """Pinned in one group, held back in another: the groups between them are told apart as without those."""
+    n, E, groups = 300, 64, 8
+    r = np.random.RandomState(5)
+    z, bias = r.randn(n, E).astype(np.float32), (0.1 * r.randn(E)).astype(np.float32)
+    bias[8:16], bias[40:48] = large, -large
+    ids, _ = gpu_lib.kmeans_gate(torch.from_numpy(z).cuda(), 12, scores="sigmoid", bias=torch.from_numpy(bias).cuda(),
+                                 groups=groups, topk_groups=3)
+    assert np.array_equal(ids.cpu().numpy(), by_definition(z, bias, "sigmoid", 12, groups, 3))
