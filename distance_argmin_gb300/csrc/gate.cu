@@ -22,7 +22,7 @@
 // bounds the values that are looked at further, a few more than topk.  They are
 // brought together, one to a lane, and each counts the ones before it.
 //
-// Instructions bound it, 1205 of a warp per token: 16384 tokens, 8 of 256 float32
+// Instructions bound it, 1239 of a warp per token: 16384 tokens, 8 of 256 float32
 // experts in 4 of 8 groups, sigmoid and bias take 22 to 23 us a call, where reading
 // the logits takes 2.6; 18.5 without the groups, 24 without the bias (the logits are
 // loaded once more, for their order), 12.4 without both.  An argmax over all lanes
